@@ -4,9 +4,9 @@ Three families: rotary positions for Q and K (forward and backward), the linear 
 residual (forward and backward), and the 4-bit KV cache (append and read back, attention over its pages).  With
 `own` false every case runs in elementary torch operations in 32 bits; with `own` true it makes the library's calls.
 
-Cache page block of one KV head (`page` tokens, head dim d): page*d/2 bytes of K codes (two codes to a byte, the even
-column in the low nibble), as many of V codes, then page (scale, offset) bf16 pairs of K, then of V.  A code c stands
-for offset + scale * c.
+A page of the cache holds, for each KV head, page/16 blocks of 16 tokens (head dim d): 16 rows of d/2 bytes of K codes
+(two codes to a byte, the even column in the low nibble), 16 rows of V codes, then 16 (scale, offset) bf16 pairs of K,
+then of V.  A code c stands for offset + scale * c.
 """
 import math
 
@@ -185,14 +185,13 @@ def prepare(case, seed):
         at += n
     table = cpu.to(dev)
     table = torch.where(table >= 0, order[table.clamp(min=0)], table).to(torch.int32)
-    cache = torch.empty((n_pages, Hkv, page * (d + 8)), dtype=torch.uint8, device=dev)
-    cache[:, :, :page * d] = torch.randint(0, 256, (n_pages, Hkv, page * d), generator=g, device=dev,
-                                           dtype=torch.uint8)
-    scale = 0.12 + 0.2 * torch.rand((n_pages, Hkv, 2 * page, 1), generator=g, device=dev)
-    off = -7.5 * scale + 0.3 * torch.randn((n_pages, Hkv, 2 * page, 1), generator=g, device=dev)
-    pair = torch.cat([scale, off], -1).to(torch.bfloat16).reshape(n_pages, Hkv, page * 4)
-    cache[:, :, page * d:] = pair.view(torch.uint8)
-    s = dict(case=case, cache=cache.view(n_pages, -1), table=table)
+    blocks = n_pages * Hkv * page // 16
+    cache = torch.empty((blocks, 16 * (d + 8)), dtype=torch.uint8, device=dev)
+    cache[:, :16 * d] = torch.randint(0, 256, (blocks, 16 * d), generator=g, device=dev, dtype=torch.uint8)
+    scale = 0.12 + 0.2 * torch.rand((blocks, 32, 1), generator=g, device=dev)
+    off = -7.5 * scale + 0.3 * torch.randn((blocks, 32, 1), generator=g, device=dev)
+    cache[:, 16 * d:] = torch.cat([scale, off], -1).to(torch.bfloat16).reshape(blocks, 64).view(torch.uint8)
+    s = dict(case=case, cache=cache.view(n_pages, Hkv, page * (d + 8)), table=table)
     if op == "kv4_append":
         s.update(k=k, v=v, start=torch.tensor(start, dtype=torch.int32, device=dev))
     else:
@@ -258,23 +257,23 @@ def plain_codes(x):
 def plain_rows(cache, table, Hkv, d, page):
     """Dequantised K and V of the tables' pages, float32 [B, Hkv, wide * page, d]."""
     B, wide = table.shape
-    blk = cache.view(cache.shape[0], Hkv, -1)[table.clamp(min=0).long()].transpose(1, 2)  # [B, Hkv, wide, bytes]
-    n = page * d // 2
+    blk = cache.view(cache.shape[0], Hkv, page // 16, -1)[table.clamp(min=0).long()].transpose(1, 2)
 
-    def part(codes, pair):
-        c = blk[..., codes:codes + n].reshape(B, Hkv, wide * page, d // 2)
+    def part(codes, pair):  # of [B, Hkv, wide, page / 16, bytes]
+        c = blk[..., codes:codes + 8 * d].reshape(B, Hkv, wide * page, d // 2)
         c = torch.stack([c & 15, c >> 4], -1).reshape(B, Hkv, wide * page, d).float()
-        p = blk[..., pair:pair + 4 * page].contiguous().view(torch.bfloat16).reshape(B, Hkv, wide * page, 2).float()
+        p = blk[..., pair:pair + 64].contiguous().view(torch.bfloat16).reshape(B, Hkv, wide * page, 2).float()
         return c.mul_(p[..., :1]).add_(p[..., 1:])
-    return part(0, 2 * n), part(n, 2 * n + 4 * page)
+    return part(0, 16 * d), part(8 * d, 16 * d + 64)
 
 
 def plain_append(s):
     case = s["case"]
     B, S, Hkv, d, page = (case[k] for k in ("B", "S", "Hkv", "d", "page"))
-    cache = s["cache"].view(s["cache"].shape[0], Hkv, -1)
+    cache = s["cache"].view(-1, Hkv, page // 16, 16 * (d + 8))
     pos = s["start"].long()[:, None] + torch.arange(S, device=cache.device)
-    pg, at = torch.gather(s["table"].long(), 1, pos // page), pos % page
+    pg, blk, at = torch.gather(s["table"].long(), 1, pos // page), pos % page // 16, pos % 16
+    pg, blk = pg[..., None, None], blk[..., None, None]
     col = torch.arange(d // 2, device=cache.device)
     byte = torch.arange(4, device=cache.device)
     out = []
@@ -283,8 +282,8 @@ def plain_append(s):
         code = (c[..., 0::2] | (c[..., 1::2] << 4)).permute(0, 2, 1, 3)
         pair = torch.cat([scale, off], -1).contiguous().view(torch.uint8).permute(0, 2, 1, 3)
         head = torch.arange(Hkv, device=cache.device)[:, None]
-        cache[pg[..., None, None], head, (j * page * d // 2 + at * (d // 2))[..., None, None] + col] = code
-        cache[pg[..., None, None], head, (page * d + j * 4 * page + at * 4)[..., None, None] + byte] = pair
+        cache[pg, head, blk, (j * 8 * d + at * (d // 2))[..., None, None] + col] = code
+        cache[pg, head, blk, (16 * d + j * 64 + at * 4)[..., None, None] + byte] = pair
         out.append((off.float() + scale.float() * c.float()).to(x.dtype))
     return tuple(out)
 
@@ -451,11 +450,11 @@ def exact(case, seed):
         used = (n + page - 1) // page
         if not used:
             continue
-        raw = s["cache"][s["table"][b, :used].long()].view(used, Hkv, page * (d + 8))
+        raw = s["cache"][s["table"][b, :used].long()].view(used, Hkv, page // 16, 16 * (d + 8))
         both = []
         for j in (0, 1):
-            codes = raw[:, :, j * page * d // 2:(j + 1) * page * d // 2].reshape(used, Hkv, page, d // 2).to(torch.int32)
-            pair = raw[:, :, page * (d + 4 * j):page * (d + 4 * j + 4)].contiguous().view(torch.bfloat16)
+            codes = raw[..., j * 8 * d:(j + 1) * 8 * d].reshape(used, Hkv, page, d // 2).to(torch.int32)
+            pair = raw[..., 16 * d + 64 * j:16 * d + 64 * j + 64].contiguous().view(torch.bfloat16)
             pair = pair.view(used, Hkv, page, 2).to(f8)
             val = torch.empty((used, Hkv, page, d), dtype=f8, device="cuda")
             val[..., 0::2] = pair[..., :1] * (codes % 16) + pair[..., 1:]
