@@ -341,6 +341,148 @@ PSR_API size_t psr_gemm_rs_workspace_bytes(const psr_rs_shape* shape);
 PSR_API int psr_gemm_rs(const psr_rs_shape* shape, const void* a, const void* w, void* out, void* workspace,
                         size_t workspace_bytes, const psr_partition* part, void* stream);
 
+/* ---- The attention layer around the ring ------------------------------------------------------
+ * What a layer needs next to the ring: rotary positions for Q and K, the linear projections with
+ * their epilogue and gradients, and, once the prompt has gone through the ring, a KV cache held in
+ * 4 bits with the attention of single tokens over it.  The calls are asynchronous on `stream`, work
+ * on the current device (sm_103), allocate no device memory and can be captured into a graph.
+ * Sizes of zero (no tokens, no rows) are accepted and write nothing unless said otherwise. */
+
+/* element types of the calls below */
+#define PSR_BF16 0
+#define PSR_F16 1
+#define PSR_F32 2
+
+/* Element strides of a [B][H][S][d] tensor's first three axes; the last axis is contiguous.  An input
+ * may repeat elements (stride 0); the elements of an output must not overlap. */
+typedef struct {
+  long long b, h, s;
+} psr_strides;
+
+/* Rotary positions.  For each row of Q and K at position p, and each pair i < rot/2 of its first `rot`
+ * columns, (x1, x2) becomes
+ *     (a (x1 cos t - x2 sin t), a (x2 cos t + x1 sin t)),   t = p * f_i,  a = amplitude,
+ * computed in fp32 and rounded once; the other d - rot columns are copied.  Pairs are columns (i, i + rot/2),
+ * or (2i, 2i + 1) if `interleaved`.  The frequencies come as turns per position in 64-bit fixed
+ * point, table[i] = f_i / (2 pi) * 2^64 mod 2^64, so the angle of every 64-bit position is exact modulo a
+ * turn.  `inverse` rotates by -t: applied to the gradients of the outputs it gives those of the
+ * inputs.
+ * Row s of batch b is at position positions[b * positions_b + s] if `positions` is given (device), else
+ * at offset + the global position of row s of the ring's shard order (P, causal as in psr_shape:
+ * row s itself, or the load-balanced order of PSR_CAUSAL_BALANCED, which needs S % (2P) == 0). */
+typedef struct {
+  int B, Hq, Hkv; /* batch, heads of q and of k; Hkv = 0: no k */
+  int S, P;       /* rows of the sequence axis, shards; S % P == 0 */
+  int d;          /* columns, 1..1024 */
+  int causal;     /* as in psr_shape; only PSR_CAUSAL_BALANCED changes the positions */
+  int rot;        /* rotated columns, even, 2..d */
+  int interleaved, inverse;
+  int type;       /* PSR_BF16, PSR_F16 or PSR_F32 */
+  float amplitude;
+  long long offset;
+} psr_rotary_shape;
+
+/* Frequency scaling for positions beyond the trained length (psr_rotary_table). */
+#define PSR_ROTARY_PLAIN 0    /* f_i = base^(-2i/rot) */
+#define PSR_ROTARY_LINEAR 1   /* f_i / factor */
+#define PSR_ROTARY_BY_PARTS 2 /* f_i kept where it turns more than beta_fast times over original_length, f_i / factor
+                                 where it turns less than beta_slow times, blended linearly in i between them */
+
+/* Fills table[0 .. rot/2) (HOST memory) with the fixed-point frequencies.  factor >= 1 (ignored by PLAIN);
+ * original_length, beta_fast > beta_slow > 0 are read by BY_PARTS only. */
+PSR_API int psr_rotary_table(int rot, double base, int scaling, double factor, double original_length,
+                             double beta_fast, double beta_slow, uint64_t* table);
+
+/* q, k (read) and q_out, k_out (written): device, strides as given; an output may be its own input
+ * (same pointer and strides).  k, k_out and their strides may be NULL when Hkv = 0.  table: device, rot/2
+ * words; positions: device, or NULL. */
+PSR_API int psr_rotary(const psr_rotary_shape* shape, const void* q, const psr_strides* q_strides, void* q_out,
+                       const psr_strides* q_out_strides, const void* k, const psr_strides* k_strides, void* k_out,
+                       const psr_strides* k_out_strides, const uint64_t* table, const int64_t* positions,
+                       long long positions_b, void* stream);
+
+/* activations of psr_linear */
+#define PSR_ACT_NONE 0
+#define PSR_ACT_RELU 1
+#define PSR_ACT_GELU 2      /* z Phi(z) */
+#define PSR_ACT_GELU_TANH 3 /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+#define PSR_ACT_SILU 4      /* z / (1 + exp(-z)) */
+
+/* Row strides are in elements; 0 selects the contiguous one.  Any M >= 0, N >= 1, K >= 1.  Tensors whose rows
+ * all start on 16-byte boundaries run on the tensor cores; others take a slower kernel. */
+typedef struct {
+  int M, N, K;
+  int act;  /* PSR_ACT_* */
+  int type; /* PSR_BF16 or PSR_F16, of every tensor */
+  long long ldx, ldw, ldr, ldy, ldz; /* x [M][K], w [N][K], residual [M][N], y (dy) [M][N], z [M][N] */
+} psr_linear_shape;
+
+/* Bytes of device workspace psr_linear (backward = 0) or psr_linear_bwd (1) needs; 0 if invalid. */
+PSR_API size_t psr_linear_workspace_bytes(const psr_linear_shape* shape, int backward);
+
+/* z = x w^T + bias,  y = act(z) + residual: fp32 accumulation, y and z each rounded once.
+ *   x, w: device; bias [N], residual: device or NULL; y: device (written; may be the residual itself);
+ *   z: device or NULL (written; what psr_linear_bwd reads);
+ *   workspace: device, >= psr_linear_workspace_bytes(shape, 0), 256-byte aligned; not shared by launches in flight;
+ *   timeout_ms: bound on every device wait (<= 0: 2000 ms), reported by psr_get_stats. */
+PSR_API int psr_linear(const psr_linear_shape* shape, const void* x, const void* w, const void* bias,
+                       const void* residual, void* y, void* z, void* workspace, size_t workspace_bytes, int timeout_ms,
+                       void* stream);
+
+/* dz = dy act'(z) (rounded to `type`: the operand of the products),  dx = dz w,  dw = dz^T x,  db = column sums
+ * of the unrounded dz.  The residual's gradient is dy itself.
+ *   dy, x, w: device; z: device, the forward's, or NULL when act is PSR_ACT_NONE;
+ *   dx [M][K], dw [N][K], db [N]: device, contiguous, any of them NULL to leave it out;
+ *   workspace: >= psr_linear_workspace_bytes(shape, 1). */
+PSR_API int psr_linear_bwd(const psr_linear_shape* shape, const void* dy, const void* z, const void* x, const void* w,
+                           void* dx, void* dw, void* db, void* workspace, size_t workspace_bytes, int timeout_ms,
+                           void* stream);
+
+/* KV cache in 4 bits.  The cache is [n_pages][Hkv][page / 16] blocks of 16 tokens, each block 16 (d + 8) bytes:
+ * 16 rows of d/2 bytes of K codes (column 2i in the low nibble of byte i), 16 rows of V codes, then a bf16
+ * (scale, offset) pair for each K row, then for each V row.  A code c stands for offset + scale * c, with
+ * offset = bf16(min of the row), scale = bf16(max/15 - min/15), c = (x - offset) / scale rounded half to even
+ * and clamped to 0..15 (0 if scale is 0).  A row with an element that is not finite reads back as NaN.
+ * table [B][max_pages] (int32, device): table[b][j] is the page of positions [j page, (j+1) page) of sequence b.
+ * Page numbers outside [0, n_pages) and positions outside the table are never read or written. */
+typedef struct {
+  int B, Hq, Hkv;              /* sequences, query heads, KV heads; Hq % Hkv == 0 */
+  int S;                       /* new tokens of each sequence */
+  int d;                       /* 64 or 128 */
+  int page, n_pages, max_pages; /* tokens of a page (16, 32, 64, 128 or 256), pages of the cache, columns of the table */
+  int type;                    /* PSR_BF16 or PSR_F16, of q, k, v, o */
+  float scale;                 /* of the scores; <= 0 selects 1/sqrt(d) */
+} psr_kv4_shape;
+
+/* Bytes of the cache: n_pages * Hkv * page * (d + 8); 0 if invalid. */
+PSR_API size_t psr_kv4_cache_bytes(const psr_kv4_shape* shape);
+
+/* Quantises the first count[b] (NULL: all) of the S rows of k and v [B][Hkv][S][d] (strides as given) into positions
+ * start[b] + i of sequence b.  Rows that fall outside the table or on a page outside the cache are not written.
+ * Two rows for one place of the cache (a page listed twice) leave either row's or a mixture there. */
+PSR_API int psr_kv4_append(const psr_kv4_shape* shape, const void* k, const psr_strides* k_strides, const void* v,
+                           const psr_strides* v_strides, void* cache, const int32_t* table, const int32_t* start,
+                           const int32_t* count, void* stream);
+
+/* Reads positions start[b] + i, i < S, back into k and v [B][Hkv][S][d] (contiguous): zeros for rows i >= count[b]
+ * (NULL: none), NaN for rows outside the table or on a page outside the cache. */
+PSR_API int psr_kv4_read(const psr_kv4_shape* shape, const void* cache, const int32_t* table, const int32_t* start,
+                         const int32_t* count, void* k, void* v, void* stream);
+
+/* Bytes of device workspace psr_kv4_attn needs on the current device; 0 if invalid. */
+PSR_API size_t psr_kv4_attn_workspace_bytes(const psr_kv4_shape* shape);
+
+/* Attention of the last S positions of each cached sequence (S = 1: single tokens) over the sequence: with n = lens[b]
+ * (device, int32) positions cached, the new ones included, query i attends to positions 0 .. n - S + i.
+ * q, o: [B][Hq][S][d], strides as given; lse: [B][Hq][S] fp32, natural log, as psr_ring_attn_fwd's.  A query with no
+ * position gets o = 0, lse = -infinity.  A sequence with n < 0, n > max_pages * page, or a page outside the cache
+ * among the pages of its n positions gets NaN.
+ *   workspace: >= psr_kv4_attn_workspace_bytes(shape), 256-byte aligned; not shared by launches in flight;
+ *   timeout_ms: bound on every device wait (<= 0: 2000 ms), reported by psr_get_stats. */
+PSR_API int psr_kv4_attn(const psr_kv4_shape* shape, const void* q, const psr_strides* q_strides, const void* cache,
+                         const int32_t* table, const int32_t* lens, void* o, const psr_strides* o_strides, float* lse,
+                         void* workspace, size_t workspace_bytes, int timeout_ms, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

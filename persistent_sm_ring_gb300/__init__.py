@@ -18,6 +18,8 @@ from .build import LIB, LIB_PAIRS, LIB_TRACE, build as _build
 __all__ = ["build", "load", "Shape", "AgShape", "RsShape", "Partition", "Stats", "ring_attn_fwd", "ring_attn_fwd_host",
            "workspace_bytes", "ag_gemm", "ag_gemm_workspace_bytes", "gemm_rs", "gemm_rs_workspace_bytes",
            "ring_attn_bwd", "ring_attn_bwd_workspace_bytes",
+           "rotary_table", "rotary", "rotary_bwd", "linear", "linear_bwd", "linear_workspace_bytes",
+           "kv4_cache", "kv4_append", "kv4_read", "kv4_attn", "kv4_attn_workspace_bytes",
            "get_stats", "get_trajectory", "controller_target", "num_ctas", "status_string", "PsrError",
            "STATIC", "ADAPTIVE", "FAULT_NONE", "FAULT_DROP_FIRST_FLAG", "FAULT_SLOW_STAGING", "CAUSAL",
            "CAUSAL_BALANCED"]
@@ -30,7 +32,13 @@ CAUSAL, CAUSAL_BALANCED = 1, 2
 EXPORTED = ("psr_workspace_bytes", "psr_ring_attn_fwd", "psr_ring_attn_fwd_host", "psr_get_stats",
             "psr_get_trajectory", "psr_controller_target", "psr_status_string", "psr_num_ctas",
             "psr_ring_attn_fwd_noalloc", "psr_noalloc_get_stats", "psr_ag_gemm_workspace_bytes", "psr_ag_gemm", "psr_gemm_rs_workspace_bytes",
-            "psr_gemm_rs", "psr_ring_attn_bwd_workspace_bytes", "psr_ring_attn_bwd")
+            "psr_gemm_rs", "psr_ring_attn_bwd_workspace_bytes", "psr_ring_attn_bwd",
+            "psr_rotary_table", "psr_rotary", "psr_linear_workspace_bytes", "psr_linear", "psr_linear_bwd",
+            "psr_kv4_cache_bytes", "psr_kv4_append", "psr_kv4_read", "psr_kv4_attn_workspace_bytes", "psr_kv4_attn")
+
+BF16, F16, F32 = 0, 1, 2
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+ROTARY_SCALINGS = {"plain": 0, "linear": 1, "by_parts": 2}
 
 
 class Shape(ctypes.Structure):
@@ -44,6 +52,29 @@ class AgShape(ctypes.Structure):
 
 class RsShape(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int), ("N", ctypes.c_int), ("Ks", ctypes.c_int), ("P", ctypes.c_int)]
+
+
+class Strides(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_longlong), ("h", ctypes.c_longlong), ("s", ctypes.c_longlong)]
+
+
+class RotaryShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("S", ctypes.c_int),
+                ("P", ctypes.c_int), ("d", ctypes.c_int), ("causal", ctypes.c_int), ("rot", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("inverse", ctypes.c_int), ("type", ctypes.c_int),
+                ("amplitude", ctypes.c_float), ("offset", ctypes.c_longlong)]
+
+
+class LinearShape(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int), ("act", ctypes.c_int),
+                ("type", ctypes.c_int), ("ldx", ctypes.c_longlong), ("ldw", ctypes.c_longlong),
+                ("ldr", ctypes.c_longlong), ("ldy", ctypes.c_longlong), ("ldz", ctypes.c_longlong)]
+
+
+class Kv4Shape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("S", ctypes.c_int),
+                ("d", ctypes.c_int), ("page", ctypes.c_int), ("n_pages", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("type", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 class Partition(ctypes.Structure):
@@ -132,6 +163,23 @@ def load(trace: bool = False, variant: str = "") -> ctypes.CDLL:
         lib.psr_ring_attn_fwd_noalloc.restype = ctypes.c_int
         lib.psr_noalloc_get_stats.argtypes = [ctypes.POINTER(Stats), vp]
         lib.psr_noalloc_get_stats.restype = ctypes.c_int
+        P_st, P_rot, P_lin, P_kv4 = map(ctypes.POINTER, (Strides, RotaryShape, LinearShape, Kv4Shape))
+        dbl = ctypes.c_double
+        lib.psr_rotary_table.argtypes = [ctypes.c_int, dbl, ctypes.c_int, dbl, dbl, dbl, dbl, vp]
+        lib.psr_rotary.argtypes = [P_rot, vp, P_st, vp, P_st, vp, P_st, vp, P_st, vp, vp, ctypes.c_longlong, vp]
+        lib.psr_linear_workspace_bytes.argtypes = [P_lin, ctypes.c_int]
+        lib.psr_linear.argtypes = [P_lin, vp, vp, vp, vp, vp, vp, vp, sz, ctypes.c_int, vp]
+        lib.psr_linear_bwd.argtypes = [P_lin, vp, vp, vp, vp, vp, vp, vp, vp, sz, ctypes.c_int, vp]
+        lib.psr_kv4_cache_bytes.argtypes = [P_kv4]
+        lib.psr_kv4_append.argtypes = [P_kv4, vp, P_st, vp, P_st, vp, vp, vp, vp, vp]
+        lib.psr_kv4_read.argtypes = [P_kv4, vp, vp, vp, vp, vp, vp, vp]
+        lib.psr_kv4_attn_workspace_bytes.argtypes = [P_kv4]
+        lib.psr_kv4_attn.argtypes = [P_kv4, vp, P_st, vp, vp, vp, vp, P_st, vp, vp, sz, ctypes.c_int, vp]
+        for name in ("psr_rotary_table", "psr_rotary", "psr_linear", "psr_linear_bwd", "psr_kv4_append", "psr_kv4_read",
+                     "psr_kv4_attn"):
+            getattr(lib, name).restype = ctypes.c_int
+        for name in ("psr_linear_workspace_bytes", "psr_kv4_cache_bytes", "psr_kv4_attn_workspace_bytes"):
+            getattr(lib, name).restype = sz
         lib.psr_num_ctas.argtypes = []
         lib.psr_num_ctas.restype = ctypes.c_int
         _lib = lib
@@ -411,6 +459,458 @@ def gemm_rs(a, w, *, partition=None, workspace=None, out=None, stream=None):
     if rc != OK:
         raise PsrError(rc, "psr_gemm_rs")
     return out, workspace
+
+
+# ------------------------------------------------------------------------------------------------
+# The attention layer around the ring: rotary positions, linear, 4-bit KV cache
+# ------------------------------------------------------------------------------------------------
+# These calls run on their tensors' device whatever the current one is.  Memory that a call makes
+# (outputs and workspaces not passed in) belongs to the stream the call runs on.
+
+class _Launch:
+    """The device and stream of a call: makes the device current, and the stream while memory is made."""
+
+    def __init__(self, device, stream, what):
+        import torch
+        self.torch, self.device = torch, device
+        if stream is not None and stream.device != device:
+            raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {device}")
+        self.stream = stream
+
+    def __enter__(self):
+        cuda = self.torch.cuda
+        self.back = None
+        if cuda.current_device() != self.device.index:
+            self.back = cuda.current_device()
+            cuda.set_device(self.device)
+        current = cuda.current_stream()
+        if self.stream is None:
+            self.stream = current
+        self.other = self.stream != current
+        self.handle = self.stream.cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            self.torch.cuda.set_device(self.back)
+
+    def empty(self, shape, dtype):
+        if not self.other:
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+        with self.torch.cuda.stream(self.stream):
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+
+
+_TYPES = {"torch.bfloat16": BF16, "torch.float16": F16, "torch.float32": F32}
+
+
+def _type_of(t, name, allowed):
+    """The type code of a tensor."""
+    code = _TYPES.get(str(t.dtype), F32 + 1)
+    if code > allowed:
+        raise ValueError(f"{name} must be bfloat16{', float16 or float32' if allowed == F32 else ' or float16'}, "
+                         f"got {t.dtype}")
+    return code
+
+
+def _check_like(t, name, shape, dtype, device):
+    """A CUDA tensor of this shape and type on this device, of any strides."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _check_flat(t, name, shape, dtype, device):
+    _check_like(t, name, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _check_cuda(t, name, dims):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must be {dims}-d, got {tuple(t.shape)}")
+
+
+def _heads_strides(t, name, written=False):
+    """Strides of a [B, H, S, d] tensor whose last axis is contiguous; no element of a written one twice."""
+    b, h, s, e = t.stride()
+    B, H, S, d = t.shape
+    if e != 1 and d > 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    if written and t.numel() > 0:
+        reach = d  # elements spanned so far; every further axis must step over them
+        for step, n in sorted(zip((b, h, s), (B, H, S))):
+            if n > 1:
+                if step < reach:
+                    raise ValueError(f"{name}: elements overlap (strides {t.stride()})")
+                reach = step * (n - 1) + reach
+    return Strides(b, h, s)
+
+
+def _span(t):
+    """First byte and the byte past the last of a tensor's elements."""
+    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
+def _check_apart(out, x, what, same_ok):
+    """`out` shares no memory with `x`, or is `x` itself where that is allowed."""
+    if out.numel() == 0 or x.numel() == 0:
+        return
+    if same_ok and out.data_ptr() == x.data_ptr() and out.stride() == x.stride():
+        return
+    (a, b), (c, d) = _span(out), _span(x)
+    if a < d and c < b:
+        raise ValueError(f"{what}: an output overlaps an input")
+
+
+def rotary_table(rot, base=10000.0, *, scaling="plain", factor=1.0, original_length=0, beta_fast=32.0, beta_slow=1.0,
+                 device="cuda"):
+    """Frequencies of `rot` rotated columns for rotary(): [rot/2] int64 holding turns per position in 64-bit
+    fixed point.  scaling: "plain", "linear" (all divided by `factor`) or "by_parts" (those that turn less than beta_slow
+    times over `original_length` divided, those that turn more than beta_fast times kept, blended between)."""
+    import torch
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"rotary_table: scaling must be one of {sorted(ROTARY_SCALINGS)}, got {scaling!r}")
+    host = torch.empty(max(0, int(rot)) // 2, dtype=torch.int64)
+    rc = load().psr_rotary_table(int(rot), float(base), ROTARY_SCALINGS[scaling], float(factor), float(original_length),
+                                 float(beta_fast), float(beta_slow), host.data_ptr() if rot > 0 else None)
+    if rc != OK:
+        raise PsrError(rc, "psr_rotary_table")
+    return host.to(device)
+
+
+def rotary(q, k, table, *, P=1, causal=CAUSAL, positions=None, offset=0, interleaved=False, amplitude=1.0, q_out=None,
+           k_out=None, stream=None, inverse=False):
+    """Rotary positions of q [B, Hq, S, d] and k [B, Hkv, S, d] (or None), bf16, fp16 or fp32, any strides with a
+    contiguous last axis (views of a projection's output, say).  The first 2 * len(table) columns are turned, pairs
+    (i, i + rot/2) or, interleaved, (2i, 2i + 1); the others are copied.
+
+    positions: int64 [S] or [B, S]; None takes offset + the global position of each row in the ring's shard order
+    (P, causal as for ring_attn_fwd).  Returns (q_out, k_out), contiguous unless passed in; an output may be its own
+    input."""
+    _check_cuda(q, "q", 4)
+    B, Hq, S, d = q.shape
+    dev, dtype = q.device, q.dtype
+    code = _type_of(q, "q", F32)
+    Hkv = 0
+    if k is not None:
+        _check_cuda(k, "k", 4)
+        Hkv = k.shape[1]
+        _check_like(k, "k", (B, Hkv, S, d), dtype, dev)
+    import torch
+    _check_flat(table, "table", (table.numel(),), torch.int64, dev)
+    pos_b = 0
+    if positions is not None:
+        _check_like(positions, "positions", (B, S) if positions.dim() == 2 else (S,), torch.int64, dev)
+        if S > 1 and positions.stride(-1) != 1:
+            raise ValueError("positions: the last axis must be contiguous")
+        pos_b = positions.stride(0) if positions.dim() == 2 else 0
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    for x, out, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+        if out is not None:
+            _check_like(out, name, x.shape, dtype, dev)
+            _check_apart(out, x, "rotary", True)
+    qs, qos = _heads_strides(q, "q"), None if q_out is None else _heads_strides(q_out, "q_out", True)
+    ks, kos = None if k is None else _heads_strides(k, "k"), None if k_out is None else _heads_strides(k_out, "k_out", True)
+    with _Launch(dev, stream, "rotary") as at:
+        flat = lambda H: Strides(H * S * d, S * d, d)
+        if q_out is None:
+            q_out, qos = at.empty((B, Hq, S, d), dtype), flat(Hq)
+        if k is not None and k_out is None:
+            k_out, kos = at.empty((B, Hkv, S, d), dtype), flat(Hkv)
+        shape = RotaryShape(B, Hq, Hkv, S, int(P), d, int(causal), 2 * table.numel(), int(bool(interleaved)),
+                            int(bool(inverse)), code, float(amplitude), int(offset))
+        if B == 0 or S == 0:  # no rows, no pointers
+            if int(P) < 1 or S % int(P):
+                raise PsrError(ERR_ARG if int(P) < 1 else ERR_UNSUPPORTED, "psr_rotary")
+            return q_out, k_out
+        rc = load().psr_rotary(shape, q.data_ptr(), qs, q_out.data_ptr(), qos, None if k is None else k.data_ptr(), ks,
+                               None if k is None else k_out.data_ptr(), kos, table.data_ptr(),
+                               None if positions is None else positions.data_ptr(), pos_b, at.handle)
+    if rc != OK:
+        raise PsrError(rc, "psr_rotary")
+    return q_out, k_out
+
+
+def rotary_bwd(dq, dk, table, **kwargs):
+    """The gradient of rotary(): dq, dk are those of its outputs, the arguments are the forward's.  Returns the
+    gradients of its inputs (rows turned back; the same scaling by `amplitude`)."""
+    return rotary(dq, dk, table, inverse=True, **kwargs)
+
+
+def _linear_shape(x, w, activation, what):
+    _check_cuda(x, "x", 2)
+    _check_cuda(w, "w", 2)
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"{what}: activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    code = _type_of(x, "x", F16)
+    M, K = x.shape
+    N = w.shape[0]
+    _check_like(w, "w", (N, K), x.dtype, x.device)
+    sh = LinearShape(M, N, K, ACTIVATIONS[activation], code, _row_stride(x, "x"), _row_stride(w, "w"), 0, 0, 0)
+    return sh, M, N, K
+
+
+def _row_stride(t, name, written=False):
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    if rows <= 1:
+        return 0
+    if t.stride(0) < cols:
+        raise ValueError(f"{name}: rows must not overlap (stride {t.stride(0)}, {cols} columns)")
+    return t.stride(0)
+
+
+def _workspace(at, workspace, need, what):
+    if workspace is None:
+        import torch
+        return at.empty((need,), torch.uint8)
+    if not workspace.is_cuda or workspace.device != at.device or not workspace.is_contiguous() \
+            or workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"{what}: workspace must be a contiguous CUDA tensor on {at.device} of at least {need} bytes")
+    return workspace
+
+
+def linear_workspace_bytes(M, N, K, *, activation="none", backward=False) -> int:
+    """Bytes of workspace that linear() or linear_bwd() needs."""
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    n = load().psr_linear_workspace_bytes(LinearShape(int(M), int(N), int(K), ACTIVATIONS[activation], BF16),
+                                          int(bool(backward)))
+    if n == 0:
+        raise PsrError(ERR_ARG, "psr_linear_workspace_bytes")
+    return int(n)
+
+
+def linear(x, w, bias=None, residual=None, *, activation="none", save_z=False, out=None, z=None, workspace=None,
+           timeout_ms=0, stream=None):
+    """y = act(x w^T + bias) + residual: x [M, K], w [N, K], bias [N], residual [M, N], bf16 or fp16, fp32 sums;
+    rows may be strided.  activation: "none", "relu", "gelu", "gelu_tanh" or "silu".
+
+    Returns (y [M, N], z, workspace).  With save_z (or a tensor z) z = x w^T + bias is written too, for
+    linear_bwd(); otherwise it is None.  `out` may be the residual."""
+    sh, M, N, K = _linear_shape(x, w, activation, "linear")
+    dev, dtype = x.device, x.dtype
+    if bias is not None:
+        _check_flat(bias, "bias", (N,), dtype, dev)
+    if residual is not None:
+        _check_like(residual, "residual", (M, N), dtype, dev)
+        sh.ldr = _row_stride(residual, "residual")
+    if out is not None:
+        _check_like(out, "out", (M, N), dtype, dev)
+        sh.ldy = _row_stride(out, "out")
+        for t in (x, w, bias):
+            if t is not None:
+                _check_apart(out, t, "linear", False)
+        if residual is not None:
+            _check_apart(out, residual, "linear", True)
+    if z is not None:
+        _check_like(z, "z", (M, N), dtype, dev)
+        sh.ldz = _row_stride(z, "z")
+        for t in (x, w, bias, residual, out):
+            if t is not None:
+                _check_apart(z, t, "linear", False)
+    lib = load()
+    with _Launch(dev, stream, "linear") as at:
+        if out is None:
+            out = at.empty((M, N), dtype)
+        if z is None and save_z:
+            z = at.empty((M, N), dtype)
+        need = lib.psr_linear_workspace_bytes(sh, 0)
+        if need == 0:
+            raise PsrError(ERR_ARG, "psr_linear")
+        workspace = _workspace(at, workspace, need, "linear")
+        if M == 0:
+            return out, z, workspace
+        rc = lib.psr_linear(sh, x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
+                            None if residual is None else residual.data_ptr(), out.data_ptr(),
+                            None if z is None else z.data_ptr(), workspace.data_ptr(), need, int(timeout_ms), at.handle)
+    if rc != OK:
+        raise PsrError(rc, "psr_linear")
+    return out, z, workspace
+
+
+def linear_bwd(dy, x, w, z=None, *, activation="none", need_dx=True, need_dw=True, need_db=True, dx=None, dw=None,
+               db=None, workspace=None, timeout_ms=0, stream=None):
+    """Gradients of linear(): dy [M, N] is that of y, z the forward's (needed unless activation is "none"); the
+    residual's gradient is dy itself.  Returns (dx [M, K], dw [N, K], db [N], workspace), None for those not asked for;
+    dx, dw, db may be passed in (contiguous)."""
+    sh, M, N, K = _linear_shape(x, w, activation, "linear_bwd")
+    dev, dtype = x.device, x.dtype
+    _check_like(dy, "dy", (M, N), dtype, dev)
+    sh.ldy = _row_stride(dy, "dy")
+    if activation != "none":
+        if z is None:
+            raise ValueError(f"linear_bwd: activation {activation!r} needs the forward's z")
+        _check_like(z, "z", (M, N), dtype, dev)
+        sh.ldz = _row_stride(z, "z")
+    wanted = ((need_dx, dx, "dx", (M, K)), (need_dw, dw, "dw", (N, K)), (need_db, db, "db", (N,)))
+    for _, t, name, shape in wanted:
+        if t is not None:
+            _check_flat(t, name, shape, dtype, dev)
+            for u in (dy, x, w, z):
+                if u is not None:
+                    _check_apart(t, u, "linear_bwd", False)
+    lib = load()
+    with _Launch(dev, stream, "linear_bwd") as at:
+        outs = [at.empty(shape, dtype) if t is None and need else t for need, t, _, shape in wanted]
+        dx, dw, db = outs
+        need = lib.psr_linear_workspace_bytes(sh, 1)
+        if need == 0:
+            raise PsrError(ERR_ARG, "psr_linear_bwd")
+        workspace = _workspace(at, workspace, need, "linear_bwd")
+        if M == 0:  # sums over no rows
+            import torch
+            with torch.cuda.stream(at.stream):
+                for t in (dw, db):
+                    if t is not None:
+                        t.zero_()
+            return dx, dw, db, workspace
+        rc = lib.psr_linear_bwd(sh, dy.data_ptr(), z.data_ptr() if activation != "none" else None, x.data_ptr(),
+                                w.data_ptr(), *(None if t is None else t.data_ptr() for t in outs),
+                                workspace.data_ptr(), need, int(timeout_ms), at.handle)
+    if rc != OK:
+        raise PsrError(rc, "psr_linear_bwd")
+    return dx, dw, db, workspace
+
+
+def kv4_cache(n_pages, Hkv, d, page, device="cuda"):
+    """An empty 4-bit KV cache, uint8 [n_pages, Hkv, page * (d + 8)] (a page is one contiguous piece); d 64 or 128,
+    page 16, 32, 64, 128 or 256 tokens."""
+    import torch
+    need = load().psr_kv4_cache_bytes(Kv4Shape(0, int(Hkv), int(Hkv), 0, int(d), int(page), int(n_pages), 1, BF16, 0.0))
+    if need == 0:
+        raise PsrError(ERR_UNSUPPORTED, "psr_kv4_cache_bytes")
+    return torch.zeros((int(n_pages), int(Hkv), int(page) * (int(d) + 8)), dtype=torch.uint8, device=device)
+
+
+def _kv4_shape(cache, table, B, Hq, Hkv, S, d, page, code, scale, dev):
+    import torch
+    _check_cuda(cache, "cache", 3)
+    _check_flat(cache, "cache", (cache.shape[0], int(Hkv), int(page) * (d + 8)), torch.uint8, dev)
+    _check_cuda(table, "table", 2)
+    _check_flat(table, "table", (B, table.shape[1]), torch.int32, dev)
+    return Kv4Shape(B, Hq, int(Hkv), S, d, int(page), cache.shape[0], table.shape[1], code,
+                    0.0 if scale is None else float(scale))
+
+
+def _check_counts(B, dev, **named):
+    import torch
+    for name, t in named.items():
+        if t is not None:
+            _check_flat(t, name, (B,), torch.int32, dev)
+
+
+def kv4_append(k, v, cache, table, start, *, page, count=None, stream=None):
+    """Quantises k, v [B, Hkv, S, d] (bf16 or fp16, any strides with a contiguous last axis) into the cache: row i of
+    sequence b, i < count[b] (default: all S), goes to position start[b] + i, which is on page table[b, position // page].
+
+    table: int32 [B, max_pages]; start, count: int32 [B].  Rows whose position is outside the table or whose page is
+    outside the cache are left out.  The places written must differ.  Returns the cache."""
+    _check_cuda(k, "k", 4)
+    B, Hkv, S, d = k.shape
+    dev = k.device
+    code = _type_of(k, "k", F16)
+    _check_like(v, "v", k.shape, k.dtype, dev)
+    sh = _kv4_shape(cache, table, B, Hkv, Hkv, S, d, page, code, None, dev)
+    _check_counts(B, dev, start=start, count=count)
+    if B == 0 or S == 0:
+        return cache
+    with _Launch(dev, stream, "kv4_append") as at:
+        rc = load().psr_kv4_append(sh, k.data_ptr(), _heads_strides(k, "k"), v.data_ptr(), _heads_strides(v, "v"),
+                                   cache.data_ptr(), table.data_ptr(), start.data_ptr(),
+                                   None if count is None else count.data_ptr(), at.handle)
+    if rc != OK:
+        raise PsrError(rc, "psr_kv4_append")
+    return cache
+
+
+def kv4_read(cache, table, start, *, S, Hkv, d, page, count=None, dtype=None, k=None, v=None, stream=None):
+    """Positions start[b] .. start[b] + S - 1 of each sequence, read back as k, v [B, Hkv, S, d] (bf16 unless `dtype`
+    says float16): zeros from row count[b] on, NaN where the table or the cache has no such place."""
+    import torch
+    _check_cuda(table, "table", 2)
+    B, dev = table.shape[0], table.device
+    dtype = dtype if dtype is not None else (k.dtype if k is not None else torch.bfloat16)
+    shape = (B, int(Hkv), int(S), int(d))
+    sh = _kv4_shape(cache, table, B, int(Hkv), Hkv, int(S), int(d), page,
+                    _type_of(torch.empty(0, dtype=dtype), "dtype", F16), None, dev)
+    _check_counts(B, dev, start=start, count=count)
+    for t, name in ((k, "k"), (v, "v")):
+        if t is not None:
+            _check_flat(t, name, shape, dtype, dev)
+            _check_apart(t, cache, "kv4_read", False)
+    with _Launch(dev, stream, "kv4_read") as at:
+        k = at.empty(shape, dtype) if k is None else k
+        v = at.empty(shape, dtype) if v is None else v
+        if k.numel() == 0:
+            return k, v
+        rc = load().psr_kv4_read(sh, cache.data_ptr(), table.data_ptr(), start.data_ptr(),
+                                 None if count is None else count.data_ptr(), k.data_ptr(), v.data_ptr(), at.handle)
+    if rc != OK:
+        raise PsrError(rc, "psr_kv4_read")
+    return k, v
+
+
+def kv4_attn_workspace_bytes(B, Hq, Hkv, S, d, *, page, n_pages, max_pages) -> int:
+    """Bytes of workspace that kv4_attn() needs on the current device."""
+    n = load().psr_kv4_attn_workspace_bytes(Kv4Shape(int(B), int(Hq), int(Hkv), int(S), int(d), int(page), int(n_pages),
+                                                     int(max_pages), BF16, 0.0))
+    if n == 0:
+        raise PsrError(ERR_UNSUPPORTED, "psr_kv4_attn_workspace_bytes")
+    return int(n)
+
+
+def kv4_attn(q, cache, table, lens, *, Hkv, page, scale=None, out=None, lse=None, workspace=None, timeout_ms=0,
+             stream=None):
+    """Attention of the last S positions of each cached sequence over the sequence (S = 1: single tokens).
+
+    q: [B, Hq, S, d] bf16 or fp16, any strides with a contiguous last axis; cache, table as in kv4_append; lens: int32
+    [B], the positions cached, the S new ones included.  Query i of sequence b sees positions 0 .. lens[b] - S + i.
+    Returns (o [B, Hq, S, d], lse [B, Hq, S] fp32, workspace): o = 0 and lse = -inf for a query that sees nothing, NaN
+    for a sequence whose length or pages are out of range."""
+    import torch
+    _check_cuda(q, "q", 4)
+    B, Hq, S, d = q.shape
+    dev = q.device
+    sh = _kv4_shape(cache, table, B, Hq, Hkv, S, d, page, _type_of(q, "q", F16), scale, dev)
+    _check_counts(B, dev, lens=lens)
+    qs, os_ = _heads_strides(q, "q"), None
+    if out is not None:
+        _check_like(out, "out", (B, Hq, S, d), q.dtype, dev)
+        _check_apart(out, q, "kv4_attn", False)
+        _check_apart(out, cache, "kv4_attn", False)
+        os_ = _heads_strides(out, "out", True)
+    if lse is not None:
+        _check_flat(lse, "lse", (B, Hq, S), torch.float32, dev)
+    lib = load()
+    with _Launch(dev, stream, "kv4_attn") as at:
+        if out is None:
+            out, os_ = at.empty((B, Hq, S, d), q.dtype), Strides(Hq * S * d, S * d, d)
+        if lse is None:
+            lse = at.empty((B, Hq, S), torch.float32)
+        need = lib.psr_kv4_attn_workspace_bytes(sh)
+        if need == 0:
+            raise PsrError(ERR_UNSUPPORTED, "psr_kv4_attn")
+        workspace = _workspace(at, workspace, need, "kv4_attn")
+        if B == 0 or S == 0:
+            return out, lse, workspace
+        rc = lib.psr_kv4_attn(sh, q.data_ptr(), qs, cache.data_ptr(), table.data_ptr(), lens.data_ptr(), out.data_ptr(),
+                              os_, lse.data_ptr(), workspace.data_ptr(), need, int(timeout_ms), at.handle)
+    if rc != OK:
+        raise PsrError(rc, "psr_kv4_attn")
+    return out, lse, workspace
 
 
 def get_stats(workspace, stream=None) -> dict:

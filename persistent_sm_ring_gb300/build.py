@@ -14,9 +14,10 @@ LIB_PAIRS = os.path.join(HERE, "libpsr_pairs.so")  # same library with CTA-pair 
 # variant -> (extra nvcc defines, output)
 VARIANTS = {"": ([], LIB), "trace": (["-DPSR_TRACE=1"], LIB_TRACE), "pairs": (["-DPSR_PAIRS=1"], LIB_PAIRS)}
 SOURCES = [os.path.join(CSRC, f) for f in ("psr_ring_attn.cu", "psr_ring_attn_bwd.cu", "psr_ag_gemm.cu", "psr_gemm_rs.cu",
-                                            "psr_noalloc.cu")]
+                                            "psr_noalloc.cu", "psr_rotary.cu", "psr_linear.cu", "psr_kv4.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f)
-                  for f in ("psr_device.cuh", "psr_schedule.h", "psr_control.cuh", "psr_gemm_tile.cuh", "psr_internal.h")] + [
+                  for f in ("psr_device.cuh", "psr_schedule.h", "psr_control.cuh", "psr_gemm_tile.cuh", "psr_internal.h",
+                            "psr_host.h")] + [
     os.path.join(ROOT, "include", "psr.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 _lock = threading.Lock()
@@ -47,7 +48,7 @@ def build(force: bool = False, verbose: bool = False, trace: bool = False, varia
         if not force and not needs_build(lib):
             return lib
         tmp = lib + f".{os.getpid()}.tmp"
-        cmd = [nvcc(), *ARCH, "-O3", "-std=c++17", "-lineinfo", "-shared", "-Xcompiler", "-fPIC",
+        cmd = [nvcc(), *ARCH, "-O3", "-std=c++17", "-lineinfo", "-shared", "--threads", "0", "-Xcompiler", "-fPIC",
                "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include"),
                *defines, *SOURCES, "-o", tmp]
         if verbose:

@@ -1,0 +1,242 @@
+"""GPU parity of psr_linear and psr_linear_bwd against the fp64 oracle, through the binding.
+
+Tolerance.  A product's fp32 sum of K terms is off by at most K 2^-23 sum |x| |w| (each addition rounds or truncates,
+2^-23), bias and residual add a rounding each, the activation a few units of 2^-24 of |z| + 1 (its slope is at most
+1.13 in size), and the result is rounded once to its type (half a step; 2^-25 absolute below the normal fp16
+numbers).  Backward: act' is evaluated in fp32 (2^-19 |dy|), dz is rounded to the type before the products, which adds
+half a step of |dz| |w| (|dz| |x|); db sums the unrounded dz.
+"""
+import numpy as np
+import pytest
+import torch
+
+from layer_util import check, f64, need_gpu, randn
+from oracle import layer as ol
+
+pytestmark = pytest.mark.gpu
+
+TINY = {"bf16": 0.0, "f16": 2.0**-25}
+
+
+def sum_tol(a, b):
+    """|a| [M, K], |b| [N, K] -> bound on the fp32 sum of a b^T."""
+    return a.shape[1] * 2.0**-23 * (np.abs(a) @ np.abs(b).T)
+
+
+def check_forward(got_y, got_z, x, w, bias, res, act, t, what):
+    a = [None if v is None else f64(v) for v in (x, w, bias, res)]
+    y, z = ol.linear(a[0], a[1], a[2], a[3], act)
+    e = sum_tol(a[0], a[1]) + 2.0**-23 * np.abs(z)
+    r = np.zeros_like(y) if res is None else a[3]
+    h = ol.HALF_STEP[t]
+    check(got_y, y, h * np.abs(y) * 1.01 + 1.13 * e + 2.0**-20 * (np.abs(z) + np.abs(r) + 1) * (act != "none" or res is not None)
+          + TINY[t], what)
+    if got_z is not None:
+        check(got_z, z, h * np.abs(z) * 1.01 + e + TINY[t], what + " z")
+
+
+def check_backward(got, dy, x, w, z, act, t, what):
+    d = [None if v is None else f64(v) for v in (dy, x, w, z)]
+    dx, dw, db, dz = ol.linear_bwd(d[0], d[1], d[2], d[3], act)
+    h = ol.HALF_STEP[t]
+    edz = (2.0**-19 * np.abs(d[0]) + h * np.abs(dz) * 1.01 + TINY[t]) if act != "none" else np.zeros_like(dz)
+    if got[0] is not None:
+        check(got[0], dx, h * np.abs(dx) * 1.01 + edz @ np.abs(d[2]) + sum_tol(dz, d[2].T) + TINY[t], what + " dx")
+    if got[1] is not None:
+        check(got[1], dw, h * np.abs(dw) * 1.01 + edz.T @ np.abs(d[1]) + sum_tol(dz.T, d[1].T) + TINY[t], what + " dw")
+    if got[2] is not None:
+        slope = 2.0**-19 * np.abs(d[0]).sum(0) if act != "none" else 0.0
+        check(got[2], db, h * np.abs(db) * 1.01 + slope + len(dz) * 2.0**-23 * np.abs(dz).sum(0) + TINY[t], what + " db")
+
+
+ACTS = ["none", "relu", "gelu", "gelu_tanh", "silu"]
+
+FORWARD = [  # M N K act bias residual z type
+    (1, 8, 8, "none", False, False, False, "bf16"),
+    (1, 1, 1, "none", True, True, True, "bf16"),
+    (1, 256, 512, "silu", True, True, True, "bf16"),
+    (1, 1000, 4104, "none", True, True, False, "f16"),
+    (2, 264, 72, "gelu", False, True, False, "bf16"),
+    (3, 33, 17, "relu", True, False, True, "f16"),
+    (5, 640, 2048, "gelu_tanh", True, False, True, "bf16"),
+    (8, 128, 64, "none", False, False, False, "f16"),
+    (9, 136, 1032, "silu", True, True, True, "bf16"),
+    (16, 72, 192, "relu", True, True, False, "bf16"),
+    (17, 512, 256, "gelu", True, True, True, "f16"),
+    (31, 1024, 776, "none", True, False, False, "bf16"),
+    (33, 96, 520, "silu", False, False, True, "bf16"),
+    (64, 256, 128, "none", True, True, True, "bf16"),
+    (65, 200, 136, "gelu_tanh", True, True, True, "bf16"),
+    (100, 77, 50, "gelu", True, True, True, "bf16"),
+    (127, 264, 64, "relu", True, True, True, "f16"),
+    (128, 256, 64, "none", False, False, False, "bf16"),
+    (129, 512, 328, "silu", True, True, True, "bf16"),
+    (255, 520, 96, "gelu", True, False, True, "f16"),
+    (256, 256, 256, "none", True, True, False, "bf16"),
+    (257, 776, 200, "gelu_tanh", True, True, True, "bf16"),
+    (300, 1288, 40, "relu", True, True, True, "bf16"),
+    (513, 264, 1000, "none", True, True, True, "f16"),
+    (1000, 8, 24, "silu", True, True, True, "bf16"),
+    (1100, 1032, 264, "gelu", True, True, True, "bf16"),
+]
+
+
+@pytest.mark.parametrize("case", FORWARD, ids=str)
+def test_linear(psr, case):
+    need_gpu()
+    M, N, K, act, bias, res, save, t = case
+    g = torch.Generator().manual_seed(M * 7 + N)
+    x, w = randn(g, (M, K), t), randn(g, (N, K), t, K**-0.5)
+    b = randn(g, (N,), t) if bias else None
+    r = randn(g, (M, N), t) if res else None
+    y, z, ws = psr.linear(x, w, b, r, activation=act, save_z=save)
+    assert psr.get_stats(ws)["status"] == 0
+    assert (z is not None) == save
+    check_forward(y, z, x, w, b, r, act, t, str(case))
+
+
+BACKWARD = [  # M N K act type
+    (1, 8, 8, "none", "bf16"),
+    (1, 1, 1, "gelu", "bf16"),
+    (1, 264, 136, "silu", "bf16"),
+    (3, 33, 17, "relu", "f16"),
+    (7, 128, 512, "none", "bf16"),
+    (40, 520, 72, "gelu_tanh", "bf16"),
+    (63, 64, 64, "relu", "bf16"),
+    (64, 256, 512, "none", "f16"),
+    (65, 264, 520, "gelu", "bf16"),
+    (100, 77, 50, "silu", "bf16"),
+    (129, 384, 256, "gelu_tanh", "f16"),
+    (257, 1000, 264, "silu", "bf16"),
+    (511, 136, 1288, "relu", "bf16"),
+    (1027, 520, 264, "gelu", "bf16"),
+    (2000, 16, 8, "none", "bf16"),
+]
+
+
+@pytest.mark.parametrize("case", BACKWARD, ids=str)
+def test_linear_bwd(psr, case):
+    need_gpu()
+    M, N, K, act, t = case
+    g = torch.Generator().manual_seed(M + 3 * N)
+    dy, x, w = randn(g, (M, N), t), randn(g, (M, K), t), randn(g, (N, K), t, K**-0.5)
+    z = randn(g, (M, N), t) if act != "none" else None
+    dx, dw, db, ws = psr.linear_bwd(dy, x, w, z, activation=act)
+    assert psr.get_stats(ws)["status"] == 0
+    check_backward((dx, dw, db), dy, x, w, z, act, t, str(case))
+
+
+@pytest.mark.parametrize("need", [(1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 1, 0), (0, 0, 0)], ids=str)
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_linear_bwd_of_some(psr, need, act):
+    need_gpu()
+    g = torch.Generator().manual_seed(4)
+    M, N, K = 70, 136, 264
+    dy, x, w, z = (randn(g, s, "bf16") for s in ((M, N), (M, K), (N, K), (M, N)))
+    got = psr.linear_bwd(dy, x, w, z, activation=act, need_dx=need[0], need_dw=need[1], need_db=need[2])[:3]
+    assert [v is not None for v in got] == [bool(v) for v in need]
+    check_backward(got, dy, x, w, z, act, "bf16", str(need))
+
+
+@pytest.mark.parametrize("pad,shift", [(8, 0), (1, 0), (0, 1), (8, 8)])
+@pytest.mark.parametrize("M", [1, 5, 70, 300])
+def test_linear_strided_rows(psr, pad, shift, M):
+    # rows on 16-byte boundaries and off them
+    need_gpu()
+    g = torch.Generator().manual_seed(pad + M)
+    N, K, t = 264, 136, "bf16"
+
+    def padded(rows, cols, std=1.0):
+        flat = randn(g, (rows * (cols + pad) + shift,), t, std)[shift:]
+        return flat.view(rows, cols + pad)[:, :cols]
+    x, w, r, y, z, dy = padded(M, K), padded(N, K, K**-0.5), padded(M, N), padded(M, N), padded(M, N), padded(M, N)
+    edge = torch.as_strided(y, (M, pad), (N + pad, 1), y.storage_offset() + N).clone()
+    a, b, _ = psr.linear(x, w, None, r, activation="gelu", out=y, z=z)
+    assert a is y and b is z
+    check_forward(y, z, x, w, None, r, "gelu", t, "strided")
+    if M > 1:  # between the rows nothing is written
+        last = slice(0, M - 1 if shift or pad else M)
+        assert torch.equal(torch.as_strided(y, (M, pad), (N + pad, 1), y.storage_offset() + N)[last], edge[last])
+    got = psr.linear_bwd(dy, x, w, z, activation="gelu")[:3]
+    check_backward(got, dy, x, w, z, "gelu", t, "strided bwd")
+
+
+def test_linear_residual_in_place(psr):
+    need_gpu()
+    for M in (1, 40, 300):
+        g = torch.Generator().manual_seed(M)
+        x, w, r = randn(g, (M, 128), "bf16"), randn(g, (264, 128), "bf16", 0.1), randn(g, (M, 264), "bf16")
+        keep = r.clone()
+        y, _, _ = psr.linear(x, w, None, r, out=r)
+        assert y is r
+        check_forward(y, None, x, w, None, keep, "none", "bf16", "in place")
+
+
+def test_linear_no_rows(psr):
+    need_gpu()
+    x, w = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), torch.ones((16, 64), dtype=torch.bfloat16, device="cuda")
+    y, z, _ = psr.linear(x, w, save_z=True)
+    assert y.shape == z.shape == (0, 16)
+    dx, dw, db, _ = psr.linear_bwd(y, x, w)
+    assert dx.shape == (0, 64) and not dw.any() and not db.any() and dw.shape == (16, 64) and db.shape == (16,)
+
+
+def test_linear_rows_do_not_mix(psr):
+    # a NaN or an infinity in a row of x stays in that row, one in a row of w in that column, at the edges of tiles too
+    need_gpu()
+    for M, N, K in ((1, 264, 136), (20, 264, 136), (300, 264, 136)):
+        g = torch.Generator().manual_seed(N)
+        x, w = randn(g, (M, K), "bf16"), randn(g, (N, K), "bf16")
+        x[M - 1, K - 1] = float("nan")
+        w[N - 1, 0] = float("inf")
+        y = psr.linear(x, w)[0]
+        bad = ~torch.isfinite(y)
+        want = torch.zeros_like(bad)
+        want[M - 1] = True
+        want[:, N - 1] = True
+        assert torch.equal(bad, want)
+
+
+def test_linear_is_deterministic_and_graph_safe(psr):
+    need_gpu()
+    g = torch.Generator().manual_seed(2)
+    for M, N, K in ((1, 1032, 2056), (24, 520, 4104), (400, 520, 264)):
+        x, w, r = randn(g, (M, K), "bf16"), randn(g, (N, K), "bf16", K**-0.5), randn(g, (M, N), "bf16")
+        want = psr.linear(x, w, None, r, activation="silu", save_z=True)[:2]
+        dwant = psr.linear_bwd(r, x, w, want[1], activation="silu")[:3]
+        for _ in range(3):
+            assert all(torch.equal(a, b) for a, b in zip(psr.linear(x, w, None, r, activation="silu", save_z=True)[:2], want))
+            assert all(torch.equal(a, b) for a, b in zip(psr.linear_bwd(r, x, w, want[1], activation="silu")[:3], dwant))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        got = psr.linear(x, w, None, r, activation="silu", save_z=True, stream=side)[:2]
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        out = [torch.zeros_like(v) for v in (*want, *dwant)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            psr.linear(x, w, None, r, activation="silu", out=out[0], z=out[1])
+            psr.linear_bwd(r, x, w, out[1], activation="silu", dx=out[2], dw=out[3], db=out[4])
+        for _ in range(2):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, (*want, *dwant)))
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_linear_bwd_is_the_gradient(psr, act):
+    # against difference quotients of the oracle's forward along random directions
+    need_gpu()
+    g = torch.Generator().manual_seed(6)
+    M, N, K = 33, 40, 24
+    x, w, b, dy = (randn(g, s, "f16", std) for s, std in (((M, K), 1), ((N, K), K**-0.5), ((N,), 0.5), ((M, N), 1)))
+    y, z, _ = psr.linear(x, w, b, activation=act, save_z=True)
+    grads = [f64(v) for v in psr.linear_bwd(dy, x, w, z, activation=act)[:3]]
+    args = [f64(v) for v in (x, w, b)]
+    rng = np.random.default_rng(1)
+    for i in range(3):
+        step = rng.standard_normal(args[i].shape)
+        f = lambda h: (ol.linear(*[v + (h * step if j == i else 0) for j, v in enumerate(args)], None, act)[0] * f64(dy)).sum()
+        want = (f(1e-5) - f(-1e-5)) / 2e-5
+        # z, dz and the gradients are fp16 (2^-11 each, random signs); relu changes slope where a difference crosses 0
+        assert abs((grads[i] * step).sum() - want) <= 2.0**-8 * np.linalg.norm(grads[i]) * 4, (act, i)
