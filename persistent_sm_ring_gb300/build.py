@@ -17,7 +17,7 @@ SOURCES = [os.path.join(CSRC, f) for f in ("psr_ring_attn.cu", "psr_ring_attn_bw
                                             "psr_noalloc.cu", "psr_rotary.cu", "psr_linear.cu", "psr_kv4.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f)
                   for f in ("psr_device.cuh", "psr_schedule.h", "psr_control.cuh", "psr_gemm_tile.cuh", "psr_internal.h",
-                            "psr_host.h")] + [
+                            "psr_host.h", "psr_linear_mma.cuh")] + [
     os.path.join(ROOT, "include", "psr.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 _lock = threading.Lock()

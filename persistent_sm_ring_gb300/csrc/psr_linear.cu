@@ -1,67 +1,26 @@
 // The linear layer y = act(x w^T + bias) + residual and its gradients on sm_103a.
+//
+// Operands whose rows start on 16-byte boundaries go to the tcgen05 products of psr_linear_mma.cuh; others (odd
+// strides, odd offsets) to a plain tiled product on the fp32 units.
 #include <cmath>
 #include <cstring>
 
 #include "psr_control.cuh"
 #include "psr_host.h"
+#include "psr_linear_mma.cuh"
 
 namespace psr {
 namespace linear {
 
-// act(z) and act'(z) in fp32
-template <int ACT>
-__device__ __forceinline__ float act_fwd(float z) {
-  if constexpr (ACT == PSR_ACT_RELU) return z > 0.f ? z : (z == z ? 0.f : z);
-  if constexpr (ACT == PSR_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-  if constexpr (ACT == PSR_ACT_GELU_TANH)
-    return 0.5f * z * (1.f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
-  if constexpr (ACT == PSR_ACT_SILU) return z / (1.f + expf(-z));
-  return z;
-}
-template <int ACT>
-__device__ __forceinline__ float act_slope(float z) {
-  if constexpr (ACT == PSR_ACT_RELU) return z > 0.f ? 1.f : 0.f;
-  if constexpr (ACT == PSR_ACT_GELU)
-    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * expf(-0.5f * z * z);
-  if constexpr (ACT == PSR_ACT_GELU_TANH) {
-    const float u = 0.79788456080286536f * (z + 0.044715f * z * z * z);
-    const float t = tanhf(u);
-    return 0.5f * (1.f + t) + 0.5f * z * (1.f - t * t) * 0.79788456080286536f * (1.f + 0.134145f * z * z);
-  }
-  if constexpr (ACT == PSR_ACT_SILU) {
-    const float s = 1.f / (1.f + expf(-z));
-    return s * (1.f + z * (1.f - s));
-  }
-  return 1.f;
-}
-
-// What becomes of an fp32 sum: z = sum + bias, y = act(z) + residual (or a plain gradient: act none, no bias).
-struct Epilogue {
-  const void* bias;
-  const void* res;
-  void* y;
-  void* z;
-  long long ldr, ldy, ldz;
-};
-
-template <class T, int ACT>
-__device__ __forceinline__ void finish(const Epilogue& e, long long i, int j, float v) {
-  if (e.bias) v += to_f32(static_cast<const T*>(e.bias)[j]);
-  if (e.z) static_cast<T*>(e.z)[i * e.ldz + j] = from_f32<T>(v);
-  v = act_fwd<ACT>(v);
-  if (e.res) v += to_f32(static_cast<const T*>(e.res)[i * e.ldr + j]);
-  static_cast<T*>(e.y)[i * e.ldy + j] = from_f32<T>(v);
-}
-
 // C[i][j] = sum_k A(i, k) B(j, k), A(i, k) = a[i lda + k] (or a[k lda + i] with AT), B alike: 64 x 64 tiles in
 // shared memory, 4 x 4 sums a thread.
-template <class T, int ACT, bool AT, bool BT>
+template <class T, bool AT, bool BT>
 __global__ void __launch_bounds__(256)
     simple_gemm(const T* __restrict__ a, long long lda, const T* __restrict__ b, long long ldb, int M, int N, int K,
                 const Epilogue e) {
   __shared__ float sa[16][68], sb[16][68];
-  const long long i0 = (long long)blockIdx.y * 64;
-  const int j0 = blockIdx.x * 64;
+  const long long i0 = (long long)blockIdx.x * 64;
+  const int j0 = blockIdx.y * 64;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   float acc[4][4] = {};
   for (int k0 = 0; k0 < K; k0 += 16) {
@@ -85,16 +44,16 @@ __global__ void __launch_bounds__(256)
   }
   for (int r = 0; r < 4; ++r)
     for (int c = 0; c < 4; ++c)
-      if (i0 + ty * 4 + r < M && j0 + tx * 4 + c < N) finish<T, ACT>(e, i0 + ty * 4 + r, j0 + tx * 4 + c, acc[r][c]);
+      if (i0 + ty * 4 + r < M && j0 + tx * 4 + c < N) finish(e, i0 + ty * 4 + r, j0 + tx * 4 + c, acc[r][c]);
 }
 
-template <class T, int ACT, bool AT, bool BT>
+template <class T, bool AT, bool BT>
 static int launch_simple(const void* a, long long lda, const void* b, long long ldb, int M, int N, int K,
                          const Epilogue& e, cudaStream_t st) {
   if (M == 0) return PSR_OK;
-  const dim3 grid((unsigned)((N + 63) / 64), (unsigned)((M + 63) / 64));
+  const dim3 grid((unsigned)((M + 63) / 64), (unsigned)((N + 63) / 64));
   if (grid.y > 65535) return PSR_ERR_UNSUPPORTED;
-  simple_gemm<T, ACT, AT, BT><<<grid, 256, 0, st>>>(static_cast<const T*>(a), lda, static_cast<const T*>(b), ldb, M, N,
+  simple_gemm<T, AT, BT><<<grid, 256, 0, st>>>(static_cast<const T*>(a), lda, static_cast<const T*>(b), ldb, M, N,
                                                    K, e);
   return launch_status();
 }
@@ -104,20 +63,20 @@ static int launch_simple(const void* a, long long lda, const void* b, long long 
 // ------------------------------------------------------------------------------------------------
 constexpr int kDzRows = 64;  // rows of a chunk
 
-template <class T, int ACT>
+template <class T>
 __global__ void dz_kernel(const T* __restrict__ dy, long long ldy, const T* __restrict__ z, long long ldz, T* dz,
-                          long long lddz, float* partial, int M, int N) {
-  const int j = blockIdx.x * 256 + threadIdx.x;
+                          long long lddz, float* partial, int M, int N, int act) {
+  const int j = blockIdx.y * 256 + threadIdx.x;
   if (j >= N) return;
-  const long long i0 = (long long)blockIdx.y * kDzRows;
+  const long long i0 = (long long)blockIdx.x * kDzRows;
   float sum = 0.f;
   for (int r = 0; r < kDzRows && i0 + r < M; ++r) {
     float v = to_f32(dy[(i0 + r) * ldy + j]);
-    if constexpr (ACT != PSR_ACT_NONE) v *= act_slope<ACT>(to_f32(z[(i0 + r) * ldz + j]));
+    if (act != PSR_ACT_NONE) v *= act_slope(act, to_f32(z[(i0 + r) * ldz + j]));
     if (dz) dz[(i0 + r) * lddz + j] = from_f32<T>(v);
     sum += v;
   }
-  if (partial) partial[(long long)blockIdx.y * N + j] = sum;
+  if (partial) partial[(long long)blockIdx.x * N + j] = sum;
 }
 
 template <class T>
@@ -136,7 +95,7 @@ struct Sizes {
   long long ldx, ldw, ldr, ldy, ldz;
   int chunks;     // row chunks of the column sums
   long long lddz; // row stride of dz in the workspace
-  size_t dz, partial, total_fwd, total_bwd;
+  size_t stream, dz, partial, total_fwd, total_bwd;
 };
 
 static size_t au(size_t x) { return (x + 255) / 256 * 256; }
@@ -153,6 +112,8 @@ static int sizes(const psr_linear_shape* sh, Sizes& s) {
   s.chunks = (sh->M + kDzRows - 1) / kDzRows;
   s.lddz = (sh->N + 7) / 8 * 8;
   size_t off = 256;  // control block
+  s.stream = off;
+  off = au(off + stream_partial_bytes(sh->M));
   s.total_fwd = off;
   s.dz = off;
   if (sh->act != PSR_ACT_NONE) off = au(off + (size_t)sh->M * s.lddz * 2);
@@ -162,59 +123,85 @@ static int sizes(const psr_linear_shape* sh, Sizes& s) {
   return PSR_OK;
 }
 
-template <class T, int ACT>
-static int forward(const psr_linear_shape* sh, const Sizes& s, const void* x, const void* w, const Epilogue& e,
-                   cudaStream_t st) {
-  return launch_simple<T, ACT, false, false>(x, s.ldx, w, s.ldw, sh->M, sh->N, sh->K, e, st);
-}
+struct Launch {
+  int dev, n_sm;
+  Ctrl* ctrl;
+  float* stream_partial;
+  unsigned long long timeout_ns;
+  cudaStream_t st;
+};
 
-template <class T, int ACT>
-static int make_dz(const psr_linear_shape* sh, const Sizes& s, const void* dy, const void* z, void* dz, float* partial,
-                   cudaStream_t st) {
-  if (sh->M == 0) return PSR_OK;
-  const dim3 grid((unsigned)((sh->N + 255) / 256), (unsigned)s.chunks);
-  if (grid.y > 65535) return PSR_ERR_UNSUPPORTED;
-  dz_kernel<T, ACT><<<grid, 256, 0, st>>>(static_cast<const T*>(dy), s.ldy, static_cast<const T*>(z), s.ldz,
-                                         static_cast<T*>(dz), s.lddz, partial, sh->M, sh->N);
-  return launch_status();
+// C = A B^T with A [M][K] (or AMN: [K][M]) and B [N][K] (or BMN: [K][N]).  W is the operand that streams when
+// there are few rows of A.
+template <class T, bool AMN, bool BMN>
+static int product(const Operands& o, Epilogue e, const Launch& l) {
+  if (o.M == 0) return PSR_OK;
+  if (!mappable(o.a, AMN ? o.K : o.M, o.lda) || !mappable(o.b, BMN ? o.K : o.N, o.ldb))
+    return launch_simple<T, AMN, BMN>(o.a, o.lda, o.b, o.ldb, o.M, o.N, o.K, e, l.st);
+  auto flat = [&](const void* p, long long ld) { return !p || (aligned_to(p, 16) && (o.M == 1 || ld % 8 == 0)); };
+  e.vec = o.N % 8 == 0 && flat(e.y, e.ldy) && flat(e.z, e.ldz) && flat(e.res, e.ldr) && flat(e.bias, 0);
+  if constexpr (!AMN)
+    if (o.M <= kStreamMaxM) return launch_stream<BMN>(o, e, l.stream_partial, l.ctrl, l.timeout_ns, l.dev, l.n_sm, l.st);
+  // 512 columns feed the tensor cores best; 256 where their finer grain saves more than that
+  const long long rows = (o.M + 255) / 256, n_pairs = l.n_sm / 2;
+  auto waves = [&](long long cols) { return (rows * ((o.N + cols - 1) / cols) + n_pairs - 1) / n_pairs; };
+  if (100 * waves(512) * 2 <= 113 * waves(256))
+    return launch_pair<2, AMN, BMN>(o, e, l.ctrl, l.timeout_ns, l.dev, l.n_sm, l.st);
+  return launch_pair<1, AMN, BMN>(o, e, l.ctrl, l.timeout_ns, l.dev, l.n_sm, l.st);
 }
 
 template <class T>
 static int backward(const psr_linear_shape* sh, const Sizes& s, const void* dy, const void* z, const void* x,
-                    const void* w, void* dx, void* dw, void* db, uint8_t* ws, cudaStream_t st) {
+                    const void* w, void* dx, void* dw, void* db, uint8_t* ws, const Launch& l) {
   const bool act = sh->act != PSR_ACT_NONE;
   void* dz = act ? ws + s.dz : nullptr;
-  float* partial = db ? reinterpret_cast<float*>(ws + s.partial) : nullptr;
   int rc = PSR_OK;
-  if (act || db) {
-    switch (sh->act) {
-      case PSR_ACT_RELU: rc = make_dz<T, PSR_ACT_RELU>(sh, s, dy, z, dz, partial, st); break;
-      case PSR_ACT_GELU: rc = make_dz<T, PSR_ACT_GELU>(sh, s, dy, z, dz, partial, st); break;
-      case PSR_ACT_GELU_TANH: rc = make_dz<T, PSR_ACT_GELU_TANH>(sh, s, dy, z, dz, partial, st); break;
-      case PSR_ACT_SILU: rc = make_dz<T, PSR_ACT_SILU>(sh, s, dy, z, dz, partial, st); break;
-      default: rc = make_dz<T, PSR_ACT_NONE>(sh, s, dy, z, dz, partial, st);
-    }
-    if (rc != PSR_OK) return rc;
+  if (sh->M > 0 && (db || (act && (dx || dw)))) {
+    const dim3 grid((unsigned)s.chunks, (unsigned)((sh->N + 255) / 256));
+    if (grid.y > 65535) return PSR_ERR_UNSUPPORTED;
+    dz_kernel<T><<<grid, 256, 0, l.st>>>(static_cast<const T*>(dy), s.ldy, static_cast<const T*>(z), s.ldz,
+                                         static_cast<T*>(dz), s.lddz,
+                                         db ? reinterpret_cast<float*>(ws + s.partial) : nullptr, sh->M, sh->N, sh->act);
+    if ((rc = launch_status()) != PSR_OK) return rc;
   }
   if (db) {
-    db_kernel<T><<<(unsigned)((sh->N + 255) / 256), 256, 0, st>>>(partial, s.chunks, sh->N, static_cast<T*>(db));
+    db_kernel<T><<<(unsigned)((sh->N + 255) / 256), 256, 0, l.st>>>(reinterpret_cast<float*>(ws + s.partial), s.chunks,
+                                                                   sh->N, static_cast<T*>(db));
     if ((rc = launch_status()) != PSR_OK) return rc;
   }
   const void* g = act ? dz : dy;
   const long long ldg = act ? s.lddz : s.ldy;
   Epilogue e = {};
+  e.half = sh->type == PSR_F16;
+  e.ldy = sh->K;
   if (dx) {
     e.y = dx;
-    e.ldy = sh->K;
-    rc = launch_simple<T, PSR_ACT_NONE, false, true>(g, ldg, w, s.ldw, sh->M, sh->K, sh->N, e, st);
-    if (rc != PSR_OK) return rc;
+    if ((rc = product<T, false, true>({g, ldg, w, s.ldw, sh->M, sh->K, sh->N}, e, l)) != PSR_OK) return rc;
   }
   if (dw) {
     e.y = dw;
-    e.ldy = sh->K;
-    rc = launch_simple<T, PSR_ACT_NONE, true, true>(g, ldg, x, s.ldx, sh->N, sh->K, sh->M, e, st);
+    if (sh->M == 0) {
+      if (cudaMemsetAsync(dw, 0, (size_t)sh->N * sh->K * 2, l.st) != cudaSuccess) return PSR_ERR_CUDA;
+    } else {
+      rc = product<T, true, true>({g, ldg, x, s.ldx, sh->N, sh->K, sh->M}, e, l);
+    }
   }
   return rc;
+}
+
+static int launch_of(void* workspace, const Sizes& s, int timeout_ms, void* stream, Launch& l) {
+  const int rc = check_device(&l.n_sm);
+  if (rc != PSR_OK) return rc;
+  if (cudaGetDevice(&l.dev) != cudaSuccess) return PSR_ERR_CUDA;
+  l.ctrl = static_cast<Ctrl*>(workspace);
+  l.stream_partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + s.stream);
+  l.timeout_ns = (unsigned long long)(timeout_ms > 0 ? timeout_ms : 2000) * 1000000ull;
+  l.st = static_cast<cudaStream_t>(stream);
+  if (cudaMemsetAsync(workspace, 0, sizeof(Ctrl), l.st) != cudaSuccess) {
+    cudaGetLastError();
+    return PSR_ERR_CUDA;
+  }
+  return PSR_OK;
 }
 
 }  // namespace linear
@@ -241,21 +228,15 @@ int psr_linear(const psr_linear_shape* sh, const void* x, const void* w, const v
   int rc = sizes(sh, s);
   if (rc != PSR_OK) return rc;
   if (ws_bytes < s.total_fwd) return PSR_ERR_ARG;
-  if ((rc = check_device(nullptr)) != PSR_OK) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, 256, st) != cudaSuccess) return PSR_ERR_CUDA;
-  const Epilogue e = {bias, residual, y, z, s.ldr, s.ldy, s.ldz};
-  auto go = [&](auto tag) {
-    using T = decltype(tag);
-    switch (sh->act) {
-      case PSR_ACT_RELU: return forward<T, PSR_ACT_RELU>(sh, s, x, w, e, st);
-      case PSR_ACT_GELU: return forward<T, PSR_ACT_GELU>(sh, s, x, w, e, st);
-      case PSR_ACT_GELU_TANH: return forward<T, PSR_ACT_GELU_TANH>(sh, s, x, w, e, st);
-      case PSR_ACT_SILU: return forward<T, PSR_ACT_SILU>(sh, s, x, w, e, st);
-      default: return forward<T, PSR_ACT_NONE>(sh, s, x, w, e, st);
-    }
-  };
-  return sh->type == PSR_BF16 ? go(__nv_bfloat16()) : go(__half());
+  Launch l;
+  if ((rc = launch_of(workspace, s, timeout_ms, stream, l)) != PSR_OK) return rc;
+  Epilogue e = {};
+  e.bias = bias; e.res = residual; e.y = y; e.z = z;
+  e.ldr = s.ldr; e.ldy = s.ldy; e.ldz = s.ldz;
+  e.act = sh->act;
+  e.half = sh->type == PSR_F16;
+  const Operands o = {x, s.ldx, w, s.ldw, sh->M, sh->N, sh->K};
+  return sh->type == PSR_BF16 ? product<__nv_bfloat16, false, false>(o, e, l) : product<__half, false, false>(o, e, l);
 }
 
 int psr_linear_bwd(const psr_linear_shape* sh, const void* dy, const void* z, const void* x, const void* w, void* dx,
@@ -268,12 +249,11 @@ int psr_linear_bwd(const psr_linear_shape* sh, const void* dy, const void* z, co
   int rc = sizes(sh, s);
   if (rc != PSR_OK) return rc;
   if (ws_bytes < s.total_bwd) return PSR_ERR_ARG;
-  if ((rc = check_device(nullptr)) != PSR_OK) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, 256, st) != cudaSuccess) return PSR_ERR_CUDA;
+  Launch l;
+  if ((rc = launch_of(workspace, s, timeout_ms, stream, l)) != PSR_OK) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  return sh->type == PSR_BF16 ? backward<__nv_bfloat16>(sh, s, dy, z, x, w, dx, dw, db, ws, st)
-                              : backward<__half>(sh, s, dy, z, x, w, dx, dw, db, ws, st);
+  return sh->type == PSR_BF16 ? backward<__nv_bfloat16>(sh, s, dy, z, x, w, dx, dw, db, ws, l)
+                              : backward<__half>(sh, s, dy, z, x, w, dx, dw, db, ws, l);
 }
 
 }  // extern "C"

@@ -1,0 +1,810 @@
+// The matrix products of the linear layer on tcgen05 (sm_103a), C[i][j] = sum_k A(i, k) B(j, k).
+//
+// Either operand may be stored K-major (A[i][k]) or MN-major (A[k][i]); the shared-memory descriptors and the
+// instruction descriptor take both, so no operand is transposed in memory: forward x w^T is K-major twice,
+// dx = dz w has w MN-major, dw = dz^T x has both MN-major.  Two kernels:
+//
+//  * pair_gemm: a pair of CTAs (cta_group::2) computes a 256 x 256 H tile, each CTA 128 rows and 128 columns of
+//    each 256-column half.  H = 2 fills all 512 tensor memory columns and moves 48 B/clk per SM at the tensor rate
+//    (64 B/clk for H = 1, above what TMA tile loads land); H = 1 double-buffers the accumulator.
+//  * stream_gemm: for few rows of A.  The output is computed transposed, W's rows on the 128 tensor memory lanes
+//    and the tokens in the columns, so that W streams through once.  The (tile, K step) units are dealt out
+//    evenly over one CTA per SM; a tile whose K range is split leaves fp32 partials that a second kernel joins.
+#pragma once
+#include <mutex>
+#include <type_traits>
+
+#include "psr_control.cuh"
+#include "psr_device.cuh"
+#include "psr_gemm_tile.cuh"
+#include "psr_host.h"
+
+namespace psr {
+namespace linear {
+
+constexpr int kBK = 64;  // K per stage: one 128-byte swizzle atom of 16-bit elements
+constexpr uint32_t kSlack = 4;
+enum : uint32_t { SITE_FULL = 41, SITE_EMPTY = 42, SITE_ACC = 43, SITE_ACC_EMPTY = 44, SITE_LAUNCH = 45 };
+
+// What becomes of an fp32 sum: z = sum + bias, y = act(z) + residual.
+struct Epilogue {
+  const void* bias;
+  const void* res;
+  void* y;
+  void* z;
+  long long ldr, ldy, ldz;
+  int act;
+  int half;  // fp16 (0: bf16)
+  int vec;   // every row and column offset that the tiles use is 16-byte aligned
+};
+
+// act(z) and act'(z) in fp32
+__device__ __forceinline__ float act_fwd(int act, float z) {
+  switch (act) {
+    case PSR_ACT_RELU: return z > 0.f ? z : (z == z ? 0.f : z);
+    case PSR_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    case PSR_ACT_GELU_TANH: return 0.5f * z * (1.f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
+    case PSR_ACT_SILU: return z / (1.f + expf(-z));
+    default: return z;
+  }
+}
+__device__ __forceinline__ float act_slope(int act, float z) {
+  switch (act) {
+    case PSR_ACT_RELU: return z > 0.f ? 1.f : 0.f;
+    case PSR_ACT_GELU:
+      return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+    case PSR_ACT_GELU_TANH: {
+      const float t = tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z));
+      return 0.5f * (1.f + t) + 0.5f * z * (1.f - t * t) * 0.79788456080286536f * (1.f + 0.134145f * z * z);
+    }
+    case PSR_ACT_SILU: {
+      const float s = 1.f / (1.f + expf(-z));
+      return s * (1.f + z * (1.f - s));
+    }
+    default: return 1.f;
+  }
+}
+
+// 16-bit elements of a type known at run time
+__device__ __forceinline__ float load16(const void* p, long long i, int half) {
+  return half ? __half2float(static_cast<const __half*>(p)[i]) : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+__device__ __forceinline__ void store16(void* p, long long i, int half, float v) {
+  if (half) static_cast<__half*>(p)[i] = __float2half_rn(v);
+  else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, int half) {
+  if (!half) return pack_bf16x2(lo, hi);
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void unpack16(uint32_t v, int half, float& lo, float& hi) {
+  if (half) {
+    const float2 f = __half22float2(*reinterpret_cast<__half2*>(&v));
+    lo = f.x;
+    hi = f.y;
+  } else {
+    lo = __uint_as_float(v << 16);
+    hi = __uint_as_float(v & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ void finish(const Epilogue& e, long long i, int j, float v) {
+  if (e.bias) v += load16(e.bias, j, e.half);
+  if (e.z) store16(e.z, i * e.ldz + j, e.half, v);
+  v = act_fwd(e.act, v);
+  if (e.res) v += load16(e.res, i * e.ldr + j, e.half);
+  store16(e.y, i * e.ldy + j, e.half, v);
+}
+
+// Instruction descriptor: idesc_bf16_f32 with either operand MN-major and fp16 operands if `half`.
+__host__ __device__ constexpr uint32_t idesc16(uint32_t M, uint32_t N, bool a_mn, bool b_mn, bool half) {
+  return (idesc_bf16_f32(M, N, b_mn) | ((a_mn ? 1u : 0u) << 15)) & ~(half ? ((1u << 7) | (1u << 10)) : 0u);
+}
+
+// Descriptor low word of the 16-element K step kk of an operand tile of one stage: K-major rows of 128 bytes, or
+// (MN) boxes of 64 K rows x 64 columns, 8 KiB apart.
+template <bool MN>
+__device__ __forceinline__ uint32_t operand_lo(uint32_t tile, int kk) {
+  return MN ? sdesc_lo(tile + kk * 2048, 8192) : sdesc_lo(tile + kk * 32, 16);
+}
+
+// ================================================================================================
+// pair_gemm
+// ================================================================================================
+constexpr int kRows = 128;           // A rows, and B rows of a half, that one CTA loads
+constexpr int kHalf = kRows * kBK * 2;
+constexpr int kPairWarps = 12, kPairThreads = kPairWarps * 32, kEpiWarps = 8;
+constexpr int kEpiWarpBytes = 4096;  // one warp's 32 rows x 128 bytes
+template <int H>
+struct PairCfg {
+  static constexpr int kStage = (1 + H) * kHalf;
+  static constexpr int kStages = H == 2 ? 4 : 6;
+  static constexpr int kEpiOff = kStage * kStages;
+  static constexpr int kSmem = 1024 + kEpiOff + kEpiWarps * kEpiWarpBytes;
+};
+static_assert(PairCfg<1>::kSmem + 1024 <= 232448 && PairCfg<2>::kSmem + 1024 <= 232448, "shared memory");
+
+struct PairParams {
+  int M, N, n_k;
+  int tiles_m, tiles_n;   // 256 rows, 256 H columns
+  int group;              // tile rows of a raster group
+  uint32_t idesc;
+  Epilogue e;
+  Ctrl* ctrl;
+  unsigned long long timeout_ns;
+};
+
+struct PairSmem {
+  uint64_t full[6], empty[6], acc_full[2], acc_empty[2], drain;
+  uint32_t tmem_base;
+  uint32_t peer_fills;
+  volatile uint32_t abort;
+};
+
+// Tile t -> (row block, column block): groups of `group` tile rows, columns inside a group, rows fastest, so that the
+// tiles in flight at once share few rows of either operand.
+__device__ __forceinline__ void pair_tile(const PairParams& p, int t, int& tm, int& tn) {
+  const int per = p.group * p.tiles_n, g = t / per, r = t - g * per;
+  const int rows = min(p.group, p.tiles_m - g * p.group);
+  tn = r / rows;
+  tm = g * p.group + (r - tn * rows);
+}
+
+// One 128-row operand tile of a stage.
+template <bool MN>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* m, int k, int row, uint32_t bar) {
+  if constexpr (MN) {
+    tma_load_2d_pair(dst, m, row, k, bar);
+    tma_load_2d_pair(dst + 8192, m, row + 64, k, bar);
+  } else {
+    tma_load_2d_pair(dst, m, k, row, bar);
+  }
+}
+
+// The warp's 32 rows x 64 columns at (i0, j0), row `lane` in v: bias, z, activation, residual, y.
+// ACT: the epilogue may have an activation (the gradients have none).
+template <bool ACT>
+__device__ __forceinline__ void pair_store(const PairParams& p, uint8_t* stage, int i0, int j0, uint32_t* v) {
+  const Epilogue& e = p.e;
+  const int lane = threadIdx.x % 32;
+  const int rows = min(32, p.M - i0), cols = min(64, p.N - j0);
+  if (rows <= 0 || cols <= 0) return;
+  if (!e.vec) {
+    if (lane < rows)
+#pragma unroll
+      for (int c = 0; c < 64; ++c)
+        if (c < cols) finish(e, i0 + lane, j0 + c, __uint_as_float(v[c]));
+    return;
+  }
+  // cols is a multiple of 8 here
+  // 16-byte chunks of a 128-byte row, XOR-swizzled by the row: both passes are free of bank conflicts
+  auto copy_out = [&](void* base, long long ld) {
+    __syncwarp();
+    uint8_t* g = static_cast<uint8_t*>(base) + ((long long)i0 * ld + j0) * 2;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = k * 4 + lane / 8, c = lane % 8;
+      const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r % 8)) * 16));
+      if (r < rows && c * 8 < cols) *reinterpret_cast<uint4*>(g + (long long)r * ld * 2 + c * 16) = w;
+    }
+    __syncwarp();
+  };
+  auto chunk = [&](int j) { return reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane % 8)) * 16)); };
+  if (e.bias) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j * 8 < cols) {
+        const uint4 b = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.bias) + j0 + j * 8);
+        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float lo, hi;
+          unpack16(w[q], e.half, lo, hi);
+          v[j * 8 + 2 * q] = __float_as_uint(__uint_as_float(v[j * 8 + 2 * q]) + lo);
+          v[j * 8 + 2 * q + 1] = __float_as_uint(__uint_as_float(v[j * 8 + 2 * q + 1]) + hi);
+        }
+      }
+    }
+  }
+  auto put = [&]() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        w[q] = pack16(__uint_as_float(v[j * 8 + 2 * q]), __uint_as_float(v[j * 8 + 2 * q + 1]), e.half);
+      *chunk(j) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  };
+  if (e.z) {
+    put();
+    copy_out(e.z, e.ldz);
+  }
+  if constexpr (ACT) {
+    auto apply = [&](auto act) {
+#pragma unroll
+      for (int c = 0; c < 64; ++c) v[c] = __float_as_uint(act_fwd(decltype(act)::value, __uint_as_float(v[c])));
+    };
+    switch (e.act) {
+      case PSR_ACT_RELU: apply(std::integral_constant<int, PSR_ACT_RELU>()); break;
+      case PSR_ACT_GELU: apply(std::integral_constant<int, PSR_ACT_GELU>()); break;
+      case PSR_ACT_GELU_TANH: apply(std::integral_constant<int, PSR_ACT_GELU_TANH>()); break;
+      case PSR_ACT_SILU: apply(std::integral_constant<int, PSR_ACT_SILU>()); break;
+      default: break;
+    }
+  }
+  if (e.res) {
+    const uint8_t* g = static_cast<const uint8_t*>(e.res) + ((long long)i0 * e.ldr + j0) * 2;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = k * 4 + lane / 8, c = lane % 8;
+      if (r < rows && c * 8 < cols)
+        *reinterpret_cast<uint4*>(stage + r * 128 + ((c ^ (r % 8)) * 16)) =
+            *reinterpret_cast<const uint4*>(g + (long long)r * e.ldr * 2 + c * 16);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j * 8 < cols) {
+        const uint4 b = *chunk(j);
+        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float lo, hi;
+          unpack16(w[q], e.half, lo, hi);
+          v[j * 8 + 2 * q] = __float_as_uint(__uint_as_float(v[j * 8 + 2 * q]) + lo);
+          v[j * 8 + 2 * q + 1] = __float_as_uint(__uint_as_float(v[j * 8 + 2 * q + 1]) + hi);
+        }
+      }
+    }
+    __syncwarp();
+  }
+  put();
+  copy_out(e.y, e.ldy);
+}
+
+template <int H, bool AMN, bool BMN>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    pair_gemm(const __grid_constant__ PairParams p, const __grid_constant__ CUtensorMap ma,
+              const __grid_constant__ CUtensorMap mb) {
+  using C = PairCfg<H>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ PairSmem sc;
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t smem_base = (raw + 1023u) & ~1023u;
+  uint8_t* epi = smem_raw + (smem_base - raw) + C::kEpiOff;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  uint32_t n_rank;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n_rank));
+  if (n_rank != 2u) {  // no caller launches it without pairs
+    if (threadIdx.x == 0) raise_error(p, SITE_LAUNCH);
+    return;
+  }
+  const uint32_t rank = cluster_ctarank();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&sc.full[s], 1);
+      mbar_init(&sc.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sc.acc_full[b], 1);
+      mbar_init(&sc.acc_empty[b], 2 * kEpiWarps);
+    }
+    mbar_init(&sc.drain, 1);
+    sc.peer_fills = 0;
+    sc.abort = 0;
+    fence_barrier_init();
+    prefetch_tmap(&ma);
+    prefetch_tmap(&mb);
+  }
+  if (warp == 1) {
+    tmem_alloc_cg<2>(&sc.tmem_base, 512);
+    tmem_relinquish_cg<2>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+
+  const int n_tiles = p.tiles_m * p.tiles_n;
+  const int pair = blockIdx.x / 2, n_pairs = gridDim.x / 2;
+  uint32_t fills = 0;  // thread 0: stages this CTA filled
+  if (warp == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int t = pair; t < n_tiles && ok; t += n_pairs) {
+        int tm, tn;
+        pair_tile(p, t, tm, tn);
+        const int arow = tm * 256 + (int)rank * kRows, brow = tn * 256 * H + (int)rank * kRows;
+        for (int ks = 0; ks < p.n_k; ++ks) {
+          const uint32_t s = fills % C::kStages, use = fills / C::kStages;
+          if (use > 0 && !wait_bar(&sc.empty[s], (use - 1) & 1u, p, &sc, SITE_EMPTY, kSlack)) { ok = false; break; }
+          if (rank == 0) mbar_expect_tx(&sc.full[s], 2 * C::kStage);  // both CTAs' bytes
+          const uint32_t bar = mapa_shared(smem_u32(&sc.full[s]), 0);
+          const uint32_t base = smem_base + s * C::kStage;
+          load_operand<AMN>(base, &ma, ks * kBK, arow, bar);
+#pragma unroll
+          for (int h = 0; h < H; ++h) load_operand<BMN>(base + (1 + h) * kHalf, &mb, ks * kBK, brow + h * 256, bar);
+          ++fills;
+        }
+      }
+      if (!ok) sc.abort = 1;
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t kHi = sdesc_hi_sw128(1024);
+      uint32_t c = 0, u = 0;  // stages consumed, accumulator halves begun
+      bool ok = true;
+      for (int t = pair; t < n_tiles && ok; t += n_pairs, u += H) {
+        for (int ks = 0; ks < p.n_k && ok; ++ks, ++c) {
+          const uint32_t s = c % C::kStages;
+          if (!wait_bar(&sc.full[s], (c / C::kStages) & 1u, p, &sc, SITE_FULL, kSlack)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t base = smem_base + s * C::kStage;
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            const uint32_t slot = (u + h) % 2;
+            if (ks == 0) {  // the half's previous sums have been read back
+              if (u + h >= 2 &&
+                  !wait_bar<true>(&sc.acc_empty[slot], ((u + h) / 2 - 1) & 1u, p, &sc, SITE_ACC_EMPTY, kSlack)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+            }
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              mma_ss_cg<2>(sc.tmem_base + slot * 256, operand_lo<AMN>(base, kk), kHi,
+                           operand_lo<BMN>(base + (1 + h) * kHalf, kk), kHi, p.idesc, (ks > 0 || kk > 0) ? 1u : 0u);
+          }
+          if (!ok) break;
+          mma_commit_cg<2>(&sc.empty[s], 3);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int h = 0; h < H; ++h) mma_commit_cg<2>(&sc.acc_full[(u + h) % 2], 3);
+      }
+      if (!ok) sc.abort = 1;
+    }
+  } else if (warp >= 4) {
+    uint8_t* stage = epi + (warp - 4) * kEpiWarpBytes;
+    const int quarter = warp % 4, chalf = (warp - 4) / 4;
+    uint32_t u = 0;
+    bool ok = true;
+    for (int t = pair; t < n_tiles && ok; t += n_pairs) {
+      int tm, tn;
+      pair_tile(p, t, tm, tn);
+      const int i0 = tm * 256 + (int)rank * kRows + quarter * 32;
+#pragma unroll 1
+      for (int h = 0; h < H; ++h, ++u) {
+        const uint32_t slot = u % 2;
+        ok = __all_sync(0xffffffffu, wait_bar(&sc.acc_full[slot], (u / 2) & 1u, p, &sc, SITE_ACC, kSlack));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tacc = sc.tmem_base + ((uint32_t)(quarter * 32) << 16) + slot * 256 + chalf * 128;
+        const int j0 = tn * 256 * H + h * 256 + chalf * 128;
+#pragma unroll 1
+        for (int cb = 0; cb < 2; ++cb) {
+          uint32_t v[64];
+          tmem_ld64(tacc + cb * 64, v);
+          tmem_ld_wait();
+          if (cb == 1) {  // this warp's share of the half is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (rank == 0) mbar_arrive(&sc.acc_empty[slot]);
+              else mbar_arrive_cluster(mapa_shared(smem_u32(&sc.acc_empty[slot]), 0));
+            }
+          }
+          pair_store<!BMN>(p, stage, i0, j0 + cb * 64, v);
+        }
+      }
+    }
+    if (!ok) sc.abort = 1;
+  }
+  // Every tcgen05 op has completed and every load has landed (bounded waits) before tensor memory is released and
+  // either CTA leaves.  After an abort the two producers may have issued different numbers of fills: the even CTA
+  // arms a phase that only the odd one loaded, and accounts for the odd one's bytes of a phase only it loaded itself.
+  if (warp == 1 && lane == 0 && rank == 0) {
+    mma_commit_cg<2>(&sc.drain, 1);
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(&sc.drain, 0) && globaltimer_ns() - t0 < 100000000ull) {
+    }
+  }
+  if (threadIdx.x == 0 && rank == 1) st_shared_cluster(mapa_shared(smem_u32(&sc.peer_fills), 0), fills);
+  __syncthreads();
+  cluster_sync();
+  if (threadIdx.x == 0 && rank == 0) {
+    const uint32_t L = fills, Q = sc.peer_fills, F = L > Q ? L : Q;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t s = 0; s < (uint32_t)C::kStages && s < F; ++s) {
+      const uint32_t m = s + ((F - 1 - s) / C::kStages) * C::kStages;  // the stage's last fill by either CTA
+      if (m >= L) mbar_expect_tx(&sc.full[s], C::kStage);
+      else if (m >= Q) mbar_complete_tx(&sc.full[s], C::kStage);
+      while (!mbar_try_wait(&sc.full[s], (m / C::kStages) & 1u) && globaltimer_ns() - t0 < 100000000ull) {
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other may still signal it
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_cg<2>(sc.tmem_base, 512);
+}
+
+// ================================================================================================
+// stream_gemm
+// ================================================================================================
+constexpr int kStreamThreads = 256;
+constexpr int kStreamArea = 216 * 1024;  // shared memory of the stages
+constexpr int kStreamMaxStages = 12;
+constexpr int kStreamSmem = 1024 + kStreamArea;
+static_assert(kStreamSmem + 2048 <= 232448, "shared memory");
+
+struct StreamParams {
+  int M, N;        // tokens, output columns (the rows of W)
+  int n_k;         // K steps
+  int tb, n_tb;    // tokens of a block (a multiple of 16, at most 256), token blocks
+  int n_tiles;     // ceil(N / 128) * n_tb; tile = column tile * n_tb + token block
+  int per_cta;     // units (tile, K step) of a CTA, in order
+  int stages;
+  uint32_t tmem_cols;
+  uint32_t idesc;
+  float* partial;  // [2 gridDim.x][tb][128]
+  Epilogue e;
+  Ctrl* ctrl;
+  unsigned long long timeout_ns;
+};
+
+struct StreamSmem {
+  uint64_t full[kStreamMaxStages], empty[kStreamMaxStages], acc_full[2], acc_empty[2], drain;
+  uint32_t tmem_base;
+  volatile uint32_t abort;
+};
+
+// 32 lanes x 32 bits, 16 consecutive columns
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+template <bool AMN>
+__global__ void __launch_bounds__(kStreamThreads, 1)
+    stream_gemm(const __grid_constant__ StreamParams p, const __grid_constant__ CUtensorMap mw,
+                const __grid_constant__ CUtensorMap mx) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ StreamSmem sc;
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t smem_base = (raw + 1023u) & ~1023u;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t stage_bytes = kHalf + (uint32_t)p.tb * kBK * 2;
+  const uint32_t n_st = (uint32_t)p.stages;
+  if (threadIdx.x == 0) {
+    for (uint32_t s = 0; s < n_st; ++s) {
+      mbar_init(&sc.full[s], 1);
+      mbar_init(&sc.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sc.acc_full[b], 1);
+      mbar_init(&sc.acc_empty[b], 4);
+    }
+    mbar_init(&sc.drain, 1);
+    sc.abort = 0;
+    fence_barrier_init();
+    prefetch_tmap(&mw);
+    prefetch_tmap(&mx);
+  }
+  if (warp == 1) {
+    tmem_alloc(&sc.tmem_base, p.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  const long long total = (long long)p.n_tiles * p.n_k;
+  const long long u0 = (long long)blockIdx.x * p.per_cta;
+  const long long u1 = u0 + p.per_cta < total ? u0 + p.per_cta : total;
+  uint32_t fills = 0;
+  if (warp == 0) {
+    if (lane == 0) {
+      long long u = u0;
+      int tile = (int)(u / p.n_k), ks = (int)(u % p.n_k);
+      for (; u < u1; ++u) {
+        const uint32_t s = fills % n_st, use = fills / n_st;
+        if (use > 0 && !wait_bar(&sc.empty[s], (use - 1) & 1u, p, &sc, SITE_EMPTY, kSlack)) {
+          sc.abort = 1;
+          break;
+        }
+        mbar_expect_tx(&sc.full[s], stage_bytes);
+        const uint32_t base = smem_base + s * stage_bytes;
+        const int wrow = tile / p.n_tb * kRows, k = ks * kBK;
+        if constexpr (AMN) {
+          tma_load_2d(base, &mw, wrow, k, &sc.full[s]);
+          tma_load_2d(base + 8192, &mw, wrow + 64, k, &sc.full[s]);
+        } else {
+          tma_load_2d(base, &mw, k, wrow, &sc.full[s]);
+        }
+        tma_load_2d(base + kHalf, &mx, k, tile % p.n_tb * p.tb, &sc.full[s]);
+        ++fills;
+        if (++ks == p.n_k) {
+          ks = 0;
+          ++tile;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t kHi = sdesc_hi_sw128(1024);
+      uint32_t c = 0, seg = 0;
+      bool ok = true;
+      for (long long u = u0; u < u1 && ok; ++seg) {
+        const int left = p.n_k - (int)(u % p.n_k);
+        const int n = (int)(u1 - u < left ? u1 - u : left);
+        const uint32_t slot = seg % 2;
+        if (seg >= 2 && !wait_bar(&sc.acc_empty[slot], (seg / 2 - 1) & 1u, p, &sc, SITE_ACC_EMPTY, kSlack)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        for (int ks = 0; ks < n; ++ks, ++c) {
+          const uint32_t s = c % n_st;
+          if (!wait_bar(&sc.full[s], (c / n_st) & 1u, p, &sc, SITE_FULL, kSlack)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t base = smem_base + s * stage_bytes;
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            mma_ss_w(sc.tmem_base + slot * p.tb, operand_lo<AMN>(base, kk), kHi, operand_lo<false>(base + kHalf, kk), kHi,
+                     p.idesc, (ks > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&sc.empty[s]);
+        }
+        if (!ok) break;
+        mma_commit(&sc.acc_full[slot]);
+        u += n;
+      }
+      if (!ok) sc.abort = 1;
+    }
+  } else if (warp >= 4) {
+    const int quarter = warp % 4, row = quarter * 32 + lane;
+    uint32_t seg = 0;
+    bool ok = true;
+    for (long long u = u0; u < u1; ++seg) {
+      const int tile = (int)(u / p.n_k), first = (int)(u % p.n_k);
+      const int n = (int)(u1 - u < p.n_k - first ? u1 - u : p.n_k - first);
+      const uint32_t slot = seg % 2;
+      ok = __all_sync(0xffffffffu, wait_bar(&sc.acc_full[slot], (seg / 2) & 1u, p, &sc, SITE_ACC, kSlack));
+      if (!ok) break;
+      tc_fence_after();
+      const int j = tile / p.n_tb * kRows + row, i0 = tile % p.n_tb * p.tb;
+      const bool whole = n == p.n_k;
+      float* part = p.partial + (2ll * blockIdx.x + (u == u0 ? 0 : 1)) * p.tb * kRows + row;
+      const uint32_t tacc = sc.tmem_base + ((uint32_t)(quarter * 32) << 16) + slot * p.tb;
+#pragma unroll 1
+      for (int c = 0; c < p.tb && i0 + c < p.M; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(tacc + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (i0 + c + e < p.M) {
+            if (!whole) part[(c + e) * kRows] = __uint_as_float(v[e]);
+            else if (j < p.N) finish(p.e, i0 + c + e, j, __uint_as_float(v[e]));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sc.acc_empty[slot]);
+      u += n;
+    }
+    if (!ok) sc.abort = 1;
+  }
+  // every MMA has completed and every load has landed before the CTA leaves
+  if (warp == 1 && lane == 0) {
+    mma_commit(&sc.drain);
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(&sc.drain, 0) && globaltimer_ns() - t0 < 100000000ull) {
+    }
+  }
+  if (threadIdx.x == 0) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t s = 0; s < n_st && s < fills; ++s) {
+      const uint32_t m = s + ((fills - 1 - s) / n_st) * n_st;
+      while (!mbar_try_wait(&sc.full[s], (m / n_st) & 1u) && globaltimer_ns() - t0 < 100000000ull) {
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(sc.tmem_base, p.tmem_cols);
+}
+
+// Joins the partials of the tiles whose K range is split, in the order of the CTAs that hold them.
+__global__ void __launch_bounds__(128) stream_join(const __grid_constant__ StreamParams p) {
+  const int tile = blockIdx.x;
+  const long long b = (long long)tile * p.n_k, e = b + p.n_k;
+  const int c0 = (int)(b / p.per_cta), c1 = (int)((e - 1) / p.per_cta);
+  if (c0 == c1) return;
+  const int j = tile / p.n_tb * kRows + threadIdx.x, i0 = tile % p.n_tb * p.tb;
+  for (int c = blockIdx.y; c < p.tb && i0 + c < p.M; c += gridDim.y) {
+    float sum = 0.f;
+    for (int g = c0; g <= c1; ++g) {
+      const int slot = 2 * g + ((long long)g * p.per_cta >= b ? 0 : 1);  // the tile that CTA g begins or ends with
+      sum += p.partial[((long long)slot * p.tb + c) * kRows + threadIdx.x];
+    }
+    if (j < p.N) finish(p.e, i0 + c, j, sum);
+  }
+}
+
+// ================================================================================================
+// Host side
+// ================================================================================================
+constexpr int kStreamCtas = 152;  // most CTAs of stream_gemm (one per SM); bounds the partials
+constexpr int kStreamMaxM = 256;  // stream_gemm takes up to this many rows
+
+// A 16-bit matrix of `outer` rows of `inner` elements, boxes of 64 x box_outer, 128-byte swizzle.  The element type
+// only names the width: the copies do no arithmetic and the fill is zero.
+inline bool tmap16(CUtensorMap* m, const void* base, int inner, int outer, long long ld, int box_outer) {
+  const auto encode = gemm::encode_tiled_fn();
+  if (!encode) return false;
+  if (outer == 1) ld = (inner + 7ll) / 8 * 8;
+  cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+  cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_outer};
+  cuuint32_t es[2] = {1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The matrix's rows all start on 16-byte boundaries (what a tensor map needs).
+inline bool mappable(const void* base, int rows, long long ld) {
+  return aligned_to(base, 16) && (rows <= 1 || (ld % 8 == 0 && ld * 2 < (1ll << 40)));
+}
+
+// Shared memory and co-resident pairs of one pair_gemm instantiation on the current device; 0 on error.
+template <int H, bool AMN, bool BMN>
+inline int pairs_of(int dev, int n_sm) {
+  static std::mutex mu;
+  static int known[64] = {};
+  std::lock_guard<std::mutex> lk(mu);
+  if (dev >= 0 && dev < 64 && known[dev]) return known[dev];
+  auto kern = pair_gemm<H, AMN, BMN>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PairCfg<H>::kSmem) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(n_sm / 2 * 2));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = PairCfg<H>::kSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (n > n_sm / 2) n = n_sm / 2;
+  if (dev >= 0 && dev < 64) known[dev] = n;
+  return n;
+}
+
+struct Operands {
+  const void* a;
+  long long lda;
+  const void* b;
+  long long ldb;
+  int M, N, K;  // C is [M][N]
+};
+
+template <int H, bool AMN, bool BMN>
+inline int launch_pair(const Operands& o, const Epilogue& e, Ctrl* ctrl, unsigned long long timeout_ns, int dev, int n_sm,
+                       cudaStream_t st) {
+  const int n_pairs = pairs_of<H, AMN, BMN>(dev, n_sm);
+  if (n_pairs < 1) return PSR_ERR_CUDA;
+  PairParams p = {};
+  p.M = o.M;
+  p.N = o.N;
+  p.n_k = (o.K + kBK - 1) / kBK;
+  p.tiles_m = (o.M + 255) / 256;
+  p.tiles_n = (o.N + 256 * H - 1) / (256 * H);
+  if ((long long)p.tiles_m * p.tiles_n >= (1ll << 31)) return PSR_ERR_UNSUPPORTED;
+  p.group = 8;
+  p.idesc = idesc16(256, 256, AMN, BMN, e.half != 0);
+  p.e = e;
+  p.ctrl = ctrl;
+  p.timeout_ns = timeout_ns;
+  CUtensorMap ma, mb;
+  const bool ok_a = AMN ? tmap16(&ma, o.a, o.M, o.K, o.lda, 64) : tmap16(&ma, o.a, o.K, o.M, o.lda, kRows);
+  const bool ok_b = BMN ? tmap16(&mb, o.b, o.N, o.K, o.ldb, 64) : tmap16(&mb, o.b, o.K, o.N, o.ldb, kRows);
+  if (!ok_a || !ok_b) return PSR_ERR_CUDA;
+  const int tiles = p.tiles_m * p.tiles_n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * (tiles < n_pairs ? tiles : n_pairs)));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = PairCfg<H>::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, pair_gemm<H, AMN, BMN>, p, ma, mb) != cudaSuccess) {
+    cudaGetLastError();
+    return PSR_ERR_CUDA;
+  }
+  return PSR_OK;
+}
+
+// Bytes of partials that stream_gemm may leave for M rows.
+inline size_t stream_partial_bytes(int M) {
+  if (M > kStreamMaxM) return 0;
+  return (size_t)2 * kStreamCtas * ((M + 15) / 16 * 16) * kRows * 4;
+}
+
+// o.a: the tokens [M][K], o.b: W, K-major [N][K] or (WMN) [K][N].
+template <bool WMN>
+inline int launch_stream(const Operands& o, const Epilogue& e, float* partial, Ctrl* ctrl, unsigned long long timeout_ns,
+                         int dev, int n_sm, cudaStream_t st) {
+  static std::mutex mu;
+  static bool known[64] = {};
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (dev < 0 || dev >= 64 || !known[dev]) {
+      if (cudaFuncSetAttribute(stream_gemm<WMN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem) != cudaSuccess) {
+        cudaGetLastError();
+        return PSR_ERR_CUDA;
+      }
+      if (dev >= 0 && dev < 64) known[dev] = true;
+    }
+  }
+  StreamParams p = {};
+  p.M = o.M;
+  p.N = o.N;
+  p.n_k = (o.K + kBK - 1) / kBK;
+  p.tb = (o.M + 15) / 16 * 16;
+  p.n_tb = 1;
+  p.n_tiles = (o.N + kRows - 1) / kRows * p.n_tb;
+  const int most = n_sm < kStreamCtas ? n_sm : kStreamCtas;
+  const long long units = (long long)p.n_tiles * p.n_k;
+  long long per = (units + most - 1) / most;
+  if (p.n_k <= 16) per = (per + p.n_k - 1) / p.n_k * p.n_k;  // short rows: whole tiles, nothing to join
+  else if (per < 8) per = 8;
+  if (per >= (1ll << 31)) return PSR_ERR_UNSUPPORTED;
+  p.per_cta = (int)per;
+  const int stage = kHalf + p.tb * kBK * 2;
+  p.stages = kStreamArea / stage < kStreamMaxStages ? kStreamArea / stage : kStreamMaxStages;
+  p.tmem_cols = 32;
+  while (p.tmem_cols < 2u * p.tb) p.tmem_cols *= 2;
+  p.idesc = idesc16(128, p.tb, WMN, false, e.half != 0);
+  p.partial = partial;
+  p.e = e;
+  p.ctrl = ctrl;
+  p.timeout_ns = timeout_ns;
+  CUtensorMap mw, mx;
+  const bool ok_w = WMN ? tmap16(&mw, o.b, o.N, o.K, o.ldb, 64) : tmap16(&mw, o.b, o.K, o.N, o.ldb, kRows);
+  if (!ok_w || !tmap16(&mx, o.a, o.K, o.M, o.lda, p.tb)) return PSR_ERR_CUDA;
+  const unsigned grid = (unsigned)((units + per - 1) / per);
+  stream_gemm<WMN><<<grid, kStreamThreads, kStreamSmem, st>>>(p, mw, mx);
+  int rc = launch_status();
+  if (rc != PSR_OK || per % p.n_k == 0) return rc;
+  stream_join<<<dim3((unsigned)p.n_tiles, (unsigned)(p.tb < 16 ? p.tb : 16)), 128, 0, st>>>(p);
+  return launch_status();
+}
+
+}  // namespace linear
+}  // namespace psr
