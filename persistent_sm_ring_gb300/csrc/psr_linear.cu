@@ -17,7 +17,8 @@ namespace linear {
 template <class T, bool AT, bool BT>
 __global__ void __launch_bounds__(256)
     simple_gemm(const T* __restrict__ a, long long lda, const T* __restrict__ b, long long ldb, int M, int N, int K,
-                const Epilogue e) {
+                const Epilogue e, Ctrl* clear) {
+  clear_ctrl(clear);
   __shared__ float sa[16][68], sb[16][68];
   const long long i0 = (long long)blockIdx.x * 64;
   const int j0 = blockIdx.y * 64;
@@ -49,43 +50,77 @@ __global__ void __launch_bounds__(256)
 
 template <class T, bool AT, bool BT>
 static int launch_simple(const void* a, long long lda, const void* b, long long ldb, int M, int N, int K,
-                         const Epilogue& e, cudaStream_t st) {
+                         const Epilogue& e, Launch& l) {
   if (M == 0) return PSR_OK;
   const dim3 grid((unsigned)((M + 63) / 64), (unsigned)((N + 63) / 64));
   if (grid.y > 65535) return PSR_ERR_UNSUPPORTED;
-  simple_gemm<T, AT, BT><<<grid, 256, 0, st>>>(static_cast<const T*>(a), lda, static_cast<const T*>(b), ldb, M, N,
-                                                   K, e);
+  simple_gemm<T, AT, BT><<<grid, 256, 0, l.st>>>(static_cast<const T*>(a), lda, static_cast<const T*>(b), ldb, M, N, K, e,
+                                                l.clear);
+  l.clear = nullptr;
   return launch_status();
 }
 
 // ------------------------------------------------------------------------------------------------
 // dz = dy act'(z), and the column sums of its unrounded values over chunks of rows
 // ------------------------------------------------------------------------------------------------
+// Memory bound.  A thread takes V adjacent columns (16 bytes where the rows allow it) of every eighth row of a chunk, the
+// eight warps of a block join their sums in shared memory, and a second kernel joins the chunks in order: the sums do not
+// depend on the order in which blocks run.
 constexpr int kDzRows = 64;  // rows of a chunk
 
-template <class T>
-__global__ void dz_kernel(const T* __restrict__ dy, long long ldy, const T* __restrict__ z, long long ldz, T* dz,
-                          long long lddz, float* partial, int M, int N, int act) {
-  const int j = blockIdx.y * 256 + threadIdx.x;
-  if (j >= N) return;
-  const long long i0 = (long long)blockIdx.x * kDzRows;
-  float sum = 0.f;
-  for (int r = 0; r < kDzRows && i0 + r < M; ++r) {
-    float v = to_f32(dy[(i0 + r) * ldy + j]);
-    if (act != PSR_ACT_NONE) v *= act_slope(act, to_f32(z[(i0 + r) * ldz + j]));
-    if (dz) dz[(i0 + r) * lddz + j] = from_f32<T>(v);
-    sum += v;
+template <class T, int V>
+__global__ void __launch_bounds__(256)
+    dz_kernel(const T* __restrict__ dy, long long ldy, const T* __restrict__ z, long long ldz, T* __restrict__ dz,
+              long long lddz, float* __restrict__ partial, int M, int N, int act, Ctrl* clear) {
+  __shared__ float sums[8][32 * V];
+  clear_ctrl(clear);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int j = (blockIdx.y * 32 + lane) * V;
+  const long long i0 = (long long)blockIdx.x * kDzRows, i1 = i0 + kDzRows < M ? i0 + kDzRows : M;
+  struct alignas(sizeof(T) * V) Vec { T v[V]; };
+  float sum[V] = {};
+  if (j < N) {
+#pragma unroll 4
+    for (long long i = i0 + warp; i < i1; i += 8) {
+      Vec g = *reinterpret_cast<const Vec*>(dy + i * ldy + j), zz;
+      if (act != PSR_ACT_NONE) zz = *reinterpret_cast<const Vec*>(z + i * ldz + j);
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        float f = to_f32(g.v[c]);
+        if (act != PSR_ACT_NONE) f *= act_slope(act, to_f32(zz.v[c]));
+        g.v[c] = from_f32<T>(f);
+        sum[c] += f;
+      }
+      if (dz) *reinterpret_cast<Vec*>(dz + i * lddz + j) = g;
+    }
   }
-  if (partial) partial[(long long)blockIdx.x * N + j] = sum;
+  if (!partial) return;
+#pragma unroll
+  for (int c = 0; c < V; ++c) sums[warp][lane * V + c] = sum[c];
+  __syncthreads();
+  for (int c = threadIdx.x; c < 32 * V; c += 256) {
+    const int col = blockIdx.y * 32 * V + c;
+    float f = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) f += sums[w][c];
+    if (col < N) partial[(long long)blockIdx.x * N + col] = f;
+  }
 }
 
+// Column sums over the chunks: eight warps take every eighth chunk of 32 columns.
 template <class T>
-__global__ void db_kernel(const float* __restrict__ partial, int chunks, int N, T* db) {
-  const int j = blockIdx.x * 256 + threadIdx.x;
-  if (j >= N) return;
-  float sum = 0.f;
-  for (int c = 0; c < chunks; ++c) sum += partial[(long long)c * N + j];
-  db[j] = from_f32<T>(sum);
+__global__ void __launch_bounds__(256) db_kernel(const float* __restrict__ partial, int chunks, int N, T* db) {
+  __shared__ float sums[8][32];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, j = blockIdx.x * 32 + lane;
+  float f = 0.f;
+  if (j < N)
+#pragma unroll 8
+    for (int c = warp; c < chunks; c += 8) f += partial[(long long)c * N + j];
+  sums[warp][lane] = f;
+  __syncthreads();
+  if (warp || j >= N) return;
+  for (int w = 1; w < 8; ++w) f += sums[w][lane];
+  db[j] = from_f32<T>(f);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -95,12 +130,31 @@ struct Sizes {
   long long ldx, ldw, ldr, ldy, ldz;
   int chunks;     // row chunks of the column sums
   long long lddz; // row stride of dz in the workspace
-  size_t stream, dz, partial, total_fwd, total_bwd;
+  size_t sums, sums_bytes, dz, partial, total;
 };
+
+static int launch_of(void* workspace, const Sizes& s, int timeout_ms, void* stream, Launch& l) {
+  const int rc = check_device(&l.n_sm);
+  if (rc != PSR_OK) return rc;
+  if (cudaGetDevice(&l.dev) != cudaSuccess) return PSR_ERR_CUDA;
+  l.ctrl = l.clear = static_cast<Ctrl*>(workspace);
+  l.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + s.sums);
+  l.partial_bytes = s.sums_bytes;
+  l.timeout_ns = (unsigned long long)(timeout_ms > 0 ? timeout_ms : 2000) * 1000000ull;
+  l.st = static_cast<cudaStream_t>(stream);
+  return PSR_OK;
+}
+
+// A call that launched nothing still leaves a cleared control block for psr_get_stats.
+static int clear_rest(const Launch& l) {
+  if (!l.clear || cudaMemsetAsync(l.clear, 0, sizeof(Ctrl), l.st) == cudaSuccess) return PSR_OK;
+  cudaGetLastError();
+  return PSR_ERR_CUDA;
+}
 
 static size_t au(size_t x) { return (x + 255) / 256 * 256; }
 
-static int sizes(const psr_linear_shape* sh, Sizes& s) {
+static int sizes(const psr_linear_shape* sh, bool backward, Sizes& s) {
   if (!sh) return PSR_ERR_ARG;
   if (sh->M < 0 || sh->N < 1 || sh->K < 1) return PSR_ERR_ARG;
   if (sh->act < PSR_ACT_NONE || sh->act > PSR_ACT_SILU) return PSR_ERR_ARG;
@@ -112,61 +166,69 @@ static int sizes(const psr_linear_shape* sh, Sizes& s) {
   s.chunks = (sh->M + kDzRows - 1) / kDzRows;
   s.lddz = (sh->N + 7) / 8 * 8;
   size_t off = 256;  // control block
-  s.stream = off;
-  off = au(off + stream_partial_bytes(sh->M));
-  s.total_fwd = off;
-  s.dz = off;
-  if (sh->act != PSR_ACT_NONE) off = au(off + (size_t)sh->M * s.lddz * 2);
-  s.partial = off;
-  off = au(off + (size_t)s.chunks * sh->N * 4);
-  s.total_bwd = off;
+  s.sums = off;      // fp32 partials of one split product at a time
+  if (backward) {
+    const size_t x = partial_bytes(sh->M, sh->K, sh->N, false), w = partial_bytes(sh->N, sh->K, sh->M, true);
+    s.sums_bytes = x > w ? x : w;
+  } else {
+    s.sums_bytes = partial_bytes(sh->M, sh->N, sh->K, false);
+  }
+  off = au(off + s.sums_bytes);
+  s.dz = s.partial = off;
+  if (backward) {
+    if (sh->act != PSR_ACT_NONE) off = au(off + (size_t)sh->M * s.lddz * 2);
+    s.partial = off;
+    off = au(off + (size_t)s.chunks * sh->N * 4);
+  }
+  s.total = off;
   return PSR_OK;
 }
-
-struct Launch {
-  int dev, n_sm;
-  Ctrl* ctrl;
-  float* stream_partial;
-  unsigned long long timeout_ns;
-  cudaStream_t st;
-};
 
 // C = A B^T with A [M][K] (or AMN: [K][M]) and B [N][K] (or BMN: [K][N]).  W is the operand that streams when
 // there are few rows of A.
 template <class T, bool AMN, bool BMN>
-static int product(const Operands& o, Epilogue e, const Launch& l) {
+static int product(const Operands& o, Epilogue e, Launch& l) {
   if (o.M == 0) return PSR_OK;
   if (!mappable(o.a, AMN ? o.K : o.M, o.lda) || !mappable(o.b, BMN ? o.K : o.N, o.ldb))
-    return launch_simple<T, AMN, BMN>(o.a, o.lda, o.b, o.ldb, o.M, o.N, o.K, e, l.st);
+    return launch_simple<T, AMN, BMN>(o.a, o.lda, o.b, o.ldb, o.M, o.N, o.K, e, l);
   auto flat = [&](const void* p, long long ld) { return !p || (aligned_to(p, 16) && (o.M == 1 || ld % 8 == 0)); };
   e.vec = o.N % 8 == 0 && flat(e.y, e.ldy) && flat(e.z, e.ldz) && flat(e.res, e.ldr) && flat(e.bias, 0);
   if constexpr (!AMN)
-    if (o.M <= kStreamMaxM) return launch_stream<BMN>(o, e, l.stream_partial, l.ctrl, l.timeout_ns, l.dev, l.n_sm, l.st);
-  // 512 columns feed the tensor cores best; 256 where their finer grain saves more than that
+    if (streams(o.M)) return launch_stream<BMN>(o, e, l);
+  const int splits = pair_splits(o.M, o.N, o.K);
+  if (splits > 1) return launch_pair<1, AMN, BMN>(o, e, splits, l);
+  // A wave of 512-column tiles takes 16 clocks for each K plus its epilogue's first three quarters, when the accumulators
+  // are not free for the next tile; one of 256-column tiles 9.2 for each K (the tile loads bound it) or its whole epilogue,
+  // whichever is longer.
   const long long rows = (o.M + 255) / 256, n_pairs = l.n_sm / 2;
   auto waves = [&](long long cols) { return (rows * ((o.N + cols - 1) / cols) + n_pairs - 1) / n_pairs; };
-  if (100 * waves(512) * 2 <= 113 * waves(256))
-    return launch_pair<2, AMN, BMN>(o, e, l.ctrl, l.timeout_ns, l.dev, l.n_sm, l.st);
-  return launch_pair<1, AMN, BMN>(o, e, l.ctrl, l.timeout_ns, l.dev, l.n_sm, l.st);
+  const double epi = 1500.0 + (e.act ? 3000.0 : 0.0) + (e.z ? 1000.0 : 0.0) + (e.res ? 1000.0 : 0.0);
+  const double two = waves(512) * (16.0 * o.K + 1.5 * epi), one = waves(256) * (9.2 * o.K > epi ? 9.2 * o.K : epi);
+  return two <= one ? launch_pair<2, AMN, BMN>(o, e, 1, l) : launch_pair<1, AMN, BMN>(o, e, 1, l);
 }
 
 template <class T>
 static int backward(const psr_linear_shape* sh, const Sizes& s, const void* dy, const void* z, const void* x,
-                    const void* w, void* dx, void* dw, void* db, uint8_t* ws, const Launch& l) {
+                    const void* w, void* dx, void* dw, void* db, uint8_t* ws, Launch& l) {
   const bool act = sh->act != PSR_ACT_NONE;
   void* dz = act ? ws + s.dz : nullptr;
   int rc = PSR_OK;
   if (sh->M > 0 && (db || (act && (dx || dw)))) {
-    const dim3 grid((unsigned)s.chunks, (unsigned)((sh->N + 255) / 256));
+    T* out = dx || dw ? static_cast<T*>(dz) : nullptr;
+    float* partial = db ? reinterpret_cast<float*>(ws + s.partial) : nullptr;
+    auto flat = [&](const void* p, long long ld) { return !p || (aligned_to(p, 16) && (sh->M == 1 || ld % 8 == 0)); };
+    const bool vec = sh->N % 8 == 0 && flat(dy, s.ldy) && flat(z, s.ldz);
+    const dim3 grid((unsigned)s.chunks, (unsigned)((sh->N + 32 * (vec ? 8 : 1) - 1) / (32 * (vec ? 8 : 1))));
     if (grid.y > 65535) return PSR_ERR_UNSUPPORTED;
-    dz_kernel<T><<<grid, 256, 0, l.st>>>(static_cast<const T*>(dy), s.ldy, static_cast<const T*>(z), s.ldz,
-                                         static_cast<T*>(dz), s.lddz,
-                                         db ? reinterpret_cast<float*>(ws + s.partial) : nullptr, sh->M, sh->N, sh->act);
+    const T *dy_t = static_cast<const T*>(dy), *z_t = static_cast<const T*>(z);
+    if (vec) dz_kernel<T, 8><<<grid, 256, 0, l.st>>>(dy_t, s.ldy, z_t, s.ldz, out, s.lddz, partial, sh->M, sh->N, sh->act, l.clear);
+    else dz_kernel<T, 1><<<grid, 256, 0, l.st>>>(dy_t, s.ldy, z_t, s.ldz, out, s.lddz, partial, sh->M, sh->N, sh->act, l.clear);
+    l.clear = nullptr;
     if ((rc = launch_status()) != PSR_OK) return rc;
   }
   if (db) {
-    db_kernel<T><<<(unsigned)((sh->N + 255) / 256), 256, 0, l.st>>>(reinterpret_cast<float*>(ws + s.partial), s.chunks,
-                                                                   sh->N, static_cast<T*>(db));
+    db_kernel<T><<<(unsigned)((sh->N + 31) / 32), 256, 0, l.st>>>(reinterpret_cast<float*>(ws + s.partial), s.chunks, sh->N,
+                                                                 static_cast<T*>(db));
     if ((rc = launch_status()) != PSR_OK) return rc;
   }
   const void* g = act ? dz : dy;
@@ -189,21 +251,6 @@ static int backward(const psr_linear_shape* sh, const Sizes& s, const void* dy, 
   return rc;
 }
 
-static int launch_of(void* workspace, const Sizes& s, int timeout_ms, void* stream, Launch& l) {
-  const int rc = check_device(&l.n_sm);
-  if (rc != PSR_OK) return rc;
-  if (cudaGetDevice(&l.dev) != cudaSuccess) return PSR_ERR_CUDA;
-  l.ctrl = static_cast<Ctrl*>(workspace);
-  l.stream_partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + s.stream);
-  l.timeout_ns = (unsigned long long)(timeout_ms > 0 ? timeout_ms : 2000) * 1000000ull;
-  l.st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, sizeof(Ctrl), l.st) != cudaSuccess) {
-    cudaGetLastError();
-    return PSR_ERR_CUDA;
-  }
-  return PSR_OK;
-}
-
 }  // namespace linear
 }  // namespace psr
 
@@ -214,8 +261,8 @@ extern "C" {
 
 size_t psr_linear_workspace_bytes(const psr_linear_shape* sh, int backward) {
   Sizes s;
-  if (sizes(sh, s) != PSR_OK) return 0;
-  return backward ? s.total_bwd : s.total_fwd;
+  if (sizes(sh, backward != 0, s) != PSR_OK) return 0;
+  return s.total;
 }
 
 int psr_linear(const psr_linear_shape* sh, const void* x, const void* w, const void* bias, const void* residual,
@@ -225,9 +272,9 @@ int psr_linear(const psr_linear_shape* sh, const void* x, const void* w, const v
   for (const void* ptr : {x, w, bias, residual, (const void*)y, (const void*)z})
     if (!aligned_to(ptr, 2)) return PSR_ERR_ARG;
   Sizes s;
-  int rc = sizes(sh, s);
+  int rc = sizes(sh, false, s);
   if (rc != PSR_OK) return rc;
-  if (ws_bytes < s.total_fwd) return PSR_ERR_ARG;
+  if (ws_bytes < s.total) return PSR_ERR_ARG;
   Launch l;
   if ((rc = launch_of(workspace, s, timeout_ms, stream, l)) != PSR_OK) return rc;
   Epilogue e = {};
@@ -236,7 +283,8 @@ int psr_linear(const psr_linear_shape* sh, const void* x, const void* w, const v
   e.act = sh->act;
   e.half = sh->type == PSR_F16;
   const Operands o = {x, s.ldx, w, s.ldw, sh->M, sh->N, sh->K};
-  return sh->type == PSR_BF16 ? product<__nv_bfloat16, false, false>(o, e, l) : product<__half, false, false>(o, e, l);
+  rc = sh->type == PSR_BF16 ? product<__nv_bfloat16, false, false>(o, e, l) : product<__half, false, false>(o, e, l);
+  return rc != PSR_OK ? rc : clear_rest(l);
 }
 
 int psr_linear_bwd(const psr_linear_shape* sh, const void* dy, const void* z, const void* x, const void* w, void* dx,
@@ -246,14 +294,15 @@ int psr_linear_bwd(const psr_linear_shape* sh, const void* dy, const void* z, co
   for (const void* ptr : {dy, z, x, w, (const void*)dx, (const void*)dw, (const void*)db})
     if (!aligned_to(ptr, 2)) return PSR_ERR_ARG;
   Sizes s;
-  int rc = sizes(sh, s);
+  int rc = sizes(sh, true, s);
   if (rc != PSR_OK) return rc;
-  if (ws_bytes < s.total_bwd) return PSR_ERR_ARG;
+  if (ws_bytes < s.total) return PSR_ERR_ARG;
   Launch l;
   if ((rc = launch_of(workspace, s, timeout_ms, stream, l)) != PSR_OK) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  return sh->type == PSR_BF16 ? backward<__nv_bfloat16>(sh, s, dy, z, x, w, dx, dw, db, ws, l)
-                              : backward<__half>(sh, s, dy, z, x, w, dx, dw, db, ws, l);
+  rc = sh->type == PSR_BF16 ? backward<__nv_bfloat16>(sh, s, dy, z, x, w, dx, dw, db, ws, l)
+                            : backward<__half>(sh, s, dy, z, x, w, dx, dw, db, ws, l);
+  return rc != PSR_OK ? rc : clear_rest(l);
 }
 
 }  // extern "C"

@@ -23,8 +23,39 @@ namespace psr {
 namespace linear {
 
 constexpr int kBK = 64;  // K per stage: one 128-byte swizzle atom of 16-bit elements
-constexpr uint32_t kSlack = 4;
 enum : uint32_t { SITE_FULL = 41, SITE_EMPTY = 42, SITE_ACC = 43, SITE_ACC_EMPTY = 44, SITE_LAUNCH = 45 };
+
+// Bounded wait on a barrier: false after the timeout, or once another wait of the CTA has given up.  The control block's
+// abort word is not consulted: it is cleared by the launch itself (clear_ctrl), while other CTAs already run.
+template <bool CL = false, class KP, class SC>
+__device__ __forceinline__ bool wait_own(uint64_t* bar, uint32_t parity, const KP& p, SC* sc, uint32_t site) {
+  auto poll = [&]() { return CL ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+  if (poll()) return true;
+  const uint64_t t0 = globaltimer_ns();
+  uint32_t it = 0;
+  while (true) {
+    if (poll()) return true;
+    if ((++it & 15u) == 0) {
+      if (sc->abort) return false;
+      if (globaltimer_ns() - t0 > p.timeout_ns) {
+        raise_error(p, site);
+        sc->abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// The first kernel of a call clears the control block (a memset before it would cost a launch).  A wait of the same call
+// can give up only a timeout later.
+__device__ __forceinline__ void clear_ctrl(Ctrl* ctrl) {
+  if (ctrl && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < sizeof(Ctrl) / 4)
+    reinterpret_cast<uint32_t*>(ctrl)[threadIdx.x] = 0;
+}
+
+// Programmatic launches: let the next kernel's launch begin / wait for the whole previous kernel and its writes.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // What becomes of an fp32 sum: z = sum + bias, y = act(z) + residual.
 struct Epilogue {
@@ -38,27 +69,54 @@ struct Epilogue {
   int vec;   // every row and column offset that the tiles use is 16-byte aligned
 };
 
-// act(z) and act'(z) in fp32
+// act(z) and act'(z) in fp32, branch-free: expf, erff and tanhf of the CUDA library cost the epilogue 30 to 40 issue
+// slots an element (a 256-column half of a 1024-deep tile then waits on its epilogue).  The exponential and the reciprocal
+// are the special function unit's (2^-22 each); the normal distribution function is Abramowitz and Stegun's formula 7.1.26
+// for erf (error below 1.5e-7), taken as its complement so that the left tail keeps its digits.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.f + ex2_approx(-1.4426950408889634f * x)); }
+// Phi(z); *e = exp(-z^2 / 2)
+__device__ __forceinline__ float normal_cdf(float z, float* e) {
+  const float t = rcp_approx(fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.f));
+  *e = ex2_approx(-0.72134752044448170f * z * z);
+  float q = fmaf(1.061405429f, t, -1.453152027f);
+  q = fmaf(q, t, 1.421413741f);
+  q = fmaf(q, t, -0.284496736f);
+  q = fmaf(q, t, 0.254829592f);
+  const float h = 0.5f * q * t * *e;
+  return z < 0.f ? h : 1.f - h;
+}
+
 __device__ __forceinline__ float act_fwd(int act, float z) {
   switch (act) {
     case PSR_ACT_RELU: return z > 0.f ? z : (z == z ? 0.f : z);
-    case PSR_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-    case PSR_ACT_GELU_TANH: return 0.5f * z * (1.f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
-    case PSR_ACT_SILU: return z / (1.f + expf(-z));
+    case PSR_ACT_GELU: {
+      float e;
+      return z * normal_cdf(z, &e);
+    }
+    case PSR_ACT_GELU_TANH: return z * sigmoid(1.5957691216057307f * (z + 0.044715f * z * z * z));  // (1 + tanh u)/2 = sigmoid(2u)
+    case PSR_ACT_SILU: return z * sigmoid(z);
     default: return z;
   }
 }
 __device__ __forceinline__ float act_slope(int act, float z) {
   switch (act) {
     case PSR_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-    case PSR_ACT_GELU:
-      return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+    case PSR_ACT_GELU: {
+      float e;
+      const float f = normal_cdf(z, &e);
+      return fmaf(z * 0.39894228040143268f, e, f);
+    }
     case PSR_ACT_GELU_TANH: {
-      const float t = tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z));
-      return 0.5f * (1.f + t) + 0.5f * z * (1.f - t * t) * 0.79788456080286536f * (1.f + 0.134145f * z * z);
+      const float s = sigmoid(1.5957691216057307f * (z + 0.044715f * z * z * z));
+      return s + z * s * (1.f - s) * 1.5957691216057307f * (1.f + 0.134145f * z * z);
     }
     case PSR_ACT_SILU: {
-      const float s = 1.f / (1.f + expf(-z));
+      const float s = sigmoid(z);
       return s * (1.f + z * (1.f - s));
     }
     default: return 1.f;
@@ -115,8 +173,9 @@ __device__ __forceinline__ uint32_t operand_lo(uint32_t tile, int kk) {
 // ================================================================================================
 constexpr int kRows = 128;           // A rows, and B rows of a half, that one CTA loads
 constexpr int kHalf = kRows * kBK * 2;
-constexpr int kPairWarps = 12, kPairThreads = kPairWarps * 32, kEpiWarps = 8;
-constexpr int kEpiWarpBytes = 4096;  // one warp's 32 rows x 128 bytes
+constexpr int kEpiWarps = 16;  // four to a scheduler: an epilogue block is a chain of latencies
+constexpr int kPairThreads = (4 + kEpiWarps) * 32;
+constexpr int kEpiWarpBytes = 2048;  // one warp's 32 rows x 64 bytes
 template <int H>
 struct PairCfg {
   static constexpr int kStage = (1 + H) * kHalf;
@@ -130,9 +189,13 @@ struct PairParams {
   int M, N, n_k;
   int tiles_m, tiles_n;   // 256 rows, 256 H columns
   int group;              // tile rows of a raster group
+  int splits, split_k;    // parts of the K steps, K steps of a part
+  float* partial;         // splits > 1: fp32 sums [splits][M][ldp]
+  long long ldp;
   uint32_t idesc;
   Epilogue e;
   Ctrl* ctrl;
+  Ctrl* clear;            // control block to clear, or null
   unsigned long long timeout_ns;
 };
 
@@ -163,69 +226,91 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* m,
   }
 }
 
-// The warp's 32 rows x 64 columns at (i0, j0), row `lane` in v: bias, z, activation, residual, y.
-// ACT: the epilogue may have an activation (the gradients have none).
+// A warp's 32 rows x 32 columns of 16-bit elements, or 32 x 16 of fp32, between global memory and its staging area: 64
+// bytes of a row, whose four 16-byte chunks are XOR-swizzled by the row so that row-wise and column-wise passes are both
+// free of bank conflicts.  Lane l holds chunk l % 4 of rows k * 8 + l / 4.
+__device__ __forceinline__ uint4* stage_chunk(uint8_t* stage, int row, int c) {
+  return reinterpret_cast<uint4*>(stage + row * 64 + ((c ^ ((row >> 1) & 3)) * 16));
+}
+// 16-byte columns below `chunks` of rows below `rows`
+__device__ __forceinline__ void rows_out(uint8_t* stage, uint8_t* g, long long pitch, int rows, int chunks) {
+  const int lane = threadIdx.x % 32, c = lane % 4;
+  __syncwarp();
+  g += (long long)(lane / 4) * pitch + c * 16;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = k * 8 + lane / 4;
+    const uint4 w = *stage_chunk(stage, r, c);
+    if (r < rows && c < chunks) *reinterpret_cast<uint4*>(g) = w;
+    g += 8 * pitch;
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void rows_in(uint4 (&w)[4], const uint8_t* g, long long pitch, int rows, int chunks) {
+  const int lane = threadIdx.x % 32, c = lane % 4;
+  g += (long long)(lane / 4) * pitch + c * 16;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    w[k] = make_uint4(0, 0, 0, 0);
+    if (k * 8 + lane / 4 < rows && c < chunks) w[k] = *reinterpret_cast<const uint4*>(g);
+    g += 8 * pitch;
+  }
+}
+__device__ __forceinline__ void add16(uint32_t* v, const uint4& b, int half) {
+  const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float lo, hi;
+    unpack16(w[q], half, lo, hi);
+    v[2 * q] = __float_as_uint(__uint_as_float(v[2 * q]) + lo);
+    v[2 * q + 1] = __float_as_uint(__uint_as_float(v[2 * q + 1]) + hi);
+  }
+}
+
+// The block's 32 rows x 32 columns at (i0, j0), row `lane` in v: bias, z, activation, residual (its rows in `res`, as
+// rows_in read them), y.  ACT: there may be an activation (the gradients have none).
 template <bool ACT>
-__device__ __forceinline__ void pair_store(const PairParams& p, uint8_t* stage, int i0, int j0, uint32_t* v) {
-  const Epilogue& e = p.e;
+__device__ __forceinline__ void pair_store(const Epilogue& e, int M, int N, uint8_t* stage, int i0, int j0,
+                                           uint32_t (&v)[32], const uint4 (&res)[4]) {
   const int lane = threadIdx.x % 32;
-  const int rows = min(32, p.M - i0), cols = min(64, p.N - j0);
+  const int rows = min(32, M - i0), cols = min(32, N - j0);
   if (rows <= 0 || cols <= 0) return;
   if (!e.vec) {
     if (lane < rows)
 #pragma unroll
-      for (int c = 0; c < 64; ++c)
-        if (c < cols) finish(e, i0 + lane, j0 + c, __uint_as_float(v[c]));
-    return;
-  }
-  // cols is a multiple of 8 here
-  // 16-byte chunks of a 128-byte row, XOR-swizzled by the row: both passes are free of bank conflicts
-  auto copy_out = [&](void* base, long long ld) {
-    __syncwarp();
-    uint8_t* g = static_cast<uint8_t*>(base) + ((long long)i0 * ld + j0) * 2;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int r = k * 4 + lane / 8, c = lane % 8;
-      const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r % 8)) * 16));
-      if (r < rows && c * 8 < cols) *reinterpret_cast<uint4*>(g + (long long)r * ld * 2 + c * 16) = w;
-    }
-    __syncwarp();
-  };
-  auto chunk = [&](int j) { return reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane % 8)) * 16)); };
-  if (e.bias) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j * 8 < cols) {
-        const uint4 b = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.bias) + j0 + j * 8);
-        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float lo, hi;
-          unpack16(w[q], e.half, lo, hi);
-          v[j * 8 + 2 * q] = __float_as_uint(__uint_as_float(v[j * 8 + 2 * q]) + lo);
-          v[j * 8 + 2 * q + 1] = __float_as_uint(__uint_as_float(v[j * 8 + 2 * q + 1]) + hi);
+      for (int c = 0; c < 32; ++c)
+        if (c < cols) {
+          float f = __uint_as_float(v[c]);
+          if (e.bias) f += load16(e.bias, j0 + c, e.half);
+          if (e.z) store16(e.z, (i0 + lane) * e.ldz + j0 + c, e.half, f);
+          v[c] = __float_as_uint(f);
         }
-      }
+  } else {
+    if (e.bias) {
+      const uint4* b = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.bias) + j0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j * 8 < cols) add16(v + 8 * j, b[j], e.half);
     }
   }
   auto put = [&]() {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
       uint32_t w[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         w[q] = pack16(__uint_as_float(v[j * 8 + 2 * q]), __uint_as_float(v[j * 8 + 2 * q + 1]), e.half);
-      *chunk(j) = make_uint4(w[0], w[1], w[2], w[3]);
+      *stage_chunk(stage, lane, j) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   };
-  if (e.z) {
+  if (e.vec && e.z) {
     put();
-    copy_out(e.z, e.ldz);
+    rows_out(stage, static_cast<uint8_t*>(e.z) + ((long long)i0 * e.ldz + j0) * 2, e.ldz * 2, rows, cols / 8);
   }
   if constexpr (ACT) {
     auto apply = [&](auto act) {
 #pragma unroll
-      for (int c = 0; c < 64; ++c) v[c] = __float_as_uint(act_fwd(decltype(act)::value, __uint_as_float(v[c])));
+      for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(act_fwd(decltype(act)::value, __uint_as_float(v[c])));
     };
     switch (e.act) {
       case PSR_ACT_RELU: apply(std::integral_constant<int, PSR_ACT_RELU>()); break;
@@ -235,34 +320,45 @@ __device__ __forceinline__ void pair_store(const PairParams& p, uint8_t* stage, 
       default: break;
     }
   }
-  if (e.res) {
-    const uint8_t* g = static_cast<const uint8_t*>(e.res) + ((long long)i0 * e.ldr + j0) * 2;
+  if (!e.vec) {
+    if (lane < rows)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int r = k * 4 + lane / 8, c = lane % 8;
-      if (r < rows && c * 8 < cols)
-        *reinterpret_cast<uint4*>(stage + r * 128 + ((c ^ (r % 8)) * 16)) =
-            *reinterpret_cast<const uint4*>(g + (long long)r * e.ldr * 2 + c * 16);
-    }
+      for (int c = 0; c < 32; ++c)
+        if (c < cols) {
+          float f = __uint_as_float(v[c]);
+          if (e.res) f += load16(e.res, (i0 + lane) * e.ldr + j0 + c, e.half);
+          store16(e.y, (i0 + lane) * e.ldy + j0 + c, e.half, f);
+        }
+    return;
+  }
+  if (e.res) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) *stage_chunk(stage, k * 8 + lane / 4, lane % 4) = res[k];
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j * 8 < cols) {
-        const uint4 b = *chunk(j);
-        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float lo, hi;
-          unpack16(w[q], e.half, lo, hi);
-          v[j * 8 + 2 * q] = __float_as_uint(__uint_as_float(v[j * 8 + 2 * q]) + lo);
-          v[j * 8 + 2 * q + 1] = __float_as_uint(__uint_as_float(v[j * 8 + 2 * q + 1]) + hi);
-        }
-      }
-    }
+    for (int j = 0; j < 4; ++j) add16(v + 8 * j, *stage_chunk(stage, lane, j), e.half);
     __syncwarp();
   }
   put();
-  copy_out(e.y, e.ldy);
+  rows_out(stage, static_cast<uint8_t*>(e.y) + ((long long)i0 * e.ldy + j0) * 2, e.ldy * 2, rows, cols / 8);
+}
+
+// The block's fp32 sums into the split's partials.
+__device__ __forceinline__ void partial_store(const PairParams& p, int split, uint8_t* stage, int i0, int j0,
+                                              const uint32_t (&v)[32]) {
+  const int lane = threadIdx.x % 32;
+  const int rows = min(32, p.M - i0);
+  if (rows <= 0) return;
+  float* g = p.partial + ((long long)split * p.M + i0) * p.ldp + j0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t* w = v + h * 16 + j * 4;
+      *stage_chunk(stage, lane, j) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    rows_out(stage, reinterpret_cast<uint8_t*>(g + h * 16), p.ldp * 4, rows, 4);
+  }
 }
 
 template <int H, bool AMN, bool BMN>
@@ -283,6 +379,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     return;
   }
   const uint32_t rank = cluster_ctarank();
+  clear_ctrl(p.clear);
+  launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&sc.full[s], 1);
@@ -308,19 +406,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   cluster_sync();
   tc_fence_after();
 
-  const int n_tiles = p.tiles_m * p.tiles_n;
+  const int n_items = p.tiles_m * p.tiles_n * p.splits;  // the splits of a tile run one after another
   const int pair = blockIdx.x / 2, n_pairs = gridDim.x / 2;
   uint32_t fills = 0;  // thread 0: stages this CTA filled
   if (warp == 0) {
     if (lane == 0) {
       bool ok = true;
-      for (int t = pair; t < n_tiles && ok; t += n_pairs) {
+      for (int t = pair; t < n_items && ok; t += n_pairs) {
         int tm, tn;
-        pair_tile(p, t, tm, tn);
+        pair_tile(p, t / p.splits, tm, tn);
         const int arow = tm * 256 + (int)rank * kRows, brow = tn * 256 * H + (int)rank * kRows;
-        for (int ks = 0; ks < p.n_k; ++ks) {
+        const int k0 = t % p.splits * p.split_k, k1 = min(p.n_k, k0 + p.split_k);
+        for (int ks = k0; ks < k1; ++ks) {
           const uint32_t s = fills % C::kStages, use = fills / C::kStages;
-          if (use > 0 && !wait_bar(&sc.empty[s], (use - 1) & 1u, p, &sc, SITE_EMPTY, kSlack)) { ok = false; break; }
+          if (use > 0 && !wait_own(&sc.empty[s], (use - 1) & 1u, p, &sc, SITE_EMPTY)) { ok = false; break; }
           if (rank == 0) mbar_expect_tx(&sc.full[s], 2 * C::kStage);  // both CTAs' bytes
           const uint32_t bar = mapa_shared(smem_u32(&sc.full[s]), 0);
           const uint32_t base = smem_base + s * C::kStage;
@@ -337,10 +436,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       constexpr uint32_t kHi = sdesc_hi_sw128(1024);
       uint32_t c = 0, u = 0;  // stages consumed, accumulator halves begun
       bool ok = true;
-      for (int t = pair; t < n_tiles && ok; t += n_pairs, u += H) {
-        for (int ks = 0; ks < p.n_k && ok; ++ks, ++c) {
+      for (int t = pair; t < n_items && ok; t += n_pairs, u += H) {
+        const int n_k = min(p.split_k, p.n_k - t % p.splits * p.split_k);
+        for (int ks = 0; ks < n_k && ok; ++ks, ++c) {
           const uint32_t s = c % C::kStages;
-          if (!wait_bar(&sc.full[s], (c / C::kStages) & 1u, p, &sc, SITE_FULL, kSlack)) { ok = false; break; }
+          if (!wait_own(&sc.full[s], (c / C::kStages) & 1u, p, &sc, SITE_FULL)) { ok = false; break; }
           tc_fence_after();
           const uint32_t base = smem_base + s * C::kStage;
 #pragma unroll
@@ -348,7 +448,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const uint32_t slot = (u + h) % 2;
             if (ks == 0) {  // the half's previous sums have been read back
               if (u + h >= 2 &&
-                  !wait_bar<true>(&sc.acc_empty[slot], ((u + h) / 2 - 1) & 1u, p, &sc, SITE_ACC_EMPTY, kSlack)) {
+                  !wait_own<true>(&sc.acc_empty[slot], ((u + h) / 2 - 1) & 1u, p, &sc, SITE_ACC_EMPTY)) {
                 ok = false;
                 break;
               }
@@ -370,36 +470,41 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp >= 4) {
     uint8_t* stage = epi + (warp - 4) * kEpiWarpBytes;
-    const int quarter = warp % 4, chalf = (warp - 4) / 4;
+    const int quarter = warp % 4, cgroup = (warp - 4) / 4;  // lanes 32 quarter .., columns 64 cgroup .. of a half
+    const Epilogue& e = p.e;
+    const bool res = e.res && e.vec && p.splits == 1;
     uint32_t u = 0;
     bool ok = true;
-    for (int t = pair; t < n_tiles && ok; t += n_pairs) {
+    for (int t = pair; t < n_items && ok; t += n_pairs) {
       int tm, tn;
-      pair_tile(p, t, tm, tn);
+      pair_tile(p, t / p.splits, tm, tn);
       const int i0 = tm * 256 + (int)rank * kRows + quarter * 32;
 #pragma unroll 1
-      for (int h = 0; h < H; ++h, ++u) {
+      for (int b = 0; b < 2 * H && ok; ++b) {
         const uint32_t slot = u % 2;
-        ok = __all_sync(0xffffffffu, wait_bar(&sc.acc_full[slot], (u / 2) & 1u, p, &sc, SITE_ACC, kSlack));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t tacc = sc.tmem_base + ((uint32_t)(quarter * 32) << 16) + slot * 256 + chalf * 128;
-        const int j0 = tn * 256 * H + h * 256 + chalf * 128;
-#pragma unroll 1
-        for (int cb = 0; cb < 2; ++cb) {
-          uint32_t v[64];
-          tmem_ld64(tacc + cb * 64, v);
-          tmem_ld_wait();
-          if (cb == 1) {  // this warp's share of the half is in registers
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if (rank == 0) mbar_arrive(&sc.acc_empty[slot]);
-              else mbar_arrive_cluster(mapa_shared(smem_u32(&sc.acc_empty[slot]), 0));
-            }
-          }
-          pair_store<!BMN>(p, stage, i0, j0 + cb * 64, v);
+        const int j0 = tn * 256 * H + (b / 2) * 256 + cgroup * 64 + (b % 2) * 32;
+        uint4 rr[4];
+        if (res)  // in flight while the sums are waited for
+          rows_in(rr, static_cast<const uint8_t*>(e.res) + ((long long)i0 * e.ldr + j0) * 2, e.ldr * 2, p.M - i0, (p.N - j0) / 8);
+        if (b % 2 == 0) {
+          ok = __all_sync(0xffffffffu, wait_own(&sc.acc_full[slot], (u / 2) & 1u, p, &sc, SITE_ACC));
+          if (!ok) break;
+          tc_fence_after();
         }
+        uint32_t v[32];
+        tmem_ld32(sc.tmem_base + ((uint32_t)(quarter * 32) << 16) + slot * 256 + cgroup * 64 + (b % 2) * 32, v);
+        tmem_ld_wait();
+        if (b % 2 == 1) {  // this warp's share of the half is in registers
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (rank == 0) mbar_arrive(&sc.acc_empty[slot]);
+            else mbar_arrive_cluster(mapa_shared(smem_u32(&sc.acc_empty[slot]), 0));
+          }
+          ++u;
+        }
+        if (p.splits > 1) partial_store(p, t % p.splits, stage, i0, j0, v);
+        else pair_store<!BMN>(e, p.M, p.N, stage, i0, j0, v, rr);
       }
     }
     if (!ok) sc.abort = 1;
@@ -455,6 +560,7 @@ struct StreamParams {
   float* partial;  // [2 gridDim.x][tb][128]
   Epilogue e;
   Ctrl* ctrl;
+  Ctrl* clear;
   unsigned long long timeout_ns;
 };
 
@@ -484,6 +590,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t stage_bytes = kHalf + (uint32_t)p.tb * kBK * 2;
   const uint32_t n_st = (uint32_t)p.stages;
+  clear_ctrl(p.clear);
+  launch_dependents();
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < n_st; ++s) {
       mbar_init(&sc.full[s], 1);
@@ -517,7 +625,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       int tile = (int)(u / p.n_k), ks = (int)(u % p.n_k);
       for (; u < u1; ++u) {
         const uint32_t s = fills % n_st, use = fills / n_st;
-        if (use > 0 && !wait_bar(&sc.empty[s], (use - 1) & 1u, p, &sc, SITE_EMPTY, kSlack)) {
+        if (use > 0 && !wait_own(&sc.empty[s], (use - 1) & 1u, p, &sc, SITE_EMPTY)) {
           sc.abort = 1;
           break;
         }
@@ -547,14 +655,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         const int left = p.n_k - (int)(u % p.n_k);
         const int n = (int)(u1 - u < left ? u1 - u : left);
         const uint32_t slot = seg % 2;
-        if (seg >= 2 && !wait_bar(&sc.acc_empty[slot], (seg / 2 - 1) & 1u, p, &sc, SITE_ACC_EMPTY, kSlack)) {
+        if (seg >= 2 && !wait_own(&sc.acc_empty[slot], (seg / 2 - 1) & 1u, p, &sc, SITE_ACC_EMPTY)) {
           ok = false;
           break;
         }
         tc_fence_after();
         for (int ks = 0; ks < n; ++ks, ++c) {
           const uint32_t s = c % n_st;
-          if (!wait_bar(&sc.full[s], (c / n_st) & 1u, p, &sc, SITE_FULL, kSlack)) { ok = false; break; }
+          if (!wait_own(&sc.full[s], (c / n_st) & 1u, p, &sc, SITE_FULL)) { ok = false; break; }
           tc_fence_after();
           const uint32_t base = smem_base + s * stage_bytes;
 #pragma unroll
@@ -577,7 +685,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       const int tile = (int)(u / p.n_k), first = (int)(u % p.n_k);
       const int n = (int)(u1 - u < p.n_k - first ? u1 - u : p.n_k - first);
       const uint32_t slot = seg % 2;
-      ok = __all_sync(0xffffffffu, wait_bar(&sc.acc_full[slot], (seg / 2) & 1u, p, &sc, SITE_ACC, kSlack));
+      ok = __all_sync(0xffffffffu, wait_own(&sc.acc_full[slot], (seg / 2) & 1u, p, &sc, SITE_ACC));
       if (!ok) break;
       tc_fence_after();
       const int j = tile / p.n_tb * kRows + row, i0 = tile % p.n_tb * p.tb;
@@ -625,28 +733,73 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   if (warp == 1) tmem_dealloc(sc.tmem_base, p.tmem_cols);
 }
 
-// Joins the partials of the tiles whose K range is split, in the order of the CTAs that hold them.
+// Joins the partials of the tiles whose K range is split, in the order of the CTAs that hold them: a thread for each
+// output column, a block for each token of a tile.
 __global__ void __launch_bounds__(128) stream_join(const __grid_constant__ StreamParams p) {
   const int tile = blockIdx.x;
   const long long b = (long long)tile * p.n_k, e = b + p.n_k;
   const int c0 = (int)(b / p.per_cta), c1 = (int)((e - 1) / p.per_cta);
   if (c0 == c1) return;
-  const int j = tile / p.n_tb * kRows + threadIdx.x, i0 = tile % p.n_tb * p.tb;
-  for (int c = blockIdx.y; c < p.tb && i0 + c < p.M; c += gridDim.y) {
-    float sum = 0.f;
-    for (int g = c0; g <= c1; ++g) {
-      const int slot = 2 * g + ((long long)g * p.per_cta >= b ? 0 : 1);  // the tile that CTA g begins or ends with
-      sum += p.partial[((long long)slot * p.tb + c) * kRows + threadIdx.x];
-    }
-    if (j < p.N) finish(p.e, i0 + c, j, sum);
+  const int j = tile / p.n_tb * kRows + threadIdx.x, c = blockIdx.y, i = tile % p.n_tb * p.tb + c;
+  if (i >= p.M) return;
+  wait_previous();
+  float sum = 0.f;
+#pragma unroll 4
+  for (int g = c0; g <= c1; ++g) {
+    const int slot = 2 * g + ((long long)g * p.per_cta >= b ? 0 : 1);  // the tile that CTA g begins or ends with
+    sum += p.partial[((long long)slot * p.tb + c) * kRows + threadIdx.x];
   }
+  if (j < p.N) finish(p.e, i, j, sum);
+}
+
+// Joins the splits' partials in order: four columns to a thread.
+__global__ void __launch_bounds__(256) pair_join(const __grid_constant__ PairParams p) {
+  const long long per = p.ldp / 4, n = per * p.M;
+  const long long t = blockIdx.x * 256ll + threadIdx.x;
+  if (t >= n) return;
+  const long long i = t / per;
+  const int j = (int)(t - i * per) * 4;
+  if (j >= p.N) return;
+  wait_previous();
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) {
+    const float4 v = *reinterpret_cast<const float4*>(p.partial + ((long long)s * p.M + i) * p.ldp + j);
+    sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+  }
+  const Epilogue& e = p.e;
+  float f[4] = {sum.x, sum.y, sum.z, sum.w};
+  if (!e.vec) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (j + c < p.N) finish(e, i, j + c, f[c]);
+    return;
+  }
+  auto add = [&](const void* base, long long at) {
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at);
+    float lo, hi;
+    unpack16(w.x, e.half, lo, hi);
+    f[0] += lo; f[1] += hi;
+    unpack16(w.y, e.half, lo, hi);
+    f[2] += lo; f[3] += hi;
+  };
+  auto put = [&](void* base, long long at) {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + at) = make_uint2(pack16(f[0], f[1], e.half), pack16(f[2], f[3], e.half));
+  };
+  if (e.bias) add(e.bias, j);
+  if (e.z) put(e.z, i * e.ldz + j);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) f[c] = act_fwd(e.act, f[c]);
+  if (e.res) add(e.res, i * e.ldr + j);
+  put(e.y, i * e.ldy + j);
 }
 
 // ================================================================================================
 // Host side
 // ================================================================================================
 constexpr int kStreamCtas = 152;  // most CTAs of stream_gemm (one per SM); bounds the partials
-constexpr int kStreamMaxM = 256;  // stream_gemm takes up to this many rows
+constexpr int kStreamMaxM = 64;   // stream_gemm takes up to this many rows
+constexpr int kPairs = 76;        // pairs of CTAs that a product is split for
 
 // A 16-bit matrix of `outer` rows of `inner` elements, boxes of 64 x box_outer, 128-byte swizzle.  The element type
 // only names the width: the copies do no arithmetic and the fill is zero.
@@ -701,6 +854,36 @@ inline int pairs_of(int dev, int n_sm) {
   return n;
 }
 
+// Launch a kernel whose launch may begin while the previous one ends (it calls wait_previous before it reads).
+template <class Kern, class P>
+inline int launch_after(Kern kern, dim3 grid, int threads, const P& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
+    cudaGetLastError();
+    return PSR_ERR_CUDA;
+  }
+  return PSR_OK;
+}
+
+// Where a call's kernels run and what they share.
+struct Launch {
+  int dev, n_sm;
+  Ctrl* ctrl;
+  Ctrl* clear;     // the control block until a kernel has cleared it, then null
+  float* partial;  // fp32 sums of split products
+  size_t partial_bytes;
+  unsigned long long timeout_ns;
+  cudaStream_t st;
+};
+
 struct Operands {
   const void* a;
   long long lda;
@@ -710,9 +893,8 @@ struct Operands {
 };
 
 template <int H, bool AMN, bool BMN>
-inline int launch_pair(const Operands& o, const Epilogue& e, Ctrl* ctrl, unsigned long long timeout_ns, int dev, int n_sm,
-                       cudaStream_t st) {
-  const int n_pairs = pairs_of<H, AMN, BMN>(dev, n_sm);
+inline int launch_pair(const Operands& o, const Epilogue& e, int splits, Launch& l) {
+  const int n_pairs = pairs_of<H, AMN, BMN>(l.dev, l.n_sm);
   if (n_pairs < 1) return PSR_ERR_CUDA;
   PairParams p = {};
   p.M = o.M;
@@ -720,22 +902,28 @@ inline int launch_pair(const Operands& o, const Epilogue& e, Ctrl* ctrl, unsigne
   p.n_k = (o.K + kBK - 1) / kBK;
   p.tiles_m = (o.M + 255) / 256;
   p.tiles_n = (o.N + 256 * H - 1) / (256 * H);
-  if ((long long)p.tiles_m * p.tiles_n >= (1ll << 31)) return PSR_ERR_UNSUPPORTED;
+  if ((long long)p.tiles_m * p.tiles_n * splits >= (1ll << 31)) return PSR_ERR_UNSUPPORTED;
   p.group = 8;
+  p.split_k = (p.n_k + splits - 1) / splits;
+  p.splits = (p.n_k + p.split_k - 1) / p.split_k;  // none of them empty
+  p.partial = l.partial;
+  p.ldp = 256ll * H * p.tiles_n;
+  if (p.splits > 1 && (size_t)p.splits * o.M * p.ldp * 4 > l.partial_bytes) return PSR_ERR_ARG;
   p.idesc = idesc16(256, 256, AMN, BMN, e.half != 0);
   p.e = e;
-  p.ctrl = ctrl;
-  p.timeout_ns = timeout_ns;
+  p.ctrl = l.ctrl;
+  p.clear = l.clear;
+  p.timeout_ns = l.timeout_ns;
   CUtensorMap ma, mb;
   const bool ok_a = AMN ? tmap16(&ma, o.a, o.M, o.K, o.lda, 64) : tmap16(&ma, o.a, o.K, o.M, o.lda, kRows);
   const bool ok_b = BMN ? tmap16(&mb, o.b, o.N, o.K, o.ldb, 64) : tmap16(&mb, o.b, o.K, o.N, o.ldb, kRows);
   if (!ok_a || !ok_b) return PSR_ERR_CUDA;
-  const int tiles = p.tiles_m * p.tiles_n;
+  const int items = p.tiles_m * p.tiles_n * p.splits;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * (tiles < n_pairs ? tiles : n_pairs)));
+  cfg.gridDim = dim3((unsigned)(2 * (items < n_pairs ? items : n_pairs)));
   cfg.blockDim = dim3(kPairThreads);
   cfg.dynamicSmemBytes = PairCfg<H>::kSmem;
-  cfg.stream = st;
+  cfg.stream = l.st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -747,19 +935,35 @@ inline int launch_pair(const Operands& o, const Epilogue& e, Ctrl* ctrl, unsigne
     cudaGetLastError();
     return PSR_ERR_CUDA;
   }
-  return PSR_OK;
+  l.clear = nullptr;
+  if (p.splits == 1) return PSR_OK;
+  return launch_after(pair_join, dim3((unsigned)((p.ldp / 4 * o.M + 255) / 256)), 256, p, l.st);
 }
 
-// Bytes of partials that stream_gemm may leave for M rows.
-inline size_t stream_partial_bytes(int M) {
-  if (M > kStreamMaxM) return 0;
-  return (size_t)2 * kStreamCtas * ((M + 15) / 16 * 16) * kRows * 4;
+// Whether stream_gemm takes a product with M rows of A.
+inline bool streams(int M) { return M <= kStreamMaxM; }
+
+// Parts that a product of few tiles is split into along K so that every pair of CTAs has one: as many as still fit at
+// once, of at least 8 K steps (a part's sums go through memory: 256 KiB written and read for each 256 x 256 tile).
+inline int pair_splits(int M, int N, int K) {
+  const long long tiles = ((M + 255ll) / 256) * ((N + 255ll) / 256);
+  long long s = kPairs / tiles;
+  const long long most = ((K + kBK - 1) / kBK) / 8;
+  if (s > most) s = most;
+  return s < 1 ? 1 : (int)s;
+}
+
+// Bytes of fp32 partials that a product with C [M][N] may leave (weights: A's rows are not tokens, so it never streams).
+inline size_t partial_bytes(int M, int N, int K, bool weights) {
+  if (!weights && streams(M)) return (size_t)2 * kStreamCtas * ((M + 15) / 16 * 16) * kRows * 4;
+  const int s = pair_splits(M, N, K);
+  return s > 1 ? (size_t)s * M * ((N + 255) / 256 * 256) * 4 : 0;
 }
 
 // o.a: the tokens [M][K], o.b: W, K-major [N][K] or (WMN) [K][N].
 template <bool WMN>
-inline int launch_stream(const Operands& o, const Epilogue& e, float* partial, Ctrl* ctrl, unsigned long long timeout_ns,
-                         int dev, int n_sm, cudaStream_t st) {
+inline int launch_stream(const Operands& o, const Epilogue& e, Launch& l) {
+  const int dev = l.dev, n_sm = l.n_sm;
   static std::mutex mu;
   static bool known[64] = {};
   {
@@ -791,19 +995,20 @@ inline int launch_stream(const Operands& o, const Epilogue& e, float* partial, C
   p.tmem_cols = 32;
   while (p.tmem_cols < 2u * p.tb) p.tmem_cols *= 2;
   p.idesc = idesc16(128, p.tb, WMN, false, e.half != 0);
-  p.partial = partial;
+  p.partial = l.partial;
   p.e = e;
-  p.ctrl = ctrl;
-  p.timeout_ns = timeout_ns;
+  p.ctrl = l.ctrl;
+  p.clear = l.clear;
+  p.timeout_ns = l.timeout_ns;
   CUtensorMap mw, mx;
   const bool ok_w = WMN ? tmap16(&mw, o.b, o.N, o.K, o.ldb, 64) : tmap16(&mw, o.b, o.K, o.N, o.ldb, kRows);
   if (!ok_w || !tmap16(&mx, o.a, o.K, o.M, o.lda, p.tb)) return PSR_ERR_CUDA;
   const unsigned grid = (unsigned)((units + per - 1) / per);
-  stream_gemm<WMN><<<grid, kStreamThreads, kStreamSmem, st>>>(p, mw, mx);
-  int rc = launch_status();
+  stream_gemm<WMN><<<grid, kStreamThreads, kStreamSmem, l.st>>>(p, mw, mx);
+  const int rc = launch_status();
+  l.clear = nullptr;
   if (rc != PSR_OK || per % p.n_k == 0) return rc;
-  stream_join<<<dim3((unsigned)p.n_tiles, (unsigned)(p.tb < 16 ? p.tb : 16)), 128, 0, st>>>(p);
-  return launch_status();
+  return launch_after(stream_join, dim3((unsigned)p.n_tiles, (unsigned)o.M), 128, p, l.st);
 }
 
 }  // namespace linear
