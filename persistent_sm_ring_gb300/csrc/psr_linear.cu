@@ -61,6 +61,91 @@ static int launch_simple(const void* a, long long lda, const void* b, long long 
 }
 
 // ------------------------------------------------------------------------------------------------
+// One to four rows of x: dot products on the fp32 units
+// ------------------------------------------------------------------------------------------------
+// Bound by reading W once.  A warp takes R rows of W, a lane 16 bytes of each at a time (the warp 512 adjacent bytes of a
+// row), kAhead of them in flight, and keeps M x R sums; x comes from L1.  Against the tensor core kernel this has no
+// tensor memory, barriers or partials to set up.
+template <class T, int M, int R>
+__global__ void __launch_bounds__(256)
+    gemv_kernel(const T* __restrict__ x, long long ldx, const T* __restrict__ w, long long ldw, int N, int K,
+                const __grid_constant__ Epilogue e, Ctrl* clear) {
+  constexpr int kAhead = 8 / R;
+  clear_ctrl(clear);
+  const int lane = threadIdx.x % 32;
+  const int j0 = (blockIdx.x * 8 + threadIdx.x / 32) * R;
+  if (j0 >= N) return;
+  const T* wr[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) wr[r] = w + (long long)min(j0 + r, N - 1) * ldw + lane * 8;
+  float acc[M][R] = {};
+  auto dot = [&](const uint4 (&v)[R], int k) {
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const uint4 u = *reinterpret_cast<const uint4*>(x + m * ldx + k);
+      const uint32_t a[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint32_t b[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float al, ah, bl, bh;
+          unpack16(a[q], std::is_same<T, __half>::value, al, ah);
+          unpack16(b[q], std::is_same<T, __half>::value, bl, bh);
+          acc[m][r] = fmaf(al, bl, acc[m][r]);
+          acc[m][r] = fmaf(ah, bh, acc[m][r]);
+        }
+      }
+    }
+  };
+  int k = 0;
+  for (; k + 256 * kAhead <= K; k += 256 * kAhead) {
+    uint4 v[kAhead][R];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+      for (int r = 0; r < R; ++r) v[a][r] = __ldcs(reinterpret_cast<const uint4*>(wr[r] + k + 256 * a));
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) dot(v[a], k + 256 * a + lane * 8);
+  }
+  for (; k + lane * 8 < K; k += 256) {  // K is a multiple of 8
+    uint4 v[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] = __ldcs(reinterpret_cast<const uint4*>(wr[r] + k));
+    dot(v, k + lane * 8);
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) acc[m][r] += __shfl_xor_sync(0xffffffffu, acc[m][r], o);
+      if (lane == m * R + r && j0 + r < N) finish(e, m, j0 + r, acc[m][r]);
+    }
+}
+
+template <class T>
+static int launch_gemv(const Operands& o, const Epilogue& e, Launch& l) {
+  // two rows of W to a warp halve the reads of x, one keeps more warps busy when W is short
+  const bool two = o.N >= 8 * 8 * l.n_sm;
+  const unsigned grid = (unsigned)((o.N + (two ? 16 : 8) - 1) / (two ? 16 : 8));
+  const T *x = static_cast<const T*>(o.a), *w = static_cast<const T*>(o.b);
+  auto go = [&](auto m) {
+    constexpr int M = decltype(m)::value;
+    if (two) gemv_kernel<T, M, 2><<<grid, 256, 0, l.st>>>(x, o.lda, w, o.ldb, o.N, o.K, e, l.clear);
+    else gemv_kernel<T, M, 1><<<grid, 256, 0, l.st>>>(x, o.lda, w, o.ldb, o.N, o.K, e, l.clear);
+  };
+  switch (o.M) {
+    case 1: go(std::integral_constant<int, 1>()); break;
+    case 2: go(std::integral_constant<int, 2>()); break;
+    case 3: go(std::integral_constant<int, 3>()); break;
+    default: go(std::integral_constant<int, 4>());
+  }
+  l.clear = nullptr;
+  return launch_status();
+}
+
+// ------------------------------------------------------------------------------------------------
 // dz = dy act'(z), and the column sums of its unrounded values over chunks of rows
 // ------------------------------------------------------------------------------------------------
 // Memory bound.  A thread takes V adjacent columns (16 bytes where the rows allow it) of every eighth row of a chunk, the
@@ -193,17 +278,21 @@ static int product(const Operands& o, Epilogue e, Launch& l) {
     return launch_simple<T, AMN, BMN>(o.a, o.lda, o.b, o.ldb, o.M, o.N, o.K, e, l);
   auto flat = [&](const void* p, long long ld) { return !p || (aligned_to(p, 16) && (o.M == 1 || ld % 8 == 0)); };
   e.vec = o.N % 8 == 0 && flat(e.y, e.ldy) && flat(e.z, e.ldz) && flat(e.res, e.ldr) && flat(e.bias, 0);
+  if constexpr (!AMN && !BMN)
+    if (o.M <= 4 && o.K % 8 == 0) return launch_gemv<T>(o, e, l);
   if constexpr (!AMN)
     if (streams(o.M)) return launch_stream<BMN>(o, e, l);
   const int splits = pair_splits(o.M, o.N, o.K);
   if (splits > 1) return launch_pair<1, AMN, BMN>(o, e, splits, l);
-  // A wave of 512-column tiles takes 16 clocks for each K plus its epilogue's first three quarters, when the accumulators
-  // are not free for the next tile; one of 256-column tiles 9.2 for each K (the tile loads bound it) or its whole epilogue,
-  // whichever is longer.
+  // A wave of 512-column tiles takes 16 clocks for each K and then its epilogue, when the accumulators are not free for the
+  // next tile (all SMs write at once); one of 256-column tiles 11.5 for each K (the tile loads bound it) with the
+  // epilogue of the tile before behind it.  Clocks as measured at 2048 x 8192 x 4096 (89 us and 103 us, with gelu, bias,
+  // residual and z 109 and 116) and 8192 x 8192 x 1024 (110 and 107; 178 and 147).
   const long long rows = (o.M + 255) / 256, n_pairs = l.n_sm / 2;
   auto waves = [&](long long cols) { return (rows * ((o.N + cols - 1) / cols) + n_pairs - 1) / n_pairs; };
-  const double epi = 1500.0 + (e.act ? 3000.0 : 0.0) + (e.z ? 1000.0 : 0.0) + (e.res ? 1000.0 : 0.0);
-  const double two = waves(512) * (16.0 * o.K + 1.5 * epi), one = waves(256) * (9.2 * o.K > epi ? 9.2 * o.K : epi);
+  const double epi = 6000.0 + (e.act ? 3000.0 : 0.0) + (e.z ? 4000.0 : 0.0) + (e.res ? 4000.0 : 0.0);  // of 256 columns
+  const double two = waves(512) * (16.0 * o.K + 2.0 * epi);
+  const double one = waves(256) * (11.5 * o.K + 1500.0 > epi ? 11.5 * o.K + 1500.0 : epi);
   return two <= one ? launch_pair<2, AMN, BMN>(o, e, 1, l) : launch_pair<1, AMN, BMN>(o, e, 1, l);
 }
 
