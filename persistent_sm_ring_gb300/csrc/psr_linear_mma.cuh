@@ -148,10 +148,13 @@ __device__ __forceinline__ void unpack16(uint32_t v, int half, float& lo, float&
   }
 }
 
+// One copy of the code for kernels that run their epilogue once: there, fetching instructions is what takes the time.
+__device__ __noinline__ float act_call(int act, float z) { return act_fwd(act, z); }
+
 __device__ __forceinline__ void finish(const Epilogue& e, long long i, int j, float v) {
   if (e.bias) v += load16(e.bias, j, e.half);
   if (e.z) store16(e.z, i * e.ldz + j, e.half, v);
-  v = act_fwd(e.act, v);
+  if (e.act) v = act_call(e.act, v);
   if (e.res) v += load16(e.res, i * e.ldr + j, e.half);
   store16(e.y, i * e.ldy + j, e.half, v);
 }
@@ -546,7 +549,6 @@ constexpr int kStreamThreads = 256;
 constexpr int kStreamArea = 216 * 1024;  // shared memory of the stages
 constexpr int kStreamMaxStages = 12;
 constexpr int kStreamSmem = 1024 + kStreamArea;
-static_assert(kStreamSmem + 2048 <= 232448, "shared memory");
 
 struct StreamParams {
   int M, N;        // tokens, output columns (the rows of W)
@@ -568,7 +570,9 @@ struct StreamSmem {
   uint64_t full[kStreamMaxStages], empty[kStreamMaxStages], acc_full[2], acc_empty[2], drain;
   uint32_t tmem_base;
   volatile uint32_t abort;
+  float sums[4][16][32];  // epilogue warp, token, lane
 };
+static_assert(kStreamSmem + sizeof(StreamSmem) <= 232448, "shared memory");
 
 // 32 lanes x 32 bits, 16 consecutive columns
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -690,6 +694,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       tc_fence_after();
       const int j = tile / p.n_tb * kRows + row, i0 = tile % p.n_tb * p.tb;
       const bool whole = n == p.n_k;
+      const float bias = whole && p.e.bias && j < p.N ? load16(p.e.bias, j, p.e.half) : 0.f;
       float* part = p.partial + (2ll * blockIdx.x + (u == u0 ? 0 : 1)) * p.tb * kRows + row;
       const uint32_t tacc = sc.tmem_base + ((uint32_t)(quarter * 32) << 16) + slot * p.tb;
 #pragma unroll 1
@@ -697,11 +702,34 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         uint32_t v[16];
         tmem_ld16(tacc + c, v);
         tmem_ld_wait();
+        const int n_c = min(16, p.M - i0 - c);
+        if (!whole) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (i0 + c + e < p.M) {
-            if (!whole) part[(c + e) * kRows] = __uint_as_float(v[e]);
-            else if (j < p.N) finish(p.e, i0 + c + e, j, __uint_as_float(v[e]));
+          for (int e = 0; e < 16; ++e)
+            if (e < n_c) part[(c + e) * kRows] = __uint_as_float(v[e]);
+          continue;
+        }
+        if (j >= p.N) continue;
+        // four tokens at a time, their residuals in flight together; each lane reads its own sums back
+        float* own = &sc.sums[quarter][0][lane];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) own[e * 32] = __uint_as_float(v[e]);
+#pragma unroll 1
+        for (int e = 0; e < n_c; e += 4) {
+          float f[4], r[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const long long i = i0 + c + e + q;
+            f[q] = own[(e + q) * 32] + bias;
+            r[q] = p.e.res && e + q < n_c ? load16(p.e.res, i * p.e.ldr + j, p.e.half) : 0.f;
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (e + q >= n_c) break;
+            const long long i = i0 + c + e + q;
+            if (p.e.z) store16(p.e.z, i * p.e.ldz + j, p.e.half, f[q]);
+            if (p.e.act) f[q] = act_call(p.e.act, f[q]);
+            store16(p.e.y, i * p.e.ldy + j, p.e.half, f[q] + r[q]);
           }
         }
       }
