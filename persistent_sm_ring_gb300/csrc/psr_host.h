@@ -1,4 +1,5 @@
-// Host-side checks and device element types shared by the layer operators (rotary positions, linear, 4-bit cache).
+// Shared by the layer operators (rotary positions, linear, 4-bit cache): host-side checks, element types, bounded waits
+// and launches that follow one another.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -8,6 +9,7 @@
 #include <cstdint>
 
 #include "../../include/psr.h"
+#include "psr_control.cuh"
 
 namespace psr {
 
@@ -48,5 +50,56 @@ template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 template <>
 __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+
+// Bounded wait on a barrier: false after the timeout, or once another wait of the CTA has given up.  The control block's
+// abort word is not consulted: it is cleared by the launch itself (clear_ctrl), while other CTAs already run.
+template <bool CL = false, class KP, class SC>
+__device__ __forceinline__ bool wait_own(uint64_t* bar, uint32_t parity, const KP& p, SC* sc, uint32_t site) {
+  auto poll = [&]() { return CL ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+  if (poll()) return true;
+  const uint64_t t0 = globaltimer_ns();
+  uint32_t it = 0;
+  while (true) {
+    if (poll()) return true;
+    if ((++it & 15u) == 0) {
+      if (sc->abort) return false;
+      if (globaltimer_ns() - t0 > p.timeout_ns) {
+        raise_error(p, site);
+        sc->abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// The first kernel of a call clears the control block (a memset before it would cost a launch).  A wait of the same call
+// can give up only a timeout later.
+__device__ __forceinline__ void clear_ctrl(Ctrl* ctrl) {
+  if (ctrl && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < sizeof(Ctrl) / 4)
+    reinterpret_cast<uint32_t*>(ctrl)[threadIdx.x] = 0;
+}
+
+// Programmatic launches: let the next kernel's launch begin / wait for the whole previous kernel and its writes.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launch a kernel whose launch may begin while the previous one ends (it calls wait_previous before it reads).
+template <class Kern, class P>
+inline int launch_after(Kern kern, dim3 grid, int threads, const P& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
+    cudaGetLastError();
+    return PSR_ERR_CUDA;
+  }
+  return PSR_OK;
+}
 
 }  // namespace psr

@@ -5,9 +5,10 @@
 // One scale and offset for a row (not for groups of columns) keeps them out of the products: with c the codes,
 //     q . k = scale (q . c) + offset sum(q),        sum_j p_j v_j = sum_j (p_j scale_j) c_j + sum_j p_j offset_j.
 #include <cmath>
-#include <cstring>
+#include <mutex>
+#include <type_traits>
 
-#include "psr_control.cuh"
+#include "psr_device.cuh"
 #include "psr_host.h"
 
 namespace psr {
@@ -151,8 +152,30 @@ __global__ void read_kernel(const ReadParams p) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Attention: one block for a query row, its warps over the positions
+// Attention
 // ------------------------------------------------------------------------------------------------
+// Bound by reading the cache once.  A unit is one block of 16 tokens for one KV head and a tile of up to 8 NT query rows
+// (the group's heads times the new tokens); the units of all sequences stand in a line, segment by segment (a segment:
+// sequence, head, row tile), and each CTA takes an equal stretch of it, so ragged batches and single long sequences load
+// every SM alike.  A segment that lies within one CTA is finished there; the pieces of one that does not meet in
+// combine_kernel through fp32 partial results and their running maxima and sums, as the ring's chunks do.
+//
+// Each warp has its own ring of stages, filled with one bulk copy per block, and its own softmax state:
+//   S^T[token][row] = K codes . q      (mma.m16n8k16: tokens on its 16 rows, query rows on its 8 columns)
+//   O^T[column][row] += V codes^T . P  (columns of V on the 16 rows, tokens in the contraction)
+// The codes become 16-bit floats 16 + c with one shift and one three-input logic operation for two of them (the code goes
+// to the top bits of the mantissa of 16); scale and offset are applied to the sums, and 16 times the sum of the other factor
+// is taken off there.  Any order of the contraction will do, so K and V fragments are read straight from the stage:
+// a lane takes 16 adjacent bytes of a K row, and the tokens are dealt to the mma's rows so that V's loads fall on
+// different banks.  P leaves the first product in the layout that movmatrix turns into the second one's operand.
+// The maximum is only raised when a score passes it by kRaise: the check is one vote, the weights stay below 2^kRaise.
+constexpr int kWarps = 8;
+constexpr int kStages = 4;
+constexpr int kMaxCtas = 2 * 152;  // bounds the partial results
+constexpr float kRaise = 8.f;
+constexpr float kLog2e = 1.4426950408889634f;
+enum : uint32_t { SITE_BLOCK = 51 };
+
 struct AttnParams {
   Cache c;
   const void* q;
@@ -160,70 +183,500 @@ struct AttnParams {
   float* lse;
   const int32_t* lens;
   psr_strides sq, so;
-  int B, Hq, S;
+  int B, Hq, S, group, n_rt;  // group = Hq / Hkv; row tiles of group * S rows
+  int page_shift;             // log2(page / 16)
+  int vec;                    // q's rows are 16-byte aligned
   float scale;
+  float* part;                // [2 kMaxCtas][rows of a tile][D + 2]
+  Ctrl* ctrl;
+  unsigned long long timeout_ns;
 };
 
-template <class T, int D>
-__global__ void __launch_bounds__(128) attn_kernel(const AttnParams p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  __shared__ float so[4][D], sm[4], sl[4];
-  const long long row = blockIdx.x;
-  const int i = (int)(row % p.S), hq = (int)(row / p.S % p.Hq), b = (int)(row / p.S / p.Hq);
-  const int h = hq / (p.Hq / p.c.Hkv);
+// Blocks of sequence b: 0 if it is empty or its length is out of range.
+__device__ __forceinline__ int blocks_of(const AttnParams& p, int b) {
   const int n = p.lens[b];
-  const T* q = static_cast<const T*>(p.q) + b * p.sq.b + hq * p.sq.h + i * p.sq.s;
-  float qv[E], o[E] = {}, m = -INFINITY, l = 0.f, bad = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) qv[e] = to_f32(q[lane * E + e]) * p.scale;
-  if (n < 0 || n > p.c.max_pages * (long long)p.c.page) bad = NAN;
-  else
-    for (int j = warp; j < n; j += 4) {
-      const uint8_t* blk = block_of(p.c, b, h, j);
-      if (!blk) { bad = NAN; continue; }
-      if (j > n - p.S + i) continue;
-      auto load = [&](int kv, float (&x)[E]) {
-        const __nv_bfloat162 pair = *reinterpret_cast<const __nv_bfloat162*>(blk + kBlk * D + kv * kBlk * 4 + j % kBlk * 4);
-        const uint8_t* src = blk + kv * kBlk * (D / 2) + j % kBlk * (D / 2) + lane * (E / 2);
-        uint32_t codes;
-        if constexpr (E == 4) codes = *reinterpret_cast<const uint16_t*>(src);
-        else codes = *src;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          x[e] = fmaf((float)((codes >> (4 * e)) & 15u), __bfloat162float(pair.x), __bfloat162float(pair.y));
-      };
-      float kk[E], vv[E], x = 0.f;
-      load(0, kk);
-      load(1, vv);
-#pragma unroll
-      for (int e = 0; e < E; ++e) x += qv[e] * kk[e];
-      x = warp_sum(x);
-      const float mn = fmaxf(m, x);
-      const float a = expf(m - mn), w = expf(x - mn);
-      m = mn;
-      l = l * a + w;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * a + w * vv[e];
+  return n < 0 || n > (long long)p.c.max_pages * p.c.page ? 0 : (n + kBlk - 1) / kBlk;
+}
+
+// A place in the line of units.
+struct Cursor {
+  int b, h, rt, len;
+  long long start;  // first unit of the segment
+  __device__ __forceinline__ void advance(const AttnParams& p, long long u) {
+    while (u >= start + len) {
+      start += len;
+      if (++rt == p.n_rt) {
+        rt = 0;
+        if (++h == p.c.Hkv) {
+          h = 0;
+          len = blocks_of(p, ++b);
+        }
+      }
     }
+  }
+};
+
+// One warp: units before sequence b for every b in turn, 32 at a time.  Returns their total; with target >= 0 the cursor of
+// the segment that holds that unit (target < total).
+__device__ __forceinline__ long long walk(const AttnParams& p, long long target, Cursor& cur) {
+  const int lane = threadIdx.x % 32;
+  const int per = p.c.Hkv * p.n_rt;
+  long long base = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int n = b0 + lane < p.B ? blocks_of(p, b0 + lane) : 0;
+    const long long own = (long long)n * per;
+    long long sum = own;
 #pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
+    for (int o = 1; o < 32; o *= 2) {
+      const long long v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    const long long all = __shfl_sync(0xffffffffu, sum, 31);
+    if (target >= 0 && target < base + all) {
+      const int at = __ffs(__ballot_sync(0xffffffffu, target < base + sum)) - 1;
+      const int len = __shfl_sync(0xffffffffu, n, at);
+      const long long first = base + __shfl_sync(0xffffffffu, sum - own, at);
+      const int seg = (int)((target - first) / len);
+      cur.b = b0 + at;
+      cur.h = seg / p.n_rt;
+      cur.rt = seg % p.n_rt;
+      cur.len = len;
+      cur.start = first + (long long)seg * len;
+      return base;
+    }
+    base += all;
+  }
+  return base;
+}
+
+// Units of a CTA: an equal share, at least one block a warp.
+__device__ __forceinline__ long long share(long long total, int ctas) {
+  const long long per = (total + ctas - 1) / ctas;
+  return per < kWarps ? kWarps : per;
+}
+
+template <class T>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// Nibbles P and P + 4 of w as the 16-bit floats 16 + c.
+template <class T, int P>
+__device__ __forceinline__ uint32_t codes16(uint32_t w) {
+  if constexpr (std::is_same<T, __half>::value) {  // 16 = 0x4C00, the code in mantissa bits 6..9
+    const uint32_t s = P == 0 ? w << 6 : P == 1 ? w << 2 : P == 2 ? w >> 2 : w >> 6;
+    return (s & 0x03C003C0u) | 0x4C004C00u;
+  } else {  // 16 = 0x4180, mantissa bits 3..6
+    const uint32_t s = P == 0 ? w << 3 : P == 1 ? w >> 1 : P == 2 ? w >> 5 : w >> 9;
+    return (s & 0x00780078u) | 0x41804180u;
+  }
+}
+
+template <int D, int NT>
+struct AttnSmem {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kBytes = kBlk * (D + 8);
+  alignas(128) uint8_t ring[kWarps][kStages][kBytes];
+  alignas(16) float o[kWarps][kRows][D];  // a segment's results, by warp
+  float m[kWarps][kRows], l[kWarps][kRows], corr[kWarps][kRows];
+  uint64_t full[kWarps][kStages];
+  uint32_t bad[kWarps][kStages];  // the stage's block has no page
+  volatile uint32_t abort;
+};
+
+template <class T, int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(const __grid_constant__ AttnParams p) {
+  using Sm = AttnSmem<D, NT>;
+  constexpr int kRows = Sm::kRows, kBytes = Sm::kBytes;
+  constexpr int KW = D / 32;  // words of K codes a lane takes of a row
+  constexpr int VW = D / 64;  // words of V codes a lane takes of a token
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
+  clear_ctrl(p.ctrl);
+  launch_dependents();
+  if (threadIdx.x == 0) sm.abort = 0;
   if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l + bad;
+    for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[warp][s], 1);
+    fence_barrier_init();
+  }
+  Cursor seg = {};
+  const long long total = walk(p, -1, seg);
+  const long long per = share(total, gridDim.x);
+  const long long u0 = blockIdx.x * per, u1 = u0 + per < total ? u0 + per : total;
+  if (u0 >= u1) return;
+  walk(p, u0, seg);
+  __syncthreads();
+
+  // ---- the warp's ring: unit u0 + warp + 8 k goes to stage k % kStages -------------------------
+  Cursor pre = seg;
+  long long up = u0 + warp;
+  uint32_t filled = 0, used = 0;
+  int page_id = -1;
+  auto look_up = [&]() {  // the next unit's page, read a step ahead of its copy
+    if (up < u1) {
+      pre.advance(p, up);
+      page_id = p.c.table[(long long)pre.b * p.c.max_pages + ((int)(up - pre.start) >> p.page_shift)];
+    }
+  };
+  auto fill = [&]() {
+    if (up >= u1) return;
+    if (lane == 0) {
+      const uint32_t s = filled % kStages;
+      const bool ok = page_id >= 0 && page_id < p.c.n_pages;
+      sm.bad[warp][s] = !ok;
+      if (ok) {
+        const int blk = (int)(up - pre.start), per_page = 1 << p.page_shift;
+        const uint8_t* src = p.c.base + (((long long)page_id * p.c.Hkv + pre.h) * per_page + (blk & (per_page - 1))) * kBytes;
+        mbar_expect_tx(&sm.full[warp][s], kBytes);
+        bulk_load(smem_u32(sm.ring[warp][s]), src, kBytes, &sm.full[warp][s]);
+      } else {
+        mbar_arrive(&sm.full[warp][s]);
+      }
+    }
+    ++filled;
+    up += kWarps;
+    look_up();
+  };
+  look_up();
+  for (int s = 0; s < kStages; ++s) fill();
+
+  for (long long lo = u0; lo < u1;) {
+    seg.advance(p, lo);
+    const long long hi = seg.start + seg.len < u1 ? seg.start + seg.len : u1;
+    const int n = p.lens[seg.b];
+    const int R = p.group * p.S;  // query rows of the KV head: row = new token * group + head of the group
+    // ---- query fragments: the row g of each tile, columns in the order of the K codes' words -----
+    uint32_t qf[NT][KW][4];
+    float qsum[NT][2];   // of rows 2t and 2t + 1
+    int last[NT][2];     // last position that they see
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = seg.rt * kRows + nt * 8 + g;
+      float sum = 0.f;
+      if (row < R) {
+        const T* q = static_cast<const T*>(p.q) + (long long)seg.b * p.sq.b +
+                     (long long)(seg.h * p.group + row % p.group) * p.sq.h + (long long)(row / p.group) * p.sq.s + t * (D / 4);
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          uint4 v;
+          if (p.vec) {
+            v = *reinterpret_cast<const uint4*>(q + w * 8);
+          } else {
+            uint32_t e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              e[i] = reinterpret_cast<const uint16_t*>(q)[w * 8 + 2 * i] |
+                     (uint32_t)reinterpret_cast<const uint16_t*>(q)[w * 8 + 2 * i + 1] << 16;
+            v = make_uint4(e[0], e[1], e[2], e[3]);
+          }
+          qf[nt][w][0] = __byte_perm(v.x, v.z, 0x5410);  // columns (0, 4), (1, 5), (2, 6), (3, 7)
+          qf[nt][w][1] = __byte_perm(v.x, v.z, 0x7632);
+          qf[nt][w][2] = __byte_perm(v.y, v.w, 0x5410);
+          qf[nt][w][3] = __byte_perm(v.y, v.w, 0x7632);
+          const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint16_t lo16 = (uint16_t)e[i], hi16 = (uint16_t)(e[i] >> 16);
+            sum += to_f32(*reinterpret_cast<T*>(&lo16)) + to_f32(*reinterpret_cast<T*>(&hi16));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int w = 0; w < KW; ++w) qf[nt][w][0] = qf[nt][w][1] = qf[nt][w][2] = qf[nt][w][3] = 0;
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        qsum[nt][c] = __shfl_sync(0xffffffffu, sum, (2 * t + c) * 4);
+        last[nt][c] = n - p.S + (seg.rt * kRows + nt * 8 + 2 * t + c) / p.group;
+      }
+    }
+    const float s2 = p.scale * kLog2e;
+    float acc[NT][D / 16][4], m[NT][2], l[NT][2], corr[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = corr[nt][0] = corr[nt][1] = 0.f;
+    }
+    // ---- this warp's blocks of the segment -------------------------------------------------------
+    long long u = lo + (warp + kWarps - (int)((lo - u0) % kWarps)) % kWarps;
+    for (; u < hi; u += kWarps) {
+      const uint32_t s = used % kStages;
+      const bool in = wait_own(&sm.full[warp][s], (used / kStages) & 1u, p, &sm, SITE_BLOCK);
+      ++used;
+      if (!__all_sync(0xffffffffu, in) || sm.bad[warp][s]) {
+        l[0][0] = l[0][1] = NAN;
+        if (NT == 2) l[NT - 1][0] = l[NT - 1][1] = NAN;
+      } else {
+        const uint8_t* blk = sm.ring[warp][s];
+        // mma row g holds token g / 2 + 4 (g % 2) of the block, row g + 8 that plus 8
+        const int tok = g / 2 + 4 * (g % 2);
+        const int j0 = (int)(u - seg.start) * kBlk + tok;
+        uint32_t ka[KW], kb[KW];
+        if constexpr (D == 128) {
+          const uint4 a = *reinterpret_cast<const uint4*>(blk + tok * 64 + t * 16);
+          const uint4 b = *reinterpret_cast<const uint4*>(blk + (tok + 8) * 64 + t * 16);
+          ka[0] = a.x; ka[1] = a.y; ka[2] = a.z; ka[3] = a.w;
+          kb[0] = b.x; kb[1] = b.y; kb[2] = b.z; kb[3] = b.w;
+        } else {
+          const uint2 a = *reinterpret_cast<const uint2*>(blk + tok * 32 + t * 8);
+          const uint2 b = *reinterpret_cast<const uint2*>(blk + (tok + 8) * 32 + t * 8);
+          ka[0] = a.x; ka[1] = a.y;
+          kb[0] = b.x; kb[1] = b.y;
+        }
+        float x[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          const uint32_t a0 = codes16<T, 0>(ka[w]), a1 = codes16<T, 0>(kb[w]);
+          const uint32_t a2 = codes16<T, 1>(ka[w]), a3 = codes16<T, 1>(kb[w]);
+          const uint32_t a4 = codes16<T, 2>(ka[w]), a5 = codes16<T, 2>(kb[w]);
+          const uint32_t a6 = codes16<T, 3>(ka[w]), a7 = codes16<T, 3>(kb[w]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816<T>(x[nt], a0, a1, a2, a3, qf[nt][w][0], qf[nt][w][1]);
+            mma16816<T>(x[nt], a4, a5, a6, a7, qf[nt][w][2], qf[nt][w][3]);
+          }
+        }
+        // V's codes: tokens t, t + 4 (contraction 2t, 2t + 1) and t + 8, t + 12, this lane's D / 8 columns from g D / 8 on
+        uint32_t va[4][VW];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint8_t* v = blk + kBlk * D / 2 + (t + 4 * i) * (D / 2) + g * (D / 16);
+          if constexpr (D == 128) {
+            const uint2 w = *reinterpret_cast<const uint2*>(v);
+            va[i][0] = w.x;
+            va[i][1] = w.y;
+          } else {
+            va[i][0] = *reinterpret_cast<const uint32_t*>(v);
+          }
+        }
+        const uint32_t* pairs = reinterpret_cast<const uint32_t*>(blk + kBlk * D);
+        const uint32_t kp0 = pairs[tok], kp1 = pairs[tok + 8], vp0 = pairs[16 + tok], vp1 = pairs[16 + tok + 8];
+        auto lo_of = [](uint32_t v) { return __uint_as_float(v << 16); };
+        auto hi_of = [](uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); };
+        // scores in powers of two: scale (s_k (sum q (16 + c) - 16 sum q) + o_k sum q)
+        const float ks[2] = {lo_of(kp0) * s2, lo_of(kp1) * s2};
+        const float ko[2] = {fmaf(lo_of(kp0), -16.f, hi_of(kp0)) * s2, fmaf(lo_of(kp1), -16.f, hi_of(kp1)) * s2};
+        const float vs[2] = {lo_of(vp0), lo_of(vp1)};
+        const float vo[2] = {fmaf(lo_of(vp0), 8.f, hi_of(vp0)), fmaf(lo_of(vp1), 8.f, hi_of(vp1))};
+        bool raise = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {  // token e / 2, row e % 2
+            x[nt][e] = fmaf(ks[e / 2], x[nt][e], ko[e / 2] * qsum[nt][e % 2]);
+            if (j0 + 8 * (e / 2) > last[nt][e % 2]) x[nt][e] = -INFINITY;
+            raise = raise || x[nt][e] > m[nt][e % 2] + kRaise;
+          }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float top = fmaxf(m[nt][c], fmaxf(x[nt][c], x[nt][2 + c]));
+#pragma unroll
+              for (int o = 4; o < 32; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+              const float f = top == -INFINITY ? 1.f : ex2_approx(m[nt][c] - top);
+              m[nt][c] = top;
+              l[nt][c] *= f;
+              corr[nt][c] *= f;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                acc[nt][i][c] *= f;
+                acc[nt][i][2 + c] *= f;
+              }
+            }
+        }
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // token
+            float w[2], ws[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const bool seen = j0 + 8 * h <= last[nt][c];
+              w[c] = seen ? ex2_approx(x[nt][2 * h + c] - m[nt][c]) : 0.f;
+              ws[c] = seen ? w[c] * vs[h] : 0.f;  // a row that is not seen may hold anything
+              l[nt][c] += w[c];
+            }
+            // weights times scale in bf16, the operand of the product; what is taken off for the 24 = 16 + 8 uses the same
+            // rounded values, so that the rounding meets c - 8 only
+            const uint32_t r = pack_bf16x2(ws[0], ws[1]);
+            corr[nt][0] += fmaf(lo_of(r), -24.f, w[0] != 0.f ? w[0] * vo[h] : 0.f);
+            corr[nt][1] += fmaf(hi_of(r), -24.f, w[1] != 0.f ? w[1] * vo[h] : 0.f);
+            pb[nt][h] = transpose8x8(r);
+          }
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          const uint32_t l01 = __byte_perm(va[0][w], va[1][w], 0x5410), h01 = __byte_perm(va[0][w], va[1][w], 0x7632);
+          const uint32_t l23 = __byte_perm(va[2][w], va[3][w], 0x5410), h23 = __byte_perm(va[2][w], va[3][w], 0x7632);
+          // columns 8 w + 0 .. 7 of the lane's: two to an mma, on its rows g and g + 8
+          using BF = __nv_bfloat16;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816<BF>(acc[nt][4 * w], codes16<BF, 0>(l01), codes16<BF, 1>(l01), codes16<BF, 0>(l23), codes16<BF, 1>(l23),
+                         pb[nt][0], pb[nt][1]);
+            mma16816<BF>(acc[nt][4 * w + 1], codes16<BF, 2>(l01), codes16<BF, 3>(l01), codes16<BF, 2>(l23),
+                         codes16<BF, 3>(l23), pb[nt][0], pb[nt][1]);
+            mma16816<BF>(acc[nt][4 * w + 2], codes16<BF, 0>(h01), codes16<BF, 1>(h01), codes16<BF, 0>(h23),
+                         codes16<BF, 1>(h23), pb[nt][0], pb[nt][1]);
+            mma16816<BF>(acc[nt][4 * w + 3], codes16<BF, 2>(h01), codes16<BF, 3>(h01), codes16<BF, 2>(h23),
+                         codes16<BF, 3>(h23), pb[nt][0], pb[nt][1]);
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      fill();
+    }
+    // ---- the warps' results meet --------------------------------------------------------------------
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float a = l[nt][c], b = corr[nt][c];
+#pragma unroll
+        for (int o = 4; o < 32; o *= 2) {
+          a += __shfl_xor_sync(0xffffffffu, a, o);
+          b += __shfl_xor_sync(0xffffffffu, b, o);
+        }
+        const int row = nt * 8 + 2 * t + c;
+        if (g == 0) {
+          sm.m[warp][row] = m[nt][c];
+          sm.l[warp][row] = a;
+          sm.corr[warp][row] = b;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {  // columns 2i and 2i + 1 of the lane's
+          float2* o = reinterpret_cast<float2*>(&sm.o[warp][row][g * (D / 8) + 2 * i]);
+          *o = make_float2(acc[nt][i][c], acc[nt][i][2 + c]);
+        }
+      }
+    __syncthreads();
+    const bool whole = lo == seg.start && hi == seg.start + seg.len;
+    float* part = p.part + (2ll * blockIdx.x + (lo == u0 ? 0 : 1)) * kRows * (D + 2);
+    for (int e = threadIdx.x; e < kRows * D; e += kWarps * 32) {
+      const int row = e / D, col = e % D, r = seg.rt * kRows + row;
+      if (r >= R) continue;
+      float top = -INFINITY, sum = 0.f, v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm.m[w][row]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = sm.m[w][row];
+        const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - top);
+        sum += mw == -INFINITY ? sm.l[w][row] : sm.l[w][row] * f;  // a warp that saw nothing: 0, or NaN
+        v += (sm.o[w][row][col] + sm.corr[w][row]) * f;
+      }
+      if (whole) {
+        const long long hq = seg.h * p.group + r % p.group, i = r / p.group;
+        static_cast<T*>(p.o)[seg.b * p.so.b + hq * p.so.h + i * p.so.s + col] =
+            from_f32<T>(sum == 0.f ? 0.f : sum != sum ? NAN : v / sum);
+        if (col == 0)
+          p.lse[(seg.b * (long long)p.Hq + hq) * p.S + i] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+      } else {
+        part[row * (D + 2) + col] = v;
+        if (col == 0) {
+          part[row * (D + 2) + D] = top;
+          part[row * (D + 2) + D + 1] = sum;
+        }
+      }
+    }
+    __syncthreads();
+    lo = hi;
+  }
+}
+
+// A query row of a segment that lies in several CTAs, or in none: the pieces' results, eight warps taking every eighth.
+template <class T, int D, int NT>
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnParams p, int ctas) {
+  constexpr int kRows = 8 * NT, E = D / 32;
+  __shared__ float so[8][D], sl[8], st[8];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int R = p.group * p.S;
+  const int row = blockIdx.x % R, h = (int)(blockIdx.x / R) % p.c.Hkv, b = (int)(blockIdx.x / R / p.c.Hkv);
+  const int rt = row / kRows, hq = h * p.group + row % p.group, i = row / p.group;
+  T* o = static_cast<T*>(p.o) + b * p.so.b + hq * p.so.h + i * p.so.s;
+  float* lse = p.lse + ((long long)b * p.Hq + hq) * p.S + i;
+  // every warp walks: where the segment begins, and how many units there are.  No block leaves before the kernel that
+  // writes the pieces has ended: what follows on the stream may rely on both.
+  const int n = p.lens[b], len = blocks_of(p, b);
+  if (len == 0) {
+    wait_previous();
+    const bool empty = n == 0;
+    for (int c = threadIdx.x; c < D; c += 256) o[c] = from_f32<T>(empty ? 0.f : NAN);
+    if (threadIdx.x == 0) *lse = empty ? -INFINITY : NAN;
+    return;
+  }
+  Cursor none = {};
+  const long long total = walk(p, -1, none);
+  long long start = 0;
+  for (int b0 = 0; b0 < b; b0 += 32) {
+    long long v = b0 + lane < b ? (long long)blocks_of(p, b0 + lane) * p.c.Hkv * p.n_rt : 0;
+#pragma unroll
+    for (int s = 16; s; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+    start += v;
+  }
+  start += (long long)(h * p.n_rt + rt) * len;
+  const long long per = share(total, ctas);
+  const int c0 = (int)(start / per), c1 = (int)((start + len - 1) / per);
+  wait_previous();
+  if (c0 == c1) return;
+  float top = -INFINITY, sum = 0.f, acc[E] = {};
+#pragma unroll 4
+  for (int c = c0 + warp; c <= c1; c += 8) {
+    const float* part = p.part + ((2ll * c + (c * per >= start ? 0 : 1)) * kRows + row % kRows) * (D + 2);
+    const float mc = part[D], lc = part[D + 1];
+    float v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = part[lane + 32 * e];
+    const float t = fmaxf(top, mc);
+    const float f = t == -INFINITY ? 1.f : ex2_approx(top - t), w = t == -INFINITY ? 1.f : ex2_approx(mc - t);
+    top = t;
+    sum = sum * f + lc * w;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + v[e] * w;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) so[warp][lane + 32 * e] = acc[e];
+  if (lane == 0) {
+    st[warp] = top;
+    sl[warp] = sum;
   }
   __syncthreads();
-  if (warp) return;
-  const float mm = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  float ll = 0.f, acc[E] = {};
-  for (int w = 0; w < 4; ++w) {
-    const float a = sm[w] == -INFINITY ? 0.f : expf(sm[w] - mm);
-    ll += sm[w] == -INFINITY ? sl[w] : sl[w] * a;
-    for (int e = 0; e < E; ++e) acc[e] += so[w][lane * E + e] * a;
+  if (threadIdx.x >= D) return;
+  top = st[0];
+#pragma unroll
+  for (int w = 1; w < 8; ++w) top = fmaxf(top, st[w]);
+  float v = 0.f;
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const float f = top == -INFINITY ? 1.f : ex2_approx(st[w] - top);
+    sum += sl[w] * f;
+    v += so[w][threadIdx.x] * f;
   }
-  T* out = static_cast<T*>(p.o) + b * p.so.b + hq * p.so.h + i * p.so.s;
-  for (int e = 0; e < E; ++e) out[lane * E + e] = from_f32<T>(ll == 0.f ? 0.f : acc[e] / ll);
-  if (lane == 0) p.lse[row] = ll == 0.f ? -INFINITY : mm + logf(ll);
+  o[threadIdx.x] = from_f32<T>(sum == 0.f ? 0.f : sum != sum ? NAN : v / sum);
+  if (threadIdx.x == 0) *lse = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -250,6 +703,46 @@ static int by_type(const psr_kv4_shape* sh, Go&& go) {
     return sh->d == 64 ? go(__nv_bfloat16(), std::integral_constant<int, 64>())
                        : go(__nv_bfloat16(), std::integral_constant<int, 128>());
   return sh->d == 64 ? go(__half(), std::integral_constant<int, 64>()) : go(__half(), std::integral_constant<int, 128>());
+}
+
+// Query rows of a tile: 8, or 16 where that halves the reads of the cache.
+static int tile_rows(const psr_kv4_shape* sh) { return (long long)sh->Hq / sh->Hkv * sh->S > 8 ? 16 : 8; }
+
+template <class T, int D, int NT>
+static int launch_attn(AttnParams& p, int dev, int n_sm, cudaStream_t st) {
+  static std::mutex mu;
+  static bool known[64] = {};
+  constexpr int smem = (int)sizeof(AttnSmem<D, NT>);
+  static_assert(NT == 2 ? smem <= 232448 : 2 * (smem + 1024) <= 233472, "shared memory");
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (dev < 0 || dev >= 64 || !known[dev]) {
+      if (cudaFuncSetAttribute(attn_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+        cudaGetLastError();
+        return PSR_ERR_CUDA;
+      }
+      if (dev >= 0 && dev < 64) known[dev] = true;
+    }
+  }
+  const long long R = (long long)p.group * p.S;
+  p.n_rt = (int)((R + 8 * NT - 1) / (8 * NT));
+  const int ctas = (n_sm < 152 ? n_sm : 152) * (NT == 1 ? 2 : 1);
+  attn_kernel<T, D, NT><<<ctas, kWarps * 32, smem, st>>>(p);
+  if (launch_status() != PSR_OK) return PSR_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.B * p.c.Hkv * R));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, combine_kernel<T, D, NT>, p, ctas) != cudaSuccess) {
+    cudaGetLastError();
+    return PSR_ERR_CUDA;
+  }
+  return PSR_OK;
 }
 
 static unsigned row_blocks(const psr_kv4_shape* sh, int n_sm) {
@@ -309,7 +802,7 @@ int psr_kv4_read(const psr_kv4_shape* sh, const void* cache, const int32_t* tabl
 
 size_t psr_kv4_attn_workspace_bytes(const psr_kv4_shape* sh) {
   if (check_shape(sh) != PSR_OK) return 0;
-  return 256;
+  return 256 + (size_t)2 * kMaxCtas * tile_rows(sh) * (sh->d + 2) * 4;
 }
 
 int psr_kv4_attn(const psr_kv4_shape* sh, const void* q, const psr_strides* qs, const void* cache, const int32_t* table,
@@ -324,15 +817,27 @@ int psr_kv4_attn(const psr_kv4_shape* sh, const void* q, const psr_strides* qs, 
   if (ws_bytes < psr_kv4_attn_workspace_bytes(sh)) return PSR_ERR_ARG;
   const long long rows = (long long)sh->B * sh->Hq * sh->S;
   if (rows >= (1LL << 31)) return PSR_ERR_UNSUPPORTED;
-  if ((rc = check_device(nullptr)) != PSR_OK) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, 256, st) != cudaSuccess) return PSR_ERR_CUDA;
+  int n_sm = 0, dev = 0;
+  if ((rc = check_device(&n_sm)) != PSR_OK) return rc;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PSR_ERR_CUDA;
   if (rows == 0) return PSR_OK;
-  AttnParams p = {cache_of(sh, cache, table), q, o, lse, lens, *qs, *os, sh->B, sh->Hq, sh->S,
-                  sh->scale > 0.f ? sh->scale : 1.f / sqrtf((float)sh->d)};
+  AttnParams p = {};
+  p.c = cache_of(sh, cache, table);
+  p.q = q; p.o = o; p.lse = lse; p.lens = lens;
+  p.sq = *qs; p.so = *os;
+  p.B = sh->B; p.Hq = sh->Hq; p.S = sh->S;
+  p.group = sh->Hq / sh->Hkv;
+  for (int n = sh->page / kBlk; n > 1; n /= 2) ++p.page_shift;
+  auto even = [](long long stride, int n) { return n <= 1 || stride % 8 == 0; };
+  p.vec = aligned_to(q, 16) && even(qs->b, sh->B) && even(qs->h, sh->Hq) && even(qs->s, sh->S);
+  p.scale = sh->scale > 0.f ? sh->scale : 1.f / sqrtf((float)sh->d);
+  p.ctrl = static_cast<Ctrl*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
+  p.timeout_ns = (unsigned long long)(timeout_ms > 0 ? timeout_ms : 2000) * 1000000ull;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   return by_type(sh, [&](auto t, auto d) {
-    attn_kernel<decltype(t), decltype(d)::value><<<(unsigned)rows, 128, 0, st>>>(p);
-    return launch_status();
+    return tile_rows(sh) == 8 ? launch_attn<decltype(t), decltype(d)::value, 1>(p, dev, n_sm, st)
+                              : launch_attn<decltype(t), decltype(d)::value, 2>(p, dev, n_sm, st);
   });
 }
 

@@ -25,38 +25,6 @@ namespace linear {
 constexpr int kBK = 64;  // K per stage: one 128-byte swizzle atom of 16-bit elements
 enum : uint32_t { SITE_FULL = 41, SITE_EMPTY = 42, SITE_ACC = 43, SITE_ACC_EMPTY = 44, SITE_LAUNCH = 45 };
 
-// Bounded wait on a barrier: false after the timeout, or once another wait of the CTA has given up.  The control block's
-// abort word is not consulted: it is cleared by the launch itself (clear_ctrl), while other CTAs already run.
-template <bool CL = false, class KP, class SC>
-__device__ __forceinline__ bool wait_own(uint64_t* bar, uint32_t parity, const KP& p, SC* sc, uint32_t site) {
-  auto poll = [&]() { return CL ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
-  if (poll()) return true;
-  const uint64_t t0 = globaltimer_ns();
-  uint32_t it = 0;
-  while (true) {
-    if (poll()) return true;
-    if ((++it & 15u) == 0) {
-      if (sc->abort) return false;
-      if (globaltimer_ns() - t0 > p.timeout_ns) {
-        raise_error(p, site);
-        sc->abort = 1;
-        return false;
-      }
-    }
-  }
-}
-
-// The first kernel of a call clears the control block (a memset before it would cost a launch).  A wait of the same call
-// can give up only a timeout later.
-__device__ __forceinline__ void clear_ctrl(Ctrl* ctrl) {
-  if (ctrl && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < sizeof(Ctrl) / 4)
-    reinterpret_cast<uint32_t*>(ctrl)[threadIdx.x] = 0;
-}
-
-// Programmatic launches: let the next kernel's launch begin / wait for the whole previous kernel and its writes.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // What becomes of an fp32 sum: z = sum + bias, y = act(z) + residual.
 struct Epilogue {
   const void* bias;
@@ -767,10 +735,9 @@ __global__ void __launch_bounds__(128) stream_join(const __grid_constant__ Strea
   const int tile = blockIdx.x;
   const long long b = (long long)tile * p.n_k, e = b + p.n_k;
   const int c0 = (int)(b / p.per_cta), c1 = (int)((e - 1) / p.per_cta);
-  if (c0 == c1) return;
   const int j = tile / p.n_tb * kRows + threadIdx.x, c = blockIdx.y, i = tile % p.n_tb * p.tb + c;
-  if (i >= p.M) return;
-  wait_previous();
+  wait_previous();  // before any exit: what follows on the stream may rely on the products' kernel too
+  if (c0 == c1 || i >= p.M) return;
   float sum = 0.f;
 #pragma unroll 4
   for (int g = c0; g <= c1; ++g) {
@@ -784,11 +751,10 @@ __global__ void __launch_bounds__(128) stream_join(const __grid_constant__ Strea
 __global__ void __launch_bounds__(256) pair_join(const __grid_constant__ PairParams p) {
   const long long per = p.ldp / 4, n = per * p.M;
   const long long t = blockIdx.x * 256ll + threadIdx.x;
-  if (t >= n) return;
   const long long i = t / per;
   const int j = (int)(t - i * per) * 4;
-  if (j >= p.N) return;
   wait_previous();
+  if (t >= n || j >= p.N) return;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int s = 0; s < p.splits; ++s) {
@@ -880,25 +846,6 @@ inline int pairs_of(int dev, int n_sm) {
   if (n > n_sm / 2) n = n_sm / 2;
   if (dev >= 0 && dev < 64) known[dev] = n;
   return n;
-}
-
-// Launch a kernel whose launch may begin while the previous one ends (it calls wait_previous before it reads).
-template <class Kern, class P>
-inline int launch_after(Kern kern, dim3 grid, int threads, const P& p, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
-    cudaGetLastError();
-    return PSR_ERR_CUDA;
-  }
-  return PSR_OK;
 }
 
 // Where a call's kernels run and what they share.

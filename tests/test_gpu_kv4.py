@@ -163,7 +163,9 @@ def test_attention_of_query_views(psr):
 
 
 def test_attention_of_bad_lengths_and_pages(psr):
-    # a length below 0 or past the table, or a page that the cache does not have: NaN, the others as without it
+    # a length below 0 or past the table, or a page that the cache does not have: NaN; the others are not touched by it.
+    # Where a sequence is cut into pieces depends on the whole batch's lengths, and with it the order of the fp32 sums:
+    # the good sequence is held to the oracle's bound, not to the bits that it has in another batch.
     need_gpu()
     rng = np.random.default_rng(1)
     g = torch.Generator().manual_seed(1)
@@ -177,7 +179,7 @@ def test_attention_of_bad_lengths_and_pages(psr):
         o, lse, _ = psr.kv4_attn(q, cache, torch.from_numpy(table).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"),
                                  Hkv=Hkv, page=page)
         return o, lse
-    good = run(table, lens)
+    run(table, lens)
     table2, lens2 = table.copy(), list(lens)
     lens2[0], lens2[1] = -1, 49
     table2[2, 0], table2[3, 2], lens2[3] = n_pages, -7, 33
@@ -187,7 +189,9 @@ def test_attention_of_bad_lengths_and_pages(psr):
     for b in range(4):
         assert torch.isnan(o[b]).all() and torch.isnan(lse[b]).all(), b
     assert not o[4].any() and torch.isneginf(lse[4]).all()
-    assert torch.equal(o[5], good[0][5]) and torch.equal(lse[5], good[1][5])
+    ro, rl, to, tl = ol.kv4_attention(f64(q[5:]), cache.cpu().numpy(), table[5:], [40], page, Hkv, 1 / math.sqrt(d))
+    check(lse[5:], rl, tl, "lse beside bad sequences")
+    check(o[5:], ro, to + 2.0**-8 * np.abs(ro) * 1.01, "o beside bad sequences")
     table3 = table.copy()
     table3[:, 2] = 1 << 30  # behind 32 positions the table is not looked at
     o, lse = run(table3, [32] * B)
