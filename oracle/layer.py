@@ -154,11 +154,12 @@ def kv4_attention(q, cache, table, lens, page, Hkv, scale):
     """q [B, Hq, S, d] -> (o, lse, tol_o, tol_lse): the tolerances are bounds on what the arithmetic of the
     kernel may be off by before the final rounding of o.
 
-    Scores: q.c is summed in fp32 from products of q and c + 16 (exact), at most d roundings (or truncations, 2^-23)
-    of sum |q| (c + 16) and of sum |q|, so score j is off by at most
-        e_j = scale * d * 2^-23 * (s_j sum |q| 31 + (|o_j| + 24 s_j) sum |q|) + 2^-21 |x_j|,
+    Scores: q.c is summed in fp32 from exact products, at most d roundings (or truncations, 2^-23) of sum |q| c (c <= 15)
+    and of sum |q|; so score j is off by at most
+        e_j = scale * d * 2^-23 * sum |q| (15 s_j + |o_j|) + 2^-21 |x_j|,
     LSE by max e + 2^-20 (1 + |LSE|), each weight by the fraction 2 max e + 2^-20.  Output: the weight times s_j is rounded
-    to bf16 (2^-8) and multiplies c - 8; the sums in fp32 add n 2^-23 of their terms' sizes."""
+    to fp16 (2^-11; 2^-25 of the largest such product where it is subnormal) and multiplies c; the sums in fp32 add
+    n 2^-23 of their terms' sizes."""
     B, Hq, S, d = q.shape
     o = np.zeros((B, Hq, S, d))
     lse = np.full((B, Hq, S), -np.inf)
@@ -183,10 +184,10 @@ def kv4_attention(q, cache, table, lens, page, Hkv, scale):
                     w = w / w.sum()
                     o[b, hq, i] = w @ v[:m]
                     size = np.abs(q[b, hq, i]).sum()
-                    e = scale * d * 2.0**-23 * size * (55 * np.abs(ks[:m]) + np.abs(ko[:m])) + 2.0**-21 * np.abs(x)
+                    e = scale * d * 2.0**-23 * size * (15 * np.abs(ks[:m]) + np.abs(ko[:m])) + 2.0**-21 * np.abs(x)
                     e = float(e.max())
                     tol_lse[b, hq, i] = e + 2.0**-20 * (1 + abs(lse[b, hq, i]))
-                    off8 = np.abs(vc[:m] - 8) * vs[:m, None]
-                    tol_o[b, hq, i] = (2.0**-8 * (w @ off8) + (2 * e + 2.0**-20) * (w @ np.abs(v[:m]) + np.abs(o[b, hq, i]))
-                                       + (m + 32) * 2.0**-23 * (w @ (55 * vs[:m] + np.abs(vo[:m]))))
+                    tol_o[b, hq, i] = (2.0**-11 * (w @ (vc[:m] * vs[:m, None])) + m * 15 * 2.0**-25 * (w * vs[:m]).max()
+                                       + (2 * e + 2.0**-20) * (w @ np.abs(v[:m]) + np.abs(o[b, hq, i]))
+                                       + (m + 32) * 2.0**-23 * (w @ (15 * vs[:m] + np.abs(vo[:m]))))
     return o, lse, tol_o, tol_lse

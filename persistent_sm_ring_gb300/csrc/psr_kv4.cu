@@ -154,27 +154,36 @@ __global__ void read_kernel(const ReadParams p) {
 // ------------------------------------------------------------------------------------------------
 // Attention
 // ------------------------------------------------------------------------------------------------
-// Bound by reading the cache once.  A unit is one block of 16 tokens for one KV head and a tile of up to 8 NT query rows
+// Bound by reading the cache once.  A unit is two blocks (32 tokens) of one KV head and a tile of up to 8 NT query rows
 // (the group's heads times the new tokens); the units of all sequences stand in a line, segment by segment (a segment:
 // sequence, head, row tile), and each CTA takes an equal stretch of it, so ragged batches and single long sequences load
 // every SM alike.  A segment that lies within one CTA is finished there; the pieces of one that does not meet in
 // combine_kernel through fp32 partial results and their running maxima and sums, as the ring's chunks do.
 //
-// Each warp has its own ring of stages, filled with one bulk copy per block, and its own softmax state:
+// Each of seven warps has its own ring of stages, which an eighth one fills with bulk copies, and its own softmax state:
 //   S^T[token][row] = K codes . q      (mma.m16n8k16: tokens on its 16 rows, query rows on its 8 columns)
 //   O^T[column][row] += V codes^T . P  (columns of V on the 16 rows, tokens in the contraction)
-// The codes become 16-bit floats 16 + c with one shift and one three-input logic operation for two of them (the code goes
-// to the top bits of the mantissa of 16); scale and offset are applied to the sums, and 16 times the sum of the other factor
-// is taken off there.  Any order of the contraction will do, so K and V fragments are read straight from the stage:
-// a lane takes 16 adjacent bytes of a K row, and the tokens are dealt to the mma's rows so that V's loads fall on
-// different banks.  P leaves the first product in the layout that movmatrix turns into the second one's operand.
-// The maximum is only raised when a score passes it by kRaise: the check is one vote, the weights stay below 2^kRaise.
-constexpr int kWarps = 8;
-constexpr int kStages = 4;
-constexpr int kMaxCtas = 2 * 152;  // bounds the partial results
+// The issue slots are what is scarce (a first version that made 16-bit floats 16 + c of the codes took 485 instructions for
+// 16 tokens of d = 128 and ran at 3.2 TB/s).  So:
+//  * a code needs no conversion: its four bits, masked in place, are a subnormal fp16 number, c 2^-24 in bits 0..3 and
+//    16 c 2^-24 in bits 4..7, exact, and the matrix product takes it so.  One shift and four masks give eight codes.
+//  * q becomes fp16 for it, scaled by a power of two that puts the tile's largest element below 2^15 (exact for bf16
+//    down to 2^-25 of that); the scales 2^24, 1/16 and that power go to the sums.
+//  * P becomes fp16 times its row's scale: the exponent x + log2(scale) has a running maximum of its own (m + d), so that
+//    no ratio of the scales of different tokens costs P its digits.  Exponents are kept relative to m, where large scores
+//    leave them exact.
+//  * any order of the contraction will do, so K and V fragments are read straight from the stage: a lane takes 16 adjacent
+//    bytes of a K row, and the tokens are dealt to the mma's rows so that V's loads fall on different banks; P leaves the
+//    first product in the layout that movmatrix turns into the second one's operand.
+//  * a maximum is only raised when a score passes it by kRaise: the check is one vote, the weights stay below 2^kRaise.
+constexpr int kWarps = 7;           // and one that fills their stages
+constexpr int kStages = 2;
+constexpr int kUnit = 2 * kBlk;     // tokens of a unit
+constexpr int kMaxCtas = 2 * 152;   // bounds the partial results
 constexpr float kRaise = 8.f;
-constexpr float kLog2e = 1.4426950408889634f;
-enum : uint32_t { SITE_BLOCK = 51 };
+constexpr float kLowest = -1e30f;   // a maximum that nothing has raised
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+enum : uint32_t { SITE_BLOCK = 51, SITE_STAGE = 52 };
 
 struct AttnParams {
   Cache c;
@@ -192,10 +201,10 @@ struct AttnParams {
   unsigned long long timeout_ns;
 };
 
-// Blocks of sequence b: 0 if it is empty or its length is out of range.
-__device__ __forceinline__ int blocks_of(const AttnParams& p, int b) {
+// Units of sequence b: 0 if it is empty or its length is out of range.
+__device__ __forceinline__ int units_of(const AttnParams& p, int b) {
   const int n = p.lens[b];
-  return n < 0 || n > (long long)p.c.max_pages * p.c.page ? 0 : (n + kBlk - 1) / kBlk;
+  return n < 0 || n > (long long)p.c.max_pages * p.c.page ? 0 : (n + kUnit - 1) / kUnit;
 }
 
 // A place in the line of units.
@@ -209,21 +218,31 @@ struct Cursor {
         rt = 0;
         if (++h == p.c.Hkv) {
           h = 0;
-          len = blocks_of(p, ++b);
+          len = units_of(p, ++b);
         }
       }
     }
   }
 };
 
-// One warp: units before sequence b for every b in turn, 32 at a time.  Returns their total; with target >= 0 the cursor of
-// the segment that holds that unit (target < total).
-__device__ __forceinline__ long long walk(const AttnParams& p, long long target, Cursor& cur) {
+// One warp: the units of the sequences before `end`.
+__device__ __forceinline__ long long units_before(const AttnParams& p, int end) {
+  const int lane = threadIdx.x % 32;
+  long long sum = 0;
+  for (int b = lane; b < end; b += 32) sum += units_of(p, b);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum * p.c.Hkv * p.n_rt;
+}
+
+// One warp: the segment that holds a unit (of those there are).
+__device__ __forceinline__ Cursor segment_at(const AttnParams& p, long long target) {
   const int lane = threadIdx.x % 32;
   const int per = p.c.Hkv * p.n_rt;
+  Cursor cur = {};
   long long base = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int n = b0 + lane < p.B ? blocks_of(p, b0 + lane) : 0;
+    const int n = b0 + lane < p.B ? units_of(p, b0 + lane) : 0;
     const long long own = (long long)n * per;
     long long sum = own;
 #pragma unroll
@@ -232,7 +251,7 @@ __device__ __forceinline__ long long walk(const AttnParams& p, long long target,
       if (lane >= o) sum += v;
     }
     const long long all = __shfl_sync(0xffffffffu, sum, 31);
-    if (target >= 0 && target < base + all) {
+    if (target < base + all) {
       const int at = __ffs(__ballot_sync(0xffffffffu, target < base + sum)) - 1;
       const int len = __shfl_sync(0xffffffffu, n, at);
       const long long first = base + __shfl_sync(0xffffffffu, sum - own, at);
@@ -242,63 +261,100 @@ __device__ __forceinline__ long long walk(const AttnParams& p, long long target,
       cur.rt = seg % p.n_rt;
       cur.len = len;
       cur.start = first + (long long)seg * len;
-      return base;
+      break;
     }
     base += all;
   }
-  return base;
+  return cur;
 }
 
-// Units of a CTA: an equal share, at least one block a warp.
+// Units of a CTA: an equal share, at least one a warp.
 __device__ __forceinline__ long long share(long long total, int ctas) {
   const long long per = (total + ctas - 1) / ctas;
   return per < kWarps ? kWarps : per;
 }
 
-template <class T>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  if constexpr (std::is_same<T, __half>::value)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-
-// Nibbles P and P + 4 of w as the 16-bit floats 16 + c.
-template <class T, int P>
-__device__ __forceinline__ uint32_t codes16(uint32_t w) {
-  if constexpr (std::is_same<T, __half>::value) {  // 16 = 0x4C00, the code in mantissa bits 6..9
-    const uint32_t s = P == 0 ? w << 6 : P == 1 ? w << 2 : P == 2 ? w >> 2 : w >> 6;
-    return (s & 0x03C003C0u) | 0x4C004C00u;
-  } else {  // 16 = 0x4180, mantissa bits 3..6
-    const uint32_t s = P == 0 ? w << 3 : P == 1 ? w >> 1 : P == 2 ? w >> 5 : w >> 9;
-    return (s & 0x00780078u) | 0x41804180u;
-  }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lo_bf16(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+__device__ __forceinline__ void sync_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
 
 template <int D, int NT>
 struct AttnSmem {
   static constexpr int kRows = 8 * NT;
   static constexpr int kBytes = kBlk * (D + 8);
-  alignas(128) uint8_t ring[kWarps][kStages][kBytes];
+  alignas(128) uint8_t ring[kWarps][kStages][2 * kBytes];
   alignas(16) float o[kWarps][kRows][D];  // a segment's results, by warp
-  float m[kWarps][kRows], l[kWarps][kRows], corr[kWarps][kRows];
-  uint64_t full[kWarps][kStages];
-  uint32_t bad[kWarps][kStages];  // the stage's block has no page
+  float m[kWarps][kRows], d[kWarps][kRows], l[kWarps][kRows], corr[kWarps][kRows];
+  uint64_t full[kWarps][kStages], empty[kWarps][kStages];
+  uint32_t bad[kWarps][kStages];  // a block of the stage has no page
+  long long total, u0;
+  Cursor first;
   volatile uint32_t abort;
 };
 
+// Lane w < 7 of the last warp: the units u0 + w + 7 k of the CTA into warp w's stages.
+template <int D, int NT>
+__device__ __forceinline__ void fill_rings(const AttnParams& p, AttnSmem<D, NT>& sm, int w, long long u0, long long u1) {
+  constexpr int kBytes = AttnSmem<D, NT>::kBytes;
+  Cursor cur = sm.first;
+  uint32_t k = 0;
+  for (long long u = u0 + w; u < u1; u += kWarps, ++k) {
+    cur.advance(p, u);
+    const int blk = 2 * (int)(u - cur.start);
+    const bool two = blk + 1 < (p.lens[cur.b] + kBlk - 1) / kBlk;
+    const int32_t* row = p.c.table + (long long)cur.b * p.c.max_pages;
+    const int in_page = (1 << p.page_shift) - 1;
+    const int pg0 = row[blk >> p.page_shift];
+    const int pg1 = two && p.page_shift == 0 ? row[blk + 1] : pg0;
+    const uint32_t s = k % kStages;
+    if (k >= kStages && !wait_own(&sm.empty[w][s], (k / kStages - 1) & 1u, p, &sm, SITE_STAGE)) break;
+    const bool ok = pg0 >= 0 && pg0 < p.c.n_pages && pg1 >= 0 && pg1 < p.c.n_pages;
+    sm.bad[w][s] = !ok;
+    if (!ok) {
+      mbar_arrive(&sm.full[w][s]);
+      continue;
+    }
+    auto block = [&](int pg, int b) {
+      return p.c.base + ((((long long)pg * p.c.Hkv + cur.h) << p.page_shift) + (b & in_page)) * kBytes;
+    };
+    const uint32_t dst = smem_u32(sm.ring[w][s]);
+    mbar_expect_tx(&sm.full[w][s], two ? 2 * kBytes : kBytes);
+    bulk_load(dst, block(pg0, blk), two && p.page_shift > 0 ? 2 * kBytes : kBytes, &sm.full[w][s]);
+    if (two && p.page_shift == 0) bulk_load(dst + kBytes, block(pg1, blk + 1), kBytes, &sm.full[w][s]);
+  }
+  if (sm.abort) {  // nothing of this CTA's is in flight when it leaves
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t s = 0; s < kStages && s < k; ++s) {
+      const uint32_t m = s + (k - 1 - s) / kStages * kStages;
+      while (!mbar_try_wait(&sm.full[w][s], (m / kStages) & 1u) && globaltimer_ns() - t0 < 100000000ull) {
+      }
+    }
+  }
+}
+
 template <class T, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__((kWarps + 1) * 32, NT == 1 ? 2 : 1) attn_kernel(const __grid_constant__ AttnParams p) {
   using Sm = AttnSmem<D, NT>;
   constexpr int kRows = Sm::kRows, kBytes = Sm::kBytes;
   constexpr int KW = D / 32;  // words of K codes a lane takes of a row
@@ -308,52 +364,36 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
   clear_ctrl(p.ctrl);
   launch_dependents();
-  if (threadIdx.x == 0) sm.abort = 0;
-  if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[warp][s], 1);
+  if (warp == 0) {
+    const long long total = units_before(p, p.B);
+    const long long u0 = blockIdx.x * share(total, gridDim.x);
+    if (u0 < total) {
+      const Cursor c = segment_at(p, u0);
+      if (lane == 0) sm.first = c;
+    }
+    if (lane == 0) {
+      sm.total = total;
+      sm.u0 = u0;
+    }
+  } else if (warp == kWarps && lane < kWarps) {
+    if (lane == 0) sm.abort = 0;
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm.full[lane][s], 1);
+      mbar_init(&sm.empty[lane][s], 1);
+    }
     fence_barrier_init();
   }
-  Cursor seg = {};
-  const long long total = walk(p, -1, seg);
-  const long long per = share(total, gridDim.x);
-  const long long u0 = blockIdx.x * per, u1 = u0 + per < total ? u0 + per : total;
-  if (u0 >= u1) return;
-  walk(p, u0, seg);
   __syncthreads();
+  const long long total = sm.total, u0 = sm.u0;
+  const long long end = u0 + share(total, gridDim.x), u1 = end < total ? end : total;
+  if (u0 >= u1) return;
+  if (warp == kWarps) {
+    if (lane < kWarps) fill_rings<D, NT>(p, sm, lane, u0, u1);
+    return;
+  }
 
-  // ---- the warp's ring: unit u0 + warp + 8 k goes to stage k % kStages -------------------------
-  Cursor pre = seg;
-  long long up = u0 + warp;
-  uint32_t filled = 0, used = 0;
-  int page_id = -1;
-  auto look_up = [&]() {  // the next unit's page, read a step ahead of its copy
-    if (up < u1) {
-      pre.advance(p, up);
-      page_id = p.c.table[(long long)pre.b * p.c.max_pages + ((int)(up - pre.start) >> p.page_shift)];
-    }
-  };
-  auto fill = [&]() {
-    if (up >= u1) return;
-    if (lane == 0) {
-      const uint32_t s = filled % kStages;
-      const bool ok = page_id >= 0 && page_id < p.c.n_pages;
-      sm.bad[warp][s] = !ok;
-      if (ok) {
-        const int blk = (int)(up - pre.start), per_page = 1 << p.page_shift;
-        const uint8_t* src = p.c.base + (((long long)page_id * p.c.Hkv + pre.h) * per_page + (blk & (per_page - 1))) * kBytes;
-        mbar_expect_tx(&sm.full[warp][s], kBytes);
-        bulk_load(smem_u32(sm.ring[warp][s]), src, kBytes, &sm.full[warp][s]);
-      } else {
-        mbar_arrive(&sm.full[warp][s]);
-      }
-    }
-    ++filled;
-    up += kWarps;
-    look_up();
-  };
-  look_up();
-  for (int s = 0; s < kStages; ++s) fill();
-
+  Cursor seg = sm.first;
+  uint32_t used = 0;
   for (long long lo = u0; lo < u1;) {
     seg.advance(p, lo);
     const long long hi = seg.start + seg.len < u1 ? seg.start + seg.len : u1;
@@ -363,100 +403,189 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
     uint32_t qf[NT][KW][4];
     float qsum[NT][2];   // of rows 2t and 2t + 1
     int last[NT][2];     // last position that they see
+    float big = 0.f;
+    uint4 raw[NT][KW];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int row = seg.rt * kRows + nt * 8 + g;
-      float sum = 0.f;
-      if (row < R) {
-        const T* q = static_cast<const T*>(p.q) + (long long)seg.b * p.sq.b +
-                     (long long)(seg.h * p.group + row % p.group) * p.sq.h + (long long)(row / p.group) * p.sq.s + t * (D / 4);
+      const T* q = static_cast<const T*>(p.q) + (long long)seg.b * p.sq.b +
+                   (long long)(seg.h * p.group + row % p.group) * p.sq.h + (long long)(row / p.group) * p.sq.s + t * (D / 4);
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          uint4 v;
+      for (int w = 0; w < KW; ++w) {
+        raw[nt][w] = make_uint4(0, 0, 0, 0);
+        if (row < R) {
           if (p.vec) {
-            v = *reinterpret_cast<const uint4*>(q + w * 8);
+            raw[nt][w] = *reinterpret_cast<const uint4*>(q + w * 8);
           } else {
-            uint32_t e[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              e[i] = reinterpret_cast<const uint16_t*>(q)[w * 8 + 2 * i] |
-                     (uint32_t)reinterpret_cast<const uint16_t*>(q)[w * 8 + 2 * i + 1] << 16;
-            v = make_uint4(e[0], e[1], e[2], e[3]);
-          }
-          qf[nt][w][0] = __byte_perm(v.x, v.z, 0x5410);  // columns (0, 4), (1, 5), (2, 6), (3, 7)
-          qf[nt][w][1] = __byte_perm(v.x, v.z, 0x7632);
-          qf[nt][w][2] = __byte_perm(v.y, v.w, 0x5410);
-          qf[nt][w][3] = __byte_perm(v.y, v.w, 0x7632);
-          const uint32_t e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint16_t lo16 = (uint16_t)e[i], hi16 = (uint16_t)(e[i] >> 16);
-            sum += to_f32(*reinterpret_cast<T*>(&lo16)) + to_f32(*reinterpret_cast<T*>(&hi16));
+            const uint16_t* e = reinterpret_cast<const uint16_t*>(q) + w * 8;
+            raw[nt][w] = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16,
+                                    e[6] | (uint32_t)e[7] << 16);
           }
         }
-      } else {
+      }
+    }
+    auto element = [](const uint4& v, int i) {
+      const uint32_t e = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+      uint16_t h = (uint16_t)(i % 2 ? e >> 16 : e);
+      return to_f32(*reinterpret_cast<T*>(&h));
+    };
 #pragma unroll
-        for (int w = 0; w < KW; ++w) qf[nt][w][0] = qf[nt][w][1] = qf[nt][w][2] = qf[nt][w][3] = 0;
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int w = 0; w < KW; ++w)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(element(raw[nt][w], i)));
+    big = warp_max(big);
+    // 2^(14 - exponent of the largest); 1 if it is zero, subnormal or not finite
+    const int ex = (int)(__float_as_uint(big) >> 23);
+    const float up = ex == 0 || ex == 255 ? 1.f : __uint_as_float((uint32_t)min(254, max(1, 127 + 14 - (ex - 127))) << 23);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          f[i] = element(raw[nt][w], i);
+          sum += f[i];
+          f[i] *= i % 2 ? up * 0.0625f : up;  // the codes of odd columns stand 16 times too high
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qf[nt][w][i] = pack_f16x2(f[i], f[i + 4]);
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        qsum[nt][c] = __shfl_sync(0xffffffffu, sum, (2 * t + c) * 4);
+        qsum[nt][c] = __shfl_sync(0xffffffffu, sum, (2 * t + c) * 4) * (p.scale * kLog2e);
         last[nt][c] = n - p.S + (seg.rt * kRows + nt * 8 + 2 * t + c) / p.group;
       }
     }
-    const float s2 = p.scale * kLog2e;
-    float acc[NT][D / 16][4], m[NT][2], l[NT][2], corr[NT][2];
+    const float kscale = p.scale * kLog2e * 16777216.f / up;
+    float acc[NT][D / 16][4], m[NT][2], d[NT][2], l[NT][2], corr[NT][2];
+    bool fresh = true;  // no unit yet: the first one sets the maxima (a row that sees nothing of it sees nothing later)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = d[nt][0] = d[nt][1] = 0.f;
       l[nt][0] = l[nt][1] = corr[nt][0] = corr[nt][1] = 0.f;
     }
-    // ---- this warp's blocks of the segment -------------------------------------------------------
-    long long u = lo + (warp + kWarps - (int)((lo - u0) % kWarps)) % kWarps;
-    for (; u < hi; u += kWarps) {
-      const uint32_t s = used % kStages;
-      const bool in = wait_own(&sm.full[warp][s], (used / kStages) & 1u, p, &sm, SITE_BLOCK);
-      ++used;
-      if (!__all_sync(0xffffffffu, in) || sm.bad[warp][s]) {
-        l[0][0] = l[0][1] = NAN;
-        if (NT == 2) l[NT - 1][0] = l[NT - 1][1] = NAN;
-      } else {
-        const uint8_t* blk = sm.ring[warp][s];
-        // mma row g holds token g / 2 + 4 (g % 2) of the block, row g + 8 that plus 8
-        const int tok = g / 2 + 4 * (g % 2);
-        const int j0 = (int)(u - seg.start) * kBlk + tok;
+    // one unit: MASKED where some row does not see all of its tokens
+    auto unit = [&](const uint8_t* stage, int j0, auto masked_tag) {
+      constexpr bool MASKED = decltype(masked_tag)::value;
+      // mma row g holds token g / 2 + 4 (g % 2) of a block, row g + 8 that plus 8
+      const int tok = g / 2 + 4 * (g % 2);
+      float x[NT][8];  // block, token half, row
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[nt][e] = 0.f;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint8_t* blk = stage + b * kBytes;
         uint32_t ka[KW], kb[KW];
         if constexpr (D == 128) {
           const uint4 a = *reinterpret_cast<const uint4*>(blk + tok * 64 + t * 16);
-          const uint4 b = *reinterpret_cast<const uint4*>(blk + (tok + 8) * 64 + t * 16);
+          const uint4 c = *reinterpret_cast<const uint4*>(blk + (tok + 8) * 64 + t * 16);
           ka[0] = a.x; ka[1] = a.y; ka[2] = a.z; ka[3] = a.w;
-          kb[0] = b.x; kb[1] = b.y; kb[2] = b.z; kb[3] = b.w;
+          kb[0] = c.x; kb[1] = c.y; kb[2] = c.z; kb[3] = c.w;
         } else {
           const uint2 a = *reinterpret_cast<const uint2*>(blk + tok * 32 + t * 8);
-          const uint2 b = *reinterpret_cast<const uint2*>(blk + (tok + 8) * 32 + t * 8);
+          const uint2 c = *reinterpret_cast<const uint2*>(blk + (tok + 8) * 32 + t * 8);
           ka[0] = a.x; ka[1] = a.y;
-          kb[0] = b.x; kb[1] = b.y;
+          kb[0] = c.x; kb[1] = c.y;
         }
-        float x[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
-          const uint32_t a0 = codes16<T, 0>(ka[w]), a1 = codes16<T, 0>(kb[w]);
-          const uint32_t a2 = codes16<T, 1>(ka[w]), a3 = codes16<T, 1>(kb[w]);
-          const uint32_t a4 = codes16<T, 2>(ka[w]), a5 = codes16<T, 2>(kb[w]);
-          const uint32_t a6 = codes16<T, 3>(ka[w]), a7 = codes16<T, 3>(kb[w]);
+          const uint32_t a8 = ka[w] >> 8, b8 = kb[w] >> 8;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma16816<T>(x[nt], a0, a1, a2, a3, qf[nt][w][0], qf[nt][w][1]);
-            mma16816<T>(x[nt], a4, a5, a6, a7, qf[nt][w][2], qf[nt][w][3]);
+            float(&c)[4] = *reinterpret_cast<float(*)[4]>(&x[nt][4 * b]);
+            mma_f16(c, ka[w] & 0x000F000Fu, kb[w] & 0x000F000Fu, ka[w] & 0x00F000F0u, kb[w] & 0x00F000F0u, qf[nt][w][0],
+                    qf[nt][w][1]);
+            mma_f16(c, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u, qf[nt][w][2], qf[nt][w][3]);
           }
         }
-        // V's codes: tokens t, t + 4 (contraction 2t, 2t + 1) and t + 8, t + 12, this lane's D / 8 columns from g D / 8 on
+      }
+      // x: scores in powers of two above m; y: with V's scale, above m + d
+      float y[NT][8], vo[4], tx[NT][2], ty[NT][2];
+      auto pair_of = [&](int b, int h, int kv) {
+        return reinterpret_cast<const uint32_t*>(stage + b * kBytes + kBlk * D)[kv * 16 + tok + 8 * h];
+      };
+      bool raise = fresh;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t kp = pair_of(b, h, 0), vp = pair_of(b, h, 1);
+          const float ks = lo_bf16(kp) * kscale, ko = hi_bf16(kp), lv = lg2_approx(lo_bf16(vp));
+          vo[2 * b + h] = hi_bf16(vp);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int e = 4 * b + 2 * h + c;
+              x[nt][e] = fmaf(ks, x[nt][e], fmaf(ko, qsum[nt][c], -m[nt][c]));
+              y[nt][e] = x[nt][e] + (lv - d[nt][c]);
+              if (MASKED && j0 + 16 * b + 8 * h + tok > last[nt][c])  // such a row may hold anything
+                x[nt][e] = y[nt][e] = -INFINITY;
+            }
+        }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          tx[nt][c] = fmax3(fmaxf(x[nt][c], x[nt][2 + c]), x[nt][4 + c], x[nt][6 + c]);
+          ty[nt][c] = fmax3(fmaxf(y[nt][c], y[nt][2 + c]), y[nt][4 + c], y[nt][6 + c]);
+          raise = raise || tx[nt][c] > kRaise || ty[nt][c] > kRaise;
+        }
+      if (__any_sync(0xffffffffu, raise)) {
+        float lv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lv[i] = lg2_approx(lo_bf16(pair_of(i / 2, i % 2, 1)));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float a = tx[nt][c], b = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (x[nt][2 * i + c] != -INFINITY) b = fmaxf(b, x[nt][2 * i + c] + lv[i]);
+#pragma unroll
+            for (int o = 4; o < 32; o *= 2) {
+              a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+              b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+            }
+            const float up = a == -INFINITY ? 0.f : fresh ? a : fmaxf(a, 0.f);
+            const float old = fresh ? kLowest : d[nt][c] - up;
+            const float fa = ex2_approx(-up), nd = fmaxf(old, b - up), fb = ex2_approx(old - nd);
+            m[nt][c] += up;
+            d[nt][c] = nd;
+            if (!fresh) {
+              l[nt][c] *= fa;
+              corr[nt][c] *= fa;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                acc[nt][i][c] *= fb;
+                acc[nt][i][2 + c] *= fb;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int e = 2 * i + c;
+              if (MASKED && x[nt][e] == -INFINITY) continue;
+              x[nt][e] -= up;
+              y[nt][e] = x[nt][e] + (lv[i] - nd);
+            }
+          }
+        fresh = false;
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint8_t* blk = stage + b * kBytes;
+        // V's codes: tokens t, t + 4 (contraction 2t, 2t + 1) and t + 8, t + 12, the lane's D / 8 columns from g D / 8 on
         uint32_t va[4][VW];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -469,84 +598,55 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
             va[i][0] = *reinterpret_cast<const uint32_t*>(v);
           }
         }
-        const uint32_t* pairs = reinterpret_cast<const uint32_t*>(blk + kBlk * D);
-        const uint32_t kp0 = pairs[tok], kp1 = pairs[tok + 8], vp0 = pairs[16 + tok], vp1 = pairs[16 + tok + 8];
-        auto lo_of = [](uint32_t v) { return __uint_as_float(v << 16); };
-        auto hi_of = [](uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); };
-        // scores in powers of two: scale (s_k (sum q (16 + c) - 16 sum q) + o_k sum q)
-        const float ks[2] = {lo_of(kp0) * s2, lo_of(kp1) * s2};
-        const float ko[2] = {fmaf(lo_of(kp0), -16.f, hi_of(kp0)) * s2, fmaf(lo_of(kp1), -16.f, hi_of(kp1)) * s2};
-        const float vs[2] = {lo_of(vp0), lo_of(vp1)};
-        const float vo[2] = {fmaf(lo_of(vp0), 8.f, hi_of(vp0)), fmaf(lo_of(vp1), 8.f, hi_of(vp1))};
-        bool raise = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {  // token e / 2, row e % 2
-            x[nt][e] = fmaf(ks[e / 2], x[nt][e], ko[e / 2] * qsum[nt][e % 2]);
-            if (j0 + 8 * (e / 2) > last[nt][e % 2]) x[nt][e] = -INFINITY;
-            raise = raise || x[nt][e] > m[nt][e % 2] + kRaise;
-          }
-        if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float top = fmaxf(m[nt][c], fmaxf(x[nt][c], x[nt][2 + c]));
-#pragma unroll
-              for (int o = 4; o < 32; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-              const float f = top == -INFINITY ? 1.f : ex2_approx(m[nt][c] - top);
-              m[nt][c] = top;
-              l[nt][c] *= f;
-              corr[nt][c] *= f;
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
-                acc[nt][i][c] *= f;
-                acc[nt][i][2 + c] *= f;
-              }
-            }
-        }
         uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // token
-            float w[2], ws[2];
+          for (int h = 0; h < 2; ++h) {
+            float w[2], wo[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const bool seen = j0 + 8 * h <= last[nt][c];
-              w[c] = seen ? ex2_approx(x[nt][2 * h + c] - m[nt][c]) : 0.f;
-              ws[c] = seen ? w[c] * vs[h] : 0.f;  // a row that is not seen may hold anything
+              const int e = 4 * b + 2 * h + c;
+              w[c] = ex2_approx(x[nt][e]);
+              wo[c] = ex2_approx(y[nt][e]);
               l[nt][c] += w[c];
+              if (!MASKED || x[nt][e] != -INFINITY) corr[nt][c] = fmaf(w[c], vo[2 * b + h], corr[nt][c]);
             }
-            // weights times scale in bf16, the operand of the product; what is taken off for the 24 = 16 + 8 uses the same
-            // rounded values, so that the rounding meets c - 8 only
-            const uint32_t r = pack_bf16x2(ws[0], ws[1]);
-            corr[nt][0] += fmaf(lo_of(r), -24.f, w[0] != 0.f ? w[0] * vo[h] : 0.f);
-            corr[nt][1] += fmaf(hi_of(r), -24.f, w[1] != 0.f ? w[1] * vo[h] : 0.f);
-            pb[nt][h] = transpose8x8(r);
+            pb[nt][h] = transpose8x8(pack_f16x2(wo[0], wo[1]));
           }
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
           const uint32_t l01 = __byte_perm(va[0][w], va[1][w], 0x5410), h01 = __byte_perm(va[0][w], va[1][w], 0x7632);
           const uint32_t l23 = __byte_perm(va[2][w], va[3][w], 0x5410), h23 = __byte_perm(va[2][w], va[3][w], 0x7632);
-          // columns 8 w + 0 .. 7 of the lane's: two to an mma, on its rows g and g + 8
-          using BF = __nv_bfloat16;
+          const uint32_t l01s = l01 >> 8, h01s = h01 >> 8, l23s = l23 >> 8, h23s = h23 >> 8;
+          constexpr uint32_t L = 0x000F000Fu, H = 0x00F000F0u;
+          // columns 8 w + 0 .. 7 of the lane's: two to an mma, the even one on row g, the odd one, 16 times too high, on g + 8
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma16816<BF>(acc[nt][4 * w], codes16<BF, 0>(l01), codes16<BF, 1>(l01), codes16<BF, 0>(l23), codes16<BF, 1>(l23),
-                         pb[nt][0], pb[nt][1]);
-            mma16816<BF>(acc[nt][4 * w + 1], codes16<BF, 2>(l01), codes16<BF, 3>(l01), codes16<BF, 2>(l23),
-                         codes16<BF, 3>(l23), pb[nt][0], pb[nt][1]);
-            mma16816<BF>(acc[nt][4 * w + 2], codes16<BF, 0>(h01), codes16<BF, 1>(h01), codes16<BF, 0>(h23),
-                         codes16<BF, 1>(h23), pb[nt][0], pb[nt][1]);
-            mma16816<BF>(acc[nt][4 * w + 3], codes16<BF, 2>(h01), codes16<BF, 3>(h01), codes16<BF, 2>(h23),
-                         codes16<BF, 3>(h23), pb[nt][0], pb[nt][1]);
+            mma_f16(acc[nt][4 * w], l01 & L, l01 & H, l23 & L, l23 & H, pb[nt][0], pb[nt][1]);
+            mma_f16(acc[nt][4 * w + 1], l01s & L, l01s & H, l23s & L, l23s & H, pb[nt][0], pb[nt][1]);
+            mma_f16(acc[nt][4 * w + 2], h01 & L, h01 & H, h23 & L, h23 & H, pb[nt][0], pb[nt][1]);
+            mma_f16(acc[nt][4 * w + 3], h01s & L, h01s & H, h23s & L, h23s & H, pb[nt][0], pb[nt][1]);
           }
         }
       }
+    };
+    // ---- this warp's units of the segment -----------------------------------------------------------
+    const int all_see = n - p.S;  // the last position that every row sees
+    long long u = lo + (warp + kWarps - (int)((lo - u0) % kWarps)) % kWarps;
+    for (; u < hi; u += kWarps, ++used) {
+      const uint32_t s = used % kStages;
+      const bool in = wait_own(&sm.full[warp][s], (used / kStages) & 1u, p, &sm, SITE_BLOCK);
+      if (!__all_sync(0xffffffffu, in) || sm.bad[warp][s]) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) l[nt][0] = l[nt][1] = NAN;
+      } else {
+        const int j0 = (int)(u - seg.start) * kUnit;
+        if (j0 + kUnit - 1 <= all_see) unit(sm.ring[warp][s], j0, std::false_type());
+        else unit(sm.ring[warp][s], j0, std::true_type());
+      }
       __syncwarp();  // every lane has read the stage
-      fill();
+      if (lane == 0) mbar_arrive(&sm.empty[warp][s]);
     }
     // ---- the warps' results meet --------------------------------------------------------------------
 #pragma unroll
@@ -561,38 +661,38 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
         }
         const int row = nt * 8 + 2 * t + c;
         if (g == 0) {
-          sm.m[warp][row] = m[nt][c];
+          sm.m[warp][row] = a == 0.f ? kLowest : m[nt][c];  // the row saw nothing
+          sm.d[warp][row] = d[nt][c];
           sm.l[warp][row] = a;
           sm.corr[warp][row] = b;
         }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {  // columns 2i and 2i + 1 of the lane's
           float2* o = reinterpret_cast<float2*>(&sm.o[warp][row][g * (D / 8) + 2 * i]);
-          *o = make_float2(acc[nt][i][c], acc[nt][i][2 + c]);
+          *o = make_float2(acc[nt][i][c] * 16777216.f, acc[nt][i][2 + c] * 1048576.f);
         }
       }
-    __syncthreads();
+    sync_consumers();
     const bool whole = lo == seg.start && hi == seg.start + seg.len;
     float* part = p.part + (2ll * blockIdx.x + (lo == u0 ? 0 : 1)) * kRows * (D + 2);
     for (int e = threadIdx.x; e < kRows * D; e += kWarps * 32) {
       const int row = e / D, col = e % D, r = seg.rt * kRows + row;
       if (r >= R) continue;
-      float top = -INFINITY, sum = 0.f, v = 0.f;
+      float top = kLowest, sum = 0.f, v = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm.m[w][row]);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float mw = sm.m[w][row];
-        const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - top);
-        sum += mw == -INFINITY ? sm.l[w][row] : sm.l[w][row] * f;  // a warp that saw nothing: 0, or NaN
-        v += (sm.o[w][row][col] + sm.corr[w][row]) * f;
+        const float f = ex2_approx(sm.m[w][row] - top);
+        sum += sm.l[w][row] * f;
+        const float fo = ex2_approx(sm.m[w][row] - top + sm.d[w][row]);
+        v += sm.o[w][row][col] * fo + sm.corr[w][row] * f;
       }
       if (whole) {
         const long long hq = seg.h * p.group + r % p.group, i = r / p.group;
         static_cast<T*>(p.o)[seg.b * p.so.b + hq * p.so.h + i * p.so.s + col] =
             from_f32<T>(sum == 0.f ? 0.f : sum != sum ? NAN : v / sum);
-        if (col == 0)
-          p.lse[(seg.b * (long long)p.Hq + hq) * p.S + i] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+        if (col == 0) p.lse[(seg.b * (long long)p.Hq + hq) * p.S + i] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
       } else {
         part[row * (D + 2) + col] = v;
         if (col == 0) {
@@ -601,7 +701,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
         }
       }
     }
-    __syncthreads();
+    sync_consumers();
     lo = hi;
   }
 }
@@ -619,7 +719,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
   float* lse = p.lse + ((long long)b * p.Hq + hq) * p.S + i;
   // every warp walks: where the segment begins, and how many units there are.  No block leaves before the kernel that
   // writes the pieces has ended: what follows on the stream may rely on both.
-  const int n = p.lens[b], len = blocks_of(p, b);
+  const int n = p.lens[b], len = units_of(p, b);
   if (len == 0) {
     wait_previous();
     const bool empty = n == 0;
@@ -627,21 +727,13 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
     if (threadIdx.x == 0) *lse = empty ? -INFINITY : NAN;
     return;
   }
-  Cursor none = {};
-  const long long total = walk(p, -1, none);
-  long long start = 0;
-  for (int b0 = 0; b0 < b; b0 += 32) {
-    long long v = b0 + lane < b ? (long long)blocks_of(p, b0 + lane) * p.c.Hkv * p.n_rt : 0;
-#pragma unroll
-    for (int s = 16; s; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
-    start += v;
-  }
-  start += (long long)(h * p.n_rt + rt) * len;
+  const long long total = units_before(p, p.B);
+  const long long start = units_before(p, b) + (long long)(h * p.n_rt + rt) * len;
   const long long per = share(total, ctas);
   const int c0 = (int)(start / per), c1 = (int)((start + len - 1) / per);
   wait_previous();
   if (c0 == c1) return;
-  float top = -INFINITY, sum = 0.f, acc[E] = {};
+  float top = kLowest, sum = 0.f, acc[E] = {};
 #pragma unroll 4
   for (int c = c0 + warp; c <= c1; c += 8) {
     const float* part = p.part + ((2ll * c + (c * per >= start ? 0 : 1)) * kRows + row % kRows) * (D + 2);
@@ -649,8 +741,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
     float v[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = part[lane + 32 * e];
-    const float t = fmaxf(top, mc);
-    const float f = t == -INFINITY ? 1.f : ex2_approx(top - t), w = t == -INFINITY ? 1.f : ex2_approx(mc - t);
+    const float t = fmaxf(top, mc), f = ex2_approx(top - t), w = ex2_approx(mc - t);
     top = t;
     sum = sum * f + lc * w;
 #pragma unroll
@@ -671,12 +762,12 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
   sum = 0.f;
 #pragma unroll
   for (int w = 0; w < 8; ++w) {
-    const float f = top == -INFINITY ? 1.f : ex2_approx(st[w] - top);
+    const float f = ex2_approx(st[w] - top);
     sum += sl[w] * f;
     v += so[w][threadIdx.x] * f;
   }
   o[threadIdx.x] = from_f32<T>(sum == 0.f ? 0.f : sum != sum ? NAN : v / sum);
-  if (threadIdx.x == 0) *lse = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+  if (threadIdx.x == 0) *lse = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -727,7 +818,7 @@ static int launch_attn(AttnParams& p, int dev, int n_sm, cudaStream_t st) {
   const long long R = (long long)p.group * p.S;
   p.n_rt = (int)((R + 8 * NT - 1) / (8 * NT));
   const int ctas = (n_sm < 152 ? n_sm : 152) * (NT == 1 ? 2 : 1);
-  attn_kernel<T, D, NT><<<ctas, kWarps * 32, smem, st>>>(p);
+  attn_kernel<T, D, NT><<<ctas, (kWarps + 1) * 32, smem, st>>>(p);
   if (launch_status() != PSR_OK) return PSR_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.B * p.c.Hkv * R));

@@ -1,7 +1,7 @@
 """GPU parity of the 4-bit KV cache (psr_kv4_append, psr_kv4_read, psr_kv4_attn) against the fp64 oracle.
 
 Append and read are held to equality: the format defines every rounding.  Attention: the oracle's kv4_attention gives,
-element by element, what the kernel's arithmetic may be off by (bf16 weights, fp32 sums); the output's rounding
+element by element, what the kernel's arithmetic may be off by (fp16 weights, fp32 sums); the output's rounding
 adds half a step.
 """
 import math
