@@ -177,7 +177,8 @@ __global__ void read_kernel(const ReadParams p) {
 //    first product in the layout that movmatrix turns into the second one's operand.
 //  * a maximum is only raised when a score passes it by kRaise: the check is one vote, the weights stay below 2^kRaise.
 constexpr int kWarps = 7;           // and one that fills their stages
-constexpr int kStages = 2;
+template <int D>
+constexpr int kStages = D == 128 ? 2 : 4;
 constexpr int kUnit = 2 * kBlk;     // tokens of a unit
 constexpr int kMaxCtas = 2 * 152;   // bounds the partial results
 constexpr float kRaise = 8.f;
@@ -303,51 +304,76 @@ template <int D, int NT>
 struct AttnSmem {
   static constexpr int kRows = 8 * NT;
   static constexpr int kBytes = kBlk * (D + 8);
-  alignas(128) uint8_t ring[kWarps][kStages][2 * kBytes];
+  alignas(128) uint8_t ring[kWarps][kStages<D>][2 * kBytes];
   alignas(16) float o[kWarps][kRows][D];  // a segment's results, by warp
   float m[kWarps][kRows], d[kWarps][kRows], l[kWarps][kRows], corr[kWarps][kRows];
-  uint64_t full[kWarps][kStages], empty[kWarps][kStages];
-  uint32_t bad[kWarps][kStages];  // a block of the stage has no page
+  uint64_t full[kWarps][kStages<D>], empty[kWarps][kStages<D>];
+  uint32_t bad[kWarps][kStages<D>];  // a block of the stage has no page
   long long total, u0;
   Cursor first;
   volatile uint32_t abort;
 };
 
-// Lane w < 7 of the last warp: the units u0 + w + 7 k of the CTA into warp w's stages.
+// Lane w < 7 of the last warp: the units u0 + w + 7 k of the CTA into warp w's stages.  The lanes take turns: none waits
+// for another's stage, and a unit's pages are looked up while the stage before it is still in use.
 template <int D, int NT>
 __device__ __forceinline__ void fill_rings(const AttnParams& p, AttnSmem<D, NT>& sm, int w, long long u0, long long u1) {
   constexpr int kBytes = AttnSmem<D, NT>::kBytes;
+  constexpr uint32_t S = kStages<D>;
+  const int in_page = (1 << p.page_shift) - 1;
   Cursor cur = sm.first;
-  uint32_t k = 0;
-  for (long long u = u0 + w; u < u1; u += kWarps, ++k) {
+  long long u = u0 + w;
+  uint32_t k = 0, idle = 0;
+  uint64_t t0 = 0;
+  int blk = 0, pg0 = 0, pg1 = 0;
+  bool two = false;
+  auto look_up = [&]() {
     cur.advance(p, u);
-    const int blk = 2 * (int)(u - cur.start);
-    const bool two = blk + 1 < (p.lens[cur.b] + kBlk - 1) / kBlk;
+    blk = 2 * (int)(u - cur.start);
+    two = blk + 1 < (p.lens[cur.b] + kBlk - 1) / kBlk;
     const int32_t* row = p.c.table + (long long)cur.b * p.c.max_pages;
-    const int in_page = (1 << p.page_shift) - 1;
-    const int pg0 = row[blk >> p.page_shift];
-    const int pg1 = two && p.page_shift == 0 ? row[blk + 1] : pg0;
-    const uint32_t s = k % kStages;
-    if (k >= kStages && !wait_own(&sm.empty[w][s], (k / kStages - 1) & 1u, p, &sm, SITE_STAGE)) break;
-    const bool ok = pg0 >= 0 && pg0 < p.c.n_pages && pg1 >= 0 && pg1 < p.c.n_pages;
-    sm.bad[w][s] = !ok;
-    if (!ok) {
-      mbar_arrive(&sm.full[w][s]);
+    pg0 = row[blk >> p.page_shift];
+    pg1 = two && p.page_shift == 0 ? row[blk + 1] : 0;
+  };
+  auto block = [&](int pg, int b) {
+    return p.c.base + ((((long long)pg * p.c.Hkv + cur.h) << p.page_shift) + (b & in_page)) * kBytes;
+  };
+  if (u < u1) look_up();
+  while (u < u1) {
+    const uint32_t s = k % S;
+    if (k >= S && !mbar_test_wait(&sm.empty[w][s], (k / S - 1) & 1u)) {
+      if (++idle % 64 == 0) {
+        const uint64_t now = globaltimer_ns();
+        if (idle == 64) t0 = now;
+        if (now - t0 > p.timeout_ns) {
+          raise_error(p, SITE_STAGE);
+          sm.abort = 1;
+        }
+        if (sm.abort) break;
+      }
+      nanosleep_ns(20);
       continue;
     }
-    auto block = [&](int pg, int b) {
-      return p.c.base + ((((long long)pg * p.c.Hkv + cur.h) << p.page_shift) + (b & in_page)) * kBytes;
-    };
-    const uint32_t dst = smem_u32(sm.ring[w][s]);
-    mbar_expect_tx(&sm.full[w][s], two ? 2 * kBytes : kBytes);
-    bulk_load(dst, block(pg0, blk), two && p.page_shift > 0 ? 2 * kBytes : kBytes, &sm.full[w][s]);
-    if (two && p.page_shift == 0) bulk_load(dst + kBytes, block(pg1, blk + 1), kBytes, &sm.full[w][s]);
+    idle = 0;
+    const bool ok = pg0 >= 0 && pg0 < p.c.n_pages && pg1 >= 0 && pg1 < p.c.n_pages;
+    sm.bad[w][s] = !ok;
+    if (ok) {
+      const uint32_t dst = smem_u32(sm.ring[w][s]);
+      mbar_expect_tx(&sm.full[w][s], two ? 2 * kBytes : kBytes);
+      bulk_load(dst, block(pg0, blk), two && p.page_shift > 0 ? 2 * kBytes : kBytes, &sm.full[w][s]);
+      if (two && p.page_shift == 0) bulk_load(dst + kBytes, block(pg1, blk + 1), kBytes, &sm.full[w][s]);
+    } else {
+      mbar_arrive(&sm.full[w][s]);
+    }
+    ++k;
+    u += kWarps;
+    if (u < u1) look_up();
   }
   if (sm.abort) {  // nothing of this CTA's is in flight when it leaves
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t s = 0; s < kStages && s < k; ++s) {
-      const uint32_t m = s + (k - 1 - s) / kStages * kStages;
-      while (!mbar_try_wait(&sm.full[w][s], (m / kStages) & 1u) && globaltimer_ns() - t0 < 100000000ull) {
+    const uint64_t begin = globaltimer_ns();
+    for (uint32_t s = 0; s < S && s < k; ++s) {
+      const uint32_t m = s + (k - 1 - s) / S * S;
+      while (!mbar_try_wait(&sm.full[w][s], (m / S) & 1u) && globaltimer_ns() - begin < 100000000ull) {
       }
     }
   }
@@ -377,7 +403,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NT == 1 ? 2 : 1) attn_kerne
     }
   } else if (warp == kWarps && lane < kWarps) {
     if (lane == 0) sm.abort = 0;
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kStages<D>; ++s) {
       mbar_init(&sm.full[lane][s], 1);
       mbar_init(&sm.empty[lane][s], 1);
     }
@@ -635,8 +661,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NT == 1 ? 2 : 1) attn_kerne
     const int all_see = n - p.S;  // the last position that every row sees
     long long u = lo + (warp + kWarps - (int)((lo - u0) % kWarps)) % kWarps;
     for (; u < hi; u += kWarps, ++used) {
-      const uint32_t s = used % kStages;
-      const bool in = wait_own(&sm.full[warp][s], (used / kStages) & 1u, p, &sm, SITE_BLOCK);
+      const uint32_t s = used % kStages<D>;
+      const bool in = wait_own(&sm.full[warp][s], (used / kStages<D>) & 1u, p, &sm, SITE_BLOCK);
       if (!__all_sync(0xffffffffu, in) || sm.bad[warp][s]) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) l[nt][0] = l[nt][1] = NAN;
