@@ -156,9 +156,11 @@ __global__ void read_kernel(const ReadParams p) {
 // ------------------------------------------------------------------------------------------------
 // Bound by reading the cache once.  A unit is two blocks (32 tokens) of one KV head and a tile of up to 8 NT query rows
 // (the group's heads times the new tokens); the units of all sequences stand in a line, segment by segment (a segment:
-// sequence, head, row tile), and each CTA takes an equal stretch of it, so ragged batches and single long sequences load
-// every SM alike.  A segment that lies within one CTA is finished there; the pieces of one that does not meet in
-// combine_kernel through fp32 partial results and their running maxima and sums, as the ring's chunks do.
+// sequence, head, row tile), and each warp takes an equal stretch of it, so ragged batches and single long sequences load
+// every SM alike.  A segment that lies within one stretch is finished there; the pieces of one that does not meet in
+// combine_kernel through fp32 partial results and their running maxima and sums, as the ring's chunks do.  (With
+// stretches for whole CTAs, whose warps met in shared memory after every segment, batches of short sequences took 3 to 5 us
+// a segment.)
 //
 // Each of seven warps has its own ring of stages, which an eighth one fills with bulk copies, and its own softmax state:
 //   S^T[token][row] = K codes . q      (mma.m16n8k16: tokens on its 16 rows, query rows on its 8 columns)
@@ -180,7 +182,10 @@ constexpr int kWarps = 7;           // and one that fills their stages
 template <int D>
 constexpr int kStages = D == 128 ? 2 : 4;
 constexpr int kUnit = 2 * kBlk;     // tokens of a unit
+constexpr int kMinUnits = 4;        // of a warp's stretch: short ones would only move work to the join
 constexpr int kMaxCtas = 2 * 152;   // bounds the partial results
+template <int D>
+constexpr int kPart = D + 4;        // floats of a row's partial result: sums, maximum, weight
 constexpr float kRaise = 8.f;
 constexpr float kLowest = -1e30f;   // a maximum that nothing has raised
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
@@ -197,7 +202,8 @@ struct AttnParams {
   int page_shift;             // log2(page / 16)
   int vec;                    // q's rows are 16-byte aligned
   float scale;
-  float* part;                // [2 kMaxCtas][rows of a tile][D + 2]
+  int vec_o;                  // o's rows are 16-byte aligned
+  float* part;                // [2 kMaxCtas kWarps][rows of a tile][kPart]
   Ctrl* ctrl;
   unsigned long long timeout_ns;
 };
@@ -269,10 +275,10 @@ __device__ __forceinline__ Cursor segment_at(const AttnParams& p, long long targ
   return cur;
 }
 
-// Units of a CTA: an equal share, at least one a warp.
+// Units of a warp's stretch: an equal share.
 __device__ __forceinline__ long long share(long long total, int ctas) {
-  const long long per = (total + ctas - 1) / ctas;
-  return per < kWarps ? kWarps : per;
+  const long long per = (total + (long long)ctas * kWarps - 1) / ((long long)ctas * kWarps);
+  return per < kMinUnits ? kMinUnits : per;
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -298,31 +304,28 @@ __device__ __forceinline__ float lg2_approx(float x) {
 }
 __device__ __forceinline__ float lo_bf16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
-__device__ __forceinline__ void sync_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
 
-template <int D, int NT>
+template <int D>
 struct AttnSmem {
-  static constexpr int kRows = 8 * NT;
   static constexpr int kBytes = kBlk * (D + 8);
   alignas(128) uint8_t ring[kWarps][kStages<D>][2 * kBytes];
-  alignas(16) float o[kWarps][kRows][D];  // a segment's results, by warp
-  float m[kWarps][kRows], d[kWarps][kRows], l[kWarps][kRows], corr[kWarps][kRows];
   uint64_t full[kWarps][kStages<D>], empty[kWarps][kStages<D>];
   uint32_t bad[kWarps][kStages<D>];  // a block of the stage has no page
-  long long total, u0;
-  Cursor first;
+  long long u0[kWarps], u1[kWarps];  // the warps' stretches, and the segments that they begin in
+  Cursor first[kWarps];
   volatile uint32_t abort;
 };
 
-// Lane w < 7 of the last warp: the units u0 + w + 7 k of the CTA into warp w's stages.  The lanes take turns: none waits
+// Lane w < 7 of the last warp: the units of warp w's stretch into its stages.  The lanes take turns: none waits
 // for another's stage, and a unit's pages are looked up while the stage before it is still in use.
-template <int D, int NT>
-__device__ __forceinline__ void fill_rings(const AttnParams& p, AttnSmem<D, NT>& sm, int w, long long u0, long long u1) {
-  constexpr int kBytes = AttnSmem<D, NT>::kBytes;
+template <int D>
+__device__ __forceinline__ void fill_rings(const AttnParams& p, AttnSmem<D>& sm, int w) {
+  constexpr int kBytes = AttnSmem<D>::kBytes;
   constexpr uint32_t S = kStages<D>;
   const int in_page = (1 << p.page_shift) - 1;
-  Cursor cur = sm.first;
-  long long u = u0 + w;
+  Cursor cur = sm.first[w];
+  long long u = sm.u0[w];
+  const long long u1 = sm.u1[w];
   uint32_t k = 0, idle = 0;
   uint64_t t0 = 0;
   int blk = 0, pg0 = 0, pg1 = 0;
@@ -366,7 +369,7 @@ __device__ __forceinline__ void fill_rings(const AttnParams& p, AttnSmem<D, NT>&
       mbar_arrive(&sm.full[w][s]);
     }
     ++k;
-    u += kWarps;
+    ++u;
     if (u < u1) look_up();
   }
   if (sm.abort) {  // nothing of this CTA's is in flight when it leaves
@@ -381,27 +384,27 @@ __device__ __forceinline__ void fill_rings(const AttnParams& p, AttnSmem<D, NT>&
 
 template <class T, int D, int NT>
 __global__ void __launch_bounds__((kWarps + 1) * 32, NT == 1 ? 2 : 1) attn_kernel(const __grid_constant__ AttnParams p) {
-  using Sm = AttnSmem<D, NT>;
-  constexpr int kRows = Sm::kRows, kBytes = Sm::kBytes;
+  using Sm = AttnSmem<D>;
+  constexpr int kRows = 8 * NT, kBytes = Sm::kBytes;
   constexpr int KW = D / 32;  // words of K codes a lane takes of a row
   constexpr int VW = D / 64;  // words of V codes a lane takes of a token
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
+  const int slot = warp * gridDim.x + blockIdx.x;  // neighbouring stretches on different SMs
   clear_ctrl(p.ctrl);
   launch_dependents();
-  if (warp == 0) {
+  if (warp < kWarps) {
     const long long total = units_before(p, p.B);
-    const long long u0 = blockIdx.x * share(total, gridDim.x);
-    if (u0 < total) {
-      const Cursor c = segment_at(p, u0);
-      if (lane == 0) sm.first = c;
-    }
+    const long long per = share(total, gridDim.x), u0 = slot * per;
+    Cursor c = {};
+    if (u0 < total) c = segment_at(p, u0);
     if (lane == 0) {
-      sm.total = total;
-      sm.u0 = u0;
+      sm.first[warp] = c;
+      sm.u0[warp] = u0;
+      sm.u1[warp] = u0 + per < total ? u0 + per : total;
     }
-  } else if (warp == kWarps && lane < kWarps) {
+  } else if (lane < kWarps) {
     if (lane == 0) sm.abort = 0;
     for (int s = 0; s < kStages<D>; ++s) {
       mbar_init(&sm.full[lane][s], 1);
@@ -410,15 +413,13 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NT == 1 ? 2 : 1) attn_kerne
     fence_barrier_init();
   }
   __syncthreads();
-  const long long total = sm.total, u0 = sm.u0;
-  const long long end = u0 + share(total, gridDim.x), u1 = end < total ? end : total;
-  if (u0 >= u1) return;
   if (warp == kWarps) {
-    if (lane < kWarps) fill_rings<D, NT>(p, sm, lane, u0, u1);
+    if (lane < kWarps) fill_rings<D>(p, sm, lane);
     return;
   }
 
-  Cursor seg = sm.first;
+  const long long u0 = sm.u0[warp], u1 = sm.u1[warp];
+  Cursor seg = sm.first[warp];
   uint32_t used = 0;
   for (long long lo = u0; lo < u1;) {
     seg.advance(p, lo);
@@ -657,10 +658,9 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NT == 1 ? 2 : 1) attn_kerne
         }
       }
     };
-    // ---- this warp's units of the segment -----------------------------------------------------------
+    // ---- the units of the segment --------------------------------------------------------------------
     const int all_see = n - p.S;  // the last position that every row sees
-    long long u = lo + (warp + kWarps - (int)((lo - u0) % kWarps)) % kWarps;
-    for (; u < hi; u += kWarps, ++used) {
+    for (long long u = lo; u < hi; ++u, ++used) {
       const uint32_t s = used % kStages<D>;
       const bool in = wait_own(&sm.full[warp][s], (used / kStages<D>) & 1u, p, &sm, SITE_BLOCK);
       if (!__all_sync(0xffffffffu, in) || sm.bad[warp][s]) {
@@ -674,60 +674,56 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NT == 1 ? 2 : 1) attn_kerne
       __syncwarp();  // every lane has read the stage
       if (lane == 0) mbar_arrive(&sm.empty[warp][s]);
     }
-    // ---- the warps' results meet --------------------------------------------------------------------
+    // ---- the results: o if the segment is whole, else a piece ----------------------------------------
+    const bool whole = lo == seg.start && hi == seg.start + seg.len;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float a = l[nt][c], b = corr[nt][c];
+        float sum = l[nt][c], base = corr[nt][c];
 #pragma unroll
         for (int o = 4; o < 32; o *= 2) {
-          a += __shfl_xor_sync(0xffffffffu, a, o);
-          b += __shfl_xor_sync(0xffffffffu, b, o);
+          sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          base += __shfl_xor_sync(0xffffffffu, base, o);
         }
-        const int row = nt * 8 + 2 * t + c;
-        if (g == 0) {
-          sm.m[warp][row] = a == 0.f ? kLowest : m[nt][c];  // the row saw nothing
-          sm.d[warp][row] = d[nt][c];
-          sm.l[warp][row] = a;
-          sm.corr[warp][row] = b;
-        }
+        const int row = nt * 8 + 2 * t + c, r = seg.rt * kRows + row;
+        if (r >= R) continue;
+        const float fo = ex2_approx(d[nt][c]);
+        float v[D / 8];  // the lane's columns, from g D / 8 on
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {  // columns 2i and 2i + 1 of the lane's
-          float2* o = reinterpret_cast<float2*>(&sm.o[warp][row][g * (D / 8) + 2 * i]);
-          *o = make_float2(acc[nt][i][c] * 16777216.f, acc[nt][i][2 + c] * 1048576.f);
+        for (int i = 0; i < D / 16; ++i) {
+          v[2 * i] = fmaf(acc[nt][i][c] * 16777216.f, fo, base);
+          v[2 * i + 1] = fmaf(acc[nt][i][2 + c] * 1048576.f, fo, base);
+        }
+        if (whole) {
+          const long long hq = seg.h * p.group + r % p.group, i = r / p.group;
+          T* out = static_cast<T*>(p.o) + seg.b * p.so.b + hq * p.so.h + i * p.so.s + g * (D / 8);
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          if (p.vec_o) {
+#pragma unroll
+            for (int q = 0; q < D / 64; ++q) {
+              struct alignas(16) Eight { T e[8]; } w;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w.e[e] = from_f32<T>(sum == 0.f ? 0.f : v[q * 8 + e] * inv);
+              *reinterpret_cast<Eight*>(out + q * 8) = w;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < D / 8; ++e) out[e] = from_f32<T>(sum == 0.f ? 0.f : v[e] * inv);
+          }
+          if (g == 0)
+            p.lse[(seg.b * (long long)p.Hq + hq) * p.S + i] = sum == 0.f ? -INFINITY : (m[nt][c] + log2f(sum)) * kLn2;
+        } else {
+          float* part = p.part + ((2ll * slot + (lo == u0 ? 0 : 1)) * kRows + row) * kPart<D>;
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q)
+            *reinterpret_cast<float4*>(part + g * (D / 8) + q * 4) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          if (g == 0) {
+            part[D] = sum == 0.f ? kLowest : m[nt][c];  // kLowest: the row saw nothing
+            part[D + 1] = sum;
+          }
         }
       }
-    sync_consumers();
-    const bool whole = lo == seg.start && hi == seg.start + seg.len;
-    float* part = p.part + (2ll * blockIdx.x + (lo == u0 ? 0 : 1)) * kRows * (D + 2);
-    for (int e = threadIdx.x; e < kRows * D; e += kWarps * 32) {
-      const int row = e / D, col = e % D, r = seg.rt * kRows + row;
-      if (r >= R) continue;
-      float top = kLowest, sum = 0.f, v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm.m[w][row]);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2_approx(sm.m[w][row] - top);
-        sum += sm.l[w][row] * f;
-        const float fo = ex2_approx(sm.m[w][row] - top + sm.d[w][row]);
-        v += sm.o[w][row][col] * fo + sm.corr[w][row] * f;
-      }
-      if (whole) {
-        const long long hq = seg.h * p.group + r % p.group, i = r / p.group;
-        static_cast<T*>(p.o)[seg.b * p.so.b + hq * p.so.h + i * p.so.s + col] =
-            from_f32<T>(sum == 0.f ? 0.f : sum != sum ? NAN : v / sum);
-        if (col == 0) p.lse[(seg.b * (long long)p.Hq + hq) * p.S + i] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-      } else {
-        part[row * (D + 2) + col] = v;
-        if (col == 0) {
-          part[row * (D + 2) + D] = top;
-          part[row * (D + 2) + D + 1] = sum;
-        }
-      }
-    }
-    sync_consumers();
     lo = hi;
   }
 }
@@ -762,7 +758,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
   float top = kLowest, sum = 0.f, acc[E] = {};
 #pragma unroll 4
   for (int c = c0 + warp; c <= c1; c += 8) {
-    const float* part = p.part + ((2ll * c + (c * per >= start ? 0 : 1)) * kRows + row % kRows) * (D + 2);
+    const float* part = p.part + ((2ll * c + (c * per >= start ? 0 : 1)) * kRows + row % kRows) * kPart<D>;
     const float mc = part[D], lc = part[D + 1];
     float v[E];
 #pragma unroll
@@ -829,8 +825,8 @@ template <class T, int D, int NT>
 static int launch_attn(AttnParams& p, int dev, int n_sm, cudaStream_t st) {
   static std::mutex mu;
   static bool known[64] = {};
-  constexpr int smem = (int)sizeof(AttnSmem<D, NT>);
-  static_assert(NT == 2 ? smem <= 232448 : 2 * (smem + 1024) <= 233472, "shared memory");
+  constexpr int smem = (int)sizeof(AttnSmem<D>);
+  static_assert(2 * (smem + 1024) <= 233472, "shared memory");
   {
     std::lock_guard<std::mutex> lk(mu);
     if (dev < 0 || dev >= 64 || !known[dev]) {
@@ -919,7 +915,8 @@ int psr_kv4_read(const psr_kv4_shape* sh, const void* cache, const int32_t* tabl
 
 size_t psr_kv4_attn_workspace_bytes(const psr_kv4_shape* sh) {
   if (check_shape(sh) != PSR_OK) return 0;
-  return 256 + (size_t)2 * kMaxCtas * tile_rows(sh) * (sh->d + 2) * 4;
+  // a tile of 16 rows runs one CTA to an SM, one of 8 rows two
+  return 256 + (size_t)2 * kMaxCtas * kWarps * 8 * (sh->d + 4) * 4;
 }
 
 int psr_kv4_attn(const psr_kv4_shape* sh, const void* q, const psr_strides* qs, const void* cache, const int32_t* table,
@@ -947,6 +944,7 @@ int psr_kv4_attn(const psr_kv4_shape* sh, const void* q, const psr_strides* qs, 
   for (int n = sh->page / kBlk; n > 1; n /= 2) ++p.page_shift;
   auto even = [](long long stride, int n) { return n <= 1 || stride % 8 == 0; };
   p.vec = aligned_to(q, 16) && even(qs->b, sh->B) && even(qs->h, sh->Hq) && even(qs->s, sh->S);
+  p.vec_o = aligned_to(o, 16) && even(os->b, sh->B) && even(os->h, sh->Hq) && even(os->s, sh->S);
   p.scale = sh->scale > 0.f ? sh->scale : 1.f / sqrtf((float)sh->d);
   p.ctrl = static_cast<Ctrl*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
