@@ -162,7 +162,8 @@ __global__ void read_kernel(const ReadParams p) {
 // stretches for whole CTAs, whose warps met in shared memory after every segment, batches of short sequences took 3 to 5 us
 // a segment.)
 //
-// Each of seven warps has its own ring of stages, which an eighth one fills with bulk copies, and its own softmax state:
+// Each warp has its own ring of stages, filled with one bulk copy for the two blocks of a unit (two where pages hold one
+// block), and its own softmax state:
 //   S^T[token][row] = K codes . q      (mma.m16n8k16: tokens on its 16 rows, query rows on its 8 columns)
 //   O^T[column][row] += V codes^T . P  (columns of V on the 16 rows, tokens in the contraction)
 // The issue slots are what is scarce (a first version that made 16-bit floats 16 + c of the codes took 485 instructions for
@@ -178,7 +179,7 @@ __global__ void read_kernel(const ReadParams p) {
 //    bytes of a K row, and the tokens are dealt to the mma's rows so that V's loads fall on different banks; P leaves the
 //    first product in the layout that movmatrix turns into the second one's operand.
 //  * a maximum is only raised when a score passes it by kRaise: the check is one vote, the weights stay below 2^kRaise.
-constexpr int kWarps = 7;           // and one that fills their stages
+constexpr int kWarps = 8;
 template <int D>
 constexpr int kStages = D == 128 ? 2 : 4;
 constexpr int kUnit = 2 * kBlk;     // tokens of a unit
@@ -189,7 +190,7 @@ constexpr int kPart = D + 4;        // floats of a row's partial result: sums, m
 constexpr float kRaise = 8.f;
 constexpr float kLowest = -1e30f;   // a maximum that nothing has raised
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
-enum : uint32_t { SITE_BLOCK = 51, SITE_STAGE = 52 };
+enum : uint32_t { SITE_BLOCK = 51 };
 
 struct AttnParams {
   Cache c;
@@ -208,24 +209,25 @@ struct AttnParams {
   unsigned long long timeout_ns;
 };
 
-// Units of sequence b: 0 if it is empty or its length is out of range.
-__device__ __forceinline__ int units_of(const AttnParams& p, int b) {
+// Blocks of sequence b: 0 if it is empty or its length is out of range.  Two make a unit.
+__device__ __forceinline__ int blocks_of(const AttnParams& p, int b) {
   const int n = p.lens[b];
-  return n < 0 || n > (long long)p.c.max_pages * p.c.page ? 0 : (n + kUnit - 1) / kUnit;
+  return n < 0 || n > (long long)p.c.max_pages * p.c.page ? 0 : (n + kBlk - 1) / kBlk;
 }
 
-// A place in the line of units.
+// A place in the line of units (fewer than 2^31: checked on the host).
 struct Cursor {
-  int b, h, rt, len;
-  long long start;  // first unit of the segment
-  __device__ __forceinline__ void advance(const AttnParams& p, long long u) {
-    while (u >= start + len) {
-      start += len;
+  int b, h, rt, blocks;
+  int start;  // first unit of the segment
+  __device__ __forceinline__ int end() const { return start + (blocks + 1) / 2; }
+  __device__ __forceinline__ void advance(const AttnParams& p, int u) {
+    while (u >= end()) {
+      start = end();
       if (++rt == p.n_rt) {
         rt = 0;
         if (++h == p.c.Hkv) {
           h = 0;
-          len = units_of(p, ++b);
+          blocks = blocks_of(p, ++b);
         }
       }
     }
@@ -233,41 +235,39 @@ struct Cursor {
 };
 
 // One warp: the units of the sequences before `end`.
-__device__ __forceinline__ long long units_before(const AttnParams& p, int end) {
+__device__ __forceinline__ int units_before(const AttnParams& p, int end) {
   const int lane = threadIdx.x % 32;
-  long long sum = 0;
-  for (int b = lane; b < end; b += 32) sum += units_of(p, b);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum * p.c.Hkv * p.n_rt;
+  int sum = 0;
+#pragma unroll 4
+  for (int b = lane; b < end; b += 32) sum += (blocks_of(p, b) + 1) / 2;
+  return __reduce_add_sync(0xffffffffu, sum) * p.c.Hkv * p.n_rt;
 }
 
 // One warp: the segment that holds a unit (of those there are).
-__device__ __forceinline__ Cursor segment_at(const AttnParams& p, long long target) {
+__device__ __forceinline__ Cursor segment_at(const AttnParams& p, int target) {
   const int lane = threadIdx.x % 32;
   const int per = p.c.Hkv * p.n_rt;
   Cursor cur = {};
-  long long base = 0;
+  int base = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int n = b0 + lane < p.B ? units_of(p, b0 + lane) : 0;
-    const long long own = (long long)n * per;
-    long long sum = own;
+    const int n = b0 + lane < p.B ? blocks_of(p, b0 + lane) : 0;
+    const int own = (n + 1) / 2 * per;
+    int sum = own;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-      const long long v = __shfl_up_sync(0xffffffffu, sum, o);
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += v;
     }
-    const long long all = __shfl_sync(0xffffffffu, sum, 31);
+    const int all = __shfl_sync(0xffffffffu, sum, 31);
     if (target < base + all) {
       const int at = __ffs(__ballot_sync(0xffffffffu, target < base + sum)) - 1;
-      const int len = __shfl_sync(0xffffffffu, n, at);
-      const long long first = base + __shfl_sync(0xffffffffu, sum - own, at);
-      const int seg = (int)((target - first) / len);
+      const int first = base + __shfl_sync(0xffffffffu, sum - own, at);
+      cur.blocks = __shfl_sync(0xffffffffu, n, at);
+      const int len = (cur.blocks + 1) / 2, seg = (target - first) / len;
       cur.b = b0 + at;
       cur.h = seg / p.n_rt;
       cur.rt = seg % p.n_rt;
-      cur.len = len;
-      cur.start = first + (long long)seg * len;
+      cur.start = first + seg * len;
       break;
     }
     base += all;
@@ -276,8 +276,8 @@ __device__ __forceinline__ Cursor segment_at(const AttnParams& p, long long targ
 }
 
 // Units of a warp's stretch: an equal share.
-__device__ __forceinline__ long long share(long long total, int ctas) {
-  const long long per = (total + (long long)ctas * kWarps - 1) / ((long long)ctas * kWarps);
+__device__ __forceinline__ int share(int total, int ctas) {
+  const int per = (total + ctas * kWarps - 1) / (ctas * kWarps);
   return per < kMinUnits ? kMinUnits : per;
 }
 
@@ -309,81 +309,12 @@ template <int D>
 struct AttnSmem {
   static constexpr int kBytes = kBlk * (D + 8);
   alignas(128) uint8_t ring[kWarps][kStages<D>][2 * kBytes];
-  uint64_t full[kWarps][kStages<D>], empty[kWarps][kStages<D>];
-  uint32_t bad[kWarps][kStages<D>];  // a block of the stage has no page
-  long long u0[kWarps], u1[kWarps];  // the warps' stretches, and the segments that they begin in
-  Cursor first[kWarps];
+  uint64_t full[kWarps][kStages<D>];
   volatile uint32_t abort;
 };
 
-// Lane w < 7 of the last warp: the units of warp w's stretch into its stages.  The lanes take turns: none waits
-// for another's stage, and a unit's pages are looked up while the stage before it is still in use.
-template <int D>
-__device__ __forceinline__ void fill_rings(const AttnParams& p, AttnSmem<D>& sm, int w) {
-  constexpr int kBytes = AttnSmem<D>::kBytes;
-  constexpr uint32_t S = kStages<D>;
-  const int in_page = (1 << p.page_shift) - 1;
-  Cursor cur = sm.first[w];
-  long long u = sm.u0[w];
-  const long long u1 = sm.u1[w];
-  uint32_t k = 0, idle = 0;
-  uint64_t t0 = 0;
-  int blk = 0, pg0 = 0, pg1 = 0;
-  bool two = false;
-  auto look_up = [&]() {
-    cur.advance(p, u);
-    blk = 2 * (int)(u - cur.start);
-    two = blk + 1 < (p.lens[cur.b] + kBlk - 1) / kBlk;
-    const int32_t* row = p.c.table + (long long)cur.b * p.c.max_pages;
-    pg0 = row[blk >> p.page_shift];
-    pg1 = two && p.page_shift == 0 ? row[blk + 1] : 0;
-  };
-  auto block = [&](int pg, int b) {
-    return p.c.base + ((((long long)pg * p.c.Hkv + cur.h) << p.page_shift) + (b & in_page)) * kBytes;
-  };
-  if (u < u1) look_up();
-  while (u < u1) {
-    const uint32_t s = k % S;
-    if (k >= S && !mbar_test_wait(&sm.empty[w][s], (k / S - 1) & 1u)) {
-      if (++idle % 64 == 0) {
-        const uint64_t now = globaltimer_ns();
-        if (idle == 64) t0 = now;
-        if (now - t0 > p.timeout_ns) {
-          raise_error(p, SITE_STAGE);
-          sm.abort = 1;
-        }
-        if (sm.abort) break;
-      }
-      nanosleep_ns(20);
-      continue;
-    }
-    idle = 0;
-    const bool ok = pg0 >= 0 && pg0 < p.c.n_pages && pg1 >= 0 && pg1 < p.c.n_pages;
-    sm.bad[w][s] = !ok;
-    if (ok) {
-      const uint32_t dst = smem_u32(sm.ring[w][s]);
-      mbar_expect_tx(&sm.full[w][s], two ? 2 * kBytes : kBytes);
-      bulk_load(dst, block(pg0, blk), two && p.page_shift > 0 ? 2 * kBytes : kBytes, &sm.full[w][s]);
-      if (two && p.page_shift == 0) bulk_load(dst + kBytes, block(pg1, blk + 1), kBytes, &sm.full[w][s]);
-    } else {
-      mbar_arrive(&sm.full[w][s]);
-    }
-    ++k;
-    ++u;
-    if (u < u1) look_up();
-  }
-  if (sm.abort) {  // nothing of this CTA's is in flight when it leaves
-    const uint64_t begin = globaltimer_ns();
-    for (uint32_t s = 0; s < S && s < k; ++s) {
-      const uint32_t m = s + (k - 1 - s) / S * S;
-      while (!mbar_try_wait(&sm.full[w][s], (m / S) & 1u) && globaltimer_ns() - begin < 100000000ull) {
-      }
-    }
-  }
-}
-
 template <class T, int D, int NT>
-__global__ void __launch_bounds__((kWarps + 1) * 32, NT == 1 ? 2 : 1) attn_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(const __grid_constant__ AttnParams p) {
   using Sm = AttnSmem<D>;
   constexpr int kRows = 8 * NT, kBytes = Sm::kBytes;
   constexpr int KW = D / 32;  // words of K codes a lane takes of a row
@@ -392,38 +323,62 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NT == 1 ? 2 : 1) attn_kerne
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
   const int slot = warp * gridDim.x + blockIdx.x;  // neighbouring stretches on different SMs
+  constexpr uint32_t S = kStages<D>;
   clear_ctrl(p.ctrl);
   launch_dependents();
-  if (warp < kWarps) {
-    const long long total = units_before(p, p.B);
-    const long long per = share(total, gridDim.x), u0 = slot * per;
-    Cursor c = {};
-    if (u0 < total) c = segment_at(p, u0);
-    if (lane == 0) {
-      sm.first[warp] = c;
-      sm.u0[warp] = u0;
-      sm.u1[warp] = u0 + per < total ? u0 + per : total;
-    }
-  } else if (lane < kWarps) {
-    if (lane == 0) sm.abort = 0;
-    for (int s = 0; s < kStages<D>; ++s) {
-      mbar_init(&sm.full[lane][s], 1);
-      mbar_init(&sm.empty[lane][s], 1);
-    }
+  if (threadIdx.x == 0) sm.abort = 0;
+  if (lane == 0) {
+    for (uint32_t s = 0; s < S; ++s) mbar_init(&sm.full[warp][s], 1);
     fence_barrier_init();
   }
   __syncthreads();
-  if (warp == kWarps) {
-    if (lane < kWarps) fill_rings<D>(p, sm, lane);
-    return;
-  }
+  const int total = units_before(p, p.B), per = share(total, gridDim.x);
+  if (slot > (total - 1) / per) return;  // (total 0: slot 0 finds an empty stretch below)
+  const int u0 = slot * per, u1 = min(u0 + per, total);
+  if (u0 >= u1) return;
+  Cursor seg = segment_at(p, u0);
 
-  const long long u0 = sm.u0[warp], u1 = sm.u1[warp];
-  Cursor seg = sm.first[warp];
-  uint32_t used = 0;
-  for (long long lo = u0; lo < u1;) {
+  // ---- the ring: unit u0 + k goes to stage k % S; a unit's pages are looked next one unit ahead of its copy -----------
+  Cursor pre = seg;
+  int next = u0, blk = 0, pg0 = 0, pg1 = 0;
+  auto look_up = [&]() {
+    pre.advance(p, next);
+    blk = 2 * (next - pre.start);
+    const int32_t* row = p.c.table + (long long)pre.b * p.c.max_pages;
+    pg0 = row[blk >> p.page_shift];
+    pg1 = 0;  // not pg0: a copy would wait for its load here
+    if (p.page_shift == 0 && blk + 1 < pre.blocks) pg1 = row[blk + 1];
+  };
+  uint32_t bad = 0;  // bit s: a block of stage s has no page
+  auto fill = [&]() {
+    if (next >= u1) return;
+    const uint32_t s = (uint32_t)(next - u0) % S;
+    const bool ok = pg0 >= 0 && pg0 < p.c.n_pages && pg1 >= 0 && pg1 < p.c.n_pages;
+    bad = (bad & ~(1u << s)) | (ok ? 0u : 1u << s);
+    if (lane == 0) {
+      if (ok) {
+        const bool two = blk + 1 < pre.blocks;
+        const int in_page = (1 << p.page_shift) - 1;
+        auto block = [&](int pg, int b) {
+          return p.c.base + ((((long long)pg * p.c.Hkv + pre.h) << p.page_shift) + (b & in_page)) * kBytes;
+        };
+        const uint32_t dst = smem_u32(sm.ring[warp][s]);
+        mbar_expect_tx(&sm.full[warp][s], two ? 2 * kBytes : kBytes);
+        bulk_load(dst, block(pg0, blk), two && p.page_shift > 0 ? 2 * kBytes : kBytes, &sm.full[warp][s]);
+        if (two && p.page_shift == 0) bulk_load(dst + kBytes, block(pg1, blk + 1), kBytes, &sm.full[warp][s]);
+      } else {
+        mbar_arrive(&sm.full[warp][s]);
+      }
+    }
+    ++next;
+    if (next < u1) look_up();
+  };
+  look_up();
+  for (uint32_t s = 0; s < S; ++s) fill();
+
+  for (int lo = u0; lo < u1;) {
     seg.advance(p, lo);
-    const long long hi = seg.start + seg.len < u1 ? seg.start + seg.len : u1;
+    const int hi = min(seg.end(), u1);
     const int n = p.lens[seg.b];
     const int R = p.group * p.S;  // query rows of the KV head: row = new token * group + head of the group
     // ---- query fragments: the row g of each tile, columns in the order of the K codes' words -----
@@ -660,22 +615,23 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NT == 1 ? 2 : 1) attn_kerne
     };
     // ---- the units of the segment --------------------------------------------------------------------
     const int all_see = n - p.S;  // the last position that every row sees
-    for (long long u = lo; u < hi; ++u, ++used) {
-      const uint32_t s = used % kStages<D>;
-      const bool in = wait_own(&sm.full[warp][s], (used / kStages<D>) & 1u, p, &sm, SITE_BLOCK);
-      if (!__all_sync(0xffffffffu, in) || sm.bad[warp][s]) {
+    for (int u = lo; u < hi; ++u) {
+      const uint32_t k = (uint32_t)(u - u0), s = k % S;
+      const bool in = wait_own(&sm.full[warp][s], (k / S) & 1u, p, &sm, SITE_BLOCK);
+      if (!__all_sync(0xffffffffu, in) || (bad >> s & 1u)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) l[nt][0] = l[nt][1] = NAN;
       } else {
-        const int j0 = (int)(u - seg.start) * kUnit;
+        const int j0 = (u - seg.start) * kUnit;
         if (j0 + kUnit - 1 <= all_see) unit(sm.ring[warp][s], j0, std::false_type());
         else unit(sm.ring[warp][s], j0, std::true_type());
       }
       __syncwarp();  // every lane has read the stage
-      if (lane == 0) mbar_arrive(&sm.empty[warp][s]);
+      if (!sm.abort) fill();
+      else next = u1;
     }
     // ---- the results: o if the segment is whole, else a piece ----------------------------------------
-    const bool whole = lo == seg.start && hi == seg.start + seg.len;
+    const bool whole = lo == seg.start && hi == seg.end();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -726,38 +682,45 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NT == 1 ? 2 : 1) attn_kerne
       }
     lo = hi;
   }
+  if (sm.abort) {  // a wait gave up: the copies still in flight (at most a few KiB) have landed when the warp leaves
+    nanosleep_ns(1000000);
+  }
 }
 
-// A query row of a segment that lies in several CTAs, or in none: the pieces' results, eight warps taking every eighth.
+// The query rows of the segments that lie in several stretches, or in none: a row to a warp where segments are many (their
+// pieces are few), or to a block, whose warps take every 32nd piece.
 template <class T, int D, int NT>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnParams p, int ctas) {
+__global__ void __launch_bounds__(1024) combine_kernel(const __grid_constant__ AttnParams p, int ctas, int rows) {
   constexpr int kRows = 8 * NT, E = D / 32;
-  __shared__ float so[8][D], sl[8], st[8];
+  __shared__ float so[32][D], sl[32], st[32];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const bool by_block = blockDim.x == 1024;
   const int R = p.group * p.S;
-  const int row = blockIdx.x % R, h = (int)(blockIdx.x / R) % p.c.Hkv, b = (int)(blockIdx.x / R / p.c.Hkv);
+  const int at = by_block ? blockIdx.x : blockIdx.x * (blockDim.x / 32) + warp;
+  const int row = at % R, h = at / R % p.c.Hkv, b = min(at / R / p.c.Hkv, p.B - 1);
   const int rt = row / kRows, hq = h * p.group + row % p.group, i = row / p.group;
+  // where the segment begins, and how many units there are
+  const int blocks = blocks_of(p, b), len = (blocks + 1) / 2;
+  const int per = share(units_before(p, p.B), ctas);
+  const int start = units_before(p, b) + (h * p.n_rt + rt) * len;
+  // No warp leaves before the kernel that writes the pieces has ended: what follows on the stream may rely on both.
+  wait_previous();
+  if (at >= rows) return;
   T* o = static_cast<T*>(p.o) + b * p.so.b + hq * p.so.h + i * p.so.s;
   float* lse = p.lse + ((long long)b * p.Hq + hq) * p.S + i;
-  // every warp walks: where the segment begins, and how many units there are.  No block leaves before the kernel that
-  // writes the pieces has ended: what follows on the stream may rely on both.
-  const int n = p.lens[b], len = units_of(p, b);
   if (len == 0) {
-    wait_previous();
-    const bool empty = n == 0;
-    for (int c = threadIdx.x; c < D; c += 256) o[c] = from_f32<T>(empty ? 0.f : NAN);
-    if (threadIdx.x == 0) *lse = empty ? -INFINITY : NAN;
+    if (by_block && warp) return;
+    const bool empty = p.lens[b] == 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[lane + 32 * e] = from_f32<T>(empty ? 0.f : NAN);
+    if (lane == 0) *lse = empty ? -INFINITY : NAN;
     return;
   }
-  const long long total = units_before(p, p.B);
-  const long long start = units_before(p, b) + (long long)(h * p.n_rt + rt) * len;
-  const long long per = share(total, ctas);
-  const int c0 = (int)(start / per), c1 = (int)((start + len - 1) / per);
-  wait_previous();
+  const int c0 = start / per, c1 = (start + len - 1) / per;
   if (c0 == c1) return;
   float top = kLowest, sum = 0.f, acc[E] = {};
 #pragma unroll 4
-  for (int c = c0 + warp; c <= c1; c += 8) {
+  for (int c = by_block ? c0 + warp : c0; c <= c1; c += by_block ? 32 : 1) {
     const float* part = p.part + ((2ll * c + (c * per >= start ? 0 : 1)) * kRows + row % kRows) * kPart<D>;
     const float mc = part[D], lc = part[D + 1];
     float v[E];
@@ -769,27 +732,31 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + v[e] * w;
   }
+  if (by_block) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][lane + 32 * e] = acc[e];
-  if (lane == 0) {
-    st[warp] = top;
-    sl[warp] = sum;
+    for (int e = 0; e < E; ++e) so[warp][lane + 32 * e] = acc[e];
+    if (lane == 0) {
+      st[warp] = top;
+      sl[warp] = sum;
+    }
+    __syncthreads();
+    if (warp) return;
+    top = warp_max(st[lane]);
+    const float f = ex2_approx(st[lane] - top);
+    sum = sl[lane] * f;
+#pragma unroll
+    for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int w = 0; w < 32; ++w) {
+      const float fw = __shfl_sync(0xffffffffu, f, w);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += so[w][lane + 32 * e] * fw;
+    }
   }
-  __syncthreads();
-  if (threadIdx.x >= D) return;
-  top = st[0];
 #pragma unroll
-  for (int w = 1; w < 8; ++w) top = fmaxf(top, st[w]);
-  float v = 0.f;
-  sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    const float f = ex2_approx(st[w] - top);
-    sum += sl[w] * f;
-    v += so[w][threadIdx.x] * f;
-  }
-  o[threadIdx.x] = from_f32<T>(sum == 0.f ? 0.f : sum != sum ? NAN : v / sum);
-  if (threadIdx.x == 0) *lse = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  for (int e = 0; e < E; ++e) o[lane + 32 * e] = from_f32<T>(sum == 0.f ? 0.f : acc[e] / sum);
+  if (lane == 0) *lse = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -840,18 +807,21 @@ static int launch_attn(AttnParams& p, int dev, int n_sm, cudaStream_t st) {
   const long long R = (long long)p.group * p.S;
   p.n_rt = (int)((R + 8 * NT - 1) / (8 * NT));
   const int ctas = (n_sm < 152 ? n_sm : 152) * (NT == 1 ? 2 : 1);
-  attn_kernel<T, D, NT><<<ctas, (kWarps + 1) * 32, smem, st>>>(p);
+  attn_kernel<T, D, NT><<<ctas, kWarps * 32, smem, st>>>(p);
   if (launch_status() != PSR_OK) return PSR_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.B * p.c.Hkv * R));
-  cfg.blockDim = dim3(256);
+  // up to 2 ctas kWarps pieces lie in the segments: a block to a row while a segment may have more than 16 of them
+  const int rows = (int)(p.B * p.c.Hkv * R);
+  const bool by_block = (long long)p.B * p.c.Hkv * p.n_rt * 16 < (long long)ctas * kWarps;
+  cfg.gridDim = dim3((unsigned)(by_block ? rows : (rows + 7) / 8));
+  cfg.blockDim = dim3(by_block ? 1024 : 256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, combine_kernel<T, D, NT>, p, ctas) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, combine_kernel<T, D, NT>, p, ctas, rows) != cudaSuccess) {
     cudaGetLastError();
     return PSR_ERR_CUDA;
   }
@@ -930,7 +900,9 @@ int psr_kv4_attn(const psr_kv4_shape* sh, const void* q, const psr_strides* qs, 
   if (rc != PSR_OK) return rc;
   if (ws_bytes < psr_kv4_attn_workspace_bytes(sh)) return PSR_ERR_ARG;
   const long long rows = (long long)sh->B * sh->Hq * sh->S;
-  if (rows >= (1LL << 31)) return PSR_ERR_UNSUPPORTED;
+  const long long tiles = ((long long)sh->Hq / sh->Hkv * sh->S + 7) / 8;
+  if (rows >= (1LL << 30) || (double)sh->B * sh->Hkv * tiles * ((double)sh->max_pages * sh->page / kUnit + 1) >= 2147483648.0)
+    return PSR_ERR_UNSUPPORTED;
   int n_sm = 0, dev = 0;
   if ((rc = check_device(&n_sm)) != PSR_OK) return rc;
   if (cudaGetDevice(&dev) != cudaSuccess) return PSR_ERR_CUDA;
