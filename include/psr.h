@@ -478,11 +478,10 @@ PSR_API size_t psr_kv4_attn_workspace_bytes(const psr_kv4_shape* shape);
  * position gets o = 0, lse = -infinity.  A sequence with n < 0, n > max_pages * page, or a page outside the cache
  * among the pages of its n positions gets NaN.  The work is dealt out over the whole batch, so the order of a
  * sequence's sums (not the bound on their rounding) depends on the other lengths; the same call gives the same bits.
- *   workspace: >= psr_kv4_attn_workspace_bytes(shape), 256-byte aligned; not shared by launches in flight;
- *   timeout_ms: bound on every device wait (<= 0: 2000 ms), reported by psr_get_stats. */
+ *   workspace: >= psr_kv4_attn_workspace_bytes(shape), 256-byte aligned; not shared by launches in flight. */
 PSR_API int psr_kv4_attn(const psr_kv4_shape* shape, const void* q, const psr_strides* q_strides, const void* cache,
                          const int32_t* table, const int32_t* lens, void* o, const psr_strides* o_strides, float* lse,
-                         void* workspace, size_t workspace_bytes, int timeout_ms, void* stream);
+                         void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -174,7 +174,7 @@ def load(trace: bool = False, variant: str = "") -> ctypes.CDLL:
         lib.psr_kv4_append.argtypes = [P_kv4, vp, P_st, vp, P_st, vp, vp, vp, vp, vp]
         lib.psr_kv4_read.argtypes = [P_kv4, vp, vp, vp, vp, vp, vp, vp]
         lib.psr_kv4_attn_workspace_bytes.argtypes = [P_kv4]
-        lib.psr_kv4_attn.argtypes = [P_kv4, vp, P_st, vp, vp, vp, vp, P_st, vp, vp, sz, ctypes.c_int, vp]
+        lib.psr_kv4_attn.argtypes = [P_kv4, vp, P_st, vp, vp, vp, vp, P_st, vp, vp, sz, vp]
         for name in ("psr_rotary_table", "psr_rotary", "psr_linear", "psr_linear_bwd", "psr_kv4_append", "psr_kv4_read",
                      "psr_kv4_attn"):
             getattr(lib, name).restype = ctypes.c_int
@@ -872,8 +872,7 @@ def kv4_attn_workspace_bytes(B, Hq, Hkv, S, d, *, page, n_pages, max_pages) -> i
     return int(n)
 
 
-def kv4_attn(q, cache, table, lens, *, Hkv, page, scale=None, out=None, lse=None, workspace=None, timeout_ms=0,
-             stream=None):
+def kv4_attn(q, cache, table, lens, *, Hkv, page, scale=None, out=None, lse=None, workspace=None, stream=None):
     """Attention of the last S positions of each cached sequence over the sequence (S = 1: single tokens).
 
     q: [B, Hq, S, d] bf16 or fp16, any strides with a contiguous last axis; cache, table as in kv4_append; lens: int32
@@ -907,7 +906,7 @@ def kv4_attn(q, cache, table, lens, *, Hkv, page, scale=None, out=None, lse=None
         if B == 0 or S == 0:
             return out, lse, workspace
         rc = lib.psr_kv4_attn(sh, q.data_ptr(), qs, cache.data_ptr(), table.data_ptr(), lens.data_ptr(), out.data_ptr(),
-                              os_, lse.data_ptr(), workspace.data_ptr(), need, int(timeout_ms), at.handle)
+                              os_, lse.data_ptr(), workspace.data_ptr(), need, at.handle)
     if rc != OK:
         raise PsrError(rc, "psr_kv4_attn")
     return out, lse, workspace

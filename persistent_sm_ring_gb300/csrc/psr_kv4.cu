@@ -162,8 +162,8 @@ __global__ void read_kernel(const ReadParams p) {
 // stretches for whole CTAs, whose warps met in shared memory after every segment, batches of short sequences took 3 to 5 us
 // a segment.)
 //
-// Each warp has its own ring of stages, filled with one bulk copy for the two blocks of a unit (two where pages hold one
-// block), and its own softmax state:
+// Each warp has its own ring of stages, filled a unit or more ahead with 16-byte asynchronous copies by all of its lanes, and
+// its own softmax state.  (One lane's bulk copy and barrier took 700 clocks of a unit's 2200 at d = 64.)
 //   S^T[token][row] = K codes . q      (mma.m16n8k16: tokens on its 16 rows, query rows on its 8 columns)
 //   O^T[column][row] += V codes^T . P  (columns of V on the 16 rows, tokens in the contraction)
 // The issue slots are what is scarce (a first version that made 16-bit floats 16 + c of the codes took 485 instructions for
@@ -190,7 +190,6 @@ constexpr int kPart = D + 4;        // floats of a row's partial result: sums, m
 constexpr float kRaise = 8.f;
 constexpr float kLowest = -1e30f;   // a maximum that nothing has raised
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
-enum : uint32_t { SITE_BLOCK = 51 };
 
 struct AttnParams {
   Cache c;
@@ -206,7 +205,6 @@ struct AttnParams {
   int vec_o;                  // o's rows are 16-byte aligned
   float* part;                // [2 kMaxCtas kWarps][rows of a tile][kPart]
   Ctrl* ctrl;
-  unsigned long long timeout_ns;
 };
 
 // Blocks of sequence b: 0 if it is empty or its length is out of range.  Two make a unit.
@@ -309,9 +307,17 @@ template <int D>
 struct AttnSmem {
   static constexpr int kBytes = kBlk * (D + 8);
   alignas(128) uint8_t ring[kWarps][kStages<D>][2 * kBytes];
-  uint64_t full[kWarps][kStages<D>];
-  volatile uint32_t abort;
 };
+
+// 16 bytes, global to shared memory, past L1; groups of them complete in order
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {  // all but the N newest groups of this thread
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 template <class T, int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(const __grid_constant__ AttnParams p) {
@@ -323,15 +329,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
   const int slot = warp * gridDim.x + blockIdx.x;  // neighbouring stretches on different SMs
-  constexpr uint32_t S = kStages<D>;
+  constexpr int S = kStages<D>;
   clear_ctrl(p.ctrl);
   launch_dependents();
-  if (threadIdx.x == 0) sm.abort = 0;
-  if (lane == 0) {
-    for (uint32_t s = 0; s < S; ++s) mbar_init(&sm.full[warp][s], 1);
-    fence_barrier_init();
-  }
-  __syncthreads();
   const int total = units_before(p, p.B), per = share(total, gridDim.x);
   if (slot > (total - 1) / per) return;  // (total 0: slot 0 finds an empty stretch below)
   const int u0 = slot * per, u1 = min(u0 + per, total);
@@ -351,30 +351,33 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
   };
   uint32_t bad = 0;  // bit s: a block of stage s has no page
   auto fill = [&]() {
-    if (next >= u1) return;
-    const uint32_t s = (uint32_t)(next - u0) % S;
-    const bool ok = pg0 >= 0 && pg0 < p.c.n_pages && pg1 >= 0 && pg1 < p.c.n_pages;
-    bad = (bad & ~(1u << s)) | (ok ? 0u : 1u << s);
-    if (lane == 0) {
+    if (next < u1) {
+      const int s = (next - u0) % S;
+      const bool ok = pg0 >= 0 && pg0 < p.c.n_pages && pg1 >= 0 && pg1 < p.c.n_pages;
+      bad = (bad & ~(1u << s)) | (ok ? 0u : 1u << s);
       if (ok) {
-        const bool two = blk + 1 < pre.blocks;
+        constexpr int kChunks = kBytes / 16;  // of a block
+        const int n = blk + 1 < pre.blocks ? 2 * kChunks : kChunks;
         const int in_page = (1 << p.page_shift) - 1;
         auto block = [&](int pg, int b) {
-          return p.c.base + ((((long long)pg * p.c.Hkv + pre.h) << p.page_shift) + (b & in_page)) * kBytes;
+          return p.c.base + ((((long long)pg * p.c.Hkv + pre.h) << p.page_shift) + (b & in_page)) * kBytes + lane * 16;
         };
-        const uint32_t dst = smem_u32(sm.ring[warp][s]);
-        mbar_expect_tx(&sm.full[warp][s], two ? 2 * kBytes : kBytes);
-        bulk_load(dst, block(pg0, blk), two && p.page_shift > 0 ? 2 * kBytes : kBytes, &sm.full[warp][s]);
-        if (two && p.page_shift == 0) bulk_load(dst + kBytes, block(pg1, blk + 1), kBytes, &sm.full[warp][s]);
-      } else {
-        mbar_arrive(&sm.full[warp][s]);
+        const uint8_t* src0 = block(pg0, blk);
+        // the second block, as if it followed the first; it does where a page holds two
+        const uint8_t* src1 = p.page_shift > 0 ? src0 : block(pg1, blk + 1) - kBytes;
+        const uint32_t dst = smem_u32(sm.ring[warp][s]) + lane * 16;
+#pragma unroll
+        for (int i = 0; i < (2 * kChunks + 31) / 32; ++i) {
+          const int c = i * 32 + lane;
+          if (c < n) copy16(dst + i * 512, (c < kChunks ? src0 : src1) + i * 512);
+        }
       }
+      if (++next < u1) look_up();
     }
-    ++next;
-    if (next < u1) look_up();
+    copy_commit();  // a group for every unit, empty or not: they are counted
   };
   look_up();
-  for (uint32_t s = 0; s < S; ++s) fill();
+  for (int s = 0; s < S; ++s) fill();
 
   for (int lo = u0; lo < u1;) {
     seg.advance(p, lo);
@@ -616,9 +619,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
     // ---- the units of the segment --------------------------------------------------------------------
     const int all_see = n - p.S;  // the last position that every row sees
     for (int u = lo; u < hi; ++u) {
-      const uint32_t k = (uint32_t)(u - u0), s = k % S;
-      const bool in = wait_own(&sm.full[warp][s], (k / S) & 1u, p, &sm, SITE_BLOCK);
-      if (!__all_sync(0xffffffffu, in) || (bad >> s & 1u)) {
+      const int s = (u - u0) % S;
+      copy_wait<S - 1>();
+      __syncwarp();  // every lane's copies are there
+      if (bad >> s & 1u) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) l[nt][0] = l[nt][1] = NAN;
       } else {
@@ -627,8 +631,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
         else unit(sm.ring[warp][s], j0, std::true_type());
       }
       __syncwarp();  // every lane has read the stage
-      if (!sm.abort) fill();
-      else next = u1;
+      fill();
     }
     // ---- the results: o if the segment is whole, else a piece ----------------------------------------
     const bool whole = lo == seg.start && hi == seg.end();
@@ -681,9 +684,6 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
         }
       }
     lo = hi;
-  }
-  if (sm.abort) {  // a wait gave up: the copies still in flight (at most a few KiB) have landed when the warp leaves
-    nanosleep_ns(1000000);
   }
 }
 
@@ -891,7 +891,7 @@ size_t psr_kv4_attn_workspace_bytes(const psr_kv4_shape* sh) {
 
 int psr_kv4_attn(const psr_kv4_shape* sh, const void* q, const psr_strides* qs, const void* cache, const int32_t* table,
                  const int32_t* lens, void* o, const psr_strides* os, float* lse, void* workspace, size_t ws_bytes,
-                 int timeout_ms, void* stream) {
+                 void* stream) {
   if (!sh || !q || !qs || !cache || !table || !lens || !o || !os || !lse || !workspace) return PSR_ERR_ARG;
   if (!aligned_to(q, 2) || !aligned_to(o, 2) || !aligned_to(lse, 4) || !aligned_to(cache, 16) ||
       !aligned_to(table, 4) || !aligned_to(lens, 4) || !aligned_to(workspace, 256))
@@ -920,7 +920,6 @@ int psr_kv4_attn(const psr_kv4_shape* sh, const void* q, const psr_strides* qs, 
   p.scale = sh->scale > 0.f ? sh->scale : 1.f / sqrtf((float)sh->d);
   p.ctrl = static_cast<Ctrl*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
-  p.timeout_ns = (unsigned long long)(timeout_ms > 0 ? timeout_ms : 2000) * 1000000ull;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return by_type(sh, [&](auto t, auto d) {
     return tile_rows(sh) == 8 ? launch_attn<decltype(t), decltype(d)::value, 1>(p, dev, n_sm, st)

@@ -180,7 +180,7 @@ def kv4_call(psr, what, shape=None, ws=1 << 30, **over):
     if what == "read":
         return lib.psr_kv4_read(a["sh"], a["cache"], a["table"], a["start"], a["count"], a["k"], a["v"], None)
     return lib.psr_kv4_attn(a["sh"], a["k"], a["ks"], a["cache"], a["table"], a["start"], a["v"], a["vs"], a["lse"], a["wsp"],
-                            ws, 0, None)
+                            ws, None)
 
 
 def test_kv4_refuses(psr):
