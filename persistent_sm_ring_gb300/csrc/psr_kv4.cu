@@ -172,13 +172,12 @@ __global__ void read_kernel(const ReadParams p) {
 //    16 c 2^-24 in bits 4..7, exact, and the matrix product takes it so.  One shift and four masks give eight codes.
 //  * q becomes fp16 for it, scaled by a power of two that puts the tile's largest element below 2^15 (exact for bf16
 //    down to 2^-25 of that); the scales 2^24, 1/16 and that power go to the sums.
-//  * P becomes fp16 times its row's scale: the exponent x + log2(scale) has a running maximum of its own (m + d), so that
-//    no ratio of the scales of different tokens costs P its digits.  Exponents are kept relative to m, where large scores
-//    leave them exact.
+//  * P becomes fp16 times its row's scale, divided by a power of two of its own for each query row, which follows the
+//    largest product of a weight and a scale, so that no ratio of the scales of different tokens costs P its digits.
 //  * any order of the contraction will do, so K and V fragments are read straight from the stage: a lane takes 16 adjacent
 //    bytes of a K row, and the tokens are dealt to the mma's rows so that V's loads fall on different banks; P leaves the
 //    first product in the layout that movmatrix turns into the second one's operand.
-//  * a maximum is only raised when a score passes it by kRaise: the check is one vote, the weights stay below 2^kRaise.
+//  * the maximum and that power are only raised when a weight or a product passes kRaise: the check is one vote.
 constexpr int kWarps = 8;
 template <int D>
 constexpr int kStages = D == 128 ? 2 : 4;
@@ -187,7 +186,7 @@ constexpr int kMinUnits = 4;        // of a warp's stretch: short ones would onl
 constexpr int kMaxCtas = 2 * 152;   // bounds the partial results
 template <int D>
 constexpr int kPart = D + 4;        // floats of a row's partial result: sums, maximum, weight
-constexpr float kRaise = 8.f;
+constexpr float kRaise = 256.f;
 constexpr float kLowest = -1e30f;   // a maximum that nothing has raised
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
@@ -297,7 +296,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 __device__ __forceinline__ float lg2_approx(float x) {
   float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float lo_bf16(uint32_t v) { return __uint_as_float(v << 16); }
@@ -349,6 +348,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
     pg1 = 0;  // not pg0: a copy would wait for its load here
     if (p.page_shift == 0 && blk + 1 < pre.blocks) pg1 = row[blk + 1];
   };
+  const uint8_t* lane_base = p.c.base + lane * 16;
   uint32_t bad = 0;  // bit s: a block of stage s has no page
   auto fill = [&]() {
     if (next < u1) {
@@ -357,10 +357,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
       bad = (bad & ~(1u << s)) | (ok ? 0u : 1u << s);
       if (ok) {
         constexpr int kChunks = kBytes / 16;  // of a block
-        const int n = blk + 1 < pre.blocks ? 2 * kChunks : kChunks;
+        const bool two = blk + 1 < pre.blocks;
         const int in_page = (1 << p.page_shift) - 1;
-        auto block = [&](int pg, int b) {
-          return p.c.base + ((((long long)pg * p.c.Hkv + pre.h) << p.page_shift) + (b & in_page)) * kBytes + lane * 16;
+        auto block = [&](int pg, int b) {  // fewer than 2^31 blocks: checked on the host
+          return lane_base + (unsigned long long)(uint32_t)(((pg * p.c.Hkv + pre.h) << p.page_shift) + (b & in_page)) * kBytes;
         };
         const uint8_t* src0 = block(pg0, blk);
         // the second block, as if it followed the first; it does where a page holds two
@@ -369,7 +369,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
 #pragma unroll
         for (int i = 0; i < (2 * kChunks + 31) / 32; ++i) {
           const int c = i * 32 + lane;
-          if (c < n) copy16(dst + i * 512, (c < kChunks ? src0 : src1) + i * 512);
+          if (c < kChunks) copy16(dst + i * 512, src0 + i * 512);
+          else if (two && c < 2 * kChunks) copy16(dst + i * 512, src1 + i * 512);
         }
       }
       if (++next < u1) look_up();
@@ -448,13 +449,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
       }
     }
     const float kscale = p.scale * kLog2e * 16777216.f / up;
-    float acc[NT][D / 16][4], m[NT][2], d[NT][2], l[NT][2], corr[NT][2];
+    float acc[NT][D / 16][4], m[NT][2], di[NT][2], l[NT][2], corr[NT][2];
     bool fresh = true;  // no unit yet: the first one sets the maxima (a row that sees nothing of it sees nothing later)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
-      m[nt][0] = m[nt][1] = d[nt][0] = d[nt][1] = 0.f;
+      m[nt][0] = m[nt][1] = 0.f;
+      di[nt][0] = di[nt][1] = 1.f;
       l[nt][0] = l[nt][1] = corr[nt][0] = corr[nt][1] = 0.f;
     }
     // one unit: MASKED where some row does not see all of its tokens
@@ -494,61 +496,57 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
           }
         }
       }
-      // x: scores in powers of two above m; y: with V's scale, above m + d
-      float y[NT][8], vo[4], tx[NT][2], ty[NT][2];
-      auto pair_of = [&](int b, int h, int kv) {
-        return reinterpret_cast<const uint32_t*>(stage + b * kBytes + kBlk * D)[kv * 16 + tok + 8 * h];
+      // x: scores in powers of two above m; w: weights; y: weights times V's scale, in units of 1 / di
+      float w[NT][8], y[NT][8], vo[4], top = 0.f;
+      auto pair_of = [&](int i, int kv) {  // of the lane's token i (block, half)
+        return reinterpret_cast<const uint32_t*>(stage + i / 2 * kBytes + kBlk * D)[kv * 16 + tok + 8 * (i % 2)];
       };
-      bool raise = fresh;
+      auto unseen = [&](int i, int nt, int c) { return MASKED && j0 + 16 * (i / 2) + 8 * (i % 2) + tok > last[nt][c]; };
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t kp = pair_of(b, h, 0), vp = pair_of(b, h, 1);
-          const float ks = lo_bf16(kp) * kscale, ko = hi_bf16(kp), lv = lg2_approx(lo_bf16(vp));
-          vo[2 * b + h] = hi_bf16(vp);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int e = 4 * b + 2 * h + c;
-              x[nt][e] = fmaf(ks, x[nt][e], fmaf(ko, qsum[nt][c], -m[nt][c]));
-              y[nt][e] = x[nt][e] + (lv - d[nt][c]);
-              if (MASKED && j0 + 16 * b + 8 * h + tok > last[nt][c])  // such a row may hold anything
-                x[nt][e] = y[nt][e] = -INFINITY;
-            }
-        }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          tx[nt][c] = fmax3(fmaxf(x[nt][c], x[nt][2 + c]), x[nt][4 + c], x[nt][6 + c]);
-          ty[nt][c] = fmax3(fmaxf(y[nt][c], y[nt][2 + c]), y[nt][4 + c], y[nt][6 + c]);
-          raise = raise || tx[nt][c] > kRaise || ty[nt][c] > kRaise;
-        }
-      if (__any_sync(0xffffffffu, raise)) {
-        float lv[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) lv[i] = lg2_approx(lo_bf16(pair_of(i / 2, i % 2, 1)));
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t kp = pair_of(i, 0), vp = pair_of(i, 1);
+        const float ks = lo_bf16(kp) * kscale, ko = hi_bf16(kp), vs = lo_bf16(vp);
+        vo[i] = hi_bf16(vp);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float a = tx[nt][c], b = -INFINITY;
+            const int e = 2 * i + c;
+            x[nt][e] = fmaf(ks, x[nt][e], fmaf(ko, qsum[nt][c], -m[nt][c]));
+            if (unseen(i, nt, c)) x[nt][e] = -INFINITY;  // such a row may hold anything
+            w[nt][e] = ex2_approx(x[nt][e]);
+            y[nt][e] = unseen(i, nt, c) ? 0.f : w[nt][e] * (vs * di[nt][c]);
+          }
+      }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (x[nt][2 * i + c] != -INFINITY) b = fmaxf(b, x[nt][2 * i + c] + lv[i]);
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmax3(top, w[nt][e], y[nt][e]);
+      if (__any_sync(0xffffffffu, fresh || top > kRaise)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float a = -INFINITY, b = -INFINITY;  // largest score, largest exponent of a product
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (unseen(i, nt, c)) continue;
+              a = fmaxf(a, x[nt][2 * i + c]);
+              b = fmaxf(b, x[nt][2 * i + c] + lg2_approx(lo_bf16(pair_of(i, 1))));
+            }
 #pragma unroll
             for (int o = 4; o < 32; o *= 2) {
               a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
               b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
             }
             const float up = a == -INFINITY ? 0.f : fresh ? a : fmaxf(a, 0.f);
-            const float old = fresh ? kLowest : d[nt][c] - up;
-            const float fa = ex2_approx(-up), nd = fmaxf(old, b - up), fb = ex2_approx(old - nd);
+            // the power of two, from 2^-126 to 2^126: at least the largest product so far, and at least the old one
+            const float old = fresh ? -126.f : 127.f - (float)(__float_as_uint(di[nt][c]) >> 23) - up;
+            const float nd = fminf(fmaxf(fmaxf(old, -126.f), ceilf(b - up)), 126.f);
             m[nt][c] += up;
-            d[nt][c] = nd;
+            di[nt][c] = __uint_as_float((uint32_t)(127 - (int)ceilf(nd)) << 23);
             if (!fresh) {
+              const float fa = ex2_approx(-up), fb = ex2_approx(old - ceilf(nd));
               l[nt][c] *= fa;
               corr[nt][c] *= fa;
 #pragma unroll
@@ -560,9 +558,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int e = 2 * i + c;
-              if (MASKED && x[nt][e] == -INFINITY) continue;
-              x[nt][e] -= up;
-              y[nt][e] = x[nt][e] + (lv[i] - nd);
+              if (unseen(i, nt, c)) continue;
+              w[nt][e] = ex2_approx(x[nt][e] - up);
+              y[nt][e] = w[nt][e] * (lo_bf16(pair_of(i, 1)) * di[nt][c]);
             }
           }
         fresh = false;
@@ -588,30 +586,27 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float w[2], wo[2];
+            const int i = 2 * b + h;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const int e = 4 * b + 2 * h + c;
-              w[c] = ex2_approx(x[nt][e]);
-              wo[c] = ex2_approx(y[nt][e]);
-              l[nt][c] += w[c];
-              if (!MASKED || x[nt][e] != -INFINITY) corr[nt][c] = fmaf(w[c], vo[2 * b + h], corr[nt][c]);
+              l[nt][c] += w[nt][2 * i + c];
+              if (!unseen(i, nt, c)) corr[nt][c] = fmaf(w[nt][2 * i + c], vo[i], corr[nt][c]);
             }
-            pb[nt][h] = transpose8x8(pack_f16x2(wo[0], wo[1]));
+            pb[nt][h] = transpose8x8(pack_f16x2(y[nt][2 * i], y[nt][2 * i + 1]));
           }
 #pragma unroll
-        for (int w = 0; w < VW; ++w) {
-          const uint32_t l01 = __byte_perm(va[0][w], va[1][w], 0x5410), h01 = __byte_perm(va[0][w], va[1][w], 0x7632);
-          const uint32_t l23 = __byte_perm(va[2][w], va[3][w], 0x5410), h23 = __byte_perm(va[2][w], va[3][w], 0x7632);
+        for (int q = 0; q < VW; ++q) {
+          const uint32_t l01 = __byte_perm(va[0][q], va[1][q], 0x5410), h01 = __byte_perm(va[0][q], va[1][q], 0x7632);
+          const uint32_t l23 = __byte_perm(va[2][q], va[3][q], 0x5410), h23 = __byte_perm(va[2][q], va[3][q], 0x7632);
           const uint32_t l01s = l01 >> 8, h01s = h01 >> 8, l23s = l23 >> 8, h23s = h23 >> 8;
           constexpr uint32_t L = 0x000F000Fu, H = 0x00F000F0u;
-          // columns 8 w + 0 .. 7 of the lane's: two to an mma, the even one on row g, the odd one, 16 times too high, on g + 8
+          // columns 8 q + 0 .. 7 of the lane's: two to an mma, the even one on row g, the odd one, 16 times too high, on g + 8
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma_f16(acc[nt][4 * w], l01 & L, l01 & H, l23 & L, l23 & H, pb[nt][0], pb[nt][1]);
-            mma_f16(acc[nt][4 * w + 1], l01s & L, l01s & H, l23s & L, l23s & H, pb[nt][0], pb[nt][1]);
-            mma_f16(acc[nt][4 * w + 2], h01 & L, h01 & H, h23 & L, h23 & H, pb[nt][0], pb[nt][1]);
-            mma_f16(acc[nt][4 * w + 3], h01s & L, h01s & H, h23s & L, h23s & H, pb[nt][0], pb[nt][1]);
+            mma_f16(acc[nt][4 * q], l01 & L, l01 & H, l23 & L, l23 & H, pb[nt][0], pb[nt][1]);
+            mma_f16(acc[nt][4 * q + 1], l01s & L, l01s & H, l23s & L, l23s & H, pb[nt][0], pb[nt][1]);
+            mma_f16(acc[nt][4 * q + 2], h01 & L, h01 & H, h23 & L, h23 & H, pb[nt][0], pb[nt][1]);
+            mma_f16(acc[nt][4 * q + 3], h01s & L, h01s & H, h23s & L, h23s & H, pb[nt][0], pb[nt][1]);
           }
         }
       }
@@ -647,7 +642,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
         }
         const int row = nt * 8 + 2 * t + c, r = seg.rt * kRows + row;
         if (r >= R) continue;
-        const float fo = ex2_approx(d[nt][c]);
+        const float fo = 1.f / di[nt][c];
         float v[D / 8];  // the lane's columns, from g D / 8 on
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
@@ -767,6 +762,7 @@ static int check_shape(const psr_kv4_shape* sh) {
   if (sh->B < 0 || sh->S < 0 || sh->Hq < 1 || sh->Hkv < 1 || sh->n_pages < 1 || sh->max_pages < 1) return PSR_ERR_ARG;
   if (sh->type != PSR_BF16 && sh->type != PSR_F16) return PSR_ERR_ARG;
   if (sh->Hq % sh->Hkv != 0 || (sh->d != 64 && sh->d != 128)) return PSR_ERR_UNSUPPORTED;
+  if ((double)sh->n_pages * sh->Hkv * sh->page / 16 >= 2147483648.0) return PSR_ERR_UNSUPPORTED;
   if (sh->page < 16 || sh->page > 256 || (sh->page & (sh->page - 1)) != 0) return PSR_ERR_UNSUPPORTED;
   if ((long long)sh->max_pages * sh->page >= (1LL << 31)) return PSR_ERR_UNSUPPORTED;
   return PSR_OK;
