@@ -46,108 +46,142 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Append: one warp quantises one row of K or V
+// Append and read
 // ------------------------------------------------------------------------------------------------
-struct AppendParams {
+// Memory bound.  D / 8 lanes take a row, eight columns (16 bytes) each; a block takes kTokens tokens of one sequence and KV
+// head, and a lane the K and V rows of two of them, so that four loads are in flight.
+template <int D>
+struct Rows {
+  static constexpr int kLanes = D / 8;           // of a row
+  static constexpr int kTokens = 2 * 256 / kLanes;  // of a block
+};
+
+struct MoveParams {
   Cache c;
-  const void* x[2];
-  psr_strides st[2];
+  const void* in[2];  // append
+  void* out[2];       // read
+  psr_strides st[2];  // of `in`
   const int32_t *start, *count;
-  int B, S;
+  int S, tiles;       // rows, blocks of a sequence and head
+  int vec;            // `in`'s rows are 16-byte aligned
+};
+
+template <class T>
+struct alignas(16) Eight {
+  T e[8];
 };
 
 template <class T, int D>
-__global__ void append_kernel(const AppendParams p) {
-  constexpr int E = D / 32;  // elements a lane, adjacent columns
-  const int lane = threadIdx.x % 32;
-  const long long rows = 2LL * p.B * p.c.Hkv * p.S;
-  for (long long r = (blockIdx.x * (long long)blockDim.x + threadIdx.x) / 32; r < rows;
-       r += (long long)gridDim.x * blockDim.x / 32) {
-    const int kv = (int)(r & 1);
-    long long t = r >> 1;
-    const int i = (int)(t % p.S);
-    t /= p.S;
-    const int h = (int)(t % p.c.Hkv), b = (int)(t / p.c.Hkv);
-    if (p.count && i >= p.count[b]) continue;
-    const long long pos = (long long)p.start[b] + i;
-    uint8_t* blk = block_of(p.c, b, h, pos);
-    if (!blk) continue;
-    const T* x = static_cast<const T*>(p.x[kv]) + b * p.st[kv].b + h * p.st[kv].h + i * p.st[kv].s;
-    float v[E];
-    bool fine = true;
-    float mn = INFINITY, mx = -INFINITY;
+__global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ MoveParams p) {
+  using R = Rows<D>;
+  const int bh = blockIdx.x / p.tiles, b = bh / p.c.Hkv, h = bh - b * p.c.Hkv;
+  const int part = threadIdx.x % R::kLanes;
+  const int first = (blockIdx.x - bh * p.tiles) * R::kTokens + threadIdx.x / R::kLanes;
+  const int end = p.count ? min(p.S, p.count[b]) : p.S;
+  const long long start = p.start[b];
+  uint8_t* blk[2];
+  Eight<T> raw[2][2];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      v[e] = to_f32(x[lane * E + e]);
-      fine = fine && isfinite(v[e]);
-      mn = fminf(mn, v[e]);
-      mx = fmaxf(mx, v[e]);
-    }
-    mn = warp_min(mn);
-    mx = warp_max(mx);
-    fine = __all_sync(0xffffffffu, fine);
-    // max/15 - min/15: max - min can pass the largest fp32 number
-    __nv_bfloat16 sc = __float2bfloat16_rn(__fsub_rn(__fdiv_rn(mx, 15.f), __fdiv_rn(mn, 15.f)));
-    __nv_bfloat16 of = __float2bfloat16_rn(mn);
-    const float s = __bfloat162float(sc), o = __bfloat162float(of);
-    uint32_t codes = 0;
+  for (int n = 0; n < 2; ++n) {
+    const int i = first + n * (R::kTokens / 2);
+    blk[n] = i < end ? block_of(p.c, b, h, start + i) : nullptr;
+    if (!blk[n]) continue;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(v[e], o), s)), 0.f), 15.f);
-      if (fine && s > 0.f) codes |= (uint32_t)c << (4 * e);
+    for (int kv = 0; kv < 2; ++kv) {
+      const T* x = static_cast<const T*>(p.in[kv]) + b * p.st[kv].b + h * p.st[kv].h + i * p.st[kv].s + part * 8;
+      if (p.vec) raw[n][kv] = *reinterpret_cast<const Eight<T>*>(x);
+      else
+#pragma unroll
+        for (int e = 0; e < 8; ++e) raw[n][kv].e[e] = x[e];
     }
-    if (!fine) sc = of = __ushort_as_bfloat16(0x7FFF);
-    const int row = (int)(pos % kBlk);
-    uint8_t* dst = blk + kv * kBlk * (D / 2) + row * (D / 2) + lane * (E / 2);
-    if constexpr (E == 4) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)codes;
-    else *dst = (uint8_t)codes;
-    if (lane == 0) {
-      __nv_bfloat162 pair;
-      pair.x = sc;
-      pair.y = of;
-      *reinterpret_cast<__nv_bfloat162*>(blk + kBlk * D + kv * kBlk * 4 + row * 4) = pair;
+  }
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const int row = (int)((start + first + n * (R::kTokens / 2)) & (kBlk - 1));
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      float v[8], mn = INFINITY, mx = -INFINITY, big = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = blk[n] ? to_f32(raw[n][kv].e[e]) : 0.f;
+        mn = fminf(mn, v[e]);
+        mx = fmaxf(mx, v[e]);
+        big = v[e] - v[e] != 0.f ? 1.f : big;  // an infinity or a NaN
+      }
+#pragma unroll
+      for (int o = R::kLanes / 2; o; o >>= 1) {
+        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      }
+      if (!blk[n]) continue;
+      const bool fine = big == 0.f;
+      // max/15 - min/15: max - min can pass the largest fp32 number
+      __nv_bfloat16 sc = __float2bfloat16_rn(__fsub_rn(__fdiv_rn(mx, 15.f), __fdiv_rn(mn, 15.f)));
+      __nv_bfloat16 of = __float2bfloat16_rn(mn);
+      const float s = __bfloat162float(sc), o = __bfloat162float(of);
+      uint32_t codes = 0;
+      if (fine && s > 0.f) {
+        // The code is the rounded quotient rounded to an integer.  A product with the reciprocal is within 2^-21 of a
+        // quotient below 16, so only one that close to a half needs the division (and one whose reciprocal overflows).
+        const float inv = __fdividef(1.f, s);
+        const bool plain = s > 1e-37f && s < 1e37f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = __fsub_rn(v[e], o);
+          float q = x * inv;
+          if (!plain || fabsf(q - floorf(q) - 0.5f) < 1e-4f) q = __fdiv_rn(x, s);
+          codes |= (uint32_t)fminf(fmaxf(rintf(q), 0.f), 15.f) << (4 * e);
+        }
+      }
+      if (!fine) sc = of = __ushort_as_bfloat16(0x7FFF);
+      *reinterpret_cast<uint32_t*>(blk[n] + kv * kBlk * (D / 2) + row * (D / 2) + part * 4) = codes;
+      if (part == 0) {
+        __nv_bfloat162 pair;
+        pair.x = sc;
+        pair.y = of;
+        *reinterpret_cast<__nv_bfloat162*>(blk[n] + kBlk * D + kv * kBlk * 4 + row * 4) = pair;
+      }
     }
   }
 }
 
-// ------------------------------------------------------------------------------------------------
-// Read: one warp dequantises one row of K or V
-// ------------------------------------------------------------------------------------------------
-struct ReadParams {
-  Cache c;
-  void* x[2];
-  const int32_t *start, *count;
-  int B, S;
-};
-
 template <class T, int D>
-__global__ void read_kernel(const ReadParams p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x % 32;
-  const long long rows = 2LL * p.B * p.c.Hkv * p.S;
-  for (long long r = (blockIdx.x * (long long)blockDim.x + threadIdx.x) / 32; r < rows;
-       r += (long long)gridDim.x * blockDim.x / 32) {
-    const int kv = (int)(r & 1);
-    const long long t = r >> 1;
-    const int i = (int)(t % p.S);
-    const int h = (int)(t / p.S % p.c.Hkv), b = (int)(t / p.S / p.c.Hkv);
-    T* x = static_cast<T*>(p.x[kv]) + t * D + lane * E;
-    const bool live = !p.count || i < p.count[b];
-    const long long pos = (long long)p.start[b] + i;
-    const uint8_t* blk = live ? block_of(p.c, b, h, pos) : nullptr;
-    float s = 0.f, o = live ? NAN : 0.f;
-    uint32_t codes = 0;
-    if (blk) {
-      const int row = (int)(pos % kBlk);
-      const __nv_bfloat162 pair = *reinterpret_cast<const __nv_bfloat162*>(blk + kBlk * D + kv * kBlk * 4 + row * 4);
-      s = __bfloat162float(pair.x);
-      o = __bfloat162float(pair.y);
-      const uint8_t* src = blk + kv * kBlk * (D / 2) + row * (D / 2) + lane * (E / 2);
-      if constexpr (E == 4) codes = *reinterpret_cast<const uint16_t*>(src);
-      else codes = *src;
-    }
+__global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ MoveParams p) {
+  using R = Rows<D>;
+  const int bh = blockIdx.x / p.tiles, b = bh / p.c.Hkv, h = bh - b * p.c.Hkv;
+  const int part = threadIdx.x % R::kLanes;
+  const int first = (blockIdx.x - bh * p.tiles) * R::kTokens + threadIdx.x / R::kLanes;
+  const int end = p.count ? min(p.S, p.count[b]) : p.S;
+  const long long start = p.start[b];
+  uint32_t codes[2][2] = {};
+  float s[2][2], o[2][2];
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = from_f32<T>(fmaf((float)((codes >> (4 * e)) & 15u), s, o));
+  for (int n = 0; n < 2; ++n) {
+    const int i = first + n * (R::kTokens / 2), row = (int)((start + i) & (kBlk - 1));
+    const uint8_t* blk = i < end ? block_of(p.c, b, h, start + i) : nullptr;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      s[n][kv] = 0.f;
+      o[n][kv] = i < end ? NAN : 0.f;
+      if (!blk) continue;
+      codes[n][kv] = *reinterpret_cast<const uint32_t*>(blk + kv * kBlk * (D / 2) + row * (D / 2) + part * 4);
+      const __nv_bfloat162 pair = *reinterpret_cast<const __nv_bfloat162*>(blk + kBlk * D + kv * kBlk * 4 + row * 4);
+      s[n][kv] = __bfloat162float(pair.x);
+      o[n][kv] = __bfloat162float(pair.y);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const int i = first + n * (R::kTokens / 2);
+    if (i >= p.S) continue;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      Eight<T> w;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w.e[e] = from_f32<T>(fmaf((float)((codes[n][kv] >> (4 * e)) & 15u), s[n][kv], o[n][kv]));
+      *reinterpret_cast<Eight<T>*>(static_cast<T*>(p.out[kv]) + ((long long)bh * p.S + i) * D + part * 8) = w;
+    }
   }
 }
 
@@ -656,10 +690,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
           if (p.vec_o) {
 #pragma unroll
             for (int q = 0; q < D / 64; ++q) {
-              struct alignas(16) Eight { T e[8]; } w;
+              Eight<T> w;
 #pragma unroll
               for (int e = 0; e < 8; ++e) w.e[e] = from_f32<T>(sum == 0.f ? 0.f : v[q * 8 + e] * inv);
-              *reinterpret_cast<Eight*>(out + q * 8) = w;
+              *reinterpret_cast<Eight<T>*>(out + q * 8) = w;
             }
           } else {
 #pragma unroll
@@ -824,10 +858,19 @@ static int launch_attn(AttnParams& p, int dev, int n_sm, cudaStream_t st) {
   return PSR_OK;
 }
 
-static unsigned row_blocks(const psr_kv4_shape* sh, int n_sm) {
-  const long long rows = 2LL * sh->B * sh->Hkv * sh->S;
-  const long long blocks = (rows + 7) / 8;
-  return (unsigned)(blocks < n_sm * 32 ? blocks : n_sm * 32);
+// Blocks of an append or a read; 0 if there are too many.
+static unsigned move_blocks(const psr_kv4_shape* sh, MoveParams& p) {
+  const int tokens = sh->d == 64 ? Rows<64>::kTokens : Rows<128>::kTokens;
+  p.S = sh->S;
+  p.tiles = (sh->S + tokens - 1) / tokens;
+  const double n = (double)sh->B * sh->Hkv * p.tiles;
+  return n < 2147483648.0 ? (unsigned)(sh->B * sh->Hkv * p.tiles) : 0u;
+}
+
+// Every row of a strided tensor starts on a 16-byte boundary.
+static bool rows_aligned(const void* x, const psr_strides* st, int B, int H, int S) {
+  auto even = [](long long stride, int n) { return n <= 1 || stride % 8 == 0; };
+  return aligned_to(x, 16) && even(st->b, B) && even(st->h, H) && even(st->s, S);
 }
 
 }  // namespace kv4
@@ -851,12 +894,18 @@ int psr_kv4_append(const psr_kv4_shape* sh, const void* k, const psr_strides* ks
     return PSR_ERR_ARG;
   int rc = check_shape(sh);
   if (rc != PSR_OK) return rc;
-  int n_sm = 0;
-  if ((rc = check_device(&n_sm)) != PSR_OK) return rc;
+  if ((rc = check_device(nullptr)) != PSR_OK) return rc;
   if (sh->B == 0 || sh->S == 0) return PSR_OK;
-  AppendParams p = {cache_of(sh, cache, table), {k, v}, {*ks, *vs}, start, count, sh->B, sh->S};
+  MoveParams p = {};
+  p.c = cache_of(sh, cache, table);
+  p.in[0] = k; p.in[1] = v;
+  p.st[0] = *ks; p.st[1] = *vs;
+  p.start = start; p.count = count;
+  p.vec = rows_aligned(k, ks, sh->B, sh->Hkv, sh->S) && rows_aligned(v, vs, sh->B, sh->Hkv, sh->S);
+  const unsigned blocks = move_blocks(sh, p);
+  if (!blocks) return PSR_ERR_UNSUPPORTED;
   return by_type(sh, [&](auto t, auto d) {
-    append_kernel<decltype(t), decltype(d)::value><<<row_blocks(sh, n_sm), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    append_kernel<decltype(t), decltype(d)::value><<<blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
     return launch_status();
   });
 }
@@ -869,12 +918,16 @@ int psr_kv4_read(const psr_kv4_shape* sh, const void* cache, const int32_t* tabl
     return PSR_ERR_ARG;
   int rc = check_shape(sh);
   if (rc != PSR_OK) return rc;
-  int n_sm = 0;
-  if ((rc = check_device(&n_sm)) != PSR_OK) return rc;
+  if ((rc = check_device(nullptr)) != PSR_OK) return rc;
   if (sh->B == 0 || sh->S == 0) return PSR_OK;
-  ReadParams p = {cache_of(sh, cache, table), {k, v}, start, count, sh->B, sh->S};
+  MoveParams p = {};
+  p.c = cache_of(sh, cache, table);
+  p.out[0] = k; p.out[1] = v;
+  p.start = start; p.count = count;
+  const unsigned blocks = move_blocks(sh, p);
+  if (!blocks) return PSR_ERR_UNSUPPORTED;
   return by_type(sh, [&](auto t, auto d) {
-    read_kernel<decltype(t), decltype(d)::value><<<row_blocks(sh, n_sm), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    read_kernel<decltype(t), decltype(d)::value><<<blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
     return launch_status();
   });
 }
@@ -910,9 +963,8 @@ int psr_kv4_attn(const psr_kv4_shape* sh, const void* q, const psr_strides* qs, 
   p.B = sh->B; p.Hq = sh->Hq; p.S = sh->S;
   p.group = sh->Hq / sh->Hkv;
   for (int n = sh->page / kBlk; n > 1; n /= 2) ++p.page_shift;
-  auto even = [](long long stride, int n) { return n <= 1 || stride % 8 == 0; };
-  p.vec = aligned_to(q, 16) && even(qs->b, sh->B) && even(qs->h, sh->Hq) && even(qs->s, sh->S);
-  p.vec_o = aligned_to(o, 16) && even(os->b, sh->B) && even(os->h, sh->Hq) && even(os->s, sh->S);
+  p.vec = rows_aligned(q, qs, sh->B, sh->Hq, sh->S);
+  p.vec_o = rows_aligned(o, os, sh->B, sh->Hq, sh->S);
   p.scale = sh->scale > 0.f ? sh->scale : 1.f / sqrtf((float)sh->d);
   p.ctrl = static_cast<Ctrl*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);

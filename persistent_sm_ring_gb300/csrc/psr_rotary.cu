@@ -25,6 +25,7 @@ struct Params {
   int B, Hq, Hkv, S, d, rot;
   int half;  // rows of a half-chunk of load-balanced shards (S / (2P)), 0: rows are in order
   int P;
+  int chunk;  // heads that a thread goes through
   float amplitude, sign;
 };
 
@@ -47,43 +48,108 @@ __device__ __forceinline__ void turn(const Params& p, long long pos, uint64_t fr
   s *= p.sign * p.amplitude;
 }
 
-template <class T, bool INTER>
-__global__ void rotary_kernel(const Params p) {
-  const int units = p.rot / 2 + (p.d - p.rot);  // pairs, then copied columns
-  const int H = p.Hq + p.Hkv;
-  const long long n = (long long)p.B * p.S * H * units;
-  for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
-    const int u = (int)(i % units);
-    long long r = i / units;
-    const int h = (int)(r % H);
-    r /= H;
-    const int s = (int)(r % p.S), b = (int)(r / p.S);
-    const Operand& o = h < p.Hq ? p.q : p.k;
-    const int hh = h < p.Hq ? h : h - p.Hq;
-    const T* x = static_cast<const T*>(o.in) + b * o.si.b + hh * o.si.h + s * o.si.s;
-    T* y = static_cast<T*>(o.out) + b * o.so.b + hh * o.so.h + s * o.so.s;
-    if (u >= p.rot / 2) {
-      const int c = p.rot / 2 + u;
-      y[c] = x[c];
-      continue;
+// Memory bound: every element is read and written once.  A thread takes V pairs of a row (two vectors of V elements, 16 bytes
+// each where the layout allows it) or V copied columns, computes their cosines and sines once, and goes through the heads
+// of its chunk with kAhead of them in flight.
+constexpr int kAhead = 4;
+
+template <class T, bool INTER, int V>
+__global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ Params p) {
+  struct alignas(sizeof(T) * V) Vec { T e[V]; };
+  const int pairs = p.rot / 2 / V, units = pairs + (p.d - p.rot) / V;
+  const long long i = blockIdx.x * 256ll + threadIdx.x, rows = (long long)p.B * p.S;
+  const long long r = i / units;
+  if (r >= rows) return;
+  const int u = (int)(i - r * units), b = (int)(r / p.S), s = (int)(r - (long long)b * p.S);
+  const int h0 = blockIdx.y * p.chunk, h1 = min(h0 + p.chunk, p.Hq + p.Hkv);
+  const bool turned = u < pairs;
+  const int c1 = !turned ? p.rot + (u - pairs) * V : INTER ? 2 * V * u : V * u;
+  const int c2 = INTER ? c1 + V : c1 + p.rot / 2;
+  float cs[V], sn[V];
+  if (turned) {
+    const long long pos = position(p, b, s);
+#pragma unroll
+    for (int e = 0; e < V; ++e) turn(p, pos, p.table[u * V + e], cs[e], sn[e]);
+  }
+  auto at = [&](int h, bool out) -> T* {
+    const bool q = h < p.Hq;
+    const Operand& o = q ? p.q : p.k;
+    const psr_strides& st = out ? o.so : o.si;
+    return static_cast<T*>(const_cast<void*>(out ? o.out : o.in)) + b * st.b + (q ? h : h - p.Hq) * st.h + s * st.s;
+  };
+  for (int h = h0; h < h1; h += kAhead) {
+    Vec x1[kAhead], x2[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      if (h + a >= h1) break;
+      const T* x = at(h + a, false);
+      x1[a] = *reinterpret_cast<const Vec*>(x + c1);
+      if (turned) x2[a] = *reinterpret_cast<const Vec*>(x + c2);
     }
-    const int c1 = INTER ? 2 * u : u, c2 = INTER ? 2 * u + 1 : u + p.rot / 2;
-    float cs, sn;
-    turn(p, position(p, b, s), p.table[u], cs, sn);
-    const float x1 = to_f32(x[c1]), x2 = to_f32(x[c2]);
-    y[c1] = from_f32<T>(x1 * cs - x2 * sn);
-    y[c2] = from_f32<T>(x2 * cs + x1 * sn);
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      if (h + a >= h1) break;
+      T* y = at(h + a, true);
+      if (!turned) {
+        *reinterpret_cast<Vec*>(y + c1) = x1[a];
+        continue;
+      }
+      Vec y1, y2;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        // pair e: element e of either vector, or elements 2e and 2e + 1 of the two taken as one
+        const float f1 = to_f32(!INTER ? x1[a].e[e] : 2 * e < V ? x1[a].e[2 * e % V] : x2[a].e[2 * e % V]);
+        const float f2 = to_f32(!INTER ? x2[a].e[e] : 2 * e + 1 < V ? x1[a].e[(2 * e + 1) % V] : x2[a].e[(2 * e + 1) % V]);
+        const T g1 = from_f32<T>(f1 * cs[e] - f2 * sn[e]), g2 = from_f32<T>(f2 * cs[e] + f1 * sn[e]);
+        if (!INTER) {
+          y1.e[e] = g1;
+          y2.e[e] = g2;
+        } else {
+          (2 * e < V ? y1 : y2).e[2 * e % V] = g1;
+          (2 * e + 1 < V ? y1 : y2).e[(2 * e + 1) % V] = g2;
+        }
+      }
+      *reinterpret_cast<Vec*>(y + c1) = y1;
+      *reinterpret_cast<Vec*>(y + c2) = y2;
+    }
   }
 }
 
-template <class T>
-static int launch(const Params& p, bool inter, int n_sm, cudaStream_t st) {
-  const long long n = (long long)p.B * p.S * (p.Hq + p.Hkv) * (p.rot / 2 + (p.d - p.rot));
-  long long blocks = (n + 255) / 256;
-  if (blocks > n_sm * 64) blocks = n_sm * 64;
-  if (inter) rotary_kernel<T, true><<<(unsigned)blocks, 256, 0, st>>>(p);
-  else rotary_kernel<T, false><<<(unsigned)blocks, 256, 0, st>>>(p);
+template <class T, bool INTER, int V>
+static int launch_v(Params& p, int n_sm, cudaStream_t st) {
+  const long long threads = (long long)p.B * p.S * (p.rot / 2 / V + (p.d - p.rot) / V), blocks = (threads + 255) / 256;
+  const int H = p.Hq + p.Hkv;
+  // a chunk of heads shares the cosines and sines; shorter ones where there are few rows
+  p.chunk = 16;
+  while (p.chunk > 1 && blocks * ((H + p.chunk - 1) / p.chunk) < 8 * n_sm) p.chunk /= 2;
+  const int chunks = (H + p.chunk - 1) / p.chunk;
+  if (blocks >= (1ll << 31) || chunks > 65535) return PSR_ERR_UNSUPPORTED;
+  rotary_kernel<T, INTER, V><<<dim3((unsigned)blocks, (unsigned)chunks), 256, 0, st>>>(p);
   return launch_status();
+}
+
+template <class T, bool INTER>
+static int launch_t(Params& p, int n_sm, cudaStream_t st) {
+  // the longest vectors that every row, column group and pair of column groups starts on a boundary of
+  auto fits = [&](int v) {
+    auto even = [&](const Operand& o, int H) {
+      for (const psr_strides* t : {&o.si, &o.so})
+        if ((p.B > 1 && t->b % v) || (H > 1 && t->h % v) || (p.S > 1 && t->s % v)) return false;
+      return aligned_to(o.in, v * sizeof(T)) && aligned_to(o.out, v * sizeof(T));
+    };
+    return (INTER ? p.rot % (2 * v) == 0 : p.rot / 2 % v == 0) && (p.d - p.rot) % v == 0 && even(p.q, p.Hq) &&
+           (p.Hkv == 0 || even(p.k, p.Hkv));
+  };
+  constexpr int kMost = 16 / sizeof(T);
+  if (fits(kMost)) return launch_v<T, INTER, kMost>(p, n_sm, st);
+  if (kMost > 4 && fits(4)) return launch_v<T, INTER, kMost < 4 ? kMost : 4>(p, n_sm, st);
+  if (fits(2)) return launch_v<T, INTER, 2>(p, n_sm, st);
+  return launch_v<T, INTER, 1>(p, n_sm, st);
+}
+
+template <class T>
+static int launch(Params& p, bool inter, int n_sm, cudaStream_t st) {
+  return inter ? launch_t<T, true>(p, n_sm, st) : launch_t<T, false>(p, n_sm, st);
 }
 
 }  // namespace rotary
