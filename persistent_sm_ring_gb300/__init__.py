@@ -469,29 +469,27 @@ def gemm_rs(a, w, *, partition=None, workspace=None, out=None, stream=None):
 
 class _Launch:
     """The device and stream of a call: makes the device current, and the stream while memory is made."""
+    __slots__ = ("torch", "device", "stream", "handle", "other", "back")
 
     def __init__(self, device, stream, what):
         import torch
-        self.torch, self.device = torch, device
+        self.torch, self.device, self.stream = torch, device, stream
         if stream is not None and stream.device != device:
             raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {device}")
-        self.stream = stream
 
     def __enter__(self):
-        cuda = self.torch.cuda
-        self.back = None
-        if cuda.current_device() != self.device.index:
-            self.back = cuda.current_device()
-            cuda.set_device(self.device)
-        current = cuda.current_stream()
-        if self.stream is None:
-            self.stream = current
-        self.other = self.stream != current
-        self.handle = self.stream.cuda_stream
+        # the raw getters: torch.cuda.current_stream() alone takes longer than a small call's kernel
+        raw, index = self.torch._C, self.device.index
+        self.back = raw._cuda_getDevice()
+        if self.back != index:
+            self.torch.cuda.set_device(index)
+        current = raw._cuda_getCurrentRawStream(index)
+        self.handle = current if self.stream is None else self.stream.cuda_stream
+        self.other = self.handle != current
         return self
 
     def __exit__(self, *exc):
-        if self.back is not None:
+        if self.back != self.device.index:
             self.torch.cuda.set_device(self.back)
 
     def empty(self, shape, dtype):
@@ -501,16 +499,23 @@ class _Launch:
             return self.torch.empty(shape, dtype=dtype, device=self.device)
 
 
-_TYPES = {"torch.bfloat16": BF16, "torch.float16": F16, "torch.float32": F32}
+_TYPES = {}  # torch.dtype -> type code
+
+
+def _type_code(dtype, name, allowed):
+    if not _TYPES:
+        import torch
+        _TYPES.update({torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32})
+    code = _TYPES.get(dtype, F32 + 1)
+    if code > allowed:
+        raise ValueError(f"{name} must be bfloat16{', float16 or float32' if allowed == F32 else ' or float16'}, "
+                         f"got {dtype}")
+    return code
 
 
 def _type_of(t, name, allowed):
     """The type code of a tensor."""
-    code = _TYPES.get(str(t.dtype), F32 + 1)
-    if code > allowed:
-        raise ValueError(f"{name} must be bfloat16{', float16 or float32' if allowed == F32 else ' or float16'}, "
-                         f"got {t.dtype}")
-    return code
+    return _type_code(t.dtype, name, allowed)
 
 
 def _check_like(t, name, shape, dtype, device):
@@ -772,7 +777,7 @@ def linear_bwd(dy, x, w, z=None, *, activation="none", need_dx=True, need_dw=Tru
         workspace = _workspace(at, workspace, need, "linear_bwd")
         if M == 0:  # sums over no rows
             import torch
-            with torch.cuda.stream(at.stream):
+            with torch.cuda.stream(stream):  # None: the current one
                 for t in (dw, db):
                     if t is not None:
                         t.zero_()
@@ -845,7 +850,7 @@ def kv4_read(cache, table, start, *, S, Hkv, d, page, count=None, dtype=None, k=
     dtype = dtype if dtype is not None else (k.dtype if k is not None else torch.bfloat16)
     shape = (B, int(Hkv), int(S), int(d))
     sh = _kv4_shape(cache, table, B, int(Hkv), Hkv, int(S), int(d), page,
-                    _type_of(torch.empty(0, dtype=dtype), "dtype", F16), None, dev)
+                    _type_code(dtype, "dtype", F16), None, dev)
     _check_counts(B, dev, start=start, count=count)
     for t, name in ((k, "k"), (v, "v")):
         if t is not None:
