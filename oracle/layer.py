@@ -158,8 +158,8 @@ def kv4_attention(q, cache, table, lens, page, Hkv, scale):
     and of sum |q|; so score j is off by at most
         e_j = scale * d * 2^-23 * sum |q| (15 s_j + |o_j|) + 2^-21 |x_j|,
     LSE by max e + 2^-20 (1 + |LSE|), each weight by the fraction 2 max e + 2^-20.  Output: the weight times s_j is rounded
-    to fp16 (2^-11; 2^-25 of the largest such product where it is subnormal) and multiplies c; the sums in fp32 add
-    n 2^-23 of their terms' sizes."""
+    to fp16 (2^-11; 2^-25 of the largest such product where it is subnormal) and multiplies c - 8, as the difference of two
+    products; the sums in fp32 add n 2^-23 of their terms' sizes, s (c + 8) and |o + 8 s|."""
     B, Hq, S, d = q.shape
     o = np.zeros((B, Hq, S, d))
     lse = np.full((B, Hq, S), -np.inf)
@@ -187,7 +187,7 @@ def kv4_attention(q, cache, table, lens, page, Hkv, scale):
                     e = scale * d * 2.0**-23 * size * (15 * np.abs(ks[:m]) + np.abs(ko[:m])) + 2.0**-21 * np.abs(x)
                     e = float(e.max())
                     tol_lse[b, hq, i] = e + 2.0**-20 * (1 + abs(lse[b, hq, i]))
-                    tol_o[b, hq, i] = (2.0**-11 * (w @ (vc[:m] * vs[:m, None])) + m * 15 * 2.0**-25 * (w * vs[:m]).max()
+                    tol_o[b, hq, i] = (2.0**-11 * (w @ (np.abs(vc[:m] - 8) * vs[:m, None])) + m * 15 * 2.0**-25 * (w * vs[:m]).max()
                                        + (2 * e + 2.0**-20) * (w @ np.abs(v[:m]) + np.abs(o[b, hq, i]))
-                                       + (m + 32) * 2.0**-23 * (w @ (15 * vs[:m] + np.abs(vo[:m]))))
+                                       + (m + 32) * 2.0**-23 * (w @ (31 * vs[:m] + np.abs(vo[:m]))))
     return o, lse, tol_o, tol_lse

@@ -207,7 +207,10 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ MoveP
 //  * q becomes fp16 for it, scaled by a power of two that puts the tile's largest element below 2^15 (exact for bf16
 //    down to 2^-25 of that); the scales 2^24, 1/16 and that power go to the sums.
 //  * P becomes fp16 times its row's scale, divided by a power of two of its own for each query row, which follows the
-//    largest product of a weight and a scale, so that no ratio of the scales of different tokens costs P its digits.
+//    largest product of a weight and a scale, so that no ratio of the scales of different tokens costs P its digits.  An mma
+//    more for 16 tokens multiplies it with a constant code 8: what is wanted is the sum of P (c - 8), as large as the output,
+//    and the two sums' roundings go together (with the sum of P c alone those of a long context showed, 2.1e-3 of the output
+//    against 1.7e-3 for its own rounding).
 //  * any order of the contraction will do, so K and V fragments are read straight from the stage: a lane takes 16 adjacent
 //    bytes of a K row, and the tokens are dealt to the mma's rows so that V's loads fall on different banks; P leaves the
 //    first product in the layout that movmatrix turns into the second one's operand.
@@ -483,12 +486,13 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
       }
     }
     const float kscale = p.scale * kLog2e * 16777216.f / up;
-    float acc[NT][D / 16][4], m[NT][2], di[NT][2], l[NT][2], corr[NT][2];
+    float acc[NT][D / 16][4], eight[NT][4], m[NT][2], di[NT][2], l[NT][2], corr[NT][2];
     bool fresh = true;  // no unit yet: the first one sets the maxima (a row that sees nothing of it sees nothing later)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
+      eight[nt][0] = eight[nt][1] = eight[nt][2] = eight[nt][3] = 0.f;
       m[nt][0] = m[nt][1] = 0.f;
       di[nt][0] = di[nt][1] = 1.f;
       l[nt][0] = l[nt][1] = corr[nt][0] = corr[nt][1] = 0.f;
@@ -540,7 +544,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
       for (int i = 0; i < 4; ++i) {
         const uint32_t kp = pair_of(i, 0), vp = pair_of(i, 1);
         const float ks = lo_bf16(kp) * kscale, ko = hi_bf16(kp), vs = lo_bf16(vp);
-        vo[i] = hi_bf16(vp);
+        vo[i] = fmaf(8.f, vs, hi_bf16(vp));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -583,6 +587,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
               const float fa = ex2_approx(-up), fb = ex2_approx(old - ceilf(nd));
               l[nt][c] *= fa;
               corr[nt][c] *= fa;
+              eight[nt][c] *= fb;
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
                 acc[nt][i][c] *= fb;
@@ -628,6 +633,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
             }
             pb[nt][h] = transpose8x8(pack_f16x2(y[nt][2 * i], y[nt][2 * i + 1]));
           }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_f16(eight[nt], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, pb[nt][0], pb[nt][1]);
 #pragma unroll
         for (int q = 0; q < VW; ++q) {
           const uint32_t l01 = __byte_perm(va[0][q], va[1][q], 0x5410), h01 = __byte_perm(va[0][q], va[1][q], 0x7632);
@@ -680,8 +688,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
         float v[D / 8];  // the lane's columns, from g D / 8 on
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          v[2 * i] = fmaf(acc[nt][i][c] * 16777216.f, fo, base);
-          v[2 * i + 1] = fmaf(acc[nt][i][2 + c] * 1048576.f, fo, base);
+          v[2 * i] = fmaf((acc[nt][i][c] - eight[nt][c]) * 16777216.f, fo, base);
+          v[2 * i + 1] = fmaf(fmaf(-16.f, eight[nt][c], acc[nt][i][2 + c]) * 1048576.f, fo, base);
         }
         if (whole) {
           const long long hq = seg.h * p.group + r % p.group, i = r / p.group;
