@@ -317,9 +317,9 @@ __device__ __forceinline__ int share(int total, int ctas) {
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
@@ -507,33 +507,34 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[nt][e] = 0.f;
+      uint32_t ka[2][KW], kb[2][KW];
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const uint8_t* blk = stage + b * kBytes;
-        uint32_t ka[KW], kb[KW];
         if constexpr (D == 128) {
           const uint4 a = *reinterpret_cast<const uint4*>(blk + tok * 64 + t * 16);
           const uint4 c = *reinterpret_cast<const uint4*>(blk + (tok + 8) * 64 + t * 16);
-          ka[0] = a.x; ka[1] = a.y; ka[2] = a.z; ka[3] = a.w;
-          kb[0] = c.x; kb[1] = c.y; kb[2] = c.z; kb[3] = c.w;
+          ka[b][0] = a.x; ka[b][1] = a.y; ka[b][2] = a.z; ka[b][3] = a.w;
+          kb[b][0] = c.x; kb[b][1] = c.y; kb[b][2] = c.z; kb[b][3] = c.w;
         } else {
           const uint2 a = *reinterpret_cast<const uint2*>(blk + tok * 32 + t * 8);
           const uint2 c = *reinterpret_cast<const uint2*>(blk + (tok + 8) * 32 + t * 8);
-          ka[0] = a.x; ka[1] = a.y;
-          kb[0] = c.x; kb[1] = c.y;
-        }
-#pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          const uint32_t a8 = ka[w] >> 8, b8 = kb[w] >> 8;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float(&c)[4] = *reinterpret_cast<float(*)[4]>(&x[nt][4 * b]);
-            mma_f16(c, ka[w] & 0x000F000Fu, kb[w] & 0x000F000Fu, ka[w] & 0x00F000F0u, kb[w] & 0x00F000F0u, qf[nt][w][0],
-                    qf[nt][w][1]);
-            mma_f16(c, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u, qf[nt][w][2], qf[nt][w][3]);
-          }
+          ka[b][0] = a.x; ka[b][1] = a.y;
+          kb[b][0] = c.x; kb[b][1] = c.y;
         }
       }
+#pragma unroll
+      for (int w = 0; w < KW; ++w)  // the two blocks' chains of products side by side
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const uint32_t a8 = half ? ka[b][w] >> 8 : ka[b][w], b8 = half ? kb[b][w] >> 8 : kb[b][w];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(*reinterpret_cast<float(*)[4]>(&x[nt][4 * b]), a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u,
+                      b8 & 0x00F000F0u, qf[nt][w][2 * half], qf[nt][w][2 * half + 1]);
+          }
       // x: scores in powers of two above m; w: weights; y: weights times V's scale, in units of 1 / di
       float w[NT][8], y[NT][8], vo[4], top = 0.f;
       auto pair_of = [&](int i, int kv) {  // of the lane's token i (block, half)
