@@ -374,41 +374,44 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
   if (u0 >= u1) return;
   Cursor seg = segment_at(p, u0);
 
-  // ---- the ring: unit u0 + k goes to stage k % S; a unit's pages are looked next one unit ahead of its copy -----------
+  // ---- the ring: unit u0 + k goes to stage k % S; a unit's pages are looked up one unit ahead of its copy -----------
   Cursor pre = seg;
-  int next = u0, blk = 0, pg0 = 0, pg1 = 0;
+  int next = u0, pre_end = seg.end(), pg0 = 0, pg1 = 0, off = 0;
+  const int32_t* row = p.c.table + (long long)seg.b * p.c.max_pages;
+  const int in_page = (1 << p.page_shift) - 1, per_page = p.c.Hkv << p.page_shift;  // blocks of a page, and of all heads
+  const uint8_t* lane_base = p.c.base + lane * 16;
+  const uint32_t lane_ring = smem_u32(sm.ring[warp]) + lane * 16;
+  uint32_t bad = 0;  // bit s: a block of stage s has no page
   auto look_up = [&]() {
-    pre.advance(p, next);
-    blk = 2 * (next - pre.start);
-    const int32_t* row = p.c.table + (long long)pre.b * p.c.max_pages;
+    if (next >= pre_end) {
+      pre.advance(p, next);
+      pre_end = pre.end();
+      row = p.c.table + (long long)pre.b * p.c.max_pages;
+    }
+    const int blk = 2 * (next - pre.start);
     pg0 = row[blk >> p.page_shift];
-    pg1 = 0;  // not pg0: a copy would wait for its load here
+    off = (pre.h << p.page_shift) + (blk & in_page);
+    pg1 = 0;  // any page: a last block without a second one reads what is there, and masks it
     if (p.page_shift == 0 && blk + 1 < pre.blocks) pg1 = row[blk + 1];
   };
-  const uint8_t* lane_base = p.c.base + lane * 16;
-  uint32_t bad = 0;  // bit s: a block of stage s has no page
   auto fill = [&]() {
     if (next < u1) {
       const int s = (next - u0) % S;
-      const bool ok = pg0 >= 0 && pg0 < p.c.n_pages && pg1 >= 0 && pg1 < p.c.n_pages;
-      bad = (bad & ~(1u << s)) | (ok ? 0u : 1u << s);
-      if (ok) {
+      if ((uint32_t)pg0 < (uint32_t)p.c.n_pages && (uint32_t)pg1 < (uint32_t)p.c.n_pages) {
         constexpr int kChunks = kBytes / 16;  // of a block
-        const bool two = blk + 1 < pre.blocks;
-        const int in_page = (1 << p.page_shift) - 1;
-        auto block = [&](int pg, int b) {  // fewer than 2^31 blocks: checked on the host
-          return lane_base + (unsigned long long)(uint32_t)(((pg * p.c.Hkv + pre.h) << p.page_shift) + (b & in_page)) * kBytes;
-        };
-        const uint8_t* src0 = block(pg0, blk);
-        // the second block, as if it followed the first; it does where a page holds two
-        const uint8_t* src1 = p.page_shift > 0 ? src0 : block(pg1, blk + 1) - kBytes;
-        const uint32_t dst = smem_u32(sm.ring[warp][s]) + lane * 16;
+        // (fewer than 2^31 blocks: checked on the host)
+        const uint8_t* src0 = lane_base + (unsigned long long)(uint32_t)(pg0 * per_page + off) * kBytes;
+        const uint8_t* src1 = src0;  // the second block follows the first where a page holds two
+        if (p.page_shift == 0) src1 = lane_base + (unsigned long long)(uint32_t)(pg1 * per_page + off) * kBytes - kBytes;
+        const uint32_t dst = lane_ring + s * (2 * kBytes);
 #pragma unroll
         for (int i = 0; i < (2 * kChunks + 31) / 32; ++i) {
-          const int c = i * 32 + lane;
-          if (c < kChunks) copy16(dst + i * 512, src0 + i * 512);
-          else if (two && c < 2 * kChunks) copy16(dst + i * 512, src1 + i * 512);
+          const int c = i * 32;
+          if (c + 32 <= 2 * kChunks || lane < 2 * kChunks - c)
+            copy16(dst + i * 512, (c + 32 <= kChunks ? src0 : c >= kChunks ? src1 : lane < kChunks - c ? src0 : src1) + i * 512);
         }
+      } else {
+        bad |= 1u << s;
       }
       if (++next < u1) look_up();
     }
@@ -661,6 +664,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
       copy_wait<S - 1>();
       __syncwarp();  // every lane's copies are there
       if (bad >> s & 1u) {
+        bad ^= 1u << s;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) l[nt][0] = l[nt][1] = NAN;
       } else {
