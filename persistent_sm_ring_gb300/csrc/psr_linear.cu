@@ -1,7 +1,8 @@
 // The linear layer y = act(x w^T + bias) + residual and its gradients on sm_103a.
 //
-// Operands whose rows start on 16-byte boundaries go to the tcgen05 products of psr_linear_mma.cuh; others (odd
-// strides, odd offsets) to a plain tiled product on the fp32 units.
+// The products are the tcgen05 kernels of psr_linear_mma.cuh.  A tensor map wants rows that start on 16-byte boundaries: an
+// operand with other strides is copied into the workspace first (4100 columns: 0.09 ms of 0.26 at 8192 x 4096 x 4100).  What is
+// left, an odd base address, takes a plain tiled product on the fp32 units.
 #include <cmath>
 #include <cstring>
 
@@ -58,6 +59,25 @@ static int launch_simple(const void* a, long long lda, const void* b, long long 
                                                 l.clear);
   l.clear = nullptr;
   return launch_status();
+}
+
+// ------------------------------------------------------------------------------------------------
+// An operand with rows of any stride into rows of a multiple of 8
+// ------------------------------------------------------------------------------------------------
+__global__ void __launch_bounds__(256)
+    align_kernel(const uint16_t* __restrict__ x, long long ld, uint4* __restrict__ y, int rows, int cols, Ctrl* clear) {
+  clear_ctrl(clear);
+  const int per = (cols + 7) / 8;
+  const long long n = (long long)rows * per;
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
+    const long long r = i / per;
+    const int c = (int)(i - r * per) * 8;
+    const uint16_t* p = x + r * ld + c;
+    uint32_t e[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = c + j < cols ? p[j] : 0;
+    y[i] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+  }
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -207,6 +227,7 @@ struct Sizes {
   int chunks;     // row chunks of the column sums
   long long lddz; // row stride of dz in the workspace
   size_t sums, sums_bytes, dz, partial, total;
+  size_t x, w, dy;  // aligned copies of operands (0: the tensor's own rows are)
 };
 
 static int launch_of(void* workspace, const Sizes& s, int timeout_ms, void* stream, Launch& l) {
@@ -219,6 +240,19 @@ static int launch_of(void* workspace, const Sizes& s, int timeout_ms, void* stre
   l.timeout_ns = (unsigned long long)(timeout_ms > 0 ? timeout_ms : 2000) * 1000000ull;
   l.st = static_cast<cudaStream_t>(stream);
   return PSR_OK;
+}
+
+// The operand's aligned copy, if it needs one: x and ld then name that.
+static int align(const void*& x, long long& ld, size_t at, int rows, int cols, void* workspace, Launch& l) {
+  if (!at || rows == 0) return PSR_OK;
+  uint4* y = reinterpret_cast<uint4*>(static_cast<uint8_t*>(workspace) + at);
+  const long long blocks = ((long long)rows * ((cols + 7) / 8) + 255) / 256;
+  align_kernel<<<(unsigned)(blocks < l.n_sm * 16 ? blocks : l.n_sm * 16), 256, 0, l.st>>>(static_cast<const uint16_t*>(x), ld, y,
+                                                                                        rows, cols, l.clear);
+  l.clear = nullptr;
+  x = y;
+  ld = (cols + 7ll) / 8 * 8;
+  return launch_status();
 }
 
 // A call that launched nothing still leaves a cleared control block for psr_get_stats.
@@ -256,6 +290,15 @@ static int sizes(const psr_linear_shape* sh, bool backward, Sizes& s) {
     s.partial = off;
     off = au(off + (size_t)s.chunks * sh->N * 4);
   }
+  auto copy = [&](long long ld, int rows, int cols) {
+    const size_t at = off;
+    if (rows <= 1 || ld % 8 == 0) return (size_t)0;
+    off = au(off + (size_t)rows * ((cols + 7ll) / 8 * 8) * 2);
+    return at;
+  };
+  s.x = copy(s.ldx, sh->M, sh->K);
+  s.w = copy(s.ldw, sh->N, sh->K);
+  s.dy = backward && sh->act == PSR_ACT_NONE ? copy(s.ldy, sh->M, sh->N) : 0;
   s.total = off;
   return PSR_OK;
 }
@@ -274,7 +317,7 @@ static int product(const Operands& o, Epilogue e, Launch& l) {
   if constexpr (!AMN)
     if (streams(o.M)) return launch_stream<BMN>(o, e, l);
   const int splits = pair_splits(o.M, o.N, o.K);
-  if (splits > 1) return launch_pair<1, AMN, BMN>(o, e, splits, l);
+  if (splits > 1) return launch_pair<AMN, BMN>(o, e, false, splits, l);
   // A wave of 512-column tiles takes 16 clocks for each K and then its epilogue, when the accumulators are not free for the
   // next tile (all SMs write at once); one of 256-column tiles 11.5 for each K (the tile loads bound it) with the
   // epilogue of the tile before behind it.  Clocks as measured at 2048 x 8192 x 4096 (89 us and 103 us, with gelu, bias,
@@ -282,9 +325,11 @@ static int product(const Operands& o, Epilogue e, Launch& l) {
   const long long rows = (o.M + 255) / 256, n_pairs = l.n_sm / 2;
   auto waves = [&](long long cols) { return (rows * ((o.N + cols - 1) / cols) + n_pairs - 1) / n_pairs; };
   const double epi = 6000.0 + (e.act ? 3000.0 : 0.0) + (e.z ? 4000.0 : 0.0) + (e.res ? 4000.0 : 0.0);  // of 256 columns
-  const double two = waves(512) * (16.0 * o.K + 2.0 * epi);
+  const long long tiles = rows * ((o.N + 511) / 512), halves = last_halves(tiles, (int)n_pairs);
+  const double two = (tiles / n_pairs + (halves || tiles % n_pairs == 0 ? 0 : 1)) * (16.0 * o.K + 2.0 * epi) +
+                     (halves ? 11.5 * o.K + epi : 0.0);
   const double one = waves(256) * (11.5 * o.K + 1500.0 > epi ? 11.5 * o.K + 1500.0 : epi);
-  return two <= one ? launch_pair<2, AMN, BMN>(o, e, 1, l) : launch_pair<1, AMN, BMN>(o, e, 1, l);
+  return launch_pair<AMN, BMN>(o, e, two <= one, 1, l);
 }
 
 template <class T>
@@ -312,20 +357,25 @@ static int backward(const psr_linear_shape* sh, const Sizes& s, const void* dy, 
     if ((rc = launch_status()) != PSR_OK) return rc;
   }
   const void* g = act ? dz : dy;
-  const long long ldg = act ? s.lddz : s.ldy;
+  long long ldg = act ? s.lddz : s.ldy, ldw = s.ldw, ldx = s.ldx;
+  if (sh->M > 0) {
+    if ((dx || dw) && (rc = align(g, ldg, s.dy, sh->M, sh->N, ws, l)) != PSR_OK) return rc;
+    if (dx && (rc = align(w, ldw, s.w, sh->N, sh->K, ws, l)) != PSR_OK) return rc;
+    if (dw && (rc = align(x, ldx, s.x, sh->M, sh->K, ws, l)) != PSR_OK) return rc;
+  }
   Epilogue e = {};
   e.half = sh->type == PSR_F16;
   e.ldy = sh->K;
   if (dx) {
     e.y = dx;
-    if ((rc = product<T, false, true>({g, ldg, w, s.ldw, sh->M, sh->K, sh->N}, e, l)) != PSR_OK) return rc;
+    if ((rc = product<T, false, true>({g, ldg, w, ldw, sh->M, sh->K, sh->N}, e, l)) != PSR_OK) return rc;
   }
   if (dw) {
     e.y = dw;
     if (sh->M == 0) {
       if (cudaMemsetAsync(dw, 0, (size_t)sh->N * sh->K * 2, l.st) != cudaSuccess) return PSR_ERR_CUDA;
     } else {
-      rc = product<T, true, true>({g, ldg, x, s.ldx, sh->N, sh->K, sh->M}, e, l);
+      rc = product<T, true, true>({g, ldg, x, ldx, sh->N, sh->K, sh->M}, e, l);
     }
   }
   return rc;
@@ -362,6 +412,8 @@ int psr_linear(const psr_linear_shape* sh, const void* x, const void* w, const v
   e.ldr = s.ldr; e.ldy = s.ldy; e.ldz = s.ldz;
   e.act = sh->act;
   e.half = sh->type == PSR_F16;
+  if ((rc = align(x, s.ldx, s.x, sh->M, sh->K, workspace, l)) != PSR_OK) return rc;
+  if (sh->M > 0 && (rc = align(w, s.ldw, s.w, sh->N, sh->K, workspace, l)) != PSR_OK) return rc;
   const Operands o = {x, s.ldx, w, s.ldw, sh->M, sh->N, sh->K};
   rc = sh->type == PSR_BF16 ? product<__nv_bfloat16, false, false>(o, e, l) : product<__half, false, false>(o, e, l);
   return rc != PSR_OK ? rc : clear_rest(l);

@@ -4,9 +4,10 @@
 // instruction descriptor take both, so no operand is transposed in memory: forward x w^T is K-major twice,
 // dx = dz w has w MN-major, dw = dz^T x has both MN-major.  Two kernels:
 //
-//  * pair_gemm: a pair of CTAs (cta_group::2) computes a 256 x 256 H tile, each CTA 128 rows and 128 columns of
-//    each 256-column half.  H = 2 fills all 512 tensor memory columns and moves 48 B/clk per SM at the tensor rate
-//    (64 B/clk for H = 1, above what TMA tile loads land); H = 1 double-buffers the accumulator.
+//  * pair_gemm: a pair of CTAs (cta_group::2) computes tiles of 256 rows and 512 or 256 columns, each CTA 128 rows and 128
+//    columns of each 256-column half.  512 columns fill tensor memory and move 48 B/clk per SM at the tensor rate, but the
+//    next tile's products wait for the epilogue; 256 columns move 64 B/clk, above what TMA tile loads land (a K step of 64
+//    then takes 700 to 800 clocks instead of 512), and the accumulator is double-buffered.
 //  * stream_gemm: for few rows of A.  The output is computed transposed, W's rows on the 128 tensor memory lanes
 //    and the tokens in the columns, so that W streams through once.  The (tile, K step) units are dealt out
 //    evenly over one CTA per SM; a tile whose K range is split leaves fp32 partials that a second kernel joins.
@@ -147,20 +148,20 @@ constexpr int kHalf = kRows * kBK * 2;
 constexpr int kEpiWarps = 16;  // four to a scheduler: an epilogue block is a chain of latencies
 constexpr int kPairThreads = (4 + kEpiWarps) * 32;
 constexpr int kEpiWarpBytes = 2048;  // one warp's 32 rows x 64 bytes
-template <int H>
-struct PairCfg {
-  static constexpr int kStage = (1 + H) * kHalf;
-  static constexpr int kStages = H == 2 ? 4 : 6;
-  static constexpr int kEpiOff = kStage * kStages;
-  static constexpr int kSmem = 1024 + kEpiOff + kEpiWarps * kEpiWarpBytes;
-};
-static_assert(PairCfg<1>::kSmem + 1024 <= 232448 && PairCfg<2>::kSmem + 1024 <= 232448, "shared memory");
+// The stages are cut into chunks of one operand tile (16 KiB) each: a K step takes 2 of them (one 256-column half) or 3, so
+// that either way all 192 KiB are in flight (4 steps of 48 KiB would leave one half 128 KiB, which bounds it).
+constexpr int kChunks = 12;
+constexpr int kSteps = 8;  // barriers; more than K steps in flight
+constexpr int kPairSmem = 1024 + kChunks * kHalf + kEpiWarps * kEpiWarpBytes;
+static_assert(kPairSmem + 1024 <= 232448, "shared memory");
 
 struct PairParams {
   int M, N, n_k;
-  int tiles_m, tiles_n;   // 256 rows, 256 H columns
+  int wide;               // tiles of 512 columns, else 256
+  int tiles_m, tiles_n;   // tile rows of 256, tile columns
   int group;              // tile rows of a raster group
-  int splits, split_k;    // parts of the K steps, K steps of a part
+  int splits, split_k;    // of 256-column tiles: parts of the K steps, K steps of a part
+  int halves;             // of 512-column tiles: those of the last round that are computed as two halves (pair_item)
   float* partial;         // splits > 1: fp32 sums [splits][M][ldp]
   long long ldp;
   uint32_t idesc;
@@ -171,10 +172,14 @@ struct PairParams {
 };
 
 struct PairSmem {
-  uint64_t full[6], empty[6], acc_full[2], acc_empty[2], drain;
+  uint64_t full[kSteps], empty[kSteps], acc_full[2], acc_empty[2], drain;
   uint32_t tmem_base;
-  uint32_t peer_fills;
   volatile uint32_t abort;
+};
+
+// What a pair computes next: `n` 256-column halves from column half tn on of tile row tm, K steps k0 .. k0 + n_k.
+struct PairItem {
+  int tm, tn, n, k0, n_k, split;
 };
 
 // Tile t -> (row block, column block): groups of `group` tile rows, columns inside a group, rows fastest, so that the
@@ -184,6 +189,33 @@ __device__ __forceinline__ void pair_tile(const PairParams& p, int t, int& tm, i
   const int rows = min(p.group, p.tiles_m - g * p.group);
   tn = r / rows;
   tm = g * p.group + (r - tn * rows);
+}
+
+// Item i of a pair; false past its last: the tiles stride over the pairs.  The tiles of the last round, where no more than
+// half of the pairs would have one, are dealt out as 256-column halves (256 tiles of 512 columns on 76 pairs: three rounds and
+// a half, not four).  Rounds shifted by half a tile between pairs, so that some write while others multiply, were
+// slower: the tile loads leave L2 no room for the outputs (4096^3 with gelu 100 to 118 us).
+__device__ __forceinline__ bool pair_item(const PairParams& p, int pair, int n_pairs, int i, PairItem& it) {
+  const long long n = (long long)p.tiles_m * p.tiles_n * p.splits, at = pair + (long long)i * n_pairs;
+  it.k0 = 0;
+  it.n_k = p.n_k;
+  it.split = 0;
+  if (!p.wide) {
+    if (at >= n) return false;
+    it.split = (int)(at % p.splits);
+    it.k0 = it.split * p.split_k;
+    it.n_k = min(p.split_k, p.n_k - it.k0);
+    it.n = 1;
+    pair_tile(p, (int)(at / p.splits), it.tm, it.tn);
+    return true;
+  }
+  const long long whole = n - p.halves;  // tiles in whole rounds
+  const int h = (int)(at - whole);
+  if (h >= 2 * p.halves) return false;
+  pair_tile(p, h < 0 ? (int)at : (int)whole + h / 2, it.tm, it.tn);
+  it.tn = 2 * it.tn + (h < 0 ? 0 : h % 2);
+  it.n = h < 0 && (it.tn + 1) * 256 < p.N ? 2 : 1;  // the last columns may be one half wide
+  return true;
 }
 
 // One 128-row operand tile of a stage.
@@ -227,6 +259,25 @@ __device__ __forceinline__ void rows_in(uint4 (&w)[4], const uint8_t* g, long lo
     g += 8 * pitch;
   }
 }
+// The same for rows that are not 16-byte aligned: a row of 32 columns at a time, a column to a lane.
+__device__ __forceinline__ uint16_t* stage_element(uint8_t* stage, int row, int c) {
+  return reinterpret_cast<uint16_t*>(stage_chunk(stage, row, c / 8)) + c % 8;
+}
+__device__ __forceinline__ void rows_out_odd(uint8_t* stage, uint16_t* g, long long ld, int rows, int cols) {
+  const int lane = threadIdx.x % 32;
+  __syncwarp();
+#pragma unroll 4
+  for (int r = 0; r < rows; ++r)
+    if (lane < cols) g[r * ld + lane] = *stage_element(stage, r, lane);
+  __syncwarp();
+}
+__device__ __forceinline__ void rows_in_odd(uint8_t* stage, const uint16_t* g, long long ld, int rows, int cols) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll 4
+  for (int r = 0; r < rows; ++r)
+    if (lane < cols) *stage_element(stage, r, lane) = g[r * ld + lane];
+  __syncwarp();
+}
 __device__ __forceinline__ void add16(uint32_t* v, const uint4& b, int half) {
   const uint32_t w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
@@ -246,25 +297,19 @@ __device__ __forceinline__ void pair_store(const Epilogue& e, int M, int N, uint
   const int lane = threadIdx.x % 32;
   const int rows = min(32, M - i0), cols = min(32, N - j0);
   if (rows <= 0 || cols <= 0) return;
-  if (!e.vec) {
-    if (lane < rows)
-#pragma unroll
-      for (int c = 0; c < 32; ++c)
-        if (c < cols) {
-          float f = __uint_as_float(v[c]);
-          if (e.bias) f += load16(e.bias, j0 + c, e.half);
-          if (e.z) store16(e.z, (i0 + lane) * e.ldz + j0 + c, e.half, f);
-          v[c] = __float_as_uint(f);
-        }
-  } else {
-    if (e.bias) {
+  if (e.bias) {
+    if (e.vec) {
       const uint4* b = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.bias) + j0);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (j * 8 < cols) add16(v + 8 * j, b[j], e.half);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        if (c < cols) v[c] = __float_as_uint(__uint_as_float(v[c]) + load16(e.bias, j0 + c, e.half));
     }
   }
-  auto put = [&]() {
+  auto out = [&](void* base, long long ld) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t w[4];
@@ -273,11 +318,11 @@ __device__ __forceinline__ void pair_store(const Epilogue& e, int M, int N, uint
         w[q] = pack16(__uint_as_float(v[j * 8 + 2 * q]), __uint_as_float(v[j * 8 + 2 * q + 1]), e.half);
       *stage_chunk(stage, lane, j) = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    uint16_t* g = static_cast<uint16_t*>(base) + (long long)i0 * ld + j0;
+    if (e.vec) rows_out(stage, reinterpret_cast<uint8_t*>(g), ld * 2, rows, cols / 8);
+    else rows_out_odd(stage, g, ld, rows, cols);
   };
-  if (e.vec && e.z) {
-    put();
-    rows_out(stage, static_cast<uint8_t*>(e.z) + ((long long)i0 * e.ldz + j0) * 2, e.ldz * 2, rows, cols / 8);
-  }
+  if (e.z) out(e.z, e.ldz);
   if constexpr (ACT) {
     auto apply = [&](auto act) {
 #pragma unroll
@@ -291,27 +336,19 @@ __device__ __forceinline__ void pair_store(const Epilogue& e, int M, int N, uint
       default: break;
     }
   }
-  if (!e.vec) {
-    if (lane < rows)
-#pragma unroll
-      for (int c = 0; c < 32; ++c)
-        if (c < cols) {
-          float f = __uint_as_float(v[c]);
-          if (e.res) f += load16(e.res, (i0 + lane) * e.ldr + j0 + c, e.half);
-          store16(e.y, (i0 + lane) * e.ldy + j0 + c, e.half, f);
-        }
-    return;
-  }
   if (e.res) {
+    if (e.vec) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) *stage_chunk(stage, k * 8 + lane / 4, lane % 4) = res[k];
-    __syncwarp();
+      for (int k = 0; k < 4; ++k) *stage_chunk(stage, k * 8 + lane / 4, lane % 4) = res[k];
+      __syncwarp();
+    } else {
+      rows_in_odd(stage, static_cast<const uint16_t*>(e.res) + (long long)i0 * e.ldr + j0, e.ldr, rows, cols);
+    }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) add16(v + 8 * j, *stage_chunk(stage, lane, j), e.half);
+    for (int j = 0; j < 4; ++j) add16(v + 8 * j, *stage_chunk(stage, lane, j), e.half);  // (columns past `cols` are not stored)
     __syncwarp();
   }
-  put();
-  rows_out(stage, static_cast<uint8_t*>(e.y) + ((long long)i0 * e.ldy + j0) * 2, e.ldy * 2, rows, cols / 8);
+  out(e.y, e.ldy);
 }
 
 // The block's fp32 sums into the split's partials.
@@ -332,16 +369,15 @@ __device__ __forceinline__ void partial_store(const PairParams& p, int split, ui
   }
 }
 
-template <int H, bool AMN, bool BMN>
+template <bool AMN, bool BMN>
 __global__ void __launch_bounds__(kPairThreads, 1)
     pair_gemm(const __grid_constant__ PairParams p, const __grid_constant__ CUtensorMap ma,
               const __grid_constant__ CUtensorMap mb) {
-  using C = PairCfg<H>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ PairSmem sc;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t smem_base = (raw + 1023u) & ~1023u;
-  uint8_t* epi = smem_raw + (smem_base - raw) + C::kEpiOff;
+  uint8_t* epi = smem_raw + (smem_base - raw) + kChunks * kHalf;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   uint32_t n_rank;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n_rank));
@@ -353,7 +389,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   clear_ctrl(p.clear);
   launch_dependents();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
+    for (int s = 0; s < kSteps; ++s) {
       mbar_init(&sc.full[s], 1);
       mbar_init(&sc.empty[s], 1);
     }
@@ -362,7 +398,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(&sc.acc_empty[b], 2 * kEpiWarps);
     }
     mbar_init(&sc.drain, 1);
-    sc.peer_fills = 0;
     sc.abort = 0;
     fence_barrier_init();
     prefetch_tmap(&ma);
@@ -377,27 +412,37 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   cluster_sync();
   tc_fence_after();
 
-  const int n_items = p.tiles_m * p.tiles_n * p.splits;  // the splits of a tile run one after another
   const int pair = blockIdx.x / 2, n_pairs = gridDim.x / 2;
-  uint32_t fills = 0;  // thread 0: stages this CTA filled
+  PairItem it;
   if (warp == 0) {
     if (lane == 0) {
+      uint32_t head = 0, tail = 0, chunk = 0, used = 0, wide = 0;  // steps issued and known read, chunks, step sizes
       bool ok = true;
-      for (int t = pair; t < n_items && ok; t += n_pairs) {
-        int tm, tn;
-        pair_tile(p, t / p.splits, tm, tn);
-        const int arow = tm * 256 + (int)rank * kRows, brow = tn * 256 * H + (int)rank * kRows;
-        const int k0 = t % p.splits * p.split_k, k1 = min(p.n_k, k0 + p.split_k);
-        for (int ks = k0; ks < k1; ++ks) {
-          const uint32_t s = fills % C::kStages, use = fills / C::kStages;
-          if (use > 0 && !wait_own(&sc.empty[s], (use - 1) & 1u, p, &sc, SITE_EMPTY)) { ok = false; break; }
-          if (rank == 0) mbar_expect_tx(&sc.full[s], 2 * C::kStage);  // both CTAs' bytes
+      for (int i = 0; ok && pair_item(p, pair, n_pairs, i, it); ++i) {
+        const int arow = it.tm * 256 + (int)rank * kRows, brow = it.tn * 256 + (int)rank * kRows;
+        const uint32_t n = 1 + it.n;
+        for (int ks = it.k0; ks < it.k0 + it.n_k; ++ks) {
+          while (used + n > kChunks) {  // the oldest step gives its chunks back (at most 6 are in flight)
+            const uint32_t s = tail % kSteps;
+            if (!wait_own(&sc.empty[s], (tail / kSteps) & 1u, p, &sc, SITE_EMPTY)) { ok = false; break; }
+            used -= 2 + (wide >> s & 1u);
+            ++tail;
+          }
+          if (!ok) break;
+          const uint32_t s = head % kSteps;
+          wide = (wide & ~(1u << s)) | ((n - 2) << s);
+          if (rank == 0) mbar_expect_tx(&sc.full[s], 2 * n * kHalf);  // both CTAs' bytes
           const uint32_t bar = mapa_shared(smem_u32(&sc.full[s]), 0);
-          const uint32_t base = smem_base + s * C::kStage;
-          load_operand<AMN>(base, &ma, ks * kBK, arow, bar);
-#pragma unroll
-          for (int h = 0; h < H; ++h) load_operand<BMN>(base + (1 + h) * kHalf, &mb, ks * kBK, brow + h * 256, bar);
-          ++fills;
+          auto next = [&]() {
+            const uint32_t at = smem_base + chunk * kHalf;
+            chunk = chunk + 1 == kChunks ? 0 : chunk + 1;
+            return at;
+          };
+          load_operand<AMN>(next(), &ma, ks * kBK, arow, bar);
+          load_operand<BMN>(next(), &mb, ks * kBK, brow, bar);
+          if (it.n == 2) load_operand<BMN>(next(), &mb, ks * kBK, brow + 256, bar);
+          used += n;
+          ++head;
         }
       }
       if (!ok) sc.abort = 1;
@@ -405,21 +450,25 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       constexpr uint32_t kHi = sdesc_hi_sw128(1024);
-      uint32_t c = 0, u = 0;  // stages consumed, accumulator halves begun
+      uint32_t c = 0, chunk = 0, u = 0;  // steps and chunks consumed, accumulator halves begun
       bool ok = true;
-      for (int t = pair; t < n_items && ok; t += n_pairs, u += H) {
-        const int n_k = min(p.split_k, p.n_k - t % p.splits * p.split_k);
-        for (int ks = 0; ks < n_k && ok; ++ks, ++c) {
-          const uint32_t s = c % C::kStages;
-          if (!wait_own(&sc.full[s], (c / C::kStages) & 1u, p, &sc, SITE_FULL)) { ok = false; break; }
+      auto next = [&]() {
+        const uint32_t at = smem_base + chunk * kHalf;
+        chunk = chunk + 1 == kChunks ? 0 : chunk + 1;
+        return at;
+      };
+      for (int i = 0; ok && pair_item(p, pair, n_pairs, i, it); ++i) {
+        for (int ks = 0; ks < it.n_k && ok; ++ks, ++c) {
+          const uint32_t s = c % kSteps;
+          if (!wait_own(&sc.full[s], (c / kSteps) & 1u, p, &sc, SITE_FULL)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t base = smem_base + s * C::kStage;
+          const uint32_t a = next();
 #pragma unroll
-          for (int h = 0; h < H; ++h) {
-            const uint32_t slot = (u + h) % 2;
+          for (int h = 0; h < 2; ++h) {
+            if (h >= it.n) break;
+            const uint32_t slot = (u + h) % 2, b = next();
             if (ks == 0) {  // the half's previous sums have been read back
-              if (u + h >= 2 &&
-                  !wait_own<true>(&sc.acc_empty[slot], ((u + h) / 2 - 1) & 1u, p, &sc, SITE_ACC_EMPTY)) {
+              if (u + h >= 2 && !wait_own<true>(&sc.acc_empty[slot], ((u + h) / 2 - 1) & 1u, p, &sc, SITE_ACC_EMPTY)) {
                 ok = false;
                 break;
               }
@@ -427,15 +476,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
 #pragma unroll
             for (int kk = 0; kk < kBK / 16; ++kk)
-              mma_ss_cg<2>(sc.tmem_base + slot * 256, operand_lo<AMN>(base, kk), kHi,
-                           operand_lo<BMN>(base + (1 + h) * kHalf, kk), kHi, p.idesc, (ks > 0 || kk > 0) ? 1u : 0u);
+              mma_ss_cg<2>(sc.tmem_base + slot * 256, operand_lo<AMN>(a, kk), kHi, operand_lo<BMN>(b, kk), kHi, p.idesc,
+                           (ks > 0 || kk > 0) ? 1u : 0u);
           }
           if (!ok) break;
           mma_commit_cg<2>(&sc.empty[s], 3);
         }
         if (!ok) break;
-#pragma unroll
-        for (int h = 0; h < H; ++h) mma_commit_cg<2>(&sc.acc_full[(u + h) % 2], 3);
+        for (int h = 0; h < it.n; ++h) mma_commit_cg<2>(&sc.acc_full[(u + h) % 2], 3);
+        u += it.n;
       }
       if (!ok) sc.abort = 1;
     }
@@ -446,14 +495,22 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const bool res = e.res && e.vec && p.splits == 1;
     uint32_t u = 0;
     bool ok = true;
-    for (int t = pair; t < n_items && ok; t += n_pairs) {
-      int tm, tn;
-      pair_tile(p, t / p.splits, tm, tn);
-      const int i0 = tm * 256 + (int)rank * kRows + quarter * 32;
+    for (int i = 0; ok && pair_item(p, pair, n_pairs, i, it); ++i) {
+      const int i0 = it.tm * 256 + (int)rank * kRows + quarter * 32;
+      if (res && i0 + lane < p.M) {
+        // this warp's part of the residual to L2 while the products run: 128 bytes of a row each
+        for (int h = 0; h < it.n; ++h) {
+          const int j0 = (it.tn + h) * 256 + cgroup * 64;
+          if (j0 < p.N) {
+            const uint16_t* g = static_cast<const uint16_t*>(e.res) + (i0 + lane) * e.ldr + j0;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(g));
+          }
+        }
+      }
 #pragma unroll 1
-      for (int b = 0; b < 2 * H && ok; ++b) {
+      for (int b = 0; b < 2 * it.n && ok; ++b) {
         const uint32_t slot = u % 2;
-        const int j0 = tn * 256 * H + (b / 2) * 256 + cgroup * 64 + (b % 2) * 32;
+        const int j0 = it.tn * 256 + (b / 2) * 256 + cgroup * 64 + (b % 2) * 32;
         uint4 rr[4];
         if (res)  // in flight while the sums are waited for
           rows_in(rr, static_cast<const uint8_t*>(e.res) + ((long long)i0 * e.ldr + j0) * 2, e.ldr * 2, p.M - i0, (p.N - j0) / 8);
@@ -474,34 +531,24 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
           ++u;
         }
-        if (p.splits > 1) partial_store(p, t % p.splits, stage, i0, j0, v);
+        if (p.splits > 1) partial_store(p, it.split, stage, i0, j0, v);
         else pair_store<!BMN>(e, p.M, p.N, stage, i0, j0, v, rr);
       }
     }
     if (!ok) sc.abort = 1;
   }
-  // Every tcgen05 op has completed and every load has landed (bounded waits) before tensor memory is released and
-  // either CTA leaves.  After an abort the two producers may have issued different numbers of fills: the even CTA
-  // arms a phase that only the odd one loaded, and accounts for the odd one's bytes of a phase only it loaded itself.
+  // Every tcgen05 op has completed before tensor memory is released.  Every load has landed then too, the products having
+  // waited for it; after a wait that gave up, the loads in flight get two milliseconds.
   if (warp == 1 && lane == 0 && rank == 0) {
     mma_commit_cg<2>(&sc.drain, 1);
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(&sc.drain, 0) && globaltimer_ns() - t0 < 100000000ull) {
     }
   }
-  if (threadIdx.x == 0 && rank == 1) st_shared_cluster(mapa_shared(smem_u32(&sc.peer_fills), 0), fills);
   __syncthreads();
-  cluster_sync();
-  if (threadIdx.x == 0 && rank == 0) {
-    const uint32_t L = fills, Q = sc.peer_fills, F = L > Q ? L : Q;
+  if (sc.abort && threadIdx.x == 0) {
     const uint64_t t0 = globaltimer_ns();
-    for (uint32_t s = 0; s < (uint32_t)C::kStages && s < F; ++s) {
-      const uint32_t m = s + ((F - 1 - s) / C::kStages) * C::kStages;  // the stage's last fill by either CTA
-      if (m >= L) mbar_expect_tx(&sc.full[s], C::kStage);
-      else if (m >= Q) mbar_complete_tx(&sc.full[s], C::kStage);
-      while (!mbar_try_wait(&sc.full[s], (m / C::kStages) & 1u) && globaltimer_ns() - t0 < 100000000ull) {
-      }
-    }
+    while (globaltimer_ns() - t0 < 2000000ull) nanosleep_ns(1000);
   }
   tc_fence_before();
   __syncthreads();
@@ -816,21 +863,21 @@ inline bool mappable(const void* base, int rows, long long ld) {
 }
 
 // Shared memory and co-resident pairs of one pair_gemm instantiation on the current device; 0 on error.
-template <int H, bool AMN, bool BMN>
+template <bool AMN, bool BMN>
 inline int pairs_of(int dev, int n_sm) {
   static std::mutex mu;
   static int known[64] = {};
   std::lock_guard<std::mutex> lk(mu);
   if (dev >= 0 && dev < 64 && known[dev]) return known[dev];
-  auto kern = pair_gemm<H, AMN, BMN>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PairCfg<H>::kSmem) != cudaSuccess) {
+  auto kern = pair_gemm<AMN, BMN>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(n_sm / 2 * 2));
   cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = PairCfg<H>::kSmem;
+  cfg.dynamicSmemBytes = kPairSmem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -867,22 +914,29 @@ struct Operands {
   int M, N, K;  // C is [M][N]
 };
 
-template <int H, bool AMN, bool BMN>
-inline int launch_pair(const Operands& o, const Epilogue& e, int splits, Launch& l) {
-  const int n_pairs = pairs_of<H, AMN, BMN>(l.dev, l.n_sm);
+// Tiles of the last round that are dealt out as halves.
+inline int last_halves(long long tiles, int pairs) {
+  const long long rest = tiles % pairs;
+  return 2 * rest <= pairs ? (int)rest : 0;
+}
+
+template <bool AMN, bool BMN>
+inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, int splits, Launch& l) {
+  const int n_pairs = pairs_of<AMN, BMN>(l.dev, l.n_sm), cols = wide ? 512 : 256;
   if (n_pairs < 1) return PSR_ERR_CUDA;
   PairParams p = {};
   p.M = o.M;
   p.N = o.N;
   p.n_k = (o.K + kBK - 1) / kBK;
   p.tiles_m = (o.M + 255) / 256;
-  p.tiles_n = (o.N + 256 * H - 1) / (256 * H);
+  p.wide = wide;
+  p.tiles_n = (o.N + cols - 1) / cols;
   if ((long long)p.tiles_m * p.tiles_n * splits >= (1ll << 31)) return PSR_ERR_UNSUPPORTED;
   p.group = 8;
   p.split_k = (p.n_k + splits - 1) / splits;
   p.splits = (p.n_k + p.split_k - 1) / p.split_k;  // none of them empty
   p.partial = l.partial;
-  p.ldp = 256ll * H * p.tiles_n;
+  p.ldp = (long long)cols * p.tiles_n;
   if (p.splits > 1 && (size_t)p.splits * o.M * p.ldp * 4 > l.partial_bytes) return PSR_ERR_ARG;
   p.idesc = idesc16(256, 256, AMN, BMN, e.half != 0);
   p.e = e;
@@ -893,11 +947,15 @@ inline int launch_pair(const Operands& o, const Epilogue& e, int splits, Launch&
   const bool ok_a = AMN ? tmap16(&ma, o.a, o.M, o.K, o.lda, 64) : tmap16(&ma, o.a, o.K, o.M, o.lda, kRows);
   const bool ok_b = BMN ? tmap16(&mb, o.b, o.N, o.K, o.ldb, 64) : tmap16(&mb, o.b, o.K, o.N, o.ldb, kRows);
   if (!ok_a || !ok_b) return PSR_ERR_CUDA;
-  const int items = p.tiles_m * p.tiles_n * p.splits;
+  long long items = (long long)p.tiles_m * p.tiles_n * p.splits;
+  if (wide) {
+    p.halves = last_halves(items, n_pairs);
+    items += p.halves;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * (items < n_pairs ? items : n_pairs)));
   cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = PairCfg<H>::kSmem;
+  cfg.dynamicSmemBytes = kPairSmem;
   cfg.stream = l.st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -906,7 +964,7 @@ inline int launch_pair(const Operands& o, const Epilogue& e, int splits, Launch&
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, pair_gemm<H, AMN, BMN>, p, ma, mb) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, pair_gemm<AMN, BMN>, p, ma, mb) != cudaSuccess) {
     cudaGetLastError();
     return PSR_ERR_CUDA;
   }

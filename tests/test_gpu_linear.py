@@ -78,6 +78,11 @@ FORWARD = [  # M N K act bias residual z type
     (513, 264, 1000, "none", True, True, True, "f16"),
     (1000, 8, 24, "silu", True, True, True, "bf16"),
     (1100, 1032, 264, "gelu", True, True, True, "bf16"),
+    (1, 301, 515, "silu", True, True, True, "bf16"),
+    (6, 301, 515, "relu", True, True, True, "f16"),
+    (70, 1001, 515, "gelu", True, True, True, "bf16"),
+    (300, 517, 333, "silu", True, True, True, "f16"),
+    (1300, 901, 77, "relu", True, True, True, "bf16"),
 ]
 
 
@@ -93,6 +98,20 @@ def test_linear(psr, case):
     assert psr.get_stats(ws)["status"] == 0
     assert (z is not None) == save
     check_forward(y, z, x, w, b, r, act, t, str(case))
+
+
+# several rounds of 512-column tiles over the pairs of SMs, with halves of tiles first and last, and an odd last half
+ROUNDS = [(700, 3900, 40), (2600, 2600, 72), (2600, 5200, 64), (5000, 4400, 136), (9000, 1100, 64)]
+
+
+@pytest.mark.parametrize("M,N,K", ROUNDS)
+def test_linear_rounds_of_tiles(psr, M, N, K):
+    need_gpu()
+    g = torch.Generator().manual_seed(M)
+    x, w, b, r = randn(g, (M, K), "bf16"), randn(g, (N, K), "bf16", K**-0.5), randn(g, (N,), "bf16"), randn(g, (M, N), "bf16")
+    y, z, ws = psr.linear(x, w, b, r, activation="relu", save_z=True)
+    assert psr.get_stats(ws)["status"] == 0
+    check_forward(y, z, x, w, b, r, "relu", "bf16", str((M, N, K)))
 
 
 BACKWARD = [  # M N K act type
@@ -111,6 +130,10 @@ BACKWARD = [  # M N K act type
     (511, 136, 1288, "relu", "bf16"),
     (1027, 520, 264, "gelu", "bf16"),
     (2000, 16, 8, "none", "bf16"),
+    (70, 5200, 2600, "relu", "bf16"),
+    (301, 515, 333, "none", "bf16"),
+    (301, 515, 333, "gelu", "f16"),
+    (2600, 136, 5200, "none", "bf16"),
 ]
 
 
