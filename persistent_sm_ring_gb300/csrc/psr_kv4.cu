@@ -20,17 +20,17 @@ struct Cache {
   uint8_t* base;
   const int32_t* table;
   int Hkv, d, page, n_pages, max_pages;
+  int shift;  // page = 1 << shift
 };
 
-__device__ __forceinline__ int block_bytes(int d) { return kBlk * (d + 8); }
-
 // The block that holds position pos of sequence b for KV head h, or null if the table has no usable page there.
+template <int D>
 __device__ __forceinline__ uint8_t* block_of(const Cache& c, int b, int h, long long pos) {
-  if (pos < 0 || pos >= (long long)c.max_pages * c.page) return nullptr;
-  const int pg = c.table[(long long)b * c.max_pages + (int)(pos / c.page)];
-  if (pg < 0 || pg >= c.n_pages) return nullptr;
+  if (pos < 0 || pos >> c.shift >= c.max_pages) return nullptr;
+  const int pg = c.table[(long long)b * c.max_pages + (int)(pos >> c.shift)];
+  if ((uint32_t)pg >= (uint32_t)c.n_pages) return nullptr;
   const int per = c.page / kBlk;
-  return c.base + (((long long)pg * c.Hkv + h) * per + (int)(pos % c.page) / kBlk) * block_bytes(c.d);
+  return c.base + (((long long)pg * c.Hkv + h) * per + (int)(pos & (c.page - 1)) / kBlk) * (kBlk * (D + 8));
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -50,10 +50,12 @@ __device__ __forceinline__ float warp_sum(float v) {
 // ------------------------------------------------------------------------------------------------
 // Memory bound.  D / 8 lanes take a row, eight columns (16 bytes) each; a block takes kTokens tokens of one sequence and KV
 // head, and a lane the K and V rows of two of them, so that four loads are in flight.
+constexpr int kEach = 2;  // tokens of a thread
+
 template <int D>
 struct Rows {
   static constexpr int kLanes = D / 8;           // of a row
-  static constexpr int kTokens = 2 * 256 / kLanes;  // of a block
+  static constexpr int kTokens = kEach * 256 / kLanes;  // of a block
 };
 
 struct MoveParams {
@@ -70,6 +72,16 @@ template <class T>
 struct alignas(16) Eight {
   T e[8];
 };
+template <class T>
+struct Pair {
+  using type = __nv_bfloat162;
+  static __device__ __forceinline__ type zero() { return __float2bfloat162_rn(0.f); }
+};
+template <>
+struct Pair<__half> {
+  using type = __half2;
+  static __device__ __forceinline__ type zero() { return __float2half2_rn(0.f); }
+};
 
 template <class T, int D>
 __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ MoveParams p) {
@@ -79,13 +91,11 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ Mov
   const int first = (blockIdx.x - bh * p.tiles) * R::kTokens + threadIdx.x / R::kLanes;
   const int end = p.count ? min(p.S, p.count[b]) : p.S;
   const long long start = p.start[b];
-  uint8_t* blk[2];
-  Eight<T> raw[2][2];
+  Eight<T> raw[kEach][2];
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    const int i = first + n * (R::kTokens / 2);
-    blk[n] = i < end ? block_of(p.c, b, h, start + i) : nullptr;
-    if (!blk[n]) continue;
+  for (int n = 0; n < kEach; ++n) {
+    const int i = first + n * (R::kTokens / kEach);
+    if (i >= end) continue;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
       const T* x = static_cast<const T*>(p.in[kv]) + b * p.st[kv].b + h * p.st[kv].h + i * p.st[kv].s + part * 8;
@@ -95,43 +105,65 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ Mov
         for (int e = 0; e < 8; ++e) raw[n][kv].e[e] = x[e];
     }
   }
+  uint8_t* blk[kEach];  // looked up while the rows are on their way
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    const int row = (int)((start + first + n * (R::kTokens / 2)) & (kBlk - 1));
+  for (int n = 0; n < kEach; ++n) {
+    const int i = first + n * (R::kTokens / kEach);
+    blk[n] = i < end ? block_of<D>(p.c, b, h, start + i) : nullptr;
+  }
+#pragma unroll
+  for (int n = 0; n < kEach; ++n) {
+    const int row = (int)((start + first + n * (R::kTokens / kEach)) & (kBlk - 1));
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      float v[8], mn = INFINITY, mx = -INFINITY, big = 0.f;
+      // minimum and negated maximum of the row side by side, NaN if there is one; a missing row is all zeros
+      using T2 = typename Pair<T>::type;
+      T2 w[4], low;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[e] = blk[n] ? to_f32(raw[n][kv].e[e]) : 0.f;
-        mn = fminf(mn, v[e]);
-        mx = fmaxf(mx, v[e]);
-        big = v[e] - v[e] != 0.f ? 1.f : big;  // an infinity or a NaN
+      for (int e = 0; e < 4; ++e) w[e] = blk[n] ? reinterpret_cast<const T2*>(&raw[n][kv])[e] : Pair<T>::zero();
+      {
+        const T2 a = __hmin2_nan(__hmin2_nan(w[0], w[1]), __hmin2_nan(w[2], w[3]));
+        const T2 b = __hneg2(__hmax2_nan(__hmax2_nan(w[0], w[1]), __hmax2_nan(w[2], w[3])));
+        T2 first, second;
+        first.x = a.x; first.y = b.x;
+        second.x = a.y; second.y = b.y;
+        low = __hmin2_nan(first, second);
       }
 #pragma unroll
-      for (int o = R::kLanes / 2; o; o >>= 1) {
-        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-      }
+      for (int o = R::kLanes / 2; o; o >>= 1) low = __hmin2_nan(low, __shfl_xor_sync(0xffffffffu, low, o));
       if (!blk[n]) continue;
-      const bool fine = big == 0.f;
+      const float mn = to_f32(low.x), mx = -to_f32(low.y);
+      const bool fine = fabsf(mn) < INFINITY && fabsf(mx) < INFINITY;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = to_f32(raw[n][kv].e[e]);
       // max/15 - min/15: max - min can pass the largest fp32 number
       __nv_bfloat16 sc = __float2bfloat16_rn(__fsub_rn(__fdiv_rn(mx, 15.f), __fdiv_rn(mn, 15.f)));
       __nv_bfloat16 of = __float2bfloat16_rn(mn);
       const float s = __bfloat162float(sc), o = __bfloat162float(of);
       uint32_t codes = 0;
       if (fine && s > 0.f) {
-        // The code is the rounded quotient rounded to an integer.  A product with the reciprocal is within 2^-21 of a
-        // quotient below 16, so only one that close to a half needs the division (and one whose reciprocal overflows).
-        const float inv = __fdividef(1.f, s);
-        const bool plain = s > 1e-37f && s < 1e37f;
+        // The code is the rounded quotient rounded to an integer (adding 1.5 2^23 does that, half to even, and leaves it in the
+        // low bits).  A product with the reciprocal is within 2^-21 of a quotient below 16: only one that near to a half needs
+        // the division.
+        const float inv = __fdividef(1.f, s), magic = 12582912.f;
+        bool near = !(s > 1e-37f && s < 1e37f);  // the reciprocal may have overflowed
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float x = __fsub_rn(v[e], o);
-          float q = x * inv;
-          if (!plain || fabsf(q - floorf(q) - 0.5f) < 1e-4f) q = __fdiv_rn(x, s);
-          codes |= (uint32_t)fminf(fmaxf(rintf(q), 0.f), 15.f) << (4 * e);
+          float q = __fsub_rn(v[e], o) * inv;
+          // a bf16 row's offset is its minimum and 15 rounded steps pass its maximum by less than half of one: nothing to clamp
+          if (!std::is_same<T, __nv_bfloat16>::value) q = fminf(fmaxf(q, 0.f), 15.f);
+          const float r = __fadd_rn(q, magic);
+          near = near || fabsf(q - __fsub_rn(r, magic)) > 0.4999f;
+          codes = __funnelshift_r(codes, __float_as_uint(r), 4);  // the code enters at the top
+        }
+        if (near) {
+          codes = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float q = fminf(fmaxf(__fdiv_rn(__fsub_rn(v[e], o), s), 0.f), 15.f);
+            codes |= (__float_as_uint(__fadd_rn(q, magic)) & 15u) << (4 * e);
+          }
         }
       }
       if (!fine) sc = of = __ushort_as_bfloat16(0x7FFF);
@@ -154,12 +186,12 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ MoveP
   const int first = (blockIdx.x - bh * p.tiles) * R::kTokens + threadIdx.x / R::kLanes;
   const int end = p.count ? min(p.S, p.count[b]) : p.S;
   const long long start = p.start[b];
-  uint32_t codes[2][2] = {};
-  float s[2][2], o[2][2];
+  uint32_t codes[kEach][2] = {};
+  float s[kEach][2], o[kEach][2];
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    const int i = first + n * (R::kTokens / 2), row = (int)((start + i) & (kBlk - 1));
-    const uint8_t* blk = i < end ? block_of(p.c, b, h, start + i) : nullptr;
+  for (int n = 0; n < kEach; ++n) {
+    const int i = first + n * (R::kTokens / kEach), row = (int)((start + i) & (kBlk - 1));
+    const uint8_t* blk = i < end ? block_of<D>(p.c, b, h, start + i) : nullptr;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
       s[n][kv] = 0.f;
@@ -172,8 +204,8 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ MoveP
     }
   }
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    const int i = first + n * (R::kTokens / 2);
+  for (int n = 0; n < kEach; ++n) {
+    const int i = first + n * (R::kTokens / kEach);
     if (i >= p.S) continue;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
@@ -808,6 +840,7 @@ static int check_shape(const psr_kv4_shape* sh) {
   if (!sh) return PSR_ERR_ARG;
   if (sh->B < 0 || sh->S < 0 || sh->Hq < 1 || sh->Hkv < 1 || sh->n_pages < 1 || sh->max_pages < 1) return PSR_ERR_ARG;
   if (sh->type != PSR_BF16 && sh->type != PSR_F16) return PSR_ERR_ARG;
+  if (sh->S > 1 << 28) return PSR_ERR_UNSUPPORTED;
   if (sh->Hq % sh->Hkv != 0 || (sh->d != 64 && sh->d != 128)) return PSR_ERR_UNSUPPORTED;
   if ((double)sh->n_pages * sh->Hkv * sh->page / 16 >= 2147483648.0) return PSR_ERR_UNSUPPORTED;
   if (sh->page < 16 || sh->page > 256 || (sh->page & (sh->page - 1)) != 0) return PSR_ERR_UNSUPPORTED;
@@ -815,9 +848,15 @@ static int check_shape(const psr_kv4_shape* sh) {
   return PSR_OK;
 }
 
+static int log2_of(int page) {
+  int n = 0;
+  while (1 << n < page) ++n;
+  return n;
+}
+
 static Cache cache_of(const psr_kv4_shape* sh, const void* cache, const int32_t* table) {
   return {const_cast<uint8_t*>(static_cast<const uint8_t*>(cache)), table, sh->Hkv, sh->d, sh->page, sh->n_pages,
-          sh->max_pages};
+          sh->max_pages, log2_of(sh->page)};
 }
 
 template <class Go>
@@ -975,7 +1014,7 @@ int psr_kv4_attn(const psr_kv4_shape* sh, const void* q, const psr_strides* qs, 
   p.sq = *qs; p.so = *os;
   p.B = sh->B; p.Hq = sh->Hq; p.S = sh->S;
   p.group = sh->Hq / sh->Hkv;
-  for (int n = sh->page / kBlk; n > 1; n /= 2) ++p.page_shift;
+  p.page_shift = p.c.shift - 4;
   p.vec = rows_aligned(q, qs, sh->B, sh->Hq, sh->S);
   p.vec_o = rows_aligned(o, os, sh->B, sh->Hq, sh->S);
   p.scale = sh->scale > 0.f ? sh->scale : 1.f / sqrtf((float)sh->d);

@@ -269,6 +269,7 @@ static int sizes(const psr_linear_shape* sh, bool backward, Sizes& s) {
   if (sh->M < 0 || sh->N < 1 || sh->K < 1) return PSR_ERR_ARG;
   if (sh->act < PSR_ACT_NONE || sh->act > PSR_ACT_SILU) return PSR_ERR_ARG;
   if (sh->type != PSR_BF16 && sh->type != PSR_F16) return PSR_ERR_ARG;
+  if (sh->M > 1 << 30 || sh->N > 1 << 30 || sh->K > 1 << 30) return PSR_ERR_UNSUPPORTED;
   auto ld = [](long long given, long long contiguous) { return given == 0 ? contiguous : given; };
   s.ldx = ld(sh->ldx, sh->K); s.ldw = ld(sh->ldw, sh->K);
   s.ldr = ld(sh->ldr, sh->N); s.ldy = ld(sh->ldy, sh->N); s.ldz = ld(sh->ldz, sh->N);
