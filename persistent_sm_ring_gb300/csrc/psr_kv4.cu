@@ -224,7 +224,9 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ MoveP
 // (the group's heads times the new tokens); the units of all sequences stand in a line, segment by segment (a segment:
 // sequence, head, row tile), and each warp takes an equal stretch of it, so ragged batches and single long sequences load
 // every SM alike.  A segment that lies within one stretch is finished there; the pieces of one that does not meet in
-// combine_kernel through fp32 partial results and their running maxima and sums, as the ring's chunks do.  (With
+// combine_kernel through fp32 partial results and their running maxima and sums, as the ring's chunks do.  A segment
+// stands in the line behind kPad places without work, so that a stretch of many short ones is not the longest (48 ragged
+// sequences with 4 draft tokens, d = 64: 77 to 68 us).  (With
 // stretches for whole CTAs, whose warps met in shared memory after every segment, batches of short sequences took 3 to 5 us
 // a segment.)
 //
@@ -251,7 +253,7 @@ constexpr int kWarps = 8;
 template <int D>
 constexpr int kStages = D == 128 ? 2 : 4;
 constexpr int kUnit = 2 * kBlk;     // tokens of a unit
-constexpr int kMinUnits = 4;        // of a warp's stretch: short ones would only move work to the join
+constexpr int kPad = 2;             // units that a segment counts for besides its own: loading q and writing results
 constexpr int kMaxCtas = 2 * 152;   // bounds the partial results
 template <int D>
 constexpr int kPart = D + 4;        // floats of a row's partial result: sums, maximum, weight
@@ -281,11 +283,14 @@ __device__ __forceinline__ int blocks_of(const AttnParams& p, int b) {
   return n < 0 || n > (long long)p.c.max_pages * p.c.page ? 0 : (n + kBlk - 1) / kBlk;
 }
 
-// A place in the line of units (fewer than 2^31: checked on the host).
+// Places that a segment of so many blocks takes in the line.
+__device__ __forceinline__ int places(int blocks) { return blocks ? (blocks + 1) / 2 + kPad : 0; }
+
+// A segment of the line (fewer than 2^31 places: checked on the host).
 struct Cursor {
   int b, h, rt, blocks;
-  int start;  // first unit of the segment
-  __device__ __forceinline__ int end() const { return start + (blocks + 1) / 2; }
+  int start;  // its first place
+  __device__ __forceinline__ int end() const { return start + places(blocks); }
   __device__ __forceinline__ void advance(const AttnParams& p, int u) {
     while (u >= end()) {
       start = end();
@@ -300,24 +305,24 @@ struct Cursor {
   }
 };
 
-// One warp: the units of the sequences before `end`.
+// One warp: the places of the sequences before `end`.
 __device__ __forceinline__ int units_before(const AttnParams& p, int end) {
   const int lane = threadIdx.x % 32;
   int sum = 0;
 #pragma unroll 4
-  for (int b = lane; b < end; b += 32) sum += (blocks_of(p, b) + 1) / 2;
+  for (int b = lane; b < end; b += 32) sum += places(blocks_of(p, b));
   return __reduce_add_sync(0xffffffffu, sum) * p.c.Hkv * p.n_rt;
 }
 
-// One warp: the segment that holds a unit (of those there are).
-__device__ __forceinline__ Cursor segment_at(const AttnParams& p, int target) {
+// One warp: the segment that holds a place (of those there are).  mine: the blocks of sequence `lane`, already at hand.
+__device__ __forceinline__ Cursor segment_at(const AttnParams& p, int target, int mine) {
   const int lane = threadIdx.x % 32;
   const int per = p.c.Hkv * p.n_rt;
   Cursor cur = {};
   int base = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int n = b0 + lane < p.B ? blocks_of(p, b0 + lane) : 0;
-    const int own = (n + 1) / 2 * per;
+    const int n = b0 == 0 ? mine : b0 + lane < p.B ? blocks_of(p, b0 + lane) : 0;
+    const int own = places(n) * per;
     int sum = own;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -329,7 +334,7 @@ __device__ __forceinline__ Cursor segment_at(const AttnParams& p, int target) {
       const int at = __ffs(__ballot_sync(0xffffffffu, target < base + sum)) - 1;
       const int first = base + __shfl_sync(0xffffffffu, sum - own, at);
       cur.blocks = __shfl_sync(0xffffffffu, n, at);
-      const int len = (cur.blocks + 1) / 2, seg = (target - first) / len;
+      const int len = places(cur.blocks), seg = (target - first) / len;
       cur.b = b0 + at;
       cur.h = seg / p.n_rt;
       cur.rt = seg % p.n_rt;
@@ -341,10 +346,10 @@ __device__ __forceinline__ Cursor segment_at(const AttnParams& p, int target) {
   return cur;
 }
 
-// Units of a warp's stretch: an equal share.
+// Places of a warp's stretch: an equal share.
 __device__ __forceinline__ int share(int total, int ctas) {
   const int per = (total + ctas * kWarps - 1) / (ctas * kWarps);
-  return per < kMinUnits ? kMinUnits : per;
+  return per < 1 ? 1 : per;
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -400,15 +405,19 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
   constexpr int S = kStages<D>;
   clear_ctrl(p.ctrl);
   launch_dependents();
-  const int total = units_before(p, p.B), per = share(total, gridDim.x);
+  const int mine = lane < p.B ? blocks_of(p, lane) : 0;
+  int total = places(mine);
+  for (int b = lane + 32; b < p.B; b += 32) total += places(blocks_of(p, b));
+  total = __reduce_add_sync(0xffffffffu, total) * p.c.Hkv * p.n_rt;
+  const int per = share(total, gridDim.x);
   if (slot > (total - 1) / per) return;  // (total 0: slot 0 finds an empty stretch below)
   const int u0 = slot * per, u1 = min(u0 + per, total);
   if (u0 >= u1) return;
-  Cursor seg = segment_at(p, u0);
+  Cursor seg = segment_at(p, u0, mine);
 
-  // ---- the ring: unit u0 + k goes to stage k % S; a unit's pages are looked up one unit ahead of its copy -----------
+  // ---- the ring: the stretch's unit k goes to stage k % S; a unit's pages are looked up one unit ahead of its copy -----------
   Cursor pre = seg;
-  int next = u0, pre_end = seg.end(), pg0 = 0, pg1 = 0, off = 0;
+  int next = u0, pre_end = seg.end(), pg0 = 0, pg1 = 0, off = 0, filled = 0;
   const int32_t* row = p.c.table + (long long)seg.b * p.c.max_pages;
   const int in_page = (1 << p.page_shift) - 1, per_page = p.c.Hkv << p.page_shift;  // blocks of a page, and of all heads
   const uint8_t* lane_base = p.c.base + lane * 16;
@@ -420,7 +429,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
       pre_end = pre.end();
       row = p.c.table + (long long)pre.b * p.c.max_pages;
     }
-    const int blk = 2 * (next - pre.start);
+    next = max(next, pre.start + kPad);
+    const int blk = 2 * (next - pre.start - kPad);  // (past the stretch's end: a block of the segment all the same)
     pg0 = row[blk >> p.page_shift];
     off = (pre.h << p.page_shift) + (blk & in_page);
     pg1 = 0;  // any page: a last block without a second one reads what is there, and masks it
@@ -428,7 +438,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
   };
   auto fill = [&]() {
     if (next < u1) {
-      const int s = (next - u0) % S;
+      const int s = filled++ % S;
       if ((uint32_t)pg0 < (uint32_t)p.c.n_pages && (uint32_t)pg1 < (uint32_t)p.c.n_pages) {
         constexpr int kChunks = kBytes / 16;  // of a block
         // (fewer than 2^31 blocks: checked on the host)
@@ -452,9 +462,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
   look_up();
   for (int s = 0; s < S; ++s) fill();
 
-  for (int lo = u0; lo < u1;) {
+  int used = 0;
+  for (int lo = u0, hi; lo < u1; lo = hi) {
     seg.advance(p, lo);
-    const int hi = min(seg.end(), u1);
+    const int begin = seg.start + kPad, from = max(lo, begin);
+    hi = min(seg.end(), u1);
+    if (from >= hi) continue;
     const int n = p.lens[seg.b];
     const int R = p.group * p.S;  // query rows of the KV head: row = new token * group + head of the group
     // ---- query fragments: the row g of each tile, columns in the order of the K codes' words -----
@@ -691,8 +704,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
     };
     // ---- the units of the segment --------------------------------------------------------------------
     const int all_see = n - p.S;  // the last position that every row sees
-    for (int u = lo; u < hi; ++u) {
-      const int s = (u - u0) % S;
+    for (int u = from; u < hi; ++u) {
+      const int s = used++ % S;
       copy_wait<S - 1>();
       __syncwarp();  // every lane's copies are there
       if (bad >> s & 1u) {
@@ -700,7 +713,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) l[nt][0] = l[nt][1] = NAN;
       } else {
-        const int j0 = (u - seg.start) * kUnit;
+        const int j0 = (u - begin) * kUnit;
         if (j0 + kUnit - 1 <= all_see) unit(sm.ring[warp][s], j0, std::false_type());
         else unit(sm.ring[warp][s], j0, std::true_type());
       }
@@ -708,7 +721,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
       fill();
     }
     // ---- the results: o if the segment is whole, else a piece ----------------------------------------
-    const bool whole = lo == seg.start && hi == seg.end();
+    const bool whole = from == begin && hi == seg.end();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -757,7 +770,6 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
           }
         }
       }
-    lo = hi;
   }
 }
 
@@ -776,7 +788,7 @@ __global__ void __launch_bounds__(1024) combine_kernel(const __grid_constant__ A
   // where the segment begins, and how many units there are
   const int blocks = blocks_of(p, b), len = (blocks + 1) / 2;
   const int per = share(units_before(p, p.B), ctas);
-  const int start = units_before(p, b) + (h * p.n_rt + rt) * len;
+  const int start = units_before(p, b) + (h * p.n_rt + rt) * places(blocks), first = start + kPad;
   // No warp leaves before the kernel that writes the pieces has ended: what follows on the stream may rely on both.
   wait_previous();
   if (at >= rows) return;
@@ -790,7 +802,7 @@ __global__ void __launch_bounds__(1024) combine_kernel(const __grid_constant__ A
     if (lane == 0) *lse = empty ? -INFINITY : NAN;
     return;
   }
-  const int c0 = start / per, c1 = (start + len - 1) / per;
+  const int c0 = first / per, c1 = (first + len - 1) / per;
   if (c0 == c1) return;
   float top = kLowest, sum = 0.f, acc[E] = {};
 #pragma unroll 4
@@ -1002,7 +1014,7 @@ int psr_kv4_attn(const psr_kv4_shape* sh, const void* q, const psr_strides* qs, 
   if (ws_bytes < psr_kv4_attn_workspace_bytes(sh)) return PSR_ERR_ARG;
   const long long rows = (long long)sh->B * sh->Hq * sh->S;
   const long long tiles = ((long long)sh->Hq / sh->Hkv * sh->S + 7) / 8;
-  if (rows >= (1LL << 30) || (double)sh->B * sh->Hkv * tiles * ((double)sh->max_pages * sh->page / kUnit + 1) >= 2147483648.0)
+  if (rows >= (1LL << 30) || (double)sh->B * sh->Hkv * tiles * ((double)sh->max_pages * sh->page / kUnit + 1 + kPad) >= 2147483648.0)
     return PSR_ERR_UNSUPPORTED;
   int n_sm = 0, dev = 0;
   if ((rc = check_device(&n_sm)) != PSR_OK) return rc;
