@@ -82,7 +82,8 @@ __device__ __forceinline__ float act_slope(int act, float z) {
     }
     case PSR_ACT_GELU_TANH: {
       const float s = sigmoid(1.5957691216057307f * (z + 0.044715f * z * z * z));
-      return s + z * s * (1.f - s) * 1.5957691216057307f * (1.f + 0.134145f * z * z);
+      const float q = s * (1.f - s);  // 0 far from 0, where z^2 may be infinite
+      return q == 0.f ? s : s + z * q * 1.5957691216057307f * (1.f + 0.134145f * z * z);
     }
     case PSR_ACT_SILU: {
       const float s = sigmoid(z);

@@ -263,3 +263,16 @@ def test_linear_bwd_is_the_gradient(psr, act):
         want = (f(1e-5) - f(-1e-5)) / 2e-5
         # z, dz and the gradients are fp16 (2^-11 each, random signs); relu changes slope where a difference crosses 0
         assert abs((grads[i] * step).sum() - want) <= 2.0**-8 * np.linalg.norm(grads[i]) * 4, (act, i)
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_linear_bwd_of_large_z(psr, act):
+    # where the square of z is infinite in fp32 the slopes are still 0 and 1
+    need_gpu()
+    z = torch.tensor([[-3e38, -1e20, -1e10, -300.0, 300.0, 1e10, 1e20, 3e38]] * 2, dtype=torch.bfloat16, device="cuda")
+    one = torch.ones((8, 8), dtype=torch.bfloat16, device="cuda")
+    db = psr.linear_bwd(torch.ones_like(z), one[:2], one, z, activation=act, need_dx=False, need_dw=False)[2]
+    want = torch.ones_like(db) if act == "none" else (z[0] > 0).to(torch.bfloat16)
+    assert torch.equal(db, 2 * want), (act, db)
+    dx = psr.linear_bwd(torch.ones_like(z), one[:2], one, z, activation=act, need_dw=False, need_db=False)[0]
+    assert torch.equal(dx, torch.full_like(dx, 8.0 if act == "none" else 4.0)), act
