@@ -566,15 +566,28 @@ def _span(t):
     return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
 
 
-def _check_apart(out, x, what, same_ok):
-    """`out` shares no memory with `x`, or is `x` itself where that is allowed."""
+def _check_apart(out, x, what, same_ok, kinds="an output overlaps an input"):
+    """`out` shares no memory with `x`, or is `x` itself where that is allowed.  Column ranges of the same rows are
+    apart."""
     if out.numel() == 0 or x.numel() == 0:
         return
     if same_ok and out.data_ptr() == x.data_ptr() and out.stride() == x.stride():
         return
     (a, b), (c, d) = _span(out), _span(x)
     if a < d and c < b:
-        raise ValueError(f"{what}: an output overlaps an input")
+        ld, size = out.stride(0), out.element_size()
+        if out.dim() == x.dim() == 2 and x.stride(0) == ld and size == x.element_size() and (a - c) % size == 0:
+            right = (a - c) // size % ld  # out's first column, counted from x's
+            if right >= x.shape[1] and ld - right >= out.shape[1]:
+                return
+        raise ValueError(f"{what}: {kinds}")
+
+
+def _check_other(out, x, what, kinds):
+    """Of [B, H, S, d] tensors: `out` is not `x`, and shares nothing with it if both are contiguous (views of one buffer
+    may lie between one another)."""
+    if out.data_ptr() == x.data_ptr() or (out.is_contiguous() and x.is_contiguous()):
+        _check_apart(out, x, what, False, kinds)
 
 
 def rotary_table(rot, base=10000.0, *, scaling="plain", factor=1.0, original_length=0, beta_fast=32.0, beta_slow=1.0,
@@ -601,7 +614,7 @@ def rotary(q, k, table, *, P=1, causal=CAUSAL, positions=None, offset=0, interle
 
     positions: int64 [S] or [B, S]; None takes offset + the global position of each row in the ring's shard order
     (P, causal as for ring_attn_fwd).  Returns (q_out, k_out), contiguous unless passed in; an output may be its own
-    input."""
+    input, and shares no element with the other input or output."""
     _check_cuda(q, "q", 4)
     B, Hq, S, d = q.shape
     dev, dtype = q.device, q.dtype
@@ -625,6 +638,12 @@ def rotary(q, k, table, *, P=1, causal=CAUSAL, positions=None, offset=0, interle
         if out is not None:
             _check_like(out, name, x.shape, dtype, dev)
             _check_apart(out, x, "rotary", True)
+    if k is not None:
+        for out, x in ((q_out, k), (k_out, q)):
+            if out is not None:
+                _check_other(out, x, "rotary", "an output overlaps the other input")
+        if q_out is not None and k_out is not None:
+            _check_other(q_out, k_out, "rotary", "the outputs overlap")
     qs, qos = _heads_strides(q, "q"), None if q_out is None else _heads_strides(q_out, "q_out", True)
     ks, kos = None if k is None else _heads_strides(k, "k"), None if k_out is None else _heads_strides(k_out, "k_out", True)
     with _Launch(dev, stream, "rotary") as at:
@@ -767,6 +786,9 @@ def linear_bwd(dy, x, w, z=None, *, activation="none", need_dx=True, need_dw=Tru
             for u in (dy, x, w, z):
                 if u is not None:
                     _check_apart(t, u, "linear_bwd", False)
+    for a, b in ((dx, dw), (dx, db), (dw, db)):
+        if a is not None and b is not None:
+            _check_apart(a, b, "linear_bwd", False, "the outputs overlap")
     lib = load()
     with _Launch(dev, stream, "linear_bwd") as at:
         outs = [at.empty(shape, dtype) if t is None and need else t for need, t, _, shape in wanted]

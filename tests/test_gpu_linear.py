@@ -276,3 +276,16 @@ def test_linear_bwd_of_large_z(psr, act):
     assert torch.equal(db, 2 * want), (act, db)
     dx = psr.linear_bwd(torch.ones_like(z), one[:2], one, z, activation=act, need_dw=False, need_db=False)[0]
     assert torch.equal(dx, torch.full_like(dx, 8.0 if act == "none" else 4.0)), act
+
+
+def test_linear_between_columns_of_one_buffer(psr):
+    # input, output, z and residual as column ranges of the same rows
+    need_gpu()
+    for M in (1, 20, 300):
+        g = torch.Generator().manual_seed(M)
+        rows = randn(g, (M, 136 + 3 * 264), "bf16")
+        w, keep = randn(g, (264, 136), "bf16", 0.1), rows.clone()
+        cut = lambda t, i: t[:, 136 + 264 * i:136 + 264 * (i + 1)]
+        y, z, _ = psr.linear(rows[:, :136], w, None, cut(rows, 2), activation="gelu", out=cut(rows, 0), z=cut(rows, 1))
+        check_forward(y, z, keep[:, :136], w, None, cut(keep, 2), "gelu", "bf16", "one buffer")
+        assert torch.equal(rows[:, :136], keep[:, :136]) and torch.equal(cut(rows, 2), cut(keep, 2))

@@ -302,3 +302,28 @@ def test_kv4_binding_refuses(psr, fake_device):
     bad("lse must be contiguous", q, cache, table, n, lse=torch.zeros((3, 4, 2))[..., :1])
     bad("overlaps an input", q, cache, table, n, out=q)
     bad("elements overlap", q, cache, table, n, out=torch.zeros((3, 1, 1, 64), dtype=BF).expand(3, 4, 1, 64))
+
+
+def test_outputs_that_share_memory(psr, fake_device):
+    q, k, table = torch.zeros((2, 4, 6, 64), dtype=BF), torch.zeros((2, 4, 6, 64), dtype=BF), torch.zeros(32, dtype=torch.int64)
+    _refused(psr.rotary, "overlaps the other input", q, k, table, q_out=k)
+    _refused(psr.rotary, "overlaps the other input", q, k, table, k_out=q)
+    out = torch.zeros_like(q)
+    _refused(psr.rotary, "the outputs overlap", q, k, table, q_out=out, k_out=out)
+    x, w = torch.zeros((16, 16), dtype=BF), torch.zeros((16, 16), dtype=BF)
+    dy, g = torch.zeros((16, 16), dtype=BF), torch.zeros((16, 16), dtype=BF)
+    _refused(psr.linear_bwd, "the outputs overlap", dy, x, w, dx=g, dw=g)
+    _refused(psr.linear_bwd, "the outputs overlap", dy, x, w, dw=g, db=g[3])
+
+
+def test_columns_of_the_same_rows_are_apart(psr):
+    rows = torch.zeros((5, 40), dtype=BF)
+    apart = lambda a, b: psr._check_apart(a, b, "linear", False)
+    apart(rows[:, 16:], rows[:, :16])
+    apart(rows[:, :16], rows[:, 16:])
+    apart(rows[1:, :16], rows[:-1, 16:])
+    apart(rows[:-1, 30:], rows[1:, :30])
+    for a, b in ((rows[:, 15:], rows[:, :16]), (rows[:, :17], rows[:, 16:]), (rows[1:, 10:], rows[:-1, :11]),
+                 (rows[:, :8], rows[::2, 8:16])):
+        with pytest.raises(ValueError, match="overlaps an input"):
+            apart(a, b)
