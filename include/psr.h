@@ -394,7 +394,7 @@ PSR_API int psr_rotary_table(int rot, double base, int scaling, double factor, d
                              double beta_fast, double beta_slow, uint64_t* table);
 
 /* q, k (read) and q_out, k_out (written): device, strides as given; an output may be its own input
- * (same pointer and strides).  k, k_out and their strides may be NULL when Hkv = 0.  table: device, rot/2
+ * (same pointer and strides) and shares no element with the other input or output.  k, k_out and their strides may be NULL when Hkv = 0.  table: device, rot/2
  * words; positions: device, or NULL. */
 PSR_API int psr_rotary(const psr_rotary_shape* shape, const void* q, const psr_strides* q_strides, void* q_out,
                        const psr_strides* q_out_strides, const void* k, const psr_strides* k_strides, void* k_out,
@@ -408,8 +408,9 @@ PSR_API int psr_rotary(const psr_rotary_shape* shape, const void* q, const psr_s
 #define PSR_ACT_GELU_TANH 3 /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
 #define PSR_ACT_SILU 4      /* z / (1 + exp(-z)) */
 
-/* Row strides are in elements; 0 selects the contiguous one.  Any M >= 0, N >= 1, K >= 1.  Tensors whose rows
- * all start on 16-byte boundaries run on the tensor cores; others take a slower kernel. */
+/* Row strides are in elements; 0 selects the contiguous one.  M >= 0, N >= 1, K >= 1, each at most 2^30.  Operands of a
+ * product whose row stride is not a multiple of 8 are copied to rows that are (the workspace grows by them); one
+ * whose first element is not on a 16-byte boundary makes its products run on the fp32 units, some fifty times slower. */
 typedef struct {
   int M, N, K;
   int act;  /* PSR_ACT_* */
@@ -421,7 +422,8 @@ typedef struct {
 PSR_API size_t psr_linear_workspace_bytes(const psr_linear_shape* shape, int backward);
 
 /* z = x w^T + bias,  y = act(z) + residual: fp32 accumulation, y and z each rounded once.
- *   x, w: device; bias [N], residual: device or NULL; y: device (written; may be the residual itself);
+ *   x, w: device; bias [N], residual: device or NULL; y: device (written; may be the residual itself, and shares no
+ *   element with the other tensors);
  *   z: device or NULL (written; what psr_linear_bwd reads);
  *   workspace: device, >= psr_linear_workspace_bytes(shape, 0), 256-byte aligned; not shared by launches in flight;
  *   timeout_ms: bound on every device wait (<= 0: 2000 ms), reported by psr_get_stats. */
@@ -447,7 +449,7 @@ PSR_API int psr_linear_bwd(const psr_linear_shape* shape, const void* dy, const 
  * Page numbers outside [0, n_pages) and positions outside the table are never read or written. */
 typedef struct {
   int B, Hq, Hkv;              /* sequences, query heads, KV heads; Hq % Hkv == 0 */
-  int S;                       /* new tokens of each sequence */
+  int S;                       /* new tokens of each sequence, at most 2^28 */
   int d;                       /* 64 or 128 */
   int page, n_pages, max_pages; /* tokens of a page (16, 32, 64, 128 or 256), pages of the cache, columns of the table */
   int type;                    /* PSR_BF16 or PSR_F16, of q, k, v, o */

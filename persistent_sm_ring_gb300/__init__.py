@@ -707,7 +707,8 @@ def _workspace(at, workspace, need, what):
 
 
 def linear_workspace_bytes(M, N, K, *, activation="none", backward=False) -> int:
-    """Bytes of workspace that linear() or linear_bwd() needs."""
+    """Bytes of workspace that linear() or linear_bwd() needs for contiguous tensors, or views whose row strides are
+    multiples of 8 elements."""
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
     n = load().psr_linear_workspace_bytes(LinearShape(int(M), int(N), int(K), ACTIVATIONS[activation], BF16),

@@ -38,12 +38,6 @@ __device__ __forceinline__ float warp_max(float v) {
   for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
-__device__ __forceinline__ float warp_min(float v) { return -warp_max(-v); }
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
 
 // ------------------------------------------------------------------------------------------------
 // Append and read
@@ -226,9 +220,8 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ MoveP
 // every SM alike.  A segment that lies within one stretch is finished there; the pieces of one that does not meet in
 // combine_kernel through fp32 partial results and their running maxima and sums, as the ring's chunks do.  A segment
 // stands in the line behind kPad places without work, so that a stretch of many short ones is not the longest (48 ragged
-// sequences with 4 draft tokens, d = 64: 77 to 68 us).  (With
-// stretches for whole CTAs, whose warps met in shared memory after every segment, batches of short sequences took 3 to 5 us
-// a segment.)
+// sequences with 4 draft tokens, d = 64: 77 to 68 us).  (With stretches for whole CTAs, whose warps met in shared memory
+// after every segment, batches of short sequences took 3 to 5 us a segment.)
 //
 // Each warp has its own ring of stages, filled a unit or more ahead with 16-byte asynchronous copies by all of its lanes, and
 // its own softmax state.  (One lane's bulk copy and barrier took 700 clocks of a unit's 2200 at d = 64.)
@@ -254,6 +247,7 @@ template <int D>
 constexpr int kStages = D == 128 ? 2 : 4;
 constexpr int kUnit = 2 * kBlk;     // tokens of a unit
 constexpr int kPad = 2;             // units that a segment counts for besides its own: loading q and writing results
+constexpr int kMaxPlaces = 2130706432;  // 2^31 - 2^24: a place plus a stretch stays an int
 constexpr int kMaxCtas = 2 * 152;   // bounds the partial results
 template <int D>
 constexpr int kPart = D + 4;        // floats of a row's partial result: sums, maximum, weight
@@ -286,7 +280,7 @@ __device__ __forceinline__ int blocks_of(const AttnParams& p, int b) {
 // Places that a segment of so many blocks takes in the line.
 __device__ __forceinline__ int places(int blocks) { return blocks ? (blocks + 1) / 2 + kPad : 0; }
 
-// A segment of the line (fewer than 2^31 places: checked on the host).
+// A segment of the line (fewer than kMaxPlaces places: checked on the host).
 struct Cursor {
   int b, h, rt, blocks;
   int start;  // its first place
@@ -410,9 +404,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
   for (int b = lane + 32; b < p.B; b += 32) total += places(blocks_of(p, b));
   total = __reduce_add_sync(0xffffffffu, total) * p.c.Hkv * p.n_rt;
   const int per = share(total, gridDim.x);
-  if (slot > (total - 1) / per) return;  // (total 0: slot 0 finds an empty stretch below)
+  if (total == 0 || slot > (total - 1) / per) return;
   const int u0 = slot * per, u1 = min(u0 + per, total);
-  if (u0 >= u1) return;
   Cursor seg = segment_at(p, u0, mine);
 
   // ---- the ring: the stretch's unit k goes to stage k % S; a unit's pages are looked up one unit ahead of its copy -----------
@@ -1014,7 +1007,7 @@ int psr_kv4_attn(const psr_kv4_shape* sh, const void* q, const psr_strides* qs, 
   if (ws_bytes < psr_kv4_attn_workspace_bytes(sh)) return PSR_ERR_ARG;
   const long long rows = (long long)sh->B * sh->Hq * sh->S;
   const long long tiles = ((long long)sh->Hq / sh->Hkv * sh->S + 7) / 8;
-  if (rows >= (1LL << 30) || (double)sh->B * sh->Hkv * tiles * ((double)sh->max_pages * sh->page / kUnit + 1 + kPad) >= 2147483648.0)
+  if (rows >= (1LL << 30) || (double)sh->B * sh->Hkv * tiles * ((double)sh->max_pages * sh->page / kUnit + 1 + kPad) >= kMaxPlaces)
     return PSR_ERR_UNSUPPORTED;
   int n_sm = 0, dev = 0;
   if ((rc = check_device(&n_sm)) != PSR_OK) return rc;

@@ -569,8 +569,8 @@ constexpr int kStreamSmem = 1024 + kStreamArea;
 struct StreamParams {
   int M, N;        // tokens, output columns (the rows of W)
   int n_k;         // K steps
-  int tb, n_tb;    // tokens of a block (a multiple of 16, at most 256), token blocks
-  int n_tiles;     // ceil(N / 128) * n_tb; tile = column tile * n_tb + token block
+  int tb;          // columns of a tile: M rounded up to a multiple of 16
+  int n_tiles;     // ceil(N / 128)
   int per_cta;     // units (tile, K step) of a CTA, in order
   int stages;
   uint32_t tmem_cols;
@@ -651,14 +651,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         }
         mbar_expect_tx(&sc.full[s], stage_bytes);
         const uint32_t base = smem_base + s * stage_bytes;
-        const int wrow = tile / p.n_tb * kRows, k = ks * kBK;
+        const int wrow = tile * kRows, k = ks * kBK;
         if constexpr (AMN) {
           tma_load_2d(base, &mw, wrow, k, &sc.full[s]);
           tma_load_2d(base + 8192, &mw, wrow + 64, k, &sc.full[s]);
         } else {
           tma_load_2d(base, &mw, k, wrow, &sc.full[s]);
         }
-        tma_load_2d(base + kHalf, &mx, k, tile % p.n_tb * p.tb, &sc.full[s]);
+        tma_load_2d(base + kHalf, &mx, k, 0, &sc.full[s]);
         ++fills;
         if (++ks == p.n_k) {
           ks = 0;
@@ -708,17 +708,17 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       ok = __all_sync(0xffffffffu, wait_own(&sc.acc_full[slot], (seg / 2) & 1u, p, &sc, SITE_ACC));
       if (!ok) break;
       tc_fence_after();
-      const int j = tile / p.n_tb * kRows + row, i0 = tile % p.n_tb * p.tb;
+      const int j = tile * kRows + row;
       const bool whole = n == p.n_k;
       const float bias = whole && p.e.bias && j < p.N ? load16(p.e.bias, j, p.e.half) : 0.f;
       float* part = p.partial + (2ll * blockIdx.x + (u == u0 ? 0 : 1)) * p.tb * kRows + row;
       const uint32_t tacc = sc.tmem_base + ((uint32_t)(quarter * 32) << 16) + slot * p.tb;
 #pragma unroll 1
-      for (int c = 0; c < p.tb && i0 + c < p.M; c += 16) {
+      for (int c = 0; c < p.M; c += 16) {
         uint32_t v[16];
         tmem_ld16(tacc + c, v);
         tmem_ld_wait();
-        const int n_c = min(16, p.M - i0 - c);
+        const int n_c = min(16, p.M - c);
         if (!whole) {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
@@ -735,14 +735,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           float f[4], r[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const long long i = i0 + c + e + q;
+            const long long i = c + e + q;
             f[q] = own[(e + q) * 32] + bias;
             r[q] = p.e.res && e + q < n_c ? load16(p.e.res, i * p.e.ldr + j, p.e.half) : 0.f;
           }
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             if (e + q >= n_c) break;
-            const long long i = i0 + c + e + q;
+            const long long i = c + e + q;
             if (p.e.z) store16(p.e.z, i * p.e.ldz + j, p.e.half, f[q]);
             if (p.e.act) f[q] = act_call(p.e.act, f[q]);
             store16(p.e.y, i * p.e.ldy + j, p.e.half, f[q] + r[q]);
@@ -783,14 +783,14 @@ __global__ void __launch_bounds__(128) stream_join(const __grid_constant__ Strea
   const int tile = blockIdx.x;
   const long long b = (long long)tile * p.n_k, e = b + p.n_k;
   const int c0 = (int)(b / p.per_cta), c1 = (int)((e - 1) / p.per_cta);
-  const int j = tile / p.n_tb * kRows + threadIdx.x, c = blockIdx.y, i = tile % p.n_tb * p.tb + c;
+  const int j = tile * kRows + threadIdx.x, i = blockIdx.y;
   wait_previous();  // before any exit: what follows on the stream may rely on the products' kernel too
-  if (c0 == c1 || i >= p.M) return;
+  if (c0 == c1) return;
   float sum = 0.f;
 #pragma unroll 4
   for (int g = c0; g <= c1; ++g) {
     const int slot = 2 * g + ((long long)g * p.per_cta >= b ? 0 : 1);  // the tile that CTA g begins or ends with
-    sum += p.partial[((long long)slot * p.tb + c) * kRows + threadIdx.x];
+    sum += p.partial[((long long)slot * p.tb + i) * kRows + threadIdx.x];
   }
   if (j < p.N) finish(p.e, i, j, sum);
 }
@@ -1015,8 +1015,7 @@ inline int launch_stream(const Operands& o, const Epilogue& e, Launch& l) {
   p.N = o.N;
   p.n_k = (o.K + kBK - 1) / kBK;
   p.tb = (o.M + 15) / 16 * 16;
-  p.n_tb = 1;
-  p.n_tiles = (o.N + kRows - 1) / kRows * p.n_tb;
+  p.n_tiles = (o.N + kRows - 1) / kRows;
   const int most = n_sm < kStreamCtas ? n_sm : kStreamCtas;
   const long long units = (long long)p.n_tiles * p.n_k;
   long long per = (units + most - 1) / most;
