@@ -408,14 +408,19 @@ PSR_API int psr_rotary(const psr_rotary_shape* shape, const void* q, const psr_s
 #define PSR_ACT_GELU_TANH 3 /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
 #define PSR_ACT_SILU 4      /* z / (1 + exp(-z)) */
 
-/* Row strides are in elements; 0 selects the contiguous one.  M >= 0, N >= 1, K >= 1, each at most 2^30.  Operands of a
- * product whose row stride is not a multiple of 8 are copied to rows that are (the workspace grows by them); one
- * whose first element is not on a 16-byte boundary makes its products run on the fp32 units, some fifty times slower. */
+/* Row strides are in elements; 0 selects the contiguous one.  M >= 0, N >= 1, K >= 1, each at most 2^30.  The products want
+ * rows of x, w and (psr_linear_bwd without an activation) dy that start on 16-byte boundaries.  Others are copied into the
+ * workspace first, which grows by them: those with a stride that is not a multiple of 8, and those that `odd` names because
+ * their first element is not on such a boundary. */
+#define PSR_LINEAR_ODD_X 1
+#define PSR_LINEAR_ODD_W 2
+#define PSR_LINEAR_ODD_DY 4
 typedef struct {
   int M, N, K;
   int act;  /* PSR_ACT_* */
   int type; /* PSR_BF16 or PSR_F16, of every tensor */
   long long ldx, ldw, ldr, ldy, ldz; /* x [M][K], w [N][K], residual [M][N], y (dy) [M][N], z [M][N] */
+  int odd;  /* PSR_LINEAR_ODD_* of the operands that may start anywhere */
 } psr_linear_shape;
 
 /* Bytes of device workspace psr_linear (backward = 0) or psr_linear_bwd (1) needs; 0 if invalid. */

@@ -68,7 +68,7 @@ class RotaryShape(ctypes.Structure):
 class LinearShape(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int), ("act", ctypes.c_int),
                 ("type", ctypes.c_int), ("ldx", ctypes.c_longlong), ("ldw", ctypes.c_longlong),
-                ("ldr", ctypes.c_longlong), ("ldy", ctypes.c_longlong), ("ldz", ctypes.c_longlong)]
+                ("ldr", ctypes.c_longlong), ("ldy", ctypes.c_longlong), ("ldz", ctypes.c_longlong), ("odd", ctypes.c_int)]
 
 
 class Kv4Shape(ctypes.Structure):
@@ -681,7 +681,8 @@ def _linear_shape(x, w, activation, what):
     M, K = x.shape
     N = w.shape[0]
     _check_like(w, "w", (N, K), x.dtype, x.device)
-    sh = LinearShape(M, N, K, ACTIVATIONS[activation], code, _row_stride(x, "x"), _row_stride(w, "w"), 0, 0, 0)
+    sh = LinearShape(M, N, K, ACTIVATIONS[activation], code, _row_stride(x, "x"), _row_stride(w, "w"), 0, 0, 0,
+                     (1 if x.data_ptr() % 16 else 0) | (2 if w.data_ptr() % 16 else 0))
     return sh, M, N, K
 
 
@@ -708,7 +709,7 @@ def _workspace(at, workspace, need, what):
 
 def linear_workspace_bytes(M, N, K, *, activation="none", backward=False) -> int:
     """Bytes of workspace that linear() or linear_bwd() needs for contiguous tensors, or views whose row strides are
-    multiples of 8 elements."""
+    multiples of 8 elements and that start on 16-byte boundaries."""
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
     n = load().psr_linear_workspace_bytes(LinearShape(int(M), int(N), int(K), ACTIVATIONS[activation], BF16),
@@ -775,6 +776,8 @@ def linear_bwd(dy, x, w, z=None, *, activation="none", need_dx=True, need_dw=Tru
     dev, dtype = x.device, x.dtype
     _check_like(dy, "dy", (M, N), dtype, dev)
     sh.ldy = _row_stride(dy, "dy")
+    if dy.data_ptr() % 16:
+        sh.odd |= 4
     if activation != "none":
         if z is None:
             raise ValueError(f"linear_bwd: activation {activation!r} needs the forward's z")

@@ -1,8 +1,7 @@
 // The linear layer y = act(x w^T + bias) + residual and its gradients on sm_103a.
 //
 // The products are the tcgen05 kernels of psr_linear_mma.cuh.  A tensor map wants rows that start on 16-byte boundaries: an
-// operand with other strides is copied into the workspace first (4100 columns: 0.09 ms of 0.26 at 8192 x 4096 x 4100).  What is
-// left, an odd base address, takes a plain tiled product on the fp32 units.
+// operand with others is copied into the workspace first (4100 columns: 0.09 ms of 0.21 at 8192 x 4096 x 4100).
 #include <cmath>
 #include <cstring>
 
@@ -13,56 +12,8 @@
 namespace psr {
 namespace linear {
 
-// C[i][j] = sum_k A(i, k) B(j, k), A(i, k) = a[i lda + k] (or a[k lda + i] with AT), B alike: 64 x 64 tiles in
-// shared memory, 4 x 4 sums a thread.
-template <class T, bool AT, bool BT>
-__global__ void __launch_bounds__(256)
-    simple_gemm(const T* __restrict__ a, long long lda, const T* __restrict__ b, long long ldb, int M, int N, int K,
-                const Epilogue e, Ctrl* clear) {
-  clear_ctrl(clear);
-  __shared__ float sa[16][68], sb[16][68];
-  const long long i0 = (long long)blockIdx.x * 64;
-  const int j0 = blockIdx.y * 64;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < K; k0 += 16) {
-    for (int t = threadIdx.x; t < 64 * 16; t += 256) {
-      const int ka = AT ? t / 64 : t % 16, ia = AT ? t % 64 : t / 16;
-      const bool oka = k0 + ka < K && i0 + ia < M;
-      sa[ka][ia] = oka ? to_f32(AT ? a[(long long)(k0 + ka) * lda + i0 + ia] : a[(i0 + ia) * lda + k0 + ka]) : 0.f;
-      const int kb = BT ? t / 64 : t % 16, jb = BT ? t % 64 : t / 16;
-      const bool okb = k0 + kb < K && j0 + jb < N;
-      sb[kb][jb] = okb ? to_f32(BT ? b[(long long)(k0 + kb) * ldb + j0 + jb] : b[(long long)(j0 + jb) * ldb + k0 + kb])
-                       : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[r][c] += sa[k][ty * 4 + r] * sb[k][tx * 4 + c];
-    __syncthreads();
-  }
-  for (int r = 0; r < 4; ++r)
-    for (int c = 0; c < 4; ++c)
-      if (i0 + ty * 4 + r < M && j0 + tx * 4 + c < N) finish(e, i0 + ty * 4 + r, j0 + tx * 4 + c, acc[r][c]);
-}
-
-template <class T, bool AT, bool BT>
-static int launch_simple(const void* a, long long lda, const void* b, long long ldb, int M, int N, int K,
-                         const Epilogue& e, Launch& l) {
-  if (M == 0) return PSR_OK;
-  const dim3 grid((unsigned)((M + 63) / 64), (unsigned)((N + 63) / 64));
-  if (grid.y > 65535) return PSR_ERR_UNSUPPORTED;
-  simple_gemm<T, AT, BT><<<grid, 256, 0, l.st>>>(static_cast<const T*>(a), lda, static_cast<const T*>(b), ldb, M, N, K, e,
-                                                l.clear);
-  l.clear = nullptr;
-  return launch_status();
-}
-
 // ------------------------------------------------------------------------------------------------
-// An operand with rows of any stride into rows of a multiple of 8
+// An operand with rows of any stride, from any address, into rows on 16-byte boundaries
 // ------------------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(256)
     align_kernel(const uint16_t* __restrict__ x, long long ld, uint4* __restrict__ y, int rows, int cols, Ctrl* clear) {
@@ -255,6 +206,9 @@ static int align(const void*& x, long long& ld, size_t at, int rows, int cols, v
   return launch_status();
 }
 
+// An operand that is not copied starts on a 16-byte boundary.
+static bool placed(const void* x, size_t copy) { return copy || aligned_to(x, 16); }
+
 // A call that launched nothing still leaves a cleared control block for psr_get_stats.
 static int clear_rest(const Launch& l) {
   if (!l.clear || cudaMemsetAsync(l.clear, 0, sizeof(Ctrl), l.st) == cudaSuccess) return PSR_OK;
@@ -269,6 +223,7 @@ static int sizes(const psr_linear_shape* sh, bool backward, Sizes& s) {
   if (sh->M < 0 || sh->N < 1 || sh->K < 1) return PSR_ERR_ARG;
   if (sh->act < PSR_ACT_NONE || sh->act > PSR_ACT_SILU) return PSR_ERR_ARG;
   if (sh->type != PSR_BF16 && sh->type != PSR_F16) return PSR_ERR_ARG;
+  if (sh->odd < 0 || sh->odd > 7) return PSR_ERR_ARG;
   if (sh->M > 1 << 30 || sh->N > 1 << 30 || sh->K > 1 << 30) return PSR_ERR_UNSUPPORTED;
   auto ld = [](long long given, long long contiguous) { return given == 0 ? contiguous : given; };
   s.ldx = ld(sh->ldx, sh->K); s.ldw = ld(sh->ldw, sh->K);
@@ -291,15 +246,15 @@ static int sizes(const psr_linear_shape* sh, bool backward, Sizes& s) {
     s.partial = off;
     off = au(off + (size_t)s.chunks * sh->N * 4);
   }
-  auto copy = [&](long long ld, int rows, int cols) {
+  auto copy = [&](int odd, long long ld, int rows, int cols) {
     const size_t at = off;
-    if (rows <= 1 || ld % 8 == 0) return (size_t)0;
+    if (!(sh->odd & odd) && (rows <= 1 || ld % 8 == 0)) return (size_t)0;
     off = au(off + (size_t)rows * ((cols + 7ll) / 8 * 8) * 2);
     return at;
   };
-  s.x = copy(s.ldx, sh->M, sh->K);
-  s.w = copy(s.ldw, sh->N, sh->K);
-  s.dy = backward && sh->act == PSR_ACT_NONE ? copy(s.ldy, sh->M, sh->N) : 0;
+  s.x = copy(PSR_LINEAR_ODD_X, s.ldx, sh->M, sh->K);
+  s.w = copy(PSR_LINEAR_ODD_W, s.ldw, sh->N, sh->K);
+  s.dy = backward && sh->act == PSR_ACT_NONE ? copy(PSR_LINEAR_ODD_DY, s.ldy, sh->M, sh->N) : 0;
   s.total = off;
   return PSR_OK;
 }
@@ -309,8 +264,7 @@ static int sizes(const psr_linear_shape* sh, bool backward, Sizes& s) {
 template <class T, bool AMN, bool BMN>
 static int product(const Operands& o, Epilogue e, Launch& l) {
   if (o.M == 0) return PSR_OK;
-  if (!mappable(o.a, AMN ? o.K : o.M, o.lda) || !mappable(o.b, BMN ? o.K : o.N, o.ldb))
-    return launch_simple<T, AMN, BMN>(o.a, o.lda, o.b, o.ldb, o.M, o.N, o.K, e, l);
+  if (!mappable(o.a, AMN ? o.K : o.M, o.lda) || !mappable(o.b, BMN ? o.K : o.N, o.ldb)) return PSR_ERR_UNSUPPORTED;
   auto flat = [&](const void* p, long long ld) { return !p || (aligned_to(p, 16) && (o.M == 1 || ld % 8 == 0)); };
   e.vec = o.N % 8 == 0 && flat(e.y, e.ldy) && flat(e.z, e.ldz) && flat(e.res, e.ldr) && flat(e.bias, 0);
   if constexpr (!AMN && !BMN)
@@ -405,7 +359,7 @@ int psr_linear(const psr_linear_shape* sh, const void* x, const void* w, const v
   Sizes s;
   int rc = sizes(sh, false, s);
   if (rc != PSR_OK) return rc;
-  if (ws_bytes < s.total) return PSR_ERR_ARG;
+  if (ws_bytes < s.total || !placed(x, s.x) || !placed(w, s.w)) return PSR_ERR_ARG;
   Launch l;
   if ((rc = launch_of(workspace, s, timeout_ms, stream, l)) != PSR_OK) return rc;
   Epilogue e = {};
@@ -429,7 +383,8 @@ int psr_linear_bwd(const psr_linear_shape* sh, const void* dy, const void* z, co
   Sizes s;
   int rc = sizes(sh, true, s);
   if (rc != PSR_OK) return rc;
-  if (ws_bytes < s.total) return PSR_ERR_ARG;
+  if (ws_bytes < s.total || !placed(x, s.x) || !placed(w, s.w)) return PSR_ERR_ARG;
+  if (sh->act == PSR_ACT_NONE && !placed(dy, s.dy)) return PSR_ERR_ARG;
   Launch l;
   if ((rc = launch_of(workspace, s, timeout_ms, stream, l)) != PSR_OK) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

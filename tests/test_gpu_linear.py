@@ -289,3 +289,18 @@ def test_linear_between_columns_of_one_buffer(psr):
         y, z, _ = psr.linear(rows[:, :136], w, None, cut(rows, 2), activation="gelu", out=cut(rows, 0), z=cut(rows, 1))
         check_forward(y, z, keep[:, :136], w, None, cut(keep, 2), "gelu", "bf16", "one buffer")
         assert torch.equal(rows[:, :136], keep[:, :136]) and torch.equal(cut(rows, 2), cut(keep, 2))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 264, 136), (12, 72, 64), (1, 301, 515), (70, 264, 136), (600, 1032, 264)])
+def test_linear_operands_off_their_boundary(psr, M, N, K):
+    need_gpu()
+    g = torch.Generator().manual_seed(M + K)
+    off = lambda rows, cols, std=1.0: randn(g, (rows * cols + 3,), "bf16", std)[3:].view(rows, cols)
+    x, w, dy, z = off(M, K), off(N, K, K**-0.5), off(M, N), off(M, N)
+    y, _, ws = psr.linear(x, w, dy[0], z, activation="silu")
+    assert psr.get_stats(ws)["status"] == 0
+    check_forward(y, None, x, w, dy[0], z, "silu", "bf16", "odd")
+    for act in ("none", "silu"):
+        got = psr.linear_bwd(dy, x, w, z if act != "none" else None, activation=act)
+        assert psr.get_stats(got[3])["status"] == 0
+        check_backward(got[:3], dy, x, w, z if act != "none" else None, act, "bf16", "odd bwd")

@@ -327,3 +327,12 @@ def test_columns_of_the_same_rows_are_apart(psr):
                  (rows[:, :8], rows[::2, 8:16])):
         with pytest.raises(ValueError, match="overlaps an input"):
             apart(a, b)
+
+
+def test_linear_operands_off_their_boundary(psr):
+    # off a 16-byte boundary only where the shape says so, and the workspace grows by a copy
+    for bit, name in ((1, "x"), (2, "w"), (4, "y")):
+        assert linear_call(psr, bwd=name == "y", **{name: PTR + 2}) == psr.ERR_ARG, name
+        size = lambda odd: psr.load().psr_linear_workspace_bytes(psr.LinearShape(300, 400, 512, 0, 0, 0, 0, 0, 0, 0, odd), 1)
+        assert size(bit) - size(0) >= 2 * {1: 300 * 512, 2: 400 * 512, 4: 300 * 400}[bit]
+    assert linear_call(psr, dict(odd=8)) == linear_call(psr, dict(odd=-1)) == psr.ERR_ARG
