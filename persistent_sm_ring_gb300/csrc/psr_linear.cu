@@ -34,75 +34,73 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------------------------------------
 // One row of x, or a few with a small W: dot products on the fp32 units
 // ------------------------------------------------------------------------------------------------
-// Bound by reading W once.  A warp takes R rows of W, a lane 16 bytes of each at a time (the warp 512 adjacent bytes of a
-// row), kAhead of them in flight; x comes from L1.  Against the tensor core kernels this has no tensor memory, barriers or
-// partials to set up: 8192 x 8192 in 21.8 us (6.15 TB/s) where the streaming kernel takes 29.  A few rows (a block row
-// each) read W again from L2: as fast as that kernel's 7 us for 256 x 512 up to kGemvBytes of W in all.
+// Bound by reading W once.  A warp takes a row of W, a lane 16 bytes of it at a time (the warp 512 adjacent bytes), and asks for
+// the next piece as it takes one, so that kAhead of them stay in flight; x comes from L1.  Against the tensor core kernels
+// this has no tensor memory, barriers or partials to set up: 8192 x 8192 in 22.7 us (5.9 TB/s), where the streaming kernel takes
+// 29; with groups of eight loads that are all used before the next are asked for 26.6, and 1024 x 8192 10.1 instead of 6.0.
+// A few rows (a block row each) read W again from L2: as fast as the streaming kernel's 7 us for 256 x 512 up to kGemvBytes
+// of W in all.
 constexpr long long kGemvBytes = 32 << 20;
 
-template <class T, int R>
+template <class T>
 __global__ void __launch_bounds__(256)
     gemv_kernel(const T* __restrict__ x, long long ldx, const T* __restrict__ w, long long ldw, int N, int K,
                 const __grid_constant__ Epilogue e, Ctrl* clear) {
-  constexpr int kAhead = 8 / R;
+  constexpr int kAhead = 8;
   constexpr bool kHalfType = std::is_same<T, __half>::value;
   clear_ctrl(clear);
   const int lane = threadIdx.x % 32;
-  const int j0 = (blockIdx.x * 8 + threadIdx.x / 32) * R;
-  if (j0 >= N) return;
+  const int j = blockIdx.x * 8 + threadIdx.x / 32;
+  if (j >= N) return;
   x += blockIdx.y * ldx;
-  const T* wr[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) wr[r] = w + (long long)min(j0 + r, N - 1) * ldw + lane * 8;
-  float acc[R] = {};
-  auto dot = [&](const uint4 (&v)[R], int k) {
+  const T* row = w + (long long)j * ldw + lane * 8;
+  float acc = 0.f;
+  auto load = [&](int k) { return __ldcs(reinterpret_cast<const uint4*>(row + k)); };
+  auto dot = [&](const uint4& v, int k) {
     const uint4 u = *reinterpret_cast<const uint4*>(x + k);
-    const uint32_t a[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const uint32_t b[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float al, ah, bl, bh;
-        unpack16(a[q], kHalfType, al, ah);
-        unpack16(b[q], kHalfType, bl, bh);
-        acc[r] = fmaf(al, bl, acc[r]);
-        acc[r] = fmaf(ah, bh, acc[r]);
-      }
+    for (int q = 0; q < 4; ++q) {
+      float al, ah, bl, bh;
+      unpack16(a[q], kHalfType, al, ah);
+      unpack16(b[q], kHalfType, bl, bh);
+      acc = fmaf(al, bl, acc);
+      acc = fmaf(ah, bh, acc);
     }
   };
   int k = 0;
-  for (; k + 256 * kAhead <= K; k += 256 * kAhead) {
-    uint4 v[kAhead][R];
+  if (256 * kAhead <= K) {
+    uint4 v[kAhead];
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a)
+    for (int a = 0; a < kAhead; ++a) v[a] = load(256 * a);
+    for (; k + 512 * kAhead <= K; k += 256 * kAhead) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) v[a][r] = __ldcs(reinterpret_cast<const uint4*>(wr[r] + k + 256 * a));
+      for (int a = 0; a < kAhead; ++a) {
+        dot(v[a], k + 256 * a + lane * 8);
+        v[a] = load(k + 256 * (a + kAhead));
+      }
+    }
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) dot(v[a], k + 256 * a + lane * 8);
+    k += 256 * kAhead;
   }
-  for (; k + lane * 8 < K; k += 256) {  // K is a multiple of 8
-    uint4 v[R];
+  if (k < K) {  // the rest (K is a multiple of 8), all of it in flight at once
+    uint4 v[kAhead];
 #pragma unroll
-    for (int r = 0; r < R; ++r) v[r] = __ldcs(reinterpret_cast<const uint4*>(wr[r] + k));
-    dot(v, k + lane * 8);
+    for (int a = 0; a < kAhead; ++a) v[a] = k + 256 * a + lane * 8 < K ? load(k + 256 * a) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (k + 256 * a + lane * 8 < K) dot(v[a], k + 256 * a + lane * 8);
   }
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], o);
-    if (lane == r && j0 + r < N) finish(e, blockIdx.y, j0 + r, acc[r]);
-  }
+  for (int o = 16; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  if (lane == 0) finish(e, blockIdx.y, j, acc);
 }
 
 template <class T>
 static int launch_gemv(const Operands& o, const Epilogue& e, Launch& l) {
-  // two rows of W to a warp halve the reads of x, one keeps more warps busy when W is short
-  const bool two = o.N >= 8 * 8 * l.n_sm;
-  const dim3 grid((unsigned)((o.N + (two ? 16 : 8) - 1) / (two ? 16 : 8)), (unsigned)o.M);
-  const T *x = static_cast<const T*>(o.a), *w = static_cast<const T*>(o.b);
-  if (two) gemv_kernel<T, 2><<<grid, 256, 0, l.st>>>(x, o.lda, w, o.ldb, o.N, o.K, e, l.clear);
-  else gemv_kernel<T, 1><<<grid, 256, 0, l.st>>>(x, o.lda, w, o.ldb, o.N, o.K, e, l.clear);
+  gemv_kernel<T><<<dim3((unsigned)((o.N + 7) / 8), (unsigned)o.M), 256, 0, l.st>>>(
+      static_cast<const T*>(o.a), o.lda, static_cast<const T*>(o.b), o.ldb, o.N, o.K, e, l.clear);
   l.clear = nullptr;
   return launch_status();
 }

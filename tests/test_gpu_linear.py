@@ -304,3 +304,11 @@ def test_linear_operands_off_their_boundary(psr, M, N, K):
         got = psr.linear_bwd(dy, x, w, z if act != "none" else None, activation=act)
         assert psr.get_stats(got[3])["status"] == 0
         check_backward(got[:3], dy, x, w, z if act != "none" else None, act, "bf16", "odd bwd")
+
+
+@pytest.mark.parametrize("K", [8, 248, 256, 264, 2040, 2048, 2056, 4088, 4096, 4104, 6144, 8192, 8200])
+def test_linear_one_row_of_any_length(psr, K):
+    need_gpu()
+    g = torch.Generator().manual_seed(K)
+    x, w, b = randn(g, (1, K), "f16"), randn(g, (41, K), "f16", K**-0.5), randn(g, (41,), "f16")
+    check_forward(psr.linear(x, w, b)[0], None, x, w, b, None, "none", "f16", str(K))
