@@ -564,11 +564,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 constexpr int kStreamThreads = 256;
 constexpr int kStreamArea = 216 * 1024;  // shared memory of the stages
 constexpr int kStreamMaxStages = 12;
+// A stage, and a K step of this kernel, is two boxes of kBK columns: 256 adjacent bytes of each row of W at a time (32 x 4096
+// x 4096 14.5 to 13.5 us, 16 x 4096 x 11008 24.1 to 22.7; with four 12.9 and 21.9, but 24 x 28672 x 8192 85.7 to 90.4: too
+// few stages).
+constexpr int kSub = 2;
 constexpr int kStreamSmem = 1024 + kStreamArea;
 
 struct StreamParams {
   int M, N;        // tokens, output columns (the rows of W)
-  int n_k;         // K steps
+  int n_k;         // K steps of kSub * kBK
   int tb;          // columns of a tile: M rounded up to a multiple of 16
   int n_tiles;     // ceil(N / 128)
   int per_cta;     // units (tile, K step) of a CTA, in order
@@ -608,7 +612,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t smem_base = (raw + 1023u) & ~1023u;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t stage_bytes = kHalf + (uint32_t)p.tb * kBK * 2;
+  const uint32_t x_bytes = (uint32_t)p.tb * kBK * 2, stage_bytes = kSub * (kHalf + x_bytes);
   const uint32_t n_st = (uint32_t)p.stages;
   clear_ctrl(p.clear);
   launch_dependents();
@@ -651,14 +655,21 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         }
         mbar_expect_tx(&sc.full[s], stage_bytes);
         const uint32_t base = smem_base + s * stage_bytes;
-        const int wrow = tile * kRows, k = ks * kBK;
-        if constexpr (AMN) {
-          tma_load_2d(base, &mw, wrow, k, &sc.full[s]);
-          tma_load_2d(base + 8192, &mw, wrow + 64, k, &sc.full[s]);
-        } else {
-          tma_load_2d(base, &mw, k, wrow, &sc.full[s]);
+        const int wrow = tile * kRows;
+#pragma unroll
+        for (int h = 0; h < kSub; ++h) {
+          const int k = (ks * kSub + h) * kBK;
+          const uint32_t dst = base + h * kHalf;
+          if constexpr (AMN) {
+            tma_load_2d(dst, &mw, wrow, k, &sc.full[s]);
+            tma_load_2d(dst + 8192, &mw, wrow + 64, k, &sc.full[s]);
+          } else {
+            tma_load_2d(dst, &mw, k, wrow, &sc.full[s]);
+          }
         }
-        tma_load_2d(base + kHalf, &mx, k, 0, &sc.full[s]);
+#pragma unroll
+        for (int h = 0; h < kSub; ++h)
+          tma_load_2d(base + kSub * kHalf + h * x_bytes, &mx, (ks * kSub + h) * kBK, 0, &sc.full[s]);
         ++fills;
         if (++ks == p.n_k) {
           ks = 0;
@@ -686,9 +697,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           tc_fence_after();
           const uint32_t base = smem_base + s * stage_bytes;
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            mma_ss_w(sc.tmem_base + slot * p.tb, operand_lo<AMN>(base, kk), kHi, operand_lo<false>(base + kHalf, kk), kHi,
-                     p.idesc, (ks > 0 || kk > 0) ? 1u : 0u);
+          for (int h = 0; h < kSub; ++h)
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              mma_ss_w(sc.tmem_base + slot * p.tb, operand_lo<AMN>(base + h * kHalf, kk), kHi,
+                       operand_lo<false>(base + kSub * kHalf + h * x_bytes, kk), kHi, p.idesc, (ks > 0 || h > 0 || kk > 0) ? 1u : 0u);
           mma_commit(&sc.empty[s]);
         }
         if (!ok) break;
@@ -1013,17 +1026,17 @@ inline int launch_stream(const Operands& o, const Epilogue& e, Launch& l) {
   StreamParams p = {};
   p.M = o.M;
   p.N = o.N;
-  p.n_k = (o.K + kBK - 1) / kBK;
+  p.n_k = (o.K + kSub * kBK - 1) / (kSub * kBK);
   p.tb = (o.M + 15) / 16 * 16;
   p.n_tiles = (o.N + kRows - 1) / kRows;
   const int most = n_sm < kStreamCtas ? n_sm : kStreamCtas;
   const long long units = (long long)p.n_tiles * p.n_k;
   long long per = (units + most - 1) / most;
-  if (p.n_k <= 16) per = (per + p.n_k - 1) / p.n_k * p.n_k;  // short rows: whole tiles, nothing to join
-  else if (per < 8) per = 8;
+  if (p.n_k <= 16 / kSub) per = (per + p.n_k - 1) / p.n_k * p.n_k;  // short rows: whole tiles, nothing to join
+  else if (per < 8 / kSub) per = 8 / kSub;
   if (per >= (1ll << 31)) return PSR_ERR_UNSUPPORTED;
   p.per_cta = (int)per;
-  const int stage = kHalf + p.tb * kBK * 2;
+  const int stage = kSub * (kHalf + p.tb * kBK * 2);
   p.stages = kStreamArea / stage < kStreamMaxStages ? kStreamArea / stage : kStreamMaxStages;
   p.tmem_cols = 32;
   while (p.tmem_cols < 2u * p.tb) p.tmem_cols *= 2;
