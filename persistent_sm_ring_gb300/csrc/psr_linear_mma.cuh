@@ -60,6 +60,12 @@ __device__ __forceinline__ float normal_cdf(float z, float* e) {
   return z < 0.f ? h : 1.f - h;
 }
 
+// (1 + tanh u)/2 = sigmoid(2u), u = sqrt(2/pi) (z + 0.044715 z^3)
+constexpr float kTwoU = 1.5957691216057307f, kCube = 0.044715f, kLog2eTwoU = 1.4426950408889634f * kTwoU;
+__device__ __forceinline__ float tanh_cdf(float z, float z2) {
+  return rcp_approx(1.f + ex2_approx(z * fmaf(-kLog2eTwoU * kCube, z2, -kLog2eTwoU)));
+}
+
 __device__ __forceinline__ float act_fwd(int act, float z) {
   switch (act) {
     case PSR_ACT_RELU: return z > 0.f ? z : (z == z ? 0.f : z);
@@ -67,7 +73,7 @@ __device__ __forceinline__ float act_fwd(int act, float z) {
       float e;
       return z * normal_cdf(z, &e);
     }
-    case PSR_ACT_GELU_TANH: return z * sigmoid(1.5957691216057307f * (z + 0.044715f * z * z * z));  // (1 + tanh u)/2 = sigmoid(2u)
+    case PSR_ACT_GELU_TANH: return z * tanh_cdf(z, z * z);
     case PSR_ACT_SILU: return z * sigmoid(z);
     default: return z;
   }
@@ -81,9 +87,8 @@ __device__ __forceinline__ float act_slope(int act, float z) {
       return fmaf(z * 0.39894228040143268f, e, f);
     }
     case PSR_ACT_GELU_TANH: {
-      const float s = sigmoid(1.5957691216057307f * (z + 0.044715f * z * z * z));
-      const float q = s * (1.f - s);  // 0 far from 0, where z^2 may be infinite
-      return q == 0.f ? s : s + z * q * 1.5957691216057307f * (1.f + 0.134145f * z * z);
+      const float z2 = z * z, s = tanh_cdf(z, z2), q = fmaf(-s, s, s);  // q: 0 far from 0, where z^2 may be infinite
+      return q == 0.f ? s : fmaf(q, z * fmaf(3.f * kCube * kTwoU, z2, kTwoU), s);
     }
     case PSR_ACT_SILU: {
       const float s = sigmoid(z);
