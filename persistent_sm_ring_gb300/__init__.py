@@ -4,6 +4,8 @@ Thin Python binding over the C ABI of ``libpsr.so`` (declared in
 ``include/psr.h``).  It only marshals arguments: every step of the ring
 (staging, readiness flags, the tcgen05 FlashAttention pass, the LSE-exact
 merge, the on-GPU partition controller) runs in the library's CUDA kernel.
+The layer around the ring (rotary positions, linear with its gradients, a
+4-bit KV cache with its attention) is bound at the end of the file.
 PyTorch supplies device memory and streams.  There is no fallback: if the
 library is missing or the device is not an sm_103 GPU, calls raise.
 """
