@@ -238,10 +238,16 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ MoveP
 //    more for 16 tokens multiplies it with a constant code 8: what is wanted is the sum of P (c - 8), as large as the output,
 //    and the two sums' roundings go together (with the sum of P c alone those of a long context showed, 2.1e-3 of the output
 //    against 1.7e-3 for its own rounding).
-//  * any order of the contraction will do, so K and V fragments are read straight from the stage: a lane takes 16 adjacent
-//    bytes of a K row, and the tokens are dealt to the mma's rows so that V's loads fall on different banks; P leaves the
+//  * any order of the contraction will do, so K's fragments are read straight from the stage, 16 adjacent bytes of a row to a
+//    lane.  V's come through transposing matrix loads of 16-bit elements (four columns of a token), whose pieces the copies
+//    have swizzled over the banks (48 ragged sequences: 64 to 63 us against plain loads and byte permutes).  P leaves the
 //    first product in the layout that movmatrix turns into the second one's operand.
+//  * up to four query rows fill half of the eight columns.  SPLIT then gives columns 0..3 the first block of a unit and columns
+//    4..7 the second, as rows of their own that meet at the end: a lane has half as many weights to work out (8 sequences of
+//    about 110k positions, 4 rows: 174 to 166 us; 48 ragged sequences: 68 to 64).  Both products stay as many.
 //  * the maximum and that power are only raised when a weight or a product passes kRaise: the check is one vote.
+// Units of four blocks (K and V in rings of their own), and the scores of the next unit between those of this one and its
+// second product, gained nothing at d = 128: the registers that they need are not there.
 constexpr int kWarps = 8;
 template <int D>
 constexpr int kStages = D == 128 ? 2 : 4;
@@ -386,12 +392,22 @@ __device__ __forceinline__ void copy_wait() {  // all but the N newest groups of
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <class T, int D, int NT>
+// Four transposed 8 x 8 matrices of 16-bit elements, whose rows' addresses the lanes give: lane (g, t) gets elements (2t, g) and
+// (2t + 1, g) of each.
+__device__ __forceinline__ void load_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+template <class T, int D, int NT, bool SPLIT>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(const __grid_constant__ AttnParams p) {
+  static_assert(!SPLIT || NT == 1, "four rows are one tile");
   using Sm = AttnSmem<D>;
-  constexpr int kRows = 8 * NT, kBytes = Sm::kBytes;
+  constexpr int NI = SPLIT ? 2 : 4;  // tokens of a unit whose weights a lane has
+  constexpr int kRows = 8 * NT, kBytes = Sm::kBytes, kHalf = kBlk * D / 2;  // bytes of a block, of its K or V codes
   constexpr int KW = D / 32;  // words of K codes a lane takes of a row
-  constexpr int VW = D / 64;  // words of V codes a lane takes of a token
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
@@ -414,7 +430,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
   const int32_t* row = p.c.table + (long long)seg.b * p.c.max_pages;
   const int in_page = (1 << p.page_shift) - 1, per_page = p.c.Hkv << p.page_shift;  // blocks of a page, and of all heads
   const uint8_t* lane_base = p.c.base + lane * 16;
+  // A stage holds K's codes of both blocks, then V's, then the scales.  V's 16-byte pieces are XOR-swizzled by their rows, so that
+  // eight rows of a piece fall on different banks.
+  constexpr int kSwz = D == 128 ? 3 : 1;
   const uint32_t lane_ring = smem_u32(sm.ring[warp]) + lane * 16;
+  const uint32_t lane_v = smem_u32(sm.ring[warp]) + 2 * kHalf + (lane ^ (lane >> 3 & kSwz)) * 16;
   uint32_t bad = 0;  // bit s: a block of stage s has no page
   auto look_up = [&]() {
     if (next >= pre_end) {
@@ -433,18 +453,17 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
     if (next < u1) {
       const int s = filled++ % S;
       if ((uint32_t)pg0 < (uint32_t)p.c.n_pages && (uint32_t)pg1 < (uint32_t)p.c.n_pages) {
-        constexpr int kChunks = kBytes / 16;  // of a block
         // (fewer than 2^31 blocks: checked on the host)
-        const uint8_t* src0 = lane_base + (unsigned long long)(uint32_t)(pg0 * per_page + off) * kBytes;
-        const uint8_t* src1 = src0;  // the second block follows the first where a page holds two
-        if (p.page_shift == 0) src1 = lane_base + (unsigned long long)(uint32_t)(pg1 * per_page + off) * kBytes - kBytes;
-        const uint32_t dst = lane_ring + s * (2 * kBytes);
+        const uint8_t* src[2];
+        src[0] = lane_base + (unsigned long long)(uint32_t)(pg0 * per_page + off) * kBytes;
+        src[1] = src[0] + kBytes;  // the second block follows the first where a page holds two
+        if (p.page_shift == 0) src[1] = lane_base + (unsigned long long)(uint32_t)(pg1 * per_page + off) * kBytes;
+        const uint32_t dst = lane_ring + s * (2 * kBytes), dst_v = lane_v + s * (2 * kBytes);
 #pragma unroll
-        for (int i = 0; i < (2 * kChunks + 31) / 32; ++i) {
-          const int c = i * 32;
-          if (c + 32 <= 2 * kChunks || lane < 2 * kChunks - c)
-            copy16(dst + i * 512, (c + 32 <= kChunks ? src0 : c >= kChunks ? src1 : lane < kChunks - c ? src0 : src1) + i * 512);
-        }
+        for (int c = 0; c < 2 * kHalf; c += 512) copy16(dst + c, src[c / kHalf] + c % kHalf);
+#pragma unroll
+        for (int c = 0; c < 2 * kHalf; c += 512) copy16(dst_v + c, src[c / kHalf] + kHalf + c % kHalf);
+        if (lane < 16) copy16(dst + 4 * kHalf, (lane < 8 ? src[0] : src[1] - 128) + 2 * kHalf);
       } else {
         bad |= 1u << s;
       }
@@ -463,15 +482,17 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
     if (from >= hi) continue;
     const int n = p.lens[seg.b];
     const int R = p.group * p.S;  // query rows of the KV head: row = new token * group + head of the group
-    // ---- query fragments: the row g of each tile, columns in the order of the K codes' words -----
+    // the query row of column c of tile nt
+    auto row_of = [&](int nt, int c) { return seg.rt * kRows + nt * 8 + (SPLIT ? c % 4 : c); };
+    // ---- query fragments: column g of each tile, columns of q in the order of the K codes' words -----
     uint32_t qf[NT][KW][4];
-    float qsum[NT][2];   // of rows 2t and 2t + 1
+    float qsum[NT][2];   // of columns 2t and 2t + 1
     int last[NT][2];     // last position that they see
     float big = 0.f;
     uint4 raw[NT][KW];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int row = seg.rt * kRows + nt * 8 + g;
+      const int row = row_of(nt, g);
       const T* q = static_cast<const T*>(p.q) + (long long)seg.b * p.sq.b +
                    (long long)(seg.h * p.group + row % p.group) * p.sq.h + (long long)(row / p.group) * p.sq.s + t * (D / 4);
 #pragma unroll
@@ -523,12 +544,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         qsum[nt][c] = __shfl_sync(0xffffffffu, sum, (2 * t + c) * 4) * (p.scale * kLog2e);
-        last[nt][c] = n - p.S + (seg.rt * kRows + nt * 8 + 2 * t + c) / p.group;
+        last[nt][c] = n - p.S + row_of(nt, 2 * t + c) / p.group;
       }
     }
     const float kscale = p.scale * kLog2e * 16777216.f / up;
     float acc[NT][D / 16][4], eight[NT][4], m[NT][2], di[NT][2], l[NT][2], corr[NT][2];
-    bool fresh = true;  // no unit yet: the first one sets the maxima (a row that sees nothing of it sees nothing later)
+    bool fresh = true;  // no unit yet: the first one sets the maxima (a column that sees nothing of it sees nothing later)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -543,15 +564,15 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
       constexpr bool MASKED = decltype(masked_tag)::value;
       // mma row g holds token g / 2 + 4 (g % 2) of a block, row g + 8 that plus 8
       const int tok = g / 2 + 4 * (g % 2);
-      float x[NT][8];  // block, token half, row
+      float xb[NT][8];  // block, token half, column
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[nt][e] = 0.f;
+        for (int e = 0; e < 8; ++e) xb[nt][e] = 0.f;
       uint32_t ka[2][KW], kb[2][KW];
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const uint8_t* blk = stage + b * kBytes;
+        const uint8_t* blk = stage + b * kHalf;
         if constexpr (D == 128) {
           const uint4 a = *reinterpret_cast<const uint4*>(blk + tok * 64 + t * 16);
           const uint4 c = *reinterpret_cast<const uint4*>(blk + (tok + 8) * 64 + t * 16);
@@ -573,17 +594,24 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
             const uint32_t a8 = half ? ka[b][w] >> 8 : ka[b][w], b8 = half ? kb[b][w] >> 8 : kb[b][w];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_f16(*reinterpret_cast<float(*)[4]>(&x[nt][4 * b]), a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u,
+              mma_f16(*reinterpret_cast<float(*)[4]>(&xb[nt][4 * b]), a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u,
                       b8 & 0x00F000F0u, qf[nt][w][2 * half], qf[nt][w][2 * half + 1]);
           }
       // x: scores in powers of two above m; w: weights; y: weights times V's scale, in units of 1 / di
-      float w[NT][8], y[NT][8], vo[4], top = 0.f;
-      auto pair_of = [&](int i, int kv) {  // of the lane's token i (block, half)
-        return reinterpret_cast<const uint32_t*>(stage + i / 2 * kBytes + kBlk * D)[kv * 16 + tok + 8 * (i % 2)];
-      };
-      auto unseen = [&](int i, int nt, int c) { return MASKED && j0 + 16 * (i / 2) + 8 * (i % 2) + tok > last[nt][c]; };
+      float x[NT][2 * NI], w[NT][2 * NI], y[NT][2 * NI], vo[NI], top = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2 * NI; ++e) x[nt][e] = SPLIT && t >= 2 ? xb[nt][(e + 4) % 8] : xb[nt][e];
+      // the lane's token i: block, half; with SPLIT half of the lane's block
+      const uint8_t* own = stage + 4 * kHalf + (SPLIT ? t / 2 * 128 : 0);
+      const int own_tok = tok + (SPLIT ? t / 2 * kBlk : 0);
+      auto pair_of = [&](int i, int kv) {
+        return reinterpret_cast<const uint32_t*>(own + i / 2 * 128)[kv * 16 + tok + 8 * (i % 2)];
+      };
+      auto unseen = [&](int i, int nt, int c) { return MASKED && j0 + 16 * (i / 2) + 8 * (i % 2) + own_tok > last[nt][c]; };
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
         const uint32_t kp = pair_of(i, 0), vp = pair_of(i, 1);
         const float ks = lo_bf16(kp) * kscale, ko = hi_bf16(kp), vs = lo_bf16(vp);
         vo[i] = fmaf(8.f, vs, hi_bf16(vp));
@@ -601,7 +629,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmax3(top, w[nt][e], y[nt][e]);
+        for (int e = 0; e < 2 * NI; ++e) top = fmax3(top, w[nt][e], y[nt][e]);
       if (__any_sync(0xffffffffu, fresh || top > kRaise)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -609,7 +637,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
           for (int c = 0; c < 2; ++c) {
             float a = -INFINITY, b = -INFINITY;  // largest score, largest exponent of a product
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < NI; ++i) {
               if (unseen(i, nt, c)) continue;
               a = fmaxf(a, x[nt][2 * i + c]);
               b = fmaxf(b, x[nt][2 * i + c] + lg2_approx(lo_bf16(pair_of(i, 1))));
@@ -637,7 +665,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
               }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < NI; ++i) {
               const int e = 2 * i + c;
               if (unseen(i, nt, c)) continue;
               w[nt][e] = ex2_approx(x[nt][e] - up);
@@ -646,51 +674,50 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
           }
         fresh = false;
       }
+      // the lane's row of the matrices: token and 16-byte piece
+      const int mt = lane % 8 / 2 + 4 * (lane % 2) + lane / 8 % 2 * 8, mj = lane / 16;
+      const uint32_t at_v = smem_u32(stage) + 2 * kHalf + mt * (D / 2) + ((mj ^ (D == 128 ? mt / 2 & 3 : mt / 4 & 1)) * 16);
+      uint32_t both[NT][2];  // P of the block; with SPLIT columns 0..3 are of the first block, 4..7 of the second
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const uint8_t* blk = stage + b * kBytes;
-        // V's codes: tokens t, t + 4 (contraction 2t, 2t + 1) and t + 8, t + 12, the lane's D / 8 columns from g D / 8 on
-        uint32_t va[4][VW];
+        if (!SPLIT || b == 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint8_t* v = blk + kBlk * D / 2 + (t + 4 * i) * (D / 2) + g * (D / 16);
-          if constexpr (D == 128) {
-            const uint2 w = *reinterpret_cast<const uint2*>(v);
-            va[i][0] = w.x;
-            va[i][1] = w.y;
-          } else {
-            va[i][0] = *reinterpret_cast<const uint32_t*>(v);
-          }
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int i = SPLIT ? h : 2 * b + h;
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                l[nt][c] += w[nt][2 * i + c];
+                if (!unseen(i, nt, c)) corr[nt][c] = fmaf(w[nt][2 * i + c], vo[i], corr[nt][c]);
+              }
+              both[nt][h] = transpose8x8(pack_f16x2(y[nt][2 * i], y[nt][2 * i + 1]));
+            }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_f16(eight[nt], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, both[nt][0], both[nt][1]);
         }
         uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int i = 2 * b + h;
+          for (int h = 0; h < 2; ++h) pb[nt][h] = SPLIT && g / 4 != b ? 0u : both[nt][h];
+        // V's codes: a 16-bit element is four columns of a token, an element of the transposed matrices those of tokens t, t + 4
+        // (contraction 2t, 2t + 1) or, in the odd ones, t + 8, t + 12; the lane's columns are 32 j + 4 g + 0 .. 3
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              l[nt][c] += w[nt][2 * i + c];
-              if (!unseen(i, nt, c)) corr[nt][c] = fmaf(w[nt][2 * i + c], vo[i], corr[nt][c]);
-            }
-            pb[nt][h] = transpose8x8(pack_f16x2(y[nt][2 * i], y[nt][2 * i + 1]));
-          }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma_f16(eight[nt], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, pb[nt][0], pb[nt][1]);
-#pragma unroll
-        for (int q = 0; q < VW; ++q) {
-          const uint32_t l01 = __byte_perm(va[0][q], va[1][q], 0x5410), h01 = __byte_perm(va[0][q], va[1][q], 0x7632);
-          const uint32_t l23 = __byte_perm(va[2][q], va[3][q], 0x5410), h23 = __byte_perm(va[2][q], va[3][q], 0x7632);
-          const uint32_t l01s = l01 >> 8, h01s = h01 >> 8, l23s = l23 >> 8, h23s = h23 >> 8;
+        for (int j = 0; j < D / 32; j += 2) {
+          uint32_t r[4];
+          load_trans(r, (at_v ^ (j * 16)) + b * kHalf);
           constexpr uint32_t L = 0x000F000Fu, H = 0x00F000F0u;
-          // columns 8 q + 0 .. 7 of the lane's: two to an mma, the even one on row g, the odd one, 16 times too high, on g + 8
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_f16(acc[nt][4 * q], l01 & L, l01 & H, l23 & L, l23 & H, pb[nt][0], pb[nt][1]);
-            mma_f16(acc[nt][4 * q + 1], l01s & L, l01s & H, l23s & L, l23s & H, pb[nt][0], pb[nt][1]);
-            mma_f16(acc[nt][4 * q + 2], h01 & L, h01 & H, h23 & L, h23 & H, pb[nt][0], pb[nt][1]);
-            mma_f16(acc[nt][4 * q + 3], h01s & L, h01s & H, h23s & L, h23s & H, pb[nt][0], pb[nt][1]);
+          for (int k = 0; k < 2; ++k) {
+            // two columns to an mma, the even one on row g, the odd one, 16 times too high, on g + 8
+            const uint32_t lo = r[2 * k], hi = r[2 * k + 1], los = lo >> 8, his = hi >> 8;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16(acc[nt][2 * (j + k)], lo & L, lo & H, hi & L, hi & H, pb[nt][0], pb[nt][1]);
+              mma_f16(acc[nt][2 * (j + k) + 1], los & L, los & H, his & L, his & H, pb[nt][0], pb[nt][1]);
+            }
           }
         }
       }
@@ -725,40 +752,51 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
           sum += __shfl_xor_sync(0xffffffffu, sum, o);
           base += __shfl_xor_sync(0xffffffffu, base, o);
         }
-        const int row = nt * 8 + 2 * t + c, r = seg.rt * kRows + row;
-        if (r >= R) continue;
         const float fo = 1.f / di[nt][c];
-        float v[D / 8];  // the lane's columns, from g D / 8 on
+        float top = sum == 0.f ? kLowest : m[nt][c];  // kLowest: the column saw nothing
+        float v[D / 8];  // the lane's columns, 32 j + 4 g + 0 .. 3
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           v[2 * i] = fmaf((acc[nt][i][c] - eight[nt][c]) * 16777216.f, fo, base);
           v[2 * i + 1] = fmaf(fmaf(-16.f, eight[nt][c], acc[nt][i][2 + c]) * 1048576.f, fo, base);
         }
+        if constexpr (SPLIT) {  // the row's two columns, in lanes t and t + 2
+          const float other = __shfl_xor_sync(0xffffffffu, top, 2), both = fmaxf(top, other), f = ex2_approx(top - both);
+          top = both;
+          sum *= f;
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            v[i] *= f;
+            v[i] += __shfl_xor_sync(0xffffffffu, v[i], 2);
+          }
+        }
+        const int r = row_of(nt, 2 * t + c);
+        if (r >= R || (SPLIT && t >= 2)) continue;
         if (whole) {
           const long long hq = seg.h * p.group + r % p.group, i = r / p.group;
-          T* out = static_cast<T*>(p.o) + seg.b * p.so.b + hq * p.so.h + i * p.so.s + g * (D / 8);
+          T* out = static_cast<T*>(p.o) + seg.b * p.so.b + hq * p.so.h + i * p.so.s + g * 4;
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          if (p.vec_o) {
 #pragma unroll
-            for (int q = 0; q < D / 64; ++q) {
-              Eight<T> w;
+          for (int j = 0; j < D / 32; ++j) {
+            struct alignas(8) Four { T e[4]; } w;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) w.e[e] = from_f32<T>(sum == 0.f ? 0.f : v[q * 8 + e] * inv);
-              *reinterpret_cast<Eight<T>*>(out + q * 8) = w;
+            for (int e = 0; e < 4; ++e) w.e[e] = from_f32<T>(sum == 0.f ? 0.f : v[j * 4 + e] * inv);
+            if (p.vec_o) {
+              *reinterpret_cast<Four*>(out + j * 32) = w;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) out[j * 32 + e] = w.e[e];
             }
-          } else {
-#pragma unroll
-            for (int e = 0; e < D / 8; ++e) out[e] = from_f32<T>(sum == 0.f ? 0.f : v[e] * inv);
           }
-          if (g == 0)
-            p.lse[(seg.b * (long long)p.Hq + hq) * p.S + i] = sum == 0.f ? -INFINITY : (m[nt][c] + log2f(sum)) * kLn2;
+          if (g == 0) p.lse[(seg.b * (long long)p.Hq + hq) * p.S + i] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
         } else {
-          float* part = p.part + ((2ll * slot + (lo == u0 ? 0 : 1)) * kRows + row) * kPart<D>;
+          float* part = p.part + ((2ll * slot + (lo == u0 ? 0 : 1)) * kRows + r - seg.rt * kRows) * kPart<D>;
 #pragma unroll
           for (int q = 0; q < D / 32; ++q)
-            *reinterpret_cast<float4*>(part + g * (D / 8) + q * 4) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            *reinterpret_cast<float4*>(part + q * 32 + g * 4) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
           if (g == 0) {
-            part[D] = sum == 0.f ? kLowest : m[nt][c];  // kLowest: the row saw nothing
+            part[D] = top;
             part[D + 1] = sum;
           }
         }
@@ -872,10 +910,7 @@ static int by_type(const psr_kv4_shape* sh, Go&& go) {
   return sh->d == 64 ? go(__half(), std::integral_constant<int, 64>()) : go(__half(), std::integral_constant<int, 128>());
 }
 
-// Query rows of a tile: 8, or 16 where that halves the reads of the cache.
-static int tile_rows(const psr_kv4_shape* sh) { return (long long)sh->Hq / sh->Hkv * sh->S > 8 ? 16 : 8; }
-
-template <class T, int D, int NT>
+template <class T, int D, int NT, bool SPLIT>
 static int launch_attn(AttnParams& p, int dev, int n_sm, cudaStream_t st) {
   static std::mutex mu;
   static bool known[64] = {};
@@ -884,7 +919,7 @@ static int launch_attn(AttnParams& p, int dev, int n_sm, cudaStream_t st) {
   {
     std::lock_guard<std::mutex> lk(mu);
     if (dev < 0 || dev >= 64 || !known[dev]) {
-      if (cudaFuncSetAttribute(attn_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+      if (cudaFuncSetAttribute(attn_kernel<T, D, NT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
         cudaGetLastError();
         return PSR_ERR_CUDA;
       }
@@ -894,7 +929,7 @@ static int launch_attn(AttnParams& p, int dev, int n_sm, cudaStream_t st) {
   const long long R = (long long)p.group * p.S;
   p.n_rt = (int)((R + 8 * NT - 1) / (8 * NT));
   const int ctas = (n_sm < 152 ? n_sm : 152) * (NT == 1 ? 2 : 1);
-  attn_kernel<T, D, NT><<<ctas, kWarps * 32, smem, st>>>(p);
+  attn_kernel<T, D, NT, SPLIT><<<ctas, kWarps * 32, smem, st>>>(p);
   if (launch_status() != PSR_OK) return PSR_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   // up to 2 ctas kWarps pieces lie in the segments: a block to a row while a segment may have more than 16 of them
@@ -1027,8 +1062,11 @@ int psr_kv4_attn(const psr_kv4_shape* sh, const void* q, const psr_strides* qs, 
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return by_type(sh, [&](auto t, auto d) {
-    return tile_rows(sh) == 8 ? launch_attn<decltype(t), decltype(d)::value, 1>(p, dev, n_sm, st)
-                              : launch_attn<decltype(t), decltype(d)::value, 2>(p, dev, n_sm, st);
+    constexpr int D = decltype(d)::value;
+    const long long rows = (long long)sh->Hq / sh->Hkv * sh->S;  // of a KV head
+    return rows <= 4   ? launch_attn<decltype(t), D, 1, true>(p, dev, n_sm, st)
+           : rows <= 8 ? launch_attn<decltype(t), D, 1, false>(p, dev, n_sm, st)
+                       : launch_attn<decltype(t), D, 2, false>(p, dev, n_sm, st);
   });
 }
 

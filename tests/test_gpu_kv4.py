@@ -309,3 +309,70 @@ def test_empty_batches(psr):
         o, lse, _ = psr.kv4_attn(e, cache, table, z, Hkv=2, page=16)
         assert k.shape == o.shape == (B, 2, S, 64) and lse.shape == (B, 2, S)
     assert not cache.any()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group,S", [(1, 1), (2, 1), (3, 1), (4, 1), (1, 2), (2, 2), (1, 3), (1, 4), (5, 1), (3, 2), (7, 1),
+                                     (8, 1), (9, 1), (4, 4), (17, 1)])
+def test_attention_rows_of_a_kv_head(psr, group, S, d):
+    # last units of every fill, with one to seventeen query rows to a KV head
+    need_gpu()
+    lens = [0, 1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 49, 64, 65, 300]
+    run_attention(psr, (len(lens), S, 2 * group, 2, d, 16, lens, "f16" if group % 2 else "bf16"), 40 + group)
+
+
+@pytest.mark.parametrize("Hq", [4, 8])
+def test_attention_with_large_scores_in_one_block(psr, Hq):
+    # one block of 16 tokens outweighs all others, wherever it stands, by more than fp32 or fp16 ratios hold
+    need_gpu()
+    n, d, page = 160, 64, 32
+    rng = np.random.default_rng(8)
+    for at in range(0, n, 16):
+        cache = random_cache(rng, 5, 1, d, page)
+        blocks = cache.reshape(5, 1, page // 16, 16 * (d + 8))
+        pairs = blocks[at // page, 0, at % page // 16, 16 * d:].view(np.uint16).reshape(2, 16, 2)
+        pairs[0, :, 1] = np.float32(60).view(np.uint32) >> 16  # offsets of K
+        q = torch.full((1, Hq, 1, d), 0.5, dtype=torch.bfloat16, device="cuda")
+        table = torch.arange(5, dtype=torch.int32, device="cuda")[None]
+        lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+        o, lse, _ = psr.kv4_attn(q, torch.from_numpy(cache).cuda(), table, lens, Hkv=1, page=page, scale=1.0)
+        ro, rl, to, tl = ol.kv4_attention(f64(q), cache, table.cpu().numpy(), [n], page, 1, 1.0)
+        check(lse, rl, tl, f"block at {at}: lse")
+        check(o, ro, to + ol.HALF_STEP["bf16"] * np.abs(ro) * 1.01, f"block at {at}: o")
+
+
+def test_attention_of_shared_pages(psr):
+    # sequences with the same first pages, and one with the same page over and over
+    need_gpu()
+    rng = np.random.default_rng(9)
+    Hkv, d, page = 2, 128, 16
+    cache = random_cache(rng, 6, Hkv, d, page)
+    table = np.array([[0, 1, 2, 3], [0, 1, 4, 5], [2, 2, 2, 2]], np.int32)
+    lens = [60, 49, 64]
+    g = torch.Generator().manual_seed(9)
+    q = randn(g, (3, 8, 2, d), "bf16")
+    o, lse, _ = psr.kv4_attn(q, torch.from_numpy(cache).cuda(), torch.from_numpy(table).cuda(),
+                             torch.tensor(lens, dtype=torch.int32, device="cuda"), Hkv=Hkv, page=page)
+    ro, rl, to, tl = ol.kv4_attention(f64(q), cache, table, lens, page, Hkv, 1 / math.sqrt(d))
+    check(lse, rl, tl, "shared pages: lse")
+    check(o, ro, to + ol.HALF_STEP["bf16"] * np.abs(ro) * 1.01, "shared pages: o")
+
+
+def test_attention_of_two_streams_at_once(psr):
+    need_gpu()
+    rng = np.random.default_rng(10)
+    g = torch.Generator().manual_seed(10)
+    Hkv, d, page = 4, 128, 64
+    calls = []
+    for lens in ([3000, 10, 900, 1], [40, 2500], [5000]):
+        table, n_pages = pages_for(rng, lens, page)
+        cache = torch.from_numpy(random_cache(rng, n_pages, Hkv, d, page)).cuda()
+        calls.append((randn(g, (len(lens), 16, 1, d), "bf16"), cache, torch.from_numpy(table).cuda(),
+                      torch.tensor(lens, dtype=torch.int32, device="cuda")))
+    want = [psr.kv4_attn(*c, Hkv=Hkv, page=page)[:2] for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        got = [psr.kv4_attn(*c, Hkv=Hkv, page=page, stream=s)[:2] for c, s in zip(calls, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))

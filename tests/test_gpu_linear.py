@@ -312,3 +312,21 @@ def test_linear_one_row_of_any_length(psr, K):
     g = torch.Generator().manual_seed(K)
     x, w, b = randn(g, (1, K), "f16"), randn(g, (41, K), "f16", K**-0.5), randn(g, (41,), "f16")
     check_forward(psr.linear(x, w, b)[0], None, x, w, b, None, "none", "f16", str(K))
+
+
+def test_linear_of_two_streams_at_once(psr):
+    need_gpu()
+    g = torch.Generator().manual_seed(12)
+    calls = [(randn(g, (M, K), "bf16"), randn(g, (N, K), "bf16", K**-0.5), randn(g, (N,), "bf16"), randn(g, (M, N), "bf16"))
+             for M, N, K in ((1, 4096, 4096), (24, 4096, 2048), (300, 1024, 4096), (1500, 2048, 512))]
+    want = [psr.linear(*c, activation="silu", save_z=True)[:2] for c in calls]
+    back = [psr.linear_bwd(c[3], c[0], c[1], y[1], activation="silu")[:3] for c, y in zip(calls, want)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        got = [psr.linear(*c, activation="silu", save_z=True, stream=s) for c, s in zip(calls, streams)]
+        grads = [psr.linear_bwd(c[3], c[0], c[1], y[1], activation="silu", stream=s) for c, y, s in zip(calls, want, streams)]
+        torch.cuda.synchronize()
+        assert all(psr.get_stats(x[-1])["status"] == 0 for x in got + grads)
+        assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
+        assert all(torch.equal(a, b) for x, y in zip(grads, back) for a, b in zip(x, y))
