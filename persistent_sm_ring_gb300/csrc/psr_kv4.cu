@@ -42,8 +42,10 @@ __device__ __forceinline__ float warp_max(float v) {
 // ------------------------------------------------------------------------------------------------
 // Append and read
 // ------------------------------------------------------------------------------------------------
-// Memory bound.  D / 8 lanes take a row, eight columns (16 bytes) each; a block takes kTokens tokens of one sequence and KV
-// head, and a lane the K and V rows of two of them, so that four loads are in flight.
+// D / 8 lanes take a row, eight columns (16 bytes) each; a block takes kTokens tokens of one sequence and KV head, and a lane
+// the K and V rows of two of them, so that four loads are in flight.  Bound by their instructions: 4 x 2000 tokens of 8 heads,
+// d = 128, are appended in 18 us (72 % of the issue slots, 200 instructions for a lane's part of a row) and read in 9.5, where
+// the bytes would take 6 each.
 constexpr int kEach = 2;  // tokens of a thread
 
 template <int D>
@@ -77,6 +79,22 @@ struct Pair<__half> {
   static __device__ __forceinline__ type zero() { return __float2half2_rn(0.f); }
 };
 
+// two fp32 operations at once
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(*reinterpret_cast<unsigned long long*>(&r))
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(*reinterpret_cast<unsigned long long*>(&r))
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return r;
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ MoveParams p) {
   using R = Rows<D>;
@@ -87,16 +105,16 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ Mov
   const long long start = p.start[b];
   Eight<T> raw[kEach][2];
 #pragma unroll
-  for (int n = 0; n < kEach; ++n) {
-    const int i = first + n * (R::kTokens / kEach);
-    if (i >= end) continue;
+  for (int kv = 0; kv < 2; ++kv) {
+    const T* x = static_cast<const T*>(p.in[kv]) + (b * p.st[kv].b + h * p.st[kv].h) + first * p.st[kv].s + part * 8;
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const T* x = static_cast<const T*>(p.in[kv]) + b * p.st[kv].b + h * p.st[kv].h + i * p.st[kv].s + part * 8;
-      if (p.vec) raw[n][kv] = *reinterpret_cast<const Eight<T>*>(x);
+    for (int n = 0; n < kEach; ++n) {
+      if (first + n * (R::kTokens / kEach) >= end) continue;
+      const T* y = x + n * (R::kTokens / kEach) * p.st[kv].s;
+      if (p.vec) raw[n][kv] = *reinterpret_cast<const Eight<T>*>(y);
       else
 #pragma unroll
-        for (int e = 0; e < 8; ++e) raw[n][kv].e[e] = x[e];
+        for (int e = 0; e < 8; ++e) raw[n][kv].e[e] = y[e];
     }
   }
   uint8_t* blk[kEach];  // looked up while the rows are on their way
@@ -105,53 +123,72 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ Mov
     const int i = first + n * (R::kTokens / kEach);
     blk[n] = i < end ? block_of<D>(p.c, b, h, start + i) : nullptr;
   }
+  // minimum and negated maximum of each row side by side, NaN if there is one; a missing row is all zeros
+  using T2 = typename Pair<T>::type;
+  T2 low[kEach][2];
+#pragma unroll
+  for (int n = 0; n < kEach; ++n)
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      T2 w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = blk[n] ? reinterpret_cast<const T2*>(&raw[n][kv])[e] : Pair<T>::zero();
+      const T2 a = __hmin2_nan(__hmin2_nan(w[0], w[1]), __hmin2_nan(w[2], w[3]));
+      const T2 b = __hneg2(__hmax2_nan(__hmax2_nan(w[0], w[1]), __hmax2_nan(w[2], w[3])));
+      T2 left, right;
+      left.x = a.x; left.y = b.x;
+      right.x = a.y; right.y = b.y;
+      T2 v = __hmin2_nan(left, right);
+#pragma unroll
+      for (int o = R::kLanes / 2; o; o >>= 1) v = __hmin2_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+      low[n][kv] = v;
+    }
+  // The scale and offset of the lanes' 2 kEach rows, each worked out by one lane in four (the divisions are a third of the work).
+  static_assert(kEach == 2 && R::kLanes >= 4, "a row's lanes take its four (token, K or V) in turn");
+  uint32_t pair;
+  float inv;
+  {
+    const T2 v = part & 2 ? (part & 1 ? low[1][1] : low[1][0]) : (part & 1 ? low[0][1] : low[0][0]);
+    const float mn = to_f32(v.x), mx = -to_f32(v.y);
+    // max/15 - min/15: max - min can pass the largest fp32 number
+    __nv_bfloat162 so;
+    so.x = __float2bfloat16_rn(__fsub_rn(__fdiv_rn(mx, 15.f), __fdiv_rn(mn, 15.f)));
+    so.y = __float2bfloat16_rn(mn);
+    if (!(fabsf(mn) < INFINITY && fabsf(mx) < INFINITY)) so.x = so.y = __ushort_as_bfloat16(0x7FFF);
+    inv = __fdividef(1.f, __bfloat162float(so.x));
+    pair = *reinterpret_cast<uint32_t*>(&so);
+  }
 #pragma unroll
   for (int n = 0; n < kEach; ++n) {
     const int row = (int)((start + first + n * (R::kTokens / kEach)) & (kBlk - 1));
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      // minimum and negated maximum of the row side by side, NaN if there is one; a missing row is all zeros
-      using T2 = typename Pair<T>::type;
-      T2 w[4], low;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = blk[n] ? reinterpret_cast<const T2*>(&raw[n][kv])[e] : Pair<T>::zero();
-      {
-        const T2 a = __hmin2_nan(__hmin2_nan(w[0], w[1]), __hmin2_nan(w[2], w[3]));
-        const T2 b = __hneg2(__hmax2_nan(__hmax2_nan(w[0], w[1]), __hmax2_nan(w[2], w[3])));
-        T2 first, second;
-        first.x = a.x; first.y = b.x;
-        second.x = a.y; second.y = b.y;
-        low = __hmin2_nan(first, second);
-      }
-#pragma unroll
-      for (int o = R::kLanes / 2; o; o >>= 1) low = __hmin2_nan(low, __shfl_xor_sync(0xffffffffu, low, o));
+      const uint32_t so = __shfl_sync(0xffffffffu, pair, 2 * n + kv, R::kLanes);
+      const float by = __shfl_sync(0xffffffffu, inv, 2 * n + kv, R::kLanes);
       if (!blk[n]) continue;
-      const float mn = to_f32(low.x), mx = -to_f32(low.y);
-      const bool fine = fabsf(mn) < INFINITY && fabsf(mx) < INFINITY;
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = to_f32(raw[n][kv].e[e]);
-      // max/15 - min/15: max - min can pass the largest fp32 number
-      __nv_bfloat16 sc = __float2bfloat16_rn(__fsub_rn(__fdiv_rn(mx, 15.f), __fdiv_rn(mn, 15.f)));
-      __nv_bfloat16 of = __float2bfloat16_rn(mn);
-      const float s = __bfloat162float(sc), o = __bfloat162float(of);
+      const float s = __uint_as_float(so << 16), o = __uint_as_float(so & 0xFFFF0000u);
       uint32_t codes = 0;
-      if (fine && s > 0.f) {
+      if (s > 0.f) {  // (not NaN)
         // The code is the rounded quotient rounded to an integer (adding 1.5 2^23 does that, half to even, and leaves it in the
         // low bits).  A product with the reciprocal is within 2^-21 of a quotient below 16: only one that near to a half needs
         // the division.
-        const float inv = __fdividef(1.f, s), magic = 12582912.f;
-        bool near = !(s > 1e-37f && s < 1e37f);  // the reciprocal may have overflowed
+        const float magic = 12582912.f;
+        float v[8], far = s > 1e-37f && s < 1e37f ? 0.f : 1.f;  // how far from an integer; the reciprocal may have overflowed
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float q = __fsub_rn(v[e], o) * inv;
+        for (int e = 0; e < 8; ++e) v[e] = to_f32(raw[n][kv].e[e]);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          float2 q = mul2(add2(make_float2(v[e], v[e + 1]), make_float2(-o, -o)), make_float2(by, by));
           // a bf16 row's offset is its minimum and 15 rounded steps pass its maximum by less than half of one: nothing to clamp
-          if (!std::is_same<T, __nv_bfloat16>::value) q = fminf(fmaxf(q, 0.f), 15.f);
-          const float r = __fadd_rn(q, magic);
-          near = near || fabsf(q - __fsub_rn(r, magic)) > 0.4999f;
-          codes = __funnelshift_r(codes, __float_as_uint(r), 4);  // the code enters at the top
+          if (!std::is_same<T, __nv_bfloat16>::value)
+            q = make_float2(fminf(fmaxf(q.x, 0.f), 15.f), fminf(fmaxf(q.y, 0.f), 15.f));
+          const float2 r = add2(q, make_float2(magic, magic)), t = add2(r, make_float2(-magic, -magic));
+          const float2 d = add2(q, make_float2(-t.x, -t.y));
+          far = fmax3(far, fabsf(d.x), fabsf(d.y));
+          codes = __funnelshift_r(codes, __float_as_uint(r.x), 4);  // the code enters at the top
+          codes = __funnelshift_r(codes, __float_as_uint(r.y), 4);
         }
-        if (near) {
+        if (far > 0.49997f) {
           codes = 0;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -160,14 +197,8 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ Mov
           }
         }
       }
-      if (!fine) sc = of = __ushort_as_bfloat16(0x7FFF);
       *reinterpret_cast<uint32_t*>(blk[n] + kv * kBlk * (D / 2) + row * (D / 2) + part * 4) = codes;
-      if (part == 0) {
-        __nv_bfloat162 pair;
-        pair.x = sc;
-        pair.y = of;
-        *reinterpret_cast<__nv_bfloat162*>(blk[n] + kBlk * D + kv * kBlk * 4 + row * 4) = pair;
-      }
+      if (part == 0) *reinterpret_cast<uint32_t*>(blk[n] + kBlk * D + kv * kBlk * 4 + row * 4) = so;
     }
   }
 }
@@ -250,7 +281,7 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ MoveP
 // second product, gained nothing at d = 128: the registers that they need are not there.
 constexpr int kWarps = 8;
 template <int D>
-constexpr int kStages = D == 128 ? 2 : 4;
+constexpr int kStages = D == 128 ? 2 : 3;
 constexpr int kUnit = 2 * kBlk;     // tokens of a unit
 constexpr int kPad = 2;             // units that a segment counts for besides its own: loading q and writing results
 constexpr int kMaxPlaces = 2130706432;  // 2^31 - 2^24: a place plus a stretch stays an int
