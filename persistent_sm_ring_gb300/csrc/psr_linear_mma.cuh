@@ -146,6 +146,40 @@ __device__ __forceinline__ uint32_t operand_lo(uint32_t tile, int kk) {
   return MN ? sdesc_lo(tile + kk * 2048, 8192) : sdesc_lo(tile + kk * 32, 16);
 }
 
+// The products of one K step (64 columns) of a 256 x 256 tile of a pair of CTAs: four of 16 columns, from the descriptors' low
+// words of the first, issued by the lanes that have `lead` set (one).
+template <bool AMN, bool BMN>
+__device__ __forceinline__ void mma_step(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t"
+      "setp.eq.b32 p, 0, 0;\n\t"
+      "add.s64 a, a, %7;\n\t"
+      "add.s64 b, b, %8;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t"
+      "add.s64 a, a, %7;\n\t"
+      "add.s64 b, b, %8;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t"
+      "add.s64 a, a, %7;\n\t"
+      "add.s64 b, b, %8;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(sdesc_hi_sw128(1024)), "r"(idesc), "r"(accumulate), "r"(lead), "n"(AMN ? 128 : 2), "n"(BMN ? 128 : 2)
+      : "memory");
+}
+__device__ __forceinline__ void commit_pair(uint64_t* bar, uint16_t ctas, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(
+          smem_u32(bar)),
+      "h"(ctas), "r"(lead)
+      : "memory");
+}
+
 // ================================================================================================
 // pair_gemm
 // ================================================================================================
@@ -384,14 +418,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t smem_base = (raw + 1023u) & ~1023u;
   uint8_t* epi = smem_raw + (smem_base - raw) + kChunks * kHalf;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;  // (uniform, for the compiler)
   uint32_t n_rank;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n_rank));
   if (n_rank != 2u) {  // no caller launches it without pairs
     if (threadIdx.x == 0) raise_error(p, SITE_LAUNCH);
     return;
   }
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t rank = __shfl_sync(0xffffffffu, cluster_ctarank(), 0);
   clear_ctrl(p.clear);
   launch_dependents();
   if (threadIdx.x == 0) {
@@ -454,42 +488,40 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       if (!ok) sc.abort = 1;
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      constexpr uint32_t kHi = sdesc_hi_sw128(1024);
+    if (rank == 0) {  // the whole warp, so that addresses and descriptors stay in uniform registers; lane 0 issues
+      const uint32_t tmem = sc.tmem_base;
+      const uint32_t a0 = operand_lo<AMN>(smem_base, 0), b0 = operand_lo<BMN>(smem_base, 0);
       uint32_t c = 0, chunk = 0, u = 0;  // steps and chunks consumed, accumulator halves begun
       bool ok = true;
       auto next = [&]() {
-        const uint32_t at = smem_base + chunk * kHalf;
+        const uint32_t at = chunk * (kHalf / 16);
         chunk = chunk + 1 == kChunks ? 0 : chunk + 1;
         return at;
       };
       for (int i = 0; ok && pair_item(p, pair, n_pairs, i, it); ++i) {
         for (int ks = 0; ks < it.n_k && ok; ++ks, ++c) {
           const uint32_t s = c % kSteps;
-          if (!wait_own(&sc.full[s], (c / kSteps) & 1u, p, &sc, SITE_FULL)) { ok = false; break; }
+          ok = __all_sync(0xffffffffu, wait_own(&sc.full[s], (c / kSteps) & 1u, p, &sc, SITE_FULL));
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a = next();
+          const uint32_t a = a0 + next();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (h >= it.n) break;
-            const uint32_t slot = (u + h) % 2, b = next();
+            const uint32_t slot = (u + h) % 2, b = b0 + next();
             if (ks == 0) {  // the half's previous sums have been read back
-              if (u + h >= 2 && !wait_own<true>(&sc.acc_empty[slot], ((u + h) / 2 - 1) & 1u, p, &sc, SITE_ACC_EMPTY)) {
-                ok = false;
-                break;
-              }
+              if (u + h >= 2)
+                ok = __all_sync(0xffffffffu, wait_own<true>(&sc.acc_empty[slot], ((u + h) / 2 - 1) & 1u, p, &sc, SITE_ACC_EMPTY));
+              if (!ok) break;
               tc_fence_after();
             }
-#pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk)
-              mma_ss_cg<2>(sc.tmem_base + slot * 256, operand_lo<AMN>(a, kk), kHi, operand_lo<BMN>(b, kk), kHi, p.idesc,
-                           (ks > 0 || kk > 0) ? 1u : 0u);
+            mma_step<AMN, BMN>(tmem + slot * 256, a, b, p.idesc, ks > 0, lane == 0);
           }
           if (!ok) break;
-          mma_commit_cg<2>(&sc.empty[s], 3);
+          commit_pair(&sc.empty[s], 3, lane == 0);
         }
         if (!ok) break;
-        for (int h = 0; h < it.n; ++h) mma_commit_cg<2>(&sc.acc_full[(u + h) % 2], 3);
+        for (int h = 0; h < it.n; ++h) commit_pair(&sc.acc_full[(u + h) % 2], 3, lane == 0);
         u += it.n;
       }
       if (!ok) sc.abort = 1;
@@ -547,9 +579,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   // waited for it; after a wait that gave up, the loads in flight get two milliseconds.
   if (warp == 1 && lane == 0 && rank == 0) {
     mma_commit_cg<2>(&sc.drain, 1);
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(&sc.drain, 0) && globaltimer_ns() - t0 < 100000000ull) {
-    }
+    wait_last(&sc.drain, 0);
   }
   __syncthreads();
   if (sc.abort && threadIdx.x == 0) {
@@ -777,16 +807,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   // every MMA has completed and every load has landed before the CTA leaves
   if (warp == 1 && lane == 0) {
     mma_commit(&sc.drain);
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(&sc.drain, 0) && globaltimer_ns() - t0 < 100000000ull) {
-    }
+    wait_last(&sc.drain, 0);
   }
   if (threadIdx.x == 0) {
-    const uint64_t t0 = globaltimer_ns();
     for (uint32_t s = 0; s < n_st && s < fills; ++s) {
       const uint32_t m = s + ((fills - 1 - s) / n_st) * n_st;
-      while (!mbar_try_wait(&sc.full[s], (m / n_st) & 1u) && globaltimer_ns() - t0 < 100000000ull) {
-      }
+      wait_last(&sc.full[s], (m / n_st) & 1u);
     }
   }
   tc_fence_before();
