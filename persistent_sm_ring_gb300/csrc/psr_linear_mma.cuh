@@ -258,14 +258,23 @@ __device__ __forceinline__ bool pair_item(const PairParams& p, int pair, int n_p
   return true;
 }
 
-// One 128-row operand tile of a stage.
+// One 128-row operand tile of a stage, asked for by the lanes that have `lead` set (one).
+__device__ __forceinline__ void load_pair(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];\n\t}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar), "r"(lead)
+      : "memory");
+}
 template <bool MN>
-__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* m, int k, int row, uint32_t bar) {
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* m, int k, int row, uint32_t bar, uint32_t lead) {
   if constexpr (MN) {
-    tma_load_2d_pair(dst, m, row, k, bar);
-    tma_load_2d_pair(dst + 8192, m, row + 64, k, bar);
+    load_pair(dst, m, row, k, bar, lead);
+    load_pair(dst + 8192, m, row + 64, k, bar, lead);
   } else {
-    tma_load_2d_pair(dst, m, k, row, bar);
+    load_pair(dst, m, k, row, bar, lead);
   }
 }
 
@@ -453,40 +462,40 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   tc_fence_after();
 
   const int pair = blockIdx.x / 2, n_pairs = gridDim.x / 2;
+  const uint32_t full0 = __shfl_sync(0xffffffffu, mapa_shared(smem_u32(&sc.full[0]), 0), 0);  // of the pair's first CTA
   PairItem it;
-  if (warp == 0) {
-    if (lane == 0) {
-      uint32_t head = 0, tail = 0, chunk = 0, used = 0, wide = 0;  // steps issued and known read, chunks, step sizes
-      bool ok = true;
-      for (int i = 0; ok && pair_item(p, pair, n_pairs, i, it); ++i) {
-        const int arow = it.tm * 256 + (int)rank * kRows, brow = it.tn * 256 + (int)rank * kRows;
-        const uint32_t n = 1 + it.n;
-        for (int ks = it.k0; ks < it.k0 + it.n_k; ++ks) {
-          while (used + n > kChunks) {  // the oldest step gives its chunks back (at most 6 are in flight)
-            const uint32_t s = tail % kSteps;
-            if (!wait_own(&sc.empty[s], (tail / kSteps) & 1u, p, &sc, SITE_EMPTY)) { ok = false; break; }
-            used -= 2 + (wide >> s & 1u);
-            ++tail;
-          }
+  if (warp == 0) {  // the whole warp, for the same reason as the next one
+    uint32_t head = 0, tail = 0, chunk = 0, used = 0, wide = 0;  // steps issued and known read, chunks, step sizes
+    bool ok = true;
+    for (int i = 0; ok && pair_item(p, pair, n_pairs, i, it); ++i) {
+      const int arow = it.tm * 256 + (int)rank * kRows, brow = it.tn * 256 + (int)rank * kRows;
+      const uint32_t n = 1 + it.n;
+      for (int ks = it.k0; ks < it.k0 + it.n_k; ++ks) {
+        while (used + n > kChunks) {  // the oldest step gives its chunks back (at most 6 are in flight)
+          const uint32_t s = tail % kSteps;
+          ok = __all_sync(0xffffffffu, wait_own(&sc.empty[s], (tail / kSteps) & 1u, p, &sc, SITE_EMPTY));
           if (!ok) break;
-          const uint32_t s = head % kSteps;
-          wide = (wide & ~(1u << s)) | ((n - 2) << s);
-          if (rank == 0) mbar_expect_tx(&sc.full[s], 2 * n * kHalf);  // both CTAs' bytes
-          const uint32_t bar = mapa_shared(smem_u32(&sc.full[s]), 0);
-          auto next = [&]() {
-            const uint32_t at = smem_base + chunk * kHalf;
-            chunk = chunk + 1 == kChunks ? 0 : chunk + 1;
-            return at;
-          };
-          load_operand<AMN>(next(), &ma, ks * kBK, arow, bar);
-          load_operand<BMN>(next(), &mb, ks * kBK, brow, bar);
-          if (it.n == 2) load_operand<BMN>(next(), &mb, ks * kBK, brow + 256, bar);
-          used += n;
-          ++head;
+          used -= 2 + (wide >> s & 1u);
+          ++tail;
         }
+        if (!ok) break;
+        const uint32_t s = head % kSteps;
+        wide = (wide & ~(1u << s)) | ((n - 2) << s);
+        if (rank == 0 && lane == 0) mbar_expect_tx(&sc.full[s], 2 * n * kHalf);  // both CTAs' bytes
+        const uint32_t bar = full0 + s * 8;
+        auto next = [&]() {
+          const uint32_t at = smem_base + chunk * kHalf;
+          chunk = chunk + 1 == kChunks ? 0 : chunk + 1;
+          return at;
+        };
+        load_operand<AMN>(next(), &ma, ks * kBK, arow, bar, lane == 0);
+        load_operand<BMN>(next(), &mb, ks * kBK, brow, bar, lane == 0);
+        if (it.n == 2) load_operand<BMN>(next(), &mb, ks * kBK, brow + 256, bar, lane == 0);
+        used += n;
+        ++head;
       }
-      if (!ok) sc.abort = 1;
     }
+    if (!ok) sc.abort = 1;
   } else if (warp == 1) {
     if (rank == 0) {  // the whole warp, so that addresses and descriptors stay in uniform registers; lane 0 issues
       const uint32_t tmem = sc.tmem_base;
