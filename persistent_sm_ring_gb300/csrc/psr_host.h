@@ -53,8 +53,7 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 
 // Bounded wait on a barrier: false after the timeout, or once another wait of the CTA has given up.  The control block's
 // abort word is not consulted: it is cleared by the launch itself (clear_ctrl), while other CTAs already run.
-// The clock is first read after 32 polls: reading it takes longer than most waits (a read before the second poll made every
-// 64-column step of a 256 x 256 tile take 330 ns instead of 265).
+// The clock is first read after 32 polls, most waits being shorter.
 template <bool CL = false, class KP, class SC>
 __device__ __forceinline__ bool wait_own(uint64_t* bar, uint32_t parity, const KP& p, SC* sc, uint32_t site) {
   uint64_t t0 = 0;

@@ -2,6 +2,7 @@
 //
 // The products are the tcgen05 kernels of psr_linear_mma.cuh.  A tensor map wants rows that start on 16-byte boundaries: an
 // operand with others is copied into the workspace first (4100 columns: 0.09 ms of 0.21 at 8192 x 4096 x 4100).
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -272,17 +273,19 @@ static int product(const Operands& o, Epilogue e, Launch& l) {
     if (streams(o.M)) return launch_stream<BMN>(o, e, l);
   const int splits = pair_splits(o.M, o.N, o.K);
   if (splits > 1) return launch_pair<AMN, BMN>(o, e, false, splits, l);
-  // A wave of 512-column tiles takes 16 clocks for each K and then its epilogue, when the accumulators are not free for the
-  // next tile (all SMs write at once); one of 256-column tiles 11.5 for each K (the tile loads bound it) with the
-  // epilogue of the tile before behind it.  Clocks as measured at 2048 x 8192 x 4096 (89 us and 103 us, with gelu, bias,
-  // residual and z 109 and 116) and 8192 x 8192 x 1024 (110 and 107; 178 and 147).
+  // Tiles of 256 columns take 8.6 clocks for each K and tile (a little more with an operand that is MN-major), or as long as
+  // the epilogue, which runs beside the next tile's products, if that is longer.  Tiles of 512 columns take 16 and move less, but
+  // their epilogue has the accumulators to itself: nothing runs beside it.  Rows that do not start on 128-byte boundaries
+  // take the loads half as long again.  Clocks as measured at 16384 x 4096 x 512 (one / two: 57 / 71 us, with gelu, bias, residual and
+  // z 132 / 132), 4096 x 4096 x 4096 (82 / 87, 95 / 107), dx of 8192 x 8192 x 8192 (617 / 598) and 1531 x 5000 x 1736 (31 / 28).
   const long long rows = (o.M + 255) / 256, n_pairs = l.n_sm / 2;
-  auto waves = [&](long long cols) { return (rows * ((o.N + cols - 1) / cols) + n_pairs - 1) / n_pairs; };
-  const double epi = 6000.0 + (e.act ? 3000.0 : 0.0) + (e.z ? 4000.0 : 0.0) + (e.res ? 4000.0 : 0.0);  // of 256 columns
-  const long long tiles = rows * ((o.N + 511) / 512), halves = last_halves(tiles, (int)n_pairs);
-  const double two = (tiles / n_pairs + (halves || tiles % n_pairs == 0 ? 0 : 1)) * (16.0 * o.K + 2.0 * epi) +
-                     (halves ? 11.5 * o.K + epi : 0.0);
-  const double one = waves(256) * (11.5 * o.K + 1500.0 > epi ? 11.5 * o.K + 1500.0 : epi);
+  const double more = (e.act > PSR_ACT_RELU ? 3200.0 : 0.0) + (e.z ? 2600.0 : 0.0) + (e.res ? 3200.0 : 0.0) + (e.bias ? 1000.0 : 0.0);
+  const bool ragged = o.lda % 64 || o.ldb % 64;
+  const double k1 = ragged ? 12.8 : 8.6 + 0.3 * (AMN + BMN), k2 = ragged ? 18.4 : 16.0;
+  const long long ones = rows * ((o.N + 255) / 256), tiles = rows * ((o.N + 511) / 512), halves = last_halves(tiles, (int)n_pairs);
+  const double one = (double)((ones + n_pairs - 1) / n_pairs) * std::max(k1 * o.K, 7000.0 + more);
+  const double two = (double)(tiles / n_pairs + (halves || tiles % n_pairs == 0 ? 0 : 1)) * (k2 * o.K + 2 * (4800.0 + more)) +
+                     (halves ? k1 * o.K + 4800.0 + more : 0.0);
   return launch_pair<AMN, BMN>(o, e, two <= one, 1, l);
 }
 

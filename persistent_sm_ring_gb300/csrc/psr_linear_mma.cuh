@@ -6,8 +6,9 @@
 //
 //  * pair_gemm: a pair of CTAs (cta_group::2) computes tiles of 256 rows and 512 or 256 columns, each CTA 128 rows and 128
 //    columns of each 256-column half.  512 columns fill tensor memory and move 48 B/clk per SM at the tensor rate, but the
-//    next tile's products wait for the epilogue; 256 columns move 64 B/clk, above what TMA tile loads land (a K step of 64
-//    then takes 700 to 800 clocks instead of 512), and the accumulator is double-buffered.
+//    next tile's products wait for the epilogue; 256 columns move 64 B/clk, and the accumulator is double-buffered.  The warps
+//    that issue loads and products run converged, with one lane's predicate on those instructions, so that their operands
+//    come from uniform registers: issued by a lane on its own, a K step of 64 took 330 ns instead of 273 (the products alone 265).
 //  * stream_gemm: for few rows of A.  The output is computed transposed, W's rows on the 128 tensor memory lanes
 //    and the tokens in the columns, so that W streams through once.  The (tile, K step) units are dealt out
 //    evenly over one CTA per SM; a tile whose K range is split leaves fp32 partials that a second kernel joins.
@@ -544,16 +545,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     bool ok = true;
     for (int i = 0; ok && pair_item(p, pair, n_pairs, i, it); ++i) {
       const int i0 = it.tm * 256 + (int)rank * kRows + quarter * 32;
-      if (res && i0 + lane < p.M) {
-        // this warp's part of the residual to L2 while the products run: 128 bytes of a row each
-        for (int h = 0; h < it.n; ++h) {
-          const int j0 = (it.tn + h) * 256 + cgroup * 64;
-          if (j0 < p.N) {
-            const uint16_t* g = static_cast<const uint16_t*>(e.res) + (i0 + lane) * e.ldr + j0;
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(g));
-          }
-        }
-      }
 #pragma unroll 1
       for (int b = 0; b < 2 * it.n && ok; ++b) {
         const uint32_t slot = u % 2;
