@@ -147,37 +147,59 @@ __device__ __forceinline__ uint32_t operand_lo(uint32_t tile, int kk) {
   return MN ? sdesc_lo(tile + kk * 2048, 8192) : sdesc_lo(tile + kk * 32, 16);
 }
 
-// The products of one K step (64 columns) of a 256 x 256 tile of a pair of CTAs: four of 16 columns, from the descriptors' low
-// words of the first, issued by the lanes that have `lead` set (one).
-template <bool AMN, bool BMN>
+// The products of one K step of 64 columns: four of 16, from the descriptors' low words of the first, issued by the lanes that have
+// `lead` set (one).  PAIR: for a pair of CTAs.
+template <bool PAIR, bool AMN, bool BMN>
 __device__ __forceinline__ void mma_step(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate, uint32_t lead) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
-      "setp.ne.b32 q, %6, 0;\n\t"
-      "setp.ne.b32 p, %5, 0;\n\t"
-      "mov.b64 a, {%1, %3};\n\t"
-      "mov.b64 b, {%2, %3};\n\t"
-      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t"
-      "setp.eq.b32 p, 0, 0;\n\t"
-      "add.s64 a, a, %7;\n\t"
-      "add.s64 b, b, %8;\n\t"
-      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t"
-      "add.s64 a, a, %7;\n\t"
-      "add.s64 b, b, %8;\n\t"
-      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t"
-      "add.s64 a, a, %7;\n\t"
-      "add.s64 b, b, %8;\n\t"
-      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(sdesc_hi_sw128(1024)), "r"(idesc), "r"(accumulate), "r"(lead), "n"(AMN ? 128 : 2), "n"(BMN ? 128 : 2)
-      : "memory");
+#define PSR_MMA_STEP(GROUP)                                                                                          \
+  asm volatile(                                                                                                      \
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"                                                                 \
+      "setp.ne.b32 q, %6, 0;\n\t"                                                                                    \
+      "setp.ne.b32 p, %5, 0;\n\t"                                                                                    \
+      "mov.b64 a, {%1, %3};\n\t"                                                                                     \
+      "mov.b64 b, {%2, %3};\n\t"                                                                                     \
+      "@q tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], a, b, %4, p;\n\t"                                         \
+      "setp.eq.b32 p, 0, 0;\n\t"                                                                                     \
+      "add.s64 a, a, %7;\n\t"                                                                                        \
+      "add.s64 b, b, %8;\n\t"                                                                                        \
+      "@q tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], a, b, %4, p;\n\t"                                         \
+      "add.s64 a, a, %7;\n\t"                                                                                        \
+      "add.s64 b, b, %8;\n\t"                                                                                        \
+      "@q tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], a, b, %4, p;\n\t"                                         \
+      "add.s64 a, a, %7;\n\t"                                                                                        \
+      "add.s64 b, b, %8;\n\t"                                                                                        \
+      "@q tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], a, b, %4, p;\n\t}\n" ::"r"(d),                            \
+      "r"(a), "r"(b), "r"(sdesc_hi_sw128(1024)), "r"(idesc), "r"(accumulate), "r"(lead), "n"(AMN ? 128 : 2),         \
+      "n"(BMN ? 128 : 2)                                                                                             \
+      : "memory")
+  if constexpr (PAIR) PSR_MMA_STEP("2");
+  else PSR_MMA_STEP("1");
+#undef PSR_MMA_STEP
 }
-__device__ __forceinline__ void commit_pair(uint64_t* bar, uint16_t ctas, uint32_t lead) {
+// Arrive on the barrier (of both CTAs of the pair) when the lane's products so far have completed.
+__device__ __forceinline__ void commit_pair(uint64_t* bar, uint32_t lead) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
       "setp.ne.b32 q, %2, 0;\n\t"
       "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(
           smem_u32(bar)),
-      "h"(ctas), "r"(lead)
+      "h"((uint16_t)3), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void load_one(uint32_t dst, const CUtensorMap* m, int x, int y, uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(smem_u32(bar)), "r"(lead)
       : "memory");
 }
 
@@ -525,13 +547,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               if (!ok) break;
               tc_fence_after();
             }
-            mma_step<AMN, BMN>(tmem + slot * 256, a, b, p.idesc, ks > 0, lane == 0);
+            mma_step<true, AMN, BMN>(tmem + slot * 256, a, b, p.idesc, ks > 0, lane == 0);
           }
           if (!ok) break;
-          commit_pair(&sc.empty[s], 3, lane == 0);
+          commit_pair(&sc.empty[s], lane == 0);
         }
         if (!ok) break;
-        for (int h = 0; h < it.n; ++h) commit_pair(&sc.acc_full[(u + h) % 2], 3, lane == 0);
+        for (int h = 0; h < it.n; ++h) commit_pair(&sc.acc_full[(u + h) % 2], lane == 0);
         u += it.n;
       }
       if (!ok) sc.abort = 1;
@@ -646,7 +668,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   __shared__ StreamSmem sc;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t smem_base = (raw + 1023u) & ~1023u;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;  // (uniform, for the compiler)
   const uint32_t x_bytes = (uint32_t)p.tb * kBK * 2, stage_bytes = kSub * (kHalf + x_bytes);
   const uint32_t n_st = (uint32_t)p.stages;
   clear_ctrl(p.clear);
@@ -678,73 +700,73 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   const long long u0 = (long long)blockIdx.x * p.per_cta;
   const long long u1 = u0 + p.per_cta < total ? u0 + p.per_cta : total;
   uint32_t fills = 0;
-  if (warp == 0) {
-    if (lane == 0) {
-      long long u = u0;
-      int tile = (int)(u / p.n_k), ks = (int)(u % p.n_k);
-      for (; u < u1; ++u) {
-        const uint32_t s = fills % n_st, use = fills / n_st;
-        if (use > 0 && !wait_own(&sc.empty[s], (use - 1) & 1u, p, &sc, SITE_EMPTY)) {
-          sc.abort = 1;
-          break;
-        }
-        mbar_expect_tx(&sc.full[s], stage_bytes);
-        const uint32_t base = smem_base + s * stage_bytes;
-        const int wrow = tile * kRows;
+  if (warp == 0) {  // this warp and the next converged, as in pair_gemm
+    int tile = (int)(u0 / p.n_k), ks = (int)(u0 % p.n_k);
+    uint32_t s = 0, phase = 0;
+    for (long long u = u0; u < u1; ++u) {
+      if (fills >= n_st && !__all_sync(0xffffffffu, wait_own(&sc.empty[s], phase ^ 1u, p, &sc, SITE_EMPTY))) {
+        sc.abort = 1;
+        break;
+      }
+      if (lane == 0) mbar_expect_tx(&sc.full[s], stage_bytes);
+      const uint32_t base = smem_base + s * stage_bytes;
+      const int wrow = tile * kRows;
 #pragma unroll
-        for (int h = 0; h < kSub; ++h) {
-          const int k = (ks * kSub + h) * kBK;
-          const uint32_t dst = base + h * kHalf;
-          if constexpr (AMN) {
-            tma_load_2d(dst, &mw, wrow, k, &sc.full[s]);
-            tma_load_2d(dst + 8192, &mw, wrow + 64, k, &sc.full[s]);
-          } else {
-            tma_load_2d(dst, &mw, k, wrow, &sc.full[s]);
-          }
+      for (int h = 0; h < kSub; ++h) {
+        const int k = (ks * kSub + h) * kBK;
+        const uint32_t dst = base + h * kHalf;
+        if constexpr (AMN) {
+          load_one(dst, &mw, wrow, k, &sc.full[s], lane == 0);
+          load_one(dst + 8192, &mw, wrow + 64, k, &sc.full[s], lane == 0);
+        } else {
+          load_one(dst, &mw, k, wrow, &sc.full[s], lane == 0);
         }
+      }
 #pragma unroll
-        for (int h = 0; h < kSub; ++h)
-          tma_load_2d(base + kSub * kHalf + h * x_bytes, &mx, (ks * kSub + h) * kBK, 0, &sc.full[s]);
-        ++fills;
-        if (++ks == p.n_k) {
-          ks = 0;
-          ++tile;
-        }
+      for (int h = 0; h < kSub; ++h)
+        load_one(base + kSub * kHalf + h * x_bytes, &mx, (ks * kSub + h) * kBK, 0, &sc.full[s], lane == 0);
+      ++fills;
+      if (++s == n_st) {
+        s = 0;
+        phase ^= 1u;
+      }
+      if (++ks == p.n_k) {
+        ks = 0;
+        ++tile;
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t kHi = sdesc_hi_sw128(1024);
-      uint32_t c = 0, seg = 0;
-      bool ok = true;
-      for (long long u = u0; u < u1 && ok; ++seg) {
-        const int left = p.n_k - (int)(u % p.n_k);
-        const int n = (int)(u1 - u < left ? u1 - u : left);
-        const uint32_t slot = seg % 2;
-        if (seg >= 2 && !wait_own(&sc.acc_empty[slot], (seg / 2 - 1) & 1u, p, &sc, SITE_ACC_EMPTY)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        for (int ks = 0; ks < n; ++ks, ++c) {
-          const uint32_t s = c % n_st;
-          if (!wait_own(&sc.full[s], (c / n_st) & 1u, p, &sc, SITE_FULL)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t base = smem_base + s * stage_bytes;
-#pragma unroll
-          for (int h = 0; h < kSub; ++h)
-#pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk)
-              mma_ss_w(sc.tmem_base + slot * p.tb, operand_lo<AMN>(base + h * kHalf, kk), kHi,
-                       operand_lo<false>(base + kSub * kHalf + h * x_bytes, kk), kHi, p.idesc, (ks > 0 || h > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&sc.empty[s]);
-        }
+    const uint32_t tmem = sc.tmem_base;
+    const uint32_t a0 = operand_lo<AMN>(smem_base, 0), b0 = operand_lo<false>(smem_base + kSub * kHalf, 0);
+    uint32_t s = 0, phase = 0, seg = 0;
+    bool ok = true;
+    for (long long u = u0; u < u1 && ok; ++seg) {
+      const int left = p.n_k - (int)(u % p.n_k);
+      const int n = (int)(u1 - u < left ? u1 - u : left);
+      const uint32_t slot = seg % 2;
+      if (seg >= 2) ok = __all_sync(0xffffffffu, wait_own(&sc.acc_empty[slot], (seg / 2 - 1) & 1u, p, &sc, SITE_ACC_EMPTY));
+      if (!ok) break;
+      tc_fence_after();
+      for (int ks = 0; ks < n; ++ks) {
+        ok = __all_sync(0xffffffffu, wait_own(&sc.full[s], phase, p, &sc, SITE_FULL));
         if (!ok) break;
-        mma_commit(&sc.acc_full[slot]);
-        u += n;
+        tc_fence_after();
+        const uint32_t at = s * (stage_bytes / 16);
+#pragma unroll
+        for (int h = 0; h < kSub; ++h)
+          mma_step<false, AMN, false>(tmem + slot * p.tb, a0 + at + h * (kHalf / 16), b0 + at + h * (x_bytes / 16), p.idesc,
+                                      ks > 0 || h > 0, lane == 0);
+        commit_one(&sc.empty[s], lane == 0);
+        if (++s == n_st) {
+          s = 0;
+          phase ^= 1u;
+        }
       }
-      if (!ok) sc.abort = 1;
+      if (!ok) break;
+      commit_one(&sc.acc_full[slot], lane == 0);
+      u += n;
     }
+    if (!ok) sc.abort = 1;
   } else if (warp >= 4) {
     const int quarter = warp % 4, row = quarter * 32 + lane;
     uint32_t seg = 0;
