@@ -272,7 +272,8 @@ static int product(const Operands& o, Epilogue e, Launch& l) {
   if constexpr (!AMN)
     if (streams(o.M)) return launch_stream<BMN>(o, e, l);
   const int splits = pair_splits(o.M, o.N, o.K);
-  if (splits > 1) return launch_pair<AMN, BMN>(o, e, false, splits, l);
+  constexpr bool kHalfType = std::is_same<T, __half>::value;
+  if (splits > 1) return launch_pair<AMN, BMN, kHalfType>(o, e, false, splits, l);
   // Tiles of 256 columns take 8.6 clocks for each K and tile (a little more with an operand that is MN-major), or as long as
   // the epilogue, which runs beside the next tile's products, if that is longer.  Tiles of 512 columns take 16 and move less, but
   // their epilogue has the accumulators to itself: nothing runs beside it.  Rows that do not start on 128-byte boundaries
@@ -286,7 +287,7 @@ static int product(const Operands& o, Epilogue e, Launch& l) {
   const double one = (double)((ones + n_pairs - 1) / n_pairs) * std::max(k1 * o.K, 7000.0 + more);
   const double two = (double)(tiles / n_pairs + (halves || tiles % n_pairs == 0 ? 0 : 1)) * (k2 * o.K + 2 * (4800.0 + more)) +
                      (halves ? k1 * o.K + 4800.0 + more : 0.0);
-  return launch_pair<AMN, BMN>(o, e, two <= one, 1, l);
+  return launch_pair<AMN, BMN, kHalfType>(o, e, two <= one, 1, l);
 }
 
 template <class T>

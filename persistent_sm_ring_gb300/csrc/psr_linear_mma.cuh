@@ -362,8 +362,9 @@ __device__ __forceinline__ void add16(uint32_t* v, const uint4& b, int half) {
 }
 
 // The block's 32 rows x 32 columns at (i0, j0), row `lane` in v: bias, z, activation, residual (its rows in `res`, as
-// rows_in read them), y.  ACT: there may be an activation (the gradients have none).
-template <bool ACT>
+// rows_in read them), y.  ACT: there may be an activation (the gradients have none).  HALF: fp16 (both
+// types behind a test cost a bias or a residual 700 clocks a block, the epilogue being bound by its instructions).
+template <bool ACT, bool HALF>
 __device__ __forceinline__ void pair_store(const Epilogue& e, int M, int N, uint8_t* stage, int i0, int j0,
                                            uint32_t (&v)[32], const uint4 (&res)[4]) {
   const int lane = threadIdx.x % 32;
@@ -374,11 +375,11 @@ __device__ __forceinline__ void pair_store(const Epilogue& e, int M, int N, uint
       const uint4* b = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.bias) + j0);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (j * 8 < cols) add16(v + 8 * j, b[j], e.half);
+        if (j * 8 < cols) add16(v + 8 * j, b[j], HALF);
     } else {
 #pragma unroll
       for (int c = 0; c < 32; ++c)
-        if (c < cols) v[c] = __float_as_uint(__uint_as_float(v[c]) + load16(e.bias, j0 + c, e.half));
+        if (c < cols) v[c] = __float_as_uint(__uint_as_float(v[c]) + load16(e.bias, j0 + c, HALF));
     }
   }
   auto out = [&](void* base, long long ld) {
@@ -387,7 +388,7 @@ __device__ __forceinline__ void pair_store(const Epilogue& e, int M, int N, uint
       uint32_t w[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        w[q] = pack16(__uint_as_float(v[j * 8 + 2 * q]), __uint_as_float(v[j * 8 + 2 * q + 1]), e.half);
+        w[q] = pack16(__uint_as_float(v[j * 8 + 2 * q]), __uint_as_float(v[j * 8 + 2 * q + 1]), HALF);
       *stage_chunk(stage, lane, j) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     uint16_t* g = static_cast<uint16_t*>(base) + (long long)i0 * ld + j0;
@@ -417,7 +418,7 @@ __device__ __forceinline__ void pair_store(const Epilogue& e, int M, int N, uint
       rows_in_odd(stage, static_cast<const uint16_t*>(e.res) + (long long)i0 * e.ldr + j0, e.ldr, rows, cols);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) add16(v + 8 * j, *stage_chunk(stage, lane, j), e.half);  // (columns past `cols` are not stored)
+    for (int j = 0; j < 4; ++j) add16(v + 8 * j, *stage_chunk(stage, lane, j), HALF);  // (columns past `cols` are not stored)
     __syncwarp();
   }
   out(e.y, e.ldy);
@@ -441,7 +442,7 @@ __device__ __forceinline__ void partial_store(const PairParams& p, int split, ui
   }
 }
 
-template <bool AMN, bool BMN>
+template <bool AMN, bool BMN, bool HALF>
 __global__ void __launch_bounds__(kPairThreads, 1)
     pair_gemm(const __grid_constant__ PairParams p, const __grid_constant__ CUtensorMap ma,
               const __grid_constant__ CUtensorMap mb) {
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           ++u;
         }
         if (p.splits > 1) partial_store(p, it.split, stage, i0, j0, v);
-        else pair_store<!BMN>(e, p.M, p.N, stage, i0, j0, v, rr);
+        else pair_store<!BMN, HALF>(e, p.M, p.N, stage, i0, j0, v, rr);
       }
     }
     if (!ok) sc.abort = 1;
@@ -930,13 +931,13 @@ inline bool mappable(const void* base, int rows, long long ld) {
 }
 
 // Shared memory and co-resident pairs of one pair_gemm instantiation on the current device; 0 on error.
-template <bool AMN, bool BMN>
+template <bool AMN, bool BMN, bool HALF>
 inline int pairs_of(int dev, int n_sm) {
   static std::mutex mu;
   static int known[64] = {};
   std::lock_guard<std::mutex> lk(mu);
   if (dev >= 0 && dev < 64 && known[dev]) return known[dev];
-  auto kern = pair_gemm<AMN, BMN>;
+  auto kern = pair_gemm<AMN, BMN, HALF>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem) != cudaSuccess) {
     cudaGetLastError();
     return 0;
@@ -987,9 +988,9 @@ inline int last_halves(long long tiles, int pairs) {
   return 2 * rest <= pairs ? (int)rest : 0;
 }
 
-template <bool AMN, bool BMN>
+template <bool AMN, bool BMN, bool HALF>
 inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, int splits, Launch& l) {
-  const int n_pairs = pairs_of<AMN, BMN>(l.dev, l.n_sm), cols = wide ? 512 : 256;
+  const int n_pairs = pairs_of<AMN, BMN, HALF>(l.dev, l.n_sm), cols = wide ? 512 : 256;
   if (n_pairs < 1) return PSR_ERR_CUDA;
   PairParams p = {};
   p.M = o.M;
@@ -1005,7 +1006,7 @@ inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, int spli
   p.partial = l.partial;
   p.ldp = (long long)cols * p.tiles_n;
   if (p.splits > 1 && (size_t)p.splits * o.M * p.ldp * 4 > l.partial_bytes) return PSR_ERR_ARG;
-  p.idesc = idesc16(256, 256, AMN, BMN, e.half != 0);
+  p.idesc = idesc16(256, 256, AMN, BMN, HALF);
   p.e = e;
   p.ctrl = l.ctrl;
   p.clear = l.clear;
@@ -1031,7 +1032,7 @@ inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, int spli
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, pair_gemm<AMN, BMN>, p, ma, mb) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, pair_gemm<AMN, BMN, HALF>, p, ma, mb) != cudaSuccess) {
     cudaGetLastError();
     return PSR_ERR_CUDA;
   }
