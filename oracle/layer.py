@@ -114,7 +114,8 @@ def kv4_quantise(x):
     with np.errstate(all="ignore"):
         mn, mx = x.min(-1, keepdims=True), x.max(-1, keepdims=True)
         fine = np.isfinite(x).all(-1, keepdims=True)
-        scale = to_bf16(np.where(fine, mx / np.float32(15) - mn / np.float32(15), 0))
+        r = np.float32(1) / np.float32(15)
+        scale = to_bf16(np.where(fine, mx * r - mn * r, 0))
         off = to_bf16(np.where(fine, mn, 0))
         c = np.clip(np.rint((x - off) / scale), 0, 15)
     c = np.where(fine & (scale > 0), c, 0).astype(np.uint8)

@@ -143,16 +143,17 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ Mov
       for (int o = R::kLanes / 2; o; o >>= 1) v = __hmin2_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
       low[n][kv] = v;
     }
-  // The scale and offset of the lanes' 2 kEach rows, each worked out by one lane in four (the divisions are a third of the work).
+  // The scale and offset of the lanes' 2 kEach rows, each worked out by one lane in four.
   static_assert(kEach == 2 && R::kLanes >= 4, "a row's lanes take its four (token, K or V) in turn");
   uint32_t pair;
   float inv;
   {
     const T2 v = part & 2 ? (part & 1 ? low[1][1] : low[1][0]) : (part & 1 ? low[0][1] : low[0][0]);
     const float mn = to_f32(v.x), mx = -to_f32(v.y);
-    // max/15 - min/15: max - min can pass the largest fp32 number
+    // max r - min r, r = 1/15 in fp32: max - min can pass the largest fp32 number
+    constexpr float r = 1.f / 15.f;
     __nv_bfloat162 so;
-    so.x = __float2bfloat16_rn(__fsub_rn(__fdiv_rn(mx, 15.f), __fdiv_rn(mn, 15.f)));
+    so.x = __float2bfloat16_rn(__fsub_rn(__fmul_rn(mx, r), __fmul_rn(mn, r)));
     so.y = __float2bfloat16_rn(mn);
     if (!(fabsf(mn) < INFINITY && fabsf(mx) < INFINITY)) so.x = so.y = __ushort_as_bfloat16(0x7FFF);
     inv = __fdividef(1.f, __bfloat162float(so.x));

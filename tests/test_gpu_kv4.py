@@ -40,7 +40,7 @@ def random_cache(rng, n_pages, Hkv, d, page):
 
 @pytest.mark.parametrize("case", [  # B S Hkv d page type
     (1, 1, 1, 64, 16, "bf16"), (2, 5, 3, 64, 16, "f16"), (3, 40, 2, 128, 32, "bf16"), (1, 130, 1, 128, 64, "f16"),
-    (2, 17, 2, 128, 256, "bf16")], ids=str)
+    (2, 17, 2, 128, 256, "bf16"), (1, 2500, 1, 64, 64, "f16")], ids=str)
 def test_append_and_read(psr, case):
     need_gpu()
     B, S, Hkv, d, page, t = case
