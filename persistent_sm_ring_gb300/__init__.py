@@ -501,6 +501,32 @@ class _Launch:
             return self.torch.empty(shape, dtype=dtype, device=self.device)
 
 
+# What the checks of a call found, by the shapes, strides, types and devices of its tensors and its other arguments: the checks
+# take longer than a small call's kernel, and the same call comes again for every layer and token.  Addresses are no part of
+# it (but for their alignment); what depends on them is checked every time.
+_plans = {}
+
+
+def _meta(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
+def _plan(key, check):
+    """The plan under a key, or what `check` returns for a new one.  key: a function (arguments that are no tensors, or
+    cannot be looked up, are for the checks to refuse) that takes numbers by their values: they may come as tensors, too."""
+    try:
+        key = key()
+        plan = _plans.get(key)
+    except (AttributeError, TypeError):
+        return check()
+    if plan is None:
+        plan = check()
+        if len(_plans) >= 1024:
+            _plans.clear()
+        _plans[key] = plan
+    return plan
+
+
 _TYPES = {}  # torch.dtype -> type code
 
 
@@ -617,6 +643,43 @@ def rotary(q, k, table, *, P=1, causal=CAUSAL, positions=None, offset=0, interle
     positions: int64 [S] or [B, S]; None takes offset + the global position of each row in the ring's shard order
     (P, causal as for ring_attn_fwd).  Returns (q_out, k_out), contiguous unless passed in; an output may be its own
     input, and shares no element with the other input or output."""
+    shape, qs, qos, ks, kos, pos_b, dev, q_shape, k_shape = _plan(
+        lambda: (rotary, _meta(q), _meta(k), _meta(table), _meta(positions), int(P), int(causal), bool(interleaved),
+                 float(amplitude), bool(inverse), _meta(q_out), _meta(k_out)),
+        lambda: _rotary_plan(q, k, table, P, causal, positions, interleaved, amplitude, q_out, k_out, inverse))
+    if offset:
+        shape = RotaryShape.from_buffer_copy(shape)
+        shape.offset = int(offset)
+    if q_out is not None or k_out is not None:
+        for x, out in ((q, q_out), (k, k_out)):
+            if out is not None:
+                _check_apart(out, x, "rotary", True)
+        if k is not None:
+            for out, x in ((q_out, k), (k_out, q)):
+                if out is not None:
+                    _check_other(out, x, "rotary", "an output overlaps the other input")
+            if q_out is not None and k_out is not None:
+                _check_other(q_out, k_out, "rotary", "the outputs overlap")
+    with _Launch(dev, stream, "rotary") as at:
+        if q_out is None:
+            q_out = at.empty(q_shape, q.dtype)
+        if k is None:
+            k_in = k_to = None
+        else:
+            if k_out is None:
+                k_out = at.empty(k_shape, q.dtype)
+            k_in, k_to = k.data_ptr(), k_out.data_ptr()
+        if shape.B == 0 or shape.S == 0:  # no rows, no pointers
+            return q_out, k_out
+        rc = load().psr_rotary(shape, q.data_ptr(), qs, q_out.data_ptr(), qos, k_in, ks, k_to, kos, table.data_ptr(),
+                               None if positions is None else positions.data_ptr(), pos_b, at.handle)
+    if rc != OK:
+        raise PsrError(rc, "psr_rotary")
+    return q_out, k_out
+
+
+def _rotary_plan(q, k, table, P, causal, positions, interleaved, amplitude, q_out, k_out, inverse):
+    import torch
     _check_cuda(q, "q", 4)
     B, Hq, S, d = q.shape
     dev, dtype = q.device, q.dtype
@@ -626,7 +689,6 @@ def rotary(q, k, table, *, P=1, causal=CAUSAL, positions=None, offset=0, interle
         _check_cuda(k, "k", 4)
         Hkv = k.shape[1]
         _check_like(k, "k", (B, Hkv, S, d), dtype, dev)
-    import torch
     _check_flat(table, "table", (table.numel(),), torch.int64, dev)
     pos_b = 0
     if positions is not None:
@@ -639,33 +701,16 @@ def rotary(q, k, table, *, P=1, causal=CAUSAL, positions=None, offset=0, interle
     for x, out, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
         if out is not None:
             _check_like(out, name, x.shape, dtype, dev)
-            _check_apart(out, x, "rotary", True)
+    flat = lambda H: Strides(H * S * d, S * d, d)
+    qs, qos = _heads_strides(q, "q"), flat(Hq) if q_out is None else _heads_strides(q_out, "q_out", True)
+    ks = kos = None
     if k is not None:
-        for out, x in ((q_out, k), (k_out, q)):
-            if out is not None:
-                _check_other(out, x, "rotary", "an output overlaps the other input")
-        if q_out is not None and k_out is not None:
-            _check_other(q_out, k_out, "rotary", "the outputs overlap")
-    qs, qos = _heads_strides(q, "q"), None if q_out is None else _heads_strides(q_out, "q_out", True)
-    ks, kos = None if k is None else _heads_strides(k, "k"), None if k_out is None else _heads_strides(k_out, "k_out", True)
-    with _Launch(dev, stream, "rotary") as at:
-        flat = lambda H: Strides(H * S * d, S * d, d)
-        if q_out is None:
-            q_out, qos = at.empty((B, Hq, S, d), dtype), flat(Hq)
-        if k is not None and k_out is None:
-            k_out, kos = at.empty((B, Hkv, S, d), dtype), flat(Hkv)
-        shape = RotaryShape(B, Hq, Hkv, S, int(P), d, int(causal), 2 * table.numel(), int(bool(interleaved)),
-                            int(bool(inverse)), code, float(amplitude), int(offset))
-        if B == 0 or S == 0:  # no rows, no pointers
-            if int(P) < 1 or S % int(P):
-                raise PsrError(ERR_ARG if int(P) < 1 else ERR_UNSUPPORTED, "psr_rotary")
-            return q_out, k_out
-        rc = load().psr_rotary(shape, q.data_ptr(), qs, q_out.data_ptr(), qos, None if k is None else k.data_ptr(), ks,
-                               None if k is None else k_out.data_ptr(), kos, table.data_ptr(),
-                               None if positions is None else positions.data_ptr(), pos_b, at.handle)
-    if rc != OK:
-        raise PsrError(rc, "psr_rotary")
-    return q_out, k_out
+        ks, kos = _heads_strides(k, "k"), flat(Hkv) if k_out is None else _heads_strides(k_out, "k_out", True)
+    if (B == 0 or S == 0) and (int(P) < 1 or S % int(P)):
+        raise PsrError(ERR_ARG if int(P) < 1 else ERR_UNSUPPORTED, "psr_rotary")
+    shape = RotaryShape(B, Hq, Hkv, S, int(P), d, int(causal), 2 * table.numel(), int(bool(interleaved)), int(bool(inverse)),
+                        code, float(amplitude), 0)
+    return shape, qs, qos, ks, kos, pos_b, dev, (B, Hq, S, d), (B, Hkv, S, d)
 
 
 def rotary_bwd(dq, dk, table, **kwargs):
@@ -688,7 +733,7 @@ def _linear_shape(x, w, activation, what):
     return sh, M, N, K
 
 
-def _row_stride(t, name, written=False):
+def _row_stride(t, name):
     rows, cols = t.shape
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: rows must be contiguous")
@@ -728,6 +773,37 @@ def linear(x, w, bias=None, residual=None, *, activation="none", save_z=False, o
 
     Returns (y [M, N], z, workspace).  With save_z (or a tensor z) z = x w^T + bias is written too, for
     linear_bwd(); otherwise it is None.  `out` may be the residual."""
+    sh, need, dev, shape = _plan(
+        lambda: (linear, _meta(x), _meta(w), _meta(bias), _meta(residual), activation, _meta(out), _meta(z), x.data_ptr() % 16,
+                 w.data_ptr() % 16),
+        lambda: _linear_plan(x, w, bias, residual, activation, out, z))
+    if out is not None:
+        for t in (x, w, bias):
+            if t is not None:
+                _check_apart(out, t, "linear", False)
+        if residual is not None:
+            _check_apart(out, residual, "linear", True)
+    if z is not None:
+        for t in (x, w, bias, residual, out):
+            if t is not None:
+                _check_apart(z, t, "linear", False)
+    with _Launch(dev, stream, "linear") as at:
+        if out is None:
+            out = at.empty(shape, x.dtype)
+        if z is None and save_z:
+            z = at.empty(shape, x.dtype)
+        workspace = _workspace(at, workspace, need, "linear")
+        if shape[0] == 0:
+            return out, z, workspace
+        rc = load().psr_linear(sh, x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
+                               None if residual is None else residual.data_ptr(), out.data_ptr(),
+                               None if z is None else z.data_ptr(), workspace.data_ptr(), need, int(timeout_ms), at.handle)
+    if rc != OK:
+        raise PsrError(rc, "psr_linear")
+    return out, z, workspace
+
+
+def _linear_plan(x, w, bias, residual, activation, out, z):
     sh, M, N, K = _linear_shape(x, w, activation, "linear")
     dev, dtype = x.device, x.dtype
     if bias is not None:
@@ -738,35 +814,13 @@ def linear(x, w, bias=None, residual=None, *, activation="none", save_z=False, o
     if out is not None:
         _check_like(out, "out", (M, N), dtype, dev)
         sh.ldy = _row_stride(out, "out")
-        for t in (x, w, bias):
-            if t is not None:
-                _check_apart(out, t, "linear", False)
-        if residual is not None:
-            _check_apart(out, residual, "linear", True)
     if z is not None:
         _check_like(z, "z", (M, N), dtype, dev)
         sh.ldz = _row_stride(z, "z")
-        for t in (x, w, bias, residual, out):
-            if t is not None:
-                _check_apart(z, t, "linear", False)
-    lib = load()
-    with _Launch(dev, stream, "linear") as at:
-        if out is None:
-            out = at.empty((M, N), dtype)
-        if z is None and save_z:
-            z = at.empty((M, N), dtype)
-        need = lib.psr_linear_workspace_bytes(sh, 0)
-        if need == 0:
-            raise PsrError(ERR_ARG, "psr_linear")
-        workspace = _workspace(at, workspace, need, "linear")
-        if M == 0:
-            return out, z, workspace
-        rc = lib.psr_linear(sh, x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
-                            None if residual is None else residual.data_ptr(), out.data_ptr(),
-                            None if z is None else z.data_ptr(), workspace.data_ptr(), need, int(timeout_ms), at.handle)
-    if rc != OK:
-        raise PsrError(rc, "psr_linear")
-    return out, z, workspace
+    need = load().psr_linear_workspace_bytes(sh, 0)
+    if need == 0:
+        raise PsrError(ERR_ARG, "psr_linear")
+    return sh, need, dev, (M, N)
 
 
 def linear_bwd(dy, x, w, z=None, *, activation="none", need_dx=True, need_dw=True, need_db=True, dx=None, dw=None,
@@ -774,6 +828,42 @@ def linear_bwd(dy, x, w, z=None, *, activation="none", need_dx=True, need_dw=Tru
     """Gradients of linear(): dy [M, N] is that of y, z the forward's (needed unless activation is "none"); the
     residual's gradient is dy itself.  Returns (dx [M, K], dw [N, K], db [N], workspace), None for those not asked for;
     dx, dw, db may be passed in (contiguous)."""
+    sh, need, dev, shapes = _plan(
+        lambda: (linear_bwd, _meta(dy), _meta(x), _meta(w), _meta(z), activation, _meta(dx), _meta(dw), _meta(db),
+                 x.data_ptr() % 16, w.data_ptr() % 16, dy.data_ptr() % 16),
+        lambda: _linear_bwd_plan(dy, x, w, z, activation, dx, dw, db))
+    for t in (dx, dw, db):
+        if t is not None:
+            for u in (dy, x, w, z):
+                if u is not None:
+                    _check_apart(t, u, "linear_bwd", False)
+    for a, b in ((dx, dw), (dx, db), (dw, db)):
+        if a is not None and b is not None:
+            _check_apart(a, b, "linear_bwd", False, "the outputs overlap")
+    with _Launch(dev, stream, "linear_bwd") as at:
+        if dx is None and need_dx:
+            dx = at.empty(shapes[0], x.dtype)
+        if dw is None and need_dw:
+            dw = at.empty(shapes[1], x.dtype)
+        if db is None and need_db:
+            db = at.empty(shapes[2], x.dtype)
+        workspace = _workspace(at, workspace, need, "linear_bwd")
+        if shapes[0][0] == 0:  # sums over no rows
+            import torch
+            with torch.cuda.stream(stream):  # None: the current one
+                for t in (dw, db):
+                    if t is not None:
+                        t.zero_()
+            return dx, dw, db, workspace
+        rc = load().psr_linear_bwd(sh, dy.data_ptr(), z.data_ptr() if activation != "none" else None, x.data_ptr(),
+                                   w.data_ptr(), *(None if t is None else t.data_ptr() for t in (dx, dw, db)),
+                                   workspace.data_ptr(), need, int(timeout_ms), at.handle)
+    if rc != OK:
+        raise PsrError(rc, "psr_linear_bwd")
+    return dx, dw, db, workspace
+
+
+def _linear_bwd_plan(dy, x, w, z, activation, dx, dw, db):
     sh, M, N, K = _linear_shape(x, w, activation, "linear_bwd")
     dev, dtype = x.device, x.dtype
     _check_like(dy, "dy", (M, N), dtype, dev)
@@ -785,37 +875,14 @@ def linear_bwd(dy, x, w, z=None, *, activation="none", need_dx=True, need_dw=Tru
             raise ValueError(f"linear_bwd: activation {activation!r} needs the forward's z")
         _check_like(z, "z", (M, N), dtype, dev)
         sh.ldz = _row_stride(z, "z")
-    wanted = ((need_dx, dx, "dx", (M, K)), (need_dw, dw, "dw", (N, K)), (need_db, db, "db", (N,)))
-    for _, t, name, shape in wanted:
+    shapes = (M, K), (N, K), (N,)
+    for t, name, shape in zip((dx, dw, db), ("dx", "dw", "db"), shapes):
         if t is not None:
             _check_flat(t, name, shape, dtype, dev)
-            for u in (dy, x, w, z):
-                if u is not None:
-                    _check_apart(t, u, "linear_bwd", False)
-    for a, b in ((dx, dw), (dx, db), (dw, db)):
-        if a is not None and b is not None:
-            _check_apart(a, b, "linear_bwd", False, "the outputs overlap")
-    lib = load()
-    with _Launch(dev, stream, "linear_bwd") as at:
-        outs = [at.empty(shape, dtype) if t is None and need else t for need, t, _, shape in wanted]
-        dx, dw, db = outs
-        need = lib.psr_linear_workspace_bytes(sh, 1)
-        if need == 0:
-            raise PsrError(ERR_ARG, "psr_linear_bwd")
-        workspace = _workspace(at, workspace, need, "linear_bwd")
-        if M == 0:  # sums over no rows
-            import torch
-            with torch.cuda.stream(stream):  # None: the current one
-                for t in (dw, db):
-                    if t is not None:
-                        t.zero_()
-            return dx, dw, db, workspace
-        rc = lib.psr_linear_bwd(sh, dy.data_ptr(), z.data_ptr() if activation != "none" else None, x.data_ptr(),
-                                w.data_ptr(), *(None if t is None else t.data_ptr() for t in outs),
-                                workspace.data_ptr(), need, int(timeout_ms), at.handle)
-    if rc != OK:
-        raise PsrError(rc, "psr_linear_bwd")
-    return dx, dw, db, workspace
+    need = load().psr_linear_workspace_bytes(sh, 1)
+    if need == 0:
+        raise PsrError(ERR_ARG, "psr_linear_bwd")
+    return sh, need, dev, shapes
 
 
 def kv4_cache(n_pages, Hkv, d, page, device="cuda"):
@@ -851,6 +918,19 @@ def kv4_append(k, v, cache, table, start, *, page, count=None, stream=None):
 
     table: int32 [B, max_pages]; start, count: int32 [B].  Rows whose position is outside the table or whose page is
     outside the cache are left out.  The places written must differ.  Returns the cache."""
+    sh, ks, vs, dev = _plan(lambda: (kv4_append, _meta(k), _meta(v), _meta(cache), _meta(table), _meta(start), _meta(count), int(page)),
+                            lambda: _kv4_append_plan(k, v, cache, table, start, count, page))
+    if sh.B == 0 or sh.S == 0:
+        return cache
+    with _Launch(dev, stream, "kv4_append") as at:
+        rc = load().psr_kv4_append(sh, k.data_ptr(), ks, v.data_ptr(), vs, cache.data_ptr(), table.data_ptr(),
+                                   start.data_ptr(), None if count is None else count.data_ptr(), at.handle)
+    if rc != OK:
+        raise PsrError(rc, "psr_kv4_append")
+    return cache
+
+
+def _kv4_append_plan(k, v, cache, table, start, count, page):
     _check_cuda(k, "k", 4)
     B, Hkv, S, d = k.shape
     dev = k.device
@@ -858,32 +938,21 @@ def kv4_append(k, v, cache, table, start, *, page, count=None, stream=None):
     _check_like(v, "v", k.shape, k.dtype, dev)
     sh = _kv4_shape(cache, table, B, Hkv, Hkv, S, d, page, code, None, dev)
     _check_counts(B, dev, start=start, count=count)
-    if B == 0 or S == 0:
-        return cache
-    with _Launch(dev, stream, "kv4_append") as at:
-        rc = load().psr_kv4_append(sh, k.data_ptr(), _heads_strides(k, "k"), v.data_ptr(), _heads_strides(v, "v"),
-                                   cache.data_ptr(), table.data_ptr(), start.data_ptr(),
-                                   None if count is None else count.data_ptr(), at.handle)
-    if rc != OK:
-        raise PsrError(rc, "psr_kv4_append")
-    return cache
+    return sh, _heads_strides(k, "k"), _heads_strides(v, "v"), dev
 
 
 def kv4_read(cache, table, start, *, S, Hkv, d, page, count=None, dtype=None, k=None, v=None, stream=None):
     """Positions start[b] .. start[b] + S - 1 of each sequence, read back as k, v [B, Hkv, S, d] (bf16 unless `dtype`
     says float16): zeros from row count[b] on, NaN where the table or the cache has no such place."""
-    import torch
-    _check_cuda(table, "table", 2)
-    B, dev = table.shape[0], table.device
-    dtype = dtype if dtype is not None else (k.dtype if k is not None else torch.bfloat16)
-    shape = (B, int(Hkv), int(S), int(d))
-    sh = _kv4_shape(cache, table, B, int(Hkv), Hkv, int(S), int(d), page,
-                    _type_code(dtype, "dtype", F16), None, dev)
-    _check_counts(B, dev, start=start, count=count)
-    for t, name in ((k, "k"), (v, "v")):
+    sh, shape, dtype, dev = _plan(
+        lambda: (kv4_read, _meta(cache), _meta(table), _meta(start), _meta(count), int(S), int(Hkv), int(d), int(page), dtype,
+                 _meta(k), _meta(v)),
+        lambda: _kv4_read_plan(cache, table, start, count, S, Hkv, d, page, dtype, k, v))
+    for t in (k, v):
         if t is not None:
-            _check_flat(t, name, shape, dtype, dev)
             _check_apart(t, cache, "kv4_read", False)
+    if k is not None and v is not None:
+        _check_apart(k, v, "kv4_read", False, "the outputs overlap")
     with _Launch(dev, stream, "kv4_read") as at:
         k = at.empty(shape, dtype) if k is None else k
         v = at.empty(shape, dtype) if v is None else v
@@ -894,6 +963,20 @@ def kv4_read(cache, table, start, *, S, Hkv, d, page, count=None, dtype=None, k=
     if rc != OK:
         raise PsrError(rc, "psr_kv4_read")
     return k, v
+
+
+def _kv4_read_plan(cache, table, start, count, S, Hkv, d, page, dtype, k, v):
+    import torch
+    _check_cuda(table, "table", 2)
+    B, dev = table.shape[0], table.device
+    dtype = dtype if dtype is not None else (k.dtype if k is not None else torch.bfloat16)
+    shape = (B, int(Hkv), int(S), int(d))
+    sh = _kv4_shape(cache, table, B, int(Hkv), Hkv, int(S), int(d), page, _type_code(dtype, "dtype", F16), None, dev)
+    _check_counts(B, dev, start=start, count=count)
+    for t, name in ((k, "k"), (v, "v")):
+        if t is not None:
+            _check_flat(t, name, shape, dtype, dev)
+    return sh, shape, dtype, dev
 
 
 def kv4_attn_workspace_bytes(B, Hq, Hkv, S, d, *, page, n_pages, max_pages) -> int:
@@ -912,37 +995,47 @@ def kv4_attn(q, cache, table, lens, *, Hkv, page, scale=None, out=None, lse=None
     [B], the positions cached, the S new ones included.  Query i of sequence b sees positions 0 .. lens[b] - S + i.
     Returns (o [B, Hq, S, d], lse [B, Hq, S] fp32, workspace): o = 0 and lse = -inf for a query that sees nothing, NaN
     for a sequence whose length or pages are out of range."""
+    sh, qs, os_, need, dev = _plan(
+        lambda: (kv4_attn, _meta(q), _meta(cache), _meta(table), _meta(lens), int(Hkv), int(page),
+                 None if scale is None else float(scale), _meta(out), _meta(lse)),
+        lambda: _kv4_attn_plan(q, cache, table, lens, Hkv, page, scale, out, lse))
+    if out is not None:
+        _check_apart(out, q, "kv4_attn", False)
+        _check_apart(out, cache, "kv4_attn", False)
+        if lse is not None:
+            _check_apart(lse, out, "kv4_attn", False, "the outputs overlap")
+    with _Launch(dev, stream, "kv4_attn") as at:
+        if out is None:
+            out = at.empty(q.shape, q.dtype)
+        if lse is None:
+            lse = at.empty(q.shape[:3], at.torch.float32)
+        workspace = _workspace(at, workspace, need, "kv4_attn")
+        if sh.B == 0 or sh.S == 0:
+            return out, lse, workspace
+        rc = load().psr_kv4_attn(sh, q.data_ptr(), qs, cache.data_ptr(), table.data_ptr(), lens.data_ptr(), out.data_ptr(), os_,
+                                 lse.data_ptr(), workspace.data_ptr(), need, at.handle)
+    if rc != OK:
+        raise PsrError(rc, "psr_kv4_attn")
+    return out, lse, workspace
+
+
+def _kv4_attn_plan(q, cache, table, lens, Hkv, page, scale, out, lse):
     import torch
     _check_cuda(q, "q", 4)
     B, Hq, S, d = q.shape
     dev = q.device
     sh = _kv4_shape(cache, table, B, Hq, Hkv, S, d, page, _type_of(q, "q", F16), scale, dev)
     _check_counts(B, dev, lens=lens)
-    qs, os_ = _heads_strides(q, "q"), None
+    qs, os_ = _heads_strides(q, "q"), Strides(Hq * S * d, S * d, d)
     if out is not None:
         _check_like(out, "out", (B, Hq, S, d), q.dtype, dev)
-        _check_apart(out, q, "kv4_attn", False)
-        _check_apart(out, cache, "kv4_attn", False)
         os_ = _heads_strides(out, "out", True)
     if lse is not None:
         _check_flat(lse, "lse", (B, Hq, S), torch.float32, dev)
-    lib = load()
-    with _Launch(dev, stream, "kv4_attn") as at:
-        if out is None:
-            out, os_ = at.empty((B, Hq, S, d), q.dtype), Strides(Hq * S * d, S * d, d)
-        if lse is None:
-            lse = at.empty((B, Hq, S), torch.float32)
-        need = lib.psr_kv4_attn_workspace_bytes(sh)
-        if need == 0:
-            raise PsrError(ERR_UNSUPPORTED, "psr_kv4_attn")
-        workspace = _workspace(at, workspace, need, "kv4_attn")
-        if B == 0 or S == 0:
-            return out, lse, workspace
-        rc = lib.psr_kv4_attn(sh, q.data_ptr(), qs, cache.data_ptr(), table.data_ptr(), lens.data_ptr(), out.data_ptr(),
-                              os_, lse.data_ptr(), workspace.data_ptr(), need, at.handle)
-    if rc != OK:
-        raise PsrError(rc, "psr_kv4_attn")
-    return out, lse, workspace
+    need = load().psr_kv4_attn_workspace_bytes(sh)
+    if need == 0:
+        raise PsrError(ERR_UNSUPPORTED, "psr_kv4_attn")
+    return sh, qs, os_, need, dev
 
 
 def get_stats(workspace, stream=None) -> dict:

@@ -125,3 +125,38 @@ def test_serving_layer(psr):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_calls_with_the_same_shapes(psr):
+    # what a call finds out about its arguments serves the next one: other values, strides, types and places count
+    need_gpu()
+    g = torch.Generator().manual_seed(3)
+    B, Hq, Hkv, d, page, n = 2, 4, 2, 64, 16, 40
+    cache = psr.kv4_cache(6, Hkv, d, page)
+    table = torch.arange(6, dtype=torch.int32, device="cuda").view(B, 3)
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    psr.kv4_append(randn(g, (B, Hkv, n, d), "bf16"), randn(g, (B, Hkv, n, d), "bf16"), cache, table, lens * 0, page=page)
+    q = randn(g, (B, Hq, 1, d), "bf16")
+    scale = torch.tensor(0.125)
+    for s in (0.125, 0.5, 0.125):
+        scale.fill_(s)  # a number, whatever holds it
+        got = psr.kv4_attn(q, cache, table, lens, Hkv=Hkv, page=page, scale=scale)[0]
+        ro, _, to, _ = ol.kv4_attention(f64(q), cache.cpu().numpy(), table.cpu().numpy(), [n] * B, page, Hkv, s)
+        assert (np.abs(f64(got) - ro) <= to + 2.0**-8 * np.abs(ro) * 1.01).all(), s
+    rot = psr.rotary_table(d)
+    x = randn(g, (1, 2, 8, d), "f32")
+    for off in (0, 5, 1 << 40, 0):
+        y = psr.rotary(x, None, rot, offset=off)[0]
+        assert torch.equal(y, psr.rotary(x, None, rot, positions=torch.arange(8, device="cuda") + off)[0]), off
+    for t in ("bf16", "f16", "bf16"):
+        for shift in (0, 1, 0):
+            a, w = randn(g, (3 * 64 + 1,), t)[shift:shift + 192].view(3, 64), randn(g, (40, 64), t, 0.125)
+            ref, _ = ol.linear(f64(a), f64(w))
+            y = psr.linear(a, w)[0]
+            assert y.dtype == a.dtype and rel(f64(y), ref) <= 2.0**-8
+            y2 = psr.linear(a[:, :32], w[:, 32:])[0]
+            assert rel(f64(y2), ol.linear(f64(a[:, :32]), f64(w[:, 32:]))[0]) <= 2.0**-8
+    with pytest.raises(ValueError, match="w must have shape"):
+        psr.linear(a, w[:, :32])
+    with pytest.raises(ValueError, match="w must be torch.bfloat16"):
+        psr.linear(a, w.half())
