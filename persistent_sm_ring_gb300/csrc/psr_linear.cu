@@ -271,9 +271,8 @@ static int product(const Operands& o, Epilogue e, Launch& l) {
     if (o.K % 8 == 0 && (o.M == 1 || (o.M <= 16 && 2ll * o.M * o.N * o.K <= kGemvBytes))) return launch_gemv<T>(o, e, l);
   if constexpr (!AMN)
     if (streams(o.M)) return launch_stream<BMN>(o, e, l);
-  const int splits = pair_splits(o.M, o.N, o.K);
+  const Split split = split_of(o.M, o.N, o.K);
   constexpr bool kHalfType = std::is_same<T, __half>::value;
-  if (splits > 1) return launch_pair<AMN, BMN, kHalfType>(o, e, false, splits, l);
   // Tiles of 256 columns take 8.6 clocks for each K and tile (a little more with an operand that is MN-major), or as long as
   // the epilogue, which runs beside the next tile's products, if that is longer.  Tiles of 512 columns take 16 and move less, but
   // their epilogue has the accumulators to itself: nothing runs beside it.  Rows that do not start on 128-byte boundaries
@@ -284,10 +283,12 @@ static int product(const Operands& o, Epilogue e, Launch& l) {
   const bool ragged = o.lda % 64 || o.ldb % 64;
   const double k1 = ragged ? 12.8 : 8.6 + 0.3 * (AMN + BMN), k2 = ragged ? 18.4 : 16.0;
   const long long ones = rows * ((o.N + 255) / 256), tiles = rows * ((o.N + 511) / 512), halves = last_halves(tiles, (int)n_pairs);
-  const double one = (double)((ones + n_pairs - 1) / n_pairs) * std::max(k1 * o.K, 7000.0 + more);
+  const double round = std::max(k1 * o.K, 7000.0 + more);  // of 256-column tiles
+  const double one = split.rest ? split.whole / n_pairs * round + k1 * o.K / split.parts + split.clocks + more / 2
+                                : (double)((ones + n_pairs - 1) / n_pairs) * round;
   const double two = (double)(tiles / n_pairs + (halves || tiles % n_pairs == 0 ? 0 : 1)) * (k2 * o.K + 2 * (4800.0 + more)) +
                      (halves ? k1 * o.K + 4800.0 + more : 0.0);
-  return launch_pair<AMN, BMN, kHalfType>(o, e, two <= one, 1, l);
+  return launch_pair<AMN, BMN, kHalfType>(o, e, two <= one, split, l);
 }
 
 template <class T>

@@ -223,10 +223,10 @@ struct PairParams {
   int wide;               // tiles of 512 columns, else 256
   int tiles_m, tiles_n;   // tile rows of 256, tile columns
   int group;              // tile rows of a raster group
-  int splits, split_k;    // of 256-column tiles: parts of the K steps, K steps of a part
+  int whole;              // of 256-column tiles: those computed whole, in whole rounds; the others are split
+  int splits, split_k;    // parts of a split tile's K steps, K steps of a part
   int halves;             // of 512-column tiles: those of the last round that are computed as two halves (pair_item)
-  float* partial;         // splits > 1: fp32 sums [splits][M][ldp]
-  long long ldp;
+  float* partial;         // splits > 1: fp32 sums [split tile][part][256][256]
   uint32_t idesc;
   Epilogue e;
   Ctrl* ctrl;
@@ -240,7 +240,8 @@ struct PairSmem {
   volatile uint32_t abort;
 };
 
-// What a pair computes next: `n` 256-column halves from column half tn on of tile row tm, K steps k0 .. k0 + n_k.
+// What a pair computes next: `n` 256-column halves from column half tn on of tile row tm, K steps k0 .. k0 + n_k.  split: the part
+// (of all split tiles') whose sums go to the partials, or -1.
 struct PairItem {
   int tm, tn, n, k0, n_k, split;
 };
@@ -259,17 +260,24 @@ __device__ __forceinline__ void pair_tile(const PairParams& p, int t, int& tm, i
 // a half, not four).  Rounds shifted by half a tile between pairs, so that some write while others multiply, were
 // slower: the tile loads leave L2 no room for the outputs (4096^3 with gelu 100 to 118 us).
 __device__ __forceinline__ bool pair_item(const PairParams& p, int pair, int n_pairs, int i, PairItem& it) {
-  const long long n = (long long)p.tiles_m * p.tiles_n * p.splits, at = pair + (long long)i * n_pairs;
+  const long long n = (long long)p.tiles_m * p.tiles_n, at = pair + (long long)i * n_pairs;
   it.k0 = 0;
   it.n_k = p.n_k;
-  it.split = 0;
+  it.split = -1;
   if (!p.wide) {
-    if (at >= n) return false;
-    it.split = (int)(at % p.splits);
-    it.k0 = it.split * p.split_k;
-    it.n_k = min(p.split_k, p.n_k - it.k0);
     it.n = 1;
-    pair_tile(p, (int)(at / p.splits), it.tm, it.tn);
+    int tile = (int)at;
+    if (at >= p.whole) {
+      const long long part = at - p.whole;
+      if (part >= (n - p.whole) * p.splits) return false;
+      tile = p.whole + (int)(part / p.splits);
+      if (p.splits > 1) {
+        it.split = (int)part;
+        it.k0 = (int)(part % p.splits) * p.split_k;
+        it.n_k = min(p.split_k, p.n_k - it.k0);
+      }
+    }
+    pair_tile(p, tile, it.tm, it.tn);
     return true;
   }
   const long long whole = n - p.halves;  // tiles in whole rounds
@@ -424,13 +432,12 @@ __device__ __forceinline__ void pair_store(const Epilogue& e, int M, int N, uint
   out(e.y, e.ldy);
 }
 
-// The block's fp32 sums into the split's partials.
-__device__ __forceinline__ void partial_store(const PairParams& p, int split, uint8_t* stage, int i0, int j0,
+// The first `rows` rows of the block's fp32 sums into the part's partials, at (row, col) of the tile.
+__device__ __forceinline__ void partial_store(const PairParams& p, int split, uint8_t* stage, int row, int col, int rows,
                                               const uint32_t (&v)[32]) {
   const int lane = threadIdx.x % 32;
-  const int rows = min(32, p.M - i0);
   if (rows <= 0) return;
-  float* g = p.partial + ((long long)split * p.M + i0) * p.ldp + j0;
+  float* g = p.partial + ((long long)split * 256 + row) * 256 + col;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -438,7 +445,7 @@ __device__ __forceinline__ void partial_store(const PairParams& p, int split, ui
       const uint32_t* w = v + h * 16 + j * 4;
       *stage_chunk(stage, lane, j) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    rows_out(stage, reinterpret_cast<uint8_t*>(g + h * 16), p.ldp * 4, rows, 4);
+    rows_out(stage, reinterpret_cast<uint8_t*>(g + h * 16), 1024, rows, 4);
   }
 }
 
@@ -563,7 +570,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint8_t* stage = epi + (warp - 4) * kEpiWarpBytes;
     const int quarter = warp % 4, cgroup = (warp - 4) / 4;  // lanes 32 quarter .., columns 64 cgroup .. of a half
     const Epilogue& e = p.e;
-    const bool res = e.res && e.vec && p.splits == 1;
+    const bool res = e.res && e.vec;
     uint32_t u = 0;
     bool ok = true;
     for (int i = 0; ok && pair_item(p, pair, n_pairs, i, it); ++i) {
@@ -573,7 +580,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const uint32_t slot = u % 2;
         const int j0 = it.tn * 256 + (b / 2) * 256 + cgroup * 64 + (b % 2) * 32;
         uint4 rr[4];
-        if (res)  // in flight while the sums are waited for
+        if (res && it.split < 0)  // in flight while the sums are waited for
           rows_in(rr, static_cast<const uint8_t*>(e.res) + ((long long)i0 * e.ldr + j0) * 2, e.ldr * 2, p.M - i0, (p.N - j0) / 8);
         if (b % 2 == 0) {
           ok = __all_sync(0xffffffffu, wait_own(&sc.acc_full[slot], (u / 2) & 1u, p, &sc, SITE_ACC));
@@ -592,7 +599,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
           ++u;
         }
-        if (p.splits > 1) partial_store(p, it.split, stage, i0, j0, v);
+        if (it.split >= 0)
+          partial_store(p, it.split, stage, (int)rank * kRows + quarter * 32, cgroup * 64 + (b % 2) * 32, p.M - i0, v);
         else pair_store<!BMN, HALF>(e, p.M, p.N, stage, i0, j0, v, rr);
       }
     }
@@ -862,18 +870,20 @@ __global__ void __launch_bounds__(128) stream_join(const __grid_constant__ Strea
   if (j < p.N) finish(p.e, i, j, sum);
 }
 
-// Joins the splits' partials in order: four columns to a thread.
+// Joins the parts of the split tiles in order: four columns to a thread, 64 blocks to a tile.
 __global__ void __launch_bounds__(256) pair_join(const __grid_constant__ PairParams p) {
-  const long long per = p.ldp / 4, n = per * p.M;
-  const long long t = blockIdx.x * 256ll + threadIdx.x;
-  const long long i = t / per;
-  const int j = (int)(t - i * per) * 4;
+  const int at = blockIdx.x * 256 + threadIdx.x, row = at / 64, col = at % 64 * 4;
+  int tm, tn;
+  pair_tile(p, p.whole + blockIdx.y, tm, tn);
+  const long long i = tm * 256ll + row;
+  const int j = tn * 256 + col;
   wait_previous();
-  if (t >= n || j >= p.N) return;
+  if (i >= p.M || j >= p.N) return;
+  const float* part = p.partial + (long long)blockIdx.y * p.splits * 65536 + row * 256 + col;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int s = 0; s < p.splits; ++s) {
-    const float4 v = *reinterpret_cast<const float4*>(p.partial + ((long long)s * p.M + i) * p.ldp + j);
+    const float4 v = *reinterpret_cast<const float4*>(part + s * 65536ll);
     sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
   }
   const Epilogue& e = p.e;
@@ -908,7 +918,7 @@ __global__ void __launch_bounds__(256) pair_join(const __grid_constant__ PairPar
 // ================================================================================================
 constexpr int kStreamCtas = 152;  // most CTAs of stream_gemm (one per SM); bounds the partials
 constexpr int kStreamMaxM = 64;   // stream_gemm takes up to this many rows
-constexpr int kPairs = 76;        // pairs of CTAs that a product is split for
+constexpr int kPairs = 76;        // pairs of CTAs that tiles are split for
 
 // A 16-bit matrix of `outer` rows of `inner` elements, boxes of 64 x box_outer, 128-byte swizzle.  The element type
 // only names the width: the copies do no arithmetic and the fill is zero.
@@ -988,8 +998,30 @@ inline int last_halves(long long tiles, int pairs) {
   return 2 * rest <= pairs ? (int)rest : 0;
 }
 
+// 256-column tiles that are computed whole, and parts of each of the others along K.
+struct Split {
+  long long whole, rest;
+  int parts;
+  double clocks;  // that the parts' way through memory and the join take
+};
+
+// The tiles that would leave pairs without one in the last round are split along K, into as many parts as still fit at once, of at
+// least 8 K steps, where that saves more clocks than it costs: 8.6 for each K that a pair is spared against 5500 and 180 for
+// each part (256 KiB written and read), as measured (768 x 8192 x 4096, 96 tiles: 45 to 40 us; 2048 x 2560 x 4096, 80 tiles: 44 to 36;
+// 2600 x 2304 x 2600, 99 tiles, would go from 34 to 38).
+inline Split split_of(int M, int N, int K) {
+  const long long tiles = ((M + 255ll) / 256) * ((N + 255ll) / 256), rest = tiles % kPairs;
+  if (rest == 0) return {tiles, 0, 1, 0.0};
+  long long parts = kPairs / rest;
+  const long long most = ((K + kBK - 1) / kBK) / 8;
+  if (parts > most) parts = most;
+  const double clocks = 5500.0 + 180.0 * rest * parts * (M < 256 ? M : 256) / 256.0;
+  if (parts < 2 || 8.6 * K * (1.0 - 1.0 / parts) < clocks) return {tiles, 0, 1, 0.0};
+  return {tiles - rest, rest, (int)parts, clocks};
+}
+
 template <bool AMN, bool BMN, bool HALF>
-inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, int splits, Launch& l) {
+inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, const Split& split, Launch& l) {
   const int n_pairs = pairs_of<AMN, BMN, HALF>(l.dev, l.n_sm), cols = wide ? 512 : 256;
   if (n_pairs < 1) return PSR_ERR_CUDA;
   PairParams p = {};
@@ -999,13 +1031,19 @@ inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, int spli
   p.tiles_m = (o.M + 255) / 256;
   p.wide = wide;
   p.tiles_n = (o.N + cols - 1) / cols;
-  if ((long long)p.tiles_m * p.tiles_n * splits >= (1ll << 31)) return PSR_ERR_UNSUPPORTED;
+  long long items = (long long)p.tiles_m * p.tiles_n;
+  if (items >= (1ll << 30)) return PSR_ERR_UNSUPPORTED;
   p.group = 16;  // (8192 x 28672 x 4096 in 967 us; 8, 12, 24, 32 rows: 987, 976, 984, 1010)
-  p.split_k = (p.n_k + splits - 1) / splits;
-  p.splits = (p.n_k + p.split_k - 1) / p.split_k;  // none of them empty
-  p.partial = l.partial;
-  p.ldp = (long long)cols * p.tiles_n;
-  if (p.splits > 1 && (size_t)p.splits * o.M * p.ldp * 4 > l.partial_bytes) return PSR_ERR_ARG;
+  p.whole = (int)items;
+  p.splits = 1;
+  if (!wide && split.rest > 0) {
+    p.whole = (int)split.whole;
+    p.split_k = (p.n_k + split.parts - 1) / split.parts;
+    p.splits = (p.n_k + p.split_k - 1) / p.split_k;  // none of them empty
+    p.partial = l.partial;
+    if ((size_t)split.rest * p.splits * 65536 * 4 > l.partial_bytes) return PSR_ERR_ARG;
+    items = split.whole + split.rest * p.splits;
+  }
   p.idesc = idesc16(256, 256, AMN, BMN, HALF);
   p.e = e;
   p.ctrl = l.ctrl;
@@ -1015,7 +1053,6 @@ inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, int spli
   const bool ok_a = AMN ? tmap16(&ma, o.a, o.M, o.K, o.lda, 64) : tmap16(&ma, o.a, o.K, o.M, o.lda, kRows);
   const bool ok_b = BMN ? tmap16(&mb, o.b, o.N, o.K, o.ldb, 64) : tmap16(&mb, o.b, o.K, o.N, o.ldb, kRows);
   if (!ok_a || !ok_b) return PSR_ERR_CUDA;
-  long long items = (long long)p.tiles_m * p.tiles_n * p.splits;
   if (wide) {
     p.halves = last_halves(items, n_pairs);
     items += p.halves;
@@ -1038,27 +1075,17 @@ inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, int spli
   }
   l.clear = nullptr;
   if (p.splits == 1) return PSR_OK;
-  return launch_after(pair_join, dim3((unsigned)((p.ldp / 4 * o.M + 255) / 256)), 256, p, l.st);
+  return launch_after(pair_join, dim3(64, (unsigned)split.rest), 256, p, l.st);
 }
 
 // Whether stream_gemm takes a product with M rows of A.
 inline bool streams(int M) { return M <= kStreamMaxM; }
 
-// Parts that a product of few tiles is split into along K so that every pair of CTAs has one: as many as still fit at
-// once, of at least 8 K steps (a part's sums go through memory: 256 KiB written and read for each 256 x 256 tile).
-inline int pair_splits(int M, int N, int K) {
-  const long long tiles = ((M + 255ll) / 256) * ((N + 255ll) / 256);
-  long long s = kPairs / tiles;
-  const long long most = ((K + kBK - 1) / kBK) / 8;
-  if (s > most) s = most;
-  return s < 1 ? 1 : (int)s;
-}
-
 // Bytes of fp32 partials that a product with C [M][N] may leave (weights: A's rows are not tokens, so it never streams).
 inline size_t partial_bytes(int M, int N, int K, bool weights) {
   if (!weights && streams(M)) return (size_t)2 * kStreamCtas * ((M + 15) / 16 * 16) * kRows * 4;
-  const int s = pair_splits(M, N, K);
-  return s > 1 ? (size_t)s * M * ((N + 255) / 256 * 256) * 4 : 0;
+  const Split s = split_of(M, N, K);
+  return (size_t)s.rest * s.parts * 65536 * 4;
 }
 
 // o.a: the tokens [M][K], o.b: W, K-major [N][K] or (WMN) [K][N].

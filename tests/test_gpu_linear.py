@@ -330,3 +330,18 @@ def test_linear_of_two_streams_at_once(psr):
         assert all(psr.get_stats(x[-1])["status"] == 0 for x in got + grads)
         assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
         assert all(torch.equal(a, b) for x, y in zip(grads, back) for a, b in zip(x, y))
+
+
+# whole rounds of tiles with a last one that is split along K, in two to ten parts, and calls of split tiles only
+@pytest.mark.parametrize("M,N,K", [(768, 8192, 2200), (2600, 2304, 2600), (70, 130, 4100), (300, 260, 9000), (520, 1030, 3000),
+                                   (257, 20000, 1300)])
+def test_linear_split_last_round(psr, M, N, K):
+    need_gpu()
+    g = torch.Generator().manual_seed(M)
+    x, w, b, r = randn(g, (M, K), "bf16"), randn(g, (N, K), "bf16", K**-0.5), randn(g, (N,), "bf16"), randn(g, (M, N), "bf16")
+    y, z, ws = psr.linear(x, w, b, r, activation="relu", save_z=True)
+    assert psr.get_stats(ws)["status"] == 0
+    check_forward(y, z, x, w, b, r, "relu", "bf16", str((M, N, K)))
+    got = psr.linear_bwd(r, x, w, need_db=False)
+    assert psr.get_stats(got[3])["status"] == 0
+    check_backward(got[:3], r, x, w, None, "none", "bf16", str((M, N, K)) + " bwd")
