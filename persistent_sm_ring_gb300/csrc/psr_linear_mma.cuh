@@ -216,6 +216,16 @@ __device__ __forceinline__ void load_one(uint32_t dst, const CUtensorMap* m, int
       : "memory");
 }
 
+// An arrival at the pair's other CTA, and a meeting of the two, that order no memory: a release would wait until the thread's
+// stores to global memory have been performed, a microsecond.  (What they order are reads of tensor memory, which have
+// completed, and the CTAs' ends.)
+__device__ __forceinline__ void arrive_far(uint32_t cl_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
+}
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
+}
+
 // ================================================================================================
 // pair_gemm
 // ================================================================================================
@@ -608,7 +618,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           __syncwarp();
           if (lane == 0) {
             if (rank == 0) mbar_arrive(&sc.acc_empty[slot]);
-            else mbar_arrive_cluster(mapa_shared(smem_u32(&sc.acc_empty[slot]), 0));
+            else arrive_far(mapa_shared(smem_u32(&sc.acc_empty[slot]), 0));
           }
           ++u;
         }
@@ -632,7 +642,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // neither CTA leaves while the other may still signal it
+  cluster_meet();  // neither CTA leaves while the other may still signal it
   tc_fence_after();
   if (warp == 1) tmem_dealloc_cg<2>(sc.tmem_base, 512);
 }
