@@ -39,9 +39,10 @@ __global__ void __launch_bounds__(256)
 // the next piece as it takes one, so that kAhead of them stay in flight; x comes from L1.  Against the tensor core kernels
 // this has no tensor memory, barriers or partials to set up: 8192 x 8192 in 22.7 us (5.9 TB/s), where the streaming kernel takes
 // 29; with groups of eight loads that are all used before the next are asked for 26.6, and 1024 x 8192 10.1 instead of 6.0.
-// A few rows (a block row each) read W again from L2: as fast as the streaming kernel's 7 us for 256 x 512 up to kGemvBytes
-// of W in all.
-constexpr long long kGemvBytes = 32 << 20;
+// A few rows (a block row each) read W again from L2.  That is faster while the dot products fit on the SMs at once, up to
+// kGemvDots of them and kGemvBytes of W in all (dot products / streaming: 8 x 1024 x 1024 5.2 / 5.5 us, 16 x 256 x 512 2.9 /
+// 4.8; beyond, 16 x 1024 x 64 6.3 / 4.7 and 8 x 1024 x 4096 8.9 / 6.7).
+constexpr long long kGemvDots = 8192, kGemvBytes = 32 << 20;
 
 template <class T>
 __global__ void __launch_bounds__(256)
@@ -268,7 +269,8 @@ static int product(const Operands& o, Epilogue e, Launch& l) {
   auto flat = [&](const void* p, long long ld) { return !p || (aligned_to(p, 16) && (o.M == 1 || ld % 8 == 0)); };
   e.vec = o.N % 8 == 0 && flat(e.y, e.ldy) && flat(e.z, e.ldz) && flat(e.res, e.ldr) && flat(e.bias, 0);
   if constexpr (!AMN && !BMN)
-    if (o.K % 8 == 0 && (o.M == 1 || (o.M <= 16 && 2ll * o.M * o.N * o.K <= kGemvBytes))) return launch_gemv<T>(o, e, l);
+    if (o.K % 8 == 0 && (o.M == 1 || (o.M <= 16 && (long long)o.M * o.N <= kGemvDots && 2ll * o.M * o.N * o.K <= kGemvBytes)))
+      return launch_gemv<T>(o, e, l);
   if constexpr (!AMN)
     if (streams(o.M)) return launch_stream<BMN>(o, e, l);
   const Split split = split_of(o.M, o.N, o.K);
