@@ -272,7 +272,7 @@ static int product(const Operands& o, Epilogue e, Launch& l) {
     if (o.K % 8 == 0 && (o.M == 1 || (o.M <= 16 && (long long)o.M * o.N <= kGemvDots && 2ll * o.M * o.N * o.K <= kGemvBytes)))
       return launch_gemv<T>(o, e, l);
   if constexpr (!AMN)
-    if (streams(o.M)) return launch_stream<BMN>(o, e, l);
+    if (streams(o.M, o.N, o.K)) return launch_stream<BMN>(o, e, l);
   const Split split = split_of(o.M, o.N, o.K);
   constexpr bool kHalfType = std::is_same<T, __half>::value;
   // Tiles of 256 columns take 8.6 clocks for each K and tile (a little more with an operand that is MN-major), or as long as

@@ -943,7 +943,6 @@ __global__ void __launch_bounds__(256) pair_join(const __grid_constant__ PairPar
 // Host side
 // ================================================================================================
 constexpr int kStreamCtas = 152;  // most CTAs of stream_gemm (one per SM); bounds the partials
-constexpr int kStreamMaxM = 64;   // stream_gemm takes up to this many rows
 constexpr int kPairs = 76;        // pairs of CTAs that tiles are split for
 
 // A 16-bit matrix of `outer` rows of `inner` elements, boxes of 64 x box_outer, 128-byte swizzle.  The element type
@@ -1104,12 +1103,15 @@ inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, const Sp
   return launch_after(pair_join, dim3(64, (unsigned)split.rest), 256, p, l.st);
 }
 
-// Whether stream_gemm takes a product with M rows of A.
-inline bool streams(int M) { return M <= kStreamMaxM; }
+// Whether stream_gemm takes a product with M rows of A: up to 64, and up to 128 where neither a single step, which leaves the whole
+// epilogue to one CTA, nor many columns, whose tokens' epilogue adds up, make the tiles of 256 rows faster (streaming / tiles: 128 x
+// 1024 x 1024 8.0 / 12.0 us, 128 x 4096 x 4096 17.7 / 18.5, 72 x 4096 x 8192 19.1 / 22.9; 128 x 1024 x 64 14.9 / 8.1, 128 x 8192 x
+// 1024 15.5 / 13.8, 128 x 28672 x 4096 81 / 54).
+inline bool streams(int M, int N, int K) { return M <= 64 || (M <= 128 && K >= 512 && N <= 4096); }
 
 // Bytes of fp32 partials that a product with C [M][N] may leave (weights: A's rows are not tokens, so it never streams).
 inline size_t partial_bytes(int M, int N, int K, bool weights) {
-  if (!weights && streams(M)) return (size_t)2 * kStreamCtas * ((M + 15) / 16 * 16) * kRows * 4;
+  if (!weights && streams(M, N, K)) return (size_t)2 * kStreamCtas * ((M + 15) / 16 * 16) * kRows * 4;
   const Split s = split_of(M, N, K);
   return (size_t)s.rest * s.parts * 65536 * 4;
 }

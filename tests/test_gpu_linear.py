@@ -345,3 +345,16 @@ def test_linear_split_last_round(psr, M, N, K):
     got = psr.linear_bwd(r, x, w, need_db=False)
     assert psr.get_stats(got[3])["status"] == 0
     check_backward(got[:3], r, x, w, None, "none", "bf16", str((M, N, K)) + " bwd")
+
+
+@pytest.mark.parametrize("M,N,K", [(65, 264, 520), (96, 1000, 1032), (127, 4096, 512), (128, 130, 4104), (128, 4104, 520), (112, 64, 2050)])
+def test_linear_up_to_128_rows(psr, M, N, K):
+    need_gpu()
+    g = torch.Generator().manual_seed(M + N)
+    x, w, b, r = randn(g, (M, K), "f16"), randn(g, (N, K), "f16", K**-0.5), randn(g, (N,), "f16"), randn(g, (M, N), "f16")
+    y, z, ws = psr.linear(x, w, b, r, activation="gelu", save_z=True)
+    assert psr.get_stats(ws)["status"] == 0
+    check_forward(y, z, x, w, b, r, "gelu", "f16", str((M, N, K)))
+    got = psr.linear_bwd(r, x, w, z, activation="gelu")
+    assert psr.get_stats(got[3])["status"] == 0
+    check_backward(got[:3], r, x, w, z, "gelu", "f16", str((M, N, K)) + " bwd")
