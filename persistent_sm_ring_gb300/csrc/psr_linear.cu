@@ -275,15 +275,16 @@ static int product(const Operands& o, Epilogue e, Launch& l) {
     if (streams(o.M, o.N, o.K)) return launch_stream<BMN>(o, e, l);
   const Split split = split_of(o.M, o.N, o.K);
   constexpr bool kHalfType = std::is_same<T, __half>::value;
-  // Tiles of 256 columns take 8.6 clocks for each K and tile (a little more with an operand that is MN-major), or as long as
+  // Tiles of 256 columns take 9 clocks for each K and tile (a little more with an operand that is MN-major), or as long as
   // the epilogue, which runs beside the next tile's products, if that is longer.  Tiles of 512 columns take 16 and move less, but
   // their epilogue has the accumulators to itself: nothing runs beside it.  Rows that do not start on 128-byte boundaries
   // take the loads half as long again.  Clocks as measured at 16384 x 4096 x 512 (one / two: 48 / 71 us, with gelu, bias, residual and
-  // z 112 / 132), 4096 x 4096 x 4096 (78 / 87, 87 / 107), dx of 8192 x 8192 x 8192 (617 / 598) and 1531 x 5000 x 1736 (31 / 28).
+  // z 112 / 132), 4096 x 4096 x 4096 (78 / 87, 87 / 107), 1531 x 5000 x 1736 (31 / 28) and, under lasting load, where
+  // the power limit counts what is moved, 8192 x 8192 x 8192 (668 / 639, its dx 672 / 639) and 4100 x 8192 x 4096 (174 / 181).
   const long long rows = (o.M + 255) / 256, n_pairs = l.n_sm / 2;
   const double more = (e.act > PSR_ACT_RELU ? 3200.0 : 0.0) + (e.z ? 2600.0 : 0.0) + (e.res ? 3200.0 : 0.0) + (e.bias ? 1000.0 : 0.0);
   const bool ragged = o.lda % 64 || o.ldb % 64;
-  const double k1 = ragged ? 12.8 : 8.6 + 0.3 * (AMN + BMN), k2 = ragged ? 18.4 : 16.0;
+  const double k1 = ragged ? 12.8 : 9.0 + 0.3 * (AMN + BMN), k2 = ragged ? 18.4 : 16.0;
   const long long ones = rows * ((o.N + 255) / 256), tiles = rows * ((o.N + 511) / 512), halves = last_halves(tiles, (int)n_pairs);
   const double round = std::max(k1 * o.K, 5500.0 + more);  // of 256-column tiles
   const double one = split.rest ? split.whole / n_pairs * round + k1 * o.K / split.parts + split.clocks + more / 2
