@@ -217,11 +217,11 @@ __device__ __forceinline__ void load_one(uint32_t dst, const CUtensorMap* m, int
       : "memory");
 }
 
-// An arrival at the pair's other CTA, and a meeting of the two, that order no memory: a release would wait until the thread's
-// stores to global memory have been performed, a microsecond.  (What they order are reads of tensor memory, which have
-// completed, and the CTAs' ends.)
+// An arrival at the pair's other CTA, and a meeting of the two, that do not order global memory between them: a release at
+// cluster scope would wait until the thread's stores have been performed, a microsecond.  (What they order are reads of tensor
+// memory, which have completed, and the CTAs' ends: before it leaves, a CTA has itself waited for every signal to its barriers.)
 __device__ __forceinline__ void arrive_far(uint32_t cl_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
 }
 __device__ __forceinline__ void cluster_meet() {
   asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
@@ -550,6 +550,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         ++head;
       }
     }
+    for (; ok && tail < head; ++tail)  // every signal to this CTA's barriers has come before it may leave
+      ok = __all_sync(0xffffffffu, wait_own(&sc.empty[tail % kSteps], (tail / kSteps) & 1u, p, &sc, SITE_EMPTY));
     if (!ok) sc.abort = 1;
   } else if (warp == 1) {
     if (rank == 0) {  // the whole warp, so that addresses and descriptors stay in uniform registers; lane 0 issues
@@ -588,6 +590,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int h = 0; h < it.n; ++h) commit_pair(&sc.acc_full[(u + h) % 2], lane == 0);
         u += it.n;
       }
+      for (uint32_t h = u > 2 ? u - 2 : 0; ok && h < u; ++h)  // the other CTA's last arrivals have come
+        ok = __all_sync(0xffffffffu, wait_own<true>(&sc.acc_empty[h % 2], (h / 2) & 1u, p, &sc, SITE_ACC_EMPTY));
       if (!ok) sc.abort = 1;
     }
   } else if (warp >= 4) {

@@ -358,3 +358,20 @@ def test_linear_up_to_128_rows(psr, M, N, K):
     got = psr.linear_bwd(r, x, w, z, activation="gelu")
     assert psr.get_stats(got[3])["status"] == 0
     check_backward(got[:3], r, x, w, z, "gelu", "f16", str((M, N, K)) + " bwd")
+
+
+@pytest.mark.parametrize("M,N,K", [(4096, 4096, 256), (5000, 2600, 200), (2048, 2560, 4096), (9000, 1100, 64)])
+def test_linear_many_tiles_repeat(psr, M, N, K):
+    # many tiles to a pair: accumulators and barriers go round, and the same call gives the same bits
+    need_gpu()
+    g = torch.Generator().manual_seed(K)
+    x, w, b, r = randn(g, (M, K), "bf16"), randn(g, (N, K), "bf16", K**-0.5), randn(g, (N,), "bf16"), randn(g, (M, N), "bf16")
+    y, z, ws = psr.linear(x, w, b, r, activation="silu", save_z=True)
+    z32 = x.float() @ w.float().t() + b.float()
+    # z is rounded once (2^-8), and either side's sums are off by at most K 2^-23 sum |x| |w|
+    tol = 2.0**-8 * z32.abs() * 1.01 + 2 * K * 2.0**-23 * (x.float().abs() @ w.float().abs().t()) + 1e-6
+    assert ((z.float() - z32).abs() <= tol).all()
+    for _ in range(20):
+        y2, z2, _ = psr.linear(x, w, b, r, activation="silu", save_z=True, workspace=ws)
+        assert torch.equal(y, y2) and torch.equal(z, z2)
+        assert psr.get_stats(ws)["status"] == 0
