@@ -823,6 +823,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < p.M; c += 16) {
         uint32_t v[16];
+        __syncwarp();  // the load is the whole warp's: no lane is still in the last tokens' epilogue
         tmem_ld16(tacc + c, v);
         tmem_ld_wait();
         const int n_c = min(16, p.M - c);
@@ -832,29 +833,30 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             if (e < n_c) part[(c + e) * kRows] = __uint_as_float(v[e]);
           continue;
         }
-        if (j >= p.N) continue;
         // four tokens at a time, their residuals in flight together; each lane reads its own sums back
         float* own = &sc.sums[quarter][0][lane];
 #pragma unroll
         for (int e = 0; e < 16; ++e) own[e * 32] = __uint_as_float(v[e]);
+        if (j < p.N) {
 #pragma unroll 1
-        for (int e = 0; e < n_c; e += 4) {
-          float f[4], r[4];
+          for (int e = 0; e < n_c; e += 4) {
+            float f[4], r[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const long long i = c + e + q;
-            f[q] = own[(e + q) * 32] + bias;
-            r[q] = p.e.res && e + q < n_c ? load16(p.e.res, i * p.e.ldr + j, p.e.half) : 0.f;
-          }
-          float4 y = make_float4(f[0], f[1], f[2], f[3]);
-          if (p.e.act) y = act_call4(p.e.act, y);
-          const float g[4] = {y.x, y.y, y.z, y.w};
+            for (int q = 0; q < 4; ++q) {
+              const long long i = c + e + q;
+              f[q] = own[(e + q) * 32] + bias;
+              r[q] = p.e.res && e + q < n_c ? load16(p.e.res, i * p.e.ldr + j, p.e.half) : 0.f;
+            }
+            float4 y = make_float4(f[0], f[1], f[2], f[3]);
+            if (p.e.act) y = act_call4(p.e.act, y);
+            const float g[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (e + q >= n_c) break;
-            const long long i = c + e + q;
-            if (p.e.z) store16(p.e.z, i * p.e.ldz + j, p.e.half, f[q]);
-            store16(p.e.y, i * p.e.ldy + j, p.e.half, g[q] + r[q]);
+            for (int q = 0; q < 4; ++q) {
+              if (e + q >= n_c) break;
+              const long long i = c + e + q;
+              if (p.e.z) store16(p.e.z, i * p.e.ldz + j, p.e.half, f[q]);
+              store16(p.e.y, i * p.e.ldy + j, p.e.half, g[q] + r[q]);
+            }
           }
         }
       }

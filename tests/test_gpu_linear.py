@@ -375,3 +375,16 @@ def test_linear_many_tiles_repeat(psr, M, N, K):
         y2, z2, _ = psr.linear(x, w, b, r, activation="silu", save_z=True, workspace=ws)
         assert torch.equal(y, y2) and torch.equal(z, z2)
         assert psr.get_stats(ws)["status"] == 0
+
+
+@pytest.mark.parametrize("N,K", [(31, 72), (97, 72), (129, 128), (257, 128), (1000, 72), (9741, 520)])  # tiles that are not split
+@pytest.mark.parametrize("M", [17, 40, 64])
+def test_linear_streamed_last_columns(psr, M, N, K):
+    # more than 16 tokens, and a last group of 32 columns that only some of a warp's lanes have
+    need_gpu()
+    g = torch.Generator().manual_seed(M + N)
+    x, w, b, r = randn(g, (M, K), "bf16"), randn(g, (N, K), "bf16", K**-0.5), randn(g, (N,), "bf16"), randn(g, (M, N), "bf16")
+    for act in ("gelu", "silu"):
+        y, z, ws = psr.linear(x, w, b, r, activation=act, save_z=True)
+        assert psr.get_stats(ws)["status"] == 0
+        check_forward(y, z, x, w, b, r, act, "bf16", f"{act} {M} x {N} x {K}")
