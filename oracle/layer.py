@@ -6,6 +6,7 @@ Inputs are float64 arrays that hold the bf16 / fp16 / fp32 values exactly.
 from __future__ import annotations
 
 import math
+from fractions import Fraction
 
 import numpy as np
 
@@ -108,14 +109,25 @@ def to_bf16(v):
     return u.astype(np.uint32).view(np.float32)
 
 
+def _step(low, high):
+    """(high - low) / 15 as the nearest bf16 number (half to even), from exact fractions."""
+    exact = (Fraction(float(high)) - Fraction(float(low))) / 15
+    near = int(to_bf16(np.float32([float(exact)])).view(np.uint32)[0]) >> 16
+    value = lambda bits: Fraction(float(np.array([bits << 16], np.uint32).view(np.float32)[0]))
+    bits = min((c for c in (near - 1, near, near + 1) if c >= 0), key=lambda c: (abs(value(c) - exact), c & 1))
+    return float(value(bits))
+
+
+kv4_step = np.vectorize(_step, otypes=[np.float64])
+
+
 def kv4_quantise(x):
-    """(codes uint8, scale, offset) of rows x [..., d]: every step in float32, as the format defines it."""
+    """(codes uint8, scale, offset) of rows x [..., d], as the format defines them: the codes' steps in float32."""
     x = x.astype(np.float32)
     with np.errstate(all="ignore"):
         mn, mx = x.min(-1, keepdims=True), x.max(-1, keepdims=True)
         fine = np.isfinite(x).all(-1, keepdims=True)
-        r = np.float32(1) / np.float32(15)
-        scale = to_bf16(np.where(fine, mx * r - mn * r, 0))
+        scale = kv4_step(np.where(fine, mn, 0), np.where(fine, mx, 0)).astype(np.float32)
         off = to_bf16(np.where(fine, mn, 0))
         c = np.clip(np.rint((x - off) / scale), 0, 15)
     c = np.where(fine & (scale > 0), c, 0).astype(np.uint8)

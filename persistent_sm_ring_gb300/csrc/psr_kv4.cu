@@ -96,6 +96,32 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return r;
 }
 
+// The step of a row, (max - min) / 15 rounded once to bf16.  Correct rounding without a division: the product with 1/15 is at most
+// 2.1 units of its last place off (the reciprocal one, the product half of one, the span's own rounding 8/15), so only one that
+// near to the middle of two bf16 numbers can round the wrong way.  There the sign of max - min - 15 middle decides: the product is
+// exact (9 bits by 4), the difference cancels exactly, and what the span lost is smaller than a unit of it.
+template <class T>
+__device__ __forceinline__ __nv_bfloat16 step_of(float mn, float mx) {
+  float span = __fsub_rn(mx, mn), back = 1.f;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    if (span == INFINITY) {  // the span passes the largest fp32 number, which its fifteenth does not
+      mx *= 0.0625f;
+      mn *= 0.0625f;
+      span = __fsub_rn(mx, mn);
+      back = 16.f;
+    }
+  }
+  uint32_t q = __float_as_uint(__fmul_rn(span, 1.f / 15.f));
+  if (((q + 0x8004u) & 0xFFFFu) <= 8u) {
+    q = (q & 0xFFFF0000u) | 0x8000u;
+    const float part = __fsub_rn(mx, span);  // what of the span's rounding mx and mn have each
+    const float lost = __fsub_rn(__fsub_rn(mx, __fadd_rn(span, part)), __fsub_rn(mn, part));
+    const float rest = __fadd_rn(__fmaf_rn(-15.f, __uint_as_float(q), span), lost);
+    if (rest != 0.f) q += rest > 0.f ? 1 : -1;
+  }
+  return __float2bfloat16_rn(__uint_as_float(q) * back);
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(kMove) append_kernel(const __grid_constant__ MoveParams p) {
   using R = Rows<D>;
@@ -151,10 +177,8 @@ __global__ void __launch_bounds__(kMove) append_kernel(const __grid_constant__ M
   {
     const T2 v = part & 2 ? (part & 1 ? low[1][1] : low[1][0]) : (part & 1 ? low[0][1] : low[0][0]);
     const float mn = to_f32(v.x), mx = -to_f32(v.y);
-    // max r - min r, r = 1/15 in fp32: max - min can pass the largest fp32 number
-    constexpr float r = 1.f / 15.f;
     __nv_bfloat162 so;
-    so.x = __float2bfloat16_rn(__fsub_rn(__fmul_rn(mx, r), __fmul_rn(mn, r)));
+    so.x = step_of<T>(mn, mx);
     so.y = __float2bfloat16_rn(mn);
     if (!(fabsf(mn) < INFINITY && fabsf(mx) < INFINITY)) so.x = so.y = __ushort_as_bfloat16(0x7FFF);
     inv = __fdividef(1.f, __bfloat162float(so.x));

@@ -376,3 +376,41 @@ def test_attention_of_two_streams_at_once(psr):
         got = [psr.kv4_attn(*c, Hkv=Hkv, page=page, stream=s)[:2] for c, s in zip(calls, streams)]
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
+
+
+def rows_with_steps_at_a_tie(t, d):
+    """Rows whose step is in the middle of two bf16 numbers or next to it, with that step from exact integers: multiples of 2^-20."""
+    rng, wide = np.random.default_rng(3), 2048 if t == "f16" else 255  # integers up to it are exact
+    rows, steps = [], []
+    for m in range(128, 256):
+        for high in (2048, 4096, 6144):
+            span = 15 * (2 * m + 1)  # of a step m + 1/2, doubled
+            for off in (0, 1, -1, 1024, -1024):  # of 2^-10
+                low = high * 1024 - span * 1024 + off
+                exact = torch.tensor(low / 1024.0).to(TYPES[t])
+                if abs(low) > wide * 1024 or float(exact) != low / 1024.0:
+                    continue
+                row = rng.uniform(low / 1024.0, high, d)
+                row[rng.choice(d, 2, replace=False)] = low / 1024.0, high
+                rows.append(torch.from_numpy(row * 2.0**-10))
+                up = off < 0 or (off == 0 and m % 2 == 1)  # a lower minimum is a longer span
+                steps.append((m + up) * 2.0**-9)
+    return torch.stack(rows).to(TYPES[t]), np.array(steps)
+
+
+@pytest.mark.parametrize("t,d", [("f16", 64), ("f16", 128), ("bf16", 64), ("bf16", 128)])
+def test_append_of_rows_whose_step_is_a_tie(psr, t, d):
+    need_gpu()
+    x, steps = rows_with_steps_at_a_tie(t, d)
+    n, page = len(x), 64
+    x = x.view(1, 1, n, d).cuda()
+    cache = psr.kv4_cache((n + page - 1) // page, 1, d, page)
+    table = torch.arange(cache.shape[0], dtype=torch.int32, device="cuda")[None]
+    psr.kv4_append(x, x, cache, table, torch.zeros(1, dtype=torch.int32, device="cuda"), page=page)
+    got, tab = cache.cpu().numpy(), table.cpu().numpy()
+    want, s, o = ol.kv4_quantise(x[0, 0].float().cpu().numpy())
+    for i in range(n):
+        for kv in (0, 1):
+            code, step, off = ol.kv4_row(got, tab, page, 0, 0, i, kv, d)
+            assert step == steps[i] == s[i, 0], (i, kv, float(step), steps[i])
+            assert off == o[i, 0] and np.array_equal(code, want[i]), (i, kv)

@@ -95,6 +95,20 @@ def test_oracle_quantiser_is_within_half_a_step():
     assert c[4].tolist() == [0, 15, 8, 8] or c[4].tolist() == [0, 15, 7, 7]
 
 
+def test_oracle_step_is_the_nearest_bf16_number():
+    # 15 t for a t in the middle of two bf16 numbers: to the even one; a little above or below: to that side
+    for m in range(128, 256):
+        for k in (-130, -20, 0, 100):
+            low, high = m * 2.0**k, (m + 1) * 2.0**k
+            even = low if m % 2 == 0 else high
+            top = 8192.0 * 2.0**k
+            span = 15 * (low + high) / 2
+            assert ol.kv4_step(top - span, top) == even, (m, k)
+            assert ol.kv4_step(top - span * (1 + 2.0**-30), top) == high and ol.kv4_step(top - span * (1 - 2.0**-30), top) == low
+    assert ol.kv4_step(0.0, 0.0) == 0.0 and ol.kv4_step(-2.5, -2.5) == 0.0
+    assert ol.kv4_step(-1.75 * 2.0**127, 1.75 * 2.0**127) == 239 * 2.0**117  # 238.9 of them
+
+
 # ---- sizes ---------------------------------------------------------------------------------------
 
 def test_workspace_and_cache_sizes(psr):
