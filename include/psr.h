@@ -449,7 +449,7 @@ PSR_API int psr_linear_bwd(const psr_linear_shape* shape, const void* dy, const 
  * 16 rows of d/2 bytes of K codes (column 2i in the low nibble of byte i), 16 rows of V codes, then a bf16
  * (scale, offset) pair for each K row, then for each V row.  A code c stands for offset + scale * c, with
  * offset = bf16(min of the row), scale = bf16((max - min) / 15), the exact quotient rounded once, half to even, and
- * c = (x - offset) / scale, both steps in fp32, rounded half to even and clamped to 0..15 (0 if scale is 0).  A row with an
+ * c = (x - offset) / scale, both steps in fp32 (of 1/16 of all three where scale >= 1e37), rounded half to even and clamped to 0..15 (0 if scale is 0).  A row with an
  * element that is not finite reads back as NaN.
  * table [B][max_pages] (int32, device): table[b][j] is the page of positions [j page, (j+1) page) of sequence b.
  * Page numbers outside [0, n_pages) and positions outside the table are never read or written. */

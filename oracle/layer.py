@@ -129,7 +129,8 @@ def kv4_quantise(x):
         fine = np.isfinite(x).all(-1, keepdims=True)
         scale = kv4_step(np.where(fine, mn, 0), np.where(fine, mx, 0)).astype(np.float32)
         off = to_bf16(np.where(fine, mn, 0))
-        c = np.clip(np.rint((x - off) / scale), 0, 15)
+        f = np.where(scale < 1e37, np.float32(1), np.float32(0.0625))  # a distance may pass the largest float32
+        c = np.clip(np.rint((x * f - off * f) / (scale * f)), 0, 15)
     c = np.where(fine & (scale > 0), c, 0).astype(np.uint8)
     nan = np.float32("nan")
     return c, np.where(fine, scale, nan), np.where(fine, off, nan)

@@ -216,9 +216,10 @@ __global__ void __launch_bounds__(kMove) append_kernel(const __grid_constant__ M
         }
         if (far > 0.49997f) {
           codes = 0;
+          const float f = s < 1e37f ? 1.f : 0.0625f;  // a distance from the offset may pass the largest fp32 number
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float q = fminf(fmaxf(__fdiv_rn(__fsub_rn(v[e], o), s), 0.f), 15.f);
+            const float q = fminf(fmaxf(__fdiv_rn(__fsub_rn(v[e] * f, o * f), s * f), 0.f), 15.f);
             codes |= (__float_as_uint(__fadd_rn(q, magic)) & 15u) << (4 * e);
           }
         }

@@ -414,3 +414,26 @@ def test_append_of_rows_whose_step_is_a_tie(psr, t, d):
             code, step, off = ol.kv4_row(got, tab, page, 0, 0, i, kv, d)
             assert step == steps[i] == s[i, 0], (i, kv, float(step), steps[i])
             assert off == o[i, 0] and np.array_equal(code, want[i]), (i, kv)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_of_rows_wider_than_fp32(psr, d):
+    # the span of a row, and the distance of an element from its minimum, may pass the largest fp32 number
+    need_gpu()
+    rng = np.random.default_rng(d)
+    n, page = 32, 16
+    rows = rng.uniform(-1, 1, (n, d)) * np.linspace(0.25, 1, n)[:, None] * 1.99 * 2.0**127
+    x = torch.from_numpy(rows).to(torch.bfloat16)
+    assert torch.isfinite(x).all()
+    cache = psr.kv4_cache(2, 1, d, page)
+    table = torch.arange(2, dtype=torch.int32, device="cuda")[None]
+    y = x.view(1, 1, n, d).cuda()
+    psr.kv4_append(y, y, cache, table, torch.zeros(1, dtype=torch.int32, device="cuda"), page=page)
+    got, tab, x = cache.cpu().numpy(), table.cpu().numpy(), f64(x)
+    want, s, o = ol.kv4_quantise(x)
+    for i in range(n):
+        for kv in (0, 1):
+            code, step, off = ol.kv4_row(got, tab, page, 0, 0, i, kv, d)
+            assert step == s[i, 0] and off == o[i, 0] and np.array_equal(code, want[i]), (i, kv)
+            # the nearest code, but for the rounding of the quotient (2 steps of 2^-24 below 16)
+            assert (np.abs(np.clip((x[i] - off) / step, 0, 15) - code) <= 0.5 + 2.0**-19).all(), (i, kv)

@@ -109,6 +109,12 @@ def test_oracle_step_is_the_nearest_bf16_number():
     assert ol.kv4_step(-1.75 * 2.0**127, 1.75 * 2.0**127) == 239 * 2.0**117  # 238.9 of them
 
 
+def test_oracle_quantiser_of_rows_wider_than_fp32():
+    x = np.array([[-1.0, 1.0, 0.75, 0.5, -0.75, 0.125]]) * 1.9375 * 2.0**127
+    c, s, o = ol.kv4_quantise(x)
+    assert c.tolist() == [[0, 15, 13, 11, 2, 8]] and np.isfinite(s).all() and np.isfinite(o).all()  # 7.5 (1 + x / max)
+
+
 # ---- sizes ---------------------------------------------------------------------------------------
 
 def test_workspace_and_cache_sizes(psr):
