@@ -754,6 +754,12 @@ def _workspace(at, workspace, need, what):
     return workspace
 
 
+def _clear_status(at, workspace):
+    """Of a call with nothing to do, which never reaches the library: its workspace reports success."""
+    with at.torch.cuda.stream(at.stream):  # None: the current one
+        workspace.flatten().view(at.torch.uint8)[:256].zero_()
+
+
 def linear_workspace_bytes(M, N, K, *, activation="none", backward=False) -> int:
     """Bytes of workspace that linear() or linear_bwd() needs for contiguous tensors, or views whose row strides are
     multiples of 8 elements and that start on 16-byte boundaries."""
@@ -794,6 +800,7 @@ def linear(x, w, bias=None, residual=None, *, activation="none", save_z=False, o
             z = at.empty(shape, x.dtype)
         workspace = _workspace(at, workspace, need, "linear")
         if shape[0] == 0:
+            _clear_status(at, workspace)
             return out, z, workspace
         rc = load().psr_linear(sh, x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
                                None if residual is None else residual.data_ptr(), out.data_ptr(),
@@ -849,8 +856,8 @@ def linear_bwd(dy, x, w, z=None, *, activation="none", need_dx=True, need_dw=Tru
             db = at.empty(shapes[2], x.dtype)
         workspace = _workspace(at, workspace, need, "linear_bwd")
         if shapes[0][0] == 0:  # sums over no rows
-            import torch
-            with torch.cuda.stream(stream):  # None: the current one
+            _clear_status(at, workspace)
+            with at.torch.cuda.stream(stream):  # None: the current one
                 for t in (dw, db):
                     if t is not None:
                         t.zero_()
@@ -1011,6 +1018,7 @@ def kv4_attn(q, cache, table, lens, *, Hkv, page, scale=None, out=None, lse=None
             lse = at.empty(q.shape[:3], at.torch.float32)
         workspace = _workspace(at, workspace, need, "kv4_attn")
         if sh.B == 0 or sh.S == 0:
+            _clear_status(at, workspace)
             return out, lse, workspace
         rc = load().psr_kv4_attn(sh, q.data_ptr(), qs, cache.data_ptr(), table.data_ptr(), lens.data_ptr(), out.data_ptr(), os_,
                                  lse.data_ptr(), workspace.data_ptr(), need, at.handle)

@@ -1106,7 +1106,11 @@ int psr_kv4_attn(const psr_kv4_shape* sh, const void* q, const psr_strides* qs, 
   int n_sm = 0, dev = 0;
   if ((rc = check_device(&n_sm)) != PSR_OK) return rc;
   if (cudaGetDevice(&dev) != cudaSuccess) return PSR_ERR_CUDA;
-  if (rows == 0) return PSR_OK;
+  if (rows == 0) {  // the control block still tells of a call that went well
+    if (cudaMemsetAsync(workspace, 0, sizeof(Ctrl), static_cast<cudaStream_t>(stream)) == cudaSuccess) return PSR_OK;
+    cudaGetLastError();
+    return PSR_ERR_CUDA;
+  }
   AttnParams p = {};
   p.c = cache_of(sh, cache, table);
   p.q = q; p.o = o; p.lse = lse; p.lens = lens;

@@ -437,3 +437,23 @@ def test_append_of_rows_wider_than_fp32(psr, d):
             assert step == s[i, 0] and off == o[i, 0] and np.array_equal(code, want[i]), (i, kv)
             # the nearest code, but for the rounding of the quotient (2 steps of 2^-24 below 16)
             assert (np.abs(np.clip((x[i] - off) / step, 0, 15) - code) <= 0.5 + 2.0**-19).all(), (i, kv)
+
+
+def test_attention_status_of_empty_batches(psr):
+    # a workspace that holds anything, through the binding and the C entry
+    need_gpu()
+    cache = psr.kv4_cache(2, 2, 64, 16)
+    size = psr.kv4_attn_workspace_bytes(2, 2, 2, 1, 64, page=16, n_pages=2, max_pages=1)
+    for B, S in ((0, 1), (2, 0)):
+        e = torch.empty((B, 2, S, 64), dtype=torch.bfloat16, device="cuda")
+        table, z = torch.zeros((B, 1), dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+        ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+        assert psr.kv4_attn(e, cache, table, z, Hkv=2, page=16, workspace=ws)[2] is ws
+        assert psr.get_stats(ws)["status"] == 0
+        ws.fill_(0xFF)
+        some = torch.zeros(4096, dtype=torch.uint8, device="cuda")  # stands for the tensors: nothing of them is read
+        at, st = some.data_ptr(), psr.Strides(128, 64, 64)
+        sh = psr.Kv4Shape(B, 2, 2, S, 64, 16, 2, 1, psr.BF16, 0.0)
+        assert psr.load().psr_kv4_attn(sh, at, st, cache.data_ptr(), at, at, at, st, at, ws.data_ptr(), size,
+                                       torch.cuda.current_stream().cuda_stream) == 0
+        assert psr.get_stats(ws)["status"] == 0 and not some.any()

@@ -388,3 +388,19 @@ def test_linear_streamed_last_columns(psr, M, N, K):
         y, z, ws = psr.linear(x, w, b, r, activation=act, save_z=True)
         assert psr.get_stats(ws)["status"] == 0
         check_forward(y, z, x, w, b, r, act, "bf16", f"{act} {M} x {N} x {K}")
+
+
+def test_linear_status_of_no_rows(psr):
+    # a workspace that holds anything, and one on another stream
+    need_gpu()
+    x, w = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), torch.ones((16, 64), dtype=torch.bfloat16, device="cuda")
+    dy, side = torch.empty((0, 16), dtype=torch.bfloat16, device="cuda"), torch.cuda.Stream()
+    for stream in (None, side):
+        for dtype in (torch.uint8, torch.float32):
+            size = max(psr.linear_workspace_bytes(0, 16, 64), psr.linear_workspace_bytes(0, 16, 64, backward=True))
+            for call in (lambda ws: psr.linear(x, w, workspace=ws, stream=stream), lambda ws: psr.linear_bwd(dy, x, w, workspace=ws, stream=stream)):
+                ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda").view(dtype)
+                side.wait_stream(torch.cuda.current_stream())
+                assert call(ws)[-1] is ws
+                torch.cuda.synchronize()
+                assert psr.get_stats(ws)["status"] == 0 and psr.get_stats(ws)["error_site"] == 0
