@@ -60,14 +60,14 @@ def rotary(x, pos, freq, amplitude=1.0, interleaved=False, inverse=False):
     return y
 
 
-_erf = np.vectorize(math.erf, otypes=[np.float64])
+_erfc = np.vectorize(math.erfc, otypes=[np.float64])
 
 
 def act(z, name):
     if name == "relu":
         return np.maximum(z, 0.0)
     if name == "gelu":
-        return 0.5 * z * (1 + _erf(z / math.sqrt(2)))
+        return 0.5 * z * _erfc(-z / math.sqrt(2))  # (1 + erf loses the left tail)
     if name == "gelu_tanh":
         return 0.5 * z * (1 + np.tanh(math.sqrt(2 / math.pi) * (z + 0.044715 * z**3)))
     if name == "silu":
@@ -79,7 +79,7 @@ def act_slope(z, name):
     if name == "relu":
         return (z > 0).astype(np.float64)
     if name == "gelu":
-        return 0.5 * (1 + _erf(z / math.sqrt(2))) + z * np.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+        return 0.5 * _erfc(-z / math.sqrt(2)) + z * np.exp(-z * z / 2) / math.sqrt(2 * math.pi)
     if name == "gelu_tanh":
         c = math.sqrt(2 / math.pi)
         t = np.tanh(c * (z + 0.044715 * z**3))

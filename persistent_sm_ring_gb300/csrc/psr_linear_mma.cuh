@@ -42,23 +42,25 @@ struct Epilogue {
 
 // act(z) and act'(z) in fp32, branch-free: expf, erff and tanhf of the CUDA library cost the epilogue 30 to 40 issue
 // slots an element (a 256-column half of a 1024-deep tile then waits on its epilogue).  The exponential and the reciprocal
-// are the special function unit's (2^-22 each); the normal distribution function is Abramowitz and Stegun's formula 7.1.26
-// for erf (error below 1.5e-7), taken as its complement so that the left tail keeps its digits.
+// are the special function unit's (2^-22 each).
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.f + ex2_approx(-1.4426950408889634f * x)); }
-// Phi(z); *e = exp(-z^2 / 2)
+// Phi(z); *e = exp(-z^2 / 2).  Phi(-|z|) = e t P(t), t = 1 / (1 + 0.295 |z|), P a polynomial of degree 5 whose coefficients a
+// linear program fitted over |z| <= 14.5 for the least of the absolute error in units of 1e-7 and the relative one in units of
+// 3e-5: as evaluated here it is off by at most 2.5e-7, and by 4e-5 of itself, so that the left tail keeps its digits too.
 __device__ __forceinline__ float normal_cdf(float z, float* e) {
-  const float t = rcp_approx(fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.f));
+  const float t = rcp_approx(fmaf(0.295f, fabsf(z), 1.f));
   *e = ex2_approx(-0.72134752044448170f * z * z);
-  float q = fmaf(1.061405429f, t, -1.453152027f);
-  q = fmaf(q, t, 1.421413741f);
-  q = fmaf(q, t, -0.284496736f);
-  q = fmaf(q, t, 0.254829592f);
-  const float h = 0.5f * q * t * *e;
+  float q = fmaf(-0.0838146742f, t, 0.251207165f);
+  q = fmaf(q, t, -0.0539902122f);
+  q = fmaf(q, t, 0.160338289f);
+  q = fmaf(q, t, 0.107865875f);
+  q = fmaf(q, t, 0.118393462f);
+  const float h = q * t * *e;
   return z < 0.f ? h : 1.f - h;
 }
 

@@ -10,7 +10,7 @@ import numpy as np
 import pytest
 import torch
 
-from layer_util import check, f64, need_gpu, randn
+from layer_util import TYPES, check, f64, need_gpu, randn
 from oracle import layer as ol
 
 pytestmark = pytest.mark.gpu
@@ -404,3 +404,28 @@ def test_linear_status_of_no_rows(psr):
                 assert call(ws)[-1] is ws
                 torch.cuda.synchronize()
                 assert psr.get_stats(ws)["status"] == 0 and psr.get_stats(ws)["error_site"] == 0
+
+
+# A one-hot x makes z an exact grid.  gelu = z Phi(z): the kernel's Phi is off by 4e-5 of itself, and the exponent of its tail, up
+# to 104 in powers of two, by three roundings of 2^-24 of that, 1.3e-5 together; 2^-14 bounds the two.  The slope is Phi + z phi with
+# the same two bounds on its terms.  Results below the smallest normal number may be flushed.
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_gelu_keeps_the_digits_of_its_tails(psr, t, M):
+    need_gpu()
+    grid = torch.linspace(-12, 12, 4801, dtype=torch.float64).to(TYPES[t])
+    w = torch.zeros((len(grid), 64), dtype=TYPES[t])
+    w[:, 0] = grid
+    x = torch.zeros((M, 64), dtype=TYPES[t])
+    x[:, 0] = 1
+    y, z, _ = psr.linear(x.cuda(), w.cuda(), activation="gelu", save_z=True)
+    assert torch.equal(z, grid.cuda().expand(M, -1))
+    g = f64(grid)
+    want = ol.act(g, "gelu")
+    tiny = TINY[t] + 2.0**-120
+    check(y, np.broadcast_to(want, (M, len(g))), np.abs(want) * (ol.HALF_STEP[t] * 1.01 + 2.0**-14) + tiny, "gelu")
+    db = psr.linear_bwd(torch.ones_like(z), x.cuda(), w.cuda(), z, activation="gelu", need_dx=False, need_dw=False)[2]
+    slope, phi = ol.act_slope(g, "gelu"), np.exp(-g * g / 2) / np.sqrt(2 * np.pi)
+    terms = want / np.where(g == 0, 1, g) + np.abs(g) * phi
+    # over M rows the sum has M - 1 roundings of 2^-24 as well
+    check(db, M * slope, M * np.abs(slope) * (ol.HALF_STEP[t] * 1.01 + M * 2.0**-24) + M * 2.0**-14 * terms + tiny, "slope")
