@@ -611,6 +611,25 @@ def _check_apart(out, x, what, same_ok, kinds="an output overlaps an input"):
         raise ValueError(f"{what}: {kinds}")
 
 
+def _check_outputs(what, outs, inputs, workspace=None):
+    """Outputs passed in, and the workspace, share no memory with the inputs or one another."""
+    outs = [t for t in outs if t is not None]
+    for i, out in enumerate(outs):
+        for x in inputs:
+            if x is not None:
+                _check_apart(out, x, what, False)
+        for other in outs[:i]:
+            _check_apart(out, other, what, False, "the outputs overlap")
+    if workspace is not None:
+        first = workspace.data_ptr()  # contiguous, or refused later
+        past = first + workspace.numel() * workspace.element_size()
+        for x in (*inputs, *outs):
+            if x is not None and x.numel() > 0:
+                a, b = _span(x)
+                if a < past and first < b:
+                    raise ValueError(f"{what}: the workspace overlaps a tensor")
+
+
 def _check_other(out, x, what, kinds):
     """Of [B, H, S, d] tensors: `out` is not `x`, and shares nothing with it if both are contiguous (views of one buffer
     may lie between one another)."""
@@ -660,6 +679,9 @@ def rotary(q, k, table, *, P=1, causal=CAUSAL, positions=None, offset=0, interle
                     _check_other(out, x, "rotary", "an output overlaps the other input")
             if q_out is not None and k_out is not None:
                 _check_other(q_out, k_out, "rotary", "the outputs overlap")
+        for out in (q_out, k_out):
+            if out is not None:
+                _check_outputs("rotary", (out,), (table, positions))
     with _Launch(dev, stream, "rotary") as at:
         if q_out is None:
             q_out = at.empty(q_shape, q.dtype)
@@ -793,6 +815,8 @@ def linear(x, w, bias=None, residual=None, *, activation="none", save_z=False, o
         for t in (x, w, bias, residual, out):
             if t is not None:
                 _check_apart(z, t, "linear", False)
+    if workspace is not None:
+        _check_outputs("linear", (), (x, w, bias, residual, out, z), workspace)
     with _Launch(dev, stream, "linear") as at:
         if out is None:
             out = at.empty(shape, x.dtype)
@@ -839,14 +863,7 @@ def linear_bwd(dy, x, w, z=None, *, activation="none", need_dx=True, need_dw=Tru
         lambda: (linear_bwd, _meta(dy), _meta(x), _meta(w), _meta(z), activation, _meta(dx), _meta(dw), _meta(db),
                  x.data_ptr() % 16, w.data_ptr() % 16, dy.data_ptr() % 16),
         lambda: _linear_bwd_plan(dy, x, w, z, activation, dx, dw, db))
-    for t in (dx, dw, db):
-        if t is not None:
-            for u in (dy, x, w, z):
-                if u is not None:
-                    _check_apart(t, u, "linear_bwd", False)
-    for a, b in ((dx, dw), (dx, db), (dw, db)):
-        if a is not None and b is not None:
-            _check_apart(a, b, "linear_bwd", False, "the outputs overlap")
+    _check_outputs("linear_bwd", (dx, dw, db), (dy, x, w, z), workspace)
     with _Launch(dev, stream, "linear_bwd") as at:
         if dx is None and need_dx:
             dx = at.empty(shapes[0], x.dtype)
@@ -924,7 +941,8 @@ def kv4_append(k, v, cache, table, start, *, page, count=None, stream=None):
     sequence b, i < count[b] (default: all S), goes to position start[b] + i, which is on page table[b, position // page].
 
     table: int32 [B, max_pages]; start, count: int32 [B].  Rows whose position is outside the table or whose page is
-    outside the cache are left out.  The places written must differ.  Returns the cache."""
+    outside the cache are left out.  The places written must differ, and the cache shares no memory with the other tensors.
+    Returns the cache."""
     sh, ks, vs, dev = _plan(lambda: (kv4_append, _meta(k), _meta(v), _meta(cache), _meta(table), _meta(start), _meta(count), int(page)),
                             lambda: _kv4_append_plan(k, v, cache, table, start, count, page))
     if sh.B == 0 or sh.S == 0:
@@ -955,11 +973,7 @@ def kv4_read(cache, table, start, *, S, Hkv, d, page, count=None, dtype=None, k=
         lambda: (kv4_read, _meta(cache), _meta(table), _meta(start), _meta(count), int(S), int(Hkv), int(d), int(page), dtype,
                  _meta(k), _meta(v)),
         lambda: _kv4_read_plan(cache, table, start, count, S, Hkv, d, page, dtype, k, v))
-    for t in (k, v):
-        if t is not None:
-            _check_apart(t, cache, "kv4_read", False)
-    if k is not None and v is not None:
-        _check_apart(k, v, "kv4_read", False, "the outputs overlap")
+    _check_outputs("kv4_read", (k, v), (cache, table, start, count))
     with _Launch(dev, stream, "kv4_read") as at:
         k = at.empty(shape, dtype) if k is None else k
         v = at.empty(shape, dtype) if v is None else v
@@ -1006,11 +1020,7 @@ def kv4_attn(q, cache, table, lens, *, Hkv, page, scale=None, out=None, lse=None
         lambda: (kv4_attn, _meta(q), _meta(cache), _meta(table), _meta(lens), int(Hkv), int(page),
                  None if scale is None else float(scale), _meta(out), _meta(lse)),
         lambda: _kv4_attn_plan(q, cache, table, lens, Hkv, page, scale, out, lse))
-    if out is not None:
-        _check_apart(out, q, "kv4_attn", False)
-        _check_apart(out, cache, "kv4_attn", False)
-        if lse is not None:
-            _check_apart(lse, out, "kv4_attn", False, "the outputs overlap")
+    _check_outputs("kv4_attn", (out, lse), (q, cache, table, lens), workspace)
     with _Launch(dev, stream, "kv4_attn") as at:
         if out is None:
             out = at.empty(q.shape, q.dtype)

@@ -356,3 +356,36 @@ def test_linear_operands_off_their_boundary(psr):
         size = lambda odd: psr.load().psr_linear_workspace_bytes(psr.LinearShape(300, 400, 512, 0, 0, 0, 0, 0, 0, 0, odd), 1)
         assert size(bit) - size(0) >= 2 * {1: 300 * 512, 2: 400 * 512, 4: 300 * 400}[bit]
     assert linear_call(psr, dict(odd=8)) == linear_call(psr, dict(odd=-1)) == psr.ERR_ARG
+
+
+def test_outputs_and_workspaces_share_nothing_with_other_tensors(psr, fake_device):
+    cache = torch.zeros((6, 2, 16 * 72), dtype=torch.uint8)
+    raw = torch.zeros(1 << 20, dtype=torch.uint8)
+    at = lambda first, shape, dtype: raw[first:first + int(np.prod(shape)) * dtype.itemsize].view(dtype).view(shape)
+    q, table, n = at(0, (3, 4, 1, 64), BF), at(2048, (3, 2), torch.int32), at(3000, (3,), torch.int32)
+    attn = lambda match, **kw: _refused(psr.kv4_attn, match, q, cache, table, n, Hkv=2, page=16, **kw)
+    for first in (1536 - 48, 2048 - 44, 2048, 3000, 3008):
+        attn("overlaps an input", lse=at(first, (3, 4, 1), torch.float32))
+        attn("the workspace overlaps a tensor", workspace=raw[first:])
+    attn("overlaps an input", lse=cache.view(-1)[:48].view(torch.float32).view(3, 4, 1))
+    out = at(8192, (3, 4, 1, 64), BF)
+    attn("the outputs overlap", out=out, lse=at(8192, (3, 4, 1), torch.float32))
+    attn("the workspace overlaps a tensor", out=out, workspace=raw[9000:])
+    attn("the workspace overlaps a tensor", lse=at(8192, (3, 4, 1), torch.float32), workspace=raw[4096:])
+    attn("overlaps an input", out=at(3008 - 1536 + 8, (3, 4, 1, 64), BF))
+    read = lambda match, **kw: _refused(psr.kv4_read, match, cache, table, n, S=4, Hkv=2, d=64, page=16, **kw)
+    read("overlaps an input", k=at(2016, (3, 2, 4, 64), BF))
+    read("overlaps an input", count=at(9000, (3,), torch.int32), v=at(8192, (3, 2, 4, 64), BF))
+    x, w, b, r = at(0, (4, 16), BF), at(4096, (24, 16), BF), at(8192, (24,), BF), at(12288, (4, 24), BF)
+    for t in (x, w, b, r):
+        _refused(psr.linear, "the workspace overlaps a tensor", x, w, b, r, workspace=raw[t.storage_offset() * t.element_size() + 2:])
+    _refused(psr.linear, "the workspace overlaps a tensor", x, w, out=r, workspace=raw[8192:])
+    _refused(psr.linear, "the workspace overlaps a tensor", x, w, z=r, workspace=raw[8192:])
+    for kw in (dict(dx=at(16384, (4, 16), BF)), dict(dw=at(16384, (24, 16), BF)), dict(db=at(16384, (24,), BF)), dict(z=at(16384, (4, 24), BF))):
+        _refused(psr.linear_bwd, "the workspace overlaps a tensor", r, x, w, activation="relu" if "z" in kw else "none",
+                 workspace=raw[16000:], **kw)
+    f = lambda first: at(first, (1, 1, 1, 64), torch.float32)
+    freq, pos = at(2048, (32,), torch.int64), at(4096, (1,), torch.int64)
+    for out in (f(2048), f(4096 - 252)):
+        _refused(psr.rotary, "overlaps an input", f(0), None, freq, positions=pos, q_out=out)
+        _refused(psr.rotary, "overlaps an input", f(0), f(1024), freq, positions=pos, k_out=out)
