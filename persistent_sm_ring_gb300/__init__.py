@@ -604,7 +604,7 @@ def _check_apart(out, x, what, same_ok, kinds="an output overlaps an input"):
     (a, b), (c, d) = _span(out), _span(x)
     if a < d and c < b:
         ld, size = out.stride(0), out.element_size()
-        if out.dim() == x.dim() == 2 and x.stride(0) == ld and size == x.element_size() and (a - c) % size == 0:
+        if out.dim() == x.dim() == 2 and x.stride(0) == ld > 0 and size == x.element_size() and (a - c) % size == 0:
             right = (a - c) // size % ld  # out's first column, counted from x's
             if right >= x.shape[1] and ld - right >= out.shape[1]:
                 return

@@ -389,3 +389,8 @@ def test_outputs_and_workspaces_share_nothing_with_other_tensors(psr, fake_devic
     for out in (f(2048), f(4096 - 252)):
         _refused(psr.rotary, "overlaps an input", f(0), None, freq, positions=pos, q_out=out)
         _refused(psr.rotary, "overlaps an input", f(0), f(1024), freq, positions=pos, k_out=out)
+
+
+def test_overlap_of_a_row_without_a_stride(psr, fake_device):
+    row = torch.zeros(16, dtype=BF).as_strided((1, 16), (0, 1))
+    _refused(psr.linear, "overlaps an input", row, torch.zeros((16, 16), dtype=BF), out=row)
