@@ -123,8 +123,9 @@ __global__ void __launch_bounds__(256)
   __shared__ float sums[8][32 * V];
   clear_ctrl(clear);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int j = (blockIdx.y * 32 + lane) * V;
-  const long long i0 = (long long)blockIdx.x * kDzRows, i1 = i0 + kDzRows < M ? i0 + kDzRows : M;
+  const uint32_t chunks = (M + kDzRows - 1) / kDzRows, cols = blockIdx.x / chunks, chunk = blockIdx.x - cols * chunks;
+  const int j = (int)(cols * 32 + lane) * V;
+  const long long i0 = (long long)chunk * kDzRows, i1 = i0 + kDzRows < M ? i0 + kDzRows : M;
   struct alignas(sizeof(T) * V) Vec { T v[V]; };
   float sum[V] = {};
   if (j < N) {
@@ -147,11 +148,11 @@ __global__ void __launch_bounds__(256)
   for (int c = 0; c < V; ++c) sums[warp][lane * V + c] = sum[c];
   __syncthreads();
   for (int c = threadIdx.x; c < 32 * V; c += 256) {
-    const int col = blockIdx.y * 32 * V + c;
+    const int col = (int)cols * 32 * V + c;
     float f = 0.f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) f += sums[w][c];
-    if (col < N) partial[(long long)blockIdx.x * N + col] = f;
+    if (col < N) partial[(long long)chunk * N + col] = f;
   }
 }
 
@@ -305,8 +306,10 @@ static int backward(const psr_linear_shape* sh, const Sizes& s, const void* dy, 
     float* partial = db ? reinterpret_cast<float*>(ws + s.partial) : nullptr;
     auto flat = [&](const void* p, long long ld) { return !p || (aligned_to(p, 16) && (sh->M == 1 || ld % 8 == 0)); };
     const bool vec = sh->N % 8 == 0 && flat(dy, s.ldy) && flat(z, s.ldz);
-    const dim3 grid((unsigned)s.chunks, (unsigned)((sh->N + 32 * (vec ? 8 : 1) - 1) / (32 * (vec ? 8 : 1))));
-    if (grid.y > 65535) return PSR_ERR_UNSUPPORTED;
+    const int wide = 32 * (vec ? 8 : 1);  // columns of a block
+    const long long blocks = (sh->N + wide - 1) / wide * (long long)s.chunks;  // the chunks of the same columns follow one another
+    if (blocks >= (1ll << 31)) return PSR_ERR_UNSUPPORTED;
+    const unsigned grid = (unsigned)blocks;
     const T *dy_t = static_cast<const T*>(dy), *z_t = static_cast<const T*>(z);
     if (vec) dz_kernel<T, 8><<<grid, 256, 0, l.st>>>(dy_t, s.ldy, z_t, s.ldz, out, s.lddz, partial, sh->M, sh->N, sh->act, l.clear);
     else dz_kernel<T, 1><<<grid, 256, 0, l.st>>>(dy_t, s.ldy, z_t, s.ldz, out, s.lddz, partial, sh->M, sh->N, sh->act, l.clear);

@@ -429,3 +429,23 @@ def test_gelu_keeps_the_digits_of_its_tails(psr, t, M):
     terms = want / np.where(g == 0, 1, g) + np.abs(g) * phi
     # over M rows the sum has M - 1 roundings of 2^-24 as well
     check(db, M * slope, M * np.abs(slope) * (ol.HALF_STEP[t] * 1.01 + M * 2.0**-24) + M * 2.0**-14 * terms + tiny, "slope")
+
+
+def test_linear_bwd_of_very_many_columns(psr):
+    # 65536 blocks of 32 columns where rows are not on 16-byte boundaries, two chunks of rows
+    need_gpu()
+    M, N, K = 66, 32 * 65535 + 1, 8
+    g = torch.Generator().manual_seed(8)
+    dy, x, w, z = randn(g, (M, N), "bf16"), randn(g, (M, K), "bf16"), randn(g, (N, K), "bf16"), randn(g, (M, N), "bf16")
+    dx, dw, db, ws = psr.linear_bwd(dy, x, w, z, activation="silu")
+    assert psr.get_stats(ws)["status"] == 0
+    got = dx, dw[-300:], db[-300:]
+    check_backward((None, dw[:300], db[:300]), dy[:, :300], x, w[:300], z[:, :300], "silu", "bf16", "first columns")
+    check_backward((None, *got[1:]), dy[:, -300:], x, w[-300:], z[:, -300:], "silu", "bf16", "last columns")
+    s = torch.sigmoid(z.float())
+    dz = (dy.float() * s * (1 + z.float() * (1 - s))).to(torch.bfloat16).double()
+    want = dz @ w.double()
+    # dz may have been rounded the other way (2^-8 of it, random signs: 2^-8 of the root of the sum of squares, by 6), sums of N
+    # products in fp32 drift by 2^-24 of their size a step (random signs again), and the result is rounded
+    size = ((dz**2) @ (w.double()**2)).sqrt()
+    assert ((dx.double() - want).abs() <= 2.0**-8 * want.abs() * 1.01 + (6 * 2.0**-8 + 2.0**-24 * N**0.5) * size).all()
