@@ -459,7 +459,7 @@ typedef struct {
   int d;                       /* 64 or 128 */
   int page, n_pages, max_pages; /* tokens of a page (16, 32, 64, 128 or 256), pages of the cache, columns of the table */
   int type;                    /* PSR_BF16 or PSR_F16, of q, k, v, o */
-  float scale;                 /* of the scores; <= 0 selects 1/sqrt(d) */
+  float scale;                 /* of the scores, finite; <= 0 selects 1/sqrt(d) */
 } psr_kv4_shape;
 
 /* Bytes of the cache: n_pages * Hkv * page * (d + 8); 0 if invalid. */

@@ -1014,6 +1014,7 @@ def kv4_attn(q, cache, table, lens, *, Hkv, page, scale=None, out=None, lse=None
 
     q: [B, Hq, S, d] bf16 or fp16, any strides with a contiguous last axis; cache, table as in kv4_append; lens: int32
     [B], the positions cached, the S new ones included.  Query i of sequence b sees positions 0 .. lens[b] - S + i.
+    scale: of the scores, finite; None, 0 or less: 1/sqrt(d).
     Returns (o [B, Hq, S, d], lse [B, Hq, S] fp32, workspace): o = 0 and lse = -inf for a query that sees nothing, NaN
     for a sequence whose length or pages are out of range."""
     sh, qs, os_, need, dev = _plan(

@@ -1098,7 +1098,7 @@ int psr_kv4_attn(const psr_kv4_shape* sh, const void* q, const psr_strides* qs, 
     return PSR_ERR_ARG;
   int rc = check_shape(sh);
   if (rc != PSR_OK) return rc;
-  if (ws_bytes < psr_kv4_attn_workspace_bytes(sh)) return PSR_ERR_ARG;
+  if (ws_bytes < psr_kv4_attn_workspace_bytes(sh) || !std::isfinite(sh->scale)) return PSR_ERR_ARG;
   const long long rows = (long long)sh->B * sh->Hq * sh->S;
   const long long tiles = ((long long)sh->Hq / sh->Hkv * sh->S + 7) / 8;
   if (rows >= (1LL << 30) || (double)sh->B * sh->Hkv * tiles * ((double)sh->max_pages * sh->page / kUnit + 1 + kPad) >= kMaxPlaces)

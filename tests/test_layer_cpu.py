@@ -394,3 +394,8 @@ def test_outputs_and_workspaces_share_nothing_with_other_tensors(psr, fake_devic
 def test_overlap_of_a_row_without_a_stride(psr, fake_device):
     row = torch.zeros(16, dtype=BF).as_strided((1, 16), (0, 1))
     _refused(psr.linear, "overlaps an input", row, torch.zeros((16, 16), dtype=BF), out=row)
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), float("-inf")])
+def test_kv4_attention_refuses_a_scale_that_is_not_finite(psr, scale):
+    assert kv4_call(psr, "attn", dict(scale=scale)) == psr.ERR_ARG
