@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kMove) read_kernel(const __grid_constant__ Mov
 // 16 tokens of d = 128 and ran at 3.2 TB/s).  So:
 //  * a code needs no conversion: its four bits, masked in place, are a subnormal fp16 number, c 2^-24 in bits 0..3 and
 //    16 c 2^-24 in bits 4..7, exact, and the matrix product takes it so.  One shift and four masks give eight codes.
-//  * q becomes fp16 for it, scaled by a power of two that puts the tile's largest element below 2^15 (exact for bf16
+//  * q becomes fp16 for it, each row scaled by a power of two that puts its largest element below 2^15 (exact for bf16
 //    down to 2^-25 of that); the scales 2^24, 1/16 and that power go to the sums.
 //  * P becomes fp16 times its row's scale, divided by a power of two of its own for each query row, which follows the
 //    largest product of a weight and a scale, so that no ratio of the scales of different tokens costs P its digits.  An mma
@@ -439,6 +439,10 @@ template <int D>
 struct AttnSmem {
   static constexpr int kBytes = kBlk * (D + 8);
   alignas(128) uint8_t ring[kWarps][kStages<D>][2 * kBytes];
+  // Of tile nt's columns 2t and 2t + 1: what a score is taken times, the sum of q, and the last position that they see.  (In
+  // registers they made d = 128 spill.)
+  float4 rows[kWarps][2][4];
+  int2 last[kWarps][2][4];
 };
 
 // 16 bytes, global to shared memory, past L1; groups of them complete in order
@@ -545,9 +549,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
     auto row_of = [&](int nt, int c) { return seg.rt * kRows + nt * 8 + (SPLIT ? c % 4 : c); };
     // ---- query fragments: column g of each tile, columns of q in the order of the K codes' words -----
     uint32_t qf[NT][KW][4];
-    float qsum[NT][2];   // of columns 2t and 2t + 1
-    int last[NT][2];     // last position that they see
-    float big = 0.f;
+    float up[NT], down[NT];  // the power of two that q's row g is taken times, and its inverse
     uint4 raw[NT][KW];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -574,15 +576,20 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
       return to_f32(*reinterpret_cast<T*>(&h));
     };
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      float big = 0.f;
 #pragma unroll
       for (int w = 0; w < KW; ++w)
 #pragma unroll
         for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(element(raw[nt][w], i)));
-    big = warp_max(big);
-    // 2^(14 - exponent of the largest); 1 if it is zero, subnormal or not finite
-    const int ex = (int)(__float_as_uint(big) >> 23);
-    const float up = ex == 0 || ex == 255 ? 1.f : __uint_as_float((uint32_t)min(254, max(1, 127 + 14 - (ex - 127))) << 23);
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      // 2^(14 - exponent of the row's largest); 1 if that is zero, subnormal or not finite
+      const int ex = (int)(__float_as_uint(big) >> 23);
+      const uint32_t power = ex == 0 || ex == 255 ? 127 : min(253, 127 + 14 - (ex - 127));  // (from 14 on)
+      up[nt] = __uint_as_float(power << 23);
+      down[nt] = __uint_as_float((254 - power) << 23);
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float sum = 0.f;
@@ -593,20 +600,21 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
         for (int i = 0; i < 8; ++i) {
           f[i] = element(raw[nt][w], i);
           sum += f[i];
-          f[i] *= i % 2 ? up * 0.0625f : up;  // the codes of odd columns stand 16 times too high
+          f[i] *= i % 2 ? up[nt] * 0.0625f : up[nt];  // the codes of odd columns stand 16 times too high
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) qf[nt][w][i] = pack_f16x2(f[i], f[i + 4]);
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        qsum[nt][c] = __shfl_sync(0xffffffffu, sum, (2 * t + c) * 4) * (p.scale * kLog2e);
-        last[nt][c] = n - p.S + row_of(nt, 2 * t + c) / p.group;
+      // (the last segment's units ended with all lanes' reads of these, and this one's begin behind a __syncwarp)
+      if (t == 0) {
+        float* to = reinterpret_cast<float*>(&sm.rows[warp][nt][g / 2]) + g % 2;
+        to[0] = p.scale * kLog2e * 16777216.f * down[nt];
+        to[2] = p.scale * kLog2e * sum;
+        reinterpret_cast<int*>(&sm.last[warp][nt][g / 2])[g % 2] = n - p.S + row_of(nt, g) / p.group;
       }
     }
-    const float kscale = p.scale * kLog2e * 16777216.f / up;
     float acc[NT][D / 16][4], eight[NT][4], m[NT][2], di[NT][2], l[NT][2], corr[NT][2];
     bool fresh = true;  // no unit yet: the first one sets the maxima (a column that sees nothing of it sees nothing later)
 #pragma unroll
@@ -657,7 +665,18 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
                       b8 & 0x00F000F0u, qf[nt][w][2 * half], qf[nt][w][2 * half + 1]);
           }
       // x: scores in powers of two above m; w: weights; y: weights times V's scale, in units of 1 / di
-      float x[NT][2 * NI], w[NT][2 * NI], y[NT][2 * NI], vo[NI], top = 0.f;
+      float x[NT][2 * NI], w[NT][2 * NI], y[NT][2 * NI], vo[NI], top = 0.f, kscale[NT][2], qsum[NT][2];
+      int last[NT][2] = {};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float4 v = sm.rows[warp][nt][t];
+        kscale[nt][0] = v.x; kscale[nt][1] = v.y;
+        qsum[nt][0] = v.z; qsum[nt][1] = v.w;
+        if (MASKED) {
+          const int2 at = sm.last[warp][nt][t];
+          last[nt][0] = at.x; last[nt][1] = at.y;
+        }
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -672,14 +691,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const uint32_t kp = pair_of(i, 0), vp = pair_of(i, 1);
-        const float ks = lo_bf16(kp) * kscale, ko = hi_bf16(kp), vs = lo_bf16(vp);
+        const float ks = lo_bf16(kp), ko = hi_bf16(kp), vs = lo_bf16(vp);
         vo[i] = fmaf(8.f, vs, hi_bf16(vp));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int e = 2 * i + c;
-            x[nt][e] = fmaf(ks, x[nt][e], fmaf(ko, qsum[nt][c], -m[nt][c]));
+            x[nt][e] = fmaf(ks * kscale[nt][c], x[nt][e], fmaf(ko, qsum[nt][c], -m[nt][c]));
             if (unseen(i, nt, c)) x[nt][e] = -INFINITY;  // such a row may hold anything
             w[nt][e] = ex2_approx(x[nt][e]);
             y[nt][e] = unseen(i, nt, c) ? 0.f : w[nt][e] * (vs * di[nt][c]);

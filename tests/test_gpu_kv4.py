@@ -457,3 +457,27 @@ def test_attention_status_of_empty_batches(psr):
         assert psr.load().psr_kv4_attn(sh, at, st, cache.data_ptr(), at, at, at, st, at, ws.data_ptr(), size,
                                        torch.cuda.current_stream().cuda_stream) == 0
         assert psr.get_stats(ws)["status"] == 0 and not some.any()
+
+
+@pytest.mark.parametrize("large", [2.0**30, 2.0**100, float("inf"), float("nan")])
+@pytest.mark.parametrize("Hq", [3, 4, 8, 16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_heads_of_different_sizes(psr, d, Hq, large):
+    # the rows of a KV head share matrix products: one with large or infinite elements leaves the others as they are
+    need_gpu()
+    rng = np.random.default_rng(Hq + d)
+    g = torch.Generator().manual_seed(Hq)
+    lens, page = [70, 33], 32
+    table, n_pages = pages_for(rng, lens, page)
+    cache = random_cache(rng, n_pages, 1, d, page)
+    q = randn(g, (2, Hq, 1, d), "bf16")
+    q[:, 0] *= large
+    q[:, 1] *= 300
+    q[:, 2] *= 2.0**-20
+    o, lse, _ = psr.kv4_attn(q, torch.from_numpy(cache).cuda(), torch.from_numpy(table).cuda(),
+                             torch.tensor(lens, dtype=torch.int32, device="cuda"), Hkv=1, page=page)
+    ro, rl, to, tl = ol.kv4_attention(f64(q[:, 1:]), cache, table, lens, page, 1, 1 / math.sqrt(d))
+    check(lse[:, 1:], rl, tl, "lse")
+    check(o[:, 1:], ro, to + ol.HALF_STEP["bf16"] * np.abs(ro) * 1.01, "o")
+    if math.isnan(large):
+        assert torch.isnan(o[:, 0]).all() and torch.isnan(lse[:, 0]).all()
