@@ -473,7 +473,8 @@ PSR_API int psr_kv4_append(const psr_kv4_shape* shape, const void* k, const psr_
                            const int32_t* count, void* stream);
 
 /* Reads positions start[b] + i, i < S, back into k and v [B][Hkv][S][d] (contiguous): zeros for rows i >= count[b]
- * (NULL: none), NaN for rows outside the table or on a page outside the cache. */
+ * (NULL: none), NaN for rows outside the table or on a page outside the cache.  offset + scale * c is rounded to `type`: the
+ * ends of a row that comes within a step of the type's largest number may become infinite. */
 PSR_API int psr_kv4_read(const psr_kv4_shape* shape, const void* cache, const int32_t* table, const int32_t* start,
                          const int32_t* count, void* k, void* v, void* stream);
 
@@ -486,6 +487,8 @@ PSR_API size_t psr_kv4_attn_workspace_bytes(const psr_kv4_shape* shape);
  * position gets o = 0, lse = -infinity.  A sequence with n < 0, n > max_pages * page, or a page outside the cache
  * among the pages of its n positions gets NaN.  The work is dealt out over the whole batch, so the order of a
  * sequence's sums (not the bound on their rounding) depends on the other lengths; the same call gives the same bits.
+ * Sizes: B Hq S below 2^30, and B Hkv ceil(Hq / Hkv * S / 8) (max_pages * page / 32 + 3) below 2^31 - 2^24, else
+ * PSR_ERR_UNSUPPORTED.
  *   workspace: >= psr_kv4_attn_workspace_bytes(shape), 256-byte aligned; not shared by launches in flight. */
 PSR_API int psr_kv4_attn(const psr_kv4_shape* shape, const void* q, const psr_strides* q_strides, const void* cache,
                          const int32_t* table, const int32_t* lens, void* o, const psr_strides* o_strides, float* lse,

@@ -44,10 +44,10 @@ __device__ __forceinline__ float warp_max(float v) {
 // ------------------------------------------------------------------------------------------------
 // D / 8 lanes take a row, eight columns (16 bytes) each; a block takes kTokens tokens of one sequence and KV head, and a lane
 // the K and V rows of two of them, so that four loads are in flight.  Bound by their instructions: 4 x 2000 tokens of 8 heads,
-// d = 128, are appended in 17.5 us (70 % of the issue slots, 200 instructions for a lane's part of a row) and read in 9.5, where
+// d = 128, are appended in 16.8 us (70 % of the issue slots, 200 instructions for a lane's part of a row) and read in 9.8, where
 // the bytes would take 6 each.
 constexpr int kEach = 2;  // tokens of a thread
-constexpr int kMove = 128;  // threads of a block (256: 3 % longer)
+constexpr int kMove = 128;  // threads of a block
 
 template <int D>
 struct Rows {
@@ -273,21 +273,21 @@ __global__ void __launch_bounds__(kMove) read_kernel(const __grid_constant__ Mov
 // Attention
 // ------------------------------------------------------------------------------------------------
 // Bound by reading the cache once, and by the instructions that it takes: 8 sequences of about 110k positions, 32 query and 8 KV
-// heads, d = 128, in 164 us (6.05 TB/s; 79 % of DRAM's peak, 61 % of the integer pipe's, 56 % of the issue slots).  A unit is two blocks (32 tokens) of one KV head and a tile of up to 8 NT query rows
-// (the group's heads times the new tokens); the units of all sequences stand in a line, segment by segment (a segment:
-// sequence, head, row tile), and each warp takes an equal stretch of it, so ragged batches and single long sequences load
-// every SM alike.  A segment that lies within one stretch is finished there; the pieces of one that does not meet in
-// combine_kernel through fp32 partial results and their running maxima and sums, as the ring's chunks do.  A segment
-// stands in the line behind kPad places without work, so that a stretch of many short ones is not the longest (48 ragged
-// sequences with 4 draft tokens, d = 64: 77 to 68 us).  (With stretches for whole CTAs, whose warps met in shared memory
-// after every segment, batches of short sequences took 3 to 5 us a segment.)
+// heads, d = 128, in 164 us (6.05 TB/s; 79 % of DRAM's peak, 61 % of the integer pipe's, 56 % of the issue slots).  A unit is two
+// blocks (32 tokens) of one KV head and a tile of up to 8 NT query rows (the group's heads times the new tokens); the units of
+// all sequences stand in a line, segment by segment (a segment: sequence, head, row tile), and each warp takes an equal stretch
+// of it, so ragged batches and single long sequences load every SM alike.  A segment that lies within one stretch is finished
+// there; the pieces of one that does not meet in combine_kernel through fp32 partial results and their running maxima and sums, as
+// the ring's chunks do.  A segment stands in the line behind kPad places without work, so that a stretch of many short ones is
+// not the longest (48 ragged sequences with 4 draft tokens, d = 64: 77 us without, 68 with).  Each row tile is a segment of its
+// own and reads the cache again: with 16 query rows to a KV head those 8 sequences take 251 us, with 32 and 64 (two and four
+// tiles) 451 and 881.
 //
-// Each warp has its own ring of stages, filled a unit or more ahead with 16-byte asynchronous copies by all of its lanes, and
-// its own softmax state.  (One lane's bulk copy and barrier took 700 clocks of a unit's 2200 at d = 64.)
+// Each warp has its own ring of stages, filled a unit or more ahead with 16-byte asynchronous copies by all of its lanes (one
+// lane's bulk copy and a barrier cost a third of a unit's time at d = 64), and its own softmax state.
 //   S^T[token][row] = K codes . q      (mma.m16n8k16: tokens on its 16 rows, query rows on its 8 columns)
 //   O^T[column][row] += V codes^T . P  (columns of V on the 16 rows, tokens in the contraction)
-// The issue slots are what is scarce (a first version that made 16-bit floats 16 + c of the codes took 485 instructions for
-// 16 tokens of d = 128 and ran at 3.2 TB/s).  So:
+// The issue slots are what is scarce.  So:
 //  * a code needs no conversion: its four bits, masked in place, are a subnormal fp16 number, c 2^-24 in bits 0..3 and
 //    16 c 2^-24 in bits 4..7, exact, and the matrix product takes it so.  One shift and four masks give eight codes.
 //  * q becomes fp16 for it, each row scaled by a power of two that puts its largest element below 2^15 (exact for bf16
@@ -295,18 +295,15 @@ __global__ void __launch_bounds__(kMove) read_kernel(const __grid_constant__ Mov
 //  * P becomes fp16 times its row's scale, divided by a power of two of its own for each query row, which follows the
 //    largest product of a weight and a scale, so that no ratio of the scales of different tokens costs P its digits.  An mma
 //    more for 16 tokens multiplies it with a constant code 8: what is wanted is the sum of P (c - 8), as large as the output,
-//    and the two sums' roundings go together (with the sum of P c alone those of a long context showed, 2.1e-3 of the output
-//    against 1.7e-3 for its own rounding).
+//    and the two sums' roundings go together (the sum of P c alone has those of terms that cancel: 2.1e-3 of the output in a
+//    long context, against 1.7e-3).
 //  * any order of the contraction will do, so K's fragments are read straight from the stage, 16 adjacent bytes of a row to a
 //    lane.  V's come through transposing matrix loads of 16-bit elements (four columns of a token), whose pieces the copies
-//    have swizzled over the banks (48 ragged sequences: 64 to 63 us against plain loads and byte permutes).  P leaves the
-//    first product in the layout that movmatrix turns into the second one's operand.
+//    have swizzled over the banks.  P leaves the first product in the layout that movmatrix turns into the second one's operand.
 //  * up to four query rows fill half of the eight columns.  SPLIT then gives columns 0..3 the first block of a unit and columns
 //    4..7 the second, as rows of their own that meet at the end: a lane has half as many weights to work out (8 sequences of
-//    about 110k positions, 4 rows: 174 to 166 us; 48 ragged sequences: 68 to 64).  Both products stay as many.
+//    about 110k positions, 4 rows: 174 us without, 166 with).  Both products stay as many.
 //  * the maximum and that power are only raised when a weight or a product passes kRaise: the check is one vote.
-// Units of four blocks (K and V in rings of their own), and the scores of the next unit between those of this one and its
-// second product, gained nothing at d = 128: the registers that they need are not there.
 constexpr int kWarps = 8;
 template <int D>
 constexpr int kStages = D == 128 ? 2 : 3;
@@ -882,8 +879,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_kernel(cons
   }
 }
 
-// The query rows of the segments that lie in several stretches, or in none: a row to a warp where segments are many (their
-// pieces are few), or to a block, whose warps take every 32nd piece.
+// The query rows of the segments that lie in several stretches, or in none: a row to a warp where segments are many, or to a
+// block, whose warps take every 32nd piece.  Many segments have few pieces each on average only: one sequence of 131072
+// positions among 63 of 16 has hundreds, which its rows' warps join one after another (110 us, where its bytes take 21).
 template <class T, int D, int NT>
 __global__ void __launch_bounds__(1024) combine_kernel(const __grid_constant__ AttnParams p, int ctas, int rows) {
   constexpr int kRows = 8 * NT, E = D / 32;
@@ -1010,7 +1008,7 @@ static int launch_attn(AttnParams& p, int dev, int n_sm, cudaStream_t st) {
   attn_kernel<T, D, NT, SPLIT><<<ctas, kWarps * 32, smem, st>>>(p);
   if (launch_status() != PSR_OK) return PSR_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  // up to 2 ctas kWarps pieces lie in the segments: a block to a row while a segment may have more than 16 of them
+  // a block to a row where the stretches are more than 16 to a segment on average
   const int rows = (int)(p.B * p.c.Hkv * R);
   const bool by_block = (long long)p.B * p.c.Hkv * p.n_rt * 16 < (long long)ctas * kWarps;
   cfg.gridDim = dim3((unsigned)(by_block ? rows : (rows + 7) / 8));
