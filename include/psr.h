@@ -449,8 +449,8 @@ PSR_API int psr_linear_bwd(const psr_linear_shape* shape, const void* dy, const 
  * 16 rows of d/2 bytes of K codes (column 2i in the low nibble of byte i), 16 rows of V codes, then a bf16
  * (scale, offset) pair for each K row, then for each V row.  A code c stands for offset + scale * c, with
  * offset = bf16(min of the row), scale = bf16((max - min) / 15), the exact quotient rounded once, half to even, and
- * c = (x - offset) / scale, both steps in fp32 (of 1/16 of all three where scale >= 1e37), rounded half to even and clamped to 0..15 (0 if scale is 0).  A row with an
- * element that is not finite reads back as NaN.
+ * c = (x - offset) / scale, both steps in fp32 (of 1/16 of all three where scale >= 1e37), rounded half to even and clamped to
+ * 0..15 (0 if scale is 0).  A row with an element that is not finite reads back as NaN.
  * table [B][max_pages] (int32, device): table[b][j] is the page of positions [j page, (j+1) page) of sequence b.
  * Page numbers outside [0, n_pages) and positions outside the table are never read or written. */
 typedef struct {
@@ -487,6 +487,7 @@ PSR_API size_t psr_kv4_attn_workspace_bytes(const psr_kv4_shape* shape);
  * position gets o = 0, lse = -infinity.  A sequence with n < 0, n > max_pages * page, or a page outside the cache
  * among the pages of its n positions gets NaN.  The work is dealt out over the whole batch, so the order of a
  * sequence's sums (not the bound on their rounding) depends on the other lengths; the same call gives the same bits.
+ * q is taken in fp16 times a power of two of each row (its elements below 2^100 in size), the weights in fp16 too, sums in fp32.
  * Sizes: B Hq S below 2^30, and B Hkv ceil(Hq / Hkv * S / 8) (max_pages * page / 32 + 3) below 2^31 - 2^24, else
  * PSR_ERR_UNSUPPORTED.
  *   workspace: >= psr_kv4_attn_workspace_bytes(shape), 256-byte aligned; not shared by launches in flight. */
