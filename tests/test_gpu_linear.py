@@ -10,7 +10,7 @@ import numpy as np
 import pytest
 import torch
 
-from layer_util import TYPES, check, f64, need_gpu, randn
+from layer_util import check, f64, need_gpu, randn
 from oracle import layer as ol
 
 pytestmark = pytest.mark.gpu
@@ -412,6 +412,7 @@ def test_linear_status_of_no_rows(psr):
 @pytest.mark.parametrize("t", ["bf16", "f16"])
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_gelu_keeps_the_digits_of_its_tails(psr, t, M):
+    from layer_util import TYPES
     need_gpu()
     grid = torch.linspace(-12, 12, 4801, dtype=torch.float64).to(TYPES[t])
     w = torch.zeros((len(grid), 64), dtype=TYPES[t])
