@@ -495,6 +495,36 @@ PSR_API int psr_kv4_attn(const psr_kv4_shape* shape, const void* q, const psr_st
                          const int32_t* table, const int32_t* lens, void* o, const psr_strides* o_strides, float* lse,
                          void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- The two ends of a training step around the layers ------------------------------------------
+ * What turns tokens into the first layer's rows, and what turns the last layer's rows into a loss and the first gradients.
+ * The same rules as above: asynchronous on `stream`, current device (sm_103), no device memory allocated, graphs allowed. */
+
+/* Rows of a table looked up by token and scaled, and the table's gradient. */
+typedef struct {
+  int M, V, K;             /* tokens (0 .. 2^28), rows (1 .. 2^30) and columns (1 .. 2^20) of the table */
+  int type;                /* PSR_BF16, PSR_F16 or PSR_F32 */
+  long long ids_step;      /* ids[i * ids_step] is token i's (0: the same id for all) */
+  long long ldw, ldy;      /* row strides of w and of y or dy in elements; 0: K */
+  long long padding;       /* psr_embedding_bwd: an id without gradient; negative: none */
+  int accumulate;          /* psr_embedding_bwd: add to dw */
+  float scale;             /* finite */
+} psr_embedding_shape;
+
+/* y[i] = scale * w[ids[i]], computed in fp32 and rounded once; a row of NaN for an id outside 0 .. V-1.
+ *   ids: device (read); w: device, [V][K] (read); y: device, [M][K] (written; shares no memory with the others). */
+PSR_API int psr_embedding(const psr_embedding_shape* shape, const int64_t* ids, const void* w, void* y, void* stream);
+
+/* Bytes of device workspace psr_embedding_bwd needs; 0 if invalid. */
+PSR_API size_t psr_embedding_workspace_bytes(const psr_embedding_shape* shape);
+
+/* dw[v] = scale * sum of dy[i] over the i with ids[i] = v, in the order of i, summed in fp32 and rounded once; rows that no id
+ * names are zeros.  With `accumulate` the sums are added to dw's rows (before the rounding), and rows that no id names stay as
+ * they are.  Ids outside 0 .. V-1 and the padding id are left out.  Two calls on the same inputs give the same bits.
+ *   dy: device, [M][K] (read); ids: device (read); dw: device, [V][K] contiguous (written);
+ *   workspace: device, 256-byte aligned, >= psr_embedding_workspace_bytes(shape). */
+PSR_API int psr_embedding_bwd(const psr_embedding_shape* shape, const void* dy, const int64_t* ids, void* dw, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

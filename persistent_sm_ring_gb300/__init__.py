@@ -5,7 +5,8 @@ Thin Python binding over the C ABI of ``libpsr.so`` (declared in
 (staging, readiness flags, the tcgen05 FlashAttention pass, the LSE-exact
 merge, the on-GPU partition controller) runs in the library's CUDA kernel.
 The layer around the ring (rotary positions, linear with its gradients, a
-4-bit KV cache with its attention) is bound at the end of the file.
+4-bit KV cache with its attention) and the two ends of a training step
+(embedding, the output projection's loss) are bound at the end of the file.
 PyTorch supplies device memory and streams.  There is no fallback: if the
 library is missing or the device is not an sm_103 GPU, calls raise.
 """
@@ -22,6 +23,7 @@ __all__ = ["build", "load", "Shape", "AgShape", "RsShape", "Partition", "Stats",
            "ring_attn_bwd", "ring_attn_bwd_workspace_bytes",
            "rotary_table", "rotary", "rotary_bwd", "linear", "linear_bwd", "linear_workspace_bytes",
            "kv4_cache", "kv4_append", "kv4_read", "kv4_attn", "kv4_attn_workspace_bytes",
+           "embedding", "embedding_bwd", "embedding_workspace_bytes",
            "get_stats", "get_trajectory", "controller_target", "num_ctas", "status_string", "PsrError",
            "STATIC", "ADAPTIVE", "FAULT_NONE", "FAULT_DROP_FIRST_FLAG", "FAULT_SLOW_STAGING", "CAUSAL",
            "CAUSAL_BALANCED"]
@@ -36,7 +38,8 @@ EXPORTED = ("psr_workspace_bytes", "psr_ring_attn_fwd", "psr_ring_attn_fwd_host"
             "psr_ring_attn_fwd_noalloc", "psr_noalloc_get_stats", "psr_ag_gemm_workspace_bytes", "psr_ag_gemm", "psr_gemm_rs_workspace_bytes",
             "psr_gemm_rs", "psr_ring_attn_bwd_workspace_bytes", "psr_ring_attn_bwd",
             "psr_rotary_table", "psr_rotary", "psr_linear_workspace_bytes", "psr_linear", "psr_linear_bwd",
-            "psr_kv4_cache_bytes", "psr_kv4_append", "psr_kv4_read", "psr_kv4_attn_workspace_bytes", "psr_kv4_attn")
+            "psr_kv4_cache_bytes", "psr_kv4_append", "psr_kv4_read", "psr_kv4_attn_workspace_bytes", "psr_kv4_attn",
+            "psr_embedding", "psr_embedding_workspace_bytes", "psr_embedding_bwd")
 
 BF16, F16, F32 = 0, 1, 2
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
@@ -77,6 +80,12 @@ class Kv4Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("S", ctypes.c_int),
                 ("d", ctypes.c_int), ("page", ctypes.c_int), ("n_pages", ctypes.c_int), ("max_pages", ctypes.c_int),
                 ("type", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class EmbeddingShape(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int), ("V", ctypes.c_int), ("K", ctypes.c_int), ("type", ctypes.c_int),
+                ("ids_step", ctypes.c_longlong), ("ldw", ctypes.c_longlong), ("ldy", ctypes.c_longlong),
+                ("padding", ctypes.c_longlong), ("accumulate", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 class Partition(ctypes.Structure):
@@ -165,7 +174,7 @@ def load(trace: bool = False, variant: str = "") -> ctypes.CDLL:
         lib.psr_ring_attn_fwd_noalloc.restype = ctypes.c_int
         lib.psr_noalloc_get_stats.argtypes = [ctypes.POINTER(Stats), vp]
         lib.psr_noalloc_get_stats.restype = ctypes.c_int
-        P_st, P_rot, P_lin, P_kv4 = map(ctypes.POINTER, (Strides, RotaryShape, LinearShape, Kv4Shape))
+        P_st, P_rot, P_lin, P_kv4, P_emb = map(ctypes.POINTER, (Strides, RotaryShape, LinearShape, Kv4Shape, EmbeddingShape))
         dbl = ctypes.c_double
         lib.psr_rotary_table.argtypes = [ctypes.c_int, dbl, ctypes.c_int, dbl, dbl, dbl, dbl, vp]
         lib.psr_rotary.argtypes = [P_rot, vp, P_st, vp, P_st, vp, P_st, vp, P_st, vp, vp, ctypes.c_longlong, vp]
@@ -177,10 +186,14 @@ def load(trace: bool = False, variant: str = "") -> ctypes.CDLL:
         lib.psr_kv4_read.argtypes = [P_kv4, vp, vp, vp, vp, vp, vp, vp]
         lib.psr_kv4_attn_workspace_bytes.argtypes = [P_kv4]
         lib.psr_kv4_attn.argtypes = [P_kv4, vp, P_st, vp, vp, vp, vp, P_st, vp, vp, sz, vp]
+        lib.psr_embedding.argtypes = [P_emb, vp, vp, vp, vp]
+        lib.psr_embedding_workspace_bytes.argtypes = [P_emb]
+        lib.psr_embedding_bwd.argtypes = [P_emb, vp, vp, vp, vp, sz, vp]
         for name in ("psr_rotary_table", "psr_rotary", "psr_linear", "psr_linear_bwd", "psr_kv4_append", "psr_kv4_read",
-                     "psr_kv4_attn"):
+                     "psr_kv4_attn", "psr_embedding", "psr_embedding_bwd"):
             getattr(lib, name).restype = ctypes.c_int
-        for name in ("psr_linear_workspace_bytes", "psr_kv4_cache_bytes", "psr_kv4_attn_workspace_bytes"):
+        for name in ("psr_linear_workspace_bytes", "psr_kv4_cache_bytes", "psr_kv4_attn_workspace_bytes",
+                     "psr_embedding_workspace_bytes"):
             getattr(lib, name).restype = sz
         lib.psr_num_ctas.argtypes = []
         lib.psr_num_ctas.restype = ctypes.c_int
@@ -1055,6 +1068,103 @@ def _kv4_attn_plan(q, cache, table, lens, Hkv, page, scale, out, lse):
     if need == 0:
         raise PsrError(ERR_UNSUPPORTED, "psr_kv4_attn")
     return sh, qs, os_, need, dev
+
+
+# ------------------------------------------------------------------------------------------------
+# The two ends of a training step around the layers: embedding, and the loss of the output projection
+# ------------------------------------------------------------------------------------------------
+
+def _check_ids(t, name, M, dev):
+    """Token ids [M], int64, any stride; their step."""
+    import torch
+    _check_cuda(t, name, 1)
+    _check_like(t, name, (M,), torch.int64, dev)
+    return t.stride(0) if M > 1 else 1
+
+
+def embedding(ids, w, *, scale=1.0, out=None, stream=None):
+    """Rows of a table: y[i] = scale * w[ids[i]], computed in fp32 and rounded once.
+
+    ids: int64 [M], any stride; w: [V, K] bf16, fp16 or fp32, rows may be strided.  An id outside the table gives a row of
+    NaN.  Returns y [M, K], contiguous unless passed in (its rows may be strided)."""
+    sh, dev, shape = _plan(lambda: (embedding, _meta(ids), _meta(w), float(scale), _meta(out)),
+                           lambda: _embedding_plan(ids, w, scale, out))
+    if out is not None:
+        _check_outputs("embedding", (out,), (ids, w))
+    with _Launch(dev, stream, "embedding") as at:
+        if out is None:
+            out = at.empty(shape, w.dtype)
+        if shape[0] == 0:
+            return out
+        rc = load().psr_embedding(sh, ids.data_ptr(), w.data_ptr(), out.data_ptr(), at.handle)
+    if rc != OK:
+        raise PsrError(rc, "psr_embedding")
+    return out
+
+
+def _embedding_plan(ids, w, scale, out):
+    _check_cuda(w, "w", 2)
+    _check_cuda(ids, "ids", 1)
+    V, K = w.shape
+    M, dev = ids.shape[0], w.device
+    step = _check_ids(ids, "ids", M, dev)
+    ldy = 0
+    if out is not None:
+        _check_like(out, "out", (M, K), w.dtype, dev)
+        ldy = _row_stride(out, "out")
+    sh = EmbeddingShape(M, V, K, _type_of(w, "w", F32), step, _row_stride(w, "w"), ldy, -1, 0, float(scale))
+    if load().psr_embedding_workspace_bytes(sh) == 0:
+        raise PsrError(ERR_ARG, "psr_embedding")
+    return sh, dev, (M, K)
+
+
+def embedding_workspace_bytes(M, V, K) -> int:
+    """Bytes of workspace that embedding_bwd() needs."""
+    n = load().psr_embedding_workspace_bytes(EmbeddingShape(int(M), int(V), int(K), BF16, 1, 0, 0, -1, 0, 1.0))
+    if n == 0:
+        raise PsrError(ERR_ARG, "psr_embedding_workspace_bytes")
+    return int(n)
+
+
+def embedding_bwd(dy, ids, n_rows, *, scale=1.0, padding=None, dw=None, accumulate=False, workspace=None, stream=None):
+    """The gradient of embedding() with respect to a table of n_rows rows: dw[v] = scale * the sum of dy[i] over the i with
+    ids[i] = v, in the order of i, summed in fp32 and rounded once (two calls give the same bits).
+
+    dy: [M, K] bf16, fp16 or fp32, rows may be strided; ids: int64 [M], any stride.  Ids outside the table, and the id
+    `padding`, are left out.  dw [n_rows, K] may be passed in (contiguous); with accumulate the sums are added to its rows, and
+    rows that no id names stay as they are (a table shared with the output projection, say).  Returns (dw, workspace)."""
+    sh, need, dev, shape = _plan(
+        lambda: (embedding_bwd, _meta(dy), _meta(ids), int(n_rows), float(scale), None if padding is None else int(padding),
+                 _meta(dw), bool(accumulate)),
+        lambda: _embedding_bwd_plan(dy, ids, n_rows, scale, padding, dw, accumulate))
+    _check_outputs("embedding_bwd", (dw,), (dy, ids), workspace)
+    with _Launch(dev, stream, "embedding_bwd") as at:
+        if dw is None:
+            dw = at.empty(shape, dy.dtype)
+        workspace = _workspace(at, workspace, need, "embedding_bwd")
+        rc = load().psr_embedding_bwd(sh, dy.data_ptr(), ids.data_ptr(), dw.data_ptr(), workspace.data_ptr(), need, at.handle)
+    if rc != OK:
+        raise PsrError(rc, "psr_embedding_bwd")
+    return dw, workspace
+
+
+def _embedding_bwd_plan(dy, ids, n_rows, scale, padding, dw, accumulate):
+    _check_cuda(dy, "dy", 2)
+    M, K = dy.shape
+    dev, shape = dy.device, (int(n_rows), K)
+    step = _check_ids(ids, "ids", M, dev)
+    if dw is not None:
+        _check_flat(dw, "dw", shape, dy.dtype, dev)
+    elif accumulate:
+        raise ValueError("embedding_bwd: accumulate adds to dw, which has to be passed in")
+    if padding is not None and not 0 <= int(padding) < shape[0]:
+        raise ValueError(f"embedding_bwd: padding must be an id of the table, got {padding}")
+    sh = EmbeddingShape(M, shape[0], K, _type_of(dy, "dy", F32), step, 0, _row_stride(dy, "dy"),
+                        -1 if padding is None else int(padding), int(bool(accumulate)), float(scale))
+    need = load().psr_embedding_workspace_bytes(sh)
+    if need == 0:
+        raise PsrError(ERR_ARG, "psr_embedding_bwd")
+    return sh, need, dev, shape
 
 
 def get_stats(workspace, stream=None) -> dict:
