@@ -525,6 +525,39 @@ PSR_API size_t psr_embedding_workspace_bytes(const psr_embedding_shape* shape);
 PSR_API int psr_embedding_bwd(const psr_embedding_shape* shape, const void* dy, const int64_t* ids, void* dw, void* workspace,
                               size_t workspace_bytes, void* stream);
 
+/* Softmax cross entropy of the output projection l = x w^T over V columns, without the logits in memory:
+ *     loss_i = lse_i - (1 - smoothing) l_i[t_i] - smoothing mean_j(l_ij) + z_weight lse_i^2,   lse_i = log sum_j exp l_ij,
+ * t_i = targets[i * targets_step].  A row with t_i == ignore has a loss and a lse of 0 and no gradient, whatever its x; one with
+ * another target outside 0 .. V-1 a loss and a lse of NaN and no gradient either.  The logits are products of 16-bit numbers
+ * summed in fp32 on the tensor cores, the sums of exponentials are fp32. */
+typedef struct {
+  int M, V, K;             /* rows (0 .. 2^24), vocabulary (1 .. 2^28), columns of x and w (1 .. 2^20) */
+  int type;                /* PSR_BF16 or PSR_F16 */
+  long long ldx, ldw;      /* row strides in elements; 0: K */
+  long long targets_step;  /* stride of the targets (0: one target for all rows) */
+  long long dloss_step;    /* psr_xent_bwd: stride of dloss (0: one number for all rows) */
+  long long ignore;
+  float smoothing;         /* 0 <= smoothing < 1 */
+  float z_weight;          /* finite, >= 0 */
+  int odd;                 /* PSR_LINEAR_ODD_X, _W: operands that may start off a 16-byte boundary */
+} psr_xent_shape;
+
+/* Bytes of device workspace psr_xent (backward = 0) or psr_xent_bwd (1) needs; 0 if invalid.  It grows by a copy of w where w's
+ * rows do not all start on 16-byte boundaries. */
+PSR_API size_t psr_xent_workspace_bytes(const psr_xent_shape* shape, int backward);
+
+/* x: device, [M][K]; w: device, [V][K]; targets: device (read).  loss, lse: device, fp32, [M] (written).
+ * workspace: device, 256-byte aligned; device waits that time out (timeout_ms, 0: 2 s) are reported by psr_get_stats. */
+PSR_API int psr_xent(const psr_xent_shape* shape, const void* x, const void* w, const int64_t* targets, float* loss, float* lse,
+                     void* workspace, size_t workspace_bytes, int timeout_ms, void* stream);
+
+/* Gradients of sum_i dloss_i loss_i: dx [M][K] and dw [V][K], contiguous, each NULL if not wanted.  dloss: device, fp32; lse: the
+ * forward's; x, w, targets and the shape: as the forward had them.  The slopes with respect to the logits are rounded once to the type
+ * before the products with w and x, which are summed in fp32 and rounded once.  Every element of dx and dw is written. */
+PSR_API int psr_xent_bwd(const psr_xent_shape* shape, const float* dloss, const void* x, const void* w, const int64_t* targets,
+                         const float* lse, void* dx, void* dw, void* workspace, size_t workspace_bytes, int timeout_ms,
+                         void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,6 +24,7 @@ __all__ = ["build", "load", "Shape", "AgShape", "RsShape", "Partition", "Stats",
            "rotary_table", "rotary", "rotary_bwd", "linear", "linear_bwd", "linear_workspace_bytes",
            "kv4_cache", "kv4_append", "kv4_read", "kv4_attn", "kv4_attn_workspace_bytes",
            "embedding", "embedding_bwd", "embedding_workspace_bytes",
+           "linear_xent", "linear_xent_bwd", "linear_xent_workspace_bytes",
            "get_stats", "get_trajectory", "controller_target", "num_ctas", "status_string", "PsrError",
            "STATIC", "ADAPTIVE", "FAULT_NONE", "FAULT_DROP_FIRST_FLAG", "FAULT_SLOW_STAGING", "CAUSAL",
            "CAUSAL_BALANCED"]
@@ -39,7 +40,8 @@ EXPORTED = ("psr_workspace_bytes", "psr_ring_attn_fwd", "psr_ring_attn_fwd_host"
             "psr_gemm_rs", "psr_ring_attn_bwd_workspace_bytes", "psr_ring_attn_bwd",
             "psr_rotary_table", "psr_rotary", "psr_linear_workspace_bytes", "psr_linear", "psr_linear_bwd",
             "psr_kv4_cache_bytes", "psr_kv4_append", "psr_kv4_read", "psr_kv4_attn_workspace_bytes", "psr_kv4_attn",
-            "psr_embedding", "psr_embedding_workspace_bytes", "psr_embedding_bwd")
+            "psr_embedding", "psr_embedding_workspace_bytes", "psr_embedding_bwd",
+            "psr_xent_workspace_bytes", "psr_xent", "psr_xent_bwd")
 
 BF16, F16, F32 = 0, 1, 2
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
@@ -86,6 +88,13 @@ class EmbeddingShape(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int), ("V", ctypes.c_int), ("K", ctypes.c_int), ("type", ctypes.c_int),
                 ("ids_step", ctypes.c_longlong), ("ldw", ctypes.c_longlong), ("ldy", ctypes.c_longlong),
                 ("padding", ctypes.c_longlong), ("accumulate", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class XentShape(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int), ("V", ctypes.c_int), ("K", ctypes.c_int), ("type", ctypes.c_int),
+                ("ldx", ctypes.c_longlong), ("ldw", ctypes.c_longlong), ("targets_step", ctypes.c_longlong),
+                ("dloss_step", ctypes.c_longlong), ("ignore", ctypes.c_longlong), ("smoothing", ctypes.c_float),
+                ("z_weight", ctypes.c_float), ("odd", ctypes.c_int)]
 
 
 class Partition(ctypes.Structure):
@@ -174,7 +183,8 @@ def load(trace: bool = False, variant: str = "") -> ctypes.CDLL:
         lib.psr_ring_attn_fwd_noalloc.restype = ctypes.c_int
         lib.psr_noalloc_get_stats.argtypes = [ctypes.POINTER(Stats), vp]
         lib.psr_noalloc_get_stats.restype = ctypes.c_int
-        P_st, P_rot, P_lin, P_kv4, P_emb = map(ctypes.POINTER, (Strides, RotaryShape, LinearShape, Kv4Shape, EmbeddingShape))
+        P_st, P_rot, P_lin, P_kv4, P_emb, P_xent = map(ctypes.POINTER, (Strides, RotaryShape, LinearShape, Kv4Shape, EmbeddingShape,
+                                                                        XentShape))
         dbl = ctypes.c_double
         lib.psr_rotary_table.argtypes = [ctypes.c_int, dbl, ctypes.c_int, dbl, dbl, dbl, dbl, vp]
         lib.psr_rotary.argtypes = [P_rot, vp, P_st, vp, P_st, vp, P_st, vp, P_st, vp, vp, ctypes.c_longlong, vp]
@@ -189,11 +199,14 @@ def load(trace: bool = False, variant: str = "") -> ctypes.CDLL:
         lib.psr_embedding.argtypes = [P_emb, vp, vp, vp, vp]
         lib.psr_embedding_workspace_bytes.argtypes = [P_emb]
         lib.psr_embedding_bwd.argtypes = [P_emb, vp, vp, vp, vp, sz, vp]
+        lib.psr_xent_workspace_bytes.argtypes = [P_xent, ctypes.c_int]
+        lib.psr_xent.argtypes = [P_xent, vp, vp, vp, vp, vp, vp, sz, ctypes.c_int, vp]
+        lib.psr_xent_bwd.argtypes = [P_xent, vp, vp, vp, vp, vp, vp, vp, vp, sz, ctypes.c_int, vp]
         for name in ("psr_rotary_table", "psr_rotary", "psr_linear", "psr_linear_bwd", "psr_kv4_append", "psr_kv4_read",
-                     "psr_kv4_attn", "psr_embedding", "psr_embedding_bwd"):
+                     "psr_kv4_attn", "psr_embedding", "psr_embedding_bwd", "psr_xent", "psr_xent_bwd"):
             getattr(lib, name).restype = ctypes.c_int
         for name in ("psr_linear_workspace_bytes", "psr_kv4_cache_bytes", "psr_kv4_attn_workspace_bytes",
-                     "psr_embedding_workspace_bytes"):
+                     "psr_embedding_workspace_bytes", "psr_xent_workspace_bytes"):
             getattr(lib, name).restype = sz
         lib.psr_num_ctas.argtypes = []
         lib.psr_num_ctas.restype = ctypes.c_int
@@ -1165,6 +1178,114 @@ def _embedding_bwd_plan(dy, ids, n_rows, scale, padding, dw, accumulate):
     if need == 0:
         raise PsrError(ERR_ARG, "psr_embedding_bwd")
     return sh, need, dev, shape
+
+
+def linear_xent_workspace_bytes(M, V, K, *, smoothing=0.0, backward=False) -> int:
+    """Bytes of workspace that linear_xent() or linear_xent_bwd() needs for contiguous tensors, or views whose row strides are
+    multiples of 8 elements and that start on 16-byte boundaries."""
+    n = load().psr_xent_workspace_bytes(XentShape(int(M), int(V), int(K), BF16, 0, 0, 1, 1, -100, float(smoothing)),
+                                        int(bool(backward)))
+    if n == 0:
+        raise PsrError(ERR_ARG, "psr_xent_workspace_bytes")
+    return int(n)
+
+
+def linear_xent(x, w, targets, *, smoothing=0.0, z_weight=0.0, ignore=-100, loss=None, lse=None, workspace=None, timeout_ms=0,
+                stream=None):
+    """Softmax cross entropy of the output projection, without the logits in memory: with l = x w^T [M, V],
+    loss = lse - (1 - smoothing) l[target] - smoothing mean(l) + z_weight lse^2, lse = log sum exp l.
+
+    x: [M, K], w: [V, K], bf16 or fp16, rows may be strided; targets: int64 [M], any stride.  A row whose target is `ignore` has
+    a loss and a lse of 0, whatever its x; one with another target outside the vocabulary has NaN.
+    Returns (loss [M] fp32, lse [M] fp32, workspace)."""
+    sh, need, dev, M = _plan(
+        lambda: (linear_xent, _meta(x), _meta(w), _meta(targets), float(smoothing), float(z_weight), int(ignore), _meta(loss),
+                 _meta(lse), x.data_ptr() % 16, w.data_ptr() % 16),
+        lambda: _xent_plan(x, w, targets, smoothing, z_weight, ignore, loss, lse))
+    _check_outputs("linear_xent", (loss, lse), (x, w, targets), workspace)
+    with _Launch(dev, stream, "linear_xent") as at:
+        if loss is None:
+            loss = at.empty((M,), at.torch.float32)
+        if lse is None:
+            lse = at.empty((M,), at.torch.float32)
+        workspace = _workspace(at, workspace, need, "linear_xent")
+        if M == 0:
+            _clear_status(at, workspace)
+            return loss, lse, workspace
+        rc = load().psr_xent(sh, x.data_ptr(), w.data_ptr(), targets.data_ptr(), loss.data_ptr(), lse.data_ptr(),
+                             workspace.data_ptr(), need, int(timeout_ms), at.handle)
+    if rc != OK:
+        raise PsrError(rc, "psr_xent")
+    return loss, lse, workspace
+
+
+def _xent_shape(x, w, targets, smoothing, z_weight, ignore, backward, what):
+    _check_cuda(x, "x", 2)
+    _check_cuda(w, "w", 2)
+    code = _type_of(x, "x", F16)
+    M, K = x.shape
+    V, dev = w.shape[0], x.device
+    _check_like(w, "w", (V, K), x.dtype, dev)
+    sh = XentShape(M, V, K, code, _row_stride(x, "x"), _row_stride(w, "w"), _check_ids(targets, "targets", M, dev), 0, int(ignore),
+                   float(smoothing), float(z_weight), (1 if x.data_ptr() % 16 else 0) | (2 if w.data_ptr() % 16 else 0))
+    need = load().psr_xent_workspace_bytes(sh, int(backward))
+    if need == 0:
+        raise PsrError(ERR_ARG, what)
+    return sh, need, dev, M, V, K
+
+
+def _xent_plan(x, w, targets, smoothing, z_weight, ignore, loss, lse):
+    import torch
+    sh, need, dev, M, _, _ = _xent_shape(x, w, targets, smoothing, z_weight, ignore, False, "psr_xent")
+    for t, name in ((loss, "loss"), (lse, "lse")):
+        if t is not None:
+            _check_flat(t, name, (M,), torch.float32, dev)
+    return sh, need, dev, M
+
+
+def linear_xent_bwd(dloss, x, w, targets, lse, *, smoothing=0.0, z_weight=0.0, ignore=-100, need_dx=True, need_dw=True, dx=None,
+                    dw=None, workspace=None, timeout_ms=0, stream=None):
+    """Gradients of linear_xent(): dloss [M] fp32 (any stride: one number expanded to all rows, say) is that of the losses, lse the
+    forward's; the other arguments are the forward's.  Rows without a target of the vocabulary have none.
+    Returns (dx [M, K], dw [V, K], workspace), None for those not asked for; dx, dw may be passed in (contiguous)."""
+    sh, need, dev, shapes = _plan(
+        lambda: (linear_xent_bwd, _meta(dloss), _meta(x), _meta(w), _meta(targets), _meta(lse), float(smoothing), float(z_weight),
+                 int(ignore), _meta(dx), _meta(dw), x.data_ptr() % 16, w.data_ptr() % 16),
+        lambda: _xent_bwd_plan(dloss, x, w, targets, lse, smoothing, z_weight, ignore, dx, dw))
+    _check_outputs("linear_xent_bwd", (dx, dw), (dloss, x, w, targets, lse), workspace)
+    with _Launch(dev, stream, "linear_xent_bwd") as at:
+        if dx is None and need_dx:
+            dx = at.empty(shapes[0], x.dtype)
+        if dw is None and need_dw:
+            dw = at.empty(shapes[1], x.dtype)
+        workspace = _workspace(at, workspace, need, "linear_xent_bwd")
+        if shapes[0][0] == 0 or (dx is None and dw is None):  # sums over no rows, or nothing asked for
+            _clear_status(at, workspace)
+            if dw is not None:
+                with at.torch.cuda.stream(stream):  # None: the current one
+                    dw.zero_()
+            return dx, dw, workspace
+        rc = load().psr_xent_bwd(sh, dloss.data_ptr(), x.data_ptr(), w.data_ptr(), targets.data_ptr(), lse.data_ptr(),
+                                 *(None if t is None else t.data_ptr() for t in (dx, dw)), workspace.data_ptr(), need,
+                                 int(timeout_ms), at.handle)
+    if rc != OK:
+        raise PsrError(rc, "psr_xent_bwd")
+    return dx, dw, workspace
+
+
+def _xent_bwd_plan(dloss, x, w, targets, lse, smoothing, z_weight, ignore, dx, dw):
+    import torch
+    sh, need, dev, M, V, K = _xent_shape(x, w, targets, smoothing, z_weight, ignore, True, "psr_xent_bwd")
+    _check_cuda(dloss, "dloss", 1)
+    _check_like(dloss, "dloss", (M,), torch.float32, dev)
+    sh.dloss_step = dloss.stride(0) if M > 1 else 1
+    _check_cuda(lse, "lse", 1)
+    _check_flat(lse, "lse", (M,), torch.float32, dev)
+    shapes = (M, K), (V, K)
+    for t, name, shape in ((dx, "dx", shapes[0]), (dw, "dw", shapes[1])):
+        if t is not None:
+            _check_flat(t, name, shape, x.dtype, dev)
+    return sh, need, dev, shapes
 
 
 def get_stats(workspace, stream=None) -> dict:

@@ -15,7 +15,7 @@ LIB_PAIRS = os.path.join(HERE, "libpsr_pairs.so")  # same library with CTA-pair 
 VARIANTS = {"": ([], LIB), "trace": (["-DPSR_TRACE=1"], LIB_TRACE), "pairs": (["-DPSR_PAIRS=1"], LIB_PAIRS)}
 SOURCES = [os.path.join(CSRC, f) for f in ("psr_ring_attn.cu", "psr_ring_attn_bwd.cu", "psr_ag_gemm.cu", "psr_gemm_rs.cu",
                                             "psr_noalloc.cu", "psr_rotary.cu", "psr_linear.cu", "psr_kv4.cu",
-                                            "psr_embedding.cu")]
+                                            "psr_embedding.cu", "psr_xent.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f)
                   for f in ("psr_device.cuh", "psr_schedule.h", "psr_control.cuh", "psr_gemm_tile.cuh", "psr_internal.h",
                             "psr_host.h", "psr_linear_mma.cuh")] + [

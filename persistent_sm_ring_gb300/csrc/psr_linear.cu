@@ -14,25 +14,6 @@ namespace psr {
 namespace linear {
 
 // ------------------------------------------------------------------------------------------------
-// An operand with rows of any stride, from any address, into rows on 16-byte boundaries
-// ------------------------------------------------------------------------------------------------
-__global__ void __launch_bounds__(256)
-    align_kernel(const uint16_t* __restrict__ x, long long ld, uint4* __restrict__ y, int rows, int cols, Ctrl* clear) {
-  clear_ctrl(clear);
-  const int per = (cols + 7) / 8;
-  const long long n = (long long)rows * per;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
-    const long long r = i / per;
-    const int c = (int)(i - r * per) * 8;
-    const uint16_t* p = x + r * ld + c;
-    uint32_t e[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = c + j < cols ? p[j] : 0;
-    y[i] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-  }
-}
-
-// ------------------------------------------------------------------------------------------------
 // One row of x, or a few with a small W: dot products on the fp32 units
 // ------------------------------------------------------------------------------------------------
 // Bound by reading W once.  A warp takes a row of W, a lane 16 bytes of it at a time (the warp 512 adjacent bytes), and asks for
@@ -195,19 +176,6 @@ static int launch_of(void* workspace, const Sizes& s, int timeout_ms, void* stre
   return PSR_OK;
 }
 
-// The operand's aligned copy, if it needs one: x and ld then name that.
-static int align(const void*& x, long long& ld, size_t at, int rows, int cols, void* workspace, Launch& l) {
-  if (!at || rows == 0) return PSR_OK;
-  uint4* y = reinterpret_cast<uint4*>(static_cast<uint8_t*>(workspace) + at);
-  const long long blocks = ((long long)rows * ((cols + 7) / 8) + 255) / 256;
-  align_kernel<<<(unsigned)(blocks < l.n_sm * 16 ? blocks : l.n_sm * 16), 256, 0, l.st>>>(static_cast<const uint16_t*>(x), ld, y,
-                                                                                        rows, cols, l.clear);
-  l.clear = nullptr;
-  x = y;
-  ld = (cols + 7ll) / 8 * 8;
-  return launch_status();
-}
-
 // An operand that is not copied starts on a 16-byte boundary.
 static bool placed(const void* x, size_t copy) { return copy || aligned_to(x, 16); }
 
@@ -276,23 +244,8 @@ static int product(const Operands& o, Epilogue e, Launch& l) {
     if (streams(o.M, o.N, o.K)) return launch_stream<BMN>(o, e, l);
   const Split split = split_of(o.M, o.N, o.K);
   constexpr bool kHalfType = std::is_same<T, __half>::value;
-  // Tiles of 256 columns take 9 clocks for each K and tile (a little more with an operand that is MN-major), or as long as
-  // the epilogue, which runs beside the next tile's products, if that is longer.  Tiles of 512 columns take 16 and move less, but
-  // their epilogue has the accumulators to itself: nothing runs beside it.  Rows that do not start on 128-byte boundaries
-  // take the loads half as long again.  Clocks as measured at 16384 x 4096 x 512 (one / two: 48 / 71 us, with gelu, bias, residual and
-  // z 112 / 132), 4096 x 4096 x 4096 (78 / 87, 87 / 107), 1531 x 5000 x 1736 (31 / 28) and, under lasting load, where
-  // the power limit counts what is moved, 8192 x 8192 x 8192 (668 / 639, its dx 672 / 639) and 4100 x 8192 x 4096 (174 / 181).
-  const long long rows = (o.M + 255) / 256, n_pairs = l.n_sm / 2;
   const double more = (e.act > PSR_ACT_RELU ? 3200.0 : 0.0) + (e.z ? 2600.0 : 0.0) + (e.res ? 3200.0 : 0.0) + (e.bias ? 1000.0 : 0.0);
-  const bool ragged = o.lda % 64 || o.ldb % 64;
-  const double k1 = ragged ? 12.8 : 9.0 + 0.3 * (AMN + BMN), k2 = ragged ? 18.4 : 16.0;
-  const long long ones = rows * ((o.N + 255) / 256), tiles = rows * ((o.N + 511) / 512), halves = last_halves(tiles, (int)n_pairs);
-  const double round = std::max(k1 * o.K, 5500.0 + more);  // of 256-column tiles
-  const double one = split.rest ? split.whole / n_pairs * round + k1 * o.K / split.parts + split.clocks + more / 2
-                                : (double)((ones + n_pairs - 1) / n_pairs) * round;
-  const double two = (double)(tiles / n_pairs + (halves || tiles % n_pairs == 0 ? 0 : 1)) * (k2 * o.K + 2 * (4800.0 + more)) +
-                     (halves ? k1 * o.K + 4800.0 + more : 0.0);
-  return launch_pair<AMN, BMN, kHalfType>(o, e, two <= one, split, l);
+  return launch_pair<AMN, BMN, kHalfType>(o, e, wide_tiles<AMN, BMN>(o, more, split, l.n_sm / 2), split, l);
 }
 
 template <class T>

@@ -12,8 +12,11 @@
 //  * stream_gemm: for few rows of A.  The output is computed transposed, W's rows on the 128 tensor memory lanes
 //    and the tokens in the columns, so that W streams through once.  The (tile, K step) units are dealt out
 //    evenly over one CTA per SM; a tile whose K range is split leaves fp32 partials that a second kernel joins.
+//
+// Both come in modes: what becomes of the sums in the linear layer, or in the loss of the output projection.
 #pragma once
 #include <algorithm>
+#include <cfloat>
 #include <mutex>
 #include <type_traits>
 
@@ -39,6 +42,38 @@ struct Epilogue {
   int half;  // fp16 (0: bf16)
   int vec;   // every row and column offset that the tiles use is 16-byte aligned
 };
+
+// Modes.  kLayer: the linear layer's epilogue.  The others serve the loss of the output projection, whose logits are the products of x
+// and W: kStats reduces them to sums of exponentials, kSlope turns them into the loss's slope, kSum sends products of the slope
+// with W into dx (over several pieces of W's rows), kWeight products of the slope with x into dw.
+enum Mode { kLayer, kStats, kSlope, kSum, kWeight };
+
+// What the loss's modes use besides.  In pair_gemm the rows that count are packed, and their number is known on the device alone.
+struct Head {
+  const int* rows;        // rows that count (kWeight: those summed over); null: the host's number
+  const int* index;       // kSum: the row of dx of each
+  // kStats, kSlope: the column of each row's target, of which the first here is col0
+  const int* target;      // (pair_gemm)
+  const int64_t* ids;     // (stream_gemm: the caller's)
+  long long step;
+  int col0;
+  float2* stats;          // kStats: (r, s) of each row's columns in groups of 64 (pair_gemm) or 32: sum exp(l) = s 2^r
+  float* sums;            // the logits' sums in the same order, or null
+  long long group_at, row_at;  // strides of those
+  float* at;              // the targets' logits
+  const float4* coef;     // kSlope, by row: lse log2(e), a, b, c: slope = a p - b - [target] c
+  float* acc;             // kSum: fp32 sums of earlier pieces
+  long long ldacc;
+  int first, last;        // kSum: piece
+  const float* unit;      // kSum, kWeight: what the sums are multiplied by at the end
+};
+constexpr float kLog2e = 1.4426950408889634f;
+
+// sum exp(l) as s 2^r.  Any r would do; these stay finite where a logit is infinite.
+struct ExpSum {
+  float r, s;
+};
+__device__ __forceinline__ float exp_ref(float r, float most) { return fminf(fmaxf(r, most * kLog2e), FLT_MAX); }
 
 // act(z) and act'(z) in fp32, branch-free: expf, erff and tanhf of the CUDA library cost the epilogue 30 to 40 issue
 // slots an element (a 256-column half of a 1024-deep tile then waits on its epilogue).  The exponential and the reciprocal
@@ -128,8 +163,8 @@ __device__ __forceinline__ void unpack16(uint32_t v, int half, float& lo, float&
 }
 
 // One copy of the code for kernels that run their epilogue once: there, fetching instructions is what takes the time.
-__device__ __noinline__ float act_call(int act, float z) { return act_fwd(act, z); }
-__device__ __noinline__ float4 act_call4(int act, float4 z) {  // (side by side: 64 x 1024 x 64 with silu 14.0 to 9 us)
+static __device__ __noinline__ float act_call(int act, float z) { return act_fwd(act, z); }
+static __device__ __noinline__ float4 act_call4(int act, float4 z) {  // (side by side: 64 x 1024 x 64 with silu 14.0 to 9 us)
   auto apply = [&](auto a) {
     constexpr int A = decltype(a)::value;
     return make_float4(act_fwd(A, z.x), act_fwd(A, z.y), act_fwd(A, z.z), act_fwd(A, z.w));
@@ -258,12 +293,18 @@ struct PairParams {
   Ctrl* ctrl;
   Ctrl* clear;            // control block to clear, or null
   unsigned long long timeout_ns;
+  Head h;
 };
 
 struct PairSmem {
   uint64_t full[kSteps], empty[kSteps], acc_full[2], acc_empty[2], drain;
   uint32_t tmem_base;
   volatile uint32_t abort;
+};
+
+// A product's rows, K steps and tiles: the host's, or (rows that count) what the device makes of their number.
+struct Extent {
+  int M, n_k, tiles_m, whole, halves;  // as in PairParams
 };
 
 // What a pair computes next: `n` 256-column halves from column half tn on of tile row tm, K steps k0 .. k0 + n_k.  split: the part
@@ -274,9 +315,9 @@ struct PairItem {
 
 // Tile t -> (row block, column block): groups of `group` tile rows, columns inside a group, rows fastest, so that the
 // tiles in flight at once share few rows of either operand and a group's rows of A stay in L2.
-__device__ __forceinline__ void pair_tile(const PairParams& p, int t, int& tm, int& tn) {
+__device__ __forceinline__ void pair_tile(const PairParams& p, const Extent& x, int t, int& tm, int& tn) {
   const int per = p.group * p.tiles_n, g = t / per, r = t - g * per;
-  const int rows = min(p.group, p.tiles_m - g * p.group);
+  const int rows = min(p.group, x.tiles_m - g * p.group);
   tn = r / rows;
   tm = g * p.group + (r - tn * rows);
 }
@@ -285,31 +326,31 @@ __device__ __forceinline__ void pair_tile(const PairParams& p, int t, int& tm, i
 // half of the pairs would have one, are dealt out as 256-column halves (256 tiles of 512 columns on 76 pairs: three rounds and
 // a half, not four).  Rounds shifted by half a tile between pairs, so that some write while others multiply, were
 // slower: the tile loads leave L2 no room for the outputs (4096^3 with gelu 100 to 118 us).
-__device__ __forceinline__ bool pair_item(const PairParams& p, int pair, int n_pairs, int i, PairItem& it) {
-  const long long n = (long long)p.tiles_m * p.tiles_n, at = pair + (long long)i * n_pairs;
+__device__ __forceinline__ bool pair_item(const PairParams& p, const Extent& x, int pair, int n_pairs, int i, PairItem& it) {
+  const long long n = (long long)x.tiles_m * p.tiles_n, at = pair + (long long)i * n_pairs;
   it.k0 = 0;
-  it.n_k = p.n_k;
+  it.n_k = x.n_k;
   it.split = -1;
   if (!p.wide) {
     it.n = 1;
     int tile = (int)at;
-    if (at >= p.whole) {
-      const long long part = at - p.whole;
-      if (part >= (n - p.whole) * p.splits) return false;
-      tile = p.whole + (int)(part / p.splits);
+    if (at >= x.whole) {
+      const long long part = at - x.whole;
+      if (part >= (n - x.whole) * p.splits) return false;
+      tile = x.whole + (int)(part / p.splits);
       if (p.splits > 1) {
         it.split = (int)part;
         it.k0 = (int)(part % p.splits) * p.split_k;
-        it.n_k = min(p.split_k, p.n_k - it.k0);
+        it.n_k = min(p.split_k, x.n_k - it.k0);
       }
     }
-    pair_tile(p, tile, it.tm, it.tn);
+    pair_tile(p, x, tile, it.tm, it.tn);
     return true;
   }
-  const long long whole = n - p.halves;  // tiles in whole rounds
+  const long long whole = n - x.halves;  // tiles in whole rounds
   const int h = (int)(at - whole);
-  if (h >= 2 * p.halves) return false;
-  pair_tile(p, h < 0 ? (int)at : (int)whole + h / 2, it.tm, it.tn);
+  if (h >= 2 * x.halves) return false;
+  pair_tile(p, x, h < 0 ? (int)at : (int)whole + h / 2, it.tm, it.tn);
   it.tn = 2 * it.tn + (h < 0 ? 0 : h % 2);
   it.n = h < 0 && (it.tn + 1) * 256 < p.N ? 2 : 1;  // the last columns may be one half wide
   return true;
@@ -475,7 +516,196 @@ __device__ __forceinline__ void partial_store(const PairParams& p, int split, ui
   }
 }
 
-template <bool AMN, bool BMN, bool HALF>
+// Tiles of the last round that are dealt out as halves.
+__host__ __device__ inline int last_halves(long long tiles, int pairs) {
+  const long long rest = tiles % pairs;
+  return 2 * rest <= pairs ? (int)rest : 0;
+}
+
+// (Not a changed copy of the parameters: one kept the row count that the host had given.)
+template <int MODE>
+__device__ __forceinline__ Extent extent_of(const PairParams& p, int n_pairs) {
+  Extent x = {p.M, p.n_k, p.tiles_m, p.whole, p.halves};
+  if (MODE == kLayer || !p.h.rows) return x;
+  const int rows = *p.h.rows;
+  if (MODE == kWeight) {
+    x.n_k = (rows + kBK - 1) / kBK;
+    return x;
+  }
+  x.M = rows;
+  x.tiles_m = (rows + 255) / 256;
+  const int tiles = x.tiles_m * p.tiles_n;
+  if (p.wide) x.halves = last_halves(tiles, n_pairs);
+  else x.whole = min(x.whole, tiles);
+  return x;
+}
+
+// What a thread keeps of its row over a half's two blocks.
+struct HeadRow {
+  int target;  // column (kSum: row of dx)
+  float4 coef;
+  ExpSum e;
+  float sum;
+};
+template <int MODE>
+__device__ __forceinline__ void head_row(const PairParams& p, int M, int i, HeadRow& r) {
+  r.target = -1;
+  r.coef = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (i >= M) return;
+  if constexpr (MODE == kStats || MODE == kSlope) r.target = p.h.target[i] - p.h.col0;
+  if constexpr (MODE == kSlope) r.coef = p.h.coef[i];
+  if constexpr (MODE == kSum) r.target = p.h.index[i];
+}
+
+// The block's 32 rows from i0 on, row `lane` in v, to e.y in 16 bits; SPREAD: to the row `to` of each.
+template <bool SPREAD, bool HALF>
+__device__ __forceinline__ void head_out(const Epilogue& e, int to, uint8_t* stage, int i0, int j0, int rows, int cols,
+                                         const uint32_t (&v)[32]) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      w[q] = pack16(__uint_as_float(v[j * 8 + 2 * q]), __uint_as_float(v[j * 8 + 2 * q + 1]), HALF);
+    *stage_chunk(stage, lane, j) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  uint16_t* g = static_cast<uint16_t*>(e.y) + j0;
+  if constexpr (!SPREAD) {
+    g += (long long)i0 * e.ldy;
+    if (e.vec) rows_out(stage, reinterpret_cast<uint8_t*>(g), e.ldy * 2, rows, (cols + 7) / 8);
+    else rows_out_odd(stage, g, e.ldy, rows, cols);
+    return;
+  }
+  __syncwarp();
+  if (e.vec) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = k * 8 + lane / 4, c = lane % 4;
+      const long long row = __shfl_sync(0xffffffffu, to, r);
+      const uint4 w = *stage_chunk(stage, r, c);
+      if (r < rows && c * 8 < cols) *reinterpret_cast<uint4*>(g + row * e.ldy + c * 8) = w;
+    }
+  } else {
+    for (int r = 0; r < rows; ++r) {
+      const long long row = __shfl_sync(0xffffffffu, to, r);
+      if (lane < cols) g[row * e.ldy + lane] = *stage_element(stage, r, lane);
+    }
+  }
+  __syncwarp();
+}
+
+// Block b % 2 of a half: 32 rows x 32 columns of sums at (i0, j0), row `lane` in v.
+template <int MODE, bool HALF>
+__device__ __forceinline__ void head_store(const PairParams& p, int M, uint8_t* stage, int i0, int j0, int b, HeadRow& row,
+                                           uint32_t (&v)[32]) {
+  const int lane = threadIdx.x % 32, i = i0 + lane, cols = min(32, p.N - j0);
+  if constexpr (MODE == kStats) {
+    if (b % 2 == 0) {
+      row.e = {-FLT_MAX, 0.f};
+      row.sum = 0.f;
+    }
+    if (cols > 0) {
+      if (p.h.sums) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (c < cols) row.sum += __uint_as_float(v[c]);
+      }
+      if (cols < 32) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (c >= cols) v[c] = 0xFF800000u;
+      }
+      float m[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) m[c] = __uint_as_float(v[c]);
+#pragma unroll
+      for (int c = 4; c < 32; ++c) m[c % 4] = fmaxf(m[c % 4], __uint_as_float(v[c]));
+      const float ref = exp_ref(row.e.r, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+      float s[4] = {row.e.s * ex2_approx(row.e.r - ref), 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 32; ++c) s[c % 4] += ex2_approx(fmaf(__uint_as_float(v[c]), kLog2e, -ref));
+      row.e = {ref, (s[0] + s[1]) + (s[2] + s[3])};
+      const int at = row.target - j0;
+      const bool here = at >= 0 && at < cols;
+      if (__any_sync(0xffffffffu, here)) {
+        uint32_t l = 0;
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (c == at) l = v[c];
+        if (here) p.h.at[i] = __uint_as_float(l);
+      }
+    }
+    const int group = j0 / 64;
+    if (b % 2 == 1 && i < M && group * 64 < p.N) {
+      const long long to = group * p.h.group_at + i * p.h.row_at;
+      p.h.stats[to] = make_float2(row.e.r, row.e.s);
+      if (p.h.sums) p.h.sums[to] = row.sum;
+    }
+  } else if constexpr (MODE == kSlope) {
+    // zeros for the rows up to the K step of dw's product that the last one is in
+    const int rows = min(32, (M + kBK - 1) / kBK * kBK - i0);
+    if (rows <= 0 || cols <= 0) return;
+    const bool counts = i < M;
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      const float q = ex2_approx(fmaf(__uint_as_float(v[c]), kLog2e, -row.coef.x));
+      v[c] = counts ? __float_as_uint(fmaf(row.coef.y, q, -row.coef.z)) : 0u;
+    }
+    const int at = row.target - j0;
+    if (__any_sync(0xffffffffu, at >= 0 && at < cols)) {
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        if (c == at) v[c] = __float_as_uint(__uint_as_float(v[c]) - row.coef.w);
+    }
+    head_out<false, HALF>(p.e, 0, stage, i0, j0, rows, cols, v);
+  } else {
+    const int rows = min(32, M - i0);
+    if (rows <= 0 || cols <= 0) return;
+    if constexpr (MODE == kSum) {
+      uint8_t* g = reinterpret_cast<uint8_t*>(p.h.acc + (long long)i0 * p.h.ldacc + j0);
+      const long long pitch = p.h.ldacc * 4;
+      if (!p.h.first) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint4 w[4];
+          rows_in(w, g + h * 64, pitch, rows, (cols - 16 * h + 3) / 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) *stage_chunk(stage, k * 8 + lane / 4, lane % 4) = w[k];
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 a = *stage_chunk(stage, lane, j);
+            uint32_t* to = v + 16 * h + 4 * j;
+            to[0] = __float_as_uint(__uint_as_float(to[0]) + __uint_as_float(a.x));
+            to[1] = __float_as_uint(__uint_as_float(to[1]) + __uint_as_float(a.y));
+            to[2] = __float_as_uint(__uint_as_float(to[2]) + __uint_as_float(a.z));
+            to[3] = __float_as_uint(__uint_as_float(to[3]) + __uint_as_float(a.w));
+          }
+          __syncwarp();
+        }
+      }
+      if (!p.h.last) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t* w = v + h * 16 + j * 4;
+            *stage_chunk(stage, lane, j) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          rows_out(stage, g + h * 64, pitch, rows, (cols - 16 * h + 3) / 4);
+        }
+        return;
+      }
+    }
+    const float unit = *p.h.unit;
+#pragma unroll
+    for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * unit);
+    head_out<MODE == kSum, HALF>(p.e, row.target, stage, i0, j0, rows, cols, v);
+  }
+}
+
+template <bool AMN, bool BMN, bool HALF, int MODE = kLayer>
 __global__ void __launch_bounds__(kPairThreads, 1)
     pair_gemm(const __grid_constant__ PairParams p, const __grid_constant__ CUtensorMap ma,
               const __grid_constant__ CUtensorMap mb) {
@@ -519,12 +749,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   tc_fence_after();
 
   const int pair = blockIdx.x / 2, n_pairs = gridDim.x / 2;
+  const Extent x = extent_of<MODE>(p, n_pairs);
   const uint32_t full0 = __shfl_sync(0xffffffffu, mapa_shared(smem_u32(&sc.full[0]), 0), 0);  // of the pair's first CTA
   PairItem it;
   if (warp == 0) {  // the whole warp, for the same reason as the next one
     uint32_t head = 0, tail = 0, chunk = 0, used = 0, wide = 0;  // steps issued and known read, chunks, step sizes
     bool ok = true;
-    for (int i = 0; ok && pair_item(p, pair, n_pairs, i, it); ++i) {
+    for (int i = 0; ok && pair_item(p, x, pair, n_pairs, i, it); ++i) {
       const int arow = it.tm * 256 + (int)rank * kRows, brow = it.tn * 256 + (int)rank * kRows;
       const uint32_t n = 1 + it.n;
       for (int ks = it.k0; ks < it.k0 + it.n_k; ++ks) {
@@ -566,7 +797,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         chunk = chunk + 1 == kChunks ? 0 : chunk + 1;
         return at;
       };
-      for (int i = 0; ok && pair_item(p, pair, n_pairs, i, it); ++i) {
+      for (int i = 0; ok && pair_item(p, x, pair, n_pairs, i, it); ++i) {
         for (int ks = 0; ks < it.n_k && ok; ++ks, ++c) {
           const uint32_t s = c % kSteps;
           ok = __all_sync(0xffffffffu, wait_own(&sc.full[s], (c / kSteps) & 1u, p, &sc, SITE_FULL));
@@ -589,6 +820,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           commit_pair(&sc.empty[s], lane == 0);
         }
         if (!ok) break;
+        if (MODE == kWeight && it.n_k == 0) continue;
         for (int h = 0; h < it.n; ++h) commit_pair(&sc.acc_full[(u + h) % 2], lane == 0);
         u += it.n;
       }
@@ -600,18 +832,27 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint8_t* stage = epi + (warp - 4) * kEpiWarpBytes;
     const int quarter = warp % 4, cgroup = (warp - 4) / 4;  // lanes 32 quarter .., columns 64 cgroup .. of a half
     const Epilogue& e = p.e;
-    const bool res = e.res && e.vec;
+    const bool res = MODE == kLayer && e.res && e.vec;
     uint32_t u = 0;
     bool ok = true;
-    for (int i = 0; ok && pair_item(p, pair, n_pairs, i, it); ++i) {
+    for (int i = 0; ok && pair_item(p, x, pair, n_pairs, i, it); ++i) {
       const int i0 = it.tm * 256 + (int)rank * kRows + quarter * 32;
+      HeadRow row;
+      if constexpr (MODE != kLayer) head_row<MODE>(p, x.M, i0 + lane, row);
+      if (MODE == kWeight && it.n_k == 0) {  // sums over no rows: nothing is multiplied, nothing signalled
+        for (int b = 0; b < 2 * it.n; ++b) {
+          uint32_t v[32] = {};
+          head_store<MODE, HALF>(p, x.M, stage, i0, it.tn * 256 + (b / 2) * 256 + cgroup * 64 + (b % 2) * 32, b, row, v);
+        }
+        continue;
+      }
 #pragma unroll 1
       for (int b = 0; b < 2 * it.n && ok; ++b) {
         const uint32_t slot = u % 2;
         const int j0 = it.tn * 256 + (b / 2) * 256 + cgroup * 64 + (b % 2) * 32;
         uint4 rr[4];
         if (res && it.split < 0)  // in flight while the sums are waited for
-          rows_in(rr, static_cast<const uint8_t*>(e.res) + ((long long)i0 * e.ldr + j0) * 2, e.ldr * 2, p.M - i0, (p.N - j0) / 8);
+          rows_in(rr, static_cast<const uint8_t*>(e.res) + ((long long)i0 * e.ldr + j0) * 2, e.ldr * 2, x.M - i0, (p.N - j0) / 8);
         if (b % 2 == 0) {
           ok = __all_sync(0xffffffffu, wait_own(&sc.acc_full[slot], (u / 2) & 1u, p, &sc, SITE_ACC));
           if (!ok) break;
@@ -630,8 +871,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           ++u;
         }
         if (it.split >= 0)
-          partial_store(p, it.split, stage, (int)rank * kRows + quarter * 32, cgroup * 64 + (b % 2) * 32, p.M - i0, v);
-        else pair_store<!BMN, HALF>(e, p.M, p.N, stage, i0, j0, v, rr);
+          partial_store(p, it.split, stage, (int)rank * kRows + quarter * 32, cgroup * 64 + (b % 2) * 32, x.M - i0, v);
+        else if constexpr (MODE == kLayer) pair_store<!BMN, HALF>(e, x.M, p.N, stage, i0, j0, v, rr);
+        else head_store<MODE, HALF>(p, x.M, stage, i0, j0, b, row, v);
       }
     }
     if (!ok) sc.abort = 1;
@@ -680,6 +922,7 @@ struct StreamParams {
   Ctrl* ctrl;
   Ctrl* clear;
   unsigned long long timeout_ns;
+  Head h;
 };
 
 struct StreamSmem {
@@ -699,7 +942,44 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
-template <bool AMN>
+// The loss's modes: token i, column j (a warp's 32 adjacent ones, some perhaps past the last) and its sum v.
+template <int MODE>
+__device__ __forceinline__ void head_one(const StreamParams& p, int i, int j, float v) {
+  const bool in = j < p.N;
+  if constexpr (MODE == kStats) {
+    const int lane = threadIdx.x % 32;
+    const bool target = in && p.h.ids[i * p.h.step] == (int64_t)j + p.h.col0;
+    if (target) p.h.at[i] = v;
+    float sum = in ? v : 0.f;
+    if (!in) v = -INFINITY;
+    float m = v;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = exp_ref(-FLT_MAX, m);
+    float s = ex2_approx(fmaf(v, kLog2e, -ref));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int group = j / 32;
+    const long long to = group * p.h.group_at + i * p.h.row_at;
+    if (p.h.sums) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0 && in) p.h.sums[to] = sum;
+    }
+    if (lane == 0 && in) p.h.stats[to] = make_float2(ref, s);
+  } else if (in) {
+    if constexpr (MODE == kSlope) {
+      const float4 c = p.h.coef[i];
+      v = fmaf(c.y, ex2_approx(fmaf(v, kLog2e, -c.x)), -c.z);
+      if (p.h.ids[i * p.h.step] == (int64_t)j + p.h.col0) v -= c.w;
+    } else {
+      v *= *p.h.unit;
+    }
+    store16(p.e.y, i * p.e.ldy + j, p.e.half, v);
+  }
+}
+
+template <bool AMN, int MODE = kLayer>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     stream_gemm(const __grid_constant__ StreamParams p, const __grid_constant__ CUtensorMap mw,
                 const __grid_constant__ CUtensorMap mx) {
@@ -835,6 +1115,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             if (e < n_c) part[(c + e) * kRows] = __uint_as_float(v[e]);
           continue;
         }
+        if constexpr (MODE != kLayer) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (e < n_c) head_one<MODE>(p, c + e, j, __uint_as_float(v[e]));
+          continue;
+        }
         // four tokens at a time, their residuals in flight together; each lane reads its own sums back
         float* own = &sc.sums[quarter][0][lane];
 #pragma unroll
@@ -888,6 +1174,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 
 // Joins the partials of the tiles whose K range is split, in the order of the CTAs that hold them: a thread for each
 // output column, a block for each token of a tile.
+template <int MODE = kLayer>
 __global__ void __launch_bounds__(128) stream_join(const __grid_constant__ StreamParams p) {
   const int tile = blockIdx.x;
   const long long b = (long long)tile * p.n_k, e = b + p.n_k;
@@ -901,18 +1188,23 @@ __global__ void __launch_bounds__(128) stream_join(const __grid_constant__ Strea
     const int slot = 2 * g + ((long long)g * p.per_cta >= b ? 0 : 1);  // the tile that CTA g begins or ends with
     sum += p.partial[((long long)slot * p.tb + i) * kRows + threadIdx.x];
   }
-  if (j < p.N) finish(p.e, i, j, sum);
+  if constexpr (MODE != kLayer) head_one<MODE>(p, i, j, sum);
+  else if (j < p.N) finish(p.e, i, j, sum);
 }
 
 // Joins the parts of the split tiles in order: four columns to a thread, 64 blocks to a tile.
+template <int MODE = kLayer>
 __global__ void __launch_bounds__(256) pair_join(const __grid_constant__ PairParams p) {
   const int at = blockIdx.x * 256 + threadIdx.x, row = at / 64, col = at % 64 * 4;
+  if constexpr (MODE != kLayer) wait_previous();
+  const Extent x = extent_of<MODE>(p, 1);
+  if (MODE != kLayer && x.whole + (int)blockIdx.y >= x.tiles_m * p.tiles_n) return;
   int tm, tn;
-  pair_tile(p, p.whole + blockIdx.y, tm, tn);
+  pair_tile(p, x, x.whole + blockIdx.y, tm, tn);
   const long long i = tm * 256ll + row;
   const int j = tn * 256 + col;
-  wait_previous();
-  if (i >= p.M || j >= p.N) return;
+  if constexpr (MODE == kLayer) wait_previous();
+  if (i >= x.M || j >= p.N) return;
   const float* part = p.partial + (long long)blockIdx.y * p.splits * 65536 + row * 256 + col;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -922,6 +1214,28 @@ __global__ void __launch_bounds__(256) pair_join(const __grid_constant__ PairPar
   }
   const Epilogue& e = p.e;
   float f[4] = {sum.x, sum.y, sum.z, sum.w};
+  if constexpr (MODE == kSum) {
+    float* acc = p.h.acc + i * p.h.ldacc + j;
+    if (!p.h.first) {
+      const float4 a = *reinterpret_cast<const float4*>(acc);
+      f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
+    }
+    if (!p.h.last) {
+      *reinterpret_cast<float4*>(acc) = make_float4(f[0], f[1], f[2], f[3]);
+      return;
+    }
+    const float unit = *p.h.unit;
+    const long long to = p.h.index[i] * e.ldy + j;
+    if (e.vec) {
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(e.y) + to) =
+          make_uint2(pack16(f[0] * unit, f[1] * unit, e.half), pack16(f[2] * unit, f[3] * unit, e.half));
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (j + c < p.N) store16(e.y, to + c, e.half, f[c] * unit);
+    }
+    return;
+  }
   if (!e.vec) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
@@ -974,13 +1288,13 @@ inline bool mappable(const void* base, int rows, long long ld) {
 }
 
 // Shared memory and co-resident pairs of one pair_gemm instantiation on the current device; 0 on error.
-template <bool AMN, bool BMN, bool HALF>
+template <bool AMN, bool BMN, bool HALF, int MODE = kLayer>
 inline int pairs_of(int dev, int n_sm) {
   static std::mutex mu;
   static int known[64] = {};
   std::lock_guard<std::mutex> lk(mu);
   if (dev >= 0 && dev < 64 && known[dev]) return known[dev];
-  auto kern = pair_gemm<AMN, BMN, HALF>;
+  auto kern = pair_gemm<AMN, BMN, HALF, MODE>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem) != cudaSuccess) {
     cudaGetLastError();
     return 0;
@@ -1025,12 +1339,6 @@ struct Operands {
   int M, N, K;  // C is [M][N]
 };
 
-// Tiles of the last round that are dealt out as halves.
-inline int last_halves(long long tiles, int pairs) {
-  const long long rest = tiles % pairs;
-  return 2 * rest <= pairs ? (int)rest : 0;
-}
-
 // 256-column tiles that are computed whole, and parts of each of the others along K.
 struct Split {
   long long whole, rest;
@@ -1053,11 +1361,33 @@ inline Split split_of(int M, int N, int K) {
   return {tiles - rest, rest, (int)parts, clocks};
 }
 
-template <bool AMN, bool BMN, bool HALF>
-inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, const Split& split, Launch& l) {
-  const int n_pairs = pairs_of<AMN, BMN, HALF>(l.dev, l.n_sm), cols = wide ? 512 : 256;
+// Whether a product takes tiles of 512 columns.  Tiles of 256 columns take 9 clocks for each K and tile (a little more with an operand
+// that is MN-major), or as long as the epilogue, which runs beside the next tile's products, if that is longer.  Tiles of 512
+// columns take 16 and move less, but their epilogue has the accumulators to itself: nothing runs beside it.  Rows that do not start on
+// 128-byte boundaries take the loads half as long again.  `more`: the epilogue's clocks beyond a plain store.  Clocks as measured at
+// 16384 x 4096 x 512 (one / two: 48 / 71 us, with gelu, bias, residual and z 112 / 132), 4096 x 4096 x 4096 (78 / 87, 87 / 107),
+// 1531 x 5000 x 1736 (31 / 28) and, under lasting load, where the power limit counts what is moved, 8192 x 8192 x 8192 (668 /
+// 639, its dx 672 / 639) and 4100 x 8192 x 4096 (174 / 181).
+template <bool AMN, bool BMN>
+inline bool wide_tiles(const Operands& o, double more, const Split& split, long long n_pairs) {
+  const long long rows = (o.M + 255ll) / 256;
+  const bool ragged = o.lda % 64 || o.ldb % 64;
+  const double k1 = ragged ? 12.8 : 9.0 + 0.3 * (AMN + BMN), k2 = ragged ? 18.4 : 16.0;
+  const long long ones = rows * ((o.N + 255) / 256), tiles = rows * ((o.N + 511) / 512), halves = last_halves(tiles, (int)n_pairs);
+  const double round = std::max(k1 * o.K, 5500.0 + more);  // of 256-column tiles
+  const double one = split.rest ? split.whole / n_pairs * round + k1 * o.K / split.parts + split.clocks + more / 2
+                                : (double)((ones + n_pairs - 1) / n_pairs) * round;
+  const double two = (double)(tiles / n_pairs + (halves || tiles % n_pairs == 0 ? 0 : 1)) * (k2 * o.K + 2 * (4800.0 + more)) +
+                     (halves ? k1 * o.K + 4800.0 + more : 0.0);
+  return two <= one;
+}
+
+template <bool AMN, bool BMN, bool HALF, int MODE = kLayer>
+inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, const Split& split, Launch& l, const Head& head = {}) {
+  const int n_pairs = pairs_of<AMN, BMN, HALF, MODE>(l.dev, l.n_sm), cols = wide ? 512 : 256;
   if (n_pairs < 1) return PSR_ERR_CUDA;
   PairParams p = {};
+  p.h = head;
   p.M = o.M;
   p.N = o.N;
   p.n_k = (o.K + kBK - 1) / kBK;
@@ -1077,7 +1407,7 @@ inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, const Sp
     if ((size_t)split.rest * p.splits * 65536 * 4 > l.partial_bytes) return PSR_ERR_ARG;
     items = split.whole + split.rest * p.splits;
   }
-  p.idesc = idesc16(256, 256, AMN, BMN, HALF);
+  p.idesc = idesc16(256, 256, AMN, BMN, e.half != 0);
   p.e = e;
   p.ctrl = l.ctrl;
   p.clear = l.clear;
@@ -1102,13 +1432,13 @@ inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, const Sp
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, pair_gemm<AMN, BMN, HALF>, p, ma, mb) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, pair_gemm<AMN, BMN, HALF, MODE>, p, ma, mb) != cudaSuccess) {
     cudaGetLastError();
     return PSR_ERR_CUDA;
   }
   l.clear = nullptr;
   if (p.splits == 1) return PSR_OK;
-  return launch_after(pair_join, dim3(64, (unsigned)split.rest), 256, p, l.st);
+  return launch_after(pair_join<MODE>, dim3(64, (unsigned)split.rest), 256, p, l.st);
 }
 
 // Whether stream_gemm takes a product with M rows of A: up to 64, and up to 128 where neither a single step, which leaves the whole
@@ -1125,15 +1455,15 @@ inline size_t partial_bytes(int M, int N, int K, bool weights) {
 }
 
 // o.a: the tokens [M][K], o.b: W, K-major [N][K] or (WMN) [K][N].
-template <bool WMN>
-inline int launch_stream(const Operands& o, const Epilogue& e, Launch& l) {
+template <bool WMN, int MODE = kLayer>
+inline int launch_stream(const Operands& o, const Epilogue& e, Launch& l, const Head& head = {}) {
   const int dev = l.dev, n_sm = l.n_sm;
   static std::mutex mu;
   static bool known[64] = {};
   {
     std::lock_guard<std::mutex> lk(mu);
     if (dev < 0 || dev >= 64 || !known[dev]) {
-      if (cudaFuncSetAttribute(stream_gemm<WMN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem) != cudaSuccess) {
+      if (cudaFuncSetAttribute(stream_gemm<WMN, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem) != cudaSuccess) {
         cudaGetLastError();
         return PSR_ERR_CUDA;
       }
@@ -1141,6 +1471,7 @@ inline int launch_stream(const Operands& o, const Epilogue& e, Launch& l) {
     }
   }
   StreamParams p = {};
+  p.h = head;
   p.M = o.M;
   p.N = o.N;
   p.n_k = (o.K + kSub * kBK - 1) / (kSub * kBK);
@@ -1170,11 +1501,44 @@ inline int launch_stream(const Operands& o, const Epilogue& e, Launch& l) {
   const bool ok_w = WMN ? tmap16(&mw, o.b, o.N, o.K, o.ldb, 64) : tmap16(&mw, o.b, o.K, o.N, o.ldb, kRows);
   if (!ok_w || !tmap16(&mx, o.a, o.K, o.M, o.lda, p.tb)) return PSR_ERR_CUDA;
   const unsigned grid = (unsigned)((units + per - 1) / per);
-  stream_gemm<WMN><<<grid, kStreamThreads, kStreamSmem, l.st>>>(p, mw, mx);
+  stream_gemm<WMN, MODE><<<grid, kStreamThreads, kStreamSmem, l.st>>>(p, mw, mx);
   const int rc = launch_status();
   l.clear = nullptr;
   if (rc != PSR_OK || per % p.n_k == 0) return rc;
-  return launch_after(stream_join, dim3((unsigned)p.n_tiles, (unsigned)o.M), 128, p, l.st);
+  return launch_after(stream_join<MODE>, dim3((unsigned)p.n_tiles, (unsigned)o.M), 128, p, l.st);
+}
+
+// ------------------------------------------------------------------------------------------------
+// An operand with rows of any stride, from any address, into rows on 16-byte boundaries
+// ------------------------------------------------------------------------------------------------
+template <class T>
+__global__ void __launch_bounds__(256)
+    align_kernel(const T* __restrict__ x, long long ld, uint4* __restrict__ y, int rows, int cols, Ctrl* clear) {
+  clear_ctrl(clear);
+  const int per = (cols + 7) / 8;
+  const long long n = (long long)rows * per;
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
+    const long long r = i / per;
+    const int c = (int)(i - r * per) * 8;
+    const T* p = x + r * ld + c;
+    uint32_t e[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = c + j < cols ? p[j] : 0;
+    y[i] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+  }
+}
+
+// The operand's aligned copy, if it needs one: x and ld then name that.
+inline int align(const void*& x, long long& ld, size_t at, int rows, int cols, void* workspace, Launch& l) {
+  if (!at || rows == 0) return PSR_OK;
+  uint4* y = reinterpret_cast<uint4*>(static_cast<uint8_t*>(workspace) + at);
+  const long long blocks = ((long long)rows * ((cols + 7) / 8) + 255) / 256;
+  align_kernel<uint16_t><<<(unsigned)(blocks < l.n_sm * 16 ? blocks : l.n_sm * 16), 256, 0, l.st>>>(static_cast<const uint16_t*>(x), ld, y,
+                                                                                        rows, cols, l.clear);
+  l.clear = nullptr;
+  x = y;
+  ld = (cols + 7ll) / 8 * 8;
+  return launch_status();
 }
 
 }  // namespace linear
