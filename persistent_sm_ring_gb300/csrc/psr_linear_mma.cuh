@@ -57,7 +57,7 @@ struct Head {
   const int64_t* ids;     // (stream_gemm: the caller's)
   long long step;
   int col0;
-  float2* stats;          // kStats: (r, s) of each row's columns in groups of 64 (pair_gemm) or 32: sum exp(l) = s 2^r
+  float2* stats;          // kStats: (r, s) of each row's columns in groups of kGroup (pair_gemm) or 32: sum exp(l) = s 2^r
   float* sums;            // the logits' sums in the same order, or null
   long long group_at, row_at;  // strides of those
   float* at;              // the targets' logits
@@ -264,19 +264,41 @@ __device__ __forceinline__ void cluster_meet() {
   asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 
+// 32 lanes x 32 bits, 16 consecutive columns
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
 // ================================================================================================
 // pair_gemm
 // ================================================================================================
 constexpr int kRows = 128;           // A rows, and B rows of a half, that one CTA loads
 constexpr int kHalf = kRows * kBK * 2;
-constexpr int kEpiWarps = 16;  // four to a scheduler: an epilogue block is a chain of latencies
-constexpr int kPairThreads = (4 + kEpiWarps) * 32;
+// The logits of the loss are summed in parts of at most kPartSteps K steps, which the epilogue adds up: the tensor core's sums of
+// 16 products and what they are added to lose a quarter of the last bit on average, towards zero, so that logits of 4096
+// products came out 3.9e-6 of themselves too small (of 1024, 8e-7), and their log-sum-exp 2.4e-5.  A part of 1024 takes the tensor
+// core ten times as long as the epilogue takes to add it.
+__host__ __device__ constexpr bool in_parts(int mode) { return mode == kStats || mode == kSlope; }
+constexpr int kPartSteps = 16;
+__host__ __device__ constexpr int part_steps(int n_k) {  // of all parts but the last
+  const int parts = (n_k + kPartSteps - 1) / kPartSteps;
+  return (n_k + parts - 1) / parts;
+}
+// Epilogue warps: four to a scheduler, an epilogue block being a chain of latencies; two where a thread keeps the sums of 128
+// columns over the parts (168 registers instead of 96), which gives it independent work enough.
+__host__ __device__ constexpr int epi_warps(int mode) { return in_parts(mode) ? 8 : 16; }
+__host__ __device__ constexpr int pair_threads(int mode) { return (4 + epi_warps(mode)) * 32; }
+constexpr int kGroup = 1024 / epi_warps(kStats);  // columns of a thread
 constexpr int kEpiWarpBytes = 2048;  // one warp's 32 rows x 64 bytes
 // The stages are cut into chunks of one operand tile (16 KiB) each: a K step takes 2 of them (one 256-column half) or 3, so
 // that either way all 192 KiB are in flight (4 steps of 48 KiB would leave one half 128 KiB, which bounds it).
 constexpr int kChunks = 12;
 constexpr int kSteps = 8;  // barriers; more than K steps in flight
-constexpr int kPairSmem = 1024 + kChunks * kHalf + kEpiWarps * kEpiWarpBytes;
+constexpr int kPairSmem = 1024 + kChunks * kHalf + epi_warps(kLayer) * kEpiWarpBytes;
 static_assert(kPairSmem + 1024 <= 232448, "shared memory");
 
 struct PairParams {
@@ -540,7 +562,7 @@ __device__ __forceinline__ Extent extent_of(const PairParams& p, int n_pairs) {
   return x;
 }
 
-// What a thread keeps of its row over a half's two blocks.
+// What a thread keeps of its row over the blocks of its columns.
 struct HeadRow {
   int target;  // column (kSum: row of dx)
   float4 coef;
@@ -595,13 +617,13 @@ __device__ __forceinline__ void head_out(const Epilogue& e, int to, uint8_t* sta
   __syncwarp();
 }
 
-// Block b % 2 of a half: 32 rows x 32 columns of sums at (i0, j0), row `lane` in v.
+// Block b of a warp's columns: 32 rows x 32 columns of sums at (i0, j0), row `lane` in v.
 template <int MODE, bool HALF>
 __device__ __forceinline__ void head_store(const PairParams& p, int M, uint8_t* stage, int i0, int j0, int b, HeadRow& row,
                                            uint32_t (&v)[32]) {
   const int lane = threadIdx.x % 32, i = i0 + lane, cols = min(32, p.N - j0);
   if constexpr (MODE == kStats) {
-    if (b % 2 == 0) {
+    if (b == 0) {
       row.e = {-FLT_MAX, 0.f};
       row.sum = 0.f;
     }
@@ -636,8 +658,8 @@ __device__ __forceinline__ void head_store(const PairParams& p, int M, uint8_t* 
         if (here) p.h.at[i] = __uint_as_float(l);
       }
     }
-    const int group = j0 / 64;
-    if (b % 2 == 1 && i < M && group * 64 < p.N) {
+    const int group = j0 / kGroup;
+    if (b == kGroup / 32 - 1 && i < M && group * kGroup < p.N) {
       const long long to = group * p.h.group_at + i * p.h.row_at;
       p.h.stats[to] = make_float2(row.e.r, row.e.s);
       if (p.h.sums) p.h.sums[to] = row.sum;
@@ -706,7 +728,7 @@ __device__ __forceinline__ void head_store(const PairParams& p, int M, uint8_t* 
 }
 
 template <bool AMN, bool BMN, bool HALF, int MODE = kLayer>
-__global__ void __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(pair_threads(MODE), 1)
     pair_gemm(const __grid_constant__ PairParams p, const __grid_constant__ CUtensorMap ma,
               const __grid_constant__ CUtensorMap mb) {
   extern __shared__ uint8_t smem_raw[];
@@ -731,7 +753,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sc.acc_full[b], 1);
-      mbar_init(&sc.acc_empty[b], 2 * kEpiWarps);
+      mbar_init(&sc.acc_empty[b], 2 * epi_warps(MODE));
     }
     mbar_init(&sc.drain, 1);
     sc.abort = 0;
@@ -798,31 +820,51 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         return at;
       };
       for (int i = 0; ok && pair_item(p, x, pair, n_pairs, i, it); ++i) {
-        for (int ks = 0; ks < it.n_k && ok; ++ks, ++c) {
-          const uint32_t s = c % kSteps;
-          ok = __all_sync(0xffffffffu, wait_own(&sc.full[s], (c / kSteps) & 1u, p, &sc, SITE_FULL));
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t a = a0 + next();
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (h >= it.n) break;
-            const uint32_t slot = (u + h) % 2, b = b0 + next();
-            if (ks == 0) {  // the half's previous sums have been read back
-              if (u + h >= 2)
-                ok = __all_sync(0xffffffffu, wait_own<true>(&sc.acc_empty[slot], ((u + h) / 2 - 1) & 1u, p, &sc, SITE_ACC_EMPTY));
+        if constexpr (in_parts(MODE)) {  // tiles of 256 columns, a part to an accumulator
+          const int steps = part_steps(it.n_k);
+          for (int k0 = 0; k0 < it.n_k && ok; k0 += steps, ++u) {
+            const uint32_t slot = u % 2;
+            if (u >= 2) ok = __all_sync(0xffffffffu, wait_own<true>(&sc.acc_empty[slot], (u / 2 - 1) & 1u, p, &sc, SITE_ACC_EMPTY));
+            if (!ok) break;
+            tc_fence_after();
+            for (int ks = k0; ks < min(it.n_k, k0 + steps); ++ks, ++c) {
+              const uint32_t s = c % kSteps;
+              ok = __all_sync(0xffffffffu, wait_own(&sc.full[s], (c / kSteps) & 1u, p, &sc, SITE_FULL));
               if (!ok) break;
               tc_fence_after();
+              const uint32_t a = a0 + next(), b = b0 + next();
+              mma_step<true, AMN, BMN>(tmem + slot * 256, a, b, p.idesc, ks > k0, lane == 0);
+              commit_pair(&sc.empty[s], lane == 0);
             }
-            mma_step<true, AMN, BMN>(tmem + slot * 256, a, b, p.idesc, ks > 0, lane == 0);
+            if (ok) commit_pair(&sc.acc_full[slot], lane == 0);
+          }
+        } else {
+          for (int ks = 0; ks < it.n_k && ok; ++ks, ++c) {
+            const uint32_t s = c % kSteps;
+            ok = __all_sync(0xffffffffu, wait_own(&sc.full[s], (c / kSteps) & 1u, p, &sc, SITE_FULL));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t a = a0 + next();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (h >= it.n) break;
+              const uint32_t slot = (u + h) % 2, b = b0 + next();
+              if (ks == 0) {  // the half's previous sums have been read back
+                if (u + h >= 2)
+                  ok = __all_sync(0xffffffffu, wait_own<true>(&sc.acc_empty[slot], ((u + h) / 2 - 1) & 1u, p, &sc, SITE_ACC_EMPTY));
+                if (!ok) break;
+                tc_fence_after();
+              }
+              mma_step<true, AMN, BMN>(tmem + slot * 256, a, b, p.idesc, ks > 0, lane == 0);
+            }
+            if (!ok) break;
+            commit_pair(&sc.empty[s], lane == 0);
           }
           if (!ok) break;
-          commit_pair(&sc.empty[s], lane == 0);
+          if (MODE == kWeight && it.n_k == 0) continue;
+          for (int h = 0; h < it.n; ++h) commit_pair(&sc.acc_full[(u + h) % 2], lane == 0);
+          u += it.n;
         }
-        if (!ok) break;
-        if (MODE == kWeight && it.n_k == 0) continue;
-        for (int h = 0; h < it.n; ++h) commit_pair(&sc.acc_full[(u + h) % 2], lane == 0);
-        u += it.n;
       }
       for (uint32_t h = u > 2 ? u - 2 : 0; ok && h < u; ++h)  // the other CTA's last arrivals have come
         ok = __all_sync(0xffffffffu, wait_own<true>(&sc.acc_empty[h % 2], (h / 2) & 1u, p, &sc, SITE_ACC_EMPTY));
@@ -842,8 +884,45 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       if (MODE == kWeight && it.n_k == 0) {  // sums over no rows: nothing is multiplied, nothing signalled
         for (int b = 0; b < 2 * it.n; ++b) {
           uint32_t v[32] = {};
-          head_store<MODE, HALF>(p, x.M, stage, i0, it.tn * 256 + (b / 2) * 256 + cgroup * 64 + (b % 2) * 32, b, row, v);
+          head_store<MODE, HALF>(p, x.M, stage, i0, it.tn * 256 + (b / 2) * 256 + cgroup * 64 + (b % 2) * 32, 0, row, v);
         }
+        continue;
+      }
+      if constexpr (in_parts(MODE)) {
+        uint32_t sum[kGroup / 32][32];
+        for (int k0 = 0; k0 < p.n_k; k0 += part_steps(p.n_k), ++u) {
+          ok = __all_sync(0xffffffffu, wait_own(&sc.acc_full[u % 2], (u / 2) & 1u, p, &sc, SITE_ACC));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t from = sc.tmem_base + ((uint32_t)(quarter * 32) << 16) + u % 2 * 256 + cgroup * kGroup;
+          if (k0 == 0) {
+#pragma unroll
+            for (int q = 0; q < kGroup / 32; ++q) tmem_ld32(from + q * 32, sum[q]);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int q = 0; q < kGroup / 16; ++q) {
+              uint32_t v[16];
+              tmem_ld16(from + q * 16, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                uint32_t& to = sum[q / 2][q % 2 * 16 + c];
+                to = __float_as_uint(__uint_as_float(to) + __uint_as_float(v[c]));
+              }
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (rank == 0) mbar_arrive(&sc.acc_empty[u % 2]);
+            else arrive_far(mapa_shared(smem_u32(&sc.acc_empty[u % 2]), 0));
+          }
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int q = 0; q < kGroup / 32; ++q)
+          head_store<MODE, HALF>(p, x.M, stage, i0, it.tn * 256 + cgroup * kGroup + q * 32, q, row, sum[q]);
         continue;
       }
 #pragma unroll 1
@@ -873,7 +952,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (it.split >= 0)
           partial_store(p, it.split, stage, (int)rank * kRows + quarter * 32, cgroup * 64 + (b % 2) * 32, x.M - i0, v);
         else if constexpr (MODE == kLayer) pair_store<!BMN, HALF>(e, x.M, p.N, stage, i0, j0, v, rr);
-        else head_store<MODE, HALF>(p, x.M, stage, i0, j0, b, row, v);
+        else head_store<MODE, HALF>(p, x.M, stage, i0, j0, 0, row, v);
       }
     }
     if (!ok) sc.abort = 1;
@@ -916,6 +995,7 @@ struct StreamParams {
   int per_cta;     // units (tile, K step) of a CTA, in order
   int stages;
   uint32_t tmem_cols;
+  uint32_t accs;   // accumulators of a tile, which take the K steps in turn (the loss's logits: four, see kPartSteps)
   uint32_t idesc;
   float* partial;  // [2 gridDim.x][tb][128]
   Epilogue e;
@@ -932,15 +1012,6 @@ struct StreamSmem {
   float sums[4][16][32];  // epilogue warp, token, lane
 };
 static_assert(kStreamSmem + sizeof(StreamSmem) <= 232448, "shared memory");
-
-// 32 lanes x 32 bits, 16 consecutive columns
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
 
 // The loss's modes: token i, column j (a warp's 32 adjacent ones, some perhaps past the last) and its sum v.
 template <int MODE>
@@ -1073,8 +1144,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         const uint32_t at = s * (stage_bytes / 16);
 #pragma unroll
         for (int h = 0; h < kSub; ++h)
-          mma_step<false, AMN, false>(tmem + slot * p.tb, a0 + at + h * (kHalf / 16), b0 + at + h * (x_bytes / 16), p.idesc,
-                                      ks > 0 || h > 0, lane == 0);
+          mma_step<false, AMN, false>(in_parts(MODE) ? tmem + (slot * p.accs + ks % p.accs) * p.tb : tmem + slot * p.tb,
+                                      a0 + at + h * (kHalf / 16), b0 + at + h * (x_bytes / 16), p.idesc,
+                                      (in_parts(MODE) ? ks >= (int)p.accs : ks > 0) || h > 0, lane == 0);
         commit_one(&sc.empty[s], lane == 0);
         if (++s == n_st) {
           s = 0;
@@ -1101,13 +1173,22 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       const bool whole = n == p.n_k;
       const float bias = whole && p.e.bias && j < p.N ? load16(p.e.bias, j, p.e.half) : 0.f;
       float* part = p.partial + (2ll * blockIdx.x + (u == u0 ? 0 : 1)) * p.tb * kRows + row;
-      const uint32_t tacc = sc.tmem_base + ((uint32_t)(quarter * 32) << 16) + slot * p.tb;
+      const uint32_t tacc = sc.tmem_base + ((uint32_t)(quarter * 32) << 16) + slot * p.tb * (in_parts(MODE) ? p.accs : 1);
 #pragma unroll 1
       for (int c = 0; c < p.M; c += 16) {
         uint32_t v[16];
         __syncwarp();  // the load is the whole warp's: no lane is still in the last tokens' epilogue
         tmem_ld16(tacc + c, v);
         tmem_ld_wait();
+        if constexpr (in_parts(MODE)) {
+          for (uint32_t a = 1; a < p.accs && (int)a < n; ++a) {
+            uint32_t w[16];
+            tmem_ld16(tacc + a * p.tb + c, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(w[e]));
+          }
+        }
         const int n_c = min(16, p.M - c);
         if (!whole) {
 #pragma unroll
@@ -1301,7 +1382,7 @@ inline int pairs_of(int dev, int n_sm) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(n_sm / 2 * 2));
-  cfg.blockDim = dim3(kPairThreads);
+  cfg.blockDim = dim3(pair_threads(MODE));
   cfg.dynamicSmemBytes = kPairSmem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1422,7 +1503,7 @@ inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, const Sp
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * (items < n_pairs ? items : n_pairs)));
-  cfg.blockDim = dim3(kPairThreads);
+  cfg.blockDim = dim3(pair_threads(MODE));
   cfg.dynamicSmemBytes = kPairSmem;
   cfg.stream = l.st;
   cudaLaunchAttribute attr[1];
@@ -1489,8 +1570,9 @@ inline int launch_stream(const Operands& o, const Epilogue& e, Launch& l, const 
   p.per_cta = (int)per;
   const int stage = kSub * (kHalf + p.tb * kBK * 2);
   p.stages = kStreamArea / stage < kStreamMaxStages ? kStreamArea / stage : kStreamMaxStages;
+  p.accs = in_parts(MODE) ? 4 : 1;  // (of at most 64 columns)
   p.tmem_cols = 32;
-  while (p.tmem_cols < 2u * p.tb) p.tmem_cols *= 2;
+  while (p.tmem_cols < 2u * p.tb * p.accs) p.tmem_cols *= 2;
   p.idesc = idesc16(128, p.tb, WMN, false, e.half != 0);
   p.partial = l.partial;
   p.e = e;

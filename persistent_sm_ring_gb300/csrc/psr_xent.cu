@@ -4,7 +4,7 @@
 //   loss_i = lse_i - (1 - s) l_i[t_i] - s mean(l_i) + z lse_i^2,   lse_i = log sum_j exp l_ij
 //   slope  d_ij = g_i (p_ij (1 + 2 z lse_i) - s/V - (1 - s) [j = t_i]),  p = exp(l - lse),   dx = d w,  dw = d^T x
 //
-// Forward: the logits' product reduces its sums to (r, s), sum exp(l) = s 2^r, for every 64 columns; a second kernel joins
+// Forward: the logits' product reduces its sums to (r, s), sum exp(l) = s 2^r, for every kGroup columns; a second kernel joins
 // them.  Backward: by pieces of the vocabulary, the logits again, turned into slopes of 16 bits on their way out of
 // tensor memory; dw's rows of the piece; and the piece's share of dx, summed in fp32 over the pieces.
 //
@@ -370,7 +370,7 @@ static int sizes(const psr_xent_shape* sh, bool backward, Sizes& s) {
   const long long M = sh->M, V = sh->V, K = sh->K, Mk = (M + kBK - 1) / kBK * kBK;
   s.few = M <= kFew;
   s.dot = !backward && M == 1 && !odd_x && !odd_w && K % 8 == 0;
-  s.ldxc = (K + 7) / 8 * 8;
+  s.ldxc = (K + 63) / 64 * 64;  // (rows on 128-byte boundaries: the tile loads take half as long again from others)
   size_t off = 256;
   auto take = [&](bool want, long long bytes) {
     const size_t at = off;
@@ -383,7 +383,7 @@ static int sizes(const psr_xent_shape* sh, bool backward, Sizes& s) {
   s.target = take(!s.few, M * 4);
   s.coef = take(backward, M * 16);
   s.at = take(!backward, M * 4);
-  s.groups = s.dot ? 2 * kStreamCtas : (int)(s.few ? (V + 31) / 32 : (V + 63) / 64);
+  s.groups = s.dot ? 2 * kStreamCtas : (int)(s.few ? (V + 31) / 32 : (V + kGroup - 1) / kGroup);
   s.stats = take(!backward, M * s.groups * 8);
   s.logit_sums = take(!backward && sh->smoothing > 0.f, M * s.groups * 4);
   // packed rows, or (up to kFew rows) those that count beside zeros; the products of a forward pass of few rows read x itself
@@ -404,9 +404,9 @@ static int sizes(const psr_xent_shape* sh, bool backward, Sizes& s) {
     } else {
       s.sums_bytes = std::max(s.sums_bytes, partial_bytes((int)M, (int)K, (int)V, false));
     }
-    s.ldd = (s.piece + 7ll) / 8 * 8;
+    s.ldd = (s.piece + 63ll) / 64 * 64;
     s.slope = take(true, Mk * s.ldd * 2);
-    s.ldacc = s.ldxc;
+    s.ldacc = (K + 7) / 8 * 8;
     s.acc = take(s.pieces > 1, M * s.ldacc * 4);
   }
   s.partial = take(true, (long long)s.sums_bytes);
@@ -499,7 +499,7 @@ static int forward(const psr_xent_shape* sh, const Sizes& s, const void* x, cons
     h.target = p.target;
     const Operands o = {p.xc, p.ldxc, w, ldw, sh->M, sh->V, sh->K};
     const Split whole = {((sh->M + 255ll) / 256) * ((sh->V + 255ll) / 256), 0, 1, 0.0};
-    rc = launch_pair<false, false, false, kStats>(o, e, wide_tiles<false, false>(o, 0.0, whole, l.n_sm / 2), whole, l, h);
+    rc = launch_pair<false, false, false, kStats>(o, e, false, whole, l, h);
   }
   if (rc != PSR_OK) return rc;
   f.stats = h.stats;
@@ -560,7 +560,7 @@ static int backward(const psr_xent_shape* sh, const Sizes& s, const float* dloss
     const Operands logits = {p.xc, p.ldxc, wp, ldw, M, n, K};
     const Split whole = {((M + 255ll) / 256) * ((n + 255ll) / 256), 0, 1, 0.0};
     if (s.few) rc = launch_stream<false, kSlope>(logits, e, l, h);
-    else rc = launch_pair<false, false, HALF, kSlope>(logits, e, wide_tiles<false, false>(logits, 1000.0, whole, l.n_sm / 2), whole, l, h);
+    else rc = launch_pair<false, false, HALF, kSlope>(logits, e, false, whole, l, h);
     if (rc != PSR_OK) return rc;
     e.ldy = K;
     if (dw) {
