@@ -5,6 +5,7 @@
 // blocks is joined from fp32 partials in order.  No result depends on the order in which blocks run.
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 #include <type_traits>
 
 #include "psr_control.cuh"
@@ -17,6 +18,35 @@ namespace embedding {
 // E adjacent elements of a row
 template <class T, int E>
 struct alignas(sizeof(T) * E) Vec { T v[E]; };
+
+// The same as words, two elements of 16 bits to each.
+template <class T, int E>
+using Raw = std::conditional_t<sizeof(T) * E % 4 == 0, Vec<uint32_t, (sizeof(T) * E + 3) / 4>, Vec<uint16_t, 1>>;
+template <class T, int E>
+__device__ __forceinline__ void add_to(float* acc, const Raw<T, E>& x) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] += __uint_as_float(x.v[e]);
+  } else if constexpr (E == 1) {
+    T v;
+    memcpy(&v, &x.v[0], 2);
+    acc[0] += to_f32(v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      if constexpr (std::is_same<T, __half>::value) {
+        __half2 h;
+        memcpy(&h, &x.v[e], 4);
+        const float2 f = __half22float2(h);
+        acc[2 * e] += f.x;
+        acc[2 * e + 1] += f.y;
+      } else {
+        acc[2 * e] += __uint_as_float(x.v[e] << 16);
+        acc[2 * e + 1] += __uint_as_float(x.v[e] & 0xFFFF0000u);
+      }
+    }
+  }
+}
 
 // ------------------------------------------------------------------------------------------------
 // Lookup
@@ -53,102 +83,87 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------------------------------------------
-// Sort of the tokens by id, and zeros for the rows that no token names
+// Sort of the tokens by id
 // ------------------------------------------------------------------------------------------------
 // A cluster of CTAs sorts (id, position) pairs by up to nine bits a pass, least significant first.  Each warp has a
 // contiguous share of the pairs and counts its digits; the counts before it (of smaller digits, of earlier CTAs and warps) are
 // where its pairs go, equal digits in their order.  Ids outside the table, and the padding id, become V: they end up behind all
-// others.  The grid's other clusters meanwhile write the zeros, each CTA those of its own range of the table, for
-// which it marks the ids that occur.
+// others.
 constexpr int kSortCtas = 8, kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortBits = 9, kBins = 1 << kSortBits;
-constexpr int kMarks = 32768;  // table rows that a CTA marks at a time
 
-struct SortParams {
+struct Tokens {
   const int64_t* ids;
   long long step;
   long long padding;  // an id without gradient (negative: none)
   int M, V;
+};
+
+struct SortParams {
+  Tokens t;
   uint2* a;        // the sorted pairs (key, position)
   uint2* b;        // space for them between passes
+  int* n_long;     // set to zero for the sums
   int passes, bits;
-  uint8_t* dw;     // rows to clear, or null
-  long long row_bytes;
   Ctrl* clear;
 };
 
 struct SortSmem {
   uint32_t hist[kSortWarps][kBins];
   uint32_t total[kBins];  // of this CTA, by digit; read by the others
+  uint32_t base[kBins];
   uint32_t warp_sum[kSortWarps];
 };
 
-__device__ __forceinline__ uint32_t key_of(const SortParams& p, long long i) {
-  const long long id = p.ids[i * p.step];
-  return id >= 0 && id < p.V && id != p.padding ? (uint32_t)id : (uint32_t)p.V;
-}
-
-// `n` bytes of zeros (an even number, from an even address) by a warp.
-__device__ __forceinline__ void zero_bytes(uint8_t* at, long long n) {
-  const int lane = threadIdx.x % 32;
-  long long head = (16 - (long long)(reinterpret_cast<uintptr_t>(at) % 16)) % 16;
-  if (head > n) head = n;
-  if (2 * lane < head) *reinterpret_cast<uint16_t*>(at + 2 * lane) = 0;
-  const long long body = (n - head) / 16, tail = n - head - body * 16;
-  uint4* v = reinterpret_cast<uint4*>(at + head);
-  for (long long i = lane; i < body; i += 32) v[i] = make_uint4(0, 0, 0, 0);
-  if (2 * lane < tail) *reinterpret_cast<uint16_t*>(at + n - tail + 2 * lane) = 0;
-}
-
-__device__ void zero_rows(const SortParams& p, uint32_t* marks) {
-  const int n_cta = gridDim.x - kSortCtas, cta = blockIdx.x - kSortCtas;
-  const long long per = ((long long)p.V + n_cta - 1) / n_cta;
-  const long long end = min((long long)p.V, (cta + 1) * per);
-  for (long long v0 = cta * per; v0 < end; v0 += kMarks) {
-    const int n = (int)min((long long)kMarks, end - v0);
-    for (int i = threadIdx.x; i < (n + 31) / 32; i += kSortThreads) marks[i] = 0;
-    __syncthreads();
-    for (long long i = threadIdx.x; i < p.M; i += kSortThreads) {
-      const long long r = (long long)key_of(p, i) - v0;
-      if (r >= 0 && r < n) atomicOr(&marks[r / 32], 1u << (r % 32));
-    }
-    __syncthreads();
-    for (int r = threadIdx.x / 32; r < n; r += kSortWarps)
-      if (!(marks[r / 32] >> (r % 32) & 1u)) zero_bytes(p.dw + (v0 + r) * p.row_bytes, p.row_bytes);
-    __syncthreads();
-  }
+__device__ __forceinline__ uint32_t key_of(const Tokens& t, long long i) {
+  const long long id = t.ids[i * t.step];
+  return id >= 0 && id < t.V && id != t.padding ? (uint32_t)id : (uint32_t)t.V;
 }
 
 __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_constant__ SortParams p) {
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   SortSmem& sm = *reinterpret_cast<SortSmem*>(smem_raw);
   clear_ctrl(p.clear);
-  if (blockIdx.x >= kSortCtas) {
-    zero_rows(p, &sm.hist[0][0]);
-    return;
-  }
+  launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.n_long = 0;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_ctarank();
-  const long long share = (((long long)p.M + kSortCtas * kSortWarps - 1) / (kSortCtas * kSortWarps) + 31) / 32 * 32;
+  const long long share = (((long long)p.t.M + kSortCtas * kSortWarps - 1) / (kSortCtas * kSortWarps) + 31) / 32 * 32;
   const long long i0 = ((long long)rank * kSortWarps + warp) * share;
-  const long long i1 = min((long long)p.M, i0 + share);
+  const long long i1 = min((long long)p.t.M, i0 + share);
   const uint32_t bins = 1u << p.bits;
+  constexpr int kRounds = 4;  // pairs of a lane in flight
   for (int pass = 0; pass < p.passes; ++pass) {
     const uint2* src = (p.passes - pass) % 2 ? p.b : p.a;  // the last pass writes a
     uint2* dst = (p.passes - pass) % 2 ? p.a : p.b;
     const int shift = pass * p.bits;
-    auto pair = [&](long long i) { return pass == 0 ? make_uint2(key_of(p, i), (uint32_t)i) : src[i]; };
     for (uint32_t d = lane; d < bins; d += 32) sm.hist[warp][d] = 0;
     __syncwarp();
-    for (long long i = i0; i < i1; i += 32) {  // (whole warps: a warp's last lanes may have no pair)
-      const bool in = i + lane < i1;
-      const uint32_t d = in ? pair(i + lane).x >> shift & (bins - 1) : bins;
+    // calls f(whether there is a pair, the pair, its digit) for the warp's pairs, 32 at a time in order
+    auto each = [&](auto f) {
+      for (long long i = i0; i < i1; i += 32 * kRounds) {
+        uint2 x[kRounds];
+#pragma unroll
+        for (int j = 0; j < kRounds; ++j) {
+          const long long at = i + 32 * j + lane;
+          x[j] = make_uint2(0, 0);
+          if (at < i1) x[j] = pass == 0 ? make_uint2(key_of(p.t, at), (uint32_t)at) : src[at];
+        }
+#pragma unroll
+        for (int j = 0; j < kRounds; ++j) {
+          const bool in = i + 32 * j + lane < i1;
+          f(in, x[j], in ? x[j].x >> shift & (bins - 1) : bins);
+        }
+      }
+    };
+    each([&](bool in, uint2, uint32_t d) {
       const uint32_t same = __match_any_sync(0xffffffffu, d);
       if (in && lane == __ffs(same) - 1) sm.hist[warp][d] += __popc(same);
       __syncwarp();
-    }
+    });
     __syncthreads();
     uint32_t total = 0;
     if (threadIdx.x < bins) {
+#pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
         const uint32_t n = sm.hist[w][threadIdx.x];
         sm.hist[w][threadIdx.x] = total;
@@ -160,6 +175,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
     // pairs with smaller digits, and those with this one in earlier CTAs
     uint32_t all = 0, before = 0;
     if (threadIdx.x < bins) {
+#pragma unroll
       for (uint32_t c = 0; c < (uint32_t)kSortCtas; ++c) {
         const uint32_t n = ld_shared_cluster(mapa_shared(smem_u32(&sm.total[threadIdx.x]), c));
         if (c < rank) before += n;
@@ -176,35 +192,92 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
     __syncthreads();
     if (threadIdx.x < bins) {
       uint32_t base = sum - all + before;
-      for (int w = 0; w < warp; ++w) base += sm.warp_sum[w];
-      for (int w = 0; w < kSortWarps; ++w) sm.hist[w][threadIdx.x] += base;
+#pragma unroll
+      for (int w = 0; w < kBins / 32; ++w)
+        if (w < warp) base += sm.warp_sum[w];
+      sm.base[threadIdx.x] = base;
     }
     __syncthreads();
-    for (long long i = i0; i < i1; i += 32) {
-      const bool in = i + lane < i1;
-      uint2 x = make_uint2(0, 0);
-      if (in) x = pair(i + lane);
-      const uint32_t d = in ? x.x >> shift & (bins - 1) : bins;
+    each([&](bool in, uint2 x, uint32_t d) {
       const uint32_t same = __match_any_sync(0xffffffffu, d);
       uint32_t at = 0;
-      if (in) at = sm.hist[warp][d] + __popc(same & ((1u << lane) - 1));
+      if (in) at = sm.base[d] + sm.hist[warp][d] + __popc(same & ((1u << lane) - 1));
       __syncwarp();
       if (in) {
         dst[at] = x;
         if (lane == __ffs(same) - 1) sm.hist[warp][d] += __popc(same);
       }
       __syncwarp();
-    }
+    });
     cluster_sync();  // the next pass, or the CTAs' ends: all pairs are in place, all totals read
   }
 }
 
 // ------------------------------------------------------------------------------------------------
+// Zeros for the rows that no token names
+// ------------------------------------------------------------------------------------------------
+// Memory alone takes 4.0 to 4.5 TB/s of writes (a fill of 1 GiB 268 us), where it reads and writes 6.8 in all: one CTA to an SM
+// writes the zeros by bulk copies of its own, beside the sort and the sums.  It marks the ids among its rows first.  Each has every
+// n-th 32 rows, so that what all write at a time lies together.
+constexpr int kZeroBytes = 8192;  // what one copy of zeros writes
+constexpr int kMarks = 32768;     // rows that a CTA marks at a time
+struct ZeroSmem {
+  uint4 zeros[kZeroBytes / 16];
+  uint32_t marks[kMarks / 32];
+};
+
+// `n` bytes of zeros (an even number, from an even address) by a warp; odd ends by hand.
+__device__ __forceinline__ void zero_bytes(uint8_t* at, long long n, uint32_t zeros) {
+  const int lane = threadIdx.x % 32;
+  long long head = (16 - (long long)(reinterpret_cast<uintptr_t>(at) % 16)) % 16;
+  if (head > n) head = n;
+  if (2 * lane < head) *reinterpret_cast<uint16_t*>(at + 2 * lane) = 0;
+  const long long body = (n - head) / 16 * 16, tail = n - head - body;
+  for (long long i = lane * (long long)kZeroBytes; i < body; i += 32ll * kZeroBytes)
+    bulk_store(at + head + i, zeros, (uint32_t)min((long long)kZeroBytes, body - i));
+  if (2 * lane < tail) *reinterpret_cast<uint16_t*>(at + n - tail + 2 * lane) = 0;
+}
+
+__device__ void zero_rows(const Tokens& t, uint8_t* dw, long long row_bytes, uint32_t cta, uint32_t n_cta, ZeroSmem& sm) {
+  const uint32_t words = ((uint32_t)t.V + 31) / 32, own = cta < words ? (words - cta + n_cta - 1) / n_cta : 0;
+  const uint32_t zeros = smem_u32(sm.zeros);
+  for (int i = threadIdx.x; i < kZeroBytes / 16; i += 256) sm.zeros[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  for (uint32_t w0 = 0; w0 < own; w0 += kMarks / 32) {
+    const uint32_t n = min(own - w0, (uint32_t)kMarks / 32);
+    for (uint32_t i = threadIdx.x; i < n; i += 256) sm.marks[i] = 0;
+    __syncthreads();
+#pragma unroll 8
+    for (long long i = threadIdx.x; i < t.M; i += 256) {
+      const uint32_t id = key_of(t, i), q = id / 32 / n_cta, w = q - w0, bit = 1u << (id % 32);
+      if (id / 32 - q * n_cta == cta && w < n && !(*(volatile uint32_t*)&sm.marks[w] & bit)) atomicOr(&sm.marks[w], bit);
+    }
+    __syncthreads();
+    for (uint32_t w = threadIdx.x / 32; w < n; w += 8) {  // runs of rows without a mark
+      const long long v = 32ll * ((w0 + w) * n_cta + cta);
+      const int rows = (int)min(32ll, t.V - v);
+      uint32_t left = ~sm.marks[w] & (rows == 32 ? 0xffffffffu : (1u << rows) - 1);
+      while (left) {
+        const int first = __ffs(left) - 1;
+        const uint32_t rest = ~(left >> first);
+        const int run = rest ? __ffs(rest) - 1 : 32;
+        zero_bytes(dw + (v + first) * row_bytes, run * row_bytes, zeros);
+        left = first + run == 32 ? 0 : left >> (first + run) << (first + run);
+      }
+    }
+    __syncthreads();
+  }
+  bulk_commit();
+  bulk_wait<0>();
+}
+
+// ------------------------------------------------------------------------------------------------
 // Sums of the rows of each id
 // ------------------------------------------------------------------------------------------------
-// Memory bound.  A warp takes a block of sorted positions and 32 * E * U columns, reads four rows at a time and writes a
-// row of dw where the id changes.  A run that began in an earlier block goes to the block's first partial row, one that goes
-// on in the next block to its second; join_kernel adds those up.
+// Memory bound.  A warp takes a block of sorted positions and 32 * E * U columns, reads R rows at a time and writes a row of dw
+// where the id changes.  A run of equal ids that crosses one border between blocks belongs to the block where it begins.  A longer
+// one is long: each of its blocks leaves its sum in a partial row of its own (the one where it begins in its second, the others in
+// their first), and join_kernel adds them up.
 constexpr int kBlockMost = 64;  // positions of a block
 
 struct SumParams {
@@ -213,8 +286,12 @@ struct SumParams {
   long long lddy;
   void* dw;
   float* partial;  // [blocks][2][K]
+  int* n_long;     // long runs, and the blocks where they begin
+  int* longs;
   int M, V, K, block, blocks, pieces;
   int accumulate;
+  int zero_ctas;   // the grid's first CTAs write zeros
+  Tokens t;
   float scale;
 };
 
@@ -229,51 +306,98 @@ __device__ __forceinline__ void put_row(const SumParams& p, uint32_t id, int k, 
 }
 
 template <class T, int E, int U>
-__global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumParams p) {
+__global__ void __launch_bounds__(256, 3) sum_kernel(const __grid_constant__ SumParams p) {
   constexpr int R = 4;
-  const long long item = blockIdx.x * 8ll + threadIdx.x / 32;
+  __shared__ union {
+    ZeroSmem zero;
+    uint32_t order[8][2 * kBlockMost];
+  } sm;
+  if ((int)blockIdx.x < p.zero_ctas) {  // nothing here waits for the sort
+    zero_rows(p.t, static_cast<uint8_t*>(p.dw), p.K * (long long)sizeof(T), blockIdx.x, p.zero_ctas, sm.zero);
+    wait_previous();
+    return;
+  }
+  const long long item = (blockIdx.x - p.zero_ctas) * 8ll + threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
-  const int blk = (int)(item / p.pieces);
+  const int blk = (int)(item / p.pieces), piece = (int)(item - (long long)blk * p.pieces);
   wait_previous();
   if (blk >= p.blocks) return;
-  const int k0 = (int)(item - (long long)blk * p.pieces) * 32 * E * U + lane * E;
+  const uint32_t V = (uint32_t)p.V, none = 0xffffffffu, all = 0xffffffffu;
   const long long i0 = (long long)blk * p.block;
   const int n = (int)min((long long)p.block, p.M - i0);
   const uint2* s = p.sorted + i0;
-  const uint32_t none = 0xffffffffu;
-  uint2 lo = make_uint2(none, 0), hi = make_uint2(none, 0);
+  auto key_at = [&](long long r) { return i0 + r >= 0 && i0 + r < p.M ? s[r].x : none; };  // of any position
+  uint2 lo = make_uint2(none, 0), hi = lo, lo2 = lo, hi2 = lo;  // the block's pairs, and those behind it
   if (lane < n) lo = s[lane];
   if (lane + 32 < n) hi = s[lane + 32];
-  const uint32_t before = i0 > 0 ? s[-1].x : none, after = i0 + n < p.M ? s[n].x : none;
-  auto key = [&](int r) { return __shfl_sync(0xffffffffu, r < 32 ? lo.x : hi.x, r % 32); };
-  auto row = [&](int r) { return __shfl_sync(0xffffffffu, r < 32 ? lo.y : hi.y, r % 32); };
+  if (n == p.block) {
+    if (lane < p.block && i0 + n + lane < p.M) lo2 = s[n + lane];
+    if (lane + 32 < p.block && i0 + n + lane + 32 < p.M) hi2 = s[n + lane + 32];
+  }
+  const uint32_t before = key_at(-1), past = key_at(2ll * p.block), older = key_at(-1ll - p.block);
+  const uint32_t first = __shfl_sync(all, lo.x, 0), last = __shfl_sync(all, n <= 32 ? lo.x : hi.x, (n - 1) % 32);
+  const uint32_t next = __shfl_sync(all, lo2.x, 0);
+  // positions whose id is the first's, the last's, one of the table's
+  auto mask = [&](uint32_t a, uint32_t b) { return (unsigned long long)a | (unsigned long long)b << 32; };
+  auto count = [](unsigned long long m) { return m == ~0ull ? 64 : __ffsll((long long)~m) - 1; };  // ones at the low end
+  const int named = count(mask(__ballot_sync(all, lo.x < V), __ballot_sync(all, hi.x < V)));
+  int begin = 0, end = named;
+  int head = 0;  // positions of a long run that began earlier
+  if (before == first && first < V) {
+    const int run = count(mask(__ballot_sync(all, lo.x == first), __ballot_sync(all, hi.x == first)));
+    if (older != first && (run < n || next != first)) begin = run;  // the last block's
+    else head = run;
+  }
+  int tail = n;  // position where a long run begins that goes on
+  if (named == n && next == last && head < n) {
+    if (past == last) {
+      const int same = 64 - __clzll((long long)~(mask(__ballot_sync(all, lo.x == last), __ballot_sync(all, hi.x == last)) << (64 - n)));
+      tail = same - (64 - n);
+      if (lane == 0 && piece == 0) p.longs[atomicAdd(p.n_long, 1)] = blk;
+    } else {
+      end = n + count(mask(__ballot_sync(all, lo2.x == last), __ballot_sync(all, hi2.x == last)));
+    }
+  }
+  // where the id changes; the rows' positions in shared memory, from where four at a time come
+  const uint32_t up_lo = __shfl_down_sync(all, lo.x, 1), up_hi = __shfl_down_sync(all, hi.x, 1), mid = __shfl_sync(all, hi.x, 0);
+  const uint32_t to_lo = lane == 31 ? mid : up_lo, to_hi = lane == 31 ? next : up_hi;
+  const unsigned long long changes = mask(__ballot_sync(all, lo.x != (lane == n - 1 ? next : to_lo)),
+                                          __ballot_sync(all, hi.x != (lane + 32 == n - 1 ? next : to_hi)));
+  uint32_t* rows = sm.order[threadIdx.x / 32];
+  if (lane < n) rows[lane] = lo.y;
+  if (lane + 32 < n) rows[lane + 32] = hi.y;
+  if (n == p.block) {
+    if (lane < n) rows[n + lane] = lo2.y;
+    if (lane + 32 < n) rows[n + lane + 32] = hi2.y;
+  }
+  __syncwarp();
+  const int k0 = piece * 32 * E * U + lane * E;
+  const T* dy = static_cast<const T*>(p.dy) + k0;
   float acc[U * E] = {};
-  bool first = true;
-  uint32_t id = key(0);
-  for (int r = 0; r < n && id < (uint32_t)p.V; r += R) {
-    Vec<T, E> x[R][U];
+  for (int r = begin & ~(R - 1); r < end; r += R) {
+    const uint4 at = *reinterpret_cast<const uint4*>(rows + r);
+    const uint32_t row[R] = {at.x, at.y, at.z, at.w};
+    Raw<T, E> x[R][U];
 #pragma unroll
     for (int q = 0; q < R; ++q) {
-      const bool in = r + q < n && key(min(r + q, n - 1)) < (uint32_t)p.V;
-      const T* src = static_cast<const T*>(p.dy) + (long long)row(min(r + q, n - 1)) * p.lddy;
+      const bool in = r + q >= begin && r + q < end;
+      const T* src = dy + (in ? row[q] : 0) * p.lddy;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int k = k0 + u * 32 * E;
-        if (in && k < p.K) x[q][u] = *reinterpret_cast<const Vec<T, E>*>(src + k);
+        x[q][u] = Raw<T, E>();
+        if (in && k0 + u * 32 * E < p.K) x[q][u] = *reinterpret_cast<const Raw<T, E>*>(src + u * 32 * E);
       }
     }
+    uint32_t ends = r < 64 ? (uint32_t)(changes >> r) & (r + R <= n ? (1u << R) - 1 : (1u << max(n - r, 0)) - 1) : 0;
+    if (end - 1 - r < R) ends |= 1u << (end - 1 - r);
 #pragma unroll
     for (int q = 0; q < R; ++q) {
-      if (r + q >= n || id >= (uint32_t)p.V) break;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (k0 + u * 32 * E < p.K)
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[u * E + e] += to_f32(x[q][u].v[e]);
-      const bool last = r + q + 1 == n;
-      const uint32_t next = last ? none : key(min(r + q + 1, n - 1));
-      if (next == id) continue;
-      const int slot = first && before == id ? 0 : last && after == id ? 1 : -1;
+      for (int u = 0; u < U; ++u) add_to<T, E>(acc + u * E, x[q][u]);
+      const int at_q = r + q;
+      if (!(ends >> q & 1u) || at_q < begin || at_q >= end) continue;
+      const uint32_t id = __shfl_sync(all, at_q < n && at_q < 32 ? lo.x : at_q < n ? hi.x : last, at_q % 32);
+      const int slot = at_q < head ? 0 : at_q >= tail && at_q < n ? 1 : -1;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int k = k0 + u * 32 * E;
@@ -290,49 +414,56 @@ __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumPar
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[u * E + e] = 0.f;
       }
-      id = next;
-      first = false;
     }
   }
 }
 
-// Runs that cross blocks: the block where a run begins adds its partial rows up, in order.
+// Long runs: a CTA adds the partial rows of one up in 32 * E * U columns, its warps every eighth and then their sums in order.  (The
+// order of the list depends on the launch, the sums do not.)
 template <class T, int E, int U>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ SumParams p) {
-  const long long item = blockIdx.x * 8ll + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  const int blk = (int)(item / p.pieces);
+  __shared__ float sums[8][U][32 * E];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   wait_previous();
-  if (blk >= p.blocks - 1) return;
-  const long long i0 = (long long)blk * p.block, i1 = i0 + p.block;
-  const uint32_t id = p.sorted[i1].x;
-  if (id >= (uint32_t)p.V || p.sorted[i1 - 1].x != id) return;      // no run goes on
-  if (i0 > 0 && p.sorted[i0].x == id && p.sorted[i0 - 1].x == id) return;  // it began earlier
-  int n = 1;  // blocks that it goes on in
-  for (bool more = true; more;) {
-    const long long b = blk + 1ll + n + lane;
-    const uint32_t go = __ballot_sync(0xffffffffu, b < p.blocks && p.sorted[b * p.block].x == id);
-    const int run = go == 0xffffffffu ? 32 : __ffs(~go) - 1;
-    n += run;
-    more = run == 32;
-  }
-  const int k0 = (int)(item - (long long)blk * p.pieces) * 32 * E * U + lane * E;
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int k = k0 + u * 32 * E;
-    if (k >= p.K) break;
-    const float* at = p.partial + 2ll * blk * p.K + k;
-    float acc[E];
-    const Vec<float, E> v = *reinterpret_cast<const Vec<float, E>*>(at + p.K);
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = v.v[e];
-#pragma unroll 8
-    for (int b = 1; b <= n; ++b) {
-      const Vec<float, E> w = *reinterpret_cast<const Vec<float, E>*>(at + 2ll * b * p.K);
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += w.v[e];
+  const int pieces = (p.K + 32 * E * U - 1) / (32 * E * U);
+  const long long items = (long long)*p.n_long * pieces;
+  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+    const int blk = p.longs[item / pieces], k0 = (int)(item % pieces) * 32 * E * U + lane * E;
+    const uint32_t id = p.sorted[(blk + 1ll) * p.block].x;
+    int n = 1;  // blocks that it goes on in
+    for (bool more = true; more;) {
+      const long long b = blk + 1ll + n + lane;
+      const uint32_t go = __ballot_sync(0xffffffffu, b < p.blocks && p.sorted[b * p.block].x == id);
+      const int run = go == 0xffffffffu ? 32 : __ffs(~go) - 1;
+      n += run;
+      more = run == 32;
     }
-    put_row<T, E>(p, id, k, acc);
+    float acc[U][E] = {};
+    const float* at = p.partial + 2ll * blk * p.K + k0;
+#pragma unroll 4
+    for (int b = warp; b <= n; b += 8) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (k0 + u * 32 * E >= p.K) break;
+        const Vec<float, E> v = *reinterpret_cast<const Vec<float, E>*>(at + (b ? 2ll * b : 1ll) * p.K + u * 32 * E);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[u][e] += v.v[e];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < E; ++e) sums[warp][u][lane * E + e] = acc[u][e];
+    __syncthreads();
+    if (warp >= U) continue;
+    float f[E] = {};  // a warp to each 32 * E columns
+    const int k = k0 + warp * 32 * E;
+#pragma unroll
+    for (int w = 0; w < 8; ++w)
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] += sums[w][warp][lane * E + e];
+    if (k < p.K) put_row<T, E>(p, id, k, f);
   }
 }
 
@@ -378,7 +509,7 @@ static int dispatch(int type, int e, F f) {
 
 struct Sizes {
   int block, blocks;
-  size_t a, b, partial, total;
+  size_t n_long, a, b, longs, partial, total;
 };
 
 // Positions of a block: as many as leave every SM 16 warps, between 8 and 64.
@@ -389,9 +520,11 @@ static Sizes sizes(const psr_embedding_shape* sh) {
   while (s.block < kBlockMost && warps / (2 * s.block) >= 152 * 16) s.block *= 2;
   s.blocks = (int)(((long long)sh->M + s.block - 1) / s.block);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  s.a = 256;
+  s.n_long = 256;
+  s.a = 512;
   s.b = s.a + up((size_t)sh->M * 8);
-  s.partial = s.b + up((size_t)sh->M * 8);
+  s.longs = s.b + up((size_t)sh->M * 8);
+  s.partial = s.longs + up((size_t)s.blocks * 4);
   s.total = s.partial + up((size_t)s.blocks * 2 * sh->K * 4);
   return s;
 }
@@ -445,27 +578,30 @@ int psr_embedding_bwd(const psr_embedding_shape* sh, const void* dy, const int64
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const long long lddy = sh->ldy ? sh->ldy : sh->K;
 
+  if (sh->M == 0) {
+    if (cudaMemsetAsync(ws, 0, 256, st) == cudaSuccess &&
+        (sh->accumulate || cudaMemsetAsync(dw, 0, (size_t)sh->V * sh->K * size_of(sh->type), st) == cudaSuccess))
+      return PSR_OK;
+    cudaGetLastError();
+    return PSR_ERR_CUDA;
+  }
+
   SortParams q = {};
-  q.ids = ids;
-  q.step = sh->ids_step;
-  q.padding = sh->padding;
-  q.M = sh->M;
-  q.V = sh->V;
+  q.t = {ids, sh->ids_step, sh->padding, sh->M, sh->V};
   q.a = reinterpret_cast<uint2*>(ws + s.a);
   q.b = reinterpret_cast<uint2*>(ws + s.b);
+  q.n_long = reinterpret_cast<int*>(ws + s.n_long);
   int bits = 1;
   while ((1ll << bits) <= sh->V) ++bits;  // of the keys 0 .. V
   q.passes = (bits + kSortBits - 1) / kSortBits;
   q.bits = (bits + q.passes - 1) / q.passes;
-  q.dw = sh->accumulate ? nullptr : static_cast<uint8_t*>(dw);
-  q.row_bytes = (long long)sh->K * size_of(sh->type);
   q.clear = reinterpret_cast<Ctrl*>(ws);
   if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SortSmem)) != cudaSuccess) {
     cudaGetLastError();
     return PSR_ERR_CUDA;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(sh->accumulate ? kSortCtas : n_sm / kSortCtas * kSortCtas));
+  cfg.gridDim = dim3(kSortCtas);
   cfg.blockDim = dim3(kSortThreads);
   cfg.dynamicSmemBytes = sizeof(SortSmem);
   cfg.stream = st;
@@ -480,7 +616,6 @@ int psr_embedding_bwd(const psr_embedding_shape* sh, const void* dy, const int64
     cudaGetLastError();
     return PSR_ERR_CUDA;
   }
-  if (sh->M == 0) return PSR_OK;
 
   SumParams p = {};
   p.sorted = q.a;
@@ -488,22 +623,27 @@ int psr_embedding_bwd(const psr_embedding_shape* sh, const void* dy, const int64
   p.lddy = lddy;
   p.dw = dw;
   p.partial = reinterpret_cast<float*>(ws + s.partial);
+  p.n_long = q.n_long;
+  p.longs = reinterpret_cast<int*>(ws + s.longs);
   p.M = sh->M;
   p.V = sh->V;
   p.K = sh->K;
   p.block = s.block;
   p.blocks = s.blocks;
   p.accumulate = sh->accumulate;
+  p.zero_ctas = sh->accumulate ? 0 : std::min(n_sm, (sh->V + 31) / 32);
+  p.t = q.t;
   p.scale = sh->scale;
   const int e = vector_of(sh->type, sh->K, lddy, sh->K, dy, dw);
   return dispatch(sh->type, e, [&](auto t, auto ec, auto uc) {
     using T = decltype(t);
-    constexpr int E = decltype(ec)::value, U = decltype(uc)::value;
+    constexpr int E = decltype(ec)::value, U = decltype(uc)::value, UJ = E >= 4 ? 1 : U;
     p.pieces = (sh->K + 32 * E * U - 1) / (32 * E * U);
-    const long long blocks = ((long long)s.blocks * p.pieces + 7) / 8;
+    const long long blocks = p.zero_ctas + ((long long)s.blocks * p.pieces + 7) / 8;
     if (blocks >= 1ll << 31) return (int)PSR_ERR_UNSUPPORTED;
     int r = launch_after(sum_kernel<T, E, U>, dim3((unsigned)blocks), 256, p, st);
-    if (r == PSR_OK && s.blocks > 1) r = launch_after(join_kernel<T, E, U>, dim3((unsigned)blocks), 256, p, st);
+    const long long most = (long long)s.blocks / 2 * ((sh->K + 32 * E * UJ - 1) / (32 * E * UJ));  // a long run takes over two blocks
+    if (r == PSR_OK && most > 0) r = launch_after(join_kernel<T, E, UJ>, dim3((unsigned)std::min(most, 6ll * n_sm)), 256, p, st);
     return r;
   });
 }

@@ -110,6 +110,20 @@ def test_gradient(psr, case):
     assert torch.equal(again.view(torch.uint8), dw.view(torch.uint8))
 
 
+@pytest.mark.parametrize("K,step", [(4, 8), (2600, 16), (9000, 64)])
+def test_gradient_of_runs_of_every_length(psr, K, step):
+    """Runs of equal ids that end in, at and behind the borders of the blocks in which they are summed (of `step` positions)."""
+    need_gpu()
+    g = torch.Generator().manual_seed(K)
+    lengths = torch.tensor([1, 2, step - 1, step, step + 1, 2 * step - 1, 2 * step, 2 * step + 1, 3 * step, 5 * step + 3, 3, 1, step // 2])
+    lengths = lengths.repeat(4)[torch.randperm(52, generator=g)]
+    ids = torch.repeat_interleave(torch.arange(52) * 3, lengths)
+    ids = ids[torch.randperm(len(ids), generator=g)].cuda()
+    dy = randn(g, (len(ids), K), "bf16")
+    dw, _ = psr.embedding_bwd(dy, ids, 160)
+    check_gradient(dw, dy, ids, 160, "bf16", str(K))
+
+
 @pytest.mark.parametrize("t", ["bf16", "f16", "f32"])
 def test_gradient_leaves_out_and_adds(psr, t):
     need_gpu()
