@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <mutex>
 #include <type_traits>
 
 #include "psr_control.cuh"
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(256)
 // contiguous share of the pairs and counts its digits; the counts before it (of smaller digits, of earlier CTAs and warps) are
 // where its pairs go, equal digits in their order.  Ids outside the table, and the padding id, become V: they end up behind all
 // others.
-constexpr int kSortCtas = 8, kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortBits = 9, kBins = 1 << kSortBits;
+constexpr int kSortCtasMost = 8, kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortBits = 9, kBins = 1 << kSortBits;
 
 struct Tokens {
   const int64_t* ids;
@@ -126,8 +127,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
   launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.n_long = 0;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t rank = cluster_ctarank();
-  const long long share = (((long long)p.t.M + kSortCtas * kSortWarps - 1) / (kSortCtas * kSortWarps) + 31) / 32 * 32;
+  const uint32_t rank = cluster_ctarank(), ctas = gridDim.x;  // one cluster
+  const long long share = (((long long)p.t.M + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
   const long long i0 = ((long long)rank * kSortWarps + warp) * share;
   const long long i1 = min((long long)p.t.M, i0 + share);
   const uint32_t bins = 1u << p.bits;
@@ -150,15 +151,14 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
         }
 #pragma unroll
         for (int j = 0; j < kRounds; ++j) {
+          if (i + 32 * j >= i1) break;
           const bool in = i + 32 * j + lane < i1;
           f(in, x[j], in ? x[j].x >> shift & (bins - 1) : bins);
         }
       }
     };
     each([&](bool in, uint2, uint32_t d) {
-      const uint32_t same = __match_any_sync(0xffffffffu, d);
-      if (in && lane == __ffs(same) - 1) sm.hist[warp][d] += __popc(same);
-      __syncwarp();
+      if (in) atomicAdd(&sm.hist[warp][d], 1u);
     });
     __syncthreads();
     uint32_t total = 0;
@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
     uint32_t all = 0, before = 0;
     if (threadIdx.x < bins) {
 #pragma unroll
-      for (uint32_t c = 0; c < (uint32_t)kSortCtas; ++c) {
+      for (uint32_t c = 0; c < (uint32_t)kSortCtasMost; ++c) {
+        if (c >= ctas) break;
         const uint32_t n = ld_shared_cluster(mapa_shared(smem_u32(&sm.total[threadIdx.x]), c));
         if (c < rank) before += n;
         all += n;
@@ -286,8 +287,8 @@ struct SumParams {
   long long lddy;
   void* dw;
   float* partial;  // [blocks][2][K]
-  int* n_long;     // long runs, and the blocks where they begin
-  int* longs;
+  int* n_long;     // long runs: the blocks where they begin, and their ids
+  int2* longs;
   int M, V, K, block, blocks, pieces;
   int accumulate;
   int zero_ctas;   // the grid's first CTAs write zeros
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(256, 3) sum_kernel(const __grid_constant__ Sum
     if (past == last) {
       const int same = 64 - __clzll((long long)~(mask(__ballot_sync(all, lo.x == last), __ballot_sync(all, hi.x == last)) << (64 - n)));
       tail = same - (64 - n);
-      if (lane == 0 && piece == 0) p.longs[atomicAdd(p.n_long, 1)] = blk;
+      if (lane == 0 && piece == 0) p.longs[atomicAdd(p.n_long, 1)] = make_int2(blk, (int)last);
     } else {
       end = n + count(mask(__ballot_sync(all, lo2.x == last), __ballot_sync(all, hi2.x == last)));
     }
@@ -428,27 +429,45 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ SumPa
   const int pieces = (p.K + 32 * E * U - 1) / (32 * E * U);
   const long long items = (long long)*p.n_long * pieces;
   for (long long item = blockIdx.x; item < items; item += gridDim.x) {
-    const int blk = p.longs[item / pieces], k0 = (int)(item % pieces) * 32 * E * U + lane * E;
-    const uint32_t id = p.sorted[(blk + 1ll) * p.block].x;
+    const int2 run = p.longs[item / pieces];
+    const int blk = run.x, k0 = (int)(item % pieces) * 32 * E * U + lane * E;
+    const uint32_t id = (uint32_t)run.y;
     int n = 1;  // blocks that it goes on in
     for (bool more = true; more;) {
-      const long long b = blk + 1ll + n + lane;
-      const uint32_t go = __ballot_sync(0xffffffffu, b < p.blocks && p.sorted[b * p.block].x == id);
-      const int run = go == 0xffffffffu ? 32 : __ffs(~go) - 1;
-      n += run;
-      more = run == 32;
+      bool same[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const long long b = blk + 1ll + n + 32 * j + lane;
+        same[j] = b < p.blocks && p.sorted[b * p.block].x == id;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t go = __ballot_sync(0xffffffffu, same[j]);
+        if (more) n += go == 0xffffffffu ? 32 : __ffs(~go) - 1;
+        more = more && go == 0xffffffffu;
+      }
     }
     float acc[U][E] = {};
     const float* at = p.partial + 2ll * blk * p.K + k0;
-#pragma unroll 4
-    for (int b = warp; b <= n; b += 8) {
+    constexpr int R = 4;  // partial rows in flight
+    for (int b0 = warp; b0 <= n; b0 += 8 * R) {
+      Vec<float, E> v[R][U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (k0 + u * 32 * E >= p.K) break;
-        const Vec<float, E> v = *reinterpret_cast<const Vec<float, E>*>(at + (b ? 2ll * b : 1ll) * p.K + u * 32 * E);
+      for (int r = 0; r < R; ++r) {
+        const int b = b0 + 8 * r;
+        const float* from = at + (b ? 2ll * b : 1ll) * p.K;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[u][e] += v.v[e];
+        for (int u = 0; u < U; ++u) {
+          v[r][u] = Vec<float, E>();
+          if (b <= n && k0 + u * 32 * E < p.K) v[r][u] = *reinterpret_cast<const Vec<float, E>*>(from + u * 32 * E);
+        }
       }
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[u][e] += v[r][u].v[e];
     }
     __syncthreads();
 #pragma unroll
@@ -512,6 +531,40 @@ struct Sizes {
   size_t n_long, a, b, longs, partial, total;
 };
 
+// CTAs of the sort's cluster on the current device (0: an error), and the rest of its launch.  Sixteen are more than every device
+// has to take, so it is asked; the sort of 65539 tokens takes @ us with them and @ with eight.
+static int sort_ctas(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr) {
+  static std::mutex mu;
+  static int known[64] = {};
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = sizeof(SortSmem);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lk(mu);
+  int ctas = dev < 64 ? known[dev] : 0;
+  if (!ctas) {
+    if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SortSmem)) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    ctas = 8;
+    if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+      int n = 0;
+      cfg.gridDim = dim3(kSortCtasMost);
+      attr[0].val.clusterDim.x = kSortCtasMost;
+      if (cudaOccupancyMaxActiveClusters(&n, sort_kernel, &cfg) == cudaSuccess && n > 0) ctas = kSortCtasMost;
+    }
+    cudaGetLastError();
+    if (dev < 64) known[dev] = ctas;
+  }
+  attr[0].val.clusterDim.x = ctas;
+  return ctas;
+}
+
 // Positions of a block: as many as leave every SM 16 warps, between 8 and 64.
 static Sizes sizes(const psr_embedding_shape* sh) {
   Sizes s;
@@ -524,7 +577,7 @@ static Sizes sizes(const psr_embedding_shape* sh) {
   s.a = 512;
   s.b = s.a + up((size_t)sh->M * 8);
   s.longs = s.b + up((size_t)sh->M * 8);
-  s.partial = s.longs + up((size_t)s.blocks * 4);
+  s.partial = s.longs + up((size_t)s.blocks * 8);
   s.total = s.partial + up((size_t)s.blocks * 2 * sh->K * 4);
   return s;
 }
@@ -596,22 +649,12 @@ int psr_embedding_bwd(const psr_embedding_shape* sh, const void* dy, const int64
   q.passes = (bits + kSortBits - 1) / kSortBits;
   q.bits = (bits + q.passes - 1) / q.passes;
   q.clear = reinterpret_cast<Ctrl*>(ws);
-  if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SortSmem)) != cudaSuccess) {
-    cudaGetLastError();
-    return PSR_ERR_CUDA;
-  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kSortCtas);
-  cfg.blockDim = dim3(kSortThreads);
-  cfg.dynamicSmemBytes = sizeof(SortSmem);
-  cfg.stream = st;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kSortCtas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  const int ctas = sort_ctas(cfg, attr);
+  if (ctas == 0) return PSR_ERR_CUDA;
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.stream = st;
   if (cudaLaunchKernelEx(&cfg, sort_kernel, q) != cudaSuccess) {
     cudaGetLastError();
     return PSR_ERR_CUDA;
@@ -624,7 +667,7 @@ int psr_embedding_bwd(const psr_embedding_shape* sh, const void* dy, const int64
   p.dw = dw;
   p.partial = reinterpret_cast<float*>(ws + s.partial);
   p.n_long = q.n_long;
-  p.longs = reinterpret_cast<int*>(ws + s.longs);
+  p.longs = reinterpret_cast<int2*>(ws + s.longs);
   p.M = sh->M;
   p.V = sh->V;
   p.K = sh->K;
