@@ -276,6 +276,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 // ================================================================================================
 // pair_gemm
 // ================================================================================================
+constexpr int kPairs = 76;           // pairs of CTAs that tiles are split for
 constexpr int kRows = 128;           // A rows, and B rows of a half, that one CTA loads
 constexpr int kHalf = kRows * kBK * 2;
 // The logits of the loss are summed in parts of at most kPartSteps K steps, which the epilogue adds up: the tensor core's sums of
@@ -315,6 +316,7 @@ struct PairParams {
   Ctrl* ctrl;
   Ctrl* clear;            // control block to clear, or null
   unsigned long long timeout_ns;
+  int n_pairs;
   Head h;
 };
 
@@ -326,7 +328,7 @@ struct PairSmem {
 
 // A product's rows, K steps and tiles: the host's, or (rows that count) what the device makes of their number.
 struct Extent {
-  int M, n_k, tiles_m, whole, halves;  // as in PairParams
+  int M, n_k, wide, tiles_m, tiles_n, whole, splits, split_k, halves;  // as in PairParams
 };
 
 // What a pair computes next: `n` 256-column halves from column half tn on of tile row tm, K steps k0 .. k0 + n_k.  split: the part
@@ -338,7 +340,7 @@ struct PairItem {
 // Tile t -> (row block, column block): groups of `group` tile rows, columns inside a group, rows fastest, so that the
 // tiles in flight at once share few rows of either operand and a group's rows of A stay in L2.
 __device__ __forceinline__ void pair_tile(const PairParams& p, const Extent& x, int t, int& tm, int& tn) {
-  const int per = p.group * p.tiles_n, g = t / per, r = t - g * per;
+  const int per = p.group * x.tiles_n, g = t / per, r = t - g * per;
   const int rows = min(p.group, x.tiles_m - g * p.group);
   tn = r / rows;
   tm = g * p.group + (r - tn * rows);
@@ -349,21 +351,21 @@ __device__ __forceinline__ void pair_tile(const PairParams& p, const Extent& x, 
 // a half, not four).  Rounds shifted by half a tile between pairs, so that some write while others multiply, were
 // slower: the tile loads leave L2 no room for the outputs (4096^3 with gelu 100 to 118 us).
 __device__ __forceinline__ bool pair_item(const PairParams& p, const Extent& x, int pair, int n_pairs, int i, PairItem& it) {
-  const long long n = (long long)x.tiles_m * p.tiles_n, at = pair + (long long)i * n_pairs;
+  const long long n = (long long)x.tiles_m * x.tiles_n, at = pair + (long long)i * n_pairs;
   it.k0 = 0;
   it.n_k = x.n_k;
   it.split = -1;
-  if (!p.wide) {
+  if (!x.wide) {
     it.n = 1;
     int tile = (int)at;
     if (at >= x.whole) {
       const long long part = at - x.whole;
-      if (part >= (n - x.whole) * p.splits) return false;
-      tile = x.whole + (int)(part / p.splits);
-      if (p.splits > 1) {
+      if (part >= (n - x.whole) * x.splits) return false;
+      tile = x.whole + (int)(part / x.splits);
+      if (x.splits > 1) {
         it.split = (int)part;
-        it.k0 = (int)(part % p.splits) * p.split_k;
-        it.n_k = min(p.split_k, x.n_k - it.k0);
+        it.k0 = (int)(part % x.splits) * x.split_k;
+        it.n_k = min(x.split_k, x.n_k - it.k0);
       }
     }
     pair_tile(p, x, tile, it.tm, it.tn);
@@ -544,10 +546,12 @@ __host__ __device__ inline int last_halves(long long tiles, int pairs) {
   return 2 * rest <= pairs ? (int)rest : 0;
 }
 
-// (Not a changed copy of the parameters: one kept the row count that the host had given.)
+// The product as the device knows it: with the number of rows that count.  (Not a changed copy of the parameters: one kept the row
+// count that the host had given.)  dx, whose tiles are few and whose sums are long, has its tiles chosen here, as wide_tiles and split_of
+// choose others on the host: 512 columns, or 256 with those of the last round split along K.
 template <int MODE>
 __device__ __forceinline__ Extent extent_of(const PairParams& p, int n_pairs) {
-  Extent x = {p.M, p.n_k, p.tiles_m, p.whole, p.halves};
+  Extent x = {p.M, p.n_k, p.wide, p.tiles_m, p.tiles_n, p.whole, p.splits, p.split_k, p.halves};
   if (MODE == kLayer || !p.h.rows) return x;
   const int rows = *p.h.rows;
   if (MODE == kWeight) {
@@ -556,8 +560,25 @@ __device__ __forceinline__ Extent extent_of(const PairParams& p, int n_pairs) {
   }
   x.M = rows;
   x.tiles_m = (rows + 255) / 256;
-  const int tiles = x.tiles_m * p.tiles_n;
-  if (p.wide) x.halves = last_halves(tiles, n_pairs);
+  if (MODE == kSum) {
+    const int ones = x.tiles_m * ((p.N + 255) / 256), twos = x.tiles_m * ((p.N + 511) / 512), rest = ones % kPairs;
+    const int halves = last_halves(twos, n_pairs), most = x.n_k / 8;
+    const float k = (float)(p.n_k * kBK), step = 9.3f * k;
+    int parts = rest ? min(kPairs / rest, most) : 1;
+    const float join = 5500.f + 180.f * rest * parts;
+    if (parts < 2 || 8.6f * k * (1.f - 1.f / parts) < join) parts = 1;
+    const float one = parts > 1 ? ones / kPairs * step + step / parts + join : (ones + n_pairs - 1) / n_pairs * step;
+    const float two = (twos / n_pairs + (halves || twos % n_pairs == 0 ? 0 : 1)) * (16.f * k + 15600.f) + (halves ? step + 7800.f : 0.f);
+    x.wide = two <= one;
+    x.tiles_n = x.wide ? (p.N + 511) / 512 : (p.N + 255) / 256;
+    x.whole = x.wide ? twos : ones - (parts > 1 ? rest : 0);
+    x.split_k = (x.n_k + parts - 1) / parts;
+    x.splits = x.wide ? 1 : (x.n_k + x.split_k - 1) / x.split_k;  // none of them empty
+    x.halves = x.wide ? halves : 0;
+    return x;
+  }
+  const int tiles = x.tiles_m * x.tiles_n;
+  if (x.wide) x.halves = last_halves(tiles, n_pairs);
   else x.whole = min(x.whole, tiles);
   return x;
 }
@@ -771,6 +792,7 @@ __global__ void __launch_bounds__(pair_threads(MODE), 1)
   tc_fence_after();
 
   const int pair = blockIdx.x / 2, n_pairs = gridDim.x / 2;
+  if constexpr (MODE != kLayer) wait_previous();  // the loss's kernels begin while the one before ends
   const Extent x = extent_of<MODE>(p, n_pairs);
   const uint32_t full0 = __shfl_sync(0xffffffffu, mapa_shared(smem_u32(&sc.full[0]), 0), 0);  // of the pair's first CTA
   PairItem it;
@@ -1005,48 +1027,71 @@ struct StreamParams {
   Head h;
 };
 
+constexpr int kSumPitch = 33;  // a token's row, read by column and by row
+
 struct StreamSmem {
   uint64_t full[kStreamMaxStages], empty[kStreamMaxStages], acc_full[2], acc_empty[2], drain;
   uint32_t tmem_base;
   volatile uint32_t abort;
-  float sums[4][16][32];  // epilogue warp, token, lane
+  alignas(16) float sums[4][16][kSumPitch];  // epilogue warp, token, lane
 };
 static_assert(kStreamSmem + sizeof(StreamSmem) <= 232448, "shared memory");
 
-// The loss's modes: token i, column j (a warp's 32 adjacent ones, some perhaps past the last) and its sum v.
+// The loss's modes: a warp's 32 columns from j0 on, a lane to each, and the sums v of the n tokens from i0 on.  kStats reduces them
+// with two lanes to a token, through `rows` ([16][kSumPitch] floats of the warp's, on a 16-byte boundary).
 template <int MODE>
-__device__ __forceinline__ void head_one(const StreamParams& p, int i, int j, float v) {
-  const bool in = j < p.N;
+__device__ __forceinline__ void head_tokens(const StreamParams& p, int i0, int n, int j0, const uint32_t (&v)[16], float* rows) {
+  const int lane = threadIdx.x % 32, j = j0 + lane;
   if constexpr (MODE == kStats) {
-    const int lane = threadIdx.x % 32;
-    const bool target = in && p.h.ids[i * p.h.step] == (int64_t)j + p.h.col0;
-    if (target) p.h.at[i] = v;
-    float sum = in ? v : 0.f;
-    if (!in) v = -INFINITY;
-    float m = v;
+    const int cols = min(32, p.N - j0);
+    if (cols <= 0) return;
+    __syncwarp();
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int e = 0; e < 16; ++e) rows[e * kSumPitch + lane] = lane < cols ? __uint_as_float(v[e]) : -INFINITY;
+    __syncwarp();
+    const int i = lane % 16, c0 = lane / 16 * 16;
+    const float* row = rows + i * kSumPitch;
+    float f[16], m = -INFINITY, sum = 0.f, s[2] = {};
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      f[c] = row[c0 + c];
+      m = fmaxf(m, f[c]);
+      if (c0 + c < cols) sum += f[c];
+    }
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
     const float ref = exp_ref(-FLT_MAX, m);
-    float s = ex2_approx(fmaf(v, kLog2e, -ref));
 #pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const int group = j / 32;
-    const long long to = group * p.h.group_at + i * p.h.row_at;
-    if (p.h.sums) {
+    for (int c = 0; c < 16; ++c) s[c % 2] += ex2_approx(fmaf(f[c], kLog2e, -ref));
+    s[0] += s[1];
+    s[0] += __shfl_xor_sync(0xffffffffu, s[0], 16);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+    if (lane < n) {  // (n: at most 16)
+      const long long to = j0 / 32 * p.h.group_at + (i0 + i) * p.h.row_at;
+      p.h.stats[to] = make_float2(ref, s[0]);
+      if (p.h.sums) p.h.sums[to] = sum;
+      const int64_t target = p.h.ids[(i0 + i) * p.h.step] - p.h.col0 - j0;
+      if (target >= 0 && target < cols) p.h.at[i0 + i] = row[target];
+    }
+  } else if constexpr (MODE == kSlope) {
+    __syncwarp();
+    if (lane < n) {  // the tokens' coefficients and targets, 16 bytes and 4 to each
+      reinterpret_cast<float4*>(rows)[lane] = p.h.coef[i0 + lane];
+      const int64_t target = p.h.ids[(i0 + lane) * p.h.step] - p.h.col0 - j0;
+      reinterpret_cast<int*>(rows)[64 + lane] = target >= 0 && target < 32 ? (int)target : -1;
+    }
+    __syncwarp();
 #pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane == 0 && in) p.h.sums[to] = sum;
+    for (int e = 0; e < 16; ++e) {
+      const float4 c = reinterpret_cast<const float4*>(rows)[e];
+      float f = fmaf(c.y, ex2_approx(fmaf(__uint_as_float(v[e]), kLog2e, -c.x)), -c.z);
+      if (reinterpret_cast<const int*>(rows)[64 + e] == lane) f -= c.w;
+      if (e < n && j < p.N) store16(p.e.y, (i0 + e) * p.e.ldy + j, p.e.half, f);
     }
-    if (lane == 0 && in) p.h.stats[to] = make_float2(ref, s);
-  } else if (in) {
-    if constexpr (MODE == kSlope) {
-      const float4 c = p.h.coef[i];
-      v = fmaf(c.y, ex2_approx(fmaf(v, kLog2e, -c.x)), -c.z);
-      if (p.h.ids[i * p.h.step] == (int64_t)j + p.h.col0) v -= c.w;
-    } else {
-      v *= *p.h.unit;
-    }
-    store16(p.e.y, i * p.e.ldy + j, p.e.half, v);
+  } else {
+    const float unit = *p.h.unit;
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (e < n && j < p.N) store16(p.e.y, (i0 + e) * p.e.ldy + j, p.e.half, __uint_as_float(v[e]) * unit);
   }
 }
 
@@ -1085,6 +1130,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if constexpr (MODE != kLayer) wait_previous();
 
   const long long total = (long long)p.n_tiles * p.n_k;
   const long long u0 = (long long)blockIdx.x * p.per_cta;
@@ -1197,15 +1243,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           continue;
         }
         if constexpr (MODE != kLayer) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (e < n_c) head_one<MODE>(p, c + e, j, __uint_as_float(v[e]));
+          head_tokens<MODE>(p, c, n_c, tile * kRows + quarter * 32, v, &sc.sums[quarter][0][0]);
           continue;
         }
         // four tokens at a time, their residuals in flight together; each lane reads its own sums back
         float* own = &sc.sums[quarter][0][lane];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) own[e * 32] = __uint_as_float(v[e]);
+        for (int e = 0; e < 16; ++e) own[e * kSumPitch] = __uint_as_float(v[e]);
         if (j < p.N) {
 #pragma unroll 1
           for (int e = 0; e < n_c; e += 4) {
@@ -1213,7 +1257,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const long long i = c + e + q;
-              f[q] = own[(e + q) * 32] + bias;
+              f[q] = own[(e + q) * kSumPitch] + bias;
               r[q] = p.e.res && e + q < n_c ? load16(p.e.res, i * p.e.ldr + j, p.e.half) : 0.f;
             }
             float4 y = make_float4(f[0], f[1], f[2], f[3]);
@@ -1269,22 +1313,86 @@ __global__ void __launch_bounds__(128) stream_join(const __grid_constant__ Strea
     const int slot = 2 * g + ((long long)g * p.per_cta >= b ? 0 : 1);  // the tile that CTA g begins or ends with
     sum += p.partial[((long long)slot * p.tb + i) * kRows + threadIdx.x];
   }
-  if constexpr (MODE != kLayer) head_one<MODE>(p, i, j, sum);
-  else if (j < p.N) finish(p.e, i, j, sum);
+  if (j < p.N) finish(p.e, i, j, sum);
+}
+
+// The same for the loss's modes: a block for sixteen tokens of the tile in which CTA blockIdx.x of the product began, if it is the first
+// to begin inside of it.  (A block for each token of every tile took 20 us at 48 tokens and 1000 tiles, of which 150 are split.)
+template <int MODE>
+__global__ void __launch_bounds__(128) head_join(const __grid_constant__ StreamParams p) {
+  __shared__ __align__(16) float rows[4][16][kSumPitch];
+  const long long u = (long long)blockIdx.x * p.per_cta;
+  const int tile = (int)(u / p.n_k), i0 = blockIdx.y * 16, n = min(16, p.M - i0), warp = threadIdx.x / 32;
+  wait_previous();
+  if (u % p.n_k == 0 || u - p.per_cta > (long long)tile * p.n_k) return;
+  const long long b = (long long)tile * p.n_k;
+  const int c0 = (int)(b / p.per_cta), c1 = (int)((b + p.n_k - 1) / p.per_cta);
+  float sum[16] = {};
+#pragma unroll 2
+  for (int g = c0; g <= c1; ++g) {
+    const int slot = 2 * g + ((long long)g * p.per_cta >= b ? 0 : 1);
+    const float* part = p.partial + ((long long)slot * p.tb + i0) * kRows + threadIdx.x;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) sum[e] += e < n ? part[e * kRows] : 0.f;
+  }
+  uint32_t v[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(sum[e]);
+  head_tokens<MODE>(p, i0, n, tile * kRows + warp * 32, v, &rows[warp][0][0]);
+}
+
+// Four columns of dx from the parts of a split tile: the sums of earlier pieces, these, and the row's place in dx.
+__device__ __forceinline__ void sum_parts(const PairParams& p, const float* part, int splits, long long i, int j) {
+  const Epilogue& e = p.e;
+  float f[4] = {};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float4 v = *reinterpret_cast<const float4*>(part + s * 65536ll);
+    f[0] += v.x; f[1] += v.y; f[2] += v.z; f[3] += v.w;
+  }
+  float* acc = p.h.acc + i * p.h.ldacc + j;
+  if (!p.h.first) {
+    const float4 a = *reinterpret_cast<const float4*>(acc);
+    f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
+  }
+  if (!p.h.last) {
+    *reinterpret_cast<float4*>(acc) = make_float4(f[0], f[1], f[2], f[3]);
+    return;
+  }
+  const float unit = *p.h.unit;
+  const long long to = p.h.index[i] * e.ldy + j;
+  if (e.vec) {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(e.y) + to) =
+        make_uint2(pack16(f[0] * unit, f[1] * unit, e.half), pack16(f[2] * unit, f[3] * unit, e.half));
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (j + c < p.N) store16(e.y, to + c, e.half, f[c] * unit);
+  }
 }
 
 // Joins the parts of the split tiles in order: four columns to a thread, 64 blocks to a tile.
 template <int MODE = kLayer>
 __global__ void __launch_bounds__(256) pair_join(const __grid_constant__ PairParams p) {
   const int at = blockIdx.x * 256 + threadIdx.x, row = at / 64, col = at % 64 * 4;
-  if constexpr (MODE != kLayer) wait_previous();
-  const Extent x = extent_of<MODE>(p, 1);
-  if (MODE != kLayer && x.whole + (int)blockIdx.y >= x.tiles_m * p.tiles_n) return;
   int tm, tn;
+  if constexpr (MODE == kSum) {  // as many tiles as the device made of the rows that count
+    wait_previous();
+    const Extent x = extent_of<MODE>(p, p.n_pairs);
+    if (x.splits == 1) return;
+    for (int t = blockIdx.y; x.whole + t < x.tiles_m * x.tiles_n; t += gridDim.y) {
+      pair_tile(p, x, x.whole + t, tm, tn);
+      const long long i = tm * 256ll + row;
+      const int j = tn * 256 + col;
+      if (i < x.M && j < p.N) sum_parts(p, p.partial + (long long)t * x.splits * 65536 + row * 256 + col, x.splits, i, j);
+    }
+    return;
+  }
+  const Extent x = extent_of<kLayer>(p, 1);
   pair_tile(p, x, x.whole + blockIdx.y, tm, tn);
   const long long i = tm * 256ll + row;
   const int j = tn * 256 + col;
-  if constexpr (MODE == kLayer) wait_previous();
+  wait_previous();
   if (i >= x.M || j >= p.N) return;
   const float* part = p.partial + (long long)blockIdx.y * p.splits * 65536 + row * 256 + col;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1295,28 +1403,6 @@ __global__ void __launch_bounds__(256) pair_join(const __grid_constant__ PairPar
   }
   const Epilogue& e = p.e;
   float f[4] = {sum.x, sum.y, sum.z, sum.w};
-  if constexpr (MODE == kSum) {
-    float* acc = p.h.acc + i * p.h.ldacc + j;
-    if (!p.h.first) {
-      const float4 a = *reinterpret_cast<const float4*>(acc);
-      f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
-    }
-    if (!p.h.last) {
-      *reinterpret_cast<float4*>(acc) = make_float4(f[0], f[1], f[2], f[3]);
-      return;
-    }
-    const float unit = *p.h.unit;
-    const long long to = p.h.index[i] * e.ldy + j;
-    if (e.vec) {
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(e.y) + to) =
-          make_uint2(pack16(f[0] * unit, f[1] * unit, e.half), pack16(f[2] * unit, f[3] * unit, e.half));
-    } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (j + c < p.N) store16(e.y, to + c, e.half, f[c] * unit);
-    }
-    return;
-  }
   if (!e.vec) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
@@ -1346,7 +1432,6 @@ __global__ void __launch_bounds__(256) pair_join(const __grid_constant__ PairPar
 // Host side
 // ================================================================================================
 constexpr int kStreamCtas = 152;  // most CTAs of stream_gemm (one per SM); bounds the partials
-constexpr int kPairs = 76;        // pairs of CTAs that tiles are split for
 
 // A 16-bit matrix of `outer` rows of `inner` elements, boxes of 64 x box_outer, 128-byte swizzle.  The element type
 // only names the width: the copies do no arithmetic and the fill is zero.
@@ -1469,6 +1554,7 @@ inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, const Sp
   if (n_pairs < 1) return PSR_ERR_CUDA;
   PairParams p = {};
   p.h = head;
+  p.n_pairs = n_pairs;
   p.M = o.M;
   p.N = o.N;
   p.n_k = (o.K + kBK - 1) / kBK;
@@ -1480,11 +1566,12 @@ inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, const Sp
   p.group = 16;  // (8192 x 28672 x 4096 in 967 us; 8, 12, 24, 32 rows: 987, 976, 984, 1010)
   p.whole = (int)items;
   p.splits = 1;
+  p.partial = l.partial;  // (dx: for kPairs parts, whatever the device makes of its tiles)
+  if (MODE == kSum && (size_t)kPairs * 65536 * 4 > l.partial_bytes) return PSR_ERR_ARG;
   if (!wide && split.rest > 0) {
     p.whole = (int)split.whole;
     p.split_k = (p.n_k + split.parts - 1) / split.parts;
     p.splits = (p.n_k + p.split_k - 1) / p.split_k;  // none of them empty
-    p.partial = l.partial;
     if ((size_t)split.rest * p.splits * 65536 * 4 > l.partial_bytes) return PSR_ERR_ARG;
     items = split.whole + split.rest * p.splits;
   }
@@ -1502,22 +1589,25 @@ inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, const Sp
     items += p.halves;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * (items < n_pairs ? items : n_pairs)));
+  cfg.gridDim = dim3((unsigned)(2 * (items < n_pairs && !(MODE == kSum && head.rows) ? items : n_pairs)));
   cfg.blockDim = dim3(pair_threads(MODE));
   cfg.dynamicSmemBytes = kPairSmem;
   cfg.stream = l.st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = MODE == kLayer ? 1 : 2;
   if (cudaLaunchKernelEx(&cfg, pair_gemm<AMN, BMN, HALF, MODE>, p, ma, mb) != cudaSuccess) {
     cudaGetLastError();
     return PSR_ERR_CUDA;
   }
   l.clear = nullptr;
+  if (MODE == kSum) return launch_after(pair_join<MODE>, dim3(64, 8), 256, p, l.st);
   if (p.splits == 1) return PSR_OK;
   return launch_after(pair_join<MODE>, dim3(64, (unsigned)split.rest), 256, p, l.st);
 }
@@ -1583,11 +1673,31 @@ inline int launch_stream(const Operands& o, const Epilogue& e, Launch& l, const 
   const bool ok_w = WMN ? tmap16(&mw, o.b, o.N, o.K, o.ldb, 64) : tmap16(&mw, o.b, o.K, o.N, o.ldb, kRows);
   if (!ok_w || !tmap16(&mx, o.a, o.K, o.M, o.lda, p.tb)) return PSR_ERR_CUDA;
   const unsigned grid = (unsigned)((units + per - 1) / per);
-  stream_gemm<WMN, MODE><<<grid, kStreamThreads, kStreamSmem, l.st>>>(p, mw, mx);
-  const int rc = launch_status();
-  l.clear = nullptr;
-  if (rc != PSR_OK || per % p.n_k == 0) return rc;
-  return launch_after(stream_join<MODE>, dim3((unsigned)p.n_tiles, (unsigned)o.M), 128, p, l.st);
+  if constexpr (MODE == kLayer) {
+    stream_gemm<WMN, MODE><<<grid, kStreamThreads, kStreamSmem, l.st>>>(p, mw, mx);
+    const int rc = launch_status();
+    l.clear = nullptr;
+    if (rc != PSR_OK || per % p.n_k == 0) return rc;
+    return launch_after(stream_join<MODE>, dim3((unsigned)p.n_tiles, (unsigned)o.M), 128, p, l.st);
+  } else {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kStreamThreads);
+    cfg.dynamicSmemBytes = kStreamSmem;
+    cfg.stream = l.st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = l.clear ? 0 : 1;  // (the call's first kernel clears the control block)
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, stream_gemm<WMN, MODE>, p, mw, mx) != cudaSuccess) {
+      cudaGetLastError();
+      return PSR_ERR_CUDA;
+    }
+    l.clear = nullptr;
+    if (per % p.n_k == 0) return PSR_OK;
+    return launch_after(head_join<MODE>, dim3(grid, (unsigned)((o.M + 15) / 16)), 128, p, l.st);
+  }
 }
 
 // ------------------------------------------------------------------------------------------------

@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ RowPa
 // ------------------------------------------------------------------------------------------------
 // One row: dot products
 // ------------------------------------------------------------------------------------------------
-// Bound by reading W once.  A warp takes rows of W in turn, a lane 16 bytes of one at a time with kAhead of them in flight; its first
-// lane keeps the sum of exponentials.
+// Bound by reading W once.  A warp takes rows of W in turn, a lane 16 bytes of one at a time, and asks for the piece kAhead further on, in
+// the next row perhaps, as it takes one; its lanes keep the sum of exponentials.
 constexpr int kDotThreads = 512;
 
 struct DotParams {
@@ -214,21 +214,26 @@ __global__ void __launch_bounds__(kDotThreads, 2) dot_kernel(const __grid_consta
   const int64_t target = *p.target;
   const T* x = static_cast<const T*>(p.x);
   ExpSum e = {-FLT_MAX, 0.f};
-  float sum = 0.f;
-  for (int j = blockIdx.x * (kDotThreads / 32) + warp; j < p.V; j += n_warps) {
-    const T* row = static_cast<const T*>(p.w) + j * p.ldw;
-    float acc = 0.f;
-    for (int k0 = 0; k0 < p.K; k0 += 256 * kAhead) {
-      uint4 v[kAhead];
+  float sum = 0.f, acc = 0.f;
+  // the piece asked for next and the one taken next, each by row and first column
+  int row_in = blockIdx.x * (kDotThreads / 32) + warp, k_in = lane * 8, row = row_in, k = k_in;
+  uint4 v[kAhead];
+  auto load = [&](int a) {
+    v[a] = make_uint4(0, 0, 0, 0);
+    if (row_in < p.V && k_in < p.K) v[a] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(p.w) + row_in * p.ldw + k_in));
+    k_in += 256;
+    if (k_in - lane * 8 >= p.K) {
+      k_in = lane * 8;
+      row_in += n_warps;
+    }
+  };
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        const int k = k0 + a * 256 + lane * 8;
-        if (k < p.K) v[a] = __ldcs(reinterpret_cast<const uint4*>(row + k));
-      }
+  for (int a = 0; a < kAhead; ++a) load(a);
+  while (row < p.V) {
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        const int k = k0 + a * 256 + lane * 8;
-        if (k >= p.K) break;
+    for (int a = 0; a < kAhead; ++a) {
+      if (row >= p.V) break;
+      if (k < p.K) {
         const uint4 u = *reinterpret_cast<const uint4*>(x + k);
         const uint32_t f[4] = {u.x, u.y, u.z, u.w}, g[4] = {v[a].x, v[a].y, v[a].z, v[a].w};
 #pragma unroll
@@ -240,13 +245,19 @@ __global__ void __launch_bounds__(kDotThreads, 2) dot_kernel(const __grid_consta
           acc = fmaf(ah, bh, acc);
         }
       }
-    }
+      load(a);
+      k += 256;
+      if (k - lane * 8 < p.K) continue;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    const float ref = exp_ref(e.r, acc);
-    e = {ref, e.s * ex2_approx(e.r - ref) + ex2_approx(fmaf(acc, kLog2e, -ref))};
-    sum += acc;
-    if (j == target && lane == 0) *p.at = acc;
+      for (int o = 16; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+      const float ref = exp_ref(e.r, acc);
+      e = {ref, e.s * ex2_approx(e.r - ref) + ex2_approx(fmaf(acc, kLog2e, -ref))};
+      sum += acc;
+      if (row == target && lane == 0) *p.at = acc;
+      acc = 0.f;
+      k = lane * 8;
+      row += n_warps;
+    }
   }
   if (lane == 0) {
     part[warp] = make_float2(e.r, e.s);
@@ -285,9 +296,15 @@ struct FinishParams {
   float* lse;
 };
 
-__device__ __forceinline__ void add_group(ExpSum& e, float2 g) {
-  const float ref = fmaxf(e.r, g.x);
-  e = {ref, e.s * ex2_approx(e.r - ref) + g.y * ex2_approx(g.x - ref)};
+// e and the sums g, some of which may be no group's.
+template <int N>
+__device__ __forceinline__ void add_groups(ExpSum& e, const float2 (&g)[N]) {
+  float ref = e.r, s = 0.f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) ref = fmaxf(ref, g[k].x);
+#pragma unroll
+  for (int k = 0; k < N; ++k) s = fmaf(g[k].y, ex2_approx(g[k].x - ref), s);
+  e = {ref, fmaf(e.s, ex2_approx(e.r - ref), s)};
 }
 
 __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ FinishParams p) {
@@ -301,11 +318,22 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Fin
   ExpSum e = {-FLT_MAX, 0.f};
   float sum = 0.f;
   if (i < rows) {
-#pragma unroll 8
-    for (int g = g0; g < p.groups; g += p.lanes) {
-      const long long from = g * p.group_at + i * p.row_at;
-      add_group(e, p.stats[from]);
-      if (p.sums) sum += p.sums[from];
+    constexpr int N = 8;  // groups in flight
+    for (int first = g0; first < p.groups; first += N * p.lanes) {
+      float2 g[N];
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int at = first + k * p.lanes;
+        g[k] = at < p.groups ? p.stats[at * p.group_at + i * p.row_at] : make_float2(-FLT_MAX, 0.f);
+      }
+      if (p.sums) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const int at = first + k * p.lanes;
+          if (at < p.groups) sum += p.sums[at * p.group_at + i * p.row_at];
+        }
+      }
+      add_groups(e, g);
     }
   }
   part[threadIdx.x] = make_float2(e.r, e.s);
@@ -315,7 +343,8 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Fin
     if (g0 < n) {
       const int with = threadIdx.x + n * per;
       ExpSum a = {part[threadIdx.x].x, part[threadIdx.x].y};
-      add_group(a, part[with]);
+      const float2 g[1] = {part[with]};
+      add_groups(a, g);
       part[threadIdx.x] = make_float2(a.r, a.s);
       part_sum[threadIdx.x] += part_sum[with];
     }
@@ -330,9 +359,9 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Fin
       return;
     }
   }
-  // one thread a row: 64 bits cost nothing, and the difference of two numbers near one another keeps its digits
+  // the difference of two numbers near one another, in 64 bits
   const float2 f = part[r];
-  const double lse = (f.x + log2((double)f.y)) * 0.69314718055994530942;
+  const double lse = ((double)f.x + log2f(f.y)) * 0.69314718055994530942;
   double loss = lse - (1.0 - p.smoothing) * p.at[i];
   if (p.z > 0.f) loss += p.z * lse * lse;  // (0 times infinity would be none)
   if (p.sums) loss -= p.smoothing / (double)p.V * part_sum[r];
@@ -352,7 +381,7 @@ struct Sizes {
   long long ldx, ldw;      // rows of x and w, as given
   long long ldxc, ldd, ldacc;
   int groups, pieces, piece;
-  Split split;             // of a piece's dx
+  Split all;               // of dx: the device's choice
   size_t sums_bytes;
   size_t head, index, target, coef, at, stats, logit_sums, partial, x, w, slope, acc, total;
 };
@@ -392,15 +421,14 @@ static int sizes(const psr_xent_shape* sh, bool backward, Sizes& s) {
   s.pieces = 1;
   s.piece = (int)V;
   s.sums_bytes = s.few ? partial_bytes((int)M, (int)V, (int)K, false) : 0;
-  s.split = {0, 0, 1, 0.0};
+  s.all = {((M + 255) / 256) * ((K + 255) / 256), 0, 1, 0.0};
   if (backward) {
     if (!s.few) {
       const long long most = std::max((long long)kPieceLeast, kPieceBytes / (2 * Mk) / 512 * 512);
       s.pieces = (int)((V + most - 1) / most);
       if (s.pieces > 1) s.piece = (int)(((V + s.pieces - 1) / s.pieces + 511) / 512 * 512);
       s.pieces = (int)((V + s.piece - 1) / s.piece);
-      s.split = split_of((int)M, (int)K, s.piece);
-      s.sums_bytes = (size_t)s.split.rest * s.split.parts * 65536 * 4;
+      s.sums_bytes = (size_t)kPairs * 65536 * 4;  // parts of split tiles of dx: no more than pairs
     } else {
       s.sums_bytes = std::max(s.sums_bytes, partial_bytes((int)M, (int)K, (int)V, false));
     }
@@ -577,7 +605,7 @@ static int backward(const psr_xent_shape* sh, const Sizes& s, const float* dloss
       e.vec = flat && aligned_to(dx, 16);
       const Operands o = {slope, s.ldd, wp, ldw, M, K, n};
       if (s.few) rc = launch_stream<true, kSum>(o, e, l, h);
-      else rc = launch_pair<false, true, HALF, kSum>(o, e, !s.split.rest && wide_tiles<false, true>(o, 3000.0, s.split, l.n_sm / 2), s.split, l, h);
+      else rc = launch_pair<false, true, HALF, kSum>(o, e, false, s.all, l, h);
       if (rc != PSR_OK) return rc;
     }
   }
