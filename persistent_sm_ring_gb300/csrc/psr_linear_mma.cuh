@@ -945,36 +945,36 @@ __global__ void __launch_bounds__(pair_threads(MODE), 1)
 #pragma unroll
         for (int q = 0; q < kGroup / 32; ++q)
           head_store<MODE, HALF>(p, x.M, stage, i0, it.tn * 256 + cgroup * kGroup + q * 32, q, row, sum[q]);
-        continue;
-      }
+      } else {
 #pragma unroll 1
-      for (int b = 0; b < 2 * it.n && ok; ++b) {
-        const uint32_t slot = u % 2;
-        const int j0 = it.tn * 256 + (b / 2) * 256 + cgroup * 64 + (b % 2) * 32;
-        uint4 rr[4];
-        if (res && it.split < 0)  // in flight while the sums are waited for
-          rows_in(rr, static_cast<const uint8_t*>(e.res) + ((long long)i0 * e.ldr + j0) * 2, e.ldr * 2, x.M - i0, (p.N - j0) / 8);
-        if (b % 2 == 0) {
-          ok = __all_sync(0xffffffffu, wait_own(&sc.acc_full[slot], (u / 2) & 1u, p, &sc, SITE_ACC));
-          if (!ok) break;
-          tc_fence_after();
-        }
-        uint32_t v[32];
-        tmem_ld32(sc.tmem_base + ((uint32_t)(quarter * 32) << 16) + slot * 256 + cgroup * 64 + (b % 2) * 32, v);
-        tmem_ld_wait();
-        if (b % 2 == 1) {  // this warp's share of the half is in registers
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (rank == 0) mbar_arrive(&sc.acc_empty[slot]);
-            else arrive_far(mapa_shared(smem_u32(&sc.acc_empty[slot]), 0));
+        for (int b = 0; b < 2 * it.n && ok; ++b) {
+          const uint32_t slot = u % 2;
+          const int j0 = it.tn * 256 + (b / 2) * 256 + cgroup * 64 + (b % 2) * 32;
+          uint4 rr[4];
+          if (res && it.split < 0)  // in flight while the sums are waited for
+            rows_in(rr, static_cast<const uint8_t*>(e.res) + ((long long)i0 * e.ldr + j0) * 2, e.ldr * 2, x.M - i0, (p.N - j0) / 8);
+          if (b % 2 == 0) {
+            ok = __all_sync(0xffffffffu, wait_own(&sc.acc_full[slot], (u / 2) & 1u, p, &sc, SITE_ACC));
+            if (!ok) break;
+            tc_fence_after();
           }
-          ++u;
+          uint32_t v[32];
+          tmem_ld32(sc.tmem_base + ((uint32_t)(quarter * 32) << 16) + slot * 256 + cgroup * 64 + (b % 2) * 32, v);
+          tmem_ld_wait();
+          if (b % 2 == 1) {  // this warp's share of the half is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (rank == 0) mbar_arrive(&sc.acc_empty[slot]);
+              else arrive_far(mapa_shared(smem_u32(&sc.acc_empty[slot]), 0));
+            }
+            ++u;
+          }
+          if (it.split >= 0)
+            partial_store(p, it.split, stage, (int)rank * kRows + quarter * 32, cgroup * 64 + (b % 2) * 32, x.M - i0, v);
+          else if constexpr (MODE == kLayer) pair_store<!BMN, HALF>(e, x.M, p.N, stage, i0, j0, v, rr);
+          else head_store<MODE, HALF>(p, x.M, stage, i0, j0, 0, row, v);
         }
-        if (it.split >= 0)
-          partial_store(p, it.split, stage, (int)rank * kRows + quarter * 32, cgroup * 64 + (b % 2) * 32, x.M - i0, v);
-        else if constexpr (MODE == kLayer) pair_store<!BMN, HALF>(e, x.M, p.N, stage, i0, j0, v, rr);
-        else head_store<MODE, HALF>(p, x.M, stage, i0, j0, 0, row, v);
       }
     }
     if (!ok) sc.abort = 1;
@@ -1069,15 +1069,15 @@ __device__ __forceinline__ void head_tokens(const StreamParams& p, int i0, int n
       const long long to = j0 / 32 * p.h.group_at + (i0 + i) * p.h.row_at;
       p.h.stats[to] = make_float2(ref, s[0]);
       if (p.h.sums) p.h.sums[to] = sum;
-      const int64_t target = p.h.ids[(i0 + i) * p.h.step] - p.h.col0 - j0;
-      if (target >= 0 && target < cols) p.h.at[i0 + i] = row[target];
+      const uint64_t target = (uint64_t)p.h.ids[(i0 + i) * p.h.step] - (uint64_t)(p.h.col0 + j0);
+      if (target < (uint64_t)cols) p.h.at[i0 + i] = row[target];
     }
   } else if constexpr (MODE == kSlope) {
     __syncwarp();
     if (lane < n) {  // the tokens' coefficients and targets, 16 bytes and 4 to each
       reinterpret_cast<float4*>(rows)[lane] = p.h.coef[i0 + lane];
-      const int64_t target = p.h.ids[(i0 + lane) * p.h.step] - p.h.col0 - j0;
-      reinterpret_cast<int*>(rows)[64 + lane] = target >= 0 && target < 32 ? (int)target : -1;
+      const uint64_t target = (uint64_t)p.h.ids[(i0 + lane) * p.h.step] - (uint64_t)(p.h.col0 + j0);
+      reinterpret_cast<int*>(rows)[64 + lane] = target < 32 ? (int)target : -1;
     }
     __syncwarp();
 #pragma unroll

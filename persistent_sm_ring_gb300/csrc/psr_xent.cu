@@ -36,6 +36,8 @@ struct RowParams {
   long long ldxc;
   int M, V, K, vec;  // vec: x's rows are 16-byte aligned
   int per;           // rows of a block, at most 256
+  // of each block's rows: those that count, the largest |g| and |g (1 + 2 z lse)|; null: each block looks at all rows itself
+  float4* sums;
   int packed;        // else every row stays where it is, and those that do not count are zeros
   const int64_t* targets;
   long long step, ignore;
@@ -59,6 +61,42 @@ struct RowParams {
 __device__ __forceinline__ int64_t target_of(const RowParams& p, long long i) { return p.targets[i * p.step]; }
 __device__ __forceinline__ bool counts(const RowParams& p, int64_t t) { return t >= 0 && t < p.V && t != p.ignore; }
 
+// A row's |g| and |g (1 + 2 z lse)|, as far as finite.
+__device__ __forceinline__ void most_of(const RowParams& p, long long i, float& most, float& scaled) {
+  const float g = fabsf(p.dloss[i * p.dstep]), a = fabsf(g * (1.f + 2.f * p.z * p.lse_in[i]));
+  if (g <= FLT_MAX) most = fmaxf(most, g);
+  if (a <= FLT_MAX) scaled = fmaxf(scaled, a);
+}
+
+// Of many rows: what each of rows_kernel's blocks has, so that none has to look at them all (M^2 / 256 targets: 4 ms at 10^6 rows).
+constexpr int kScanMost = 16384;
+template <bool BWD>
+__global__ void __launch_bounds__(256) block_kernel(const __grid_constant__ RowParams p) {
+  __shared__ float most_warp[8], scaled_warp[8];
+  clear_ctrl(p.clear);
+  const long long i = blockIdx.x * 256ll + threadIdx.x;
+  const bool in = i < p.M && counts(p, target_of(p, i));
+  float most = 0.f, scaled = 0.f;
+  if (BWD && in) most_of(p, i, most, scaled);
+  const int n = __syncthreads_count(in);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    scaled = fmaxf(scaled, __shfl_xor_sync(0xffffffffu, scaled, o));
+  }
+  if (threadIdx.x % 32 == 0) {
+    most_warp[threadIdx.x / 32] = most;
+    scaled_warp[threadIdx.x / 32] = scaled;
+  }
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int w = 1; w < 8; ++w) {
+    most = fmaxf(most, most_warp[w]);
+    scaled = fmaxf(scaled, scaled_warp[w]);
+  }
+  p.sums[blockIdx.x] = make_float4((float)n, most, scaled, 0.f);
+}
+
 // The slopes are multiplied by a power of two over the largest g (1 - s) on their way into 16 bits, and the sums of products by its
 // inverse: the target's share of the row with the largest g is then a power of two and rounds to itself, and fp16, which ends at
 // 2^-24, holds p down to 2^-37 of it.
@@ -67,13 +105,19 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ RowPa
   __shared__ int n_warp[8], place[256];
   __shared__ float most_warp[8], scaled_warp[8];
   clear_ctrl(p.clear);
+  launch_dependents();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const long long r0 = (long long)blockIdx.x * p.per;
   const int rows = (int)min((long long)p.per, p.M - r0);
   int before = 0;
   if (p.packed) {
+    if (p.sums) {
 #pragma unroll 4
-    for (long long i = threadIdx.x; i < r0; i += 256) before += counts(p, target_of(p, i));
+      for (int b = threadIdx.x; b < (int)blockIdx.x; b += 256) before += (int)p.sums[b].x;
+    } else {
+#pragma unroll 4
+      for (long long i = threadIdx.x; i < r0; i += 256) before += counts(p, target_of(p, i));
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
     if (lane == 0) n_warp[warp] = before;
@@ -100,13 +144,18 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ RowPa
 
   if constexpr (BWD) {
     float most = 0.f, scaled = 0.f;
+    if (p.sums) {
 #pragma unroll 4
-    for (long long i = threadIdx.x; i < p.M; i += 256)
-      if (counts(p, target_of(p, i))) {
-        const float g = fabsf(p.dloss[i * p.dstep]), a = fabsf(g * (1.f + 2.f * p.z * p.lse_in[i]));
-        if (g <= FLT_MAX) most = fmaxf(most, g);
-        if (a <= FLT_MAX) scaled = fmaxf(scaled, a);
+      for (int b = threadIdx.x; b < (int)gridDim.x; b += 256) {
+        const float4 f = p.sums[b];
+        most = fmaxf(most, f.y);
+        scaled = fmaxf(scaled, f.z);
       }
+    } else {
+#pragma unroll 4
+      for (long long i = threadIdx.x; i < p.M; i += 256)
+        if (counts(p, target_of(p, i))) most_of(p, i, most, scaled);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
@@ -383,7 +432,7 @@ struct Sizes {
   int groups, pieces, piece;
   Split all;               // of dx: the device's choice
   size_t sums_bytes;
-  size_t head, index, target, coef, at, stats, logit_sums, partial, x, w, slope, acc, total;
+  size_t head, row_sums, index, target, coef, at, stats, logit_sums, partial, x, w, slope, acc, total;
 };
 
 static int sizes(const psr_xent_shape* sh, bool backward, Sizes& s) {
@@ -408,6 +457,7 @@ static int sizes(const psr_xent_shape* sh, bool backward, Sizes& s) {
     return at;
   };
   s.head = take(true, 256);
+  s.row_sums = take(M > kScanMost, (M + 255) / 256 * 16);
   s.index = take(!s.few, M * 4);
   s.target = take(!s.few, M * 4);
   s.coef = take(backward, M * 16);
@@ -420,7 +470,7 @@ static int sizes(const psr_xent_shape* sh, bool backward, Sizes& s) {
   s.w = take(odd_w, V * ((K + 7) / 8 * 8) * 2);
   s.pieces = 1;
   s.piece = (int)V;
-  s.sums_bytes = s.few ? partial_bytes((int)M, (int)V, (int)K, false) : 0;
+  s.sums_bytes = s.few && !s.dot ? partial_bytes((int)M, (int)V, (int)K, false) : 0;
   s.all = {((M + 255) / 256) * ((K + 255) / 256), 0, 1, 0.0};
   if (backward) {
     if (!s.few) {
@@ -467,7 +517,8 @@ static int launch_rows(const psr_xent_shape* sh, const Sizes& s, RowParams& p, b
   p.V = sh->V;
   p.K = sh->K;
   p.vec = sh->K % 8 == 0 && aligned_to(x, 16) && (sh->M == 1 || s.ldx % 8 == 0);
-  p.per = std::min(256, std::max(8, (sh->M + 1023) / 1024));
+  p.per = sh->M > kScanMost ? 256 : std::max(8, (sh->M + 1023) / 1024);
+  p.sums = in<float4>(ws, s.row_sums);
   p.packed = !s.few;
   p.targets = targets;
   p.step = sh->targets_step;
@@ -482,6 +533,13 @@ static int launch_rows(const psr_xent_shape* sh, const Sizes& s, RowParams& p, b
   p.half = sh->type == PSR_F16;
   p.clear = l.clear;
   const unsigned grid = (unsigned)((sh->M + p.per - 1) / p.per);
+  if (p.sums) {
+    if (backward) block_kernel<true><<<grid, 256, 0, l.st>>>(p);
+    else block_kernel<false><<<grid, 256, 0, l.st>>>(p);
+    p.clear = l.clear = nullptr;
+    const int rc = launch_status();
+    if (rc != PSR_OK) return rc;
+  }
   if (backward) rows_kernel<true><<<grid, 256, 0, l.st>>>(p);
   else rows_kernel<false><<<grid, 256, 0, l.st>>>(p);
   l.clear = nullptr;

@@ -149,6 +149,9 @@ def test_views_and_broadcasts(psr):
         check_gradients(dx, dw, g, x, w, t, lse, "bf16", "views")
         same = torch.tensor([4]).cuda().expand(M)
         check_loss(*psr.linear_xent(x, w, same)[:2], x, w, same, "one target")
+        odd = [torch.empty(n * K + 1, dtype=x.dtype, device="cuda")[1:].view(n, K) for n in (M, V)]  # off every boundary
+        psr.linear_xent_bwd(g, x, w, t, lse, dx=odd[0], dw=odd[1])
+        assert torch.equal(odd[0], dx) and torch.equal(odd[1], dw)
 
 
 @pytest.mark.parametrize("M", [3, 100])
