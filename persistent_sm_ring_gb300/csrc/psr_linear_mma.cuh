@@ -328,7 +328,7 @@ struct PairSmem {
 
 // A product's rows, K steps and tiles: the host's, or (rows that count) what the device makes of their number.
 struct Extent {
-  int M, n_k, wide, tiles_m, tiles_n, whole, splits, split_k, halves;  // as in PairParams
+  int M, n_k, wide, tiles_m, tiles_n, whole, splits, split_k, halves;  // as in PairParams, which stand for themselves (X below)
 };
 
 // What a pair computes next: `n` 256-column halves from column half tn on of tile row tm, K steps k0 .. k0 + n_k.  split: the part
@@ -339,7 +339,8 @@ struct PairItem {
 
 // Tile t -> (row block, column block): groups of `group` tile rows, columns inside a group, rows fastest, so that the
 // tiles in flight at once share few rows of either operand and a group's rows of A stay in L2.
-__device__ __forceinline__ void pair_tile(const PairParams& p, const Extent& x, int t, int& tm, int& tn) {
+template <class X>
+__device__ __forceinline__ void pair_tile(const PairParams& p, const X& x, int t, int& tm, int& tn) {
   const int per = p.group * x.tiles_n, g = t / per, r = t - g * per;
   const int rows = min(p.group, x.tiles_m - g * p.group);
   tn = r / rows;
@@ -350,7 +351,8 @@ __device__ __forceinline__ void pair_tile(const PairParams& p, const Extent& x, 
 // half of the pairs would have one, are dealt out as 256-column halves (256 tiles of 512 columns on 76 pairs: three rounds and
 // a half, not four).  Rounds shifted by half a tile between pairs, so that some write while others multiply, were
 // slower: the tile loads leave L2 no room for the outputs (4096^3 with gelu 100 to 118 us).
-__device__ __forceinline__ bool pair_item(const PairParams& p, const Extent& x, int pair, int n_pairs, int i, PairItem& it) {
+template <class X>
+__device__ __forceinline__ bool pair_item(const PairParams& p, const X& x, int pair, int n_pairs, int i, PairItem& it) {
   const long long n = (long long)x.tiles_m * x.tiles_n, at = pair + (long long)i * n_pairs;
   it.k0 = 0;
   it.n_k = x.n_k;
@@ -552,7 +554,7 @@ __host__ __device__ inline int last_halves(long long tiles, int pairs) {
 template <int MODE>
 __device__ __forceinline__ Extent extent_of(const PairParams& p, int n_pairs) {
   Extent x = {p.M, p.n_k, p.wide, p.tiles_m, p.tiles_n, p.whole, p.splits, p.split_k, p.halves};
-  if (MODE == kLayer || !p.h.rows) return x;
+  if (!p.h.rows) return x;
   const int rows = *p.h.rows;
   if (MODE == kWeight) {
     x.n_k = (rows + kBK - 1) / kBK;
@@ -581,6 +583,12 @@ __device__ __forceinline__ Extent extent_of(const PairParams& p, int n_pairs) {
   if (x.wide) x.halves = last_halves(tiles, n_pairs);
   else x.whole = min(x.whole, tiles);
   return x;
+}
+
+template <int MODE>
+__device__ __forceinline__ decltype(auto) pair_extent(const PairParams& p, int n_pairs) {
+  if constexpr (MODE == kLayer) return (p);
+  else return extent_of<MODE>(p, n_pairs);
 }
 
 // What a thread keeps of its row over the blocks of its columns.
@@ -793,7 +801,7 @@ __global__ void __launch_bounds__(pair_threads(MODE), 1)
 
   const int pair = blockIdx.x / 2, n_pairs = gridDim.x / 2;
   if constexpr (MODE != kLayer) wait_previous();  // the loss's kernels begin while the one before ends
-  const Extent x = extent_of<MODE>(p, n_pairs);
+  auto&& x = pair_extent<MODE>(p, n_pairs);
   const uint32_t full0 = __shfl_sync(0xffffffffu, mapa_shared(smem_u32(&sc.full[0]), 0), 0);  // of the pair's first CTA
   PairItem it;
   if (warp == 0) {  // the whole warp, for the same reason as the next one
@@ -1388,12 +1396,11 @@ __global__ void __launch_bounds__(256) pair_join(const __grid_constant__ PairPar
     }
     return;
   }
-  const Extent x = extent_of<kLayer>(p, 1);
-  pair_tile(p, x, x.whole + blockIdx.y, tm, tn);
+  pair_tile(p, p, p.whole + blockIdx.y, tm, tn);
   const long long i = tm * 256ll + row;
   const int j = tn * 256 + col;
   wait_previous();
-  if (i >= x.M || j >= p.N) return;
+  if (i >= p.M || j >= p.N) return;
   const float* part = p.partial + (long long)blockIdx.y * p.splits * 65536 + row * 256 + col;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
