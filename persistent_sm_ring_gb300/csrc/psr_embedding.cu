@@ -307,7 +307,7 @@ __device__ __forceinline__ void put_row(const SumParams& p, uint32_t id, int k, 
 }
 
 template <class T, int E, int U>
-__global__ void __launch_bounds__(256, 3) sum_kernel(const __grid_constant__ SumParams p) {
+__global__ void __launch_bounds__(256, E >= 4 ? 3 : 4) sum_kernel(const __grid_constant__ SumParams p) {
   constexpr int R = 4;
   __shared__ union {
     ZeroSmem zero;

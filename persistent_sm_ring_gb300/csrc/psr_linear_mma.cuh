@@ -1324,24 +1324,28 @@ __global__ void __launch_bounds__(128) stream_join(const __grid_constant__ Strea
   if (j < p.N) finish(p.e, i, j, sum);
 }
 
-// The same for the loss's modes: a block for sixteen tokens of the tile in which CTA blockIdx.x of the product began, if it is the first
+constexpr int kJoinTokens = 4;  // of a block of head_join that has nothing to reduce
+// The same for the loss's modes: a block for sixteen or four tokens of the tile in which CTA blockIdx.x of the product began, if it is the first
 // to begin inside of it.  (A block for each token of every tile took 20 us at 48 tokens and 1000 tiles, of which 150 are split.)
 template <int MODE>
 __global__ void __launch_bounds__(128) head_join(const __grid_constant__ StreamParams p) {
   __shared__ __align__(16) float rows[4][16][kSumPitch];
   const long long u = (long long)blockIdx.x * p.per_cta;
-  const int tile = (int)(u / p.n_k), i0 = blockIdx.y * 16, n = min(16, p.M - i0), warp = threadIdx.x / 32;
+  const int tile = (int)(u / p.n_k), warp = threadIdx.x / 32;
+  constexpr int kTokens = MODE == kStats ? 16 : kJoinTokens;
+  const int i0 = blockIdx.y * kTokens, n = min(kTokens, p.M - i0);
   wait_previous();
   if (u % p.n_k == 0 || u - p.per_cta > (long long)tile * p.n_k) return;
   const long long b = (long long)tile * p.n_k;
   const int c0 = (int)(b / p.per_cta), c1 = (int)((b + p.n_k - 1) / p.per_cta);
+  constexpr int kAhead = MODE == kStats ? 2 : 4;  // parts in flight
   float sum[16] = {};
-#pragma unroll 2
+#pragma unroll kAhead
   for (int g = c0; g <= c1; ++g) {
     const int slot = 2 * g + ((long long)g * p.per_cta >= b ? 0 : 1);
     const float* part = p.partial + ((long long)slot * p.tb + i0) * kRows + threadIdx.x;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) sum[e] += e < n ? part[e * kRows] : 0.f;
+    for (int e = 0; e < kTokens; ++e) sum[e] += e < n ? part[e * kRows] : 0.f;
   }
   uint32_t v[16];
 #pragma unroll
@@ -1703,7 +1707,8 @@ inline int launch_stream(const Operands& o, const Epilogue& e, Launch& l, const 
     }
     l.clear = nullptr;
     if (per % p.n_k == 0) return PSR_OK;
-    return launch_after(head_join<MODE>, dim3(grid, (unsigned)((o.M + 15) / 16)), 128, p, l.st);
+    constexpr int tokens = MODE == kStats ? 16 : kJoinTokens;
+    return launch_after(head_join<MODE>, dim3(grid, (unsigned)((o.M + tokens - 1) / tokens)), 128, p, l.st);
   }
 }
 
