@@ -52,7 +52,8 @@ __device__ __forceinline__ void add_to(float* acc, const Raw<T, E>& x) {
 // ------------------------------------------------------------------------------------------------
 // Lookup
 // ------------------------------------------------------------------------------------------------
-// Memory bound.  A warp takes 32 * kAhead vectors of a row, all of them in flight at once.
+// Memory bound.  A warp takes 32 * kAhead vectors of a row, all of them in flight at once (16421 tokens of 4096 bf16 columns from
+// 128000 rows: 33 us, 5.7 TB/s, of which the written half alone takes 30 at the 4.4 TB/s that memory writes; 32 tokens of 8192: 4 us).
 constexpr int kAhead = 4;
 
 template <class T, int E>
@@ -89,8 +90,11 @@ __global__ void __launch_bounds__(256)
 // A cluster of CTAs sorts (id, position) pairs by up to nine bits a pass, least significant first.  Each warp has a
 // contiguous share of the pairs and counts its digits; the counts before it (of smaller digits, of earlier CTAs and warps) are
 // where its pairs go, equal digits in their order.  Ids outside the table, and the padding id, become V: they end up behind all
-// others.
-constexpr int kSortCtasMost = 8, kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortBits = 9, kBins = 1 << kSortBits;
+// others.  One kernel, so that the next one's zeros begin with it: 13 us for 2047 tokens, 16 for 16384 (two passes), 17 for 65539 of
+// 260 ids (one), bound by the latencies of its rounds and, beyond, by the scattered stores of all pairs from eight SMs.  Sixteen CTAs,
+// a size that has to be asked for, took 15 us for 65539, but the kernel behind them then began only at their end (16384 tokens into
+// 128000 rows 264 us instead of 244); separate kernels over all SMs took 12, and the kernel behind them began late, too (285).
+constexpr int kSortCtas = 8, kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortBits = 9, kBins = 1 << kSortBits;
 
 struct Tokens {
   const int64_t* ids;
@@ -127,7 +131,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
   launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.n_long = 0;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t rank = cluster_ctarank(), ctas = gridDim.x;  // one cluster
+  const uint32_t rank = cluster_ctarank(), ctas = kSortCtas;
   const long long share = (((long long)p.t.M + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
   const long long i0 = ((long long)rank * kSortWarps + warp) * share;
   const long long i1 = min((long long)p.t.M, i0 + share);
@@ -176,8 +180,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
     uint32_t all = 0, before = 0;
     if (threadIdx.x < bins) {
 #pragma unroll
-      for (uint32_t c = 0; c < (uint32_t)kSortCtasMost; ++c) {
-        if (c >= ctas) break;
+      for (uint32_t c = 0; c < ctas; ++c) {
         const uint32_t n = ld_shared_cluster(mapa_shared(smem_u32(&sm.total[threadIdx.x]), c));
         if (c < rank) before += n;
         all += n;
@@ -275,8 +278,9 @@ __device__ void zero_rows(const Tokens& t, uint8_t* dw, long long row_bytes, uin
 // ------------------------------------------------------------------------------------------------
 // Sums of the rows of each id
 // ------------------------------------------------------------------------------------------------
-// Memory bound.  A warp takes a block of sorted positions and 32 * E * U columns, reads R rows at a time and writes a row of dw
-// where the id changes.  A run of equal ids that crosses one border between blocks belongs to the block where it begins.  A longer
+// Memory bound: 65539 rows of 1001 fp32 columns in 53 us (5 TB/s; rows off 16-byte boundaries, 128 bytes to a load); 16384 rows of 4096
+// beside the zeros of 128000 in 236, which the writes take alone.  A warp takes a block of sorted positions and 32 * E * U columns,
+// reads R rows at a time and writes a row of dw where the id changes.  A run of equal ids that crosses one border between blocks belongs to the block where it begins.  A longer
 // one is long: each of its blocks leaves its sum in a partial row of its own (the one where it begins in its second, the others in
 // their first), and join_kernel adds them up.
 constexpr int kBlockMost = 64;  // positions of a block
@@ -531,41 +535,40 @@ struct Sizes {
   size_t n_long, a, b, longs, partial, total;
 };
 
-// CTAs of the sort's cluster on the current device (0: an error), and the rest of its launch.  Sixteen are more than every device
-// has to take, so it is asked; the sort of 65539 tokens takes @ us with them and @ with eight.
-static int sort_ctas(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr) {
+static int launch_sort(const SortParams& p, cudaStream_t st) {
   static std::mutex mu;
-  static int known[64] = {};
+  static bool known[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PSR_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (dev >= 64 || !known[dev]) {
+      if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SortSmem)) != cudaSuccess) {
+        cudaGetLastError();
+        return PSR_ERR_CUDA;
+      }
+      if (dev < 64) known[dev] = true;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kSortCtas);
   cfg.blockDim = dim3(kSortThreads);
   cfg.dynamicSmemBytes = sizeof(SortSmem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kSortCtas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  std::lock_guard<std::mutex> lk(mu);
-  int ctas = dev < 64 ? known[dev] : 0;
-  if (!ctas) {
-    if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SortSmem)) != cudaSuccess) {
-      cudaGetLastError();
-      return 0;
-    }
-    ctas = 8;
-    if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
-      int n = 0;
-      cfg.gridDim = dim3(kSortCtasMost);
-      attr[0].val.clusterDim.x = kSortCtasMost;
-      if (cudaOccupancyMaxActiveClusters(&n, sort_kernel, &cfg) == cudaSuccess && n > 0) ctas = kSortCtasMost;
-    }
-    cudaGetLastError();
-    if (dev < 64) known[dev] = ctas;
-  }
-  attr[0].val.clusterDim.x = ctas;
-  return ctas;
+  if (cudaLaunchKernelEx(&cfg, sort_kernel, p) == cudaSuccess) return PSR_OK;
+  cudaGetLastError();
+  return PSR_ERR_CUDA;
 }
 
-// Positions of a block: as many as leave every SM 16 warps, between 8 and 64.
+// Positions of a block: as many as leave every SM 16 warps, between 8 and 64.  Shorter blocks cost more starts than they balance
+// (65539 rows of 1001 columns in blocks of 64, 32, 16: 93, 101, 122 us).
 static Sizes sizes(const psr_embedding_shape* sh) {
   Sizes s;
   const long long warps = (long long)sh->M * ((sh->K + 511) / 512);
@@ -649,16 +652,7 @@ int psr_embedding_bwd(const psr_embedding_shape* sh, const void* dy, const int64
   q.passes = (bits + kSortBits - 1) / kSortBits;
   q.bits = (bits + q.passes - 1) / q.passes;
   q.clear = reinterpret_cast<Ctrl*>(ws);
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  const int ctas = sort_ctas(cfg, attr);
-  if (ctas == 0) return PSR_ERR_CUDA;
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.stream = st;
-  if (cudaLaunchKernelEx(&cfg, sort_kernel, q) != cudaSuccess) {
-    cudaGetLastError();
-    return PSR_ERR_CUDA;
-  }
+  if ((rc = launch_sort(q, st)) != PSR_OK) return rc;
 
   SumParams p = {};
   p.sorted = q.a;

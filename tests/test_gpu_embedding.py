@@ -142,6 +142,22 @@ def test_gradient_leaves_out_and_adds(psr, t):
     check_gradient(dw, dy, ids, V, t, "padding", 1.0, 7)
 
 
+def test_gradient_of_a_table_of_many_bits(psr):
+    """Ids of 29 bits are sorted in four passes."""
+    need_gpu()
+    g = torch.Generator().manual_seed(8)
+    V, M = (1 << 28) + 5, 5000
+    ids = torch.randint(0, V, (M // 5,), generator=g).repeat(5)[torch.randperm(M, generator=g)]
+    ids[0], ids[1] = V - 1, 0
+    dy = randn(g, (M, 1), "f32")
+    dw, _ = psr.embedding_bwd(dy, ids.cuda(), V)
+    named, at = torch.unique(ids, return_inverse=True)
+    ref, _, size = ends.embedding_bwd(f64(dy), at.tolist(), len(named))
+    check(dw[named.cuda()], ref, 8 * 2.0**-24 * size, "named rows")
+    dw[named.cuda()] = 0
+    assert not dw.any()
+
+
 def test_gradient_of_no_tokens(psr):
     need_gpu()
     dw = torch.full((5, 24), 3.0, dtype=torch.bfloat16, device="cuda")

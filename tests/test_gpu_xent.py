@@ -293,6 +293,28 @@ def test_streams_and_graphs(psr, M):
         check_gradients(dx, dw, g, x, w, t, lse, "bf16", f"replay {drop}")
 
 
+def test_two_calls_at_once(psr):
+    """Calls of different sizes on two streams, each with a workspace of its own, give the bits that they give alone."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(17)
+    sets = [inputs(gen, M, V, 128, "bf16", 0.2) for M, V in ((40, 9000), (700, 5000))]
+    streams = [torch.cuda.Stream() for _ in sets]
+
+    def run(i, stream):
+        x, w, t, g = sets[i]
+        loss, lse, _ = psr.linear_xent(x, w, t, stream=stream)
+        dx, dw, _ = psr.linear_xent_bwd(g, x, w, t, lse, stream=stream)
+        de, _ = psr.embedding_bwd(dx, t, len(w), dw=dw.clone() if stream is None else None, stream=stream)
+        return loss, lse, dx, dw, de
+    alone = [run(i, None) for i in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        both = [run(i, streams[i]) for i in range(2)]
+        torch.cuda.synchronize()
+        for a, b in zip(alone, both):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
 def test_the_two_ends_with_one_table(psr):
     """Tokens to rows, rows to a loss, and back: a table shared by both ends gets both gradients."""
     need_gpu()
