@@ -616,6 +616,9 @@ def _heads_strides(t, name, written=False):
 
 def _span(t):
     """First byte and the byte past the last of a tensor's elements."""
+    if t.is_contiguous():
+        first = t.data_ptr()
+        return first, first + t.numel() * t.element_size()
     last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
     return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
 
@@ -639,21 +642,23 @@ def _check_apart(out, x, what, same_ok, kinds="an output overlaps an input"):
 
 def _check_outputs(what, outs, inputs, workspace=None):
     """Outputs passed in, and the workspace, share no memory with the inputs or one another."""
-    outs = [t for t in outs if t is not None]
-    for i, out in enumerate(outs):
-        for x in inputs:
-            if x is not None:
+    outs = [(t, *_span(t)) for t in outs if t is not None]
+    if not outs and workspace is None:
+        return
+    inputs = [(t, *_span(t)) for t in inputs if t is not None]
+    for i, (out, a, b) in enumerate(outs):  # most are apart by their first and last bytes
+        for x, c, d in inputs:
+            if a < d and c < b:
                 _check_apart(out, x, what, False)
-        for other in outs[:i]:
-            _check_apart(out, other, what, False, "the outputs overlap")
+        for other, c, d in outs[:i]:
+            if a < d and c < b:
+                _check_apart(out, other, what, False, "the outputs overlap")
     if workspace is not None:
         first = workspace.data_ptr()  # contiguous, or refused later
         past = first + workspace.numel() * workspace.element_size()
-        for x in (*inputs, *outs):
-            if x is not None and x.numel() > 0:
-                a, b = _span(x)
-                if a < past and first < b:
-                    raise ValueError(f"{what}: the workspace overlaps a tensor")
+        for x, a, b in (*inputs, *outs):
+            if a < past and first < b and x.numel() > 0:
+                raise ValueError(f"{what}: the workspace overlaps a tensor")
 
 
 def _check_other(out, x, what, kinds):
