@@ -140,6 +140,8 @@ def load(trace: bool = False, variant: str = "") -> ctypes.CDLL:
 
     One library per process: the first call decides which."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -495,34 +497,41 @@ def gemm_rs(a, w, *, partition=None, workspace=None, out=None, stream=None):
 # These calls run on their tensors' device whatever the current one is.  Memory that a call makes
 # (outputs and workspaces not passed in) belongs to the stream the call runs on.
 
+_torch = _raw = None  # the module and its C part, imported by the first call
+
+
 class _Launch:
     """The device and stream of a call: makes the device current, and the stream while memory is made."""
     __slots__ = ("torch", "device", "stream", "handle", "other", "back")
 
     def __init__(self, device, stream, what):
-        import torch
-        self.torch, self.device, self.stream = torch, device, stream
+        global _torch, _raw
+        if _torch is None:
+            import torch
+            _torch, _raw = torch, torch._C
+        self.torch, self.device, self.stream = _torch, device, stream
         if stream is not None and stream.device != device:
             raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {device}")
 
     def __enter__(self):
         # the raw getters: torch.cuda.current_stream() alone takes longer than a small call's kernel
-        raw, index = self.torch._C, self.device.index
-        self.back = raw._cuda_getDevice()
-        if self.back != index:
-            self.torch.cuda.set_device(index)
-        current = raw._cuda_getCurrentRawStream(index)
+        index = self.device.index
+        back = _raw._cuda_getDevice()
+        self.back = None if back == index else back
+        if back != index:
+            _torch.cuda.set_device(index)
+        current = _raw._cuda_getCurrentRawStream(index)
         self.handle = current if self.stream is None else self.stream.cuda_stream
         self.other = self.handle != current
         return self
 
     def __exit__(self, *exc):
-        if self.back != self.device.index:
-            self.torch.cuda.set_device(self.back)
+        if self.back is not None:
+            _torch.cuda.set_device(self.back)
 
     def empty(self, shape, dtype):
         if not self.other:
-            return self.torch.empty(shape, dtype=dtype, device=self.device)
+            return _torch.empty(shape, dtype=dtype, device=self.device)
         with self.torch.cuda.stream(self.stream):
             return self.torch.empty(shape, dtype=dtype, device=self.device)
 
