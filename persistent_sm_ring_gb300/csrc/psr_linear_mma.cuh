@@ -1715,20 +1715,57 @@ inline int launch_stream(const Operands& o, const Epilogue& e, Launch& l, const 
 // ------------------------------------------------------------------------------------------------
 // An operand with rows of any stride, from any address, into rows on 16-byte boundaries
 // ------------------------------------------------------------------------------------------------
+// Eight elements from any (even) address, `n` of them in the row; zeros for the others.  Two aligned vectors that hold them all are
+// shifted to their place where those lie in the matrix, which has its bytes from `first` to `past`; at its two ends, and at the end of a
+// row, the elements are read one by one.
+__device__ __forceinline__ uint4 load8(const uint16_t* p, int n, const uint8_t* first, const uint8_t* past) {
+  const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) % 16);
+  const uint8_t* base = reinterpret_cast<const uint8_t*>(p) - off;
+  if (n >= 8 && base >= first && base + 32 <= past) {
+    const uint4 lo = *reinterpret_cast<const uint4*>(base);
+    uint4 hi = make_uint4(0, 0, 0, 0);
+    if (off) hi = *reinterpret_cast<const uint4*>(base + 16);
+    uint32_t w[7] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z};
+    const uint32_t last = hi.w;
+    uint32_t v[6];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) v[j] = off & 8 ? w[j + 2] : w[j];
+    v[5] = off & 8 ? last : w[5];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) w[j] = off & 4 ? v[j + 1] : v[j];
+    const uint32_t bits = off % 4 * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                      __funnelshift_r(w[3], w[4], bits));
+  }
+  uint32_t e[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) e[j] = j < n ? p[j] : 0;
+  return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+}
+
+// Memory bound.
 template <class T>
 __global__ void __launch_bounds__(256)
     align_kernel(const T* __restrict__ x, long long ld, uint4* __restrict__ y, int rows, int cols, Ctrl* clear) {
   clear_ctrl(clear);
-  const int per = (cols + 7) / 8;
-  const long long n = (long long)rows * per;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
-    const long long r = i / per;
-    const int c = (int)(i - r * per) * 8;
-    const T* p = x + r * ld + c;
-    uint32_t e[8];
+  constexpr int kAhead = 4;
+  const uint32_t per = (cols + 7) / 8;
+  const long long n = (long long)rows * per, step = gridDim.x * 256ll;
+  const uint8_t* first = reinterpret_cast<const uint8_t*>(x);
+  const uint8_t* past = reinterpret_cast<const uint8_t*>(x + (rows - 1ll) * ld + cols);
+  for (long long i0 = blockIdx.x * 256ll + threadIdx.x; i0 < n; i0 += kAhead * step) {
+    uint4 v[kAhead];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = c + j < cols ? p[j] : 0;
-    y[i] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+    for (int a = 0; a < kAhead; ++a) {
+      const long long i = i0 + a * step;
+      if (i >= n) break;
+      const long long r = n < 1ll << 32 ? (uint32_t)i / per : i / per;
+      const int c = (int)(i - r * per) * 8;
+      v[a] = load8(x + r * ld + c, cols - c, first, past);
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (i0 + a * step < n) y[i0 + a * step] = v[a];
   }
 }
 

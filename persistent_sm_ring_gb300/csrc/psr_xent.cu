@@ -212,12 +212,9 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ RowPa
 #pragma unroll 4
         for (int c = lane; c < chunks; c += 32) row[c] = reinterpret_cast<const uint4*>(from)[c];
       } else {
-        for (int c = lane; c < chunks; c += 32) {
-          uint32_t e[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) e[j] = c * 8 + j < p.K ? from[c * 8 + j] : 0;
-          row[c] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-        }
+        const uint8_t* first = reinterpret_cast<const uint8_t*>(p.x);
+        const uint8_t* past = reinterpret_cast<const uint8_t*>(p.x + (p.M - 1ll) * p.ldx + p.K);
+        for (int c = lane; c < chunks; c += 32) row[c] = load8(from + c * 8, p.K - c * 8, first, past);
       }
     } else {
       if (!p.packed) clear_row(i);
