@@ -53,7 +53,7 @@ __device__ __forceinline__ void add_to(float* acc, const Raw<T, E>& x) {
 // Lookup
 // ------------------------------------------------------------------------------------------------
 // Memory bound.  A warp takes 32 * kAhead vectors of a row, all of them in flight at once (16421 tokens of 4096 bf16 columns from
-// 128000 rows: 33 us, 5.7 TB/s, of which the written half alone takes 30 at the 4.4 TB/s that memory writes; 32 tokens of 8192: 4 us).
+// 128000 rows: 33 us, 5.8 TB/s; two vectors 35, eight 34; 32 tokens of 8192: 4 us).
 constexpr int kAhead = 4;
 
 template <class T, int E>
@@ -80,7 +80,13 @@ __global__ void __launch_bounds__(256)
     if (k >= K) break;
 #pragma unroll
     for (int e = 0; e < E; ++e) x[a].v[e] = from_f32<T>(ok ? to_f32(x[a].v[e]) * scale : __int_as_float(0x7FC00000));
-    *reinterpret_cast<Vec<T, E>*>(dst + k) = x[a];
+    if constexpr (sizeof(Vec<T, E>) == 16) {
+      uint4 q;
+      memcpy(&q, &x[a], 16);
+      __stcs(reinterpret_cast<uint4*>(dst + k), q);
+    } else {
+      *reinterpret_cast<Vec<T, E>*>(dst + k) = x[a];
+    }
   }
 }
 
@@ -90,10 +96,10 @@ __global__ void __launch_bounds__(256)
 // A cluster of CTAs sorts (id, position) pairs by up to nine bits a pass, least significant first.  Each warp has a
 // contiguous share of the pairs and counts its digits; the counts before it (of smaller digits, of earlier CTAs and warps) are
 // where its pairs go, equal digits in their order.  Ids outside the table, and the padding id, become V: they end up behind all
-// others.  One kernel, so that the next one's zeros begin with it: 13 us for 2047 tokens, 16 for 16384 (two passes), 17 for 65539 of
-// 260 ids (one), bound by the latencies of its rounds and, beyond, by the scattered stores of all pairs from eight SMs.  Sixteen CTAs,
-// a size that has to be asked for, took 15 us for 65539, but the kernel behind them then began only at their end (16384 tokens into
-// 128000 rows 264 us instead of 244); separate kernels over all SMs took 12, and the kernel behind them began late, too (285).
+// others.  One kernel, so that the next one's zeros begin with it: 10 us for 2049 tokens, 14 for 16384 (two passes), 17 for 65539 of
+// 260 ids (one), bound by the latencies of its rounds and, beyond, by the scattered stores of all pairs from eight SMs.  Separate kernels
+// over all SMs took 12 for 65539, but of several kernels in a row only one begins early: 16384 tokens into 128000 rows took 285 us
+// where the cluster took 244.
 constexpr int kSortCtas = 8, kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortBits = 9, kBins = 1 << kSortBits;
 
 struct Tokens {
@@ -217,12 +223,41 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
   }
 }
 
+// Few tokens: each finds its place by comparing itself with all others, (id, position) as one number, four threads to a token.  No
+// passes and no exchange between blocks: 5 us for 2047 tokens, where the cluster takes 10 (the whole call with 1000 rows of 512 columns
+// 9.8 and 13.6 us, with 10 tokens 4.3 and 9.3).  The comparisons grow as M^2, and beyond kRankMost the keys do not fit in 32 bits.
+constexpr int kRankBits = 11, kRankMost = 1 << kRankBits, kRankTokens = 64;  // tokens of a block
+
+__global__ void __launch_bounds__(4 * kRankTokens) rank_kernel(const __grid_constant__ SortParams p) {
+  __shared__ __align__(16) uint32_t keys[kRankMost];
+  clear_ctrl(p.clear);
+  launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.n_long = 0;
+  const int M = p.t.M, padded = (M + 15) / 16 * 16;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < padded; i += 4 * kRankTokens) keys[i] = i < M ? key_of(p.t, i) << kRankBits | (uint32_t)i : 0xffffffffu;
+  __syncthreads();
+  const int token = blockIdx.x * kRankTokens + threadIdx.x / 4;
+  const uint32_t own = token < M ? keys[token] : 0;
+  int rank = 0;
+#pragma unroll 4
+  for (int i = threadIdx.x % 4 * 4; i < padded; i += 16) {
+    const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+    rank += (k.x < own) + (k.y < own) + (k.z < own) + (k.w < own);
+  }
+  rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+  rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+  if (token < M && threadIdx.x % 4 == 0) p.a[rank] = make_uint2(own >> kRankBits, (uint32_t)token);
+}
+
 // ------------------------------------------------------------------------------------------------
 // Zeros for the rows that no token names
 // ------------------------------------------------------------------------------------------------
-// Memory alone takes 4.0 to 4.5 TB/s of writes (a fill of 1 GiB 268 us), where it reads and writes 6.8 in all: one CTA to an SM
-// writes the zeros by bulk copies of its own, beside the sort and the sums.  It marks the ids among its rows first.  Each has every
-// n-th 32 rows, so that what all write at a time lies together.
+// Memory bound.  CTAs of their own write the zeros by bulk copies, beside the sort and the sums, and mark the ids among their rows first.
+// Three to an SM, as many as fit: 16384 tokens into 128000 rows of 4096 in 188 us (1.18 GB at 6.3 TB/s), with two 215, with one 244 (a fill of
+// the library's writes 4.0 TB/s).  Each has every n-th 32 rows, so that what all write at a time lies together; nothing reads the zeros soon,
+// so they are the first to leave L2 (2047 tokens into 50021 rows of 1736: 36.7 us instead of 39).
+constexpr int kZeroCtas = 3;
 constexpr int kZeroBytes = 8192;  // what one copy of zeros writes
 constexpr int kMarks = 32768;     // rows that a CTA marks at a time
 struct ZeroSmem {
@@ -231,14 +266,16 @@ struct ZeroSmem {
 };
 
 // `n` bytes of zeros (an even number, from an even address) by a warp; odd ends by hand.
-__device__ __forceinline__ void zero_bytes(uint8_t* at, long long n, uint32_t zeros) {
+__device__ __forceinline__ void zero_bytes(uint8_t* at, long long n, uint32_t zeros, uint64_t policy) {
   const int lane = threadIdx.x % 32;
   long long head = (16 - (long long)(reinterpret_cast<uintptr_t>(at) % 16)) % 16;
   if (head > n) head = n;
   if (2 * lane < head) *reinterpret_cast<uint16_t*>(at + 2 * lane) = 0;
   const long long body = (n - head) / 16 * 16, tail = n - head - body;
   for (long long i = lane * (long long)kZeroBytes; i < body; i += 32ll * kZeroBytes)
-    bulk_store(at + head + i, zeros, (uint32_t)min((long long)kZeroBytes, body - i));
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group.L2::cache_hint [%0], [%1], %2, %3;" ::"l"(at + head + i), "r"(zeros),
+                 "r"((uint32_t)min((long long)kZeroBytes, body - i)), "l"(policy)
+                 : "memory");
   if (2 * lane < tail) *reinterpret_cast<uint16_t*>(at + n - tail + 2 * lane) = 0;
 }
 
@@ -247,6 +284,8 @@ __device__ void zero_rows(const Tokens& t, uint8_t* dw, long long row_bytes, uin
   const uint32_t zeros = smem_u32(sm.zeros);
   for (int i = threadIdx.x; i < kZeroBytes / 16; i += 256) sm.zeros[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
+  uint64_t policy;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
   for (uint32_t w0 = 0; w0 < own; w0 += kMarks / 32) {
     const uint32_t n = min(own - w0, (uint32_t)kMarks / 32);
     for (uint32_t i = threadIdx.x; i < n; i += 256) sm.marks[i] = 0;
@@ -265,7 +304,7 @@ __device__ void zero_rows(const Tokens& t, uint8_t* dw, long long row_bytes, uin
         const int first = __ffs(left) - 1;
         const uint32_t rest = ~(left >> first);
         const int run = rest ? __ffs(rest) - 1 : 32;
-        zero_bytes(dw + (v + first) * row_bytes, run * row_bytes, zeros);
+        zero_bytes(dw + (v + first) * row_bytes, run * row_bytes, zeros, policy);
         left = first + run == 32 ? 0 : left >> (first + run) << (first + run);
       }
     }
@@ -279,7 +318,7 @@ __device__ void zero_rows(const Tokens& t, uint8_t* dw, long long row_bytes, uin
 // Sums of the rows of each id
 // ------------------------------------------------------------------------------------------------
 // Memory bound: 65539 rows of 1001 fp32 columns in 53 us (5 TB/s; rows off 16-byte boundaries, 128 bytes to a load); 16384 rows of 4096
-// beside the zeros of 128000 in 236, which the writes take alone.  A warp takes a block of sorted positions and 32 * E * U columns,
+// in 105 beside the zeros of 128000.  A warp takes a block of sorted positions and 32 * E * U columns,
 // reads R rows at a time and writes a row of dw where the id changes.  A run of equal ids that crosses one border between blocks belongs to the block where it begins.  A longer
 // one is long: each of its blocks leaves its sum in a partial row of its own (the one where it begins in its second, the others in
 // their first), and join_kernel adds them up.
@@ -536,6 +575,10 @@ struct Sizes {
 };
 
 static int launch_sort(const SortParams& p, cudaStream_t st) {
+  if (p.t.M <= kRankMost && p.t.V < (1 << (32 - kRankBits)) - 1) {
+    rank_kernel<<<(unsigned)((p.t.M + kRankTokens - 1) / kRankTokens), 4 * kRankTokens, 0, st>>>(p);
+    return launch_status();
+  }
   static std::mutex mu;
   static bool known[64] = {};
   int dev = 0;
@@ -668,7 +711,7 @@ int psr_embedding_bwd(const psr_embedding_shape* sh, const void* dy, const int64
   p.block = s.block;
   p.blocks = s.blocks;
   p.accumulate = sh->accumulate;
-  p.zero_ctas = sh->accumulate ? 0 : std::min(n_sm, (sh->V + 31) / 32);
+  p.zero_ctas = sh->accumulate ? 0 : std::min(kZeroCtas * n_sm, (sh->V + 31) / 32);
   p.t = q.t;
   p.scale = sh->scale;
   const int e = vector_of(sh->type, sh->K, lddy, sh->K, dy, dw);
@@ -679,7 +722,7 @@ int psr_embedding_bwd(const psr_embedding_shape* sh, const void* dy, const int64
     const long long blocks = p.zero_ctas + ((long long)s.blocks * p.pieces + 7) / 8;
     if (blocks >= 1ll << 31) return (int)PSR_ERR_UNSUPPORTED;
     int r = launch_after(sum_kernel<T, E, U>, dim3((unsigned)blocks), 256, p, st);
-    const long long most = (long long)s.blocks / 2 * ((sh->K + 32 * E * UJ - 1) / (32 * E * UJ));  // a long run takes over two blocks
+    const long long most = (s.blocks - 1ll) / 2 * ((sh->K + 32 * E * UJ - 1) / (32 * E * UJ));  // a long run takes over two blocks
     if (r == PSR_OK && most > 0) r = launch_after(join_kernel<T, E, UJ>, dim3((unsigned)std::min(most, 6ll * n_sm)), 256, p, st);
     return r;
   });
