@@ -408,7 +408,9 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* m,
 __device__ __forceinline__ uint4* stage_chunk(uint8_t* stage, int row, int c) {
   return reinterpret_cast<uint4*>(stage + row * 64 + ((c ^ ((row >> 1) & 3)) * 16));
 }
-// 16-byte columns below `chunks` of rows below `rows`
+// 16-byte columns below `chunks` of rows below `rows`.  PASS: nothing reads them soon (the loss's dw: 40 rows of 32000 columns with
+// gradients 147 to 145 us).
+template <bool PASS = false>
 __device__ __forceinline__ void rows_out(uint8_t* stage, uint8_t* g, long long pitch, int rows, int chunks) {
   const int lane = threadIdx.x % 32, c = lane % 4;
   __syncwarp();
@@ -417,7 +419,10 @@ __device__ __forceinline__ void rows_out(uint8_t* stage, uint8_t* g, long long p
   for (int k = 0; k < 4; ++k) {
     const int r = k * 8 + lane / 4;
     const uint4 w = *stage_chunk(stage, r, c);
-    if (r < rows && c < chunks) *reinterpret_cast<uint4*>(g) = w;
+    if (r < rows && c < chunks) {
+      if constexpr (PASS) __stcs(reinterpret_cast<uint4*>(g), w);
+      else *reinterpret_cast<uint4*>(g) = w;
+    }
     g += 8 * pitch;
   }
   __syncwarp();
@@ -608,8 +613,8 @@ __device__ __forceinline__ void head_row(const PairParams& p, int M, int i, Head
   if constexpr (MODE == kSum) r.target = p.h.index[i];
 }
 
-// The block's 32 rows from i0 on, row `lane` in v, to e.y in 16 bits; SPREAD: to the row `to` of each.
-template <bool SPREAD, bool HALF>
+// The block's 32 rows from i0 on, row `lane` in v, to e.y in 16 bits; kSum: to the row `to` of each.
+template <int MODE, bool HALF>
 __device__ __forceinline__ void head_out(const Epilogue& e, int to, uint8_t* stage, int i0, int j0, int rows, int cols,
                                          const uint32_t (&v)[32]) {
   const int lane = threadIdx.x % 32;
@@ -622,9 +627,9 @@ __device__ __forceinline__ void head_out(const Epilogue& e, int to, uint8_t* sta
     *stage_chunk(stage, lane, j) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   uint16_t* g = static_cast<uint16_t*>(e.y) + j0;
-  if constexpr (!SPREAD) {
+  if constexpr (MODE != kSum) {
     g += (long long)i0 * e.ldy;
-    if (e.vec) rows_out(stage, reinterpret_cast<uint8_t*>(g), e.ldy * 2, rows, (cols + 7) / 8);
+    if (e.vec) rows_out<MODE == kWeight>(stage, reinterpret_cast<uint8_t*>(g), e.ldy * 2, rows, (cols + 7) / 8);
     else rows_out_odd(stage, g, e.ldy, rows, cols);
     return;
   }
@@ -709,7 +714,7 @@ __device__ __forceinline__ void head_store(const PairParams& p, int M, uint8_t* 
       for (int c = 0; c < 32; ++c)
         if (c == at) v[c] = __float_as_uint(__uint_as_float(v[c]) - row.coef.w);
     }
-    head_out<false, HALF>(p.e, 0, stage, i0, j0, rows, cols, v);
+    head_out<MODE, HALF>(p.e, 0, stage, i0, j0, rows, cols, v);
   } else {
     const int rows = min(32, M - i0);
     if (rows <= 0 || cols <= 0) return;
@@ -752,7 +757,7 @@ __device__ __forceinline__ void head_store(const PairParams& p, int M, uint8_t* 
     const float unit = *p.h.unit;
 #pragma unroll
     for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * unit);
-    head_out<MODE == kSum, HALF>(p.e, row.target, stage, i0, j0, rows, cols, v);
+    head_out<MODE, HALF>(p.e, row.target, stage, i0, j0, rows, cols, v);
   }
 }
 
