@@ -613,11 +613,38 @@ __device__ __forceinline__ void head_row(const PairParams& p, int M, int i, Head
   if constexpr (MODE == kSum) r.target = p.h.index[i];
 }
 
+// (the first to leave L2: nothing reads it soon)
+__device__ __forceinline__ void store_tile(const CUtensorMap* m, int x, int y, uint32_t src) {
+  asm volatile(
+      "{\n\t.reg .b64 p;\n\t"
+      "createpolicy.fractional.L2::evict_first.b64 p, 1.0;\n\t"
+      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%1, %2}], [%3], p;\n\t}\n" ::"l"(reinterpret_cast<uint64_t>(m)),
+      "r"(x), "r"(y), "r"(src)
+      : "memory");
+}
+
+// What pair_gemm has besides.  kWeight: up to kCopySteps K steps, where dw's stores bound it, a block goes out by one copy from the
+// staging area, whose swizzle is that of 64-byte rows (dw of 40 rows, 32000 x 2048, 33 to 26 us, 4.0 to 5 TB/s; the stores of the same
+// by threads keep the shared memory pipe 72 % busy).  With more steps the copies hold up the operands' (400 rows with both gradients 164
+// and 169 us).
+constexpr int kCopySteps = 2;
+template <int MODE>
+struct Out {};
+template <>
+struct Out<kWeight> {
+  CUtensorMap map;
+  int copies;
+};
+
 // The block's 32 rows from i0 on, row `lane` in v, to e.y in 16 bits; kSum: to the row `to` of each.
 template <int MODE, bool HALF>
-__device__ __forceinline__ void head_out(const Epilogue& e, int to, uint8_t* stage, int i0, int j0, int rows, int cols,
+__device__ __forceinline__ void head_out(const Epilogue& e, const Out<MODE>& out, int to, uint8_t* stage, int i0, int j0, int rows, int cols,
                                          const uint32_t (&v)[32]) {
   const int lane = threadIdx.x % 32;
+  if constexpr (MODE == kWeight) {  // the copy of the last block has read it
+    if (out.copies && lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t w[4];
@@ -625,6 +652,17 @@ __device__ __forceinline__ void head_out(const Epilogue& e, int to, uint8_t* sta
     for (int q = 0; q < 4; ++q)
       w[q] = pack16(__uint_as_float(v[j * 8 + 2 * q]), __uint_as_float(v[j * 8 + 2 * q + 1]), HALF);
     *stage_chunk(stage, lane, j) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if constexpr (MODE == kWeight) {
+    if (out.copies) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        store_tile(&out.map, j0, i0, smem_u32(stage));
+        bulk_commit();
+      }
+      return;
+    }
   }
   uint16_t* g = static_cast<uint16_t*>(e.y) + j0;
   if constexpr (MODE != kSum) {
@@ -653,7 +691,7 @@ __device__ __forceinline__ void head_out(const Epilogue& e, int to, uint8_t* sta
 
 // Block b of a warp's columns: 32 rows x 32 columns of sums at (i0, j0), row `lane` in v.
 template <int MODE, bool HALF>
-__device__ __forceinline__ void head_store(const PairParams& p, int M, uint8_t* stage, int i0, int j0, int b, HeadRow& row,
+__device__ __forceinline__ void head_store(const PairParams& p, const Out<MODE>& out, int M, uint8_t* stage, int i0, int j0, int b, HeadRow& row,
                                            uint32_t (&v)[32]) {
   const int lane = threadIdx.x % 32, i = i0 + lane, cols = min(32, p.N - j0);
   if constexpr (MODE == kStats) {
@@ -714,7 +752,7 @@ __device__ __forceinline__ void head_store(const PairParams& p, int M, uint8_t* 
       for (int c = 0; c < 32; ++c)
         if (c == at) v[c] = __float_as_uint(__uint_as_float(v[c]) - row.coef.w);
     }
-    head_out<MODE, HALF>(p.e, 0, stage, i0, j0, rows, cols, v);
+    head_out<MODE, HALF>(p.e, out, 0, stage, i0, j0, rows, cols, v);
   } else {
     const int rows = min(32, M - i0);
     if (rows <= 0 || cols <= 0) return;
@@ -757,14 +795,14 @@ __device__ __forceinline__ void head_store(const PairParams& p, int M, uint8_t* 
     const float unit = *p.h.unit;
 #pragma unroll
     for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * unit);
-    head_out<MODE, HALF>(p.e, row.target, stage, i0, j0, rows, cols, v);
+    head_out<MODE, HALF>(p.e, out, row.target, stage, i0, j0, rows, cols, v);
   }
 }
 
 template <bool AMN, bool BMN, bool HALF, int MODE = kLayer>
 __global__ void __launch_bounds__(pair_threads(MODE), 1)
     pair_gemm(const __grid_constant__ PairParams p, const __grid_constant__ CUtensorMap ma,
-              const __grid_constant__ CUtensorMap mb) {
+              const __grid_constant__ CUtensorMap mb, const __grid_constant__ Out<MODE> out) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ PairSmem sc;
   const uint32_t raw = smem_u32(smem_raw);
@@ -919,7 +957,7 @@ __global__ void __launch_bounds__(pair_threads(MODE), 1)
       if (MODE == kWeight && it.n_k == 0) {  // sums over no rows: nothing is multiplied, nothing signalled
         for (int b = 0; b < 2 * it.n; ++b) {
           uint32_t v[32] = {};
-          head_store<MODE, HALF>(p, x.M, stage, i0, it.tn * 256 + (b / 2) * 256 + cgroup * 64 + (b % 2) * 32, 0, row, v);
+          head_store<MODE, HALF>(p, out, x.M, stage, i0, it.tn * 256 + (b / 2) * 256 + cgroup * 64 + (b % 2) * 32, 0, row, v);
         }
         continue;
       }
@@ -957,7 +995,7 @@ __global__ void __launch_bounds__(pair_threads(MODE), 1)
         if (!ok) break;
 #pragma unroll
         for (int q = 0; q < kGroup / 32; ++q)
-          head_store<MODE, HALF>(p, x.M, stage, i0, it.tn * 256 + cgroup * kGroup + q * 32, q, row, sum[q]);
+          head_store<MODE, HALF>(p, out, x.M, stage, i0, it.tn * 256 + cgroup * kGroup + q * 32, q, row, sum[q]);
       } else {
 #pragma unroll 1
         for (int b = 0; b < 2 * it.n && ok; ++b) {
@@ -986,10 +1024,11 @@ __global__ void __launch_bounds__(pair_threads(MODE), 1)
           if (it.split >= 0)
             partial_store(p, it.split, stage, (int)rank * kRows + quarter * 32, cgroup * 64 + (b % 2) * 32, x.M - i0, v);
           else if constexpr (MODE == kLayer) pair_store<!BMN, HALF>(e, x.M, p.N, stage, i0, j0, v, rr);
-          else head_store<MODE, HALF>(p, x.M, stage, i0, j0, 0, row, v);
+          else head_store<MODE, HALF>(p, out, x.M, stage, i0, j0, 0, row, v);
         }
       }
     }
+    if (MODE == kWeight && lane == 0) bulk_wait<0>();  // dw has been written
     if (!ok) sc.abort = 1;
   }
   // Every tcgen05 op has completed before tensor memory is released.  Every load has landed then too, the products having
@@ -1108,6 +1147,10 @@ __device__ __forceinline__ void head_tokens(const StreamParams& p, int i0, int n
   }
 }
 
+// The slopes' product goes through W backwards: what the last one, the loss's, read at its end is still in L2.
+template <int MODE>
+__device__ __forceinline__ int backwards(int i, int n) { return MODE == kSlope ? n - 1 - i : i; }
+
 template <bool AMN, int MODE = kLayer>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     stream_gemm(const __grid_constant__ StreamParams p, const __grid_constant__ CUtensorMap mw,
@@ -1159,10 +1202,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       }
       if (lane == 0) mbar_expect_tx(&sc.full[s], stage_bytes);
       const uint32_t base = smem_base + s * stage_bytes;
-      const int wrow = tile * kRows;
+      const int wrow = backwards<MODE>(tile, p.n_tiles) * kRows, step = backwards<MODE>(ks, p.n_k);
 #pragma unroll
       for (int h = 0; h < kSub; ++h) {
-        const int k = (ks * kSub + h) * kBK;
+        const int k = (step * kSub + h) * kBK;
         const uint32_t dst = base + h * kHalf;
         if constexpr (AMN) {
           load_one(dst, &mw, wrow, k, &sc.full[s], lane == 0);
@@ -1173,7 +1216,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       }
 #pragma unroll
       for (int h = 0; h < kSub; ++h)
-        load_one(base + kSub * kHalf + h * x_bytes, &mx, (ks * kSub + h) * kBK, 0, &sc.full[s], lane == 0);
+        load_one(base + kSub * kHalf + h * x_bytes, &mx, (step * kSub + h) * kBK, 0, &sc.full[s], lane == 0);
       ++fills;
       if (++s == n_st) {
         s = 0;
@@ -1228,7 +1271,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       ok = __all_sync(0xffffffffu, wait_own(&sc.acc_full[slot], (seg / 2) & 1u, p, &sc, SITE_ACC));
       if (!ok) break;
       tc_fence_after();
-      const int j = tile * kRows + row;
+      const int first_row = backwards<MODE>(tile, p.n_tiles) * kRows, j = first_row + row;
       const bool whole = n == p.n_k;
       const float bias = whole && p.e.bias && j < p.N ? load16(p.e.bias, j, p.e.half) : 0.f;
       float* part = p.partial + (2ll * blockIdx.x + (u == u0 ? 0 : 1)) * p.tb * kRows + row;
@@ -1256,7 +1299,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           continue;
         }
         if constexpr (MODE != kLayer) {
-          head_tokens<MODE>(p, c, n_c, tile * kRows + quarter * 32, v, &sc.sums[quarter][0][0]);
+          head_tokens<MODE>(p, c, n_c, first_row + quarter * 32, v, &sc.sums[quarter][0][0]);
           continue;
         }
         // four tokens at a time, their residuals in flight together; each lane reads its own sums back
@@ -1355,7 +1398,7 @@ __global__ void __launch_bounds__(128) head_join(const __grid_constant__ StreamP
   uint32_t v[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(sum[e]);
-  head_tokens<MODE>(p, i0, n, tile * kRows + warp * 32, v, &rows[warp][0][0]);
+  head_tokens<MODE>(p, i0, n, backwards<MODE>(tile, p.n_tiles) * kRows + warp * 32, v, &rows[warp][0][0]);
 }
 
 // Four columns of dx from the parts of a split tile: the sums of earlier pieces, these, and the row's place in dx.
@@ -1462,6 +1505,19 @@ inline bool tmap16(CUtensorMap* m, const void* base, int inner, int outer, long 
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same for stores of 32 x 32, 64-byte swizzle.
+inline bool tmap16_out(CUtensorMap* m, void* base, int inner, int outer, long long ld) {
+  const auto encode = gemm::encode_tiled_fn();
+  if (!encode) return false;
+  if (outer == 1) ld = (inner + 7ll) / 8 * 8;
+  cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+  cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  cuuint32_t box[2] = {32, 32};
+  cuuint32_t es[2] = {1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The matrix's rows all start on 16-byte boundaries (what a tensor map needs).
@@ -1600,6 +1656,11 @@ inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, const Sp
   const bool ok_a = AMN ? tmap16(&ma, o.a, o.M, o.K, o.lda, 64) : tmap16(&ma, o.a, o.K, o.M, o.lda, kRows);
   const bool ok_b = BMN ? tmap16(&mb, o.b, o.N, o.K, o.ldb, 64) : tmap16(&mb, o.b, o.K, o.N, o.ldb, kRows);
   if (!ok_a || !ok_b) return PSR_ERR_CUDA;
+  Out<MODE> out = {};
+  if constexpr (MODE == kWeight) {
+    out.copies = e.vec && p.n_k <= kCopySteps;
+    if (out.copies && !tmap16_out(&out.map, e.y, o.N, o.M, e.ldy)) return PSR_ERR_CUDA;
+  }
   if (wide) {
     p.halves = last_halves(items, n_pairs);
     items += p.halves;
@@ -1618,7 +1679,7 @@ inline int launch_pair(const Operands& o, const Epilogue& e, bool wide, const Sp
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = MODE == kLayer ? 1 : 2;
-  if (cudaLaunchKernelEx(&cfg, pair_gemm<AMN, BMN, HALF, MODE>, p, ma, mb) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, pair_gemm<AMN, BMN, HALF, MODE>, p, ma, mb, out) != cudaSuccess) {
     cudaGetLastError();
     return PSR_ERR_CUDA;
   }

@@ -652,6 +652,14 @@ static int backward(const psr_xent_shape* sh, const Sizes& s, const float* dloss
     else rc = launch_pair<false, false, HALF, kSlope>(logits, e, false, whole, l, h);
     if (rc != PSR_OK) return rc;
     e.ldy = K;
+    if (dx) {  // before dw, which takes W's place in L2
+      e.y = dx;
+      e.vec = flat && aligned_to(dx, 16);
+      const Operands o = {slope, s.ldd, wp, ldw, M, K, n};
+      if (s.few) rc = launch_stream<true, kSum>(o, e, l, h);
+      else rc = launch_pair<false, true, HALF, kSum>(o, e, false, s.all, l, h);
+      if (rc != PSR_OK) return rc;
+    }
     if (dw) {
       uint16_t* to = static_cast<uint16_t*>(dw) + (long long)at * K;
       e.y = to;
@@ -659,14 +667,6 @@ static int backward(const psr_xent_shape* sh, const Sizes& s, const float* dloss
       const Operands o = {slope, s.ldd, p.xc, p.ldxc, n, K, M};
       const Split all = {((n + 255ll) / 256) * ((K + 255ll) / 256), 0, 1, 0.0};
       rc = launch_pair<true, true, HALF, kWeight>(o, e, wide_tiles<true, true>(o, 0.0, all, l.n_sm / 2), all, l, h);
-      if (rc != PSR_OK) return rc;
-    }
-    if (dx) {
-      e.y = dx;
-      e.vec = flat && aligned_to(dx, 16);
-      const Operands o = {slope, s.ldd, wp, ldw, M, K, n};
-      if (s.few) rc = launch_stream<true, kSum>(o, e, l, h);
-      else rc = launch_pair<false, true, HALF, kSum>(o, e, false, s.all, l, h);
       if (rc != PSR_OK) return rc;
     }
   }
