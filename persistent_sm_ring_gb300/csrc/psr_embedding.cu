@@ -717,7 +717,7 @@ int psr_embedding_bwd(const psr_embedding_shape* sh, const void* dy, const int64
   const int e = vector_of(sh->type, sh->K, lddy, sh->K, dy, dw);
   return dispatch(sh->type, e, [&](auto t, auto ec, auto uc) {
     using T = decltype(t);
-    constexpr int E = decltype(ec)::value, U = decltype(uc)::value, UJ = E >= 4 ? 1 : U;
+    constexpr int E = decltype(ec)::value, U = decltype(uc)::value, UJ = E >= 4 ? 1 : E == 1 ? 8 : U;
     p.pieces = (sh->K + 32 * E * U - 1) / (32 * E * U);
     const long long blocks = p.zero_ctas + ((long long)s.blocks * p.pieces + 7) / 8;
     if (blocks >= 1ll << 31) return (int)PSR_ERR_UNSUPPORTED;
