@@ -95,11 +95,12 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------------------------------------
 // A cluster of CTAs sorts (id, position) pairs by up to nine bits a pass, least significant first.  Each warp has a
 // contiguous share of the pairs and counts its digits; the counts before it (of smaller digits, of earlier CTAs and warps) are
-// where its pairs go, equal digits in their order.  Ids outside the table, and the padding id, become V: they end up behind all
-// others.  One kernel, so that the next one's zeros begin with it: 10 us for 2049 tokens, 14 for 16384 (two passes), 17 for 65539 of
-// 260 ids (one), bound by the latencies of its rounds and, beyond, by the scattered stores of all pairs from eight SMs.  Separate kernels
-// over all SMs took 12 for 65539, but of several kernels in a row only one begins early: 16384 tokens into 128000 rows took 285 us
-// where the cluster took 244.
+// where its pairs go, equal digits in their order: of 32 pairs, a word of shared memory for each digit gathers the lanes that have it
+// (with match.any 65539 tokens took 5 us longer).  Ids outside the table, and the padding id, become V: they end up behind all
+// others.  One kernel, so that the next one's zeros begin with it: 9 us for 2049 tokens, 13 for 16384 (two passes), 13 for 65539 of
+// 260 ids (one), bound by the latencies of its rounds: pairs brought into order in shared memory before they are stored, or more of them
+// in flight, are no faster.  Separate kernels over all SMs took 12 for 65539, but of several kernels in a row only one begins early: 16384
+// tokens into 128000 rows took 285 us where the cluster, before there were as many zero writers, took 244.
 constexpr int kSortCtas = 8, kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortBits = 9, kBins = 1 << kSortBits;
 
 struct Tokens {
@@ -120,6 +121,7 @@ struct SortParams {
 
 struct SortSmem {
   uint32_t hist[kSortWarps][kBins];
+  uint32_t lanes[kSortWarps][kBins];  // of a warp's 32 pairs, those with each digit
   uint32_t total[kBins];  // of this CTA, by digit; read by the others
   uint32_t base[kBins];
   uint32_t warp_sum[kSortWarps];
@@ -147,7 +149,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
     const uint2* src = (p.passes - pass) % 2 ? p.b : p.a;  // the last pass writes a
     uint2* dst = (p.passes - pass) % 2 ? p.a : p.b;
     const int shift = pass * p.bits;
-    for (uint32_t d = lane; d < bins; d += 32) sm.hist[warp][d] = 0;
+    for (uint32_t d = lane; d < bins; d += 32) sm.hist[warp][d] = sm.lanes[warp][d] = 0;
     __syncwarp();
     // calls f(whether there is a pair, the pair, its digit) for the warp's pairs, 32 at a time in order
     auto each = [&](auto f) {
@@ -209,13 +211,18 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
     }
     __syncthreads();
     each([&](bool in, uint2 x, uint32_t d) {
-      const uint32_t same = __match_any_sync(0xffffffffu, d);
-      uint32_t at = 0;
-      if (in) at = sm.base[d] + sm.hist[warp][d] + __popc(same & ((1u << lane) - 1));
+      if (in) atomicOr(&sm.lanes[warp][d], 1u << lane);
       __syncwarp();
+      uint32_t same = 0, n = 0;
       if (in) {
-        dst[at] = x;
-        if (lane == __ffs(same) - 1) sm.hist[warp][d] += __popc(same);
+        same = sm.lanes[warp][d];
+        n = sm.hist[warp][d];
+        dst[sm.base[d] + n + __popc(same & ((1u << lane) - 1))] = x;
+      }
+      __syncwarp();
+      if (in && lane == __ffs(same) - 1) {
+        sm.hist[warp][d] = n + __popc(same);
+        sm.lanes[warp][d] = 0;
       }
       __syncwarp();
     });
@@ -317,11 +324,11 @@ __device__ void zero_rows(const Tokens& t, uint8_t* dw, long long row_bytes, uin
 // ------------------------------------------------------------------------------------------------
 // Sums of the rows of each id
 // ------------------------------------------------------------------------------------------------
-// Memory bound: 65539 rows of 1001 fp32 columns in 53 us (5 TB/s; rows off 16-byte boundaries, 128 bytes to a load); 16384 rows of 4096
-// in 105 beside the zeros of 128000.  A warp takes a block of sorted positions and 32 * E * U columns,
-// reads R rows at a time and writes a row of dw where the id changes.  A run of equal ids that crosses one border between blocks belongs to the block where it begins.  A longer
-// one is long: each of its blocks leaves its sum in a partial row of its own (the one where it begins in its second, the others in
-// their first), and join_kernel adds them up.
+// Memory bound: 65539 rows of 1001 fp32 columns in 54 us (4.9 TB/s; rows off 16-byte boundaries, 128 bytes to a load), 16384 rows of 4096
+// with the zeros of 128000 in 177 (6.7 TB/s).  A warp takes a block of sorted positions and 32 * E * U columns, reads R rows at a time and
+// writes a row of dw where the id changes.  A run of equal ids that crosses one border between blocks belongs to the block where it
+// begins.  A longer one is long: each of its blocks leaves its sum in a partial row of its own (the one where it begins in its second,
+// the others in their first), and join_kernel adds them up.
 constexpr int kBlockMost = 64;  // positions of a block
 
 struct SumParams {
@@ -464,6 +471,7 @@ __global__ void __launch_bounds__(256, E >= 4 ? 3 : 4) sum_kernel(const __grid_c
 
 // Long runs: a CTA adds the partial rows of one up in 32 * E * U columns, its warps every eighth and then their sums in order.  (The
 // order of the list depends on the launch, the sums do not.)
+// (260 runs of 252 rows in 1001 columns: 12 us in pieces of 256 columns, 16 in pieces of 128.)
 template <class T, int E, int U>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ SumParams p) {
   __shared__ float sums[8][U][32 * E];
