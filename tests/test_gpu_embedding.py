@@ -124,6 +124,34 @@ def test_gradient_of_runs_of_every_length(psr, K, step):
     check_gradient(dw, dy, ids, 160, "bf16", str(K))
 
 
+@pytest.mark.parametrize("M,V", [(2048, 100), (2049, 100), (300, (1 << 21) - 2), (300, (1 << 21) - 1), (2048, (1 << 21) - 2)])
+def test_gradient_where_ranks_end(psr, M, V):
+    """Numbers of tokens and rows around those up to which tokens are ranked by comparison; nothing is written around dw."""
+    need_gpu()
+    g = torch.Generator().manual_seed(M + V)
+    ids = torch.randint(0, V, (M,), generator=g)
+    ids[: M // 3] = ids[torch.randint(0, M, (M // 3,), generator=g)]
+    ids[0], ids[1], ids[2] = V - 1, V, -1
+    dy = randn(g, (M, 8), "f32")
+    buffer = torch.full((V * 8 + 16,), 7.0, device="cuda")
+    dw = buffer[8:-8].view(V, 8)
+    psr.embedding_bwd(dy, ids.cuda(), V, dw=dw)
+    keep = (ids >= 0) & (ids < V)
+    named, at = torch.unique(ids[keep], return_inverse=True)
+    check_gradient(dw[named.cuda()], dy[keep.cuda()], at, len(named), "f32", "named rows")
+    dw[named.cuda()] = 0
+    assert not dw.any() and (buffer[:8] == 7).all() and (buffer[-8:] == 7).all()
+
+
+@pytest.mark.parametrize("K", [255, 257, 1001])
+def test_gradient_of_long_runs_of_odd_rows(psr, K):
+    need_gpu()
+    g = torch.Generator().manual_seed(K)
+    dy, ids = randn(g, (9000, K), "f32"), tokens(g, 9000, 20, "all")
+    dw, _ = psr.embedding_bwd(dy, ids, 20)
+    check_gradient(dw, dy, ids, 20, "f32", str(K))
+
+
 @pytest.mark.parametrize("t", ["bf16", "f16", "f32"])
 def test_gradient_leaves_out_and_adds(psr, t):
     need_gpu()

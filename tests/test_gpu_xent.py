@@ -253,6 +253,22 @@ def test_pieces_of_the_vocabulary(psr):
     assert not dx[~keep].any()
 
 
+@pytest.mark.parametrize("M", [40, 64, 65, 128, 129])
+def test_gradients_leave_what_stands_around_them(psr, M):
+    """Blocks of dx and dw that end inside a tile, in buffers whose other bytes stay as they were, with any number of rows that count."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(21 + M)
+    for V, K, drop in ((33, 8, 0.0), (300, 264, 0.5), (513, 40, 1.1)):
+        x, w, targets, g = inputs(gen, M, V, K, "bf16", drop)
+        _, lse, _ = psr.linear_xent(x, w, targets)
+        buffers = [torch.full((n * K + 128,), 7.0, dtype=x.dtype, device="cuda") for n in (M, V)]
+        dx, dw = (b[64:-64].view(n, K) for b, n in zip(buffers, (M, V)))
+        psr.linear_xent_bwd(g, x, w, targets, lse, dx=dx, dw=dw)
+        check_gradients(dx, dw, g, x, w, targets, lse, "bf16", str((V, K)))
+        for b in buffers:
+            assert (b[:64] == 7).all() and (b[-64:] == 7).all()
+
+
 def test_few_rows_of_dx_split_and_joined(psr):
     """dx of few tiles and a long vocabulary: parts of the sum over V, joined, with fewer rows than the host knows of."""
     need_gpu()
