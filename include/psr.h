@@ -543,7 +543,7 @@ typedef struct {
 } psr_xent_shape;
 
 /* Bytes of device workspace psr_xent (backward = 0) or psr_xent_bwd (1) needs; 0 if invalid.  It grows by a copy of w where w's
- * rows do not all start on 16-byte boundaries. */
+ * rows do not all start on 16-byte boundaries and x has more than 64. */
 PSR_API size_t psr_xent_workspace_bytes(const psr_xent_shape* shape, int backward);
 
 /* x: device, [M][K]; w: device, [V][K]; targets: device (read).  loss, lse: device, fp32, [M] (written).

@@ -1077,6 +1077,9 @@ struct StreamParams {
   Ctrl* clear;
   unsigned long long timeout_ns;
   Head h;
+  const void* w;   // odd rows: W itself
+  long long ldw;
+  int w_rows, w_cols;
 };
 
 constexpr int kSumPitch = 33;  // a token's row, read by column and by row
@@ -1147,12 +1150,102 @@ __device__ __forceinline__ void head_tokens(const StreamParams& p, int i0, int n
   }
 }
 
+// ------------------------------------------------------------------------------------------------
+// Rows off 16-byte boundaries
+// ------------------------------------------------------------------------------------------------
+// The sixteen bytes from byte `off` (even, below 16) of two vectors on.
+__device__ __forceinline__ uint4 shift8(const uint4& lo, const uint4& hi, uint32_t off) {
+  uint32_t w[7] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z};
+  uint32_t v[6];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) v[j] = off & 8 ? w[j + 2] : w[j];
+  v[5] = off & 8 ? hi.w : w[5];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) w[j] = off & 4 ? v[j + 1] : v[j];
+  const uint32_t bits = off % 4 * 8;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                    __funnelshift_r(w[3], w[4], bits));
+}
+
+// W's rows where no tensor map takes them: warps of stream_gemm's own read a stage's 128 rows of 256 bytes, in aligned vectors that
+// hold them, shift those to their place and store them where the copies would.  A thread has vector c of every 32nd row from r on;
+// steps and tiles are 128 rows or columns, so that all of a thread's vectors are shifted alike.  Bound by the loads' latency, half a stage
+// being in flight: 48 x 128000 x 4100 in 300 us, 3.6 TB/s, where a copy of W on aligned rows and the product of that took 560.  (Eight
+// warps 320; a whole stage in flight, with what follows a vector from the next lane, 370; rows asked into L2 four or eight steps ahead
+// 440, 330.)
+constexpr int kOddWarps = 16, kOddRows = 2 * kOddWarps, kOddHalf = 64 / kOddRows;  // rows at a time, and a thread's vectors of half a stage
+struct OddRows {
+  const uint8_t *first, *past;  // the matrix
+  long long pitch;              // bytes from row to row
+  int rows, cols;
+  int r, c;
+  uint32_t off;                 // where this thread's vectors begin, behind a 16-byte boundary
+};
+// An aligned vector that begins before the matrix or ends behind it: the elements inside.
+static __device__ __noinline__ uint4 odd_vector(const uint8_t* at, const uint8_t* first, const uint8_t* past) {
+  uint32_t e[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    e[j] = at + 2 * j >= first && at + 2 * j < past ? *reinterpret_cast<const uint16_t*>(at + 2 * j) : 0;
+  return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+}
+// Rows r + 64 half + kOddRows j of the box at (row0, col0).
+__device__ __forceinline__ void odd_fetch(const OddRows& w, int row0, int col0, int half, uint4 (&lo)[kOddHalf], uint4 (&hi)[kOddHalf]) {
+  const int row = row0 + w.r + 64 * half, col = col0 + 8 * w.c;
+  const uint8_t* at = w.first + row * w.pitch + 2ll * col - w.off;
+  if (row0 + 128 < w.rows && col0 + 128 <= w.cols && (row0 > 0 || col0 > 0)) {  // all of them lie in the matrix
+#pragma unroll
+    for (int j = 0; j < kOddHalf; ++j) {
+      lo[j] = __ldg(reinterpret_cast<const uint4*>(at + kOddRows * j * w.pitch));
+      hi[j] = make_uint4(0, 0, 0, 0);
+      if (w.off) hi[j] = __ldg(reinterpret_cast<const uint4*>(at + kOddRows * j * w.pitch) + 1);
+    }
+    return;
+  }
+  const int n = col < w.cols ? min(kOddHalf, (w.rows - row + kOddRows - 1) / kOddRows) : 0;  // (rows: row may be past them)
+#pragma unroll
+  for (int j = 0; j < kOddHalf; ++j) {
+    const uint8_t* from = at + kOddRows * j * w.pitch;
+    lo[j] = hi[j] = make_uint4(0, 0, 0, 0);
+    if (j < n && from >= w.first && from + 16 <= w.past) lo[j] = __ldg(reinterpret_cast<const uint4*>(from));
+    if (j < n && w.off && from + 32 <= w.past) hi[j] = __ldg(reinterpret_cast<const uint4*>(from) + 1);
+  }
+  if (at < w.first || at + kOddRows * (n - 1) * w.pitch + 32 > w.past) {  // at the matrix's first or last element
+#pragma unroll
+    for (int j = 0; j < kOddHalf; ++j) {
+      const uint8_t* from = at + kOddRows * j * w.pitch;
+      if (j < n && (from < w.first || from + 16 > w.past)) lo[j] = odd_vector(from, w.first, w.past);
+      if (j < n && w.off && from + 32 > w.past) hi[j] = odd_vector(from + 16, w.first, w.past);
+    }
+  }
+}
+// K-major W (the box's rows are W's), or the two 64-column boxes of each 64 rows.
+template <bool MN>
+__device__ __forceinline__ void odd_store(const OddRows& w, int col0, int half, uint8_t* stage, const uint4 (&lo)[kOddHalf], const uint4 (&hi)[kOddHalf]) {
+  const int n = w.cols - (col0 + 8 * w.c);  // elements of the row from the vector on
+  uint8_t* to = stage + w.c / 8 * (MN ? 8192 : kHalf) + half * (MN ? kHalf : 8192) + w.r * 128 + ((w.c % 8) ^ (w.r % 8)) * 16;
+#pragma unroll
+  for (int j = 0; j < kOddHalf; ++j) {
+    uint4 v = shift8(lo[j], hi[j], w.off);
+    if (n < 8) {
+      uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) e[q] = n > 2 * q + 1 ? e[q] : n > 2 * q ? e[q] & 0xffffu : 0u;
+      v = make_uint4(e[0], e[1], e[2], e[3]);
+    }
+    *reinterpret_cast<uint4*>(to + j * (kOddRows * 128)) = v;
+  }
+}
+
 // The slopes' product goes through W backwards: what the last one, the loss's, read at its end is still in L2.
 template <int MODE>
 __device__ __forceinline__ int backwards(int i, int n) { return MODE == kSlope ? n - 1 - i : i; }
 
-template <bool AMN, int MODE = kLayer>
-__global__ void __launch_bounds__(kStreamThreads, 1)
+__host__ __device__ constexpr int stream_threads(bool odd) { return kStreamThreads + (odd ? kOddWarps * 32 : 0); }
+
+// ODD: W's rows are off 16-byte boundaries.
+template <bool AMN, int MODE = kLayer, bool ODD = false>
+__global__ void __launch_bounds__(stream_threads(ODD), 1)
     stream_gemm(const __grid_constant__ StreamParams p, const __grid_constant__ CUtensorMap mw,
                 const __grid_constant__ CUtensorMap mx) {
   extern __shared__ uint8_t smem_raw[];
@@ -1166,7 +1259,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   launch_dependents();
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < n_st; ++s) {
-      mbar_init(&sc.full[s], 1);
+      mbar_init(&sc.full[s], ODD ? 1 + kOddWarps : 1);
       mbar_init(&sc.empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -1176,7 +1269,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     mbar_init(&sc.drain, 1);
     sc.abort = 0;
     fence_barrier_init();
-    prefetch_tmap(&mw);
+    if (!ODD) prefetch_tmap(&mw);
     prefetch_tmap(&mx);
   }
   if (warp == 1) {
@@ -1200,14 +1293,15 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         sc.abort = 1;
         break;
       }
-      if (lane == 0) mbar_expect_tx(&sc.full[s], stage_bytes);
+      if (lane == 0) mbar_expect_tx(&sc.full[s], ODD ? kSub * x_bytes : stage_bytes);
       const uint32_t base = smem_base + s * stage_bytes;
       const int wrow = backwards<MODE>(tile, p.n_tiles) * kRows, step = backwards<MODE>(ks, p.n_k);
 #pragma unroll
       for (int h = 0; h < kSub; ++h) {
         const int k = (step * kSub + h) * kBK;
         const uint32_t dst = base + h * kHalf;
-        if constexpr (AMN) {
+        if constexpr (ODD) {
+        } else if constexpr (AMN) {
           load_one(dst, &mw, wrow, k, &sc.full[s], lane == 0);
           load_one(dst + 8192, &mw, wrow + 64, k, &sc.full[s], lane == 0);
         } else {
@@ -1260,6 +1354,52 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       u += n;
     }
     if (!ok) sc.abort = 1;
+  } else if (ODD && warp >= kStreamThreads / 32) {
+    static_assert(kSub * kBK == 128 && kRows == 128, "a stage's box");
+    const int t = threadIdx.x - kStreamThreads;
+    OddRows w;
+    w.first = static_cast<const uint8_t*>(p.w);
+    w.past = w.first + ((p.w_rows - 1) * p.ldw + p.w_cols) * 2;
+    w.pitch = p.ldw * 2;
+    w.rows = p.w_rows;
+    w.cols = p.w_cols;
+    w.r = t / 16;
+    w.c = t % 16;
+    w.off = (uint32_t)(reinterpret_cast<uintptr_t>(w.first + w.r * w.pitch) % 16);
+    int tile = (int)(u0 / p.n_k), ks = (int)(u0 % p.n_k), row0 = 0, col0 = 0;
+    auto place = [&]() {
+      const int at_tile = backwards<MODE>(tile, p.n_tiles) * kRows, at_step = backwards<MODE>(ks, p.n_k) * kSub * kBK;
+      row0 = AMN ? at_step : at_tile;
+      col0 = AMN ? at_tile : at_step;
+    };
+    uint4 lo[2][kOddHalf], hi[2][kOddHalf];  // the two halves of a stage, one in flight while the other is stored
+    place();
+    if (u0 < u1) odd_fetch(w, row0, col0, 0, lo[0], hi[0]);
+    uint32_t s = 0, phase = 0;
+    for (long long u = u0; u < u1; ++u) {
+      const int col = col0;
+      odd_fetch(w, row0, col0, 1, lo[1], hi[1]);
+      if (u - u0 >= n_st && !__all_sync(0xffffffffu, wait_own(&sc.empty[s], phase ^ 1u, p, &sc, SITE_EMPTY))) {
+        sc.abort = 1;
+        break;
+      }
+      uint8_t* stage = smem_raw + (smem_base - raw) + s * stage_bytes;
+      odd_store<AMN>(w, col, 0, stage, lo[0], hi[0]);
+      if (++ks == p.n_k) {
+        ks = 0;
+        ++tile;
+      }
+      place();
+      if (u + 1 < u1) odd_fetch(w, row0, col0, 0, lo[0], hi[0]);
+      odd_store<AMN>(w, col, 1, stage, lo[1], hi[1]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sc.full[s]);
+      if (++s == n_st) {
+        s = 0;
+        phase ^= 1u;
+      }
+    }
   } else if (warp >= 4) {
     const int quarter = warp % 4, row = quarter * 32 + lane;
     uint32_t seg = 0;
@@ -1703,7 +1843,7 @@ inline size_t partial_bytes(int M, int N, int K, bool weights) {
 }
 
 // o.a: the tokens [M][K], o.b: W, K-major [N][K] or (WMN) [K][N].
-template <bool WMN, int MODE = kLayer>
+template <bool WMN, int MODE = kLayer, bool ODD = false>
 inline int launch_stream(const Operands& o, const Epilogue& e, Launch& l, const Head& head = {}) {
   const int dev = l.dev, n_sm = l.n_sm;
   static std::mutex mu;
@@ -1711,7 +1851,7 @@ inline int launch_stream(const Operands& o, const Epilogue& e, Launch& l, const 
   {
     std::lock_guard<std::mutex> lk(mu);
     if (dev < 0 || dev >= 64 || !known[dev]) {
-      if (cudaFuncSetAttribute(stream_gemm<WMN, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem) != cudaSuccess) {
+      if (cudaFuncSetAttribute(stream_gemm<WMN, MODE, ODD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem) != cudaSuccess) {
         cudaGetLastError();
         return PSR_ERR_CUDA;
       }
@@ -1746,12 +1886,16 @@ inline int launch_stream(const Operands& o, const Epilogue& e, Launch& l, const 
   p.ctrl = l.ctrl;
   p.clear = l.clear;
   p.timeout_ns = l.timeout_ns;
-  CUtensorMap mw, mx;
-  const bool ok_w = WMN ? tmap16(&mw, o.b, o.N, o.K, o.ldb, 64) : tmap16(&mw, o.b, o.K, o.N, o.ldb, kRows);
+  p.w = o.b;
+  p.ldw = o.ldb;
+  p.w_rows = WMN ? o.K : o.N;
+  p.w_cols = WMN ? o.N : o.K;
+  CUtensorMap mw = {}, mx;
+  const bool ok_w = ODD ? true : WMN ? tmap16(&mw, o.b, o.N, o.K, o.ldb, 64) : tmap16(&mw, o.b, o.K, o.N, o.ldb, kRows);
   if (!ok_w || !tmap16(&mx, o.a, o.K, o.M, o.lda, p.tb)) return PSR_ERR_CUDA;
   const unsigned grid = (unsigned)((units + per - 1) / per);
   if constexpr (MODE == kLayer) {
-    stream_gemm<WMN, MODE><<<grid, kStreamThreads, kStreamSmem, l.st>>>(p, mw, mx);
+    stream_gemm<WMN, MODE, ODD><<<grid, kStreamThreads, kStreamSmem, l.st>>>(p, mw, mx);
     const int rc = launch_status();
     l.clear = nullptr;
     if (rc != PSR_OK || per % p.n_k == 0) return rc;
@@ -1759,7 +1903,7 @@ inline int launch_stream(const Operands& o, const Epilogue& e, Launch& l, const 
   } else {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kStreamThreads);
+    cfg.blockDim = dim3(stream_threads(ODD));
     cfg.dynamicSmemBytes = kStreamSmem;
     cfg.stream = l.st;
     cudaLaunchAttribute attr[1];
@@ -1767,7 +1911,7 @@ inline int launch_stream(const Operands& o, const Epilogue& e, Launch& l, const 
     attr[0].val.programmaticStreamSerializationAllowed = l.clear ? 0 : 1;  // (the call's first kernel clears the control block)
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, stream_gemm<WMN, MODE>, p, mw, mx) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, stream_gemm<WMN, MODE, ODD>, p, mw, mx) != cudaSuccess) {
       cudaGetLastError();
       return PSR_ERR_CUDA;
     }
@@ -1791,17 +1935,7 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p, int n, const uint8_t* 
     const uint4 lo = *reinterpret_cast<const uint4*>(base);
     uint4 hi = make_uint4(0, 0, 0, 0);
     if (off) hi = *reinterpret_cast<const uint4*>(base + 16);
-    uint32_t w[7] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z};
-    const uint32_t last = hi.w;
-    uint32_t v[6];
-#pragma unroll
-    for (int j = 0; j < 5; ++j) v[j] = off & 8 ? w[j + 2] : w[j];
-    v[5] = off & 8 ? last : w[5];
-#pragma unroll
-    for (int j = 0; j < 5; ++j) w[j] = off & 4 ? v[j + 1] : v[j];
-    const uint32_t bits = off % 4 * 8;
-    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
-                      __funnelshift_r(w[3], w[4], bits));
+    return shift8(lo, hi, off);
   }
   uint32_t e[8];
 #pragma unroll

@@ -429,7 +429,7 @@ constexpr long long kPieceBytes = 512ll << 20;
 constexpr int kPieceLeast = 4096;
 
 struct Sizes {
-  bool few, dot;
+  bool few, dot, odd;      // odd: few rows whose products read W off 16-byte boundaries
   long long ldx, ldw;      // rows of x and w, as given
   long long ldxc, ldd, ldacc;
   int groups, pieces, piece;
@@ -470,7 +470,8 @@ static int sizes(const psr_xent_shape* sh, bool backward, Sizes& s) {
   s.logit_sums = take(!backward && sh->smoothing > 0.f, M * s.groups * 4);
   // packed rows, or (up to kFew rows) those that count beside zeros; the products of a forward pass of few rows read x itself
   s.x = take(!s.few || backward || odd_x, Mk * s.ldxc * 2);
-  s.w = take(odd_w, V * ((K + 7) / 8 * 8) * 2);
+  s.odd = s.few && odd_w;
+  s.w = take(odd_w && !s.few, V * ((K + 7) / 8 * 8) * 2);
   s.pieces = 1;
   s.piece = (int)V;
   s.sums_bytes = s.few && !s.dot ? partial_bytes((int)M, (int)V, (int)K, false) : 0;
@@ -573,10 +574,10 @@ static int forward(const psr_xent_shape* sh, const Sizes& s, const void* x, cons
     rc = launch_status();
   } else if (s.few) {
     if ((rc = align(x, ldx, s.x, sh->M, sh->K, ws, l)) != PSR_OK) return rc;
-    if ((rc = align(w, ldw, s.w, sh->V, sh->K, ws, l)) != PSR_OK) return rc;
     h.ids = targets;
     h.step = sh->targets_step;
-    rc = launch_stream<false, kStats>({x, ldx, w, ldw, sh->M, sh->V, sh->K}, e, l, h);
+    const Operands o = {x, ldx, w, ldw, sh->M, sh->V, sh->K};
+    rc = s.odd ? launch_stream<false, kStats, true>(o, e, l, h) : launch_stream<false, kStats>(o, e, l, h);
   } else {
     RowParams p = {};
     p.loss = loss;
@@ -648,7 +649,8 @@ static int backward(const psr_xent_shape* sh, const Sizes& s, const float* dloss
     e.vec = 1;  // (rows of a multiple of eight elements: the last chunk may go past the piece's columns)
     const Operands logits = {p.xc, p.ldxc, wp, ldw, M, n, K};
     const Split whole = {((M + 255ll) / 256) * ((n + 255ll) / 256), 0, 1, 0.0};
-    if (s.few) rc = launch_stream<false, kSlope>(logits, e, l, h);
+    if (s.odd) rc = launch_stream<false, kSlope, true>(logits, e, l, h);
+    else if (s.few) rc = launch_stream<false, kSlope>(logits, e, l, h);
     else rc = launch_pair<false, false, HALF, kSlope>(logits, e, false, whole, l, h);
     if (rc != PSR_OK) return rc;
     e.ldy = K;
@@ -656,7 +658,8 @@ static int backward(const psr_xent_shape* sh, const Sizes& s, const float* dloss
       e.y = dx;
       e.vec = flat && aligned_to(dx, 16);
       const Operands o = {slope, s.ldd, wp, ldw, M, K, n};
-      if (s.few) rc = launch_stream<true, kSum>(o, e, l, h);
+      if (s.odd) rc = launch_stream<true, kSum, true>(o, e, l, h);
+      else if (s.few) rc = launch_stream<true, kSum>(o, e, l, h);
       else rc = launch_pair<false, true, HALF, kSum>(o, e, false, s.all, l, h);
       if (rc != PSR_OK) return rc;
     }
@@ -691,7 +694,7 @@ static int xent_arguments(const psr_xent_shape* sh, const Sizes& s, const void* 
   if (!x || !w || !targets || !workspace) return PSR_ERR_ARG;
   if (!aligned_to(x, 2) || !aligned_to(w, 2) || !aligned_to(targets, 8) || !aligned_to(workspace, 256)) return PSR_ERR_ARG;
   // operands that are read where they are start on 16-byte boundaries
-  if ((!s.x && !aligned_to(x, 16)) || (!s.w && !aligned_to(w, 16))) return PSR_ERR_ARG;
+  if ((!s.x && !aligned_to(x, 16)) || (!s.w && !s.odd && !aligned_to(w, 16))) return PSR_ERR_ARG;
   return ws_bytes < s.total ? PSR_ERR_ARG : PSR_OK;
 }
 

@@ -253,6 +253,28 @@ def test_pieces_of_the_vocabulary(psr):
     assert not dx[~keep].any()
 
 
+@pytest.mark.parametrize("M", [1, 16, 64, 70])
+def test_rows_off_boundaries_among_nan(psr, M):
+    """W and x as views whose rows begin and end anywhere, with NaN between, before and behind them."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(30 + M)
+    for V, K, gap, t in ((129, 515, 0, "bf16"), (1000, 136, 3, "f16"), (257, 1029, 2, "bf16"), (128, 128, 1, "bf16"), (600, 260, 4, "f16")):
+        x, w, targets, g = inputs(gen, M, V, K, t)
+        views = []
+        for m in (x, w):
+            n = len(m)
+            buffer = torch.full((n * (K + gap) + 7,), float("nan"), dtype=m.dtype, device="cuda")
+            view = buffer[5:5 + n * (K + gap)].view(n, K + gap)[:, :K]
+            view.copy_(m)
+            views.append(view)
+        loss, lse, ws = psr.linear_xent(*views, targets)
+        assert psr.get_stats(ws)["status"] == 0
+        check_loss(loss, lse, x, w, targets, str((V, K)))
+        dx, dw, ws = psr.linear_xent_bwd(g, *views, targets, lse)
+        assert psr.get_stats(ws)["status"] == 0
+        check_gradients(dx, dw, g, x, w, targets, lse, t, str((V, K)))
+
+
 @pytest.mark.parametrize("M", [40, 64, 65, 128, 129])
 def test_gradients_leave_what_stands_around_them(psr, M):
     """Blocks of dx and dw that end inside a tile, in buffers whose other bytes stay as they were, with any number of rows that count."""
