@@ -1101,6 +1101,12 @@ def _kv4_attn_plan(q, cache, table, lens, Hkv, page, scale, out, lse):
 # The two ends of a training step around the layers: embedding, and the loss of the output projection
 # ------------------------------------------------------------------------------------------------
 
+def _check_sizes(what, *sizes):
+    """Sizes that the shapes' fields hold (they would keep the lowest bits of others)."""
+    if any(abs(int(n)) > 0x7FFFFFFF for n in sizes):
+        raise PsrError(ERR_UNSUPPORTED, what)
+
+
 def _check_ids(t, name, M, dev):
     """Token ids [M], int64, any stride; their step."""
     import torch
@@ -1134,6 +1140,7 @@ def _embedding_plan(ids, w, scale, out):
     _check_cuda(ids, "ids", 1)
     V, K = w.shape
     M, dev = ids.shape[0], w.device
+    _check_sizes("psr_embedding", M, V, K)
     step = _check_ids(ids, "ids", M, dev)
     ldy = 0
     if out is not None:
@@ -1147,6 +1154,7 @@ def _embedding_plan(ids, w, scale, out):
 
 def embedding_workspace_bytes(M, V, K) -> int:
     """Bytes of workspace that embedding_bwd() needs."""
+    _check_sizes("psr_embedding_workspace_bytes", M, V, K)
     n = load().psr_embedding_workspace_bytes(EmbeddingShape(int(M), int(V), int(K), BF16, 1, 0, 0, -1, 0, 1.0))
     if n == 0:
         raise PsrError(ERR_ARG, "psr_embedding_workspace_bytes")
@@ -1179,6 +1187,7 @@ def _embedding_bwd_plan(dy, ids, n_rows, scale, padding, dw, accumulate):
     _check_cuda(dy, "dy", 2)
     M, K = dy.shape
     dev, shape = dy.device, (int(n_rows), K)
+    _check_sizes("psr_embedding_bwd", M, *shape)
     step = _check_ids(ids, "ids", M, dev)
     if dw is not None:
         _check_flat(dw, "dw", shape, dy.dtype, dev)
@@ -1197,6 +1206,7 @@ def _embedding_bwd_plan(dy, ids, n_rows, scale, padding, dw, accumulate):
 def linear_xent_workspace_bytes(M, V, K, *, smoothing=0.0, backward=False) -> int:
     """Bytes of workspace that linear_xent() or linear_xent_bwd() needs for contiguous tensors, or views whose row strides are
     multiples of 8 elements and that start on 16-byte boundaries."""
+    _check_sizes("psr_xent_workspace_bytes", M, V, K)
     n = load().psr_xent_workspace_bytes(XentShape(int(M), int(V), int(K), BF16, 0, 0, 1, 1, -100, float(smoothing)),
                                         int(bool(backward)))
     if n == 0:
@@ -1240,6 +1250,9 @@ def _xent_shape(x, w, targets, smoothing, z_weight, ignore, backward, what):
     M, K = x.shape
     V, dev = w.shape[0], x.device
     _check_like(w, "w", (V, K), x.dtype, dev)
+    _check_sizes(what, M, V, K)
+    if not -2**63 <= int(ignore) < 2**63:
+        raise ValueError(f"ignore must be an int64, got {ignore}")
     sh = XentShape(M, V, K, code, _row_stride(x, "x"), _row_stride(w, "w"), _check_ids(targets, "targets", M, dev), 0, int(ignore),
                    float(smoothing), float(z_weight), (1 if x.data_ptr() % 16 else 0) | (2 if w.data_ptr() % 16 else 0))
     need = load().psr_xent_workspace_bytes(sh, int(backward))

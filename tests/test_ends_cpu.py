@@ -173,6 +173,20 @@ def test_embedding_binding_refuses(psr, fake_device):
         psr.embedding_bwd(w[:4], ids, 0)
 
 
+def test_sizes_and_numbers_beyond_their_fields(psr, fake_device):
+    """Sizes of 2^32 and more are refused, not cut to their lowest bits."""
+    x, w, t, g = torch.zeros((4, 16), dtype=BF), torch.zeros((9, 16), dtype=BF), torch.zeros(4, dtype=torch.int64), torch.zeros(4)
+    far = 2**32 + 5
+    for call in (lambda: psr.embedding_workspace_bytes(far, 5, 8), lambda: psr.embedding_workspace_bytes(4, -far, 8),
+                 lambda: psr.linear_xent_workspace_bytes(4, far, 8), lambda: psr.linear_xent_workspace_bytes(4, 5, far, backward=True),
+                 lambda: psr.embedding(t[:1].expand(far), w), lambda: psr.embedding_bwd(x, t, far),
+                 lambda: psr.embedding_bwd(x, t, -far)):
+        with pytest.raises(psr.PsrError):
+            call()
+    _refused(psr.linear_xent, "ignore must be an int64", x, w, t, ignore=2**64 - 100)
+    _refused(psr.linear_xent_bwd, "ignore must be an int64", g, x, w, t, g, ignore=-2**63 - 1)
+
+
 def test_xent_binding_refuses(psr, fake_device):
     x, w, t, g = torch.zeros((4, 16), dtype=BF), torch.zeros((9, 16), dtype=BF), torch.zeros(4, dtype=torch.int64), torch.zeros(4)
     bad = lambda match, *a, **kw: _refused(psr.linear_xent, match, *a, **kw)
