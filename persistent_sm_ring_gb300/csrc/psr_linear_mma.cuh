@@ -1169,10 +1169,10 @@ __device__ __forceinline__ uint4 shift8(const uint4& lo, const uint4& hi, uint32
 
 // W's rows where no tensor map takes them: warps of stream_gemm's own read a stage's 128 rows of 256 bytes, in aligned vectors that
 // hold them, shift those to their place and store them where the copies would.  A thread has vector c of every 32nd row from r on;
-// steps and tiles are 128 rows or columns, so that all of a thread's vectors are shifted alike.  Bound by the loads' latency, half a stage
-// being in flight: 48 x 128000 x 4100 in 300 us, 3.6 TB/s, where a copy of W on aligned rows and the product of that took 560.  (Eight
-// warps 320; a whole stage in flight, with what follows a vector from the next lane, 370; rows asked into L2 four or eight steps ahead
-// 440, 330.)
+// steps and tiles are 128 rows or columns, so that all of a thread's vectors are shifted alike.  48 x 128000 x 4100 in 300 us, 3.6 TB/s,
+// where a copy of W on aligned rows and the product of that took 560.  The warps wait for their loads most of the time (DRAM and L1 43 %,
+// issue slots 47 % busy), but more in flight is no faster: a whole stage, with what follows a vector from the next lane, 420; rows asked
+// into L2 four or eight steps ahead 440, 330; with eight warps instead of sixteen 320.
 constexpr int kOddWarps = 16, kOddRows = 2 * kOddWarps, kOddHalf = 64 / kOddRows;  // rows at a time, and a thread's vectors of half a stage
 struct OddRows {
   const uint8_t *first, *past;  // the matrix
@@ -1190,7 +1190,8 @@ static __device__ __noinline__ uint4 odd_vector(const uint8_t* at, const uint8_t
   return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
 }
 // Rows r + 64 half + kOddRows j of the box at (row0, col0).
-__device__ __forceinline__ void odd_fetch(const OddRows& w, int row0, int col0, int half, uint4 (&lo)[kOddHalf], uint4 (&hi)[kOddHalf]) {
+__device__ __forceinline__ void odd_fetch(const OddRows& w, int row0, int col0, int half, uint4 (&lo)[kOddHalf],
+                                          uint4 (&hi)[kOddHalf]) {
   const int row = row0 + w.r + 64 * half, col = col0 + 8 * w.c;
   const uint8_t* at = w.first + row * w.pitch + 2ll * col - w.off;
   if (row0 + 128 < w.rows && col0 + 128 <= w.cols && (row0 > 0 || col0 > 0)) {  // all of them lie in the matrix
@@ -1221,7 +1222,8 @@ __device__ __forceinline__ void odd_fetch(const OddRows& w, int row0, int col0, 
 }
 // K-major W (the box's rows are W's), or the two 64-column boxes of each 64 rows.
 template <bool MN>
-__device__ __forceinline__ void odd_store(const OddRows& w, int col0, int half, uint8_t* stage, const uint4 (&lo)[kOddHalf], const uint4 (&hi)[kOddHalf]) {
+__device__ __forceinline__ void odd_store(const OddRows& w, int col0, int half, uint8_t* stage, const uint4 (&lo)[kOddHalf],
+                                          const uint4 (&hi)[kOddHalf]) {
   const int n = w.cols - (col0 + 8 * w.c);  // elements of the row from the vector on
   uint8_t* to = stage + w.c / 8 * (MN ? 8192 : kHalf) + half * (MN ? kHalf : 8192) + w.r * 128 + ((w.c % 8) ^ (w.r % 8)) * 16;
 #pragma unroll
