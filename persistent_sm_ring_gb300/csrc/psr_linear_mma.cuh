@@ -52,9 +52,10 @@ enum Mode { kLayer, kStats, kSlope, kSum, kWeight };
 struct Head {
   const int* rows;        // rows that count (kWeight: those summed over); null: the host's number
   const int* index;       // kSum: the row of dx of each
-  // kStats, kSlope: the column of each row's target, of which the first here is col0
-  const int* target;      // (pair_gemm)
-  const int64_t* ids;     // (stream_gemm: the caller's)
+  // kStats, kSlope: the column of each row's target, of which the first here is col0 (stream_gemm: negative for a row that does not
+  // count, whose slopes and whose dx are zeros whatever stands in W)
+  const int* target;
+  const int64_t* ids;     // (stream_gemm's kStats: the caller's)
   long long step;
   int col0;
   float2* stats;          // kStats: (r, s) of each row's columns in groups of kGroup (pair_gemm) or 32: sum exp(l) = s 2^r
@@ -1131,22 +1132,23 @@ __device__ __forceinline__ void head_tokens(const StreamParams& p, int i0, int n
     __syncwarp();
     if (lane < n) {  // the tokens' coefficients and targets, 16 bytes and 4 to each
       reinterpret_cast<float4*>(rows)[lane] = p.h.coef[i0 + lane];
-      const uint64_t target = (uint64_t)p.h.ids[(i0 + lane) * p.h.step] - (uint64_t)(p.h.col0 + j0);
-      reinterpret_cast<int*>(rows)[64 + lane] = target < 32 ? (int)target : -1;
+      reinterpret_cast<int*>(rows)[64 + lane] = p.h.target[i0 + lane];
     }
     __syncwarp();
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const float4 c = reinterpret_cast<const float4*>(rows)[e];
+      const int target = reinterpret_cast<const int*>(rows)[64 + e];
       float f = fmaf(c.y, ex2_approx(fmaf(__uint_as_float(v[e]), kLog2e, -c.x)), -c.z);
-      if (reinterpret_cast<const int*>(rows)[64 + e] == lane) f -= c.w;
-      if (e < n && j < p.N) store16(p.e.y, (i0 + e) * p.e.ldy + j, p.e.half, f);
+      if (target == p.h.col0 + j) f -= c.w;
+      if (e < n && j < p.N) store16(p.e.y, (i0 + e) * p.e.ldy + j, p.e.half, target < 0 ? 0.f : f);
     }
   } else {
     const float unit = *p.h.unit;
+    const uint32_t in = __ballot_sync(0xffffffffu, lane < n && p.h.target[i0 + min(lane, n - 1)] >= 0);
 #pragma unroll
     for (int e = 0; e < 16; ++e)
-      if (e < n && j < p.N) store16(p.e.y, (i0 + e) * p.e.ldy + j, p.e.half, __uint_as_float(v[e]) * unit);
+      if (e < n && j < p.N) store16(p.e.y, (i0 + e) * p.e.ldy + j, p.e.half, in >> e & 1u ? __uint_as_float(v[e]) * unit : 0.f);
   }
 }
 

@@ -10,7 +10,7 @@
 //
 // Rows without a target are left out: the others are packed first, which costs a copy of x and saves their share of the products, and
 // keeps whatever stands in the rows left out (NaN, say) from dw.  Up to kFew rows, where the products read W and hardly multiply,
-// they stay in place.
+// they stay in place as zeros, and so that a weight that is not finite reaches neither their slopes nor their dx, those are set to zeros.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -188,10 +188,8 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ RowPa
       p.coef[at] = c;
     }
   }
-  if (p.packed && in) {
-    p.index[at] = (int)(r0 + threadIdx.x);
-    p.target[at] = (int)t;
-  }
+  if (p.packed && in) p.index[at] = (int)(r0 + threadIdx.x);
+  if ((int)threadIdx.x < rows && (in || !p.packed)) p.target[at] = in ? (int)t : -1;
   if (!BWD && p.packed && (int)threadIdx.x < rows && !in) {
     const float f = t == p.ignore ? 0.f : __int_as_float(0x7FC00000);
     p.loss[r0 + threadIdx.x] = f;
@@ -462,7 +460,7 @@ static int sizes(const psr_xent_shape* sh, bool backward, Sizes& s) {
   s.head = take(true, 256);
   s.row_sums = take(M > kScanMost, (M + 255) / 256 * 16);
   s.index = take(!s.few, M * 4);
-  s.target = take(!s.few, M * 4);
+  s.target = take(!s.few || backward, M * 4);
   s.coef = take(backward, M * 16);
   s.at = take(!backward, M * 4);
   s.groups = s.dot ? kDotBlocks * kStreamCtas : (int)(s.few ? (V + 31) / 32 : (V + kGroup - 1) / kGroup);
@@ -633,8 +631,6 @@ static int backward(const psr_xent_shape* sh, const Sizes& s, const float* dloss
     h.rows = s.few ? nullptr : p.count;
     h.index = p.index;
     h.target = p.target;
-    h.ids = targets;
-    h.step = sh->targets_step;
     h.col0 = at;
     h.coef = p.coef;
     h.acc = in<float>(ws, s.acc);

@@ -400,3 +400,36 @@ def test_refusals(psr):
             psr.linear_xent(x, w, t, **more)
         with pytest.raises(psr.PsrError):
             psr.linear_xent_bwd(g, x, w, t, g, **more)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("M", [2, 7, 40, 64, 65, 300])
+def test_rows_that_do_not_count_among_infinite_weights(psr, M, t):
+    """A weight that is infinite or NaN stays out of the gradients of rows without a target, and of dw through them."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(M)
+    for V, K in ((333, 72), (261, 67)):  # W on 16-byte boundaries and off them
+        x, w, targets, g = inputs(gen, M, V, K, t)
+        targets[targets == 7] = 8
+        # logits of -inf at column 7 in every row that counts: its probability is 0, so dw is finite, and dx (0 times -inf) NaN
+        x[:, 3] = x[:, 3].abs() + 1
+        w[7, 3] = -float("inf")
+        drop = list(range(0, M, 2))
+        targets[drop] = torch.tensor(([-100, V, -1] * M)[:len(drop)], dtype=torch.int64).cuda()
+        x[drop] = float("nan")
+        loss, lse, _ = psr.linear_xent(x, w, targets)
+        dx, dw, ws = psr.linear_xent_bwd(g, x, w, targets, lse)
+        assert psr.get_stats(ws)["status"] == 0
+        keep = np.setdiff1d(np.arange(M), drop)
+        assert not f64(dx)[drop].any()
+        assert np.isnan(f64(dx)[keep, 3]).all() and np.isfinite(np.delete(f64(dx)[keep], 3, 1)).all()
+        assert not f64(dw)[7].any()
+        finite = w.clone()
+        finite[7] = 0  # (no probability and no target: for dw's other rows any weights do, with these lse)
+        check_gradients(None, torch.cat((dw[:7], dw[8:])), g, x, torch.cat((finite[:7], finite[8:])),
+                        torch.where(targets > 7, targets - 1, targets), lse, t, str((V, K)))
+        w[9, 1], w[10, 2] = float("nan"), float("inf")
+        targets.fill_(-100)
+        loss, lse, _ = psr.linear_xent(x, w, targets)
+        dx, dw, _ = psr.linear_xent_bwd(g, x, w, targets, lse)
+        assert not loss.any() and not lse.any() and not dx.any() and not dw.any()
