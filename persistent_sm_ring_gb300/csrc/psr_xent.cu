@@ -171,7 +171,8 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ RowPa
       most = fmaxf(most, most_warp[w]);
       scaled = fmaxf(scaled, scaled_warp[w]);
     }
-    const float unit = most > 0.f ? most * (1.f - p.smoothing) : 1.f;
+    // (a normal number: the product may round to zero)
+    const float unit = most > 0.f ? fmaxf(most * (1.f - p.smoothing), FLT_MIN) : 1.f;
     int e = 0;
     if (p.half) {
       frexpf(fmaxf(scaled / unit, 1.f), &e);  // at most 2^e

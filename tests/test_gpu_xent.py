@@ -433,3 +433,18 @@ def test_rows_that_do_not_count_among_infinite_weights(psr, M, t):
         loss, lse, _ = psr.linear_xent(x, w, targets)
         dx, dw, _ = psr.linear_xent_bwd(g, x, w, targets, lse)
         assert not loss.any() and not lse.any() and not dx.any() and not dw.any()
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("M", [5, 90])
+def test_gradients_of_the_smallest_weights_of_the_loss(psr, M, t):
+    """dloss down to fp32's smallest number, which times (1 - smoothing) is none: gradients that round to zero, and no NaN."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(M)
+    x, w, targets, _ = inputs(gen, M, 200, 40, t)
+    for g, smoothing in ((2.0**-149, 0.75), (2.0**-149, 0.0), (2.0**-126, 0.75), (2.0**-100, 0.1)):
+        g = torch.full((M,), g, device="cuda")
+        _, lse, _ = psr.linear_xent(x, w, targets, smoothing=smoothing)
+        dx, dw, _ = psr.linear_xent_bwd(g, x, w, targets, lse, smoothing=smoothing)
+        for got in (dx, dw):  # slopes are at most 2 g, |x| and |w| below 8, sums of 200 terms
+            assert (got.double().abs() <= g[0].item() * 2 * 8 * 200).all()
