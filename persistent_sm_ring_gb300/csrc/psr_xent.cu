@@ -175,7 +175,8 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ RowPa
     const float unit = most > 0.f ? fmaxf(most * (1.f - p.smoothing), FLT_MIN) : 1.f;
     int e = 0;
     if (p.half) {
-      frexpf(fmaxf(scaled / unit, 1.f), &e);  // at most 2^e
+      // The three terms of a slope over the unit are at most 2^e, 2^e (of few columns much smoothed, the largest) and 1.
+      frexpf(fmaxf(fmaxf(scaled / unit, 1.f), p.smoothing / p.V / (1.f - p.smoothing)), &e);
       e = max(14 - e, -100);
     }
     const float power = ldexpf(1.f, e);

@@ -448,3 +448,20 @@ def test_gradients_of_the_smallest_weights_of_the_loss(psr, M, t):
         dx, dw, _ = psr.linear_xent_bwd(g, x, w, targets, lse, smoothing=smoothing)
         for got in (dx, dw):  # slopes are at most 2 g, |x| and |w| below 8, sums of 200 terms
             assert (got.double().abs() <= g[0].item() * 2 * 8 * 200).all()
+
+
+@pytest.mark.parametrize("M", [6, 100])
+def test_smoothed_slopes_fit_fp16(psr, M):
+    """Much smoothing of few columns with a penalty under which 1 + 2 z lse vanishes: the smoothing's share is then the largest slope."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(M)
+    for V, smoothing in ((1, 0.96875), (2, 0.9375), (3, 0.984375)):
+        x = torch.randint(-2, 3, (M, 8), generator=gen).half().cuda() / 32
+        w = torch.randint(-2, 3, (V, 8), generator=gen).half().cuda() / 4
+        x[:, 0], w[:, 0] = 2.0, -1.0 - float(np.log(V)) / 2  # lse near -2
+        targets, g = torch.randint(0, V, (M,), generator=gen).cuda(), torch.rand(M, generator=gen).cuda() + 0.5
+        more = dict(smoothing=smoothing, z_weight=0.25)
+        _, lse, _ = psr.linear_xent(x, w, targets, **more)
+        assert (1 + 0.5 * lse).abs().max() < 0.1
+        dx, dw, _ = psr.linear_xent_bwd(g, x, w, targets, lse, **more)
+        check_gradients(dx, dw, g, x, w, targets, lse, "f16", str(V), smoothing, 0.25)
