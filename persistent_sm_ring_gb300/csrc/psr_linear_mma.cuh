@@ -1071,8 +1071,9 @@ struct StreamParams {
   int stages;
   uint32_t tmem_cols;
   uint32_t accs;   // accumulators of a tile, which take the K steps in turn (the loss's logits: four, see kPartSteps)
+  int segment;     // K steps of a tile that go into its accumulators at most (the loss's logits): the sums of more stand in the partials meanwhile
   uint32_t idesc;
-  float* partial;  // [2 gridDim.x][tb][128]
+  float* partial;  // [2 gridDim.x][tb][128]: the tiles that a CTA begins and ends with, if it has not all of their K steps
   Epilogue e;
   Ctrl* ctrl;
   Ctrl* clear;
@@ -1247,6 +1248,23 @@ __device__ __forceinline__ int backwards(int i, int n) { return MODE == kSlope ?
 
 __host__ __device__ constexpr int stream_threads(bool odd) { return kStreamThreads + (odd ? kOddWarps * 32 : 0); }
 
+// A sum that is read back after another segment of W has gone through L2, as the last to leave it (logits of 64 x 32000 x 16384 in 177 us, of
+// 40 x 32000 x 8192 in 98, as without segments; with plain stores 189 and 102).
+__device__ __forceinline__ void store_kept(float* at, float v) {
+  asm volatile(
+      "{\n\t.reg .b64 p;\n\t"
+      "createpolicy.fractional.L2::evict_last.b64 p, 1.0;\n\t"
+      "st.global.L2::cache_hint.f32 [%0], %1, p;\n\t}\n" ::"l"(at), "f"(v)
+      : "memory");
+}
+
+// K steps of a tile that a CTA sums at a time, of those left to it.
+template <int MODE>
+__device__ __forceinline__ int segment_of(const StreamParams& p, int left) {
+  if constexpr (in_parts(MODE)) return min(left, p.segment);
+  else return left;
+}
+
 // ODD: W's rows are off 16-byte boundaries.
 template <bool AMN, int MODE = kLayer, bool ODD = false>
 __global__ void __launch_bounds__(stream_threads(ODD), 1)
@@ -1332,7 +1350,7 @@ __global__ void __launch_bounds__(stream_threads(ODD), 1)
     bool ok = true;
     for (long long u = u0; u < u1 && ok; ++seg) {
       const int left = p.n_k - (int)(u % p.n_k);
-      const int n = (int)(u1 - u < left ? u1 - u : left);
+      const int n = segment_of<MODE>(p, (int)(u1 - u < left ? u1 - u : left));
       const uint32_t slot = seg % 2;
       if (seg >= 2) ok = __all_sync(0xffffffffu, wait_own(&sc.acc_empty[slot], (seg / 2 - 1) & 1u, p, &sc, SITE_ACC_EMPTY));
       if (!ok) break;
@@ -1410,15 +1428,19 @@ __global__ void __launch_bounds__(stream_threads(ODD), 1)
     bool ok = true;
     for (long long u = u0; u < u1; ++seg) {
       const int tile = (int)(u / p.n_k), first = (int)(u % p.n_k);
-      const int n = (int)(u1 - u < p.n_k - first ? u1 - u : p.n_k - first);
+      const int left = (int)(u1 - u < p.n_k - first ? u1 - u : p.n_k - first), n = segment_of<MODE>(p, left);
+      // this CTA's K steps of the tile: whether there were some before, whether more come, whether they are all
+      const bool more = n < left;
+      const int had = in_parts(MODE) ? (int)(u - u0 < first ? u - u0 : first) : 0;
       const uint32_t slot = seg % 2;
       ok = __all_sync(0xffffffffu, wait_own(&sc.acc_full[slot], (seg / 2) & 1u, p, &sc, SITE_ACC));
       if (!ok) break;
       tc_fence_after();
       const int first_row = backwards<MODE>(tile, p.n_tiles) * kRows, j = first_row + row;
-      const bool whole = n == p.n_k;
+      const bool whole = had + left == p.n_k;
       const float bias = whole && p.e.bias && j < p.N ? load16(p.e.bias, j, p.e.half) : 0.f;
-      float* part = p.partial + (2ll * blockIdx.x + (u == u0 ? 0 : 1)) * p.tb * kRows + row;
+      // (the second is free until the last tile: a whole one's sums may stand there)
+      float* part = p.partial + (2ll * blockIdx.x + (u - had == u0 && !whole ? 0 : 1)) * p.tb * kRows + row;
       const uint32_t tacc = sc.tmem_base + ((uint32_t)(quarter * 32) << 16) + slot * p.tb * (in_parts(MODE) ? p.accs : 1);
 #pragma unroll 1
       for (int c = 0; c < p.M; c += 16) {
@@ -1436,6 +1458,19 @@ __global__ void __launch_bounds__(stream_threads(ODD), 1)
           }
         }
         const int n_c = min(16, p.M - c);
+        if constexpr (in_parts(MODE)) {
+          if (had) {  // what this thread has stored there
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e < n_c) v[e] = __float_as_uint(part[(c + e) * kRows] + __uint_as_float(v[e]));
+          }
+          if (more) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e < n_c) store_kept(&part[(c + e) * kRows], __uint_as_float(v[e]));
+            continue;
+          }
+        }
         if (!whole) {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
@@ -1882,6 +1917,7 @@ inline int launch_stream(const Operands& o, const Epilogue& e, Launch& l, const 
   const int stage = kSub * (kHalf + p.tb * kBK * 2);
   p.stages = kStreamArea / stage < kStreamMaxStages ? kStreamArea / stage : kStreamMaxStages;
   p.accs = in_parts(MODE) ? 4 : 1;  // (of at most 64 columns)
+  p.segment = (int)p.accs * kPartSteps / kSub;
   p.tmem_cols = 32;
   while (p.tmem_cols < 2u * p.tb * p.accs) p.tmem_cols *= 2;
   p.idesc = idesc16(128, p.tb, WMN, false, e.half != 0);

@@ -465,3 +465,37 @@ def test_smoothed_slopes_fit_fp16(psr, M):
         assert (1 + 0.5 * lse).abs().max() < 0.1
         dx, dw, _ = psr.linear_xent_bwd(g, x, w, targets, lse, **more)
         check_gradients(dx, dw, g, x, w, targets, lse, "f16", str(V), smoothing, 0.25)
+
+
+@pytest.mark.parametrize("M,K", [(1, 16384), (1, 16383), (40, 8192), (2, 16384), (40, 16384), (64, 32768), (17, 20488), (33, 16383), (40, 4096),
+                                 (65, 16384), (300, 8192), (100, 16383)])
+def test_long_logits_are_summed_in_parts(psr, M, K):
+    """Sums of 1024 products that fp32 holds exactly, and longer ones that it does not: the logits are as exact as the additions of the parts.
+
+    Products are integers (times a power of two): 512 pairs of 256 a + b, 64 <= a < 128, 0 <= b < 256, sum to less than 2^24, so a part of
+    1024 has no rounding.  Adding n parts, or parts of parts, of sum L rounds by at most 2^-24 (2 + ... + n) / n of L: below 2^-24 (n + 3) / 2.
+    lse moves by no more; the sums of exponentials of near logits, with at most 2^6 additions one after another (2^-24 each) and up to 32
+    factors of ex2's (2^-22 each), give 2^-16, log2(e) and the result's rounding 2^-24 and 2^-23 of lse.  (Sums of 4096 products, whose
+    last bits the tensor core cuts, come out too small by up to twice what is allowed at K = 16384, of 8192 products by six times.)
+    """
+    need_gpu()
+    gen = torch.Generator(device="cuda").manual_seed(K + M)
+    V = 20000  # more tiles than SMs: few rows' tiles are whole
+    a = torch.randint(64, 128, (V, (K + 1) // 2), generator=gen, device="cuda") * 256
+    b = torch.randint(0, 256, (V, (K + 1) // 2), generator=gen, device="cuda")
+    w = (torch.stack((a, b), 2).view(V, -1)[:, :K] * 2.0**-21).to(torch.bfloat16).contiguous()
+    power = torch.randint(-1, 1, (M, 1), generator=gen, device="cuda")
+    x = (2.0**power).to(torch.bfloat16).expand(M, K).contiguous()
+    t = torch.randint(0, V, (M,), generator=gen, device="cuda")
+    loss, lse, ws = psr.linear_xent(x, w, t)
+    assert psr.get_stats(ws)["status"] == 0
+    logits = 2.0**power.double() * w.double().sum(1)
+    ref = logits.logsumexp(1)
+    parts = -(-K // 1024)
+    most = 2.0**-24 * (parts + 3) / 2 * logits.amax(1)
+    tol = most + 2.0**-16 + (2.0**-23 + 2.0**-24) * ref.abs()
+    err = (lse.double() - ref).abs()
+    assert (err <= tol).all(), (err / tol).max().item()
+    at = logits.gather(1, t[:, None])[:, 0]
+    err, tol = (loss.double() - (ref - at)).abs(), tol + most
+    assert (err <= tol).all(), (err / tol).max().item()
