@@ -571,12 +571,13 @@ __device__ __forceinline__ Extent extent_of(const PairParams& p, int n_pairs) {
   if (MODE == kSum) {
     const int ones = x.tiles_m * ((p.N + 255) / 256), twos = x.tiles_m * ((p.N + 511) / 512), rest = ones % kPairs;
     const int halves = last_halves(twos, n_pairs), most = x.n_k / 8;
-    const float k = (float)(p.n_k * kBK), step = 9.3f * k;
+    // in tenths of a clock, whole numbers: pair_gemm and pair_join, compiled apart, decide alike where two ways cost the same
+    const long long k = p.n_k * (long long)kBK, step = 93 * k;
     int parts = rest ? min(kPairs / rest, most) : 1;
-    const float join = 5500.f + 180.f * rest * parts;
-    if (parts < 2 || 8.6f * k * (1.f - 1.f / parts) < join) parts = 1;
-    const float one = parts > 1 ? ones / kPairs * step + step / parts + join : (ones + n_pairs - 1) / n_pairs * step;
-    const float two = (twos / n_pairs + (halves || twos % n_pairs == 0 ? 0 : 1)) * (16.f * k + 15600.f) + (halves ? step + 7800.f : 0.f);
+    const long long join = 55000 + 1800 * rest * parts;
+    if (parts < 2 || 86 * k * (parts - 1) < join * parts) parts = 1;
+    const long long one = parts > 1 ? ones / kPairs * step + step / parts + join : (ones + n_pairs - 1) / n_pairs * step;
+    const long long two = (twos / n_pairs + (halves || twos % n_pairs == 0 ? 0 : 1)) * (160 * k + 156000) + (halves ? step + 78000 : 0);
     x.wide = two <= one;
     x.tiles_n = x.wide ? (p.N + 511) / 512 : (p.N + 255) / 256;
     x.whole = x.wide ? twos : ones - (parts > 1 ? rest : 0);

@@ -499,3 +499,46 @@ def test_long_logits_are_summed_in_parts(psr, M, K):
     at = logits.gather(1, t[:, None])[:, 0]
     err, tol = (loss.double() - (ref - at)).abs(), tol + most
     assert (err <= tol).all(), (err / tol).max().item()
+
+
+def check_on_device(dx, dw, g, x, w, t, lse, typ, smoothing=0.0, z=0.0):
+    """check_gradients for sizes that numpy takes too long for, with the same tolerance but for the logits: they, and lse, are
+    off by 2^-12 at most (64 sums of 16 products to a part, each cut by less than 2^-23 of sums below 30)."""
+    h, tiny = ol.HALF_STEP[typ], TINY[typ]
+    keep = t != -100
+    x8, w8, g8, l8, at = x[keep].double(), w.double(), g[keep].double(), lse[keep].double(), t[keep][:, None]
+    p = (x8 @ w8.T - l8[:, None]).exp_()
+    top = g8[:, None] * (1 + 2 * z * l8.abs())[:, None]
+    ed = top * (p * 2.0**-11 + 2.0**-22)
+    d = p.mul_((1 + 2 * z * l8)[:, None]).sub_(smoothing / len(w))
+    d.scatter_add_(1, at, torch.full((len(x8), 1), smoothing - 1.0, dtype=torch.float64, device="cuda"))
+    d *= g8[:, None]
+    rx = None if dx is None else d @ w8
+    rw = None if dw is None else d.T @ x8
+    a = d.abs_()
+    ed += 1.01 * h * a + (2.0**-38 * top.max() if typ == "f16" else 0.0)
+    ed += max(len(w) * (rx is not None), len(x8) * (rw is not None)) * 2.0**-23 * a  # the sums
+    for got, ref, tol in ((dx[keep] if rx is not None else None, rx, rx is not None and ed @ w8.abs()),
+                          (dw, rw, rw is not None and ed.T @ x8.abs())):
+        if ref is not None:
+            over = (got.double() - ref).abs() - tol - 1.01 * h * ref.abs() - tiny
+            assert (over <= 0).all(), over.max().item()
+    assert dx is None or not dx[~keep].any()
+
+
+@pytest.mark.parametrize("M,K", [(21760, 7936), (26880, 6400)])
+def test_dx_where_two_ways_cost_the_same(psr, M, K):
+    """Numbers of tiles for which whole and wide tiles of dx are worth exactly the same: its kernels decide alike, and write every row."""
+    need_gpu()
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    V = 7488
+    x = torch.randn((M, K), generator=gen, device="cuda").to(torch.bfloat16)
+    w = (torch.randn((V, K), generator=gen, device="cuda") * 2.5 * K**-0.5).to(torch.bfloat16)
+    t = torch.randint(0, V, (M,), generator=gen, device="cuda")
+    g = torch.rand(M, generator=gen, device="cuda")
+    _, lse, _ = psr.linear_xent(x, w, t)
+    dx = torch.full((M, K), float("nan"), dtype=x.dtype, device="cuda")
+    _, _, ws = psr.linear_xent_bwd(g, x, w, t, lse, need_dw=False, dx=dx)
+    assert psr.get_stats(ws)["status"] == 0 and not dx.isnan().any()
+    rows = torch.arange(0, M, 61, device="cuda")  # of every tile
+    check_on_device(dx[rows], None, g[rows], x[rows], w, t[rows], lse[rows], "bf16")
