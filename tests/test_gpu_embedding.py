@@ -254,3 +254,40 @@ def test_refusals(psr):
                  lambda: psr.embedding_bwd(z(4, 16), ids, 0), lambda: psr.embedding_bwd(z(4, 16), ids, 9, scale=float("inf"))):
         with pytest.raises(psr.PsrError):
             call()
+
+
+def block_of(psr, M, V, K):
+    """Positions of a block, by what the workspace holds: 512 bytes, two lists of M pairs, a pair and two fp32 rows for each block."""
+    up = lambda n: -(-n // 256) * 256
+    total = psr.embedding_workspace_bytes(M, V, K)
+    fits = [b for b in (8, 16, 32, 64) if total == 512 + 2 * up(8 * M) + up(8 * -(-M // b)) + up(8 * -(-M // b) * K)]
+    assert len(fits) == 1, fits
+    return fits[0]
+
+
+@pytest.mark.parametrize("t,K,step", [("f16", 40, 8), ("f16", 520, 16), ("bf16", 520, 32), ("bf16", 520, 64), ("f32", 516, 64),
+                                      ("f16", 514, 64), ("f32", 515, 64)])
+def test_gradient_of_runs_around_whole_blocks(psr, t, K, step):
+    """Runs of equal ids that end in, at and behind the borders of blocks of each length there is, the last block ragged."""
+    need_gpu()
+    g = torch.Generator().manual_seed(K + step)
+    lengths = [1, 2, step // 2 - 1, step // 2, step // 2 + 1, step - 1, step, step + 1, 2 * step - 1, 2 * step, 2 * step + 1, 3 * step,
+               5 * step + 3, 1, 3, 33]
+    least = {8: 1000, 16: 38912 // 2, 32: 77824 // 2, 64: 155648 // 2}[step]
+    n, total = [], 0
+    while total < least or total % step <= step // 2:
+        n.append(lengths[int(torch.randint(0, len(lengths), (), generator=g))])
+        total += n[-1]
+    V = 2 * len(n) + 3
+    assert block_of(psr, total, V, K) == step
+    ids = torch.repeat_interleave(torch.arange(len(n)) * 2 + 1, torch.tensor(n))
+    for kind in ("sorted", "shuffled"):
+        if kind == "shuffled":
+            ids = ids[torch.randperm(total, generator=g)]
+        dy = randn(g, (total, K), t)
+        dw, ws = psr.embedding_bwd(dy, ids.cuda(), V)
+        assert psr.get_stats(ws)["status"] == 0
+        check_gradient(dw, dy, ids, V, t, kind)
+    ids[torch.rand(total, generator=g) < 0.3] = V  # positions behind those of the table, from inside a block on
+    dw, _ = psr.embedding_bwd(dy, ids.cuda(), V)
+    check_gradient(dw, dy, ids, V, t, "named in part")
