@@ -542,3 +542,34 @@ def test_dx_where_two_ways_cost_the_same(psr, M, K):
     assert psr.get_stats(ws)["status"] == 0 and not dx.isnan().any()
     rows = torch.arange(0, M, 61, device="cuda")  # of every tile
     check_on_device(dx[rows], None, g[rows], x[rows], w, t[rows], lse[rows], "bf16")
+
+
+@pytest.mark.parametrize("M,V,K,drop,t,more", [
+    (20000, 14000, 1000, 0.5, "bf16", {}),                            # two pieces, dx's last tiles in 14 and 13 parts
+    (20000, 14000, 1003, 0.5, "f16", dict(smoothing=0.1)),            # the same, W and dx off 16-byte boundaries
+    (9048, 29193, 1000, 0.0, "bf16", dict(z_weight=1e-3)),            # two pieces, dx in tiles of 512 columns
+    (12183, 36851, 1001, 0.0, "f16", {}),                             # the same with halves of tiles in the last round
+    (40000, 9001, 264, 0.1, "bf16", {}),                              # two pieces, whole tiles of several blocks of columns
+    (700, 20011, 2104, 0.3, "bf16", {}), (1100, 12000, 4104, 0.0, "f16", {})],  # one piece, logits in three and five parts
+    ids=str)
+def test_gradients_of_many_rows_and_columns(psr, M, V, K, drop, t, more):
+    """dx summed over pieces of the vocabulary in every form that its tiles take, and logits of several parts over several rounds of tiles."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(M + K)
+    x, w, targets, g = inputs(gen, M, V, K, t, drop)
+    loss, lse, ws = psr.linear_xent(x, w, targets, **more)
+    assert psr.get_stats(ws)["status"] == 0
+    s, z, keep = more.get("smoothing", 0.0), more.get("z_weight", 0.0), targets != -100
+    logits = x[keep].double() @ w.double().T
+    ref = logits.logsumexp(1)
+    # a logit is off by 2^-12 at most: 64 sums of 16 products to a part, each cut by less than 2^-23 of sums below 30, and some parts
+    assert ((lse[keep].double() - ref).abs() <= 2.0**-12 + 2.0**-13 + 2.0**-22 * ref).all() and not lse[~keep].any()
+    ref = ref + z * ref**2 - (1 - s) * logits.gather(1, targets[keep][:, None])[:, 0] - s * logits.mean(1)
+    assert ((loss[keep].double() - ref).abs() <= 2.0**-11 + 2.0**-12 + 2.0**-22 * ref.abs()).all() and not loss[~keep].any()
+    del logits
+    dx, dw = (torch.full(m.shape, float("nan"), dtype=m.dtype, device="cuda") for m in (x, w))
+    _, _, ws = psr.linear_xent_bwd(g, x, w, targets, lse, dx=dx, dw=dw, **more)
+    assert psr.get_stats(ws)["status"] == 0
+    check_on_device(dx, dw, g, x, w, targets, lse, t, s, z)
+    again = psr.linear_xent_bwd(g, x, w, targets, lse, **more)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
