@@ -517,8 +517,8 @@ PSR_API int psr_embedding(const psr_embedding_shape* shape, const int64_t* ids, 
 /* Bytes of device workspace psr_embedding_bwd needs; 0 if invalid. */
 PSR_API size_t psr_embedding_workspace_bytes(const psr_embedding_shape* shape);
 
-/* dw[v] = scale * sum of dy[i] over the i with ids[i] = v, in the order of i, summed in fp32 and rounded once; rows that no id
- * names are zeros.  With `accumulate` the sums are added to dw's rows (before the rounding), and rows that no id names stay as
+/* dw[v] = scale * sum of dy[i] over the i with ids[i] = v, summed in fp32 in an order fixed by M, V, K and the ids, and rounded
+ * once; rows that no id names are zeros.  With `accumulate` the sums are added to dw's rows (before the rounding), and rows that no id names stay as
  * they are.  Ids outside 0 .. V-1 and the padding id are left out.  Two calls on the same inputs give the same bits.
  *   dy: device, [M][K] (read); ids: device (read); dw: device, [V][K] contiguous (written);
  *   workspace: device, 256-byte aligned, >= psr_embedding_workspace_bytes(shape). */

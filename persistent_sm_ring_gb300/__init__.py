@@ -1163,7 +1163,7 @@ def embedding_workspace_bytes(M, V, K) -> int:
 
 def embedding_bwd(dy, ids, n_rows, *, scale=1.0, padding=None, dw=None, accumulate=False, workspace=None, stream=None):
     """The gradient of embedding() with respect to a table of n_rows rows: dw[v] = scale * the sum of dy[i] over the i with
-    ids[i] = v, in the order of i, summed in fp32 and rounded once (two calls give the same bits).
+    ids[i] = v, summed in fp32 in an order fixed by the sizes and the ids, and rounded once (two calls give the same bits).
 
     dy: [M, K] bf16, fp16 or fp32, rows may be strided; ids: int64 [M], any stride.  Ids outside the table, and the id
     `padding`, are left out.  dw [n_rows, K] may be passed in (contiguous); with accumulate the sums are added to its rows, and

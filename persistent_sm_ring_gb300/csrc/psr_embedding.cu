@@ -1,8 +1,9 @@
 // The embedding on sm_103a: rows of a table looked up by token and scaled, and the table's gradient.
 //
-// Forward: y_i = scale w[id_i].  Backward: dw_v = scale sum of dy_i over the i with id_i = v, in the order of i, with fp32
-// sums: the tokens are sorted by id (stable), blocks of sorted positions are summed, and a run of equal ids that crosses
-// blocks is joined from fp32 partials in order.  No result depends on the order in which blocks run.
+// Forward: y_i = scale w[id_i].  Backward: dw_v = scale sum of dy_i over the i with id_i = v, with fp32 sums in an order that the
+// tokens alone decide: they are sorted by id (stable), blocks of sorted positions are summed one after another, and the blocks' sums of a
+// run of equal ids over more than two of them are added in eight interleaved series, then those.  No result depends on the order in which
+// blocks run.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -618,8 +619,10 @@ static int launch_sort(const SortParams& p, cudaStream_t st) {
   return PSR_ERR_CUDA;
 }
 
-// Positions of a block: as many as leave every SM 16 warps, between 8 and 64.  Shorter blocks cost more starts than they balance
-// (65539 rows of 1001 columns in blocks of 64, 32, 16: 93, 101, 122 us).
+// Positions of a block: as many as leave every SM 16 warps of 512 columns, between 8 and 64.  (A number for all types and alignments, so that
+// the workspace's size needs no addresses.  Rows of fp32, or off 16-byte boundaries, have two to four times the warps: 65539 rows of 1001
+// fp32 columns get 32 positions, and an SM 108 warps.)  Shorter blocks cost more starts than they balance, longer ones gain no more (those rows
+// in blocks of 64, 32, 16: 83, 83, 89 us).
 static Sizes sizes(const psr_embedding_shape* sh) {
   Sizes s;
   const long long warps = (long long)sh->M * ((sh->K + 511) / 512);
