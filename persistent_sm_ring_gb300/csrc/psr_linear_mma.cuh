@@ -1173,10 +1173,10 @@ __device__ __forceinline__ uint4 shift8(const uint4& lo, const uint4& hi, uint32
 
 // W's rows where no tensor map takes them: warps of stream_gemm's own read a stage's 128 rows of 256 bytes, in aligned vectors that
 // hold them, shift those to their place and store them where the copies would.  A thread has vector c of every 32nd row from r on;
-// steps and tiles are 128 rows or columns, so that all of a thread's vectors are shifted alike.  48 x 128000 x 4100 in 300 us, 3.6 TB/s,
+// steps and tiles are 128 rows or columns, so that all of a thread's vectors are shifted alike.  48 x 128000 x 4100 in 307 us, 3.4 TB/s,
 // where a copy of W on aligned rows and the product of that took 560.  The warps wait for their loads most of the time (DRAM and L1 43 %,
-// issue slots 47 % busy), but more in flight is no faster: a whole stage, with what follows a vector from the next lane, 420; rows asked
-// into L2 four or eight steps ahead 440, 330; with eight warps instead of sixteen 320.
+// issue slots 47 % busy), but more in flight (a whole stage, or rows asked into L2 some steps ahead) is slower, and eight warps instead of
+// sixteen are.
 constexpr int kOddWarps = 16, kOddRows = 2 * kOddWarps, kOddHalf = 64 / kOddRows;  // rows at a time, and a thread's vectors of half a stage
 struct OddRows {
   const uint8_t *first, *past;  // the matrix
